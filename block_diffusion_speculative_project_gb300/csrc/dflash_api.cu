@@ -1,7 +1,7 @@
 // C ABI of libdflash (declared in include/dflash.h): argument validation, TMA
 // descriptor encoding, workspace layout and the launch sequence of each step call.
-// All compute runs in the kernels of gemm_tc.cu, attention.cu, sampling.cu and
-// small_ops.cu.
+// All compute runs in the kernels of gemm_tc.cu, attention.cu, attention8.cu, kv_rows.cu,
+// sampling.cu and small_ops.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -154,6 +154,7 @@ struct dflash_handle_s {
   std::vector<CUtensorMap> tm_kc_wide, tm_vc_wide;
   std::vector<CUtensorMap> tm_c0, tm_c1;  // [layer*4 + which]
   float inv_freq[64];
+  unsigned long long turn[64];  // the same rotation frequencies in 2^-64 turns per position
   WsLayout ws;
   const int32_t *block_table = nullptr;  // paged caches: [max_batch][Cmax / kPageRows]
 };
@@ -438,6 +439,10 @@ int dflash_create(const dflash_config *cfg, dflash_handle_t *out) {
   }
   for (int d = 0; d < 64; ++d)
     h->inv_freq[d] = d < c.hd / 2 ? (float)std::pow((double)c.rope_base, -2.0 * d / c.hd) : 0.f;
+  for (int d = 0; d < 64; ++d)
+    h->turn[d] = d < c.hd / 2 ? (unsigned long long)std::ldexp(std::pow((double)c.rope_base, -2.0 * d / c.hd) /
+                                                                   6.283185307179586476925, 64)
+                              : 0ULL;
   plan_workspace(h);
   *out = h;
   return DFLASH_OK;
@@ -1010,6 +1015,226 @@ int dflash_attention(dflash_handle_t h, int nb, int layer, const void *q, const 
   DF_TRY(attention_params(h, w, nb, q, c.Hq * c.hd, kcache, vcache, ctx_len, max_ctx, out_o, &ap));
   ap.layer_row0 = static_cast<int>(layer * cache_layer_rows(c));
   DF_CUDA(launch_attention(ap, stream));
+  return DFLASH_OK;
+}
+
+namespace {
+
+// The row and 8-bit cache calls run on the handle's device only.
+int check_device(const dflash_handle_s *h) {
+  int dev = -1;
+  DF_CUDA(cudaGetDevice(&dev));
+  if (dev != h->device)
+    return fail(DFLASH_ERR_INVALID_ARG, "the handle is bound to device %d, the current device is %d", h->device, dev);
+  return DFLASH_OK;
+}
+
+int check_rows(const char *name, const void *rows, int64_t ld, int heads, int hd) {
+  if (!rows || reinterpret_cast<uintptr_t>(rows) % 16)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s must be a non-NULL 16-byte aligned pointer", name);
+  if (ld < (int64_t)heads * hd || ld % 8)
+    return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld of %s: a multiple of 8, at least %d", (long long)ld, name,
+                heads * hd);
+  return DFLASH_OK;
+}
+
+int check_out(const char *name, const void *out) {
+  if (!out || reinterpret_cast<uintptr_t>(out) % 16)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s must be a non-NULL 16-byte aligned pointer", name);
+  return DFLASH_OK;
+}
+
+int check_gain(const char *name, const void *g) {
+  if (reinterpret_cast<uintptr_t>(g) % 16)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s must be 16-byte aligned (or NULL)", name);
+  return DFLASH_OK;
+}
+
+// 8-bit caches are addressed in whole blocks of kPageRows rows.
+int check_cache8(const dflash_handle_s *h, const void *k8, const void *v8, const float *ks, const float *vs) {
+  if (h->cfg.Cmax % kPageRows)
+    return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "8-bit caches need Cmax %% %d == 0", kPageRows);
+  DF_TRY(check_out("kcache8", k8));
+  DF_TRY(check_out("vcache8", v8));
+  if (!ks || !vs || reinterpret_cast<uintptr_t>(ks) % 4 || reinterpret_cast<uintptr_t>(vs) % 4)
+    return fail(DFLASH_ERR_INVALID_ARG, "kscale and vscale must be non-NULL 4-byte aligned pointers");
+  return DFLASH_OK;
+}
+
+KvRowsParams rows_params(const dflash_handle_s *h, int nb, int R) {
+  KvRowsParams p;
+  std::memset(&p, 0, sizeof(p));
+  std::memcpy(p.turn, h->turn, sizeof(p.turn));
+  p.nb = nb;
+  p.R = R;
+  p.hd = h->cfg.hd;
+  p.Cmax = h->cfg.Cmax;
+  p.eps = h->cfg.eps;
+  return p;
+}
+
+// Arguments shared by the two appends; *run is false when there is nothing to do.
+int append_params(dflash_handle_t h, int nb, int layer, int R, const void *k, int64_t ldk, const void *v,
+                  int64_t ldv, const void *g_k, int rotate, const int32_t *n_rows, const int32_t *ctx_len,
+                  void *ws, size_t ws_bytes, KvRowsParams *out, bool *run) {
+  *run = false;
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  const auto &c = h->cfg;
+  if (nb < 0 || nb > c.max_batch) return fail(DFLASH_ERR_INVALID_ARG, "nb=%d outside [0, max_batch]", nb);
+  if (layer < 0 || layer >= c.N) return fail(DFLASH_ERR_INVALID_ARG, "layer=%d outside [0, N)", layer);
+  if (R < 0 || R > c.Cmax) return fail(DFLASH_ERR_INVALID_ARG, "R=%d outside [0, Cmax]", R);
+  if (nb == 0 || R == 0) return DFLASH_OK;
+  DF_TRY(check_rows("k", k, ldk, c.Hkv, c.hd));
+  DF_TRY(check_rows("v", v, ldv, c.Hkv, c.hd));
+  DF_TRY(check_gain("g_k", g_k));
+  if (!ctx_len) return fail(DFLASH_ERR_INVALID_ARG, "ctx_len is NULL");
+  DF_TRY(check_paging(h));
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  KvRowsParams &p = *out;
+  p = rows_params(h, nb, R);
+  p.src[0] = bf(k);
+  p.src[1] = bf(v);
+  p.ld[0] = ldk;
+  p.ld[1] = ldv;
+  p.g[0] = bf(g_k);
+  p.heads[0] = p.heads[1] = c.Hkv;
+  p.rotate = rotate ? 1 : 0;
+  p.n_rows = n_rows;
+  p.ctx_len = ctx_len;
+  p.page_table = c.num_pages > 0 ? h->block_table : nullptr;
+  p.pages_per_seq = c.Cmax / kPageRows;
+  p.num_pages = c.num_pages;
+  p.status = Ws{static_cast<uint8_t *>(ws), h->ws}.status();
+  *run = true;
+  return DFLASH_OK;
+}
+
+}  // namespace
+
+int dflash_qk_norm_rope(dflash_handle_t h, int nb, int R, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                        const void *g_q, const void *g_k, const int32_t *pos0, void *out_q, void *out_k,
+                        dflash_stream_t stream) {
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  const auto &c = h->cfg;
+  if (nb < 0 || R < 0) return fail(DFLASH_ERR_INVALID_ARG, "nb=%d and R=%d must be >= 0", nb, R);
+  if ((k == nullptr) != (out_k == nullptr)) return fail(DFLASH_ERR_INVALID_ARG, "k and out_k go together");
+  if (nb == 0 || R == 0) return DFLASH_OK;
+  if ((long long)nb * R > (1LL << 31) / 8)
+    return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "nb * R = %lld rows: at most 2^28", (long long)nb * R);
+  DF_TRY(check_rows("q", q, ldq, c.Hq, c.hd));
+  DF_TRY(check_out("out_q", out_q));
+  if (k) {
+    DF_TRY(check_rows("k", k, ldk, c.Hkv, c.hd));
+    DF_TRY(check_out("out_k", out_k));
+  }
+  DF_TRY(check_gain("g_q", g_q));
+  DF_TRY(check_gain("g_k", g_k));
+  if (!pos0) return fail(DFLASH_ERR_INVALID_ARG, "pos0 is NULL");
+  DF_TRY(check_device(h));
+  KvRowsParams p = rows_params(h, nb, R);
+  p.src[0] = bf(q);
+  p.src[1] = bf(k);
+  p.ld[0] = ldq;
+  p.ld[1] = ldk;
+  p.dst[0] = static_cast<uint16_t *>(out_q);
+  p.dst[1] = static_cast<uint16_t *>(out_k);
+  p.g[0] = bf(g_q);
+  p.g[1] = bf(g_k);
+  p.heads[0] = c.Hq;
+  p.heads[1] = k ? c.Hkv : 0;
+  p.rotate = 1;
+  p.ctx_len = pos0;
+  DF_CUDA(launch_qk_norm_rope(p, h->num_sms, stream));
+  return DFLASH_OK;
+}
+
+int dflash_kv_append(dflash_handle_t h, int nb, int layer, int R, const void *k, int64_t ldk, const void *v,
+                     int64_t ldv, const void *g_k, int rotate, const int32_t *n_rows, const int32_t *ctx_len,
+                     void *kcache, void *vcache, void *ws, size_t ws_bytes, dflash_stream_t stream) {
+  KvRowsParams p;
+  bool run;
+  DF_TRY(append_params(h, nb, layer, R, k, ldk, v, ldv, g_k, rotate, n_rows, ctx_len, ws, ws_bytes, &p, &run));
+  if (!run) return DFLASH_OK;
+  DF_TRY(check_out("kcache", kcache));
+  DF_TRY(check_out("vcache", vcache));
+  p.dst[0] = static_cast<uint16_t *>(kcache) + layer * cache_layer_elems(h->cfg);
+  p.dst[1] = static_cast<uint16_t *>(vcache) + layer * cache_layer_elems(h->cfg);
+  DF_CUDA(launch_kv_append(p, h->num_sms, stream));
+  return DFLASH_OK;
+}
+
+int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, const void *k, int64_t ldk, const void *v,
+                      int64_t ldv, const void *g_k, int rotate, const int32_t *n_rows, const int32_t *ctx_len,
+                      void *kcache8, void *vcache8, float *kscale, float *vscale, void *ws, size_t ws_bytes,
+                      dflash_stream_t stream) {
+  KvRowsParams p;
+  bool run;
+  DF_TRY(append_params(h, nb, layer, R, k, ldk, v, ldv, g_k, rotate, n_rows, ctx_len, ws, ws_bytes, &p, &run));
+  if (!run) return DFLASH_OK;
+  DF_TRY(check_cache8(h, kcache8, vcache8, kscale, vscale));
+  const auto &c = h->cfg;
+  if (nb > 65535 || 2 * c.Hkv > 65535)
+    return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "nb and 2*Hkv must be at most 65535");
+  const size_t blocks = layer * (cache_layer_rows(c) / kPageRows);
+  p.dst8[0] = static_cast<uint8_t *>(kcache8) + blocks * kPageRows * c.hd;
+  p.dst8[1] = static_cast<uint8_t *>(vcache8) + blocks * kPageRows * c.hd;
+  p.scale[0] = kscale + blocks;
+  p.scale[1] = vscale + blocks;
+  DF_CUDA(launch_kv_append8(p, stream));
+  return DFLASH_OK;
+}
+
+int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q, const void *kcache8,
+                      const void *vcache8, const float *kscale, const float *vscale, const int32_t *n_rows,
+                      const int32_t *ctx_len, int max_ctx_hint, int causal, void *out_o, void *ws, size_t ws_bytes,
+                      dflash_stream_t stream) {
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  const auto &c = h->cfg;
+  if (nb < 0 || nb > c.max_batch) return fail(DFLASH_ERR_INVALID_ARG, "nb=%d outside [0, max_batch]", nb);
+  if (layer < 0 || layer >= c.N) return fail(DFLASH_ERR_INVALID_ARG, "layer=%d outside [0, N)", layer);
+  if (m < 0 || m > c.B) return fail(DFLASH_ERR_INVALID_ARG, "m=%d outside [0, B]", m);
+  if (max_ctx_hint < 0 || max_ctx_hint > c.Cmax)
+    return fail(DFLASH_ERR_INVALID_ARG, "max_ctx_hint=%d outside [0, Cmax]", max_ctx_hint);
+  if (nb == 0 || m == 0) return DFLASH_OK;
+  DF_TRY(check_out("q", q));
+  DF_TRY(check_out("out_o", out_o));
+  DF_TRY(check_cache8(h, kcache8, vcache8, kscale, vscale));
+  if (!ctx_len) return fail(DFLASH_ERR_INVALID_ARG, "ctx_len is NULL");
+  DF_TRY(check_paging(h));
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  Ws w{static_cast<uint8_t *>(ws), h->ws};
+  const size_t blocks = layer * (cache_layer_rows(c) / kPageRows);
+  Attn8Params p{};
+  p.q = bf(q);
+  p.k8 = static_cast<const uint8_t *>(kcache8) + blocks * kPageRows * c.hd;
+  p.v8 = static_cast<const uint8_t *>(vcache8) + blocks * kPageRows * c.hd;
+  p.ks = kscale + blocks;
+  p.vs = vscale + blocks;
+  p.n_rows = n_rows;
+  p.ctx_len = ctx_len;
+  p.o = static_cast<uint16_t *>(out_o);
+  p.part_o = w.at<float>(h->ws.apart);
+  p.part_ml = w.at<float>(h->ws.aml);
+  p.nb = nb;
+  p.m = m;
+  p.Hq = c.Hq;
+  p.Hkv = c.Hkv;
+  p.hd = c.hd;
+  p.Cmax = c.Cmax;
+  p.max_ctx = max_ctx_hint > 0 ? max_ctx_hint : c.Cmax;
+  p.causal = causal ? 1 : 0;
+  p.page_table = c.num_pages > 0 ? h->block_table : nullptr;
+  p.pages_per_seq = c.Cmax / kPageRows;
+  p.num_pages = c.num_pages;
+  p.grid = h->num_sms;
+  p.status = w.status();
+  p.max_spin = c.max_spin;
+  p.stall = (c.flags & DFLASH_FLAG_TEST_STALL) ? 1 : 0;
+  if (attention_slots(nb, c.Hkv, p.grid) > h->ws.apart_ctas)
+    return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "attention partials exceed the workspace plan");
+  DF_CUDA(launch_attention8(p, stream));
   return DFLASH_OK;
 }
 

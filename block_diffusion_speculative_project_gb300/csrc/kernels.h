@@ -275,6 +275,52 @@ struct AttnParams {
   int stall;            // test hook: issue no loads so the waits run out
 };
 
+// Rows between a projection and its attention (kv_rows.cu). Two row tensors: queries and keys
+// (norm and rotation of both), or keys and values (appends; keys normed and rotated).
+struct KvRowsParams {
+  unsigned long long turn[64];  // base^(-2d/hd) / (2 pi) in 2^-64 turns
+  const uint16_t *src[2];       // bf16 [nb * R] rows of heads[t] * hd values
+  long long ld[2];              // their row strides in elements
+  uint16_t *dst[2];             // bf16 outputs, or the layer's bf16 caches
+  uint8_t *dst8[2];             // the layer's 8-bit caches
+  float *scale[2];              // and their scales, one per 64 rows and kv head
+  const uint16_t *g[2];         // bf16 [hd] norm gains, or null: no norm
+  int heads[2];
+  int nb, R, hd, rotate, Cmax;
+  const int *n_rows;            // [nb] or null: R
+  const int *ctx_len;           // [nb] position (cache row) of a sequence's first row
+  const int *page_table;
+  int pages_per_seq, num_pages;
+  float eps;
+  int *status;
+  int warps_per_row, iters;     // work split, set by the launch
+};
+cudaError_t launch_qk_norm_rope(KvRowsParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_append(KvRowsParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_append8(const KvRowsParams &p, cudaStream_t s);
+
+// Attention of m query rows per sequence over an 8-bit cache (attention8.cu).
+struct Attn8Params {
+  const uint16_t *q;         // bf16 [nb][m][Hq][hd]
+  const uint8_t *k8, *v8;    // e4m3, the layer's caches
+  const float *ks, *vs;      // the layer's scales, one per 64 rows and kv head
+  const int *n_rows;         // [nb] or null: m
+  const int *ctx_len;        // [nb]
+  uint16_t *o;               // bf16 [nb][m][Hq][hd]
+  float *part_o;             // [slots][G*m rows][hd] unnormalised partial outputs
+  float *part_ml;            // [slots][G*m rows][2] (running maximum in log2 units, running sum)
+  int nb, m, Hq, Hkv, hd, Cmax;
+  int max_ctx;               // caller's bound on ctx_len (larger values are reported and clamped)
+  int causal;
+  const int *page_table;
+  int pages_per_seq, num_pages;
+  int grid;
+  int *status;
+  int max_spin;
+  int stall;                 // test hook: issue no loads so the waits run out
+};
+cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s);
+
 // Slots of partial outputs the attention of nb sequences may write: at most one per
 // (pair, CTA) boundary, i.e. nb * Hkv + grid.
 inline size_t attention_slots(int nb, int Hkv, int grid) { return (size_t)nb * Hkv + grid; }

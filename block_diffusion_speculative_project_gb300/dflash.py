@@ -80,6 +80,11 @@ def _load():
         "dflash_lm_head_topk": (i, [p, i, p, i, p, p, p, p, sz, p]),
         "dflash_lm_head_topk_noalloc": (i, [p, i, p, i, p, p, p, p]),
         "dflash_attention": (i, [p, i, i, p, p, p, p, i, p, p, sz, p]),
+        "dflash_qk_norm_rope": (i, [p, i, i, p, ctypes.c_int64, p, ctypes.c_int64, p, p, p, p, p, p]),
+        "dflash_kv_append": (i, [p, i, i, i, p, ctypes.c_int64, p, ctypes.c_int64, p, i, p, p, p, p, p, sz, p]),
+        "dflash_kv_append8": (i, [p, i, i, i, p, ctypes.c_int64, p, ctypes.c_int64, p, i, p, p, p, p, p, p, p,
+                                  sz, p]),
+        "dflash_attention8": (i, [p, i, i, i, p, p, p, p, p, p, p, i, i, p, p, sz, p]),
         "dflash_topk": (i, [p, i, i, p, i, p, p, p, sz, p]),
         "dflash_accept": (i, [p, i, p, p, p, p, p]),
         "dflash_accept_topk": (i, [p, i, p, i, p, p, p, p]),
@@ -112,7 +117,8 @@ EXPORTED = ("dflash_create", "dflash_destroy", "dflash_set_weights", "dflash_set
             "dflash_lm_head_topk", "dflash_lm_head_topk_noalloc", "dflash_attention", "dflash_topk", "dflash_accept", "dflash_accept_topk", "dflash_sample", "dflash_verify_sample",
             "dflash_lm_head_sample", "dflash_draw_gumbel", "dflash2_select_sample",
             "dflash_verify_sample_walk", "dflash_recall_at_k", "dflash2_conv",
-            "dflash2_select")
+            "dflash2_select", "dflash_qk_norm_rope", "dflash_kv_append", "dflash_kv_append8",
+            "dflash_attention8")
 
 
 def _check(rc: int):
@@ -204,6 +210,32 @@ def dflash_attention(h, nb, layer, q, kcache, vcache, ctx_len, max_ctx_hint, out
     _check(LIB.dflash_attention(h, nb, layer, _ptr(q), _ptr(kcache), _ptr(vcache), _ptr(ctx_len),
                                 max_ctx_hint, _ptr(out_o), _ptr(ws), ws.numel() * ws.element_size(),
                                 _stream(stream)))
+
+
+def dflash_qk_norm_rope(h, nb, R, q, ldq, k, ldk, g_q, g_k, pos0, out_q, out_k, stream=None) -> None:
+    _check(LIB.dflash_qk_norm_rope(h, nb, R, _ptr(q), ldq, _ptr(k), ldk, _ptr(g_q), _ptr(g_k), _ptr(pos0),
+                                   _ptr(out_q), _ptr(out_k), _stream(stream)))
+
+
+def dflash_kv_append(h, nb, layer, R, k, ldk, v, ldv, g_k, rotate, n_rows, ctx_len, kcache, vcache, ws,
+                     stream=None) -> None:
+    _check(LIB.dflash_kv_append(h, nb, layer, R, _ptr(k), ldk, _ptr(v), ldv, _ptr(g_k), rotate, _ptr(n_rows),
+                                _ptr(ctx_len), _ptr(kcache), _ptr(vcache), _ptr(ws),
+                                ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def dflash_kv_append8(h, nb, layer, R, k, ldk, v, ldv, g_k, rotate, n_rows, ctx_len, kcache8, vcache8, kscale,
+                      vscale, ws, stream=None) -> None:
+    _check(LIB.dflash_kv_append8(h, nb, layer, R, _ptr(k), ldk, _ptr(v), ldv, _ptr(g_k), rotate, _ptr(n_rows),
+                                 _ptr(ctx_len), _ptr(kcache8), _ptr(vcache8), _ptr(kscale), _ptr(vscale),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def dflash_attention8(h, nb, layer, m, q, kcache8, vcache8, kscale, vscale, n_rows, ctx_len, max_ctx_hint,
+                      causal, out_o, ws, stream=None) -> None:
+    _check(LIB.dflash_attention8(h, nb, layer, m, _ptr(q), _ptr(kcache8), _ptr(vcache8), _ptr(kscale),
+                                 _ptr(vscale), _ptr(n_rows), _ptr(ctx_len), max_ctx_hint, causal, _ptr(out_o),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def dflash_topk(h, rows, cols, logits, k, out_ids, out_vals, ws=None, stream=None) -> None:

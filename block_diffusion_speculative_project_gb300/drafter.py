@@ -26,12 +26,15 @@ class Drafter:
 
     ``shape`` is any object with the workload fields D, Dt, L, N, Hq, Hkv, hd, F, V,
     B, k_top, rope_base, eps, mask_id, flags, conv_group, sel_dim and film_width.
+    ``cache8`` adds the 8-bit caches kcache8, vcache8 (e4m3, laid out as the bf16 ones) and their
+    scales kscale, vscale, for ``kv_append8`` and ``attention8``.
+
     ``weights`` maps the weight names of dflash_inputs.weight_shapes to bf16 device
     tensors.
     """
 
     def __init__(self, shape, weights: dict, max_batch: int, Cmax: int, max_proj_rows: int,
-                 max_spin: int = 0, device="cuda", num_pages: int = 0):
+                 max_spin: int = 0, device="cuda", num_pages: int = 0, cache8: bool = False):
         self.shape = shape
         s = shape
         self.cfg = _d.dflash_config(
@@ -65,6 +68,15 @@ class Drafter:
                   else (s.N, max_batch, s.Hkv, Cmax, s.hd))
         self.kcache = torch.zeros(cshape, dtype=torch.bfloat16, device=device)
         self.vcache = torch.zeros(cshape, dtype=torch.bfloat16, device=device)
+        self.kcache8 = self.vcache8 = self.kscale = self.vscale = None
+        if cache8:
+            if Cmax % _d.DFLASH_PAGE_ROWS:
+                raise ValueError(f"8-bit caches need Cmax % {_d.DFLASH_PAGE_ROWS} == 0, got {Cmax}")
+            self.kcache8 = torch.zeros(cshape, dtype=torch.float8_e4m3fn, device=device)
+            self.vcache8 = torch.zeros(cshape, dtype=torch.float8_e4m3fn, device=device)
+            sshape = cshape[:3] if num_pages > 0 else cshape[:3] + (Cmax // _d.DFLASH_PAGE_ROWS,)
+            self.kscale = torch.ones(sshape, dtype=torch.float32, device=device)
+            self.vscale = torch.ones(sshape, dtype=torch.float32, device=device)
         self.max_batch, self.Cmax, self.max_proj_rows = max_batch, Cmax, max_proj_rows
         self.num_pages = num_pages
         self.block_table = None
@@ -146,6 +158,24 @@ class Drafter:
     def attention(self, nb, layer, q, ctx_len, out_o, max_ctx_hint=0, stream=None):
         _d.dflash_attention(self.h, nb, layer, q, self.kcache, self.vcache, ctx_len, max_ctx_hint,
                             out_o, self.ws, stream)
+
+    def qk_norm_rope(self, nb, R, q, k, pos0, out_q, out_k, g_q=None, g_k=None, stream=None):
+        """q, k: rows [nb * R, heads * hd] of any row stride (k and out_k may be None)."""
+        _d.dflash_qk_norm_rope(self.h, nb, R, q, q.stride(0), k, 0 if k is None else k.stride(0), g_q, g_k, pos0,
+                               out_q, out_k, stream)
+
+    def kv_append(self, nb, layer, R, k, v, ctx_len, n_rows=None, g_k=None, rotate=True, stream=None):
+        """k, v: rows [nb * R, Hkv * hd] of any row stride."""
+        _d.dflash_kv_append(self.h, nb, layer, R, k, k.stride(0), v, v.stride(0), g_k, int(rotate), n_rows, ctx_len,
+                            self.kcache, self.vcache, self.ws, stream)
+
+    def kv_append8(self, nb, layer, R, k, v, ctx_len, n_rows=None, g_k=None, rotate=True, stream=None):
+        _d.dflash_kv_append8(self.h, nb, layer, R, k, k.stride(0), v, v.stride(0), g_k, int(rotate), n_rows, ctx_len,
+                             self.kcache8, self.vcache8, self.kscale, self.vscale, self.ws, stream)
+
+    def attention8(self, nb, layer, m, q, ctx_len, out_o, n_rows=None, causal=False, max_ctx_hint=0, stream=None):
+        _d.dflash_attention8(self.h, nb, layer, m, q, self.kcache8, self.vcache8, self.kscale, self.vscale, n_rows,
+                             ctx_len, max_ctx_hint, int(causal), out_o, self.ws, stream)
 
     def topk(self, rows, cols, logits, k, out_ids, out_vals, stream=None):
         _d.dflash_topk(self.h, rows, cols, logits, k, out_ids, out_vals, None, stream)

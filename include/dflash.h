@@ -37,6 +37,14 @@
  * rows ctx_len .. ctx_len + n_commit - 1, block rows ctx_len .. ctx_len + B - 1) must
  * lie in pages no other sequence of the call reads or writes.
  *
+ * 8-bit KV cache (dflash_kv_append8, dflash_attention8; the pages keep bf16 rows, this form
+ * halves the bytes that attention reads): the same layouts with one byte per element (e4m3),
+ * and per cache an f32 scale for each block of DFLASH_PAGE_ROWS rows and kv head: contiguous
+ * [N][max_batch][Hkv][Cmax / 64], paged [N][num_pages][Hkv]; an element stands for its e4m3
+ * value times its block's scale. Cmax must be a multiple of DFLASH_PAGE_ROWS. The caller owns
+ * all four buffers; rows and scales that no append wrote may hold anything. The same handle
+ * and block table serve both kinds of cache.
+ *
  * Block layout (reading of [DFlash] 符号约定 and 四、推理流程): block i is
  * [anchor, mask_id x (B-1)] at absolute positions ctx_len[i] .. ctx_len[i]+B-1,
  * where ctx_len counts the context rows in the cache; offsets 1..B-1 carry the
@@ -295,6 +303,83 @@ DFLASH_API int dflash_attention(dflash_handle_t h, int nb, int layer, const void
                                 const void *kcache, const void *vcache, const int32_t *ctx_len,
                                 int max_ctx_hint, void *out_o, void *ws, size_t ws_bytes,
                                 dflash_stream_t stream);
+
+/* Per-head RMSNorm of queries and keys and the position rotation (RoPE, rotate-half pairing,
+ * cfg.rope_base) in one pass over a projection's rows ([DFlash] 四、推理流程: the rotated
+ * queries and keys of the block; the norms are those of targets and drafters that normalise
+ * each head). For each head x of hd values, y = x * g / sqrt(mean(x^2) + eps), then y rotated at
+ * the row's position; fp32 arithmetic, angles exact at any position, one rounding to bf16.
+ *   q, k        bf16 rows (nb * R of them, row j of sequence i at i*R + j) of Hq and Hkv heads,
+ *               row strides ldq and ldk in elements (multiples of 8; 16-byte aligned: e.g. the
+ *               parts of a fused q|k|v projection). k and out_k may be NULL together.
+ *   g_q, g_k    bf16 [hd] gains, NULL: no norm, the rotation alone
+ *   pos0        int32 [nb] device: position of row 0; row j lies at pos0[i] + j
+ *   out_q       bf16 [nb, R, Hq, hd] (the q of dflash_attention and dflash_attention8)
+ *   out_k       bf16 [nb, R, Hkv, hd]
+ * An output may be its own input (ldq = Hq*hd); otherwise they must not overlap. Rows: at most
+ * 2^28. Not limited to max_batch; needs no weights and no workspace. */
+DFLASH_API int dflash_qk_norm_rope(dflash_handle_t h, int nb, int R, const void *q, int64_t ldq,
+                                   const void *k, int64_t ldk, const void *g_q, const void *g_k,
+                                   const int32_t *pos0, void *out_q, void *out_k, dflash_stream_t stream);
+
+/* Append of R rows per sequence of keys and values that the caller has computed to one layer of
+ * the bf16 caches, contiguous or paged, with the keys' norm and rotation on the way ([DFlash]
+ * 四、推理流程: the cache keeps projected, rotated keys; dflash_ctx_project appends what it
+ * projects itself).
+ *   layer       0..N-1
+ *   k, v        bf16 rows of Hkv heads, row j of sequence i at i*R + j, row strides ldk, ldv
+ *               (as dflash_qk_norm_rope)
+ *   g_k         bf16 [hd] gain of the keys' per-head RMSNorm, or NULL: no norm
+ *   rotate      0: the keys as they are (already rotated); else rotated at their cache row
+ *   n_rows      int32 [nb] device, 0 <= n_rows[i] <= R: rows of sequence i that are appended (the
+ *               rest of its R rows are padding and not read), or NULL: R for every sequence
+ *   ctx_len     int32 [nb] device: row j goes to cache row ctx_len[i] + j. Not changed (every
+ *               layer appends at the same rows; the caller advances it once per step).
+ * Cache rows outside [0, Cmax) are not written, and like a count outside [0, R] or a page outside
+ * the pool they are reported as DFLASH_ERR_DEVICE_CHECK by dflash_status. 0 <= R <= Cmax. */
+DFLASH_API int dflash_kv_append(dflash_handle_t h, int nb, int layer, int R, const void *k, int64_t ldk,
+                                const void *v, int64_t ldv, const void *g_k, int rotate,
+                                const int32_t *n_rows, const int32_t *ctx_len, void *kcache,
+                                void *vcache, void *ws, size_t ws_bytes, dflash_stream_t stream);
+
+/* dflash_kv_append into the 8-bit caches (layout above; no counterpart on the pages). A block of
+ * 64 cache rows and one kv head takes the scale 2^e, e the smallest of -100..119 with
+ * amax / 2^e <= 448 over the finite values appended to it, each value rounded to the nearest
+ * e4m3 (infinities to +-448, NaN stays NaN). A block that keeps rows below ctx_len never takes
+ * a smaller scale than it has; when its scale grows, those rows are rounded again to the new
+ * one (exact, but for values that become subnormal). The rows of a block that starts at or above
+ * ctx_len count for nothing, so after ctx_len was set back a block begins afresh.
+ *   kcache8, vcache8  bytes; kscale, vscale f32. Sequences of one call share no block that the
+ *               call writes. Other arguments and errors as dflash_kv_append. */
+DFLASH_API int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, const void *k, int64_t ldk,
+                                 const void *v, int64_t ldv, const void *g_k, int rotate,
+                                 const int32_t *n_rows, const int32_t *ctx_len, void *kcache8,
+                                 void *vcache8, float *kscale, float *vscale, void *ws,
+                                 size_t ws_bytes, dflash_stream_t stream);
+
+/* dflash_attention over the 8-bit caches, for 1..B query rows per sequence ([DFlash] 二、块扩散草稿
+ * attention equations; one row is the single-token step of autoregressive decoding, several
+ * causal rows the target's verify pass). The rows' own keys and values have been appended
+ * before, at cache rows ctx_len[i] + j (dflash_kv_append8 with the same n_rows and ctx_len).
+ *   m           query rows per sequence, 0..B
+ *   q           bf16 [nb, m, Hq, hd]: rotated queries
+ *   kcache8, vcache8, kscale, vscale  the 8-bit caches; scales finite and >= 0
+ *   n_rows      int32 [nb] device, 0 <= n_rows[i] <= m: query rows of sequence i, or NULL: m. Rows
+ *               j >= n_rows[i] of out_o are left as they were.
+ *   ctx_len, max_ctx_hint  as for dflash_draft_block; ctx_len[i] + n_rows[i] <= Cmax
+ *   causal      0: every row attends to cache rows [0, ctx_len[i] + n_rows[i]); else row j to
+ *               [0, ctx_len[i] + j + 1)
+ *   out_o       bf16 [nb, m, Hq, hd]: softmax(q K^T / sqrt(hd)) V, query head h reading kv head
+ *               h / (Hq/Hkv)
+ * Cache rows beyond those attended to may hold anything. Errors as dflash_attention; a length or
+ * count out of range is clamped and reported as DFLASH_ERR_DEVICE_CHECK by dflash_status, and a
+ * page outside the pool is read as page 0 and reported. Bitwise reproducible as
+ * dflash_draft_block is. */
+DFLASH_API int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q,
+                                 const void *kcache8, const void *vcache8, const float *kscale,
+                                 const float *vscale, const int32_t *n_rows, const int32_t *ctx_len,
+                                 int max_ctx_hint, int causal, void *out_o, void *ws, size_t ws_bytes,
+                                 dflash_stream_t stream);
 
 /* Top-k of each row of an fp32 matrix with the same ordering rule as
  * dflash_lm_head_topk (value descending, ties to the lower column; [DFlash2] 洞察一 keeps

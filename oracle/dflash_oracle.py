@@ -678,3 +678,74 @@ def draft_step(cfg, W: dict, hv, n_commit, ctx_len, cache: KVCache, block_ids, t
     tau, bonus = accept(draft, target)
     return dict(ctx_len=new_len, x0_relay=x0r, hidden=hidden, logits=logits, ids=ids,
                 vals=vals, path=path, draft=draft, tau=tau, bonus=bonus)
+
+
+# --------------------------------------------------------------------------- rows and the 8-bit cache
+
+E4M3_MAX = 448.0
+SCALE_EXP = (-100, 119)
+
+
+def head_rows(x: np.ndarray, g, pos, base: float, eps: float, rotate: bool = True) -> np.ndarray:
+    """Rows x [rows, heads, hd] normed per head (g [hd], or None) and rotated at pos [rows]."""
+    if g is not None:
+        x = rmsnorm(x, g, eps)
+    return rope(x, np.asarray(pos), base) if rotate else x
+
+
+def e4m3_values() -> np.ndarray:
+    """The value of each of the 256 e4m3 codes (1 sign, 4 exponent, 3 mantissa bits, bias 7, no
+    infinities, NaN only at exponent and mantissa all ones)."""
+    c = np.arange(256)
+    e, m = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v = np.where((c & 127) == 127, np.nan, v)
+    return np.where(c & 128, -v, v)
+
+
+def e4m3_round(x: np.ndarray) -> np.ndarray:
+    """Nearest e4m3 value, ties to even, beyond the largest to the largest; NaN stays NaN."""
+    a = np.minimum(np.abs(x), E4M3_MAX)
+    step = np.exp2(np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
+    return np.copysign(np.minimum(np.round(a / step) * step, E4M3_MAX), x)
+
+
+def block_scale(amax: float) -> float:
+    """Smallest 2^e, e in SCALE_EXP, with amax / 2^e <= 448."""
+    if amax == 0:
+        return 2.0 ** SCALE_EXP[0]
+    m, e = np.frexp(amax)          # 448 = 0.875 * 2^9
+    return 2.0 ** int(np.clip(e - 9 + (m > 0.875), *SCALE_EXP))
+
+
+def append8_block(vals: np.ndarray, scale: float, kept: int, new: np.ndarray):
+    """One block of one kv head after an append: vals [64, hd] (e4m3 values), `kept` rows of earlier
+    appends stay, the rows new [n, hd] follow them. Returns (e4m3 values, scale)."""
+    fin = np.abs(new[np.isfinite(new)])
+    s = block_scale(float(fin.max()) if fin.size else 0.0)
+    out = vals.copy()
+    if kept:
+        s = max(s, scale)
+        if s > scale:
+            out[:kept] = e4m3_round(vals[:kept] * (scale / s))
+    out[kept:kept + len(new)] = e4m3_round(new / s)
+    return out, s
+
+
+def attention8(q: np.ndarray, K: np.ndarray, V: np.ndarray, ctx: int, causal: bool):
+    """q [n, Hq, hd], K and V [Hkv, ctx + n, hd] (dequantised). Returns o [n, Hq, hd] and, for
+    tolerances, sum p |v| [n, Hq, hd] and max_k sum_d |q_d k_d| / sqrt(hd) [n, Hq]."""
+    n, Hq, hd = q.shape
+    G = Hq // K.shape[0]
+    o, mag, dot = np.zeros(q.shape), np.zeros(q.shape), np.zeros((n, Hq))
+    for h in range(Hq):
+        k, v = K[h // G], V[h // G]
+        for j in range(n):
+            L = ctx + j + 1 if causal else ctx + n
+            x = k[:L] @ q[j, h] / np.sqrt(hd)
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            o[j, h] = p @ v[:L]
+            mag[j, h] = p @ np.abs(v[:L])
+            dot[j, h] = (np.abs(k[:L]) @ np.abs(q[j, h])).max() / np.sqrt(hd)
+    return o, mag, dot
