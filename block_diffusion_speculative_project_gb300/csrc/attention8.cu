@@ -1,4 +1,4 @@
-// Attention of m query rows per sequence over a cache held in 8 bits: e4m3 keys and values with
+// Attention of m query rows per sequence over a cache held in 8 bits (tcgen05): e4m3 keys and values with
 // one scale for each block of 64 rows and kv head.
 //   o = softmax(q K^T / sqrt(hd)) V over the rows [0, ctx + n) of the sequence's kv head, with
 //   `causal` only over [0, ctx + j + 1) for the query of row j; rows j >= n are not computed.
@@ -11,6 +11,7 @@
 // kernel joins in CTA order.
 #include <cfloat>
 #include <cmath>
+#include <mutex>
 
 #include <cuda_fp8.h>
 
@@ -99,146 +100,630 @@ __device__ Range8 find_range(const Attn8Params &p, int cta, int lane) {
 
 }  // namespace
 
-constexpr int kA8Threads = 256;
+// ---------------------------------------------------------------- tensor-core kernel
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t b) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(b, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half *>(&h));
+// RHO copies of the query rows fill the 128 lanes of the MMA (rows padded to 128 / RHO): the lanes
+// of copy c take only the c-th part of a unit's keys, the other parts' probabilities being zero
+// in the P operand, so that every SM quarter's warps share the exponentials of few rows.
+template <int HD>
+struct A8Cfg {
+  static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
+  static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
+  static constexpr int NS = HD == 128 ? 8 : 16;      // ring of units in 8 bits
+  static constexpr int ATOM16 = kUnit * 128;
+  static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's keys (or values) in f16
+  static constexpr int OFF_V16 = 2 * TILE16;
+  static constexpr int OFF_8 = 4 * TILE16;
+  static constexpr int OFF_STG = OFF_8 + NS * 2 * UNIT8;  // O of the copies c > 0, 16 columns at a time
+  static constexpr int STG = 3 * 32 * 17 * 4;             // (RHO - 1) * (128 / RHO) rows of 17 floats
+  static constexpr int OFF_ML = OFF_STG + STG;            // [2 halves][128 lanes] (maximum, sum)
+  static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
+  static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
+  static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t S_COL = 0;                // S of unit j in buffer j % 2: 64 columns each
+  static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
+  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // f16 queries: hd / 2 columns
+  static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of unit j in buffer j % 2: 32 columns each
+  static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
+};
+constexpr int kSeqCache = 128;
+constexpr int kDrainSpin = 1 << 22;
+// P is 2^(x - m_run + kPBase), m_run the maximum at the last rescale: O is rescaled only when the
+// maximum has grown by more than 2^kRescale, so P stays at most 2^15 in f16, and what is 2^-21 of
+// the largest still has all 11 bits (2^-31 one bit).
+constexpr float kPBase = 7.f, kRescale = 8.f;
+
+// Warps: softmax half h = 0, 1 (units j % 2 == h) in 4h .. 4h + 3 (warp w reads TMEM lanes of
+// quarter w % 4), producer, S issuer, PV issuer, then the converters (two for K, two for V).
+constexpr int kWProd = 8, kWS = 9, kWPV = 10, kWConv = 11, kNumConv = 4;
+constexpr int kA8Threads = (kWConv + kNumConv) * 32;
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kA8Threads) attn8_kernel(const __grid_constant__ Attn8Params p) {
-  extern __shared__ float sm[];
-  griddep_wait();
-  griddep_launch();
-  const int G = p.Hq / p.Hkv, R = G * p.m;
-  float *sQ = sm;                         // [R][HD]
-  float *sK = sQ + R * HD;                // [64][HD + 1]
-  float *sV = sK + kUnit * (HD + 1);      // [64][HD]
-  float *sP = sV + kUnit * HD;            // [R][64]
-  float *sM = sP + R * kUnit;             // [R] maximum, [R] sum, [R] rescale
-  __shared__ Range8 range;
-  const int t = threadIdx.x;
-  if (t < 32) {
-    const Range8 r = find_range(p, blockIdx.x, t);
-    if (t == 0) range = r;
-    if (blockIdx.x == 0)
-      for (int i = t; i < p.nb; i += 32) {
-        const int n = p.n_rows ? p.n_rows[i] : p.m, c = p.ctx_len[i];
-        if (n < 0 || n > p.m || c < 0 || c > p.max_ctx || static_cast<long long>(c) + max(n, 0) > p.Cmax)
-          flag_status(p.status, kStatusCheck);
-      }
+struct Walk8 {
+  int pair, unit, n, ctx, units, left, seg, seg_unit0;
+};
+__device__ __forceinline__ void walk_pair(Walk8 &w, const Attn8Params &p, const int2 *sseq) {
+  for (;;) {
+    const int i = w.pair / p.Hkv;
+    if (i < kSeqCache) {
+      w.n = sseq[i].x;
+      w.ctx = sseq[i].y;
+      w.units = w.n > 0 ? (w.ctx + w.n + kUnit - 1) / kUnit : 0;
+    } else {
+      const Seq8 s = seq8(p, i);
+      w.n = s.n;
+      w.ctx = s.ctx;
+      w.units = s.units;
+    }
+    if (w.units > 0) return;
+    w.pair = (i + 1) * p.Hkv;  // a sequence without rows (left > 0: one with rows follows)
   }
+}
+__device__ __forceinline__ bool walk_first(const Walk8 &w) { return w.unit == w.seg_unit0; }
+__device__ __forceinline__ bool walk_last(const Walk8 &w) { return w.left == 1 || w.unit == w.units - 1; }
+__device__ __forceinline__ void walk_next(Walk8 &w, const Attn8Params &p, const int2 *sseq) {
+  --w.left;
+  if (++w.unit == w.units) {
+    ++w.pair;
+    w.unit = 0;
+    w.seg_unit0 = 0;
+    ++w.seg;
+    if (w.left > 0) walk_pair(w, p, sseq);
+  }
+}
+// One past the last unit of the current segment.
+__device__ __forceinline__ int walk_end(const Walk8 &w) { return min(w.units, w.unit + w.left); }
+
+template <int KW>
+__device__ __forceinline__ void load_s(uint32_t taddr, float (&v)[KW]) {
+  if constexpr (KW == 64)
+    tmem_ld64(taddr, v);
+  else if constexpr (KW == 32)
+    tmem_ld32(taddr, v);
+  else
+    tmem_ld16(taddr, v);
+}
+template <int KW>
+__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t *v) {
+  if constexpr (KW == 64)
+    tmem_st32_raw(taddr, v);
+  else if constexpr (KW == 32)
+    tmem_st16_raw(taddr, v);
+  else
+    tmem_st8_raw(taddr, v);
+}
+
+// 16 e4m3 values to 32 bytes of f16 (exact).
+__device__ __forceinline__ void widen16(const uint4 &u, uint32_t (&h)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] & 0xFFFFu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] >> 16), __NV_E4M3);
+    h[2 * e] = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
+    h[2 * e + 1] = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
+  }
+}
+
+template <int HD, int RHO>
+__global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
+  using C = A8Cfg<HD>;
+  constexpr int KW = kUnit / RHO;      // keys of a unit per copy
+  constexpr int ROWS = 128 / RHO;      // padded query rows
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *sK16 = smem, *sV16 = smem + C::OFF_V16, *s8 = smem + C::OFF_8;
+  float *stage = reinterpret_cast<float *>(smem + C::OFF_STG);
+  float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+  uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint64_t *kv8_empty = kv8_full + C::NS;
+  uint64_t *k16_full = kv8_empty + C::NS;   // [2] unit j in buffer j % 2
+  uint64_t *v16_full = k16_full + 2;        // [2]
+  uint64_t *s_full = v16_full + 2;          // [2] S(j) complete: also K16 buffer j % 2 read
+  uint64_t *s_empty = s_full + 2;           // [2]
+  uint64_t *p_full = s_empty + 2;           // [2]
+  uint64_t *p_empty = p_full + 2;           // [2] PV(j) complete: P and V16 buffers j % 2 read
+  uint64_t *q_full = p_empty + 2;
+  uint64_t *q_empty = q_full + 1;
+  uint64_t *o_free = q_empty + 1;           // both O and ml read at a segment's end
+  uint64_t *ml_ready = o_free + 1;
+  uint64_t *half0 = ml_ready + 1;           // the four warps of half 0 among themselves
+  uint64_t *mma_done = half0 + 1;           // [2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
+  int *sched = reinterpret_cast<int *>(tmem_slot + 1);
+  static_assert((2 * 16 + 12 + 7) * 8 + 16 <= 512, "barrier region overflows");
+  int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  const int R = G * p.m;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&kv8_full[s], 1);
+      mbar_init(&kv8_empty[s], kNumConv);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&k16_full[b], kNumConv / 2);
+      mbar_init(&v16_full[b], kNumConv / 2);
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_empty[b], 4);
+      mbar_init(&p_full[b], 4);
+      mbar_init(&p_empty[b], 1);
+      mbar_init(&mma_done[b], 1);
+    }
+    mbar_init(q_full, 4);
+    mbar_init(q_empty, 1);
+    mbar_init(o_free, 4);
+    mbar_init(ml_ready, 4);
+    mbar_init(half0, 4);
+    fence_mbar_init();
+  }
+  if (warp == kWS) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch();
+  if (warp == kWProd) {
+    const Range8 r = find_range(p, blockIdx.x, lane);
+    if (lane == 0) {
+      sched[0] = r.pair;
+      sched[1] = r.unit;
+      sched[2] = static_cast<int>(r.count);
+    }
+  } else if (warp == kWConv) {
+    for (int i = lane; i < p.nb && i < kSeqCache; i += 32) {
+      const Seq8 s = seq8(p, i);
+      sseq[i] = make_int2(s.n, s.ctx);
+    }
+  } else if (warp == kWPV && blockIdx.x == 0) {
+    for (int i = lane; i < p.nb; i += 32) {
+      const int n = p.n_rows ? p.n_rows[i] : p.m, c = p.ctx_len[i];
+      if (n < 0 || n > p.m || c < 0 || c > p.max_ctx || static_cast<long long>(c) + max(n, 0) > p.Cmax)
+        flag_status(p.status, kStatusCheck);
+    }
+  }
+  tc_fence_before();
   __syncthreads();
-  long long left = range.count;
-  int pair = range.pair, unit = range.unit;
-  const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-  constexpr int CPT = 16;                 // output columns per thread of a row
-  constexpr int TPR = HD / CPT;
-  while (left > 0) {
-    const int i = pair / p.Hkv, g = pair % p.Hkv;
-    const Seq8 s = seq8(p, i);
-    if (s.units == 0) {
-      ++pair;
-      continue;
-    }
-    const int unit0 = unit;
-    const int last = static_cast<int>(min(static_cast<long long>(s.units), unit + left));
-    for (int e = t; e < R * HD; e += kA8Threads) {
-      const int r = e / HD, d = e % HD, j = r / G, h = g * G + r % G;
-      sQ[e] = __uint_as_float(static_cast<uint32_t>(p.q[((static_cast<size_t>(i) * p.m + j) * p.Hq + h) * HD + d]) << 16);
-    }
-    for (int r = t; r < R; r += kA8Threads) {
-      sM[r] = kNoMax;
-      sM[R + r] = 0.f;
-    }
-    float acc[4][CPT];
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int c = 0; c < CPT; ++c) acc[a][c] = 0.f;
-    for (; unit < last; ++unit, --left) {
-      const long long blk = block_of(p, i, g, unit);
-      const float sk = p.ks[blk], sv = p.vs[blk];
-      const int keys = s.ctx + s.n - unit * kUnit;
-      __syncthreads();
-      for (int e = t; e < kUnit * HD; e += kA8Threads) {
-        const int k = e / HD, d = e % HD;
-        sK[k * (HD + 1) + d] = k < keys ? e4m3_to_f32(p.k8[blk * (kUnit * HD) + e]) * sk : 0.f;
-        sV[e] = k < keys ? e4m3_to_f32(p.v8[blk * (kUnit * HD) + e]) * sv : 0.f;
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int nunits = sched[2];
+  Walk8 w;
+  w.pair = sched[0];
+  w.unit = sched[1];
+  w.left = nunits;
+  w.seg = 0;
+  w.seg_unit0 = w.unit;
+  w.n = w.ctx = w.units = 0;
+  if (nunits > 0) walk_pair(w, p, sseq);
+
+  if (nunits == 0) {
+    // nothing to do
+  } else if (warp == kWProd) {
+    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each. The
+    // warp reads the block indices of 32 units at once, lane 0 issues the copies.
+    const uint64_t pol = policy_evict_first();
+    bool ok = !p.stall;
+    int j = 0, issued = 0, blk = 0;
+    for (; j < nunits && ok; ++j) {
+      const int k = (w.unit - w.seg_unit0) & 31;
+      const int i = w.pair / p.Hkv, g = w.pair % p.Hkv;
+      if (k == 0) blk = static_cast<int>(block_of(p, i, g, min(w.unit + lane, walk_end(w) - 1)));
+      const long long b = __shfl_sync(0xffffffffu, blk, k);
+      const int st = j % C::NS;
+      if (lane == 0) {
+        ok = j < C::NS || mbar_wait(&kv8_empty[st], ((j / C::NS) - 1) & 1, p.max_spin);
+        if (ok) {
+          uint8_t *dst = s8 + st * 2 * C::UNIT8;
+          mbar_arrive_expect_tx(&kv8_full[st], 2 * C::UNIT8);
+          bulk_load(dst, p.k8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
+          bulk_load(dst + C::UNIT8, p.v8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
+          ++issued;
+        }
       }
-      __syncthreads();
-      for (int e = t; e < R * kUnit; e += kA8Threads) {
-        const int r = e / kUnit, k = e % kUnit;
-        float x = 0.f;
-        for (int d = 0; d < HD; ++d) x = fmaf(sQ[r * HD + d], sK[k * (HD + 1) + d], x);
-        const int lim = p.causal ? s.ctx + r / G + 1 : s.ctx + s.n;
-        sP[e] = unit * kUnit + k < lim ? x * sl2 : -INFINITY;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      walk_next(w, p, sseq);
+    }
+    if (lane == 0) {
+      if (!ok && !p.stall) flag_status(p.status, kStatusTimeout);
+      // every issued copy must land before the CTA may exit (bounded)
+      for (int k = max(0, issued - C::NS); k < issued; ++k)
+        mbar_wait(&kv8_full[k % C::NS], (k / C::NS) & 1, kDrainSpin);
+    }
+  } else if (warp == kWS) {
+    if (lane == 0) {
+      // ---------------- S issuer: S(j) = Q K(j)^T, queries from tensor memory
+      constexpr uint32_t id_s = idesc_f16_f32(128, kUnit);
+      const uint64_t kd0 = sw128_kmajor_desc(smem_u32(sK16));
+      bool ok = true;
+      for (int j = 0; j < nunits; ++j) {
+        const int b = j & 1;
+        if (walk_first(w)) ok = mbar_wait(q_full, w.seg & 1, p.max_spin);
+        ok = ok && mbar_wait(&k16_full[b], (j >> 1) & 1, p.max_spin);
+        ok = ok && (j < 2 || mbar_wait(&s_empty[b], ((j >> 1) - 1) & 1, p.max_spin));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = kd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          tc_mma_bf16_tmem_a(tmem + C::S_COL + b * kUnit, tmem + C::Q_COL + kk * 8,
+                             kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM16 + (kk & 3) * 32) >> 4), id_s,
+                             kk > 0 ? 1u : 0u);
+        tc_commit(&s_full[b]);
+        if (walk_last(w)) tc_commit(q_empty);
+        walk_next(w, p, sseq);
       }
-      __syncthreads();
-      for (int r = t >> 5; r < R; r += kA8Threads / 32) {
-        const int l = t & 31;
-        const float x0 = sP[r * kUnit + l], x1 = sP[r * kUnit + l + 32];
-        float mx = fmaxf(x0, x1);
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m0 = sM[r], m1 = fmaxf(m0, mx);
-        const float e0 = exp2f(x0 - m1), e1 = exp2f(x1 - m1);
-        float sum = e0 + e1;
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        sP[r * kUnit + l] = e0;
-        sP[r * kUnit + l + 32] = e1;
+      if (!ok) flag_status(p.status, kStatusTimeout);
+      // every issued MMA must complete before TMEM is freed (bounded)
+      tc_commit(&mma_done[0]);
+      mbar_wait(&mma_done[0], 0, kDrainSpin);
+    }
+  } else if (warp == kWPV) {
+    if (lane == 0) {
+      // ---------------- PV issuer: O_{j%2} += P(j) V(j); the first unit of each half in a segment
+      // starts the accumulator, after both O of the previous segment were read
+      constexpr uint32_t id_pv = idesc_f16_f32(128, HD) | kIdescBMajorMN;
+      const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
+      bool ok = true;
+      int jf = 0;
+      for (int j = 0; j < nunits; ++j) {
+        const int b = j & 1;
+        if (walk_first(w)) jf = j;
+        const bool start = j < jf + 2;
+        ok = mbar_wait(&v16_full[b], (j >> 1) & 1, p.max_spin);
+        ok = ok && mbar_wait(&p_full[b], (j >> 1) & 1, p.max_spin);
+        if (start && w.seg > 0) ok = ok && mbar_wait(o_free, (w.seg - 1) & 1, p.max_spin);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kUnit / 16; ++kk)
+          tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
+                             vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
+                             (!start || kk > 0) ? 1u : 0u);
+        tc_commit(&p_empty[b]);
+        walk_next(w, p, sseq);
+      }
+      if (!ok) flag_status(p.status, kStatusTimeout);
+      tc_commit(&mma_done[1]);
+      mbar_wait(&mma_done[1], 0, kDrainSpin);
+    }
+  } else if (warp >= kWConv) {
+    // ---------------- converters: e4m3 tiles to f16 tiles in the layout of a 128-byte-swizzled
+    // copy (rows of 64 values, 16-byte chunk c of row r at c ^ (r & 7)); warps 0, 1 keys, 2, 3 values
+    const int cw = warp - kWConv;
+    const bool is_v = cw >= 2;
+    uint64_t *full16 = is_v ? v16_full : k16_full;
+    uint64_t *empty16 = is_v ? p_empty : s_full;   // the MMAs that read the buffer have completed
+    uint8_t *out = is_v ? sV16 : sK16;
+    constexpr int CPR = HD / 16;                   // 16-byte chunks of a row in 8 bits
+    constexpr int PER = kUnit * CPR / 64;          // chunks per thread (two warps)
+    const int t = (cw & 1) * 32 + lane;
+    bool ok = true;
+    for (int j = 0; j < nunits; ++j) {
+      const int st = j % C::NS, b = j & 1;
+      const int keys = w.ctx + w.n - w.unit * kUnit;  // rows of the unit that hold keys
+      ok = mbar_wait(&kv8_full[st], (j / C::NS) & 1, p.max_spin);
+      ok = ok && (j < 2 || mbar_wait(&empty16[b], ((j >> 1) - 1) & 1, p.max_spin));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint8_t *src = s8 + st * 2 * C::UNIT8 + (is_v ? C::UNIT8 : 0);
+      uint8_t *dst = out + b * C::TILE16;
+#pragma unroll 4
+      for (int e = 0; e < PER; ++e) {
+        const int c = t + e * 64;
+        const int r = c / CPR, cc = c % CPR;
+        uint4 u = *reinterpret_cast<const uint4 *>(src + c * 16);
+        // V rows beyond the last key may hold anything (even NaN); P is 0 there
+        if (is_v && r >= keys) u = make_uint4(0, 0, 0, 0);
+        uint32_t h[8];
+        widen16(u, h);
+        uint8_t *row = dst + (cc >> 2) * C::ATOM16 + r * 128;
+        const int c0 = (cc & 3) * 2;
+        // lanes of the second atom store their halves in the other order: no bank conflicts
+        const int first = (cc >> 2) & 1;
+        const uint4 a = first ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+        const uint4 d = first ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
+        *reinterpret_cast<uint4 *>(row + (((c0 + first) ^ (r & 7)) << 4)) = a;
+        *reinterpret_cast<uint4 *>(row + (((c0 + 1 - first) ^ (r & 7)) << 4)) = d;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&full16[b]);
+        mbar_arrive(&kv8_empty[st]);
+      }
+      walk_next(w, p, sseq);
+    }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+  } else {
+    // ---------------- softmax: thread = TMEM lane; lane l holds query row l % ROWS, copy l / ROWS
+    const int half = warp >> 2, q = warp & 3;
+    const int tl = q * 32 + lane;
+    const int r = tl % ROWS, copy = tl / ROWS;
+    const int k0 = copy * KW;
+    const bool real = r < R;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int jq = r / G, hq = r % G;   // row r: query row jq of query head g * G + hq
+    const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
+    if (RHO > 1) {  // the other copies' parts of the P rows stay zero
+      const uint32_t z[32] = {};
+      tmem_st32_raw(trow + C::P_COL + half * 32, z);
+      tmem_wait_st();
+    }
+    // Barrier of half 0's warps, bounded like every other wait.
+    uint32_t half0_phase = 0;
+    auto half0_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(half0);
+      const bool done = mbar_wait(half0, half0_phase, p.max_spin);
+      half0_phase ^= 1;
+      return __all_sync(0xffffffffu, done) != 0;
+    };
+    bool ok = true;
+    float m_run = kNoMax, l_run = 0.f, qfac = 0.f;
+    float ks_c = 0.f, lv_c = 0.f, iv_c = 0.f;   // scales of 32 units (this lane's): K, log2 of V, 1 / V
+    float ks_n = 0.f, vs_n = 0.f;               // the next 32
+    int jf = 0;
+    for (int j = 0; j < nunits; ++j) {
+      const int i = w.pair / p.Hkv, g = w.pair % p.Hkv;
+      const int ku = w.unit - w.seg_unit0;
+      if ((ku & 31) == 0) {
+        const int end = walk_end(w) - 1;
+        if (ku == 0) {
+          const long long b = block_of(p, i, g, min(w.unit + lane, end));
+          ks_n = p.ks[b];
+          vs_n = p.vs[b];
+        }
+        ks_c = ks_n;
+        lv_c = vs_n == 0.f ? 0.f : log2f(vs_n);
+        iv_c = vs_n == 0.f ? 0.f : 1.f / vs_n;   // 0 marks a block of zeros
+        if (w.unit + 32 <= end) {
+          const long long b = block_of(p, i, g, min(w.unit + 32 + lane, end));
+          ks_n = p.ks[b];
+          vs_n = p.vs[b];
+        }
+      }
+      if (walk_first(w)) {
+        jf = j;
+        m_run = kNoMax;
+        l_run = 0.f;
+        // this thread's query row, scaled by a power of two so that its largest value lies in
+        // [2^14, 2^15): exact in f16 down to 2^-31 of it
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + ((static_cast<size_t>(i) * p.m + jq) * p.Hq + g * G + hq) * HD);
+        const bool have = real && jq < w.n;
+        float am = 0.f;
+#pragma unroll 8
+        for (int e = 0; e < HD / 8; ++e) {
+          const uint4 u = have ? src[e] : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[f] << 16)), fabsf(__uint_as_float(x[f] & 0xFFFF0000u))));
+        }
+        int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
+        ex = ex == 128 ? 14 : max(ex, -100);
+        const float mul = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+        qfac = sl2 * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+        if (half == 0) {
+          ok = w.seg == 0 || mbar_wait(q_empty, (w.seg - 1) & 1, p.max_spin);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int part = 0; part < HD / 32; ++part) {
+            uint32_t h[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
+              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                const __half2 y = __floats2half2_rn(__uint_as_float(x[f] << 16) * mul,
+                                                    __uint_as_float(x[f] & 0xFFFF0000u) * mul);
+                h[4 * e + f] = *reinterpret_cast<const uint32_t *>(&y);
+              }
+            }
+            tmem_st16_raw(trow + C::Q_COL + part * 16, h);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+        }
+      }
+      if ((j & 1) == half) {
+        const bool first = j < jf + 2;  // first unit of this half in the segment
+        const float ks = __shfl_sync(0xffffffffu, ks_c, ku & 31);
+        const float lv = __shfl_sync(0xffffffffu, lv_c, ku & 31);
+        const float iv = __shfl_sync(0xffffffffu, iv_c, ku & 31);
+        const int lim = p.causal ? min(w.ctx + jq + 1, w.ctx + w.n) : w.ctx + w.n;
+        const int nv = lim - w.unit * kUnit - k0;  // keys this thread sees of its part
+        ok = mbar_wait(&s_full[half], (j >> 1) & 1, p.max_spin);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float sv[KW];
+        load_s<KW>(trow + C::S_COL + half * kUnit + k0, sv);
+        tc_fence_before();
         __syncwarp();
-        if (l == 0) {
-          const float al = exp2f(m0 - m1);
-          sM[r] = m1;
-          sM[R + r] = sM[R + r] * al + sum;
-          sM[2 * R + r] = al;
+        if (lane == 0) mbar_arrive(&s_empty[half]);
+
+        if (__any_sync(0xffffffffu, nv < KW)) {
+#pragma unroll
+          for (int c = 0; c < KW; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
+        }
+        const float c1 = fmaxf(qfac * ks, 1e-37f);
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int c = 4; c < KW; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
+        const float m_new = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c1, lv);
+        const bool need = m_new - m_run > kRescale;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2f(m_run - m_new);
+          m_run = m_new;
+          l_run *= alpha;
+        }
+        // P buffer and O_half: free once PV of this half's previous unit has completed
+        if (j >= 2) {
+          ok = mbar_wait(&p_empty[half], ((j >> 1) - 1) & 1, p.max_spin);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        if (!first && __any_sync(0xffffffffu, need && real)) {
+#pragma unroll 1
+          for (int cc = 0; cc < HD / 16; ++cc) {
+            float ov[16];
+            tmem_ld16(trow + C::O_COL + half * HD + cc * 16, ov);
+            uint32_t x[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(ov[c] * alpha);
+            tmem_st16_raw(trow + C::O_COL + half * HD + cc * 16, x);
+          }
+        }
+        const float c2 = lv - m_run + kPBase;
+        uint32_t pk[KW / 2];
+        float ls[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KW; c += 2) {
+          const float p0 = ex2f(fmaf(sv[c], c1, c2));
+          const float p1 = ex2f(fmaf(sv[c + 1], c1, c2));
+          ls[0] += p0;
+          ls[1] += p1;
+          const __half2 y = __floats2half2_rn(p0, p1);
+          pk[c / 2] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+        l_run = fmaf(ls[0] + ls[1], iv == 0.f ? 1.f : iv, l_run);
+        if (iv == 0.f) {
+#pragma unroll
+          for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
+        }
+        store_p<KW>(trow + C::P_COL + half * 32 + k0 / 2, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[half]);
+      }
+
+      if (walk_last(w)) {
+        // segment [jf, j]: the last unit of each half in it, or -1
+        const int seg = w.seg;
+        const int last0 = (j & 1) == 0 ? j : (j - 1 >= jf ? j - 1 : -1);
+        const int last1 = (j & 1) == 1 ? j : (j - 1 >= jf ? j - 1 : -1);
+        const int mine = half ? last1 : last0;
+        ok = mine < 0 || mbar_wait(&p_empty[half], (mine >> 1) & 1, p.max_spin);
+        // the (maximum, sum) slots are free once the previous segment's were read
+        if (half == 1) ok = ok && (seg == 0 || mbar_wait(o_free, (seg - 1) & 1, p.max_spin));
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const float2 own = mine >= 0 ? make_float2(m_run, l_run) : make_float2(kNoMax, 0.f);
+        ml[half * 128 + tl] = own;
+        if (half == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_ready);
+        } else {
+          ok = mbar_wait(ml_ready, seg & 1, p.max_spin) && ok;
+          if (!__all_sync(0xffffffffu, ok) || !half0_sync()) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float M = kNoMax;
+#pragma unroll
+          for (int c = 0; c < RHO; ++c)
+            M = fmaxf(M, fmaxf(ml[c * ROWS + r].x, ml[128 + c * ROWS + r].x));
+          float L = 0.f;
+#pragma unroll
+          for (int c = 0; c < RHO; ++c) {
+            const float2 x = ml[c * ROWS + r], y = ml[128 + c * ROWS + r];
+            L += x.y * ex2f(x.x - M) + y.y * ex2f(y.x - M);
+          }
+          const bool has0 = last0 >= 0, has1 = last1 >= 0;
+          const float a0 = ex2f(own.x - M), a1 = ex2f(ml[128 + tl].x - M);
+          const bool whole = w.seg_unit0 == 0 && w.unit == w.units - 1;
+          const size_t row = (static_cast<size_t>(w.pair) + blockIdx.x) * R + r;
+          const float inv = 1.0f / L;
+          const bool put = real && jq < w.n;
+#pragma unroll 1
+          for (int cc = 0; cc < HD / 16 && ok; ++cc) {
+            float ov[16], o1[16];
+            if (has0) tmem_ld16(trow + C::O_COL + cc * 16, ov);
+            if (has1) tmem_ld16(trow + C::O_COL + HD + cc * 16, o1);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) ov[c] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1[c] * a1 : 0.f);
+            if (RHO > 1) {
+              if (copy > 0) {
+                float *to = stage + ((copy - 1) * ROWS + r) * 17;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) to[c] = ov[c];
+              }
+              ok = half0_sync();
+              if (copy == 0) {
+#pragma unroll
+                for (int x = 0; x < RHO - 1; ++x) {
+                  const float *from = stage + (x * ROWS + r) * 17;
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) ov[c] += from[c];
+                }
+              }
+              ok = ok && half0_sync();
+            }
+            if (copy == 0 && put && whole) {
+              uint16_t *dst = p.o + ((static_cast<size_t>(i) * p.m + jq) * p.Hq + g * G + hq) * HD + cc * 16;
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                reinterpret_cast<uint4 *>(dst)[v] =
+                    make_uint4(pack_bf16x2(ov[8 * v] * inv, ov[8 * v + 1] * inv),
+                               pack_bf16x2(ov[8 * v + 2] * inv, ov[8 * v + 3] * inv),
+                               pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
+                               pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
+            } else if (copy == 0 && put) {
+              float *dst = p.part_o + row * HD + cc * 16;
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                reinterpret_cast<float4 *>(dst)[v] =
+                    make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (put && copy == 0 && !whole)
+            *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(M, L);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
         }
       }
-      __syncthreads();
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int slot = t + a * kA8Threads;
-        const int r = slot / TPR, d0 = (slot % TPR) * CPT;
-        if (r >= R) continue;
-        const float al = sM[2 * R + r];
-#pragma unroll
-        for (int c = 0; c < CPT; ++c) acc[a][c] *= al;
-        for (int k = 0; k < kUnit; ++k) {
-          const float w = sP[r * kUnit + k];
-#pragma unroll
-          for (int c = 0; c < CPT; ++c) acc[a][c] = fmaf(w, sV[k * HD + d0 + c], acc[a][c]);
-        }
-      }
+      walk_next(w, p, sseq);
     }
-    const bool whole = unit0 == 0 && unit == s.units;
-    const long long slot0 = static_cast<long long>(pair) + blockIdx.x;
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int slot = t + a * kA8Threads;
-      const int r = slot / TPR, d0 = (slot % TPR) * CPT;
-      if (r >= R || r / G >= s.n) continue;
-      if (whole) {
-        const float inv = 1.f / sM[R + r];
-        uint16_t *dst = p.o + ((static_cast<size_t>(i) * p.m + r / G) * p.Hq + g * G + r % G) * HD + d0;
-#pragma unroll
-        for (int c = 0; c < CPT; c += 2)
-          *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(acc[a][c] * inv, acc[a][c + 1] * inv);
-      } else {
-        float *dst = p.part_o + (slot0 * R + r) * HD + d0;
-#pragma unroll
-        for (int c = 0; c < CPT; ++c) dst[c] = acc[a][c];
-        if (d0 == 0) {
-          p.part_ml[(slot0 * R + r) * 2] = sM[r];
-          p.part_ml[(slot0 * R + r) * 2 + 1] = sM[R + r];
-        }
-      }
-    }
-    __syncthreads();
-    if (unit == s.units) {
-      ++pair;
-      unit = 0;
-    }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -304,22 +789,40 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
     *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int HD>
+// The dynamic shared memory limit is a property of the kernel on one device.
+template <int HD, int RHO>
+static cudaError_t configure_attn8() {
+  static std::mutex mutex;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(attn8_kernel<HD, RHO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(A8Cfg<HD>::SMEM));
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <int HD, int RHO>
 static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
   const int R = (p.Hq / p.Hkv) * p.m;
-  const size_t smem = sizeof(float) * (static_cast<size_t>(R) * HD + kUnit * (HD + 1) + kUnit * HD + R * kUnit + 3 * R);
-  static const cudaError_t configured =
-      cudaFuncSetAttribute(attn8_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (configured != cudaSuccess) return configured;
-  cudaError_t e = launch_pdl(attn8_kernel<HD>, dim3(p.grid), dim3(kA8Threads), smem, s, p);
+  cudaError_t e = configure_attn8<HD, RHO>();
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn8_kernel<HD, RHO>, dim3(p.grid), dim3(kA8Threads), A8Cfg<HD>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn8_merge_kernel<HD>, dim3(p.nb * p.Hkv, (R + kMerge8Warps - 1) / kMerge8Warps),
                     dim3(kMerge8Warps * 32), 0, s, p);
 }
 
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s) {
-  if (p.Hq % p.Hkv != 0 || (p.Hq / p.Hkv) * p.m > 128) return cudaErrorInvalidValue;
-  return p.hd == 128 ? launch_attn8<128>(p, s) : launch_attn8<64>(p, s);
+  const int R = (p.Hq / p.Hkv) * p.m;
+  if (p.Hq % p.Hkv != 0 || R > 128) return cudaErrorInvalidValue;
+  // copies of the query rows that fill the MMA's 128
+  if (p.hd == 128)
+    return R > 64 ? launch_attn8<128, 1>(p, s) : R > 32 ? launch_attn8<128, 2>(p, s) : launch_attn8<128, 4>(p, s);
+  return R > 64 ? launch_attn8<64, 1>(p, s) : R > 32 ? launch_attn8<64, 2>(p, s) : launch_attn8<64, 4>(p, s);
 }
 
 }  // namespace df

@@ -561,3 +561,14 @@ def test_decode_loop_over_the_8_bit_cache():
             check_attention(c, layer, R, q, n, lens, True, out, f"step {step} layer {layer}")
         lens = lens + (np.minimum(n, 2) if R == m else n)  # two of the candidates are accepted
     assert c.status() == 0
+
+
+def test_attention8_wait_limit_is_reported():
+    """With the producer held back every wait runs out after max_spin polls: the status says so, the
+    kernels return, and the context stays usable."""
+    D = lib()
+    c = Cache(8, 2, 128, 512, 3, N=1, max_spin=2000, flags=1 << 30)
+    q = queries(c, 4)
+    c.attend(0, 4, q, None, [100, 0, 400], False)
+    assert c.status() == D.DFLASH_ERR_TIMEOUT
+    assert c.status() == D.DFLASH_OK
