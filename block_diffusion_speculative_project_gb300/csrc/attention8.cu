@@ -105,21 +105,27 @@ __device__ Range8 find_range(const Attn8Params &p, int cta, int lane) {
 // RHO copies of the query rows fill the 128 lanes of the MMA (rows padded to 128 / RHO): the lanes
 // of copy c take only the c-th part of a unit's keys, the other parts' probabilities being zero
 // in the P operand, so that every SM quarter's warps share the exponentials of few rows.
-template <int HD>
+template <int HD, int RHO>
 struct A8Cfg {
+  static constexpr int KW = kUnit / RHO;             // keys of a unit per copy
+  static constexpr int ROWS = 128 / RHO;             // padded query rows
   static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
-  static constexpr int NS = HD == 128 ? 8 : 16;      // ring of units in 8 bits
+  static constexpr int NS = HD == 128 ? 7 : 14;      // ring of units in 8 bits
   static constexpr int ATOM16 = kUnit * 128;
   static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's keys (or values) in f16
+  static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
+  static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of a half's exchange of O between copies
   static constexpr int OFF_V16 = 2 * TILE16;
   static constexpr int OFF_8 = 4 * TILE16;
-  static constexpr int OFF_STG = OFF_8 + NS * 2 * UNIT8;  // O of the copies c > 0, 16 columns at a time
-  static constexpr int STG = 3 * 32 * 17 * 4;             // (RHO - 1) * (128 / RHO) rows of 17 floats
-  static constexpr int OFF_ML = OFF_STG + STG;            // [2 halves][128 lanes] (maximum, sum)
-  static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
+  static constexpr int OFF_Q = OFF_8 + NS * 2 * UNIT8;
+  static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
+  static constexpr int OFF_ML = OFF_STG + 2 * STAGE * 4;  // [2 halves][128 lanes] (maximum, sum)
+  static constexpr int OFF_SC = OFF_ML + 2 * 128 * 8;     // [2 chunks][32 units] scales
+  static constexpr int OFF_BAR = OFF_SC + 64 * 16;
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
   static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0;                // S of unit j in buffer j % 2: 64 columns each
   static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
@@ -145,40 +151,34 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-struct Walk8 {
-  int pair, unit, n, ctx, units, left, seg, seg_unit0;
+// A unit inside a CTA's range: sequence i, kv head g, unit of `units`.
+struct Pos8 {
+  int i, g, unit, units, n, ctx;
 };
-__device__ __forceinline__ void walk_pair(Walk8 &w, const Attn8Params &p, const int2 *sseq) {
-  for (;;) {
-    const int i = w.pair / p.Hkv;
-    if (i < kSeqCache) {
-      w.n = sseq[i].x;
-      w.ctx = sseq[i].y;
+__device__ __forceinline__ void pos_seq(Pos8 &w, const Attn8Params &p, const int2 *sseq) {
+  for (;; ++w.i) {  // a sequence without rows has no units (one with rows follows)
+    if (w.i < kSeqCache) {
+      w.n = sseq[w.i].x;
+      w.ctx = sseq[w.i].y;
       w.units = w.n > 0 ? (w.ctx + w.n + kUnit - 1) / kUnit : 0;
     } else {
-      const Seq8 s = seq8(p, i);
+      const Seq8 s = seq8(p, w.i);
       w.n = s.n;
       w.ctx = s.ctx;
       w.units = s.units;
     }
     if (w.units > 0) return;
-    w.pair = (i + 1) * p.Hkv;  // a sequence without rows (left > 0: one with rows follows)
   }
 }
-__device__ __forceinline__ bool walk_first(const Walk8 &w) { return w.unit == w.seg_unit0; }
-__device__ __forceinline__ bool walk_last(const Walk8 &w) { return w.left == 1 || w.unit == w.units - 1; }
-__device__ __forceinline__ void walk_next(Walk8 &w, const Attn8Params &p, const int2 *sseq) {
-  --w.left;
-  if (++w.unit == w.units) {
-    ++w.pair;
-    w.unit = 0;
-    w.seg_unit0 = 0;
-    ++w.seg;
-    if (w.left > 0) walk_pair(w, p, sseq);
+// To the pair after this one.
+__device__ __forceinline__ void pos_next_pair(Pos8 &w, const Attn8Params &p, const int2 *sseq) {
+  w.unit = 0;
+  if (++w.g == p.Hkv) {
+    w.g = 0;
+    ++w.i;
+    pos_seq(w, p, sseq);
   }
 }
-// One past the last unit of the current segment.
-__device__ __forceinline__ int walk_end(const Walk8 &w) { return min(w.units, w.unit + w.left); }
 
 template <int KW>
 __device__ __forceinline__ void load_s(uint32_t taddr, float (&v)[KW]) {
@@ -199,29 +199,39 @@ __device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t *v) {
     tmem_st8_raw(taddr, v);
 }
 
-// 16 e4m3 values to 32 bytes of f16 (exact).
-__device__ __forceinline__ void widen16(const uint4 &u, uint32_t (&h)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] & 0xFFFFu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[e] >> 16), __NV_E4M3);
-    h[2 * e] = static_cast<uint32_t>(lo.x) | (static_cast<uint32_t>(lo.y) << 16);
-    h[2 * e + 1] = static_cast<uint32_t>(hi.x) | (static_cast<uint32_t>(hi.y) << 16);
-  }
+// 8 e4m3 values to f16 (exact).
+__device__ __forceinline__ uint4 widen8(uint2 u) {
+  uint4 h;
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+      "mov.b32 {a, b}, %4;\n\t"
+      "mov.b32 {c, d}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+      : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
+      : "r"(u.x), "r"(u.y));
+  return h;
+}
+
+// One of the warp's threads, the same one every time; the branch on it leaves the code around it
+// warp-uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
 }
 
 template <int HD, int RHO>
 __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
-  using C = A8Cfg<HD>;
-  constexpr int KW = kUnit / RHO;      // keys of a unit per copy
-  constexpr int ROWS = 128 / RHO;      // padded query rows
+  using C = A8Cfg<HD, RHO>;
+  constexpr int KW = C::KW, ROWS = C::ROWS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint8_t *sK16 = smem, *sV16 = smem + C::OFF_V16, *s8 = smem + C::OFF_8;
-  float *stage = reinterpret_cast<float *>(smem + C::OFF_STG);
+  uint8_t *sK16 = smem, *sV16 = smem + C::OFF_V16, *s8 = smem + C::OFF_8, *sQ = smem + C::OFF_Q;
   float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+  float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
   uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv8_empty = kv8_full + C::NS;
   uint64_t *k16_full = kv8_empty + C::NS;   // [2] unit j in buffer j % 2
@@ -230,15 +240,19 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   uint64_t *s_empty = s_full + 2;           // [2]
   uint64_t *p_full = s_empty + 2;           // [2]
   uint64_t *p_empty = p_full + 2;           // [2] PV(j) complete: P and V16 buffers j % 2 read
-  uint64_t *q_full = p_empty + 2;
+  uint64_t *sc_full = p_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
+  uint64_t *sc_empty = sc_full + 2;         // [2]
+  uint64_t *half_bar = sc_empty + 2;        // [2] the four warps of a half among themselves
+  uint64_t *mma_done = half_bar + 2;        // [2]
+  uint64_t *q8_full = mma_done + 2;         // a segment's query rows have landed
+  uint64_t *q8_empty = q8_full + 1;
+  uint64_t *q_full = q8_empty + 1;          // and are in tensor memory
   uint64_t *q_empty = q_full + 1;
-  uint64_t *o_free = q_empty + 1;           // both O and ml read at a segment's end
-  uint64_t *ml_ready = o_free + 1;
-  uint64_t *half0 = ml_ready + 1;           // the four warps of half 0 among themselves
-  uint64_t *mma_done = half0 + 1;           // [2]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
+  uint64_t *seg_bar = q_empty + 1;          // both halves: (maximum, sum) of a segment written
+  uint64_t *o_free = seg_bar + 1;           // both O and ml read
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * 16 + 12 + 7) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((2 * C::NS + 20 + 6) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -257,13 +271,17 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       mbar_init(&s_empty[b], 4);
       mbar_init(&p_full[b], 4);
       mbar_init(&p_empty[b], 1);
+      mbar_init(&sc_full[b], 1);
+      mbar_init(&sc_empty[b], 8);
+      mbar_init(&half_bar[b], 4);
       mbar_init(&mma_done[b], 1);
     }
+    mbar_init(q8_full, 1);
+    mbar_init(q8_empty, 8);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
-    mbar_init(o_free, 4);
-    mbar_init(ml_ready, 4);
-    mbar_init(half0, 4);
+    mbar_init(seg_bar, 8);
+    mbar_init(o_free, 8);
     fence_mbar_init();
   }
   if (warp == kWS) {
@@ -294,29 +312,62 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int nunits = sched[2];
-  Walk8 w;
-  w.pair = sched[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const int nunits = __shfl_sync(0xffffffffu, sched[2], 0);
+  Pos8 w;
+  w.i = sched[0] / p.Hkv;
+  w.g = sched[0] % p.Hkv;
   w.unit = sched[1];
-  w.left = nunits;
-  w.seg = 0;
-  w.seg_unit0 = w.unit;
-  w.n = w.ctx = w.units = 0;
-  if (nunits > 0) walk_pair(w, p, sseq);
+  if (nunits > 0) pos_seq(w, p, sseq);
 
+  // Every role goes through the CTA's segments (runs of units of one pair): `cnt` units from unit
+  // j0 of the CTA on. A wait that runs out ends the role (ok = false).
   if (nunits == 0) {
     // nothing to do
   } else if (warp == kWProd) {
-    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each. The
-    // warp reads the block indices of 32 units at once, lane 0 issues the copies.
+    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each, a query
+    // row hd bf16. Lane l looks up the block of unit 32 c + l of the CTA's range two chunks c
+    // ahead and its scales one chunk ahead, so the copies wait for neither.
     const uint64_t pol = policy_evict_first();
     bool ok = !p.stall;
-    int j = 0, issued = 0, blk = 0;
-    for (; j < nunits && ok; ++j) {
-      const int k = (w.unit - w.seg_unit0) & 31;
-      const int i = w.pair / p.Hkv, g = w.pair % p.Hkv;
-      if (k == 0) blk = static_cast<int>(block_of(p, i, g, min(w.unit + lane, walk_end(w) - 1)));
+    int issued = 0, segs = 0;
+    Pos8 a = w;
+    int x = lane;
+    a.unit += lane;
+    auto look_up = [&]() {
+      if (x >= nunits) return 0;
+      while (a.unit >= a.units) {
+        const int over = a.unit - a.units;
+        pos_next_pair(a, p, sseq);
+        a.unit = over;
+      }
+      const int b = static_cast<int>(block_of(p, a.i, a.g, a.unit));
+      a.unit += 32;
+      return b;
+    };
+    int blk = look_up();
+    x += 32;
+    int blk1 = look_up();
+    float ks = lane < nunits ? p.ks[blk] : 0.f, vs = lane < nunits ? p.vs[blk] : 0.f;
+    int cnt_left = 0;
+    bool published = false;
+    for (int j = 0; j < nunits && ok; ++j) {
+      const int k = j & 31, c = j >> 5;
+      if (cnt_left == 0) {  // a segment begins: its query rows
+        if (j > 0) pos_next_pair(w, p, sseq);
+        cnt_left = min(w.units - w.unit, nunits - j);
+        ok = segs == 0 || mbar_wait(q8_empty, (segs - 1) & 1, p.max_spin);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
+        __syncwarp();
+        for (int r = lane; r < w.n * G; r += 32)
+          bulk_load(sQ + r * C::QPITCH,
+                    p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
+                    pol);
+        ++segs;
+      }
+      --cnt_left;
       const long long b = __shfl_sync(0xffffffffu, blk, k);
       const int st = j % C::NS;
       if (lane == 0) {
@@ -330,72 +381,105 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      walk_next(w, p, sseq);
+      // The chunk's scales, after its first copies are under way, and before any wait for a unit
+      // of the chunk: a copy waits for the unit NS > 3 before it, the next segment's queries for
+      // the units of the segment before last.
+      published = published && k != 0;
+      if (ok && !published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
+        published = true;
+        ok = c < 2 || mbar_wait(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool zero = vs == 0.f;  // a block of zeros: P must not see the scale
+        sscale[(c & 1) * 32 + lane] = make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 0.f : 1.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[c & 1]);
+      }
+      if (k == 31) {
+        blk = blk1;
+        x += 32;
+        const bool more = x - 32 < nunits;
+        ks = more ? p.ks[blk] : 0.f;
+        vs = more ? p.vs[blk] : 0.f;
+        blk1 = look_up();
+      }
     }
+    if (!ok && !p.stall && lane == 0) flag_status(p.status, kStatusTimeout);
+    // every issued copy must land before the CTA may exit (bounded)
     if (lane == 0) {
-      if (!ok && !p.stall) flag_status(p.status, kStatusTimeout);
-      // every issued copy must land before the CTA may exit (bounded)
       for (int k = max(0, issued - C::NS); k < issued; ++k)
         mbar_wait(&kv8_full[k % C::NS], (k / C::NS) & 1, kDrainSpin);
+      if (segs > 0) mbar_wait(q8_full, (segs - 1) & 1, kDrainSpin);
     }
   } else if (warp == kWS) {
-    if (lane == 0) {
-      // ---------------- S issuer: S(j) = Q K(j)^T, queries from tensor memory
-      constexpr uint32_t id_s = idesc_f16_f32(128, kUnit);
-      const uint64_t kd0 = sw128_kmajor_desc(smem_u32(sK16));
-      bool ok = true;
-      for (int j = 0; j < nunits; ++j) {
+    // ---------------- S issuer: S(j) = Q K(j)^T, queries from tensor memory
+    constexpr uint32_t id_s = idesc_f16_f32(128, kUnit);
+    const uint64_t kd0 = sw128_kmajor_desc(smem_u32(sK16));
+    bool ok = true;
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      ok = __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, p.max_spin));
+      for (int j = j0; j < j0 + cnt && ok; ++j) {
         const int b = j & 1;
-        if (walk_first(w)) ok = mbar_wait(q_full, w.seg & 1, p.max_spin);
-        ok = ok && mbar_wait(&k16_full[b], (j >> 1) & 1, p.max_spin);
+        ok = mbar_wait(&k16_full[b], (j >> 1) & 1, p.max_spin);
         ok = ok && (j < 2 || mbar_wait(&s_empty[b], ((j >> 1) - 1) & 1, p.max_spin));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          tc_mma_bf16_tmem_a(tmem + C::S_COL + b * kUnit, tmem + C::Q_COL + kk * 8,
-                             kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM16 + (kk & 3) * 32) >> 4), id_s,
-                             kk > 0 ? 1u : 0u);
-        tc_commit(&s_full[b]);
-        if (walk_last(w)) tc_commit(q_empty);
-        walk_next(w, p, sseq);
+          for (int kk = 0; kk < HD / 16; ++kk)
+            tc_mma_bf16_tmem_a(tmem + C::S_COL + b * kUnit, tmem + C::Q_COL + kk * 8,
+                               kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM16 + (kk & 3) * 32) >> 4), id_s,
+                               kk > 0 ? 1u : 0u);
+          tc_commit(&s_full[b]);
+          if (j == j0 + cnt - 1) tc_commit(q_empty);
+        }
+        __syncwarp();
       }
-      if (!ok) flag_status(p.status, kStatusTimeout);
-      // every issued MMA must complete before TMEM is freed (bounded)
-      tc_commit(&mma_done[0]);
-      mbar_wait(&mma_done[0], 0, kDrainSpin);
+      j0 += cnt;
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
     }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+    // every issued MMA must complete before TMEM is freed (bounded)
+    if (elect_one()) tc_commit(&mma_done[0]);
+    __syncwarp();
+    mbar_wait(&mma_done[0], 0, kDrainSpin);
   } else if (warp == kWPV) {
-    if (lane == 0) {
-      // ---------------- PV issuer: O_{j%2} += P(j) V(j); the first unit of each half in a segment
-      // starts the accumulator, after both O of the previous segment were read
-      constexpr uint32_t id_pv = idesc_f16_f32(128, HD) | kIdescBMajorMN;
-      const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
-      bool ok = true;
-      int jf = 0;
-      for (int j = 0; j < nunits; ++j) {
+    // ---------------- PV issuer: O_{j%2} += P(j) V(j); the first unit of each half in a segment
+    // starts the accumulator, after both O of the previous segment were read
+    constexpr uint32_t id_pv = idesc_f16_f32(128, HD) | kIdescBMajorMN;
+    const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
+    bool ok = true;
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      for (int j = j0; j < j0 + cnt && ok; ++j) {
         const int b = j & 1;
-        if (walk_first(w)) jf = j;
-        const bool start = j < jf + 2;
         ok = mbar_wait(&v16_full[b], (j >> 1) & 1, p.max_spin);
         ok = ok && mbar_wait(&p_full[b], (j >> 1) & 1, p.max_spin);
-        if (start && w.seg > 0) ok = ok && mbar_wait(o_free, (w.seg - 1) & 1, p.max_spin);
+        if (j == j0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, p.max_spin);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+        const uint32_t add = j < j0 + 2 ? 0u : 1u;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kUnit / 16; ++kk)
-          tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
-                             vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
-                             (!start || kk > 0) ? 1u : 0u);
-        tc_commit(&p_empty[b]);
-        walk_next(w, p, sseq);
+          for (int kk = 0; kk < kUnit / 16; ++kk)
+            tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
+                               vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, kk > 0 ? 1u : add);
+          tc_commit(&p_empty[b]);
+        }
+        __syncwarp();
       }
-      if (!ok) flag_status(p.status, kStatusTimeout);
-      tc_commit(&mma_done[1]);
-      mbar_wait(&mma_done[1], 0, kDrainSpin);
+      j0 += cnt;
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
     }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+    if (elect_one()) tc_commit(&mma_done[1]);
+    __syncwarp();
+    mbar_wait(&mma_done[1], 0, kDrainSpin);
   } else if (warp >= kWConv) {
     // ---------------- converters: e4m3 tiles to f16 tiles in the layout of a 128-byte-swizzled
     // copy (rows of 64 values, 16-byte chunk c of row r at c ^ (r & 7)); warps 0, 1 keys, 2, 3 values
@@ -404,44 +488,59 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     uint64_t *full16 = is_v ? v16_full : k16_full;
     uint64_t *empty16 = is_v ? p_empty : s_full;   // the MMAs that read the buffer have completed
     uint8_t *out = is_v ? sV16 : sK16;
-    constexpr int CPR = HD / 16;                   // 16-byte chunks of a row in 8 bits
+    constexpr int CPR = HD / 8;                    // 8-value chunks of a row: 8 bytes to 16
     constexpr int PER = kUnit * CPR / 64;          // chunks per thread (two warps)
+    constexpr int RPI = 64 / CPR;                  // rows per iteration: 4 or 8
     const int t = (cw & 1) * 32 + lane;
+    const int cc = t % CPR, r0 = t / CPR;
+    // chunk (r0 + RPI * e, cc) of the f16 tile; with 4 rows an iteration r & 7 alternates
+    uint8_t *o0 = out + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
+    uint8_t *o1 = out + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ ((r0 + RPI) & 7)) << 4);
+    const uint8_t *src0 = s8 + (is_v ? C::UNIT8 : 0) + t * 8;
     bool ok = true;
-    for (int j = 0; j < nunits; ++j) {
-      const int st = j % C::NS, b = j & 1;
-      const int keys = w.ctx + w.n - w.unit * kUnit;  // rows of the unit that hold keys
-      ok = mbar_wait(&kv8_full[st], (j / C::NS) & 1, p.max_spin);
-      ok = ok && (j < 2 || mbar_wait(&empty16[b], ((j >> 1) - 1) & 1, p.max_spin));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint8_t *src = s8 + st * 2 * C::UNIT8 + (is_v ? C::UNIT8 : 0);
-      uint8_t *dst = out + b * C::TILE16;
-#pragma unroll 4
-      for (int e = 0; e < PER; ++e) {
-        const int c = t + e * 64;
-        const int r = c / CPR, cc = c % CPR;
-        uint4 u = *reinterpret_cast<const uint4 *>(src + c * 16);
-        // V rows beyond the last key may hold anything (even NaN); P is 0 there
-        if (is_v && r >= keys) u = make_uint4(0, 0, 0, 0);
-        uint32_t h[8];
-        widen16(u, h);
-        uint8_t *row = dst + (cc >> 2) * C::ATOM16 + r * 128;
-        const int c0 = (cc & 3) * 2;
-        // lanes of the second atom store their halves in the other order: no bank conflicts
-        const int first = (cc >> 2) & 1;
-        const uint4 a = first ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
-        const uint4 d = first ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(h[4], h[5], h[6], h[7]);
-        *reinterpret_cast<uint4 *>(row + (((c0 + first) ^ (r & 7)) << 4)) = a;
-        *reinterpret_cast<uint4 *>(row + (((c0 + 1 - first) ^ (r & 7)) << 4)) = d;
+    int st = 0, ph = 0;
+    for (int j0 = 0; j0 < nunits && ok;) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
+      for (int j = j0; j < j0 + cnt; ++j, keys -= kUnit) {
+        const int b = j & 1;
+        ok = mbar_wait(&kv8_full[st], ph, p.max_spin);
+        ok = ok && (j < 2 || mbar_wait(&empty16[b], ((j >> 1) - 1) & 1, p.max_spin));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t *src = src0 + st * 2 * C::UNIT8;
+        if (is_v && keys < kUnit) {
+          // V rows beyond the last key may hold anything (even NaN); P is 0 there
+#pragma unroll 2
+          for (int e = 0; e < PER; ++e) {
+            uint4 h = make_uint4(0, 0, 0, 0);
+            if (r0 + e * RPI < keys) h = widen8(*reinterpret_cast<const uint2 *>(src + e * 512));
+            *reinterpret_cast<uint4 *>((e & 1 ? o1 : o0) + b * C::TILE16 + e * RPI * 128) = h;
+          }
+        } else {
+#pragma unroll
+          for (int e0 = 0; e0 < PER; e0 += 8) {
+            uint2 u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = *reinterpret_cast<const uint2 *>(src + (e0 + e) * 512);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4 *>((e & 1 ? o1 : o0) + b * C::TILE16 + (e0 + e) * RPI * 128) = widen8(u[e]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full16[b]);
+          mbar_arrive(&kv8_empty[st]);
+        }
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&full16[b]);
-        mbar_arrive(&kv8_empty[st]);
-      }
-      walk_next(w, p, sseq);
+      j0 += cnt;
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
     }
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   } else {
@@ -450,127 +549,108 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     const int tl = q * 32 + lane;
     const int r = tl % ROWS, copy = tl / ROWS;
     const int k0 = copy * KW;
-    const bool real = r < R;
     const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const int jq = r / G, hq = r % G;   // row r: query row jq of query head g * G + hq
+    const int jq = r / G;               // row r: query row jq of query head g * G + r % G
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-    if (RHO > 1) {  // the other copies' parts of the P rows stay zero
-      const uint32_t z[32] = {};
-      tmem_st32_raw(trow + C::P_COL + half * 32, z);
-      tmem_wait_st();
-    }
-    // Barrier of half 0's warps, bounded like every other wait.
-    uint32_t half0_phase = 0;
-    auto half0_sync = [&]() {
+    uint32_t half_phase = 0;
+    // Barrier of a half's warps, bounded like every other wait.
+    auto half_sync = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(half0);
-      const bool done = mbar_wait(half0, half0_phase, p.max_spin);
-      half0_phase ^= 1;
+      if (lane == 0) mbar_arrive(&half_bar[half]);
+      const bool done = mbar_wait(&half_bar[half], half_phase, p.max_spin);
+      half_phase ^= 1;
       return __all_sync(0xffffffffu, done) != 0;
     };
-    bool ok = true;
-    float m_run = kNoMax, l_run = 0.f, qfac = 0.f;
-    float ks_c = 0.f, lv_c = 0.f, iv_c = 0.f;   // scales of 32 units (this lane's): K, log2 of V, 1 / V
-    float ks_n = 0.f, vs_n = 0.f;               // the next 32
-    int jf = 0;
-    for (int j = 0; j < nunits; ++j) {
-      const int i = w.pair / p.Hkv, g = w.pair % p.Hkv;
-      const int ku = w.unit - w.seg_unit0;
-      if ((ku & 31) == 0) {
-        const int end = walk_end(w) - 1;
-        if (ku == 0) {
-          const long long b = block_of(p, i, g, min(w.unit + lane, end));
-          ks_n = p.ks[b];
-          vs_n = p.vs[b];
-        }
-        ks_c = ks_n;
-        lv_c = vs_n == 0.f ? 0.f : log2f(vs_n);
-        iv_c = vs_n == 0.f ? 0.f : 1.f / vs_n;   // 0 marks a block of zeros
-        if (w.unit + 32 <= end) {
-          const long long b = block_of(p, i, g, min(w.unit + 32 + lane, end));
-          ks_n = p.ks[b];
-          vs_n = p.vs[b];
-        }
-      }
-      if (walk_first(w)) {
-        jf = j;
-        m_run = kNoMax;
-        l_run = 0.f;
-        // this thread's query row, scaled by a power of two so that its largest value lies in
-        // [2^14, 2^15): exact in f16 down to 2^-31 of it
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + ((static_cast<size_t>(i) * p.m + jq) * p.Hq + g * G + hq) * HD);
-        const bool have = real && jq < w.n;
-        float am = 0.f;
-#pragma unroll 8
-        for (int e = 0; e < HD / 8; ++e) {
-          const uint4 u = have ? src[e] : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    if (RHO > 1) {  // the other copies' parts of the P rows stay zero
+      const uint32_t z[16] = {};
+      tmem_st16_raw(trow + C::P_COL + half * 32, z);
+      tmem_st16_raw(trow + C::P_COL + half * 32 + 16, z);
+      tmem_wait_st();
+    }
+    // The query row of segment `seg` (n rows a sequence), scaled by a power of two so that its
+    // largest value lies in [2^14, 2^15) (exact in f16 down to 2^-31 of it), to tensor memory.
+    // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
+    auto load_q = [&](int seg, int n) {
+      bool ok = mbar_wait(q8_full, seg & 1, p.max_spin);
+      if (half == 0 && seg > 0) ok = ok && mbar_wait(q_empty, (seg - 1) & 1, p.max_spin);
+      if (!__all_sync(0xffffffffu, ok)) return -1.f;
+      const uint4 *src = reinterpret_cast<const uint4 *>(sQ + r * C::QPITCH);
+      const bool have = r < n * G;
+      float am = 0.f;
+#pragma unroll 4
+      for (int e = 0; e < HD / 8; ++e) {
+        const uint4 u = have ? src[e] : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[f] << 16)), fabsf(__uint_as_float(x[f] & 0xFFFF0000u))));
-        }
-        int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
-        ex = ex == 128 ? 14 : max(ex, -100);
+        for (int f = 0; f < 4; ++f)
+          am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[f] << 16)), fabsf(__uint_as_float(x[f] & 0xFFFF0000u))));
+      }
+      int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
+      ex = ex == 128 ? 14 : max(ex, -100);
+      if (half == 0) {
         const float mul = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
-        qfac = sl2 * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
-        if (half == 0) {
-          ok = w.seg == 0 || mbar_wait(q_empty, (w.seg - 1) & 1, p.max_spin);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        tc_fence_after();
 #pragma unroll 1
-          for (int part = 0; part < HD / 32; ++part) {
-            uint32_t h[16];
+        for (int part = 0; part < HD / 32; ++part) {
+          uint32_t h[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
-              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+          for (int e = 0; e < 4; ++e) {
+            const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int f = 0; f < 4; ++f) {
-                const __half2 y = __floats2half2_rn(__uint_as_float(x[f] << 16) * mul,
-                                                    __uint_as_float(x[f] & 0xFFFF0000u) * mul);
-                h[4 * e + f] = *reinterpret_cast<const uint32_t *>(&y);
-              }
+            for (int f = 0; f < 4; ++f) {
+              const __half2 y = __floats2half2_rn(__uint_as_float(x[f] << 16) * mul,
+                                                  __uint_as_float(x[f] & 0xFFFF0000u) * mul);
+              h[4 * e + f] = *reinterpret_cast<const uint32_t *>(&y);
             }
-            tmem_st16_raw(trow + C::Q_COL + part * 16, h);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
+          tmem_st16_raw(trow + C::Q_COL + part * 16, h);
         }
+        tmem_wait_st();
+        tc_fence_before();
       }
-      if ((j & 1) == half) {
-        const bool first = j < jf + 2;  // first unit of this half in the segment
-        const float ks = __shfl_sync(0xffffffffu, ks_c, ku & 31);
-        const float lv = __shfl_sync(0xffffffffu, lv_c, ku & 31);
-        const float iv = __shfl_sync(0xffffffffu, iv_c, ku & 31);
-        const int lim = p.causal ? min(w.ctx + jq + 1, w.ctx + w.n) : w.ctx + w.n;
-        const int nv = lim - w.unit * kUnit - k0;  // keys this thread sees of its part
-        ok = mbar_wait(&s_full[half], (j >> 1) & 1, p.max_spin);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+      __syncwarp();
+      if (lane == 0) {
+        if (half == 0) mbar_arrive(q_full);
+        mbar_arrive(q8_empty);
+      }
+      return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+    };
+    float qfac = load_q(0, w.n);
+    bool ok = qfac >= 0.f;
+    int chunk = -1;                      // chunk of 32 units whose scales this warp may read
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      const int lim = p.causal ? min(w.ctx + jq + 1, w.ctx + w.n) : w.ctx + w.n;
+      float m_run = kNoMax, l_run = 0.f;
+      int mine = -1;                     // last unit of this half in the segment
+      for (int j = j0 + ((j0 ^ half) & 1); j < j0 + cnt; j += 2) {
+        while (chunk < (j >> 5)) {       // the next chunk: give the one before back
+          __syncwarp();
+          if (chunk >= 0 && lane == 0) mbar_arrive(&sc_empty[chunk & 1]);
+          ++chunk;
+          ok = ok && mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
         }
+        const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // K scale, log2 V, 1 / V, 0 for zeros
+        const int nv = lim - (w.unit + j - j0) * kUnit - k0;    // keys this thread sees of its part
+        ok = ok && mbar_wait(&s_full[half], (j >> 1) & 1, p.max_spin);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
         float sv[KW];
         load_s<KW>(trow + C::S_COL + half * kUnit + k0, sv);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[half]);
-
         if (__any_sync(0xffffffffu, nv < KW)) {
 #pragma unroll
           for (int c = 0; c < KW; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
         }
-        const float c1 = fmaxf(qfac * ks, 1e-37f);
+        const float c1 = fmaxf(qfac * sc.x, 1e-37f);
         float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
         for (int c = 4; c < KW; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-        const float m_new = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c1, lv);
+        const float m_new = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c1, sc.y);
         const bool need = m_new - m_run > kRescale;
         float alpha = 1.f;
         if (need) {
@@ -580,14 +660,11 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         }
         // P buffer and O_half: free once PV of this half's previous unit has completed
         if (j >= 2) {
-          ok = mbar_wait(&p_empty[half], ((j >> 1) - 1) & 1, p.max_spin);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&p_empty[half], ((j >> 1) - 1) & 1, p.max_spin));
+          if (!ok) break;
           tc_fence_after();
         }
-        if (!first && __any_sync(0xffffffffu, need && real)) {
+        if (j >= j0 + 2 && __any_sync(0xffffffffu, need && r < R)) {
 #pragma unroll 1
           for (int cc = 0; cc < HD / 16; ++cc) {
             float ov[16];
@@ -598,7 +675,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
             tmem_st16_raw(trow + C::O_COL + half * HD + cc * 16, x);
           }
         }
-        const float c2 = lv - m_run + kPBase;
+        const float c2 = sc.y - m_run + kPBase;
         uint32_t pk[KW / 2];
         float ls[2] = {0.f, 0.f};
 #pragma unroll
@@ -610,8 +687,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
           const __half2 y = __floats2half2_rn(p0, p1);
           pk[c / 2] = *reinterpret_cast<const uint32_t *>(&y);
         }
-        l_run = fmaf(ls[0] + ls[1], iv == 0.f ? 1.f : iv, l_run);
-        if (iv == 0.f) {
+        l_run = fmaf(ls[0] + ls[1], sc.z, l_run);
+        if (sc.w == 0.f) {
 #pragma unroll
           for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
         }
@@ -620,101 +697,116 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[half]);
+        mine = j;
       }
-
-      if (walk_last(w)) {
-        // segment [jf, j]: the last unit of each half in it, or -1
-        const int seg = w.seg;
-        const int last0 = (j & 1) == 0 ? j : (j - 1 >= jf ? j - 1 : -1);
-        const int last1 = (j & 1) == 1 ? j : (j - 1 >= jf ? j - 1 : -1);
-        const int mine = half ? last1 : last0;
-        ok = mine < 0 || mbar_wait(&p_empty[half], (mine >> 1) & 1, p.max_spin);
-        // the (maximum, sum) slots are free once the previous segment's were read
-        if (half == 1) ok = ok && (seg == 0 || mbar_wait(o_free, (seg - 1) & 1, p.max_spin));
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const float2 own = mine >= 0 ? make_float2(m_run, l_run) : make_float2(kNoMax, 0.f);
-        ml[half * 128 + tl] = own;
-        if (half == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ml_ready);
-        } else {
-          ok = mbar_wait(ml_ready, seg & 1, p.max_spin) && ok;
-          if (!__all_sync(0xffffffffu, ok) || !half0_sync()) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          float M = kNoMax;
+      if (!ok) break;
+      // ---- segment end: the next segment's queries first (its S can start), then this one's O
+      const int i = w.i, g = w.g, n = w.n;
+      const bool whole = w.unit == 0 && cnt == w.units;
+      j0 += cnt;
+      float qnext = 0.f;
+      if (j0 < nunits) {
+        pos_next_pair(w, p, sseq);
+        qnext = load_q(seg + 1, w.n);
+        ok = qnext >= 0.f;
+      }
+      ok = ok && (mine < 0 || mbar_wait(&p_empty[half], (mine >> 1) & 1, p.max_spin));
+      // the (maximum, sum) slots are free once the previous segment's were read
+      ok = ok && (seg == 0 || mbar_wait(o_free, (seg - 1) & 1, p.max_spin));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ml[half * 128 + tl] = mine >= 0 ? make_float2(m_run, l_run) : make_float2(kNoMax, 0.f);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_bar);
+      ok = __all_sync(0xffffffffu, mbar_wait(seg_bar, seg & 1, p.max_spin));
+      if (!ok) break;
+      tc_fence_after();
+      float M = kNoMax, L = 0.f;
 #pragma unroll
-          for (int c = 0; c < RHO; ++c)
-            M = fmaxf(M, fmaxf(ml[c * ROWS + r].x, ml[128 + c * ROWS + r].x));
-          float L = 0.f;
+      for (int c = 0; c < 2 * RHO; ++c) M = fmaxf(M, ml[c * ROWS + r].x);
 #pragma unroll
-          for (int c = 0; c < RHO; ++c) {
-            const float2 x = ml[c * ROWS + r], y = ml[128 + c * ROWS + r];
-            L += x.y * ex2f(x.x - M) + y.y * ex2f(y.x - M);
-          }
-          const bool has0 = last0 >= 0, has1 = last1 >= 0;
-          const float a0 = ex2f(own.x - M), a1 = ex2f(ml[128 + tl].x - M);
-          const bool whole = w.seg_unit0 == 0 && w.unit == w.units - 1;
-          const size_t row = (static_cast<size_t>(w.pair) + blockIdx.x) * R + r;
-          const float inv = 1.0f / L;
-          const bool put = real && jq < w.n;
+      for (int c = 0; c < 2 * RHO; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
+      const size_t row0 = (static_cast<size_t>(i * p.Hkv + g) + blockIdx.x) * R;   // partial rows
+      const float inv = whole ? 1.0f / L : 1.0f;
+      const bool has0 = cnt > 1 || (j0 - 1) % 2 == 0, has1 = cnt > 1 || (j0 - 1) % 2 == 1;
+      const float a0 = has0 ? ex2f(ml[tl].x - M) * inv : 0.f, a1 = has1 ? ex2f(ml[128 + tl].x - M) * inv : 0.f;
+      const int live = n * G;            // rows that are computed
+      if (half == 0 && copy == 0 && r < live && !whole)
+        *reinterpret_cast<float2 *>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
+      // Each half takes its half of the columns of O_0 and O_1. With copies, a chunk of cw columns
+      // of every copy goes through shared memory, and the half's threads add the copies up.
+      uint16_t *o = p.o + (static_cast<size_t>(i) * p.m * p.Hq + g * G) * HD;
+      if constexpr (RHO == 1) {
 #pragma unroll 1
-          for (int cc = 0; cc < HD / 16 && ok; ++cc) {
-            float ov[16], o1[16];
-            if (has0) tmem_ld16(trow + C::O_COL + cc * 16, ov);
-            if (has1) tmem_ld16(trow + C::O_COL + HD + cc * 16, o1);
+        for (int c0 = half * (HD / 2); c0 < (half + 1) * (HD / 2); c0 += 16) {
+          float ov[16], o1[16];
+          tmem_ld16(trow + C::O_COL + c0, ov);
+          tmem_ld16(trow + C::O_COL + HD + c0, o1);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) ov[c] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1[c] * a1 : 0.f);
-            if (RHO > 1) {
-              if (copy > 0) {
-                float *to = stage + ((copy - 1) * ROWS + r) * 17;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) to[c] = ov[c];
-              }
-              ok = half0_sync();
-              if (copy == 0) {
-#pragma unroll
-                for (int x = 0; x < RHO - 1; ++x) {
-                  const float *from = stage + (x * ROWS + r) * 17;
-#pragma unroll
-                  for (int c = 0; c < 16; ++c) ov[c] += from[c];
-                }
-              }
-              ok = ok && half0_sync();
-            }
-            if (copy == 0 && put && whole) {
-              uint16_t *dst = p.o + ((static_cast<size_t>(i) * p.m + jq) * p.Hq + g * G + hq) * HD + cc * 16;
+          for (int c = 0; c < 16; ++c) ov[c] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1[c] * a1 : 0.f);
+          if (r < live) {
+            if (whole) {
+              uint16_t *dst = o + (static_cast<size_t>(jq) * p.Hq + r % G) * HD + c0;
 #pragma unroll
               for (int v = 0; v < 2; ++v)
                 reinterpret_cast<uint4 *>(dst)[v] =
-                    make_uint4(pack_bf16x2(ov[8 * v] * inv, ov[8 * v + 1] * inv),
-                               pack_bf16x2(ov[8 * v + 2] * inv, ov[8 * v + 3] * inv),
-                               pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
-                               pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
-            } else if (copy == 0 && put) {
-              float *dst = p.part_o + row * HD + cc * 16;
+                    make_uint4(pack_bf16x2(ov[8 * v], ov[8 * v + 1]), pack_bf16x2(ov[8 * v + 2], ov[8 * v + 3]),
+                               pack_bf16x2(ov[8 * v + 4], ov[8 * v + 5]), pack_bf16x2(ov[8 * v + 6], ov[8 * v + 7]));
+            } else {
+              float *dst = p.part_o + (row0 + r) * HD + c0;
 #pragma unroll
               for (int v = 0; v < 4; ++v)
                 reinterpret_cast<float4 *>(dst)[v] =
                     make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
             }
+          }
+          __syncwarp();
+        }
+      } else {
+        float *stage = reinterpret_cast<float *>(smem + C::OFF_STG) + half * C::STAGE;
+        int cw = HD / 2;                 // columns per chunk: RHO * live rows of cw fit the buffer
+        while (RHO * live * cw > C::STAGE) cw >>= 1;
+        for (int c0 = 0; c0 < HD / 2 && ok; c0 += cw) {
+#pragma unroll 1
+          for (int cc = 0; cc < cw; cc += 16) {
+            const uint32_t col = half * (HD / 2) + c0 + cc;
+            float ov[16], o1[16];
+            tmem_ld16(trow + C::O_COL + col, ov);
+            tmem_ld16(trow + C::O_COL + HD + col, o1);
+            if (r < live) {
+              float *to = stage + (copy * live + r) * cw;
+#pragma unroll
+              for (int c = 0; c < 16; ++c)   // columns turned by the row: no bank conflicts
+                to[(cc + c + r) & (cw - 1)] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1[c] * a1 : 0.f);
+            }
             __syncwarp();
           }
-          if (!ok) break;
-          if (put && copy == 0 && !whole)
-            *reinterpret_cast<float2 *>(p.part_ml + row * 2) = make_float2(M, L);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_free);
+          ok = half_sync();
+          for (int e = tl; e < live * cw / 2 && ok; e += 128) {
+            const int rr = e / (cw / 2), c = (e % (cw / 2)) * 2;
+            float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+            for (int y = 0; y < RHO; ++y) {
+              const float *from = stage + (y * live + rr) * cw;
+              v0 += from[(c + rr) & (cw - 1)];
+              v1 += from[(c + 1 + rr) & (cw - 1)];
+            }
+            const int col = half * (HD / 2) + c0 + c;
+            if (whole)
+              *reinterpret_cast<uint32_t *>(o + (static_cast<size_t>(rr / G) * p.Hq + rr % G) * HD + col) =
+                  pack_bf16x2(v0, v1);
+            else
+              *reinterpret_cast<float2 *>(p.part_o + (row0 + rr) * HD + col) = make_float2(v0, v1);
+          }
+          ok = ok && half_sync();
         }
+        if (!ok) break;
       }
-      walk_next(w, p, sseq);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      qfac = qnext;
     }
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   }
@@ -800,7 +892,7 @@ static cudaError_t configure_attn8() {
   std::lock_guard<std::mutex> lock(mutex);
   if (dev < 64 && done[dev]) return cudaSuccess;
   e = cudaFuncSetAttribute(attn8_kernel<HD, RHO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(A8Cfg<HD>::SMEM));
+                           static_cast<int>(A8Cfg<HD, RHO>::SMEM));
   if (e == cudaSuccess && dev < 64) done[dev] = true;
   return e;
 }
@@ -810,7 +902,7 @@ static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
   const int R = (p.Hq / p.Hkv) * p.m;
   cudaError_t e = configure_attn8<HD, RHO>();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn8_kernel<HD, RHO>, dim3(p.grid), dim3(kA8Threads), A8Cfg<HD>::SMEM, s, p);
+  e = launch_pdl(attn8_kernel<HD, RHO>, dim3(p.grid), dim3(kA8Threads), A8Cfg<HD, RHO>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn8_merge_kernel<HD>, dim3(p.nb * p.Hkv, (R + kMerge8Warps - 1) / kMerge8Warps),
                     dim3(kMerge8Warps * 32), 0, s, p);
