@@ -111,13 +111,12 @@ struct A8Cfg {
   static constexpr int ROWS = 128 / RHO;             // padded query rows
   static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
-  static constexpr int NS = HD == 128 ? 7 : 14;      // ring of units in 8 bits
+  static constexpr int NS = HD == 128 ? 9 : 16;      // ring of units in 8 bits
   static constexpr int ATOM16 = kUnit * 128;
-  static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's keys (or values) in f16
+  static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
   static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
   static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of a half's exchange of O between copies
-  static constexpr int OFF_V16 = 2 * TILE16;
-  static constexpr int OFF_8 = 4 * TILE16;
+  static constexpr int OFF_8 = 2 * TILE16;
   static constexpr int OFF_Q = OFF_8 + NS * 2 * UNIT8;
   static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
   static constexpr int OFF_ML = OFF_STG + 2 * STAGE * 4;  // [2 halves][128 lanes] (maximum, sum)
@@ -129,7 +128,7 @@ struct A8Cfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0;                // S of unit j in buffer j % 2: 64 columns each
   static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
-  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // f16 queries: hd / 2 columns
+  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // queries, two e4m3 terms: hd / 4 columns each
   static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of unit j in buffer j % 2: 32 columns each
   static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
 };
@@ -141,7 +140,7 @@ constexpr int kDrainSpin = 1 << 22;
 constexpr float kPBase = 7.f, kRescale = 8.f;
 
 // Warps: softmax half h = 0, 1 (units j % 2 == h) in 4h .. 4h + 3 (warp w reads TMEM lanes of
-// quarter w % 4), producer, S issuer, PV issuer, then the converters (two for K, two for V).
+// quarter w % 4), producer, S issuer, PV issuer, then the converters of V.
 constexpr int kWProd = 8, kWS = 9, kWPV = 10, kWConv = 11, kNumConv = 4;
 constexpr int kA8Threads = (kWConv + kNumConv) * 32;
 
@@ -229,14 +228,13 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint8_t *sK16 = smem, *sV16 = smem + C::OFF_V16, *s8 = smem + C::OFF_8, *sQ = smem + C::OFF_Q;
+  uint8_t *sV16 = smem, *s8 = smem + C::OFF_8, *sQ = smem + C::OFF_Q;
   float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
   float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
   uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv8_empty = kv8_full + C::NS;
-  uint64_t *k16_full = kv8_empty + C::NS;   // [2] unit j in buffer j % 2
-  uint64_t *v16_full = k16_full + 2;        // [2]
-  uint64_t *s_full = v16_full + 2;          // [2] S(j) complete: also K16 buffer j % 2 read
+  uint64_t *v16_full = kv8_empty + C::NS;   // [2] unit j in buffer j % 2
+  uint64_t *s_full = v16_full + 2;          // [2] S(j) complete
   uint64_t *s_empty = s_full + 2;           // [2]
   uint64_t *p_full = s_empty + 2;           // [2]
   uint64_t *p_empty = p_full + 2;           // [2] PV(j) complete: P and V16 buffers j % 2 read
@@ -252,7 +250,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   uint64_t *o_free = seg_bar + 1;           // both O and ml read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 20 + 6) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((2 * C::NS + 18 + 6) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -262,11 +260,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&kv8_full[s], 1);
-      mbar_init(&kv8_empty[s], kNumConv);
+      mbar_init(&kv8_empty[s], kNumConv + 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&k16_full[b], kNumConv / 2);
-      mbar_init(&v16_full[b], kNumConv / 2);
+      mbar_init(&v16_full[b], kNumConv);
       mbar_init(&s_full[b], 1);
       mbar_init(&s_empty[b], 4);
       mbar_init(&p_full[b], 4);
@@ -325,8 +322,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   if (nunits == 0) {
     // nothing to do
   } else if (warp == kWProd) {
-    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each, a query
-    // row hd bf16. Lane l looks up the block of unit 32 c + l of the CTA's range two chunks c
+    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each (the keys
+    // arrive swizzled, as the tensor cores read them), a query row hd bf16. Lane l looks up the block of unit 32 c + l of the CTA's range two chunks c
     // ahead and its scales one chunk ahead, so the copies wait for neither.
     const uint64_t pol = policy_evict_first();
     bool ok = !p.stall;
@@ -375,7 +372,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         if (ok) {
           uint8_t *dst = s8 + st * 2 * C::UNIT8;
           mbar_arrive_expect_tx(&kv8_full[st], 2 * C::UNIT8);
-          bulk_load(dst, p.k8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
+          tma_load_2d(dst, &p.tmK, &kv8_full[st], 0, static_cast<int>(b) * kUnit, pol);
           bulk_load(dst + C::UNIT8, p.v8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
           ++issued;
         }
@@ -412,31 +409,37 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       if (segs > 0) mbar_wait(q8_full, (segs - 1) & 1, kDrainSpin);
     }
   } else if (warp == kWS) {
-    // ---------------- S issuer: S(j) = Q K(j)^T, queries from tensor memory
-    constexpr uint32_t id_s = idesc_f16_f32(128, kUnit);
-    const uint64_t kd0 = sw128_kmajor_desc(smem_u32(sK16));
+    // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two e4m3
+    // terms one after the other from tensor memory
+    constexpr uint32_t id_s = idesc_f32_format0(128, kUnit);
+    const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(s8)) : sw64_kmajor_desc(smem_u32(s8));
+    int st = 0, ph = 0;
     bool ok = true;
     for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
       const int cnt = min(w.units - w.unit, nunits - j0);
       ok = __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, p.max_spin));
       for (int j = j0; j < j0 + cnt && ok; ++j) {
         const int b = j & 1;
-        ok = mbar_wait(&k16_full[b], (j >> 1) & 1, p.max_spin);
+        ok = mbar_wait(&kv8_full[st], ph, p.max_spin);
         ok = ok && (j < 2 || mbar_wait(&s_empty[b], ((j >> 1) - 1) & 1, p.max_spin));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t kd = kd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+        const uint64_t kd = kd0 + static_cast<uint64_t>((st * 2 * C::UNIT8) >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            tc_mma_bf16_tmem_a(tmem + C::S_COL + b * kUnit, tmem + C::Q_COL + kk * 8,
-                               kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM16 + (kk & 3) * 32) >> 4), id_s,
-                               kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 2 * HD / 32; ++kk)
+            tc_mma_e4m3_tmem_a(tmem + C::S_COL + b * kUnit, tmem + C::Q_COL + kk * 8,
+                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id_s, kk > 0 ? 1u : 0u);
+          tc_commit(&kv8_empty[st]);
           tc_commit(&s_full[b]);
           if (j == j0 + cnt - 1) tc_commit(q_empty);
         }
         __syncwarp();
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
+        }
       }
       j0 += cnt;
       if (j0 < nunits) pos_next_pair(w, p, sseq);
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   } else if (warp == kWPV) {
     // ---------------- PV issuer: O_{j%2} += P(j) V(j); the first unit of each half in a segment
     // starts the accumulator, after both O of the previous segment were read
-    constexpr uint32_t id_pv = idesc_f16_f32(128, HD) | kIdescBMajorMN;
+    constexpr uint32_t id_pv = idesc_f32_format0(128, HD) | kIdescBMajorMN;
     const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
     bool ok = true;
     for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
@@ -481,22 +484,16 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     __syncwarp();
     mbar_wait(&mma_done[1], 0, kDrainSpin);
   } else if (warp >= kWConv) {
-    // ---------------- converters: e4m3 tiles to f16 tiles in the layout of a 128-byte-swizzled
-    // copy (rows of 64 values, 16-byte chunk c of row r at c ^ (r & 7)); warps 0, 1 keys, 2, 3 values
-    const int cw = warp - kWConv;
-    const bool is_v = cw >= 2;
-    uint64_t *full16 = is_v ? v16_full : k16_full;
-    uint64_t *empty16 = is_v ? p_empty : s_full;   // the MMAs that read the buffer have completed
-    uint8_t *out = is_v ? sV16 : sK16;
-    constexpr int CPR = HD / 8;                    // 8-value chunks of a row: 8 bytes to 16
-    constexpr int PER = kUnit * CPR / 64;          // chunks per thread (two warps)
-    constexpr int RPI = 64 / CPR;                  // rows per iteration: 4 or 8
-    const int t = (cw & 1) * 32 + lane;
+    // ---------------- converters: V from e4m3 to f16, in the layout of a 128-byte-swizzled copy (rows
+    // of 64 values, 16-byte chunk c of row r at c ^ (r & 7))
+    constexpr int CPR = HD / 8;                        // 8-value chunks of a row: 8 bytes to 16
+    constexpr int RPI = kNumConv * 32 / CPR;           // rows per iteration: 8 or 16
+    constexpr int PER = kUnit / RPI;                   // chunks per thread
+    static_assert(RPI % 8 == 0, "a thread's chunks all lie at the same place of their rows");
+    const int t = (warp - kWConv) * 32 + lane;
     const int cc = t % CPR, r0 = t / CPR;
-    // chunk (r0 + RPI * e, cc) of the f16 tile; with 4 rows an iteration r & 7 alternates
-    uint8_t *o0 = out + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
-    uint8_t *o1 = out + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ ((r0 + RPI) & 7)) << 4);
-    const uint8_t *src0 = s8 + (is_v ? C::UNIT8 : 0) + t * 8;
+    uint8_t *out = sV16 + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
+    const uint8_t *src0 = s8 + C::UNIT8 + t * 8;
     bool ok = true;
     int st = 0, ph = 0;
     for (int j0 = 0; j0 < nunits && ok;) {
@@ -505,33 +502,30 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       for (int j = j0; j < j0 + cnt; ++j, keys -= kUnit) {
         const int b = j & 1;
         ok = mbar_wait(&kv8_full[st], ph, p.max_spin);
-        ok = ok && (j < 2 || mbar_wait(&empty16[b], ((j >> 1) - 1) & 1, p.max_spin));
+        ok = ok && (j < 2 || mbar_wait(&p_empty[b], ((j >> 1) - 1) & 1, p.max_spin));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint8_t *src = src0 + st * 2 * C::UNIT8;
-        if (is_v && keys < kUnit) {
-          // V rows beyond the last key may hold anything (even NaN); P is 0 there
+        uint8_t *dst = out + b * C::TILE16;
+        if (keys < kUnit) {
+          // rows beyond the last key may hold anything (even NaN); P is 0 there
 #pragma unroll 2
           for (int e = 0; e < PER; ++e) {
             uint4 h = make_uint4(0, 0, 0, 0);
-            if (r0 + e * RPI < keys) h = widen8(*reinterpret_cast<const uint2 *>(src + e * 512));
-            *reinterpret_cast<uint4 *>((e & 1 ? o1 : o0) + b * C::TILE16 + e * RPI * 128) = h;
+            if (r0 + e * RPI < keys) h = widen8(*reinterpret_cast<const uint2 *>(src + e * RPI * HD));
+            *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = h;
           }
         } else {
+          uint2 u[PER];
 #pragma unroll
-          for (int e0 = 0; e0 < PER; e0 += 8) {
-            uint2 u[8];
+          for (int e = 0; e < PER; ++e) u[e] = *reinterpret_cast<const uint2 *>(src + e * RPI * HD);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = *reinterpret_cast<const uint2 *>(src + (e0 + e) * 512);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4 *>((e & 1 ? o1 : o0) + b * C::TILE16 + (e0 + e) * RPI * 128) = widen8(u[e]);
-          }
+          for (int e = 0; e < PER; ++e) *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = widen8(u[e]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&full16[b]);
+          mbar_arrive(&v16_full[b]);
           mbar_arrive(&kv8_empty[st]);
         }
         if (++st == C::NS) {
@@ -568,7 +562,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       tmem_wait_st();
     }
     // The query row of segment `seg` (n rows a sequence), scaled by a power of two so that its
-    // largest value lies in [2^14, 2^15) (exact in f16 down to 2^-31 of it), to tensor memory.
+    // largest value lies in [2^7, 2^8), to tensor memory as the sum of two e4m3 terms: 4 bits each
+    // hold bf16's 8, exactly down to 2^-10 of the largest value, below that to 2^-18 of it.
     // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
     auto load_q = [&](int seg, int n) {
       bool ok = mbar_wait(q8_full, seg & 1, p.max_spin);
@@ -586,25 +581,33 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
           am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[f] << 16)), fabsf(__uint_as_float(x[f] & 0xFFFF0000u))));
       }
       int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
-      ex = ex == 128 ? 14 : max(ex, -100);
+      const bool inf = ex == 128;          // the row's outputs are NaN
+      ex = max(min(ex, 127), -100);
       if (half == 0) {
-        const float mul = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);
+        const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
         tc_fence_after();
 #pragma unroll 1
         for (int part = 0; part < HD / 32; ++part) {
-          uint32_t h[16];
+          uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
             const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-              const __half2 y = __floats2half2_rn(__uint_as_float(x[f] << 16) * mul,
-                                                  __uint_as_float(x[f] & 0xFFFF0000u) * mul);
-              h[4 * e + f] = *reinterpret_cast<const uint32_t *>(&y);
+              const float2 y = make_float2(__uint_as_float(x[f] << 16) * mul, __uint_as_float(x[f] & 0xFFFF0000u) * mul);
+              const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
+              const float2 af = __half22float2(*reinterpret_cast<const __half2 *>(&ar));
+              const __nv_fp8x2_storage_t b =
+                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E4M3);
+              const int d = 2 * e + f / 2;
+              hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(a) << 16) : a;
+              lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(b) << 16) : b;
             }
           }
-          tmem_st16_raw(trow + C::Q_COL + part * 16, h);
+          tmem_st8_raw(trow + C::Q_COL + part * 8, hi);
+          tmem_st8_raw(trow + C::Q_COL + HD / 4 + part * 8, lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         if (half == 0) mbar_arrive(q_full);
         mbar_arrive(q8_empty);
       }
-      return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 14 + 127) << 23);
+      return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
     };
     float qfac = load_q(0, w.n);
     bool ok = qfac >= 0.f;

@@ -300,6 +300,18 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// D[tmem] (+)= A[tmem] * B[smem]^T, e4m3 inputs, fp32 accumulate (kind::f8f6f4): four consecutive
+// K elements of a row per 32-bit column of its lane, 32 per instruction.
+__device__ __forceinline__ void tc_mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                   uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor for a K-major operand tile written by TMA with
 // 128-byte swizzle: rows of 128 bytes (64 bf16), 8-row atoms 1024 bytes apart.
 // Bits: [0,14) start>>4, [16,30) LBO>>4 (unused here), [32,46) SBO>>4,
@@ -311,6 +323,18 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(1024 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// The same for rows of 64 bytes written with 64-byte swizzle (8-row atoms 512 bytes apart,
+// layout 4).
+__device__ __forceinline__ uint64_t sw64_kmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(512 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(4) << 61;
   return d;
 }
 
@@ -336,8 +360,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 constexpr uint32_t kIdescBMajorMN = 1u << 16;
-// The same with f16 operands (formats 0).
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+// The same with formats 0: f16 operands of kind::f16, e4m3 operands of kind::f8f6f4.
+__host__ __device__ constexpr uint32_t idesc_f32_format0(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 

@@ -1073,6 +1073,23 @@ KvRowsParams rows_params(const dflash_handle_s *h, int nb, int R) {
   return p;
 }
 
+// 8-bit rows [rows, hd] as a 2D map, box = one block of kPageRows rows, swizzled by its row of
+// hd = 64 or 128 bytes.
+int encode_rows8(CUtensorMap *m, const void *ptr, uint64_t rows, int hd) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)hd, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)hd};
+  cuuint32_t box[2] = {(cuuint32_t)hd, kPageRows};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled (8-bit rows) failed: %d", (int)r);
+  return DFLASH_OK;
+}
+
 // Arguments shared by the two appends; *run is false when there is nothing to do.
 int append_params(dflash_handle_t h, int nb, int layer, int R, const void *k, int64_t ldk, const void *v,
                   int64_t ldv, const void *g_k, int rotate, const int32_t *n_rows, const int32_t *ctx_len,
@@ -1208,7 +1225,8 @@ int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q
   const size_t blocks = layer * (cache_layer_rows(c) / kPageRows);
   Attn8Params p{};
   p.q = bf(q);
-  p.k8 = static_cast<const uint8_t *>(kcache8) + blocks * kPageRows * c.hd;
+  DF_TRY(encode_rows8(&p.tmK, static_cast<const uint8_t *>(kcache8) + blocks * kPageRows * c.hd,
+                      cache_layer_rows(c), c.hd));
   p.v8 = static_cast<const uint8_t *>(vcache8) + blocks * kPageRows * c.hd;
   p.ks = kscale + blocks;
   p.vs = vscale + blocks;
