@@ -49,53 +49,63 @@ __device__ __forceinline__ long long block_of(const Attn8Params &p, int i, int g
   return static_cast<long long>(pg) * p.Hkv + g;
 }
 
-__device__ __forceinline__ long long cta_start(long long T, int G, int c) {
-  return static_cast<long long>(c) * T / G;
-}
-__device__ __forceinline__ int cta_of(long long T, int G, long long u) {
-  return static_cast<int>(((u + 1) * G + T - 1) / T - 1);
+// The T units are split over G CTAs: the first T % G take one more than the others (T is below
+// 2^25: a handle's caches hold fewer than 2^31 rows).
+__device__ __forceinline__ int cta_start(int T, int G, int c) { return c * (T / G) + min(c, T % G); }
+__device__ __forceinline__ int cta_of(int T, int G, int u) {
+  const int q = T / G, big = (T % G) * (q + 1);
+  return u < big ? u / (q + 1) : T % G + (u - big) / q;
 }
 
-// Where a CTA's range begins: pair i * Hkv + g, unit inside it, number of units.
-struct Range8 {
-  int pair, unit;
-  long long count;
-};
-// Warp-collective.
-__device__ Range8 find_range(const Attn8Params &p, int cta, int lane) {
-  long long T = 0;
-  for (int i = lane; i < p.nb; i += 32) T += seq8(p, i).units;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
-  T *= p.Hkv;
-  const int Ge = T < p.grid ? static_cast<int>(T) : p.grid;
-  Range8 r = {0, 0, 0};
-  if (cta >= Ge) return r;
-  const long long u0 = cta_start(T, Ge, cta);
-  r.count = cta_start(T, Ge, cta + 1) - u0;
-  long long base = 0;
-  for (int b = 0; b < p.nb; b += 32) {
-    const int i = b + lane;
-    const int U = i < p.nb ? seq8(p, i).units : 0;
-    long long v = static_cast<long long>(p.Hkv) * U;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + v > u0);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const int Ul = __shfl_sync(0xffffffffu, U, l);
-      const long long off = u0 - (base + __shfl_sync(0xffffffffu, v, l) - static_cast<long long>(p.Hkv) * Ul);
-      r.pair = (b + l) * p.Hkv + static_cast<int>(off / Ul);
-      r.unit = static_cast<int>(off % Ul);
-      return r;
-    }
-    base += __shfl_sync(0xffffffffu, v, 31);
+// Units of the sequences before i (`before`) and of all of them, times Hkv. Warp-collective.
+__device__ __forceinline__ int total_units(const Attn8Params &p, int i, int lane, int *before) {
+  int t = 0, b = 0;
+#pragma unroll 1
+  for (int s = lane; s < p.nb; s += 32) {
+    const int u = seq8(p, s).units;
+    t += u;
+    b += s < i ? u : 0;
   }
-  r.count = 0;
-  return r;
+  *before = __reduce_add_sync(0xffffffffu, b) * p.Hkv;
+  return __reduce_add_sync(0xffffffffu, t) * p.Hkv;
+}
+
+// Where a CTA's range begins (pair i * Hkv + g, unit inside it) and its number of units.
+// Warp-collective.
+__device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
+  int base;
+  const int T = total_units(p, 0, lane, &base);
+  const int Ge = min(T, p.grid);
+  int count = 0, pair = 0, unit = 0;
+  if (cta < Ge) {
+    const int u0 = cta_start(T, Ge, cta);
+    count = cta_start(T, Ge, cta + 1) - u0;
+#pragma unroll 1
+    for (int b = 0; b < p.nb; b += 32) {
+      const int U = b + lane < p.nb ? seq8(p, b + lane).units : 0;
+      int v = p.Hkv * U;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + v > u0);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const int Ul = __shfl_sync(0xffffffffu, U, l);
+        const int off = u0 - (base + __shfl_sync(0xffffffffu, v, l) - p.Hkv * Ul);
+        pair = (b + l) * p.Hkv + off / Ul;
+        unit = off % Ul;
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  if (lane == 0) {
+    out[0] = pair;
+    out[1] = unit;
+    out[2] = count;
+  }
 }
 
 }  // namespace
@@ -111,13 +121,15 @@ struct A8Cfg {
   static constexpr int ROWS = 128 / RHO;             // padded query rows
   static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
-  static constexpr int NS = HD == 128 ? 9 : 16;      // ring of units in 8 bits
+  static constexpr int PAIR8 = 2 * UNIT8;
+  // ring of pairs of units in 8 bits, keys then values, as much as shared memory holds
+  static constexpr int NS = 4 * (128 / HD);
   static constexpr int ATOM16 = kUnit * 128;
   static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
   static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
   static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of a half's exchange of O between copies
   static constexpr int OFF_8 = 2 * TILE16;
-  static constexpr int OFF_Q = OFF_8 + NS * 2 * UNIT8;
+  static constexpr int OFF_Q = OFF_8 + NS * 2 * PAIR8;
   static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
   static constexpr int OFF_ML = OFF_STG + 2 * STAGE * 4;  // [2 halves][128 lanes] (maximum, sum)
   static constexpr int OFF_SC = OFF_ML + 2 * 128 * 8;     // [2 chunks][32 units] scales
@@ -126,10 +138,10 @@ struct A8Cfg {
   static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t S_COL = 0;                // S of unit j in buffer j % 2: 64 columns each
+  static constexpr uint32_t S_COL = 0;                // S of a pair of units: 64 columns each
   static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
   static constexpr uint32_t Q_COL = 128 + 2 * HD;     // queries, two e4m3 terms: hd / 4 columns each
-  static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of unit j in buffer j % 2: 32 columns each
+  static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of a pair's units: 32 columns each
   static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
 };
 constexpr int kSeqCache = 128;
@@ -139,9 +151,15 @@ constexpr int kDrainSpin = 1 << 22;
 // the largest still has all 11 bits (2^-31 one bit).
 constexpr float kPBase = 7.f, kRescale = 8.f;
 
-// Warps: softmax half h = 0, 1 (units j % 2 == h) in 4h .. 4h + 3 (warp w reads TMEM lanes of
-// quarter w % 4), producer, S issuer, PV issuer, then the converters of V.
-constexpr int kWProd = 8, kWS = 9, kWPV = 10, kWConv = 11, kNumConv = 4;
+// A segment's units are taken in pairs: one S product of 128 keys, then softmax, PV and O for each
+// unit of the pair on its own. What bounds the kernel are the steps from one role to the next (with
+// every copy, product and exponential left out it still took 0.8 of its time, a unit at a time), so
+// they are paid for two units at once. Half a pair at the end of a segment of an odd number of units
+// is signalled by every role without work.
+// Warps: producer, S issuer, PV issuer, one that only helps at the start, softmax half h = 0, 1 (a
+// pair's first or second unit) in 4 + 4h .. 7 + 4h (warp w reads TMEM lanes of quarter w % 4), then
+// the converters of V.
+constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWAid = 3, kWSoft = 4, kWConv = 12, kNumConv = 4;
 constexpr int kA8Threads = (kWConv + kNumConv) * 32;
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -154,18 +172,17 @@ __device__ __forceinline__ float ex2f(float x) {
 struct Pos8 {
   int i, g, unit, units, n, ctx;
 };
+__device__ __noinline__ int2 seq_far(const Attn8Params &p, int i) {
+  const Seq8 s = seq8(p, i);
+  return make_int2(s.n, s.ctx);
+}
 __device__ __forceinline__ void pos_seq(Pos8 &w, const Attn8Params &p, const int2 *sseq) {
+#pragma unroll 1
   for (;; ++w.i) {  // a sequence without rows has no units (one with rows follows)
-    if (w.i < kSeqCache) {
-      w.n = sseq[w.i].x;
-      w.ctx = sseq[w.i].y;
-      w.units = w.n > 0 ? (w.ctx + w.n + kUnit - 1) / kUnit : 0;
-    } else {
-      const Seq8 s = seq8(p, w.i);
-      w.n = s.n;
-      w.ctx = s.ctx;
-      w.units = s.units;
-    }
+    const int2 s = w.i < kSeqCache ? sseq[w.i] : seq_far(p, w.i);
+    w.n = s.x;
+    w.ctx = s.y;
+    w.units = w.n > 0 ? (w.ctx + w.n + kUnit - 1) / kUnit : 0;
     if (w.units > 0) return;
   }
 }
@@ -233,16 +250,16 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
   uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv8_empty = kv8_full + C::NS;
-  uint64_t *v16_full = kv8_empty + C::NS;   // [2] unit j in buffer j % 2
-  uint64_t *s_full = v16_full + 2;          // [2] S(j) complete
-  uint64_t *s_empty = s_full + 2;           // [2]
-  uint64_t *p_full = s_empty + 2;           // [2]
-  uint64_t *p_empty = p_full + 2;           // [2] PV(j) complete: P and V16 buffers j % 2 read
+  uint64_t *v16_full = kv8_empty + C::NS;   // [2] a pair's first and second unit
+  uint64_t *p_full = v16_full + 2;          // [2]
+  uint64_t *p_empty = p_full + 2;           // [2] PV complete: the P and V16 buffers have been read
   uint64_t *sc_full = p_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
   uint64_t *sc_empty = sc_full + 2;         // [2]
   uint64_t *half_bar = sc_empty + 2;        // [2] the four warps of a half among themselves
   uint64_t *mma_done = half_bar + 2;        // [2]
-  uint64_t *q8_full = mma_done + 2;         // a segment's query rows have landed
+  uint64_t *s_full = mma_done + 2;          // S of a pair complete
+  uint64_t *s_empty = s_full + 1;           // and read by both halves
+  uint64_t *q8_full = s_empty + 1;          // a segment's query rows have landed
   uint64_t *q8_empty = q8_full + 1;
   uint64_t *q_full = q8_empty + 1;          // and are in tensor memory
   uint64_t *q_empty = q_full + 1;
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   uint64_t *o_free = seg_bar + 1;           // both O and ml read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 18 + 6) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((2 * C::NS + 14 + 8) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -264,8 +281,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&v16_full[b], kNumConv);
-      mbar_init(&s_full[b], 1);
-      mbar_init(&s_empty[b], 4);
       mbar_init(&p_full[b], 4);
       mbar_init(&p_empty[b], 1);
       mbar_init(&sc_full[b], 1);
@@ -273,6 +288,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       mbar_init(&half_bar[b], 4);
       mbar_init(&mma_done[b], 1);
     }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 8);
     mbar_init(q8_full, 1);
     mbar_init(q8_empty, 8);
     mbar_init(q_full, 4);
@@ -288,13 +305,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   if (warp == kWProd) {
-    const Range8 r = find_range(p, blockIdx.x, lane);
-    if (lane == 0) {
-      sched[0] = r.pair;
-      sched[1] = r.unit;
-      sched[2] = static_cast<int>(r.count);
-    }
-  } else if (warp == kWConv) {
+    find_range(p, blockIdx.x, lane, sched);
+  } else if (warp == kWAid) {
     for (int i = lane; i < p.nb && i < kSeqCache; i += 32) {
       const Seq8 s = seq8(p, i);
       sseq[i] = make_int2(s.n, s.ctx);
@@ -317,8 +329,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   w.unit = sched[1];
   if (nunits > 0) pos_seq(w, p, sseq);
 
-  // Every role goes through the CTA's segments (runs of units of one pair): `cnt` units from unit
-  // j0 of the CTA on. A wait that runs out ends the role (ok = false).
+  // Every role goes through the CTA's segments: `cnt` units from unit j0 of the CTA on, in pairs pj
+  // of units u, u + 1 of the segment. A wait that runs out ends the role (ok = false).
   if (nunits == 0) {
     // nothing to do
   } else if (warp == kWProd) {
@@ -327,7 +339,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     // ahead and its scales one chunk ahead, so the copies wait for neither.
     const uint64_t pol = policy_evict_first();
     bool ok = !p.stall;
-    int issued = 0, segs = 0;
+    int pairs = 0, segs = 0;
     Pos8 a = w;
     int x = lane;
     a.unit += lane;
@@ -346,51 +358,59 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     x += 32;
     int blk1 = look_up();
     float ks = lane < nunits ? p.ks[blk] : 0.f, vs = lane < nunits ? p.vs[blk] : 0.f;
-    int cnt_left = 0;
+    int cnt_left = 0, slot = 0, st = 0, ph = 0;
     bool published = false;
+#pragma unroll 1
     for (int j = 0; j < nunits && ok; ++j) {
       const int k = j & 31, c = j >> 5;
       if (cnt_left == 0) {  // a segment begins: its query rows
         if (j > 0) pos_next_pair(w, p, sseq);
         cnt_left = min(w.units - w.unit, nunits - j);
-        ok = segs == 0 || mbar_wait(q8_empty, (segs - 1) & 1, p.max_spin);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = segs == 0 || mbar_wait_warp(q8_empty, (segs - 1) & 1, p.max_spin);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
         __syncwarp();
+#pragma unroll 1
         for (int r = lane; r < w.n * G; r += 32)
           bulk_load(sQ + r * C::QPITCH,
                     p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
                     pol);
         ++segs;
+        slot = 0;
       }
       --cnt_left;
       const long long b = __shfl_sync(0xffffffffu, blk, k);
-      const int st = j % C::NS;
-      if (lane == 0) {
-        ok = j < C::NS || mbar_wait(&kv8_empty[st], ((j / C::NS) - 1) & 1, p.max_spin);
-        if (ok) {
-          uint8_t *dst = s8 + st * 2 * C::UNIT8;
-          mbar_arrive_expect_tx(&kv8_full[st], 2 * C::UNIT8);
-          tma_load_2d(dst, &p.tmK, &kv8_full[st], 0, static_cast<int>(b) * kUnit, pol);
-          bulk_load(dst + C::UNIT8, p.v8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
-          ++issued;
-        }
+      if (slot == 0) ok = pairs < C::NS || mbar_wait_warp(&kv8_empty[st], ph ^ 1, p.max_spin);
+      if (!ok) break;
+      if (elect_one()) {
+        uint8_t *dst = s8 + st * 2 * C::PAIR8;
+        if (slot == 0) mbar_arrive_expect_tx(&kv8_full[st], (cnt_left > 0 ? 2 : 1) * C::PAIR8);
+        tma_load_2d(dst + slot * C::UNIT8, &p.tmK, &kv8_full[st], 0, static_cast<int>(b) * kUnit, pol);
+        bulk_load(dst + C::PAIR8 + slot * C::UNIT8, p.v8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      __syncwarp();
+      if (slot == 0) ++pairs;
+      if (slot == 1 || cnt_left == 0) {  // the pair is complete
+        slot = 0;
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      } else {
+        slot = 1;
+      }
       // The chunk's scales, after its first copies are under way, and before any wait for a unit
-      // of the chunk: a copy waits for the unit NS > 3 before it, the next segment's queries for
-      // the units of the segment before last.
+      // of the chunk: a copy waits for the pair NS > 3 before its own, the next segment's queries
+      // for the units of the segment before last.
       published = published && k != 0;
-      if (ok && !published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
+      if (!published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
         published = true;
-        ok = c < 2 || mbar_wait(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = c < 2 || mbar_wait_warp(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
         if (!ok) break;
         const bool zero = vs == 0.f;  // a block of zeros: P must not see the scale
         sscale[(c & 1) * 32 + lane] = make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 0.f : 1.f);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sc_full[c & 1]);
+        mbar_arrive_if(&sc_full[c & 1], lane == 0);
       }
       if (k == 31) {
         blk = blk1;
@@ -403,37 +423,37 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     }
     if (!ok && !p.stall && lane == 0) flag_status(p.status, kStatusTimeout);
     // every issued copy must land before the CTA may exit (bounded)
-    if (lane == 0) {
-      for (int k = max(0, issued - C::NS); k < issued; ++k)
-        mbar_wait(&kv8_full[k % C::NS], (k / C::NS) & 1, kDrainSpin);
-      if (segs > 0) mbar_wait(q8_full, (segs - 1) & 1, kDrainSpin);
-    }
+#pragma unroll 1
+    for (int x = max(0, pairs - C::NS); x < pairs; ++x)
+      mbar_wait_warp(&kv8_full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
+    if (segs > 0) mbar_wait_warp(q8_full, (segs - 1) & 1, kDrainSpin);
   } else if (warp == kWS) {
     // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two e4m3
     // terms one after the other from tensor memory
     constexpr uint32_t id_s = idesc_f32_format0(128, kUnit);
     const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(s8)) : sw64_kmajor_desc(smem_u32(s8));
-    int st = 0, ph = 0;
+    constexpr uint32_t id_s2 = idesc_f32_format0(128, 2 * kUnit);
+    int st = 0, ph = 0, pj = 0;
     bool ok = true;
+#pragma unroll 1
     for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
       const int cnt = min(w.units - w.unit, nunits - j0);
-      ok = __all_sync(0xffffffffu, mbar_wait(q_full, seg & 1, p.max_spin));
-      for (int j = j0; j < j0 + cnt && ok; ++j) {
-        const int b = j & 1;
-        ok = mbar_wait(&kv8_full[st], ph, p.max_spin);
-        ok = ok && (j < 2 || mbar_wait(&s_empty[b], ((j >> 1) - 1) & 1, p.max_spin));
-        ok = __all_sync(0xffffffffu, ok);
+      ok = mbar_wait_warp(q_full, seg & 1, p.max_spin);
+#pragma unroll 1
+      for (int u = 0; u < cnt && ok; u += 2, ++pj) {
+        ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
+        ok = ok && (pj == 0 || mbar_wait_warp(s_empty, (pj - 1) & 1, p.max_spin));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t kd = kd0 + static_cast<uint64_t>((st * 2 * C::UNIT8) >> 4);
+        const uint64_t kd = kd0 + static_cast<uint64_t>((st * 2 * C::PAIR8) >> 4);
+        const uint32_t id = u + 1 < cnt ? id_s2 : id_s;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 2 * HD / 32; ++kk)
-            tc_mma_e4m3_tmem_a(tmem + C::S_COL + b * kUnit, tmem + C::Q_COL + kk * 8,
-                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id_s, kk > 0 ? 1u : 0u);
-          tc_commit(&kv8_empty[st]);
-          tc_commit(&s_full[b]);
-          if (j == j0 + cnt - 1) tc_commit(q_empty);
+            tc_mma_e4m3_tmem_a(tmem + C::S_COL, tmem + C::Q_COL + kk * 8,
+                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id, kk > 0 ? 1u : 0u);
+          tc_commit(s_full);
+          if (u + 2 >= cnt) tc_commit(q_empty);
         }
         __syncwarp();
         if (++st == C::NS) {
@@ -448,33 +468,37 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     // every issued MMA must complete before TMEM is freed (bounded)
     if (elect_one()) tc_commit(&mma_done[0]);
     __syncwarp();
-    mbar_wait(&mma_done[0], 0, kDrainSpin);
+    mbar_wait_warp(&mma_done[0], 0, kDrainSpin);
   } else if (warp == kWPV) {
-    // ---------------- PV issuer: O_{j%2} += P(j) V(j); the first unit of each half in a segment
-    // starts the accumulator, after both O of the previous segment were read
+    // ---------------- PV issuer: O_b += P V for a pair's unit b; a segment's first pair starts the
+    // accumulators, after both O of the previous segment were read
     constexpr uint32_t id_pv = idesc_f32_format0(128, HD) | kIdescBMajorMN;
     const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
     bool ok = true;
+    int pj = 0;
+#pragma unroll 1
     for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
       const int cnt = min(w.units - w.unit, nunits - j0);
-      for (int j = j0; j < j0 + cnt && ok; ++j) {
-        const int b = j & 1;
-        ok = mbar_wait(&v16_full[b], (j >> 1) & 1, p.max_spin);
-        ok = ok && mbar_wait(&p_full[b], (j >> 1) & 1, p.max_spin);
-        if (j == j0 && seg > 0) ok = ok && mbar_wait(o_free, (seg - 1) & 1, p.max_spin);
-        ok = __all_sync(0xffffffffu, ok);
+      if (seg > 0) ok = mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin);
+#pragma unroll 1
+      for (int x = 0; x < ((cnt + 1) & ~1) && ok; ++x) {
+        const int b = x & 1;
+        ok = mbar_wait_warp(&v16_full[b], pj & 1, p.max_spin);
+        ok = ok && mbar_wait_warp(&p_full[b], pj & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
-        const uint32_t add = j < j0 + 2 ? 0u : 1u;
         if (elect_one()) {
+          if (x < cnt) {
+            const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kUnit / 16; ++kk)
-            tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
-                               vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, kk > 0 ? 1u : add);
+            for (int kk = 0; kk < kUnit / 16; ++kk)
+              tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
+                                 vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, (x > 1 || kk > 0) ? 1u : 0u);
+          }
           tc_commit(&p_empty[b]);
         }
         __syncwarp();
+        pj += b;
       }
       j0 += cnt;
       if (j0 < nunits) pos_next_pair(w, p, sseq);
@@ -482,7 +506,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
     if (elect_one()) tc_commit(&mma_done[1]);
     __syncwarp();
-    mbar_wait(&mma_done[1], 0, kDrainSpin);
+    mbar_wait_warp(&mma_done[1], 0, kDrainSpin);
   } else if (warp >= kWConv) {
     // ---------------- converters: V from e4m3 to f16, in the layout of a 128-byte-swizzled copy (rows
     // of 64 values, 16-byte chunk c of row r at c ^ (r & 7))
@@ -493,21 +517,24 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     const int t = (warp - kWConv) * 32 + lane;
     const int cc = t % CPR, r0 = t / CPR;
     uint8_t *out = sV16 + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
-    const uint8_t *src0 = s8 + C::UNIT8 + t * 8;
+    const uint8_t *src0 = s8 + C::PAIR8 + t * 8;
     bool ok = true;
-    int st = 0, ph = 0;
+    int st = 0, ph = 0, pj = 0;
+#pragma unroll 1
     for (int j0 = 0; j0 < nunits && ok;) {
       const int cnt = min(w.units - w.unit, nunits - j0);
       int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
-      for (int j = j0; j < j0 + cnt; ++j, keys -= kUnit) {
-        const int b = j & 1;
-        ok = mbar_wait(&kv8_full[st], ph, p.max_spin);
-        ok = ok && (j < 2 || mbar_wait(&p_empty[b], ((j >> 1) - 1) & 1, p.max_spin));
-        ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+      for (int x = 0; x < ((cnt + 1) & ~1); ++x, keys -= kUnit) {
+        const int b = x & 1;
+        if (b == 0) ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
+        ok = ok && (pj == 0 || mbar_wait_warp(&p_empty[b], (pj - 1) & 1, p.max_spin));
         if (!ok) break;
-        const uint8_t *src = src0 + st * 2 * C::UNIT8;
+        const uint8_t *src = src0 + st * 2 * C::PAIR8 + b * C::UNIT8;
         uint8_t *dst = out + b * C::TILE16;
-        if (keys < kUnit) {
+        if (x >= cnt) {
+          // half a pair
+        } else if (keys < kUnit) {
           // rows beyond the last key may hold anything (even NaN); P is 0 there
 #pragma unroll 2
           for (int e = 0; e < PER; ++e) {
@@ -524,22 +551,23 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&v16_full[b]);
-          mbar_arrive(&kv8_empty[st]);
-        }
-        if (++st == C::NS) {
-          st = 0;
-          ph ^= 1;
+        mbar_arrive_if(&v16_full[b], lane == 0);
+        if (b == 1) {
+          mbar_arrive_if(&kv8_empty[st], lane == 0);
+          ++pj;
+          if (++st == C::NS) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
       j0 += cnt;
       if (j0 < nunits) pos_next_pair(w, p, sseq);
     }
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
-  } else {
+  } else if (warp >= kWSoft) {
     // ---------------- softmax: thread = TMEM lane; lane l holds query row l % ROWS, copy l / ROWS
-    const int half = warp >> 2, q = warp & 3;
+    const int half = (warp - kWSoft) >> 2, q = warp & 3;
     const int tl = q * 32 + lane;
     const int r = tl % ROWS, copy = tl / ROWS;
     const int k0 = copy * KW;
@@ -550,10 +578,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     // Barrier of a half's warps, bounded like every other wait.
     auto half_sync = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&half_bar[half]);
-      const bool done = mbar_wait(&half_bar[half], half_phase, p.max_spin);
+      mbar_arrive_if(&half_bar[half], lane == 0);
+      const bool done = mbar_wait_warp(&half_bar[half], half_phase, p.max_spin);
       half_phase ^= 1;
-      return __all_sync(0xffffffffu, done) != 0;
+      return done;
     };
     if (RHO > 1) {  // the other copies' parts of the P rows stay zero
       const uint32_t z[16] = {};
@@ -566,9 +594,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     // hold bf16's 8, exactly down to 2^-10 of the largest value, below that to 2^-18 of it.
     // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
     auto load_q = [&](int seg, int n) {
-      bool ok = mbar_wait(q8_full, seg & 1, p.max_spin);
-      if (half == 0 && seg > 0) ok = ok && mbar_wait(q_empty, (seg - 1) & 1, p.max_spin);
-      if (!__all_sync(0xffffffffu, ok)) return -1.f;
+      bool ok = mbar_wait_warp(q8_full, seg & 1, p.max_spin);
+      if (half == 0 && seg > 0) ok = ok && mbar_wait_warp(q_empty, (seg - 1) & 1, p.max_spin);
+      if (!ok) return -1.f;
       const uint4 *src = reinterpret_cast<const uint4 *>(sQ + r * C::QPITCH);
       const bool have = r < n * G;
       float am = 0.f;
@@ -613,47 +641,64 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) {
-        if (half == 0) mbar_arrive(q_full);
-        mbar_arrive(q8_empty);
-      }
+      mbar_arrive_if(q_full, lane == 0 && half == 0);
+      mbar_arrive_if(q8_empty, lane == 0);
       return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
     };
-    float qfac = load_q(0, w.n);
-    bool ok = qfac >= 0.f;
+    float qfac = 0.f;
+    bool ok = true;
     int chunk = -1;                      // chunk of 32 units whose scales this warp may read
-    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
-      const int cnt = min(w.units - w.unit, nunits - j0);
+    int pj = 0, st = 0;                  // pair of units, and its stage of the ring
+    // Segment by segment: its units, then the queries of the next one (whose S can start), then the
+    // output of this one. The round before the first segment has the queries alone.
+#pragma unroll 1
+    for (int j0 = 0, seg = -1;; ++seg) {
+      const int cnt = seg < 0 ? 0 : min(w.units - w.unit, nunits - j0);
       const int lim = p.causal ? min(w.ctx + jq + 1, w.ctx + w.n) : w.ctx + w.n;
+      // keys from the segment's first unit on that every row sees
+      const int all = (p.causal ? w.ctx + 1 : w.ctx + w.n) - w.unit * kUnit;
       float m_run = kNoMax, l_run = 0.f;
-      int mine = -1;                     // last unit of this half in the segment
-      for (int j = j0 + ((j0 ^ half) & 1); j < j0 + cnt; j += 2) {
-        while (chunk < (j >> 5)) {       // the next chunk: give the one before back
+#pragma unroll 1
+      for (int u = half; u < ((cnt + 1) & ~1) + half; u += 2, ++pj) {
+        const int j = min(j0 + u, j0 + cnt - 1);
+        if (chunk < (j >> 5)) {          // the next chunk: give the one before back
           __syncwarp();
-          if (chunk >= 0 && lane == 0) mbar_arrive(&sc_empty[chunk & 1]);
+          if (chunk >= 0) mbar_arrive_if(&sc_empty[chunk & 1], lane == 0);
           ++chunk;
-          ok = ok && mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
+          ok = mbar_wait_warp(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
         }
         const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // K scale, log2 V, 1 / V, 0 for zeros
-        const int nv = lim - (w.unit + j - j0) * kUnit - k0;    // keys this thread sees of its part
-        ok = ok && mbar_wait(&s_full[half], (j >> 1) & 1, p.max_spin);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ok && mbar_wait_warp(s_full, pj & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
         float sv[KW];
         load_s<KW>(trow + C::S_COL + half * kUnit + k0, sv);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[half]);
-        if (__any_sync(0xffffffffu, nv < KW)) {
+        mbar_arrive_if(s_empty, lane == 0);
+        mbar_arrive_if(&kv8_empty[st], lane == 0 && warp == kWSoft);  // S complete: the keys have been read
+        st = st + 1 == C::NS ? 0 : st + 1;
+        // the P buffer and O_half are free once PV of this half's previous unit has completed
+        bool freed = pj == 0;
+        if (u >= cnt) {                  // half a pair
+          ok = freed || mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          if (!ok) break;
+          mbar_arrive_if(&p_full[half], lane == 0);
+          continue;
+        }
+        if (all - kUnit * u < kUnit) {   // some row does not see the whole unit
+          const int nv = lim - (w.unit + u) * kUnit - k0;  // keys this thread sees of its part
 #pragma unroll
           for (int c = 0; c < KW; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
         }
         const float c1 = fmaxf(qfac * sc.x, 1e-37f);
         float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int c = 4; c < KW; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-        const float m_new = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c1, sc.y);
+        for (int c = 4; c + 8 <= KW; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[c + 2 * e], sv[c + 2 * e + 1]);
+        mx[3] = max3(max3(mx[3], sv[KW - 4], sv[KW - 3]), sv[KW - 2], sv[KW - 1]);
+        const float m_new = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c1, sc.y);
         const bool need = m_new - m_run > kRescale;
         float alpha = 1.f;
         if (need) {
@@ -661,13 +706,11 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
           m_run = m_new;
           l_run *= alpha;
         }
-        // P buffer and O_half: free once PV of this half's previous unit has completed
-        if (j >= 2) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&p_empty[half], ((j >> 1) - 1) & 1, p.max_spin));
+        if (u >= 2 && __any_sync(0xffffffffu, need && r < R)) {
+          ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
           if (!ok) break;
           tc_fence_after();
-        }
-        if (j >= j0 + 2 && __any_sync(0xffffffffu, need && r < R)) {
+          freed = true;
 #pragma unroll 1
           for (int cc = 0; cc < HD / 16; ++cc) {
             float ov[16];
@@ -680,49 +723,52 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         }
         const float c2 = sc.y - m_run + kPBase;
         uint32_t pk[KW / 2];
-        float ls[2] = {0.f, 0.f};
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < KW; c += 2) {
-          const float p0 = ex2f(fmaf(sv[c], c1, c2));
-          const float p1 = ex2f(fmaf(sv[c + 1], c1, c2));
-          ls[0] += p0;
-          ls[1] += p1;
-          const __half2 y = __floats2half2_rn(p0, p1);
+          const float2 x = fma2(make_float2(sv[c], sv[c + 1]), make_float2(c1, c1), make_float2(c2, c2));
+          const float2 e = make_float2(ex2f(x.x), ex2f(x.y));
+          ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], e);
+          const __half2 y = __floats2half2_rn(e.x, e.y);
           pk[c / 2] = *reinterpret_cast<const uint32_t *>(&y);
         }
-        l_run = fmaf(ls[0] + ls[1], sc.z, l_run);
+        const float2 lt = add2(ls[0], ls[1]);
+        l_run = fmaf(lt.x + lt.y, sc.z, l_run);
         if (sc.w == 0.f) {
 #pragma unroll
           for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
+        }
+        if (!freed) {
+          ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          if (!ok) break;
+          tc_fence_after();
         }
         store_p<KW>(trow + C::P_COL + half * 32 + k0 / 2, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[half]);
-        mine = j;
+        mbar_arrive_if(&p_full[half], lane == 0);
       }
       if (!ok) break;
-      // ---- segment end: the next segment's queries first (its S can start), then this one's O
       const int i = w.i, g = w.g, n = w.n;
       const bool whole = w.unit == 0 && cnt == w.units;
       j0 += cnt;
-      float qnext = 0.f;
-      if (j0 < nunits) {
-        pos_next_pair(w, p, sseq);
-        qnext = load_q(seg + 1, w.n);
-        ok = qnext >= 0.f;
+      const bool more = j0 < nunits;
+      if (more) {
+        if (seg >= 0) pos_next_pair(w, p, sseq);
+        qfac = load_q(seg + 1, w.n);
+        ok = qfac >= 0.f;
       }
-      ok = ok && (mine < 0 || mbar_wait(&p_empty[half], (mine >> 1) & 1, p.max_spin));
+      if (seg < 0 && ok) continue;
+      ok = ok && mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
       // the (maximum, sum) slots are free once the previous segment's were read
-      ok = ok && (seg == 0 || mbar_wait(o_free, (seg - 1) & 1, p.max_spin));
-      ok = __all_sync(0xffffffffu, ok);
+      ok = ok && (seg == 0 || mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin));
       if (!ok) break;
-      ml[half * 128 + tl] = mine >= 0 ? make_float2(m_run, l_run) : make_float2(kNoMax, 0.f);
+      ml[half * 128 + tl] = make_float2(m_run, l_run);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(seg_bar);
-      ok = __all_sync(0xffffffffu, mbar_wait(seg_bar, seg & 1, p.max_spin));
+      mbar_arrive_if(seg_bar, lane == 0);
+      ok = mbar_wait_warp(seg_bar, seg & 1, p.max_spin);
       if (!ok) break;
       tc_fence_after();
       float M = kNoMax, L = 0.f;
@@ -732,8 +778,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       for (int c = 0; c < 2 * RHO; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
       const size_t row0 = (static_cast<size_t>(i * p.Hkv + g) + blockIdx.x) * R;   // partial rows
       const float inv = whole ? 1.0f / L : 1.0f;
-      const bool has0 = cnt > 1 || (j0 - 1) % 2 == 0, has1 = cnt > 1 || (j0 - 1) % 2 == 1;
-      const float a0 = has0 ? ex2f(ml[tl].x - M) * inv : 0.f, a1 = has1 ? ex2f(ml[128 + tl].x - M) * inv : 0.f;
+      const bool has1 = cnt > 1;
+      const float a0 = ex2f(ml[tl].x - M) * inv, a1 = has1 ? ex2f(ml[128 + tl].x - M) * inv : 0.f;
       const int live = n * G;            // rows that are computed
       if (half == 0 && copy == 0 && r < live && !whole)
         *reinterpret_cast<float2 *>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
@@ -747,7 +793,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
           tmem_ld16(trow + C::O_COL + c0, ov);
           tmem_ld16(trow + C::O_COL + HD + c0, o1);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) ov[c] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1[c] * a1 : 0.f);
+          for (int c = 0; c < 16; ++c) ov[c] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
           if (r < live) {
             if (whole) {
               uint16_t *dst = o + (static_cast<size_t>(jq) * p.Hq + r % G) * HD + c0;
@@ -781,7 +827,7 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
               float *to = stage + (copy * live + r) * cw;
 #pragma unroll
               for (int c = 0; c < 16; ++c)   // columns turned by the row: no bank conflicts
-                to[(cc + c + r) & (cw - 1)] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1[c] * a1 : 0.f);
+                to[(cc + c + r) & (cw - 1)] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
             }
             __syncwarp();
           }
@@ -808,8 +854,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
-      qfac = qnext;
+      mbar_arrive_if(o_free, lane == 0);
+      if (!more) break;
     }
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   }
@@ -829,8 +875,9 @@ constexpr int kMerge8Warps = 8;
 template <int HD>
 __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __grid_constant__ Attn8Params p) {
   constexpr int E = HD / 32;
-  griddep_wait();
-  griddep_launch();
+  // The schedule reads only the lengths, written before the attention kernel let this one start.
+  // This grid's end must imply the attention's: CTA (0, 0) always waits for it; others with
+  // nothing to join leave at once.
   const int pair = blockIdx.x;
   const int i = pair / p.Hkv, g = pair % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -838,23 +885,19 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
   const int R = G * p.m;
   const int r = blockIdx.y * kMerge8Warps + warp;
   const Seq8 s = seq8(p, i);
-  if (r >= R || r / G >= s.n) return;
-  long long T = 0, before = 0;
-  for (int q = lane; q < p.nb; q += 32) {
-    const int u = seq8(p, q).units;
-    T += u;
-    before += q < i ? u : 0;
+  int before, c0 = 0, c1 = 0;
+  const int T = total_units(p, i, lane, &before);
+  const bool live = r < R && r / G < s.n;
+  if (live) {
+    const int Ge = min(T, p.grid);
+    const int A = before + g * s.units;
+    c0 = cta_of(T, Ge, A);
+    c1 = cta_of(T, Ge, A + s.units - 1);
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    T += __shfl_xor_sync(0xffffffffu, T, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  T *= p.Hkv;
-  const int Ge = T < p.grid ? static_cast<int>(T) : p.grid;
-  const long long A = before * p.Hkv + static_cast<long long>(g) * s.units;
-  const int c0 = cta_of(T, Ge, A), c1 = cta_of(T, Ge, A + s.units - 1);
-  if (c0 == c1) return;  // written whole by the attention kernel
+  const bool join = live && c0 != c1;  // else written whole by the attention kernel
+  if (join || (blockIdx.x == 0 && blockIdx.y == 0)) griddep_wait();
+  griddep_launch();
+  if (!join) return;
   float M = kNoMax, L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
