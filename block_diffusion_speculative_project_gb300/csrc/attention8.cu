@@ -112,37 +112,51 @@ __device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
 
 // ---------------------------------------------------------------- tensor-core kernel
 
-// RHO copies of the query rows fill the 128 lanes of the MMA (rows padded to 128 / RHO): the lanes
-// of copy c take only the c-th part of a unit's keys, the other parts' probabilities being zero
-// in the P operand, so that every SM quarter's warps share the exponentials of few rows.
+// RHO copies of the query rows fill the 128 lanes of the MMA (rows padded to 128 / RHO); each copy
+// takes units of its own, so that a softmax thread works on all 64 keys of a unit and every SM
+// quarter's warps share the work of few rows. PV leaves the other copies' lanes of O as they are.
+//   RHO = 4   groups 0 .. 3 of one warp: the lanes of copy g; a pair of units (see below) goes to
+//             the groups 0, 1 or 2, 3 in turn
+//   RHO = 2   groups 0, 1 of two warps
+//   RHO = 1   groups 0, 1 of four warps, with an O each (there is no second copy), for which one
+//             pair of S and of P buffers has to do
 template <int HD, int RHO>
 struct A8Cfg {
-  static constexpr int KW = kUnit / RHO;             // keys of a unit per copy
   static constexpr int ROWS = 128 / RHO;             // padded query rows
+  static constexpr int NG = RHO == 4 ? 4 : 2;        // softmax groups
+  static constexpr int NO = RHO == 1 ? 2 : 1;        // O accumulators
+  static constexpr int WPG = RHO == 4 ? 1 : RHO == 2 ? 2 : 4;  // warps of a group
+  static constexpr int DEEP = RHO == 1 ? 1 : 2;      // buffers of a pair's S and P
   static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
   static constexpr int PAIR8 = 2 * UNIT8;
   // ring of pairs of units in 8 bits, keys then values, as much as shared memory holds
-  static constexpr int NS = 4 * (128 / HD);
+  static constexpr int NS = (RHO == 1 ? 3 : 4) * (128 / HD);
   static constexpr int ATOM16 = kUnit * 128;
   static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
   static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
-  static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of a half's exchange of O between copies
-  static constexpr int OFF_8 = 2 * TILE16;
+  static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of the exchange of O between copies
+  static constexpr int OFF_8 = 4 * TILE16;           // two pairs of units' V in f16, then the ring
   static constexpr int OFF_Q = OFF_8 + NS * 2 * PAIR8;
   static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
-  static constexpr int OFF_ML = OFF_STG + 2 * STAGE * 4;  // [2 halves][128 lanes] (maximum, sum)
-  static constexpr int OFF_SC = OFF_ML + 2 * 128 * 8;     // [2 chunks][32 units] scales
+  static constexpr int OFF_ML = OFF_STG + STAGE * 4;      // [NO][128 lanes] (maximum, sum)
+  static constexpr int OFF_SC = OFF_ML + NO * 128 * 8;    // [2 chunks][32 units] scales
   static constexpr int OFF_BAR = OFF_SC + 64 * 16;
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
   static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t S_COL = 0;                // S of a pair of units: 64 columns each
-  static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
-  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // queries, two e4m3 terms: hd / 4 columns each
-  static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of a pair's units: 32 columns each
+  static constexpr uint32_t S_COL = 0;                     // S of pair pj in buffer pj % DEEP: 64 columns a unit
+  static constexpr uint32_t O_COL = DEEP * 128;            // O: hd columns each
+  static constexpr uint32_t Q_COL = O_COL + NO * HD;       // queries, two e4m3 terms: hd / 4 columns each
+  static constexpr uint32_t P_COL = Q_COL + HD / 2;        // P: 32 columns a unit; a buffer pj % 2 for the
+                                                           // pair (its units lie in different lanes), or,
+                                                           // RHO = 1, one for either unit
   static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
+  // Warps: producer, S issuer, PV issuer, one that only helps at the start, softmax (warp w reads
+  // TMEM lanes of quarter w % 4), then the converters of V.
+  static constexpr int W_CONV = 4 + 4 * NO;
+  static constexpr int THREADS = (W_CONV + 4) * 32;
 };
 constexpr int kSeqCache = 128;
 constexpr int kDrainSpin = 1 << 22;
@@ -151,16 +165,13 @@ constexpr int kDrainSpin = 1 << 22;
 // the largest still has all 11 bits (2^-31 one bit).
 constexpr float kPBase = 7.f, kRescale = 8.f;
 
-// A segment's units are taken in pairs: one S product of 128 keys, then softmax, PV and O for each
-// unit of the pair on its own. What bounds the kernel are the steps from one role to the next (with
-// every copy, product and exponential left out it still took 0.8 of its time, a unit at a time), so
-// they are paid for two units at once. Half a pair at the end of a segment of an odd number of units
-// is signalled by every role without work.
-// Warps: producer, S issuer, PV issuer, one that only helps at the start, softmax half h = 0, 1 (a
-// pair's first or second unit) in 4 + 4h .. 7 + 4h (warp w reads TMEM lanes of quarter w % 4), then
-// the converters of V.
-constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWAid = 3, kWSoft = 4, kWConv = 12, kNumConv = 4;
-constexpr int kA8Threads = (kWConv + kNumConv) * 32;
+// A segment's units are taken in pairs: one S product of 128 keys, then a softmax for each unit by a
+// group of its own, then both PV. What bounds the kernel are the steps from one role to the next
+// (with every copy, product and exponential left out it still took 0.7 of its time, when each
+// warp went through every unit), so they are paid for two units at once, and a softmax warp goes
+// through every second or fourth unit only. Half a pair at the end of a segment of an odd number of
+// units is signalled by its group without work.
+constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWAid = 3, kWSoft = 4, kNumConv = 4;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -196,25 +207,6 @@ __device__ __forceinline__ void pos_next_pair(Pos8 &w, const Attn8Params &p, con
   }
 }
 
-template <int KW>
-__device__ __forceinline__ void load_s(uint32_t taddr, float (&v)[KW]) {
-  if constexpr (KW == 64)
-    tmem_ld64(taddr, v);
-  else if constexpr (KW == 32)
-    tmem_ld32(taddr, v);
-  else
-    tmem_ld16(taddr, v);
-}
-template <int KW>
-__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t *v) {
-  if constexpr (KW == 64)
-    tmem_st32_raw(taddr, v);
-  else if constexpr (KW == 32)
-    tmem_st16_raw(taddr, v);
-  else
-    tmem_st8_raw(taddr, v);
-}
-
 // 8 e4m3 values to f16 (exact).
 __device__ __forceinline__ uint4 widen8(uint2 u) {
   uint4 h;
@@ -239,9 +231,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int HD, int RHO>
-__global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
+__global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
   using C = A8Cfg<HD, RHO>;
-  constexpr int KW = C::KW, ROWS = C::ROWS;
+  constexpr int ROWS = C::ROWS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -250,24 +242,24 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
   float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
   uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv8_empty = kv8_full + C::NS;
-  uint64_t *v16_full = kv8_empty + C::NS;   // [2] a pair's first and second unit
-  uint64_t *p_full = v16_full + 2;          // [2]
-  uint64_t *p_empty = p_full + 2;           // [2] PV complete: the P and V16 buffers have been read
-  uint64_t *sc_full = p_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
+  uint64_t *v16_full = kv8_empty + C::NS;   // [2] V of pair pj in f16, buffer pj % 2
+  uint64_t *p_full = v16_full + 2;          // [2] P of pair pj
+  uint64_t *pv_done = p_full + 2;           // [2] PV of pair pj complete: P and V16 have been read
+  uint64_t *s_full = pv_done + 2;           // [2] S of pair pj complete, buffer pj % DEEP
+  uint64_t *s_empty = s_full + 2;           // [2] and read by both groups
+  uint64_t *sc_full = s_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
   uint64_t *sc_empty = sc_full + 2;         // [2]
-  uint64_t *half_bar = sc_empty + 2;        // [2] the four warps of a half among themselves
+  uint64_t *half_bar = sc_empty + 2;        // [2] four softmax warps among themselves
   uint64_t *mma_done = half_bar + 2;        // [2]
-  uint64_t *s_full = mma_done + 2;          // S of a pair complete
-  uint64_t *s_empty = s_full + 1;           // and read by both halves
-  uint64_t *q8_full = s_empty + 1;          // a segment's query rows have landed
+  uint64_t *q8_full = mma_done + 2;         // a segment's query rows have landed
   uint64_t *q8_empty = q8_full + 1;
   uint64_t *q_full = q8_empty + 1;          // and are in tensor memory
   uint64_t *q_empty = q_full + 1;
-  uint64_t *seg_bar = q_empty + 1;          // both halves: (maximum, sum) of a segment written
-  uint64_t *o_free = seg_bar + 1;           // both O and ml read
+  uint64_t *seg_bar = q_empty + 1;          // every softmax warp: (maximum, sum) of a segment written
+  uint64_t *o_free = seg_bar + 1;           // O and ml read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 14 + 8) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((2 * C::NS + 18 + 6) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -281,21 +273,21 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&v16_full[b], kNumConv);
-      mbar_init(&p_full[b], 4);
-      mbar_init(&p_empty[b], 1);
+      mbar_init(&p_full[b], 2 * C::WPG);
+      mbar_init(&pv_done[b], 1);
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_empty[b], 2 * C::WPG);
       mbar_init(&sc_full[b], 1);
-      mbar_init(&sc_empty[b], 8);
+      mbar_init(&sc_empty[b], 4 * C::NO);
       mbar_init(&half_bar[b], 4);
       mbar_init(&mma_done[b], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, 8);
     mbar_init(q8_full, 1);
-    mbar_init(q8_empty, 8);
+    mbar_init(q8_empty, 4 * C::NO);
     mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
-    mbar_init(seg_bar, 8);
-    mbar_init(o_free, 8);
+    mbar_init(seg_bar, 4 * C::NO);
+    mbar_init(o_free, 4 * C::NO);
     fence_mbar_init();
   }
   if (warp == kWS) {
@@ -400,10 +392,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         slot = 1;
       }
       // The chunk's scales, after its first copies are under way, and before any wait for a unit
-      // of the chunk: a copy waits for the pair NS > 3 before its own, the next segment's queries
+      // of the chunk: a copy waits for the pair NS >= 3 before its own, the next segment's queries
       // for the units of the segment before last.
       published = published && k != 0;
-      if (!published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
+      if (!published && (k == 2 || j == nunits - 1 || cnt_left == 0)) {
         published = true;
         ok = c < 2 || mbar_wait_warp(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
         if (!ok) break;
@@ -442,7 +434,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
 #pragma unroll 1
       for (int u = 0; u < cnt && ok; u += 2, ++pj) {
         ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
-        ok = ok && (pj == 0 || mbar_wait_warp(s_empty, (pj - 1) & 1, p.max_spin));
+        const int b = pj % C::DEEP;
+        ok = ok && (pj < C::DEEP || mbar_wait_warp(&s_empty[b], (pj / C::DEEP - 1) & 1, p.max_spin));
         if (!ok) break;
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>((st * 2 * C::PAIR8) >> 4);
@@ -450,9 +443,9 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 2 * HD / 32; ++kk)
-            tc_mma_e4m3_tmem_a(tmem + C::S_COL, tmem + C::Q_COL + kk * 8,
+            tc_mma_e4m3_tmem_a(tmem + C::S_COL + b * 128, tmem + C::Q_COL + kk * 8,
                                kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id, kk > 0 ? 1u : 0u);
-          tc_commit(s_full);
+          tc_commit(&s_full[b]);
           if (u + 2 >= cnt) tc_commit(q_empty);
         }
         __syncwarp();
@@ -470,8 +463,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     __syncwarp();
     mbar_wait_warp(&mma_done[0], 0, kDrainSpin);
   } else if (warp == kWPV) {
-    // ---------------- PV issuer: O_b += P V for a pair's unit b; a segment's first pair starts the
-    // accumulators, after both O of the previous segment were read
+    // ---------------- PV issuer: O += P V for both units of a pair; a segment's first unit of each
+    // group starts the accumulator, after the previous segment's O was read
     constexpr uint32_t id_pv = idesc_f32_format0(128, HD) | kIdescBMajorMN;
     const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
     bool ok = true;
@@ -481,24 +474,36 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       const int cnt = min(w.units - w.unit, nunits - j0);
       if (seg > 0) ok = mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin);
 #pragma unroll 1
-      for (int x = 0; x < ((cnt + 1) & ~1) && ok; ++x) {
-        const int b = x & 1;
-        ok = mbar_wait_warp(&v16_full[b], pj & 1, p.max_spin);
-        ok = ok && mbar_wait_warp(&p_full[b], pj & 1, p.max_spin);
+      for (int u = 0; u < cnt && ok; u += 2, ++pj) {
+        const int b = pj & 1;
+        ok = mbar_wait_warp(&v16_full[b], (pj >> 1) & 1, p.max_spin);
+        ok = ok && mbar_wait_warp(&p_full[b], (pj >> 1) & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          if (x < cnt) {
-            const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+          const uint32_t add = u >= C::NG ? 1u : 0u;
 #pragma unroll
-            for (int kk = 0; kk < kUnit / 16; ++kk)
-              tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
-                                 vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, (x > 1 || kk > 0) ? 1u : 0u);
+          for (int x = 0; x < 2; ++x) {
+            if (u + x >= cnt) break;
+            const uint64_t vd = vd0 + static_cast<uint64_t>(((b * 2 + x) * C::TILE16) >> 4);
+            const int g = RHO == 4 ? 2 * b + x : x;  // the unit's group
+            uint32_t off[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) off[y] = RHO == 1 || y * 32 / ROWS == g ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+            for (int kk = 0; kk < kUnit / 16; ++kk) {
+              const uint64_t d = vd + static_cast<uint64_t>((kk * 16 * 128) >> 4);
+              if (RHO == 1)
+                tc_mma_bf16_tmem_a(tmem + C::O_COL + x * HD, tmem + C::P_COL + x * 32 + kk * 8, d, id_pv,
+                                   kk > 0 ? 1u : add);
+              else
+                tc_mma_bf16_tmem_a_lanes(tmem + C::O_COL, tmem + C::P_COL + b * 32 + kk * 8, d, id_pv, off,
+                                         kk > 0 ? 1u : add);
+            }
           }
-          tc_commit(&p_empty[b]);
+          tc_commit(&pv_done[b]);
         }
         __syncwarp();
-        pj += b;
       }
       j0 += cnt;
       if (j0 < nunits) pos_next_pair(w, p, sseq);
@@ -507,14 +512,14 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     if (elect_one()) tc_commit(&mma_done[1]);
     __syncwarp();
     mbar_wait_warp(&mma_done[1], 0, kDrainSpin);
-  } else if (warp >= kWConv) {
+  } else if (warp >= C::W_CONV) {
     // ---------------- converters: V from e4m3 to f16, in the layout of a 128-byte-swizzled copy (rows
     // of 64 values, 16-byte chunk c of row r at c ^ (r & 7))
     constexpr int CPR = HD / 8;                        // 8-value chunks of a row: 8 bytes to 16
     constexpr int RPI = kNumConv * 32 / CPR;           // rows per iteration: 8 or 16
     constexpr int PER = kUnit / RPI;                   // chunks per thread
     static_assert(RPI % 8 == 0, "a thread's chunks all lie at the same place of their rows");
-    const int t = (warp - kWConv) * 32 + lane;
+    const int t = (warp - C::W_CONV) * 32 + lane;
     const int cc = t % CPR, r0 = t / CPR;
     uint8_t *out = sV16 + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
     const uint8_t *src0 = s8 + C::PAIR8 + t * 8;
@@ -525,16 +530,16 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       const int cnt = min(w.units - w.unit, nunits - j0);
       int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
 #pragma unroll 1
-      for (int x = 0; x < ((cnt + 1) & ~1); ++x, keys -= kUnit) {
-        const int b = x & 1;
-        if (b == 0) ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
-        ok = ok && (pj == 0 || mbar_wait_warp(&p_empty[b], (pj - 1) & 1, p.max_spin));
-        if (!ok) break;
-        const uint8_t *src = src0 + st * 2 * C::PAIR8 + b * C::UNIT8;
-        uint8_t *dst = out + b * C::TILE16;
-        if (x >= cnt) {
-          // half a pair
-        } else if (keys < kUnit) {
+      for (int x = 0; x < cnt; ++x, keys -= kUnit) {
+        const int b = pj & 1, slot = x & 1;
+        if (slot == 0) {
+          ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
+          ok = ok && (pj < 2 || mbar_wait_warp(&pv_done[b], ((pj >> 1) - 1) & 1, p.max_spin));
+          if (!ok) break;
+        }
+        const uint8_t *src = src0 + st * 2 * C::PAIR8 + slot * C::UNIT8;
+        uint8_t *dst = out + (b * 2 + slot) * C::TILE16;
+        if (keys < kUnit) {
           // rows beyond the last key may hold anything (even NaN); P is 0 there
 #pragma unroll 2
           for (int e = 0; e < PER; ++e) {
@@ -549,10 +554,10 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < PER; ++e) *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = widen8(u[e]);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        mbar_arrive_if(&v16_full[b], lane == 0);
-        if (b == 1) {
+        if (slot == 1 || x == cnt - 1) {  // the pair is complete
+          fence_proxy_async_smem();
+          __syncwarp();
+          mbar_arrive_if(&v16_full[b], lane == 0);
           mbar_arrive_if(&kv8_empty[st], lane == 0);
           ++pj;
           if (++st == C::NS) {
@@ -567,15 +572,16 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   } else if (warp >= kWSoft) {
     // ---------------- softmax: thread = TMEM lane; lane l holds query row l % ROWS, copy l / ROWS
-    const int half = (warp - kWSoft) >> 2, q = warp & 3;
-    const int tl = q * 32 + lane;
+    const int half = (warp - kWSoft) >> 2;   // RHO = 1: the group, and its O
+    const int tl = (warp & 3) * 32 + lane;
     const int r = tl % ROWS, copy = tl / ROWS;
-    const int k0 = copy * KW;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int grp = RHO == 1 ? half : copy, slot = grp & 1;
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t o_mine = trow + C::O_COL + (RHO == 1 ? half * HD : 0);
     const int jq = r / G;               // row r: query row jq of query head g * G + r % G
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
     uint32_t half_phase = 0;
-    // Barrier of a half's warps, bounded like every other wait.
+    // Barrier of four warps, bounded like every other wait.
     auto half_sync = [&]() {
       __syncwarp();
       mbar_arrive_if(&half_bar[half], lane == 0);
@@ -583,12 +589,6 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       half_phase ^= 1;
       return done;
     };
-    if (RHO > 1) {  // the other copies' parts of the P rows stay zero
-      const uint32_t z[16] = {};
-      tmem_st16_raw(trow + C::P_COL + half * 32, z);
-      tmem_st16_raw(trow + C::P_COL + half * 32 + 16, z);
-      tmem_wait_st();
-    }
     // The query row of segment `seg` (n rows a sequence), scaled by a power of two so that its
     // largest value lies in [2^7, 2^8), to tensor memory as the sum of two e4m3 terms: 4 bits each
     // hold bf16's 8, exactly down to 2^-10 of the largest value, below that to 2^-18 of it.
@@ -659,45 +659,50 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       const int all = (p.causal ? w.ctx + 1 : w.ctx + w.n) - w.unit * kUnit;
       float m_run = kNoMax, l_run = 0.f;
 #pragma unroll 1
-      for (int u = half; u < ((cnt + 1) & ~1) + half; u += 2, ++pj) {
+      for (int u = slot; u < ((cnt + 1) & ~1) + slot; u += 2, ++pj) {
         const int j = min(j0 + u, j0 + cnt - 1);
         if (chunk < (j >> 5)) {          // the next chunk: give the one before back
           __syncwarp();
           if (chunk >= 0) mbar_arrive_if(&sc_empty[chunk & 1], lane == 0);
           ++chunk;
           ok = mbar_wait_warp(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
+          if (!ok) break;
         }
+        const int st_now = st;
+        st = st + 1 == C::NS ? 0 : st + 1;
+        if (RHO == 4 && (pj & 1) != (grp >> 1)) continue;  // the other two groups' pair
         const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // K scale, log2 V, 1 / V, 0 for zeros
-        ok = ok && mbar_wait_warp(s_full, pj & 1, p.max_spin);
+        const int sb = pj % C::DEEP, pb = pj & 1;
+        ok = mbar_wait_warp(&s_full[sb], (pj / C::DEEP) & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
-        float sv[KW];
-        load_s<KW>(trow + C::S_COL + half * kUnit + k0, sv);
+        float sv[kUnit];
+        tmem_ld64(trow + C::S_COL + sb * 128 + slot * kUnit, sv);
         tc_fence_before();
         __syncwarp();
-        mbar_arrive_if(s_empty, lane == 0);
-        mbar_arrive_if(&kv8_empty[st], lane == 0 && warp == kWSoft);  // S complete: the keys have been read
-        st = st + 1 == C::NS ? 0 : st + 1;
-        // the P buffer and O_half are free once PV of this half's previous unit has completed
-        bool freed = pj == 0;
+        mbar_arrive_if(&s_empty[sb], lane == 0);
+        mbar_arrive_if(&kv8_empty[st_now], slot == 0 && r == 0);  // S complete: the keys have been read
+        // this group's P buffer is free once the PV that read it has completed
+        const int pp = RHO == 1 ? pj - 1 : pj - 2;
+        bool freed = pp < 0;
         if (u >= cnt) {                  // half a pair
-          ok = freed || mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          ok = freed || mbar_wait_warp(&pv_done[pp & 1], (pp >> 1) & 1, p.max_spin);
           if (!ok) break;
-          mbar_arrive_if(&p_full[half], lane == 0);
+          mbar_arrive_if(&p_full[pb], lane == 0);
           continue;
         }
         if (all - kUnit * u < kUnit) {   // some row does not see the whole unit
-          const int nv = lim - (w.unit + u) * kUnit - k0;  // keys this thread sees of its part
+          const int nv = lim - (w.unit + u) * kUnit;  // keys this row sees
 #pragma unroll
-          for (int c = 0; c < KW; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
+          for (int c = 0; c < kUnit; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
         }
         const float c1 = fmaxf(qfac * sc.x, 1e-37f);
         float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int c = 4; c + 8 <= KW; c += 8)
+        for (int c = 4; c + 8 <= kUnit; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[c + 2 * e], sv[c + 2 * e + 1]);
-        mx[3] = max3(max3(mx[3], sv[KW - 4], sv[KW - 3]), sv[KW - 2], sv[KW - 1]);
+        mx[3] = max3(max3(mx[3], sv[kUnit - 4], sv[kUnit - 3]), sv[kUnit - 2], sv[kUnit - 1]);
         const float m_new = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c1, sc.y);
         const bool need = m_new - m_run > kRescale;
         float alpha = 1.f;
@@ -706,26 +711,28 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
           m_run = m_new;
           l_run *= alpha;
         }
-        if (u >= 2 && __any_sync(0xffffffffu, need && r < R)) {
-          ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+        if (u >= C::NG && __any_sync(0xffffffffu, need && r < R)) {
+          // O *= alpha, once this group's last PV has completed: the pair NG / 2 before
+          const int pl = pj - C::NG / 2;
+          ok = mbar_wait_warp(&pv_done[pl & 1], (pl >> 1) & 1, p.max_spin);
           if (!ok) break;
           tc_fence_after();
-          freed = true;
+          freed = pl >= pp;
 #pragma unroll 1
           for (int cc = 0; cc < HD / 16; ++cc) {
             float ov[16];
-            tmem_ld16(trow + C::O_COL + half * HD + cc * 16, ov);
+            tmem_ld16(o_mine + cc * 16, ov);
             uint32_t x[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(ov[c] * alpha);
-            tmem_st16_raw(trow + C::O_COL + half * HD + cc * 16, x);
+            tmem_st16_raw(o_mine + cc * 16, x);
           }
         }
         const float c2 = sc.y - m_run + kPBase;
-        uint32_t pk[KW / 2];
+        uint32_t pk[kUnit / 2];
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < KW; c += 2) {
+        for (int c = 0; c < kUnit; c += 2) {
           const float2 x = fma2(make_float2(sv[c], sv[c + 1]), make_float2(c1, c1), make_float2(c2, c2));
           const float2 e = make_float2(ex2f(x.x), ex2f(x.y));
           ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], e);
@@ -736,18 +743,18 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         l_run = fmaf(lt.x + lt.y, sc.z, l_run);
         if (sc.w == 0.f) {
 #pragma unroll
-          for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
+          for (int c = 0; c < kUnit / 2; ++c) pk[c] = 0u;
         }
         if (!freed) {
-          ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          ok = mbar_wait_warp(&pv_done[pp & 1], (pp >> 1) & 1, p.max_spin);
           if (!ok) break;
           tc_fence_after();
         }
-        store_p<KW>(trow + C::P_COL + half * 32 + k0 / 2, pk);
+        tmem_st32_raw(trow + C::P_COL + (RHO == 1 ? slot : pb) * 32, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        mbar_arrive_if(&p_full[half], lane == 0);
+        mbar_arrive_if(&p_full[pb], lane == 0);
       }
       if (!ok) break;
       const int i = w.i, g = w.g, n = w.n;
@@ -760,7 +767,8 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
         ok = qfac >= 0.f;
       }
       if (seg < 0 && ok) continue;
-      ok = ok && mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+      // every PV of the segment has completed
+      ok = ok && mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
       // the (maximum, sum) slots are free once the previous segment's were read
       ok = ok && (seg == 0 || mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin));
       if (!ok) break;
@@ -771,22 +779,22 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
       ok = mbar_wait_warp(seg_bar, seg & 1, p.max_spin);
       if (!ok) break;
       tc_fence_after();
+      // the sets that make up a row: a copy's lanes, or RHO = 1 the two O of its lane
       float M = kNoMax, L = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2 * RHO; ++c) M = fmaxf(M, ml[c * ROWS + r].x);
+      for (int c = 0; c < C::NG; ++c) M = fmaxf(M, ml[c * ROWS + r].x);
 #pragma unroll
-      for (int c = 0; c < 2 * RHO; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
+      for (int c = 0; c < C::NG; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
       const size_t row0 = (static_cast<size_t>(i * p.Hkv + g) + blockIdx.x) * R;   // partial rows
       const float inv = whole ? 1.0f / L : 1.0f;
-      const bool has1 = cnt > 1;
-      const float a0 = ex2f(ml[tl].x - M) * inv, a1 = has1 ? ex2f(ml[128 + tl].x - M) * inv : 0.f;
       const int live = n * G;            // rows that are computed
       if (half == 0 && copy == 0 && r < live && !whole)
         *reinterpret_cast<float2 *>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
-      // Each half takes its half of the columns of O_0 and O_1. With copies, a chunk of cw columns
-      // of every copy goes through shared memory, and the half's threads add the copies up.
       uint16_t *o = p.o + (static_cast<size_t>(i) * p.m * p.Hq + g * G) * HD;
       if constexpr (RHO == 1) {
+        // each group takes half of the columns of both O
+        const bool has1 = cnt > 1;
+        const float a0 = ex2f(ml[tl].x - M) * inv, a1 = ex2f(ml[128 + tl].x - M) * inv;
 #pragma unroll 1
         for (int c0 = half * (HD / 2); c0 < (half + 1) * (HD / 2); c0 += 16) {
           float ov[16], o1[16];
@@ -813,25 +821,29 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
           __syncwarp();
         }
       } else {
-        float *stage = reinterpret_cast<float *>(smem + C::OFF_STG) + half * C::STAGE;
-        int cw = HD / 2;                 // columns per chunk: RHO * live rows of cw fit the buffer
+        // A chunk of cw columns of every copy goes through shared memory, and the threads add the
+        // copies up. A copy that had no unit of the segment holds what it held before.
+        const float a = ex2f(m_run - M) * inv;
+        const bool has = m_run != kNoMax || l_run != 0.f;
+        float *stage = reinterpret_cast<float *>(smem + C::OFF_STG);
+        int cw = HD;                     // columns per chunk: RHO * live rows of cw fit the buffer
         while (RHO * live * cw > C::STAGE) cw >>= 1;
-        for (int c0 = 0; c0 < HD / 2 && ok; c0 += cw) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD && ok; c0 += cw) {
 #pragma unroll 1
           for (int cc = 0; cc < cw; cc += 16) {
-            const uint32_t col = half * (HD / 2) + c0 + cc;
-            float ov[16], o1[16];
-            tmem_ld16(trow + C::O_COL + col, ov);
-            tmem_ld16(trow + C::O_COL + HD + col, o1);
+            float ov[16];
+            tmem_ld16(o_mine + c0 + cc, ov);
             if (r < live) {
               float *to = stage + (copy * live + r) * cw;
 #pragma unroll
               for (int c = 0; c < 16; ++c)   // columns turned by the row: no bank conflicts
-                to[(cc + c + r) & (cw - 1)] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
+                to[(cc + c + r) & (cw - 1)] = has ? ov[c] * a : 0.f;
             }
             __syncwarp();
           }
           ok = half_sync();
+#pragma unroll 1
           for (int e = tl; e < live * cw / 2 && ok; e += 128) {
             const int rr = e / (cw / 2), c = (e % (cw / 2)) * 2;
             float v0 = 0.f, v1 = 0.f;
@@ -841,12 +853,11 @@ __global__ void __launch_bounds__(kA8Threads, 1) attn8_kernel(const __grid_const
               v0 += from[(c + rr) & (cw - 1)];
               v1 += from[(c + 1 + rr) & (cw - 1)];
             }
-            const int col = half * (HD / 2) + c0 + c;
             if (whole)
-              *reinterpret_cast<uint32_t *>(o + (static_cast<size_t>(rr / G) * p.Hq + rr % G) * HD + col) =
+              *reinterpret_cast<uint32_t *>(o + (static_cast<size_t>(rr / G) * p.Hq + rr % G) * HD + c0 + c) =
                   pack_bf16x2(v0, v1);
             else
-              *reinterpret_cast<float2 *>(p.part_o + (row0 + rr) * HD + col) = make_float2(v0, v1);
+              *reinterpret_cast<float2 *>(p.part_o + (row0 + rr) * HD + c0 + c) = make_float2(v0, v1);
           }
           ok = ok && half_sync();
         }
@@ -948,7 +959,7 @@ static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
   const int R = (p.Hq / p.Hkv) * p.m;
   cudaError_t e = configure_attn8<HD, RHO>();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn8_kernel<HD, RHO>, dim3(p.grid), dim3(kA8Threads), A8Cfg<HD, RHO>::SMEM, s, p);
+  e = launch_pdl(attn8_kernel<HD, RHO>, dim3(p.grid), dim3(A8Cfg<HD, RHO>::THREADS), A8Cfg<HD, RHO>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn8_merge_kernel<HD>, dim3(p.nb * p.Hkv, (R + kMerge8Warps - 1) / kMerge8Warps),
                     dim3(kMerge8Warps * 32), 0, s, p);

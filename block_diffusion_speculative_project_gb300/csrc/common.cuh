@@ -331,6 +331,19 @@ __device__ __forceinline__ void tc_mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_t
       : "memory");
 }
 
+// tc_mma_bf16_tmem_a that leaves the lanes of D whose bit is set in the four words as they are.
+__device__ __forceinline__ void tc_mma_bf16_tmem_a_lanes(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                         uint32_t idesc, const uint32_t (&off)[4],
+                                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]),
+      "r"(off[3])
+      : "memory");
+}
+
 // Shared-memory matrix descriptor for a K-major operand tile written by TMA with
 // 128-byte swizzle: rows of 128 bytes (64 bf16), 8-row atoms 1024 bytes apart.
 // Bits: [0,14) start>>4, [16,30) LBO>>4 (unused here), [32,46) SBO>>4,
