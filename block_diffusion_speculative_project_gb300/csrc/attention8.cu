@@ -112,71 +112,71 @@ __device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
 
 // ---------------------------------------------------------------- tensor-core kernel
 
-// RHO copies of the query rows fill the 128 lanes of the MMA (rows padded to 128 / RHO); each copy
-// takes units of its own, so that a softmax thread works on all 64 keys of a unit and every SM
-// quarter's warps share the work of few rows. PV leaves the other copies' lanes of O as they are.
-//   RHO = 4   groups 0 .. 3 of one warp: the lanes of copy g; a pair of units (see below) goes to
-//             the groups 0, 1 or 2, 3 in turn
-//   RHO = 2   groups 0, 1 of two warps
-//   RHO = 1   groups 0, 1 of four warps, with an O each (there is no second copy), for which one
-//             pair of S and of P buffers has to do
-template <int HD, int RHO>
+// Both products read the cache's bytes as they are, with the keys and the head's columns as the 128
+// rows of the MMA and the query rows (RP of them, padded) as its columns:
+//   S^T [128 keys][2 RP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of two e4m3 terms
+//   O^T [hd][3 RP]       += V^T [hd x keys, e4m3] P^T, each probability as the sum of three e5m2 terms
+// so a term costs columns of one pass and not a pass of its own over K or V, nothing is widened,
+// and a softmax thread (a TMEM lane) is one key, whose scale is a number of the thread.
+// Two e4m3 terms (4 bits each) hold bf16's 8 bits; three e5m2 terms keep 9 bits of a probability over
+// f16's range, all that is 2^-24 of the largest or more.
+//
+// Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
+template <int HD, int RP>
 struct A8Cfg {
-  static constexpr int ROWS = 128 / RHO;             // padded query rows
-  static constexpr int NG = RHO == 4 ? 4 : 2;        // softmax groups
-  static constexpr int NO = RHO == 1 ? 2 : 1;        // O accumulators
-  static constexpr int WPG = RHO == 4 ? 1 : RHO == 2 ? 2 : 4;  // warps of a group
-  static constexpr int DEEP = RHO == 1 ? 1 : 2;      // buffers of a pair's S and P
-  static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
-  static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
+  static constexpr int NRG = RP >= 32 ? 2 : 1;       // groups of four softmax warps, ROWS query rows each
+  static constexpr int ROWS = RP / NRG;
+  static constexpr int NSW = 4 * NRG;
+  static constexpr bool STACKED = 3 * RP <= 256;     // P's terms side by side (an MMA has at most 256 columns)
+  static constexpr int SB = RP <= 64 ? 2 : 1;        // buffers of S, and of O
+  static constexpr int OB = RP <= 32 ? 2 : 1;
+  static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values)
   static constexpr int PAIR8 = 2 * UNIT8;
-  // ring of pairs of units in 8 bits, keys then values, as much as shared memory holds
-  static constexpr int NS = (RHO == 1 ? 3 : 4) * (128 / HD);
-  static constexpr int ATOM16 = kUnit * 128;
-  static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
-  static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
-  static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of the exchange of O between copies
-  static constexpr int OFF_8 = 4 * TILE16;           // two pairs of units' V in f16, then the ring
-  static constexpr int OFF_Q = OFF_8 + NS * 2 * PAIR8;
-  static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
-  static constexpr int OFF_ML = OFF_STG + STAGE * 4;      // [NO][128 lanes] (maximum, sum)
-  static constexpr int OFF_SC = OFF_ML + NO * 128 * 8;    // [2 chunks][32 units] scales
+  // rings of pairs, one of keys and one of values, as much as shared memory holds
+  static constexpr int NS = (RP <= 32 ? 5 : RP == 64 ? 4 : 2) * (128 / HD);
+  static constexpr int PBLOCK = 128 * 128;           // P^T: 128 keys of 128 of its columns
+  static constexpr int P_BYTES = (3 * RP + 127) / 128 * PBLOCK;
+  static constexpr int OFF_V8 = NS * PAIR8;
+  static constexpr int OFF_P = 2 * NS * PAIR8;       // two buffers
+  static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;  // 2 RP rows of hd bytes
+  static constexpr int OFF_TAB = OFF_Q + 2 * RP * HD;     // [RP/2] factor and -reference of two rows
+  static constexpr int OFF_LIM = OFF_TAB + RP * 8;        // [RP] keys that a row sees
+  static constexpr int OFF_RED = OFF_LIM + RP * 4;        // [4][RP] a quarter's maxima, sums
+  static constexpr int OFF_ROW = OFF_RED + 4 * RP * 4;    // [RP] a number for every row
+  static constexpr int OFF_SC = OFF_ROW + RP * 4;         // [2 chunks][32 units] scales
   static constexpr int OFF_BAR = OFF_SC + 64 * 16;
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
   static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t S_COL = 0;                     // S of pair pj in buffer pj % DEEP: 64 columns a unit
-  static constexpr uint32_t O_COL = DEEP * 128;            // O: hd columns each
-  static constexpr uint32_t Q_COL = O_COL + NO * HD;       // queries, two e4m3 terms: hd / 4 columns each
-  static constexpr uint32_t P_COL = Q_COL + HD / 2;        // P: 32 columns a unit; a buffer pj % 2 for the
-                                                           // pair (its units lie in different lanes), or,
-                                                           // RHO = 1, one for either unit
-  static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
-  // Warps: producer, S issuer, PV issuer, one that only helps at the start, softmax (warp w reads
-  // TMEM lanes of quarter w % 4), then the converters of V.
-  static constexpr int W_CONV = 4 + 4 * NO;
-  static constexpr int THREADS = (W_CONV + 4) * 32;
+  static constexpr int OCOLS = STACKED ? 3 * RP : RP;
+  static constexpr uint32_t S_COL = 0;               // S^T of pair pj in buffer pj % SB: 2 RP columns
+  static constexpr uint32_t O_COL = SB * 2 * RP;     // O^T of segment seg in buffer seg % OB
+  static_assert(O_COL + OB * OCOLS <= TMEM_COLS, "tensor memory");
+  static constexpr int THREADS = (4 + NSW) * 32;
 };
 constexpr int kSeqCache = 128;
 constexpr int kDrainSpin = 1 << 22;
-// P is 2^(x - m_run + kPBase), m_run the maximum at the last rescale: O is rescaled only when the
-// maximum has grown by more than 2^kRescale, so P stays at most 2^15 in f16, and what is 2^-21 of
-// the largest still has all 11 bits (2^-31 one bit).
-constexpr float kPBase = 7.f, kRescale = 8.f;
+// P is 2^(x - reference + kPBase) for x in log2 units; the reference moves (and O with it) only when a
+// key exceeds it by more than kRescale: P stays at most 2^15, which e5m2 and f16 hold.
+constexpr float kPBase = 12.f, kRescale = 3.f;
 
-// A segment's units are taken in pairs: one S product of 128 keys, then a softmax for each unit by a
-// group of its own, then both PV. What bounds the kernel are the steps from one role to the next
-// (with every copy, product and exponential left out it still took 0.7 of its time, when each
-// warp went through every unit), so they are paid for two units at once, and a softmax warp goes
-// through every second or fourth unit only. Half a pair at the end of a segment of an odd number of
-// units is signalled by its group without work.
-constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWAid = 3, kWSoft = 4, kNumConv = 4;
+// Warps: producer of values and scales, S issuer, PV issuer, producer of keys, softmax (warp w reads
+// TMEM lanes of quarter w % 4; rows of group (w - 4) / 4).
+constexpr int kWValues = 0, kWS = 1, kWPV = 2, kWKeys = 3, kWSoft = 4;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// One of the warp's threads, the same one every time; the branch on it leaves the code around it
+// warp-uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
 }
 
 // A unit inside a CTA's range: sequence i, kv head g, unit of `units`.
@@ -197,7 +197,7 @@ __device__ __forceinline__ void pos_seq(Pos8 &w, const Attn8Params &p, const int
     if (w.units > 0) return;
   }
 }
-// To the pair after this one.
+// To the pair (sequence, kv head) after this one.
 __device__ __forceinline__ void pos_next_pair(Pos8 &w, const Attn8Params &p, const int2 *sseq) {
   w.unit = 0;
   if (++w.g == p.Hkv) {
@@ -207,59 +207,109 @@ __device__ __forceinline__ void pos_next_pair(Pos8 &w, const Attn8Params &p, con
   }
 }
 
-// 8 e4m3 values to f16 (exact).
-__device__ __forceinline__ uint4 widen8(uint2 u) {
-  uint4 h;
-  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
-      "mov.b32 {a, b}, %4;\n\t"
-      "mov.b32 {c, d}, %5;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
-      : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
-      : "r"(u.x), "r"(u.y));
-  return h;
+// The blocks of a CTA's units in order, for a producer warp: lane l looks up unit 32 c + l of chunk
+// c, a chunk ahead.
+struct Blocks8 {
+  Pos8 a;
+  int x, now, next;
+  __device__ __forceinline__ void init(const Pos8 &w, int lane) {
+    a = w;
+    a.unit += lane;
+    x = lane;
+  }
+  __device__ __forceinline__ int look_up(const Attn8Params &p, const int2 *sseq, int nunits) {
+    int b = 0;
+    if (x < nunits) {
+#pragma unroll 1
+      while (a.unit >= a.units) {
+        const int over = a.unit - a.units;
+        pos_next_pair(a, p, sseq);
+        a.unit = over;
+      }
+      b = static_cast<int>(block_of(p, a.i, a.g, a.unit));
+    }
+    a.unit += 32;
+    x += 32;
+    return b;
+  }
+  // now, next: the blocks of the first two chunks, then of the following ones
+  __device__ __forceinline__ void start(const Attn8Params &p, const int2 *sseq, int nunits) {
+    now = look_up(p, sseq, nunits);
+    next = look_up(p, sseq, nunits);
+  }
+  __device__ __forceinline__ void step(const Attn8Params &p, const int2 *sseq, int nunits) {
+    now = next;
+    next = look_up(p, sseq, nunits);
+  }
+};
+
+// Sums v[0 .. N) over the warp's lanes; lane l gets the sum of element l % N (N <= 32), in a fixed order.
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n >>= 1) {
+    o = n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool up = lane & o;
+      const float send = up ? v[i] : v[i + n];
+      v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float s = v[0];
+#pragma unroll
+  for (int x = N; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+  return s;
 }
 
-// One of the warp's threads, the same one every time; the branch on it leaves the code around it
-// warp-uniform.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
+// Four probabilities (two f16 pairs, non-negative) as three e5m2 terms each, four to a word. e5m2 is
+// f16's upper byte: the first term cuts (the rest is exact), the other two round.
+__device__ __forceinline__ void split4(uint32_t p01, uint32_t p23, uint32_t &a, uint32_t &b, uint32_t &c) {
+  a = __byte_perm(p01, p23, 0x7531);
+  auto rest = [](uint32_t x, uint32_t y) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&d);
+  };
+  auto round = [](uint32_t x) {
+    return static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw *>(&x),
+                                                            __NV_SATFINITE, __NV_E5M2));
+  };
+  const uint32_t r01 = rest(p01, p01 & 0xFF00FF00u), r23 = rest(p23, p23 & 0xFF00FF00u);
+  const uint32_t b01 = round(r01), b23 = round(r23);
+  b = b01 | (b23 << 16);
+  c = round(rest(r01, __byte_perm(b01, 0, 0x1404))) | (round(rest(r23, __byte_perm(b23, 0, 0x1404))) << 16);
 }
 
-template <int HD, int RHO>
-__global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
-  using C = A8Cfg<HD, RHO>;
-  constexpr int ROWS = C::ROWS;
+template <int HD, int RP>
+__global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
+  using C = A8Cfg<HD, RP>;
+  constexpr int ROWS = C::ROWS, NSW = C::NSW, T = NSW * 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint8_t *sV16 = smem, *s8 = smem + C::OFF_8, *sQ = smem + C::OFF_Q;
-  float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+  uint8_t *sK8 = smem, *sV8 = smem + C::OFF_V8, *sP = smem + C::OFF_P, *sQ = smem + C::OFF_Q;
+  float4 *tab = reinterpret_cast<float4 *>(smem + C::OFF_TAB);
+  int *slim = reinterpret_cast<int *>(smem + C::OFF_LIM);
+  float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
+  float *srow = reinterpret_cast<float *>(smem + C::OFF_ROW);
   float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
-  uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-  uint64_t *kv8_empty = kv8_full + C::NS;
-  uint64_t *v16_full = kv8_empty + C::NS;   // [2] V of pair pj in f16, buffer pj % 2
-  uint64_t *p_full = v16_full + 2;          // [2] P of pair pj
-  uint64_t *pv_done = p_full + 2;           // [2] PV of pair pj complete: P and V16 have been read
-  uint64_t *s_full = pv_done + 2;           // [2] S of pair pj complete, buffer pj % DEEP
-  uint64_t *s_empty = s_full + 2;           // [2] and read by both groups
-  uint64_t *sc_full = s_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
+  uint64_t *k8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [NS] keys of a pair have landed
+  uint64_t *k8_empty = k8_full + C::NS;
+  uint64_t *v8_full = k8_empty + C::NS;
+  uint64_t *v8_empty = v8_full + C::NS;
+  uint64_t *s_full = v8_empty + C::NS;      // [2] S^T of pair pj complete (in buffer pj % SB)
+  uint64_t *s_empty = s_full + 2;           // [2] and read
+  uint64_t *p_full = s_empty + 2;           // [2] P^T of pair pj written
+  uint64_t *pv_done = p_full + 2;           // [2] O^T += of pair pj complete
+  uint64_t *sc_full = pv_done + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
   uint64_t *sc_empty = sc_full + 2;         // [2]
-  uint64_t *half_bar = sc_empty + 2;        // [2] four softmax warps among themselves
-  uint64_t *mma_done = half_bar + 2;        // [2]
-  uint64_t *q8_full = mma_done + 2;         // a segment's query rows have landed
-  uint64_t *q8_empty = q8_full + 1;
-  uint64_t *q_full = q8_empty + 1;          // and are in tensor memory
-  uint64_t *q_empty = q_full + 1;
-  uint64_t *seg_bar = q_empty + 1;          // every softmax warp: (maximum, sum) of a segment written
-  uint64_t *o_free = seg_bar + 1;           // O and ml read
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
+  uint64_t *o_free = sc_empty + 2;          // [2] O^T of segment seg read (buffer seg % OB)
+  uint64_t *mma_done = o_free + 2;          // [2]
+  uint64_t *q_full = mma_done + 2;          // a segment's query terms are in shared memory
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 18 + 6) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((4 * C::NS + 17) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -268,27 +318,27 @@ __global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(&kv8_full[s], 1);
-      mbar_init(&kv8_empty[s], kNumConv + 1);
+      mbar_init(&k8_full[s], 1);
+      mbar_init(&k8_empty[s], 1);
+      mbar_init(&v8_full[s], 1);
+      mbar_init(&v8_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&v16_full[b], kNumConv);
-      mbar_init(&p_full[b], 2 * C::WPG);
-      mbar_init(&pv_done[b], 1);
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_empty[b], 2 * C::WPG);
+      mbar_init(&s_empty[b], NSW);
+      mbar_init(&p_full[b], NSW);
+      mbar_init(&pv_done[b], 1);
       mbar_init(&sc_full[b], 1);
-      mbar_init(&sc_empty[b], 4 * C::NO);
-      mbar_init(&half_bar[b], 4);
+      mbar_init(&sc_empty[b], NSW);
+      mbar_init(&o_free[b], NSW);
       mbar_init(&mma_done[b], 1);
     }
-    mbar_init(q8_full, 1);
-    mbar_init(q8_empty, 4 * C::NO);
-    mbar_init(q_full, 4);
-    mbar_init(q_empty, 1);
-    mbar_init(seg_bar, 4 * C::NO);
-    mbar_init(o_free, 4 * C::NO);
+    mbar_init(q_full, NSW);
     fence_mbar_init();
+  }
+  if (warp == kWKeys && lane == 0) {
+    tma_prefetch_desc(&p.tmK);
+    tma_prefetch_desc(&p.tmV);
   }
   if (warp == kWS) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -296,9 +346,9 @@ __global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const
   }
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
-  if (warp == kWProd) {
+  if (warp == kWValues) {
     find_range(p, blockIdx.x, lane, sched);
-  } else if (warp == kWAid) {
+  } else if (warp == kWKeys) {
     for (int i = lane; i < p.nb && i < kSeqCache; i += 32) {
       const Seq8 s = seq8(p, i);
       sseq[i] = make_int2(s.n, s.ctx);
@@ -325,106 +375,86 @@ __global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const
   // of units u, u + 1 of the segment. A wait that runs out ends the role (ok = false).
   if (nunits == 0) {
     // nothing to do
-  } else if (warp == kWProd) {
-    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each (the keys
-    // arrive swizzled, as the tensor cores read them), a query row hd bf16. Lane l looks up the block of unit 32 c + l of the CTA's range two chunks c
-    // ahead and its scales one chunk ahead, so the copies wait for neither.
+  } else if (warp == kWKeys || warp == kWValues) {
+    // ---------------- producers of keys and of values: a unit's are 64 rows of hd bytes, which arrive
+    // swizzled as the tensor cores read them. The warp of the values also writes the scales of 32
+    // units at a time.
+    const bool keys = warp == kWKeys;
+    const CUtensorMap *map = keys ? &p.tmK : &p.tmV;
+    uint8_t *ring = keys ? sK8 : sV8;
+    uint64_t *full = keys ? k8_full : v8_full, *empty = keys ? k8_empty : v8_empty;
     const uint64_t pol = policy_evict_first();
     bool ok = !p.stall;
-    int pairs = 0, segs = 0;
-    Pos8 a = w;
-    int x = lane;
-    a.unit += lane;
-    auto look_up = [&]() {
-      if (x >= nunits) return 0;
-      while (a.unit >= a.units) {
-        const int over = a.unit - a.units;
-        pos_next_pair(a, p, sseq);
-        a.unit = over;
-      }
-      const int b = static_cast<int>(block_of(p, a.i, a.g, a.unit));
-      a.unit += 32;
-      return b;
-    };
-    int blk = look_up();
-    x += 32;
-    int blk1 = look_up();
-    float ks = lane < nunits ? p.ks[blk] : 0.f, vs = lane < nunits ? p.vs[blk] : 0.f;
-    int cnt_left = 0, slot = 0, st = 0, ph = 0;
-    bool published = false;
+    Blocks8 bl;
+    bl.init(w, lane);
+    bl.start(p, sseq, nunits);
+    float ks = 0.f, vs = 0.f;
+    if (!keys && lane < nunits) {
+      ks = p.ks[bl.now];
+      vs = p.vs[bl.now];
+    }
+    int pj = 0, st = 0, ph = 1;
+    int chunk = keys ? 1 << 30 : 0;      // chunk whose scales are to be written next
 #pragma unroll 1
-    for (int j = 0; j < nunits && ok; ++j) {
-      const int k = j & 31, c = j >> 5;
-      if (cnt_left == 0) {  // a segment begins: its query rows
-        if (j > 0) pos_next_pair(w, p, sseq);
-        cnt_left = min(w.units - w.unit, nunits - j);
-        ok = segs == 0 || mbar_wait_warp(q8_empty, (segs - 1) & 1, p.max_spin);
+    for (int j0 = 0; j0 < nunits && ok;) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+#pragma unroll 1
+      for (int u = 0; u < cnt; u += 2, ++pj) {
+        const int j = j0 + u, k = j & 31;
+        const bool two = u + 1 < cnt;
+        const int b0 = __shfl_sync(0xffffffffu, bl.now, k);
+        const int bn = __shfl_sync(0xffffffffu, bl.next, 0);
+        const int b1 = k == 31 ? bn : __shfl_sync(0xffffffffu, bl.now, (k + 1) & 31);
+        ok = pj < C::NS || mbar_wait_warp(&empty[st], ph, p.max_spin);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
+        if (elect_one()) {
+          uint8_t *dst = ring + st * C::PAIR8;
+          mbar_arrive_expect_tx(&full[st], (two ? 2 : 1) * C::UNIT8);
+          tma_load_2d(dst, map, &full[st], 0, b0 * kUnit, pol);
+          if (two) tma_load_2d(dst + C::UNIT8, map, &full[st], 0, b1 * kUnit, pol);
+        }
         __syncwarp();
-#pragma unroll 1
-        for (int r = lane; r < w.n * G; r += 32)
-          bulk_load(sQ + r * C::QPITCH,
-                    p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
-                    pol);
-        ++segs;
-        slot = 0;
-      }
-      --cnt_left;
-      const long long b = __shfl_sync(0xffffffffu, blk, k);
-      if (slot == 0) ok = pairs < C::NS || mbar_wait_warp(&kv8_empty[st], ph ^ 1, p.max_spin);
-      if (!ok) break;
-      if (elect_one()) {
-        uint8_t *dst = s8 + st * 2 * C::PAIR8;
-        if (slot == 0) mbar_arrive_expect_tx(&kv8_full[st], (cnt_left > 0 ? 2 : 1) * C::PAIR8);
-        tma_load_2d(dst + slot * C::UNIT8, &p.tmK, &kv8_full[st], 0, static_cast<int>(b) * kUnit, pol);
-        bulk_load(dst + C::PAIR8 + slot * C::UNIT8, p.v8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
-      }
-      __syncwarp();
-      if (slot == 0) ++pairs;
-      if (slot == 1 || cnt_left == 0) {  // the pair is complete
-        slot = 0;
         if (++st == C::NS) {
           st = 0;
           ph ^= 1;
         }
-      } else {
-        slot = 1;
-      }
-      // The chunk's scales, after its first copies are under way, and before any wait for a unit
-      // of the chunk: a copy waits for the pair NS >= 3 before its own, the next segment's queries
-      // for the units of the segment before last.
-      published = published && k != 0;
-      if (!published && (k == 2 || j == nunits - 1 || cnt_left == 0)) {
-        published = true;
-        ok = c < 2 || mbar_wait_warp(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
+        // The scales of a chunk, once a first pair of it is under way (of the first chunk: two pairs,
+        // whose copies wait for nothing), and before any wait for a unit that needs them; first the
+        // chunk of unit j, then that of unit j + 1 where the next chunk begins with it.
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const bool due = x == 0 ? chunk == (j >> 5) && (chunk > 0 || pj == 1 || u + 2 >= cnt || k >= 30)
+                                  : k == 31 && two && chunk == (j >> 5) + 1;
+          if (due) {
+            const int b = chunk & 1;
+            ok = chunk < 2 || mbar_wait_warp(&sc_empty[b], ((chunk >> 1) - 1) & 1, p.max_spin);
+            if (!ok) break;
+            const bool zero = vs == 0.f;  // a block of zeros: its bytes do not count
+            sscale[b * 32 + lane] =
+                make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 1.f : 0.f);
+            __syncwarp();
+            mbar_arrive_if(&sc_full[b], lane == 0);
+            ++chunk;
+            const bool more = chunk * 32 + lane < nunits;
+            ks = more ? p.ks[bl.next] : 0.f;
+            vs = more ? p.vs[bl.next] : 0.f;
+          }
+          if (x == 0 && (k == 31 || (k == 30 && two))) bl.step(p, sseq, nunits);  // the chunk ends here
+        }
         if (!ok) break;
-        const bool zero = vs == 0.f;  // a block of zeros: P must not see the scale
-        sscale[(c & 1) * 32 + lane] = make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 0.f : 1.f);
-        __syncwarp();
-        mbar_arrive_if(&sc_full[c & 1], lane == 0);
       }
-      if (k == 31) {
-        blk = blk1;
-        x += 32;
-        const bool more = x - 32 < nunits;
-        ks = more ? p.ks[blk] : 0.f;
-        vs = more ? p.vs[blk] : 0.f;
-        blk1 = look_up();
-      }
+      j0 += cnt;
+      if (ok && j0 < nunits) pos_next_pair(w, p, sseq);
     }
     if (!ok && !p.stall && lane == 0) flag_status(p.status, kStatusTimeout);
     // every issued copy must land before the CTA may exit (bounded)
 #pragma unroll 1
-    for (int x = max(0, pairs - C::NS); x < pairs; ++x)
-      mbar_wait_warp(&kv8_full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
-    if (segs > 0) mbar_wait_warp(q8_full, (segs - 1) & 1, kDrainSpin);
+    for (int x = max(0, pj - C::NS); x < pj; ++x) mbar_wait_warp(&full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
   } else if (warp == kWS) {
-    // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two e4m3
-    // terms one after the other from tensor memory
-    constexpr uint32_t id_s = idesc_f32_format0(128, kUnit);
-    const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(s8)) : sw64_kmajor_desc(smem_u32(s8));
-    constexpr uint32_t id_s2 = idesc_f32_format0(128, 2 * kUnit);
+    // ---------------- S issuer: S^T = K Q^T
+    constexpr uint32_t id = idesc_8bit_f32(128, 2 * RP);
+    const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(sK8)) : sw64_kmajor_desc(smem_u32(sK8));
+    const uint64_t qd = HD == 128 ? sw128_kmajor_desc(smem_u32(sQ)) : sw64_kmajor_desc(smem_u32(sQ));
     int st = 0, ph = 0, pj = 0;
     bool ok = true;
 #pragma unroll 1
@@ -433,20 +463,17 @@ __global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const
       ok = mbar_wait_warp(q_full, seg & 1, p.max_spin);
 #pragma unroll 1
       for (int u = 0; u < cnt && ok; u += 2, ++pj) {
-        ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
-        const int b = pj % C::DEEP;
-        ok = ok && (pj < C::DEEP || mbar_wait_warp(&s_empty[b], (pj / C::DEEP - 1) & 1, p.max_spin));
+        const int pe = pj - C::SB;
+        ok = mbar_wait_warp(&k8_full[st], ph, p.max_spin) &&
+             (pe < 0 || mbar_wait_warp(&s_empty[pe & 1], (pe >> 1) & 1, p.max_spin));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t kd = kd0 + static_cast<uint64_t>((st * 2 * C::PAIR8) >> 4);
-        const uint32_t id = u + 1 < cnt ? id_s2 : id_s;
+        const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::PAIR8) >> 4);
+        const uint32_t d = tmem + C::S_COL + (pj % C::SB) * 2 * RP;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 2 * HD / 32; ++kk)
-            tc_mma_e4m3_tmem_a(tmem + C::S_COL + b * 128, tmem + C::Q_COL + kk * 8,
-                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id, kk > 0 ? 1u : 0u);
-          tc_commit(&s_full[b]);
-          if (u + 2 >= cnt) tc_commit(q_empty);
+          for (int kk = 0; kk < HD / 32; ++kk) tc_mma_8bit(d, kd + kk * 2, qd + kk * 2, id, kk > 0 ? 1u : 0u);
+          tc_commit(&s_full[pj & 1]);
         }
         __syncwarp();
         if (++st == C::NS) {
@@ -463,47 +490,48 @@ __global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const
     __syncwarp();
     mbar_wait_warp(&mma_done[0], 0, kDrainSpin);
   } else if (warp == kWPV) {
-    // ---------------- PV issuer: O += P V for both units of a pair; a segment's first unit of each
-    // group starts the accumulator, after the previous segment's O was read
-    constexpr uint32_t id_pv = idesc_f32_format0(128, HD) | kIdescBMajorMN;
-    const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
+    // ---------------- PV issuer: O^T += V^T P^T; a segment's first pair starts the accumulator, after
+    // its buffer's previous segment was read
+    constexpr uint32_t id = idesc_8bit_f32(128, C::OCOLS) | kIdescBE5M2 | kIdescAMajorMN | kIdescBMajorMN;
+    // hd = 64: the second half of the MMA's rows reads the next unit's values and is not used
+    const uint64_t vd0 = HD == 128 ? sw128_mnmajor_desc(smem_u32(sV8), C::UNIT8)
+                                   : sw64_mnmajor_desc(smem_u32(sV8), C::UNIT8);
+    const uint64_t pd0 = sw128_mnmajor_desc(smem_u32(sP), C::PBLOCK);
+    int st = 0, ph = 0, pj = 0;
     bool ok = true;
-    int pj = 0;
 #pragma unroll 1
     for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
       const int cnt = min(w.units - w.unit, nunits - j0);
-      if (seg > 0) ok = mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin);
+      const int se = seg - C::OB;
+      ok = se < 0 || mbar_wait_warp(&o_free[se % C::OB], (se / C::OB) & 1, p.max_spin);
+      const uint32_t d = tmem + C::O_COL + (seg % C::OB) * C::OCOLS;
 #pragma unroll 1
       for (int u = 0; u < cnt && ok; u += 2, ++pj) {
         const int b = pj & 1;
-        ok = mbar_wait_warp(&v16_full[b], (pj >> 1) & 1, p.max_spin);
-        ok = ok && mbar_wait_warp(&p_full[b], (pj >> 1) & 1, p.max_spin);
+        ok = mbar_wait_warp(&v8_full[st], ph, p.max_spin) && mbar_wait_warp(&p_full[b], (pj >> 1) & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
+        const uint64_t vd = vd0 + static_cast<uint64_t>((st * C::PAIR8) >> 4);
+        const uint64_t pd = pd0 + static_cast<uint64_t>((b * C::P_BYTES) >> 4);
+        const uint32_t add = u > 0 ? 1u : 0u;
         if (elect_one()) {
-          const uint32_t add = u >= C::NG ? 1u : 0u;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (u + x >= cnt) break;
-            const uint64_t vd = vd0 + static_cast<uint64_t>(((b * 2 + x) * C::TILE16) >> 4);
-            const int g = RHO == 4 ? 2 * b + x : x;  // the unit's group
-            uint32_t off[4];
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= 2 && u + 1 >= cnt) break;   // one unit alone
 #pragma unroll
-            for (int y = 0; y < 4; ++y) off[y] = RHO == 1 || y * 32 / ROWS == g ? 0u : 0xFFFFFFFFu;
-#pragma unroll
-            for (int kk = 0; kk < kUnit / 16; ++kk) {
-              const uint64_t d = vd + static_cast<uint64_t>((kk * 16 * 128) >> 4);
-              if (RHO == 1)
-                tc_mma_bf16_tmem_a(tmem + C::O_COL + x * HD, tmem + C::P_COL + x * 32 + kk * 8, d, id_pv,
-                                   kk > 0 ? 1u : add);
-              else
-                tc_mma_bf16_tmem_a_lanes(tmem + C::O_COL, tmem + C::P_COL + b * 32 + kk * 8, d, id_pv, off,
-                                         kk > 0 ? 1u : add);
-            }
+            for (int t = 0; t < (C::STACKED ? 1 : 3); ++t)
+              tc_mma_8bit(d, vd + static_cast<uint64_t>((kk * 32 * HD) >> 4),
+                          pd + static_cast<uint64_t>((t * C::PBLOCK + kk * 32 * 128) >> 4), id,
+                          (kk > 0 || t > 0) ? 1u : add);
           }
           tc_commit(&pv_done[b]);
+          tc_commit(&v8_empty[st]);
         }
         __syncwarp();
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
+        }
       }
       j0 += cnt;
       if (j0 < nunits) pos_next_pair(w, p, sseq);
@@ -512,363 +540,327 @@ __global__ void __launch_bounds__(A8Cfg<HD, RHO>::THREADS, 1) attn8_kernel(const
     if (elect_one()) tc_commit(&mma_done[1]);
     __syncwarp();
     mbar_wait_warp(&mma_done[1], 0, kDrainSpin);
-  } else if (warp >= C::W_CONV) {
-    // ---------------- converters: V from e4m3 to f16, in the layout of a 128-byte-swizzled copy (rows
-    // of 64 values, 16-byte chunk c of row r at c ^ (r & 7))
-    constexpr int CPR = HD / 8;                        // 8-value chunks of a row: 8 bytes to 16
-    constexpr int RPI = kNumConv * 32 / CPR;           // rows per iteration: 8 or 16
-    constexpr int PER = kUnit / RPI;                   // chunks per thread
-    static_assert(RPI % 8 == 0, "a thread's chunks all lie at the same place of their rows");
-    const int t = (warp - C::W_CONV) * 32 + lane;
-    const int cc = t % CPR, r0 = t / CPR;
-    uint8_t *out = sV16 + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
-    const uint8_t *src0 = s8 + C::PAIR8 + t * 8;
-    bool ok = true;
-    int st = 0, ph = 0, pj = 0;
-#pragma unroll 1
-    for (int j0 = 0; j0 < nunits && ok;) {
-      const int cnt = min(w.units - w.unit, nunits - j0);
-      int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
-#pragma unroll 1
-      for (int x = 0; x < cnt; ++x, keys -= kUnit) {
-        const int b = pj & 1, slot = x & 1;
-        if (slot == 0) {
-          ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
-          ok = ok && (pj < 2 || mbar_wait_warp(&pv_done[b], ((pj >> 1) - 1) & 1, p.max_spin));
-          if (!ok) break;
-        }
-        const uint8_t *src = src0 + st * 2 * C::PAIR8 + slot * C::UNIT8;
-        uint8_t *dst = out + (b * 2 + slot) * C::TILE16;
-        if (keys < kUnit) {
-          // rows beyond the last key may hold anything (even NaN); P is 0 there
-#pragma unroll 2
-          for (int e = 0; e < PER; ++e) {
-            uint4 h = make_uint4(0, 0, 0, 0);
-            if (r0 + e * RPI < keys) h = widen8(*reinterpret_cast<const uint2 *>(src + e * RPI * HD));
-            *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = h;
-          }
-        } else {
-          uint2 u[PER];
-#pragma unroll
-          for (int e = 0; e < PER; ++e) u[e] = *reinterpret_cast<const uint2 *>(src + e * RPI * HD);
-#pragma unroll
-          for (int e = 0; e < PER; ++e) *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = widen8(u[e]);
-        }
-        if (slot == 1 || x == cnt - 1) {  // the pair is complete
-          fence_proxy_async_smem();
-          __syncwarp();
-          mbar_arrive_if(&v16_full[b], lane == 0);
-          mbar_arrive_if(&kv8_empty[st], lane == 0);
-          ++pj;
-          if (++st == C::NS) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-      }
-      j0 += cnt;
-      if (j0 < nunits) pos_next_pair(w, p, sseq);
-    }
-    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
-  } else if (warp >= kWSoft) {
-    // ---------------- softmax: thread = TMEM lane; lane l holds query row l % ROWS, copy l / ROWS
-    const int half = (warp - kWSoft) >> 2;   // RHO = 1: the group, and its O
-    const int tl = (warp & 3) * 32 + lane;
-    const int r = tl % ROWS, copy = tl / ROWS;
-    const int grp = RHO == 1 ? half : copy, slot = grp & 1;
-    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t o_mine = trow + C::O_COL + (RHO == 1 ? half * HD : 0);
-    const int jq = r / G;               // row r: query row jq of query head g * G + r % G
+  } else {
+    // ---------------- softmax: a thread is key `key` of the pair, for the rows [r0, r0 + ROWS). Every
+    // softmax warp goes through the same barriers, also when a wait has run out: `fail` is told
+    // to all of them at the next one, and they leave together.
+    const int tid = threadIdx.x - kWSoft * 32;
+    const int quarter = warp & 3, rg = tid >> 7, r0 = rg * ROWS;
+    const int key = quarter * 32 + lane, slot = key >> 6;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-    uint32_t half_phase = 0;
-    // Barrier of four warps, bounded like every other wait.
-    auto half_sync = [&]() {
-      __syncwarp();
-      mbar_arrive_if(&half_bar[half], lane == 0);
-      const bool done = mbar_wait_warp(&half_bar[half], half_phase, p.max_spin);
-      half_phase ^= 1;
-      return done;
-    };
-    // The query row of segment `seg` (n rows a sequence), scaled by a power of two so that its
-    // largest value lies in [2^7, 2^8), to tensor memory as the sum of two e4m3 terms: 4 bits each
-    // hold bf16's 8, exactly down to 2^-10 of the largest value, below that to 2^-18 of it.
-    // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
-    auto load_q = [&](int seg, int n) {
-      bool ok = mbar_wait_warp(q8_full, seg & 1, p.max_spin);
-      if (half == 0 && seg > 0) ok = ok && mbar_wait_warp(q_empty, (seg - 1) & 1, p.max_spin);
-      if (!ok) return -1.f;
-      const uint4 *src = reinterpret_cast<const uint4 *>(sQ + r * C::QPITCH);
-      const bool have = r < n * G;
-      float am = 0.f;
-#pragma unroll 4
-      for (int e = 0; e < HD / 8; ++e) {
-        const uint4 u = have ? src[e] : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    constexpr float kTop = kPBase + kRescale;
+    float *nref = reinterpret_cast<float *>(tab);  // -reference of row r at 4 (r / 2) + 2 + r % 2
+    bool fail = false, gone = false;
+
+    // The query rows of a segment: eight threads a row, hd/8 values each, read a segment ahead.
+    constexpr int PASS = RP * 8 / T;
+    uint4 qr[PASS][HD / 64];
+    auto fetch_q = [&](const Pos8 &a) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[f] << 16)), fabsf(__uint_as_float(x[f] & 0xFFFF0000u))));
+      for (int x = 0; x < PASS; ++x) {
+        const int r = x * (T / 8) + (tid >> 3), j = r / G;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q + ((static_cast<size_t>(a.i) * p.m + j) * p.Hq + a.g * G + r % G) * HD + (tid & 7) * (HD / 8));
+#pragma unroll
+        for (int y = 0; y < HD / 64; ++y) qr[x][y] = j < a.n ? src[y] : make_uint4(0, 0, 0, 0);
       }
-      int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
-      const bool inf = ex == 128;          // the row's outputs are NaN
-      ex = max(min(ex, 127), -100);
-      if (half == 0) {
-        const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
-        tc_fence_after();
-#pragma unroll 1
-        for (int part = 0; part < HD / 32; ++part) {
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float2 y = make_float2(__uint_as_float(x[f] << 16) * mul, __uint_as_float(x[f] & 0xFFFF0000u) * mul);
-              const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-              const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
-              const float2 af = __half22float2(*reinterpret_cast<const __half2 *>(&ar));
-              const __nv_fp8x2_storage_t b =
-                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E4M3);
-              const int d = 2 * e + f / 2;
-              hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(a) << 16) : a;
-              lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(b) << 16) : b;
-            }
-          }
-          tmem_st8_raw(trow + C::Q_COL + part * 8, hi);
-          tmem_st8_raw(trow + C::Q_COL + HD / 4 + part * 8, lo);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      __syncwarp();
-      mbar_arrive_if(q_full, lane == 0 && half == 0);
-      mbar_arrive_if(q8_empty, lane == 0);
-      return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
     };
-    float qfac = 0.f;
-    bool ok = true;
-    int chunk = -1;                      // chunk of 32 units whose scales this warp may read
-    int pj = 0, st = 0;                  // pair of units, and its stage of the ring
-    // Segment by segment: its units, then the queries of the next one (whose S can start), then the
-    // output of this one. The round before the first segment has the queries alone.
-#pragma unroll 1
-    for (int j0 = 0, seg = -1;; ++seg) {
-      const int cnt = seg < 0 ? 0 : min(w.units - w.unit, nunits - j0);
-      const int lim = p.causal ? min(w.ctx + jq + 1, w.ctx + w.n) : w.ctx + w.n;
-      // keys from the segment's first unit on that every row sees
-      const int all = (p.causal ? w.ctx + 1 : w.ctx + w.n) - w.unit * kUnit;
-      float m_run = kNoMax, l_run = 0.f;
-#pragma unroll 1
-      for (int u = slot; u < ((cnt + 1) & ~1) + slot; u += 2, ++pj) {
-        const int j = min(j0 + u, j0 + cnt - 1);
-        if (chunk < (j >> 5)) {          // the next chunk: give the one before back
-          __syncwarp();
-          if (chunk >= 0) mbar_arrive_if(&sc_empty[chunk & 1], lane == 0);
-          ++chunk;
-          ok = mbar_wait_warp(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
-          if (!ok) break;
-        }
-        const int st_now = st;
-        st = st + 1 == C::NS ? 0 : st + 1;
-        if (RHO == 4 && (pj & 1) != (grp >> 1)) continue;  // the other two groups' pair
-        const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // K scale, log2 V, 1 / V, 0 for zeros
-        const int sb = pj % C::DEEP, pb = pj & 1;
-        ok = mbar_wait_warp(&s_full[sb], (pj / C::DEEP) & 1, p.max_spin);
-        if (!ok) break;
-        tc_fence_after();
-        float sv[kUnit];
-        tmem_ld64(trow + C::S_COL + sb * 128 + slot * kUnit, sv);
-        tc_fence_before();
-        __syncwarp();
-        mbar_arrive_if(&s_empty[sb], lane == 0);
-        mbar_arrive_if(&kv8_empty[st_now], slot == 0 && r == 0);  // S complete: the keys have been read
-        // this group's P buffer is free once the PV that read it has completed
-        const int pp = RHO == 1 ? pj - 1 : pj - 2;
-        bool freed = pp < 0;
-        if (u >= cnt) {                  // half a pair
-          ok = freed || mbar_wait_warp(&pv_done[pp & 1], (pp >> 1) & 1, p.max_spin);
-          if (!ok) break;
-          mbar_arrive_if(&p_full[pb], lane == 0);
-          continue;
-        }
-        if (all - kUnit * u < kUnit) {   // some row does not see the whole unit
-          const int nv = lim - (w.unit + u) * kUnit;  // keys this row sees
+    // A row is scaled by a power of two so that its largest value lies in [2^7, 2^8), and stored as
+    // hi + lo, e4m3: bf16's 8 bits exactly down to 2^-10 of the largest value, below to 2^-18 of it.
+    auto put_q = [&](const Pos8 &a) {
 #pragma unroll
-          for (int c = 0; c < kUnit; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
+      for (int x = 0; x < PASS; ++x) {
+        const int r = x * (T / 8) + (tid >> 3), part = tid & 7;
+        float am = 0.f;
+#pragma unroll
+        for (int y = 0; y < HD / 64; ++y) {
+          const uint32_t v[4] = {qr[x][y].x, qr[x][y].y, qr[x][y].z, qr[x][y].w};
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(v[f] << 16)), fabsf(__uint_as_float(v[f] & 0xFFFF0000u))));
         }
-        const float c1 = fmaxf(qfac * sc.x, 1e-37f);
-        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int c = 4; c + 8 <= kUnit; c += 8)
+        for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;  // -127: zero or subnormal, 128: infinite
+        const bool inf = ex == 128;                                  // the row's outputs are NaN
+        ex = max(min(ex, 127), -100);
+        const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(134 - ex) << 23);
+        uint32_t hi[HD / 32], lo[HD / 32];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[c + 2 * e], sv[c + 2 * e + 1]);
-        mx[3] = max3(max3(mx[3], sv[kUnit - 4], sv[kUnit - 3]), sv[kUnit - 2], sv[kUnit - 1]);
-        const float m_new = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c1, sc.y);
-        const bool need = m_new - m_run > kRescale;
-        float alpha = 1.f;
-        if (need) {
-          alpha = ex2f(m_run - m_new);
-          m_run = m_new;
-          l_run *= alpha;
-        }
-        if (u >= C::NG && __any_sync(0xffffffffu, need && r < R)) {
-          // O *= alpha, once this group's last PV has completed: the pair NG / 2 before
-          const int pl = pj - C::NG / 2;
-          ok = mbar_wait_warp(&pv_done[pl & 1], (pl >> 1) & 1, p.max_spin);
-          if (!ok) break;
-          tc_fence_after();
-          freed = pl >= pp;
-#pragma unroll 1
-          for (int cc = 0; cc < HD / 16; ++cc) {
-            float ov[16];
-            tmem_ld16(o_mine + cc * 16, ov);
-            uint32_t x[16];
+        for (int y = 0; y < HD / 64; ++y) {
+          const uint32_t v[4] = {qr[x][y].x, qr[x][y].y, qr[x][y].z, qr[x][y].w};
 #pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(ov[c] * alpha);
-            tmem_st16_raw(o_mine + cc * 16, x);
+          for (int f = 0; f < 4; ++f) {
+            const float2 q = make_float2(__uint_as_float(v[f] << 16) * mul, __uint_as_float(v[f] & 0xFFFF0000u) * mul);
+            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+            const __nv_fp8x2_storage_t l =
+                __nv_cvt_float2_to_fp8x2(make_float2(q.x - hf.x, q.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+            const int d = y * 2 + f / 2;
+            hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(h) << 16) : h;
+            lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(l) << 16) : l;
           }
         }
-        const float c2 = sc.y - m_run + kPBase;
-        uint32_t pk[kUnit / 2];
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < kUnit; c += 2) {
-          const float2 x = fma2(make_float2(sv[c], sv[c + 1]), make_float2(c1, c1), make_float2(c2, c2));
-          const float2 e = make_float2(ex2f(x.x), ex2f(x.y));
-          ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], e);
-          const __half2 y = __floats2half2_rn(e.x, e.y);
-          pk[c / 2] = *reinterpret_cast<const uint32_t *>(&y);
+        // rows r (hi) and RP + r (lo) of the operand, 16-byte chunks swizzled as a copy would
+        uint8_t *dh = sQ + r * HD, *dl = sQ + (RP + r) * HD;
+        if constexpr (HD == 128) {
+          const int at = (part ^ (r & 7)) << 4;
+          *reinterpret_cast<uint4 *>(dh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(dl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        } else {
+          const int at = (((part >> 1) ^ ((r >> 1) & 3)) << 4) + (part & 1) * 8;
+          *reinterpret_cast<uint2 *>(dh + at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2 *>(dl + at) = make_uint2(lo[0], lo[1]);
         }
-        const float2 lt = add2(ls[0], ls[1]);
-        l_run = fmaf(lt.x + lt.y, sc.z, l_run);
-        if (sc.w == 0.f) {
-#pragma unroll
-          for (int c = 0; c < kUnit / 2; ++c) pk[c] = 0u;
+        if (part == 0) {
+          // the factor takes S to log2 units, 1/sqrt(hd) included; rows that are not there get P = 0
+          const int j = r / G;
+          const bool live = j < a.n;
+          nref[4 * (r >> 1) + (r & 1)] = live ? sl2 * __uint_as_float(static_cast<uint32_t>(ex + 120) << 23) : 0.f;
+          nref[4 * (r >> 1) + 2 + (r & 1)] = live ? 0.f : -1e30f;
+          slim[r] = p.causal ? min(a.ctx + j + 1, a.ctx + a.n) : a.ctx + a.n;
         }
-        if (!freed) {
-          ok = mbar_wait_warp(&pv_done[pp & 1], (pp >> 1) & 1, p.max_spin);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        tmem_st32_raw(trow + C::P_COL + (RHO == 1 ? slot : pb) * 32, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        mbar_arrive_if(&p_full[pb], lane == 0);
       }
-      if (!ok) break;
-      const int i = w.i, g = w.g, n = w.n;
+      fence_proxy_async_smem();
+      __syncwarp();
+      mbar_arrive_if(q_full, lane == 0);
+    };
+
+    fetch_q(w);
+    put_q(w);
+    named_bar_sync(1, T);
+    int pj = 0, st = 0, chunk = -1, freed = 0;  // chunk: scales that may be read; freed: given back
+    float lsum[ROWS];
+#pragma unroll 1
+    for (int j0 = 0, seg = 0; j0 < nunits; ++seg) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
       const bool whole = w.unit == 0 && cnt == w.units;
-      j0 += cnt;
-      const bool more = j0 < nunits;
+      Pos8 wn = w;                       // the next segment, whose queries are fetched now
+      const bool more = j0 + cnt < nunits;
       if (more) {
-        if (seg >= 0) pos_next_pair(w, p, sseq);
-        qfac = load_q(seg + 1, w.n);
-        ok = qfac >= 0.f;
+        pos_next_pair(wn, p, sseq);
+        fetch_q(wn);
       }
-      if (seg < 0 && ok) continue;
-      // every PV of the segment has completed
-      ok = ok && mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
-      // the (maximum, sum) slots are free once the previous segment's were read
-      ok = ok && (seg == 0 || mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin));
-      if (!ok) break;
-      ml[half * 128 + tl] = make_float2(m_run, l_run);
-      tc_fence_before();
-      __syncwarp();
-      mbar_arrive_if(seg_bar, lane == 0);
-      ok = mbar_wait_warp(seg_bar, seg & 1, p.max_spin);
-      if (!ok) break;
-      tc_fence_after();
-      // the sets that make up a row: a copy's lanes, or RHO = 1 the two O of its lane
-      float M = kNoMax, L = 0.f;
-#pragma unroll
-      for (int c = 0; c < C::NG; ++c) M = fmaxf(M, ml[c * ROWS + r].x);
-#pragma unroll
-      for (int c = 0; c < C::NG; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
-      const size_t row0 = (static_cast<size_t>(i * p.Hkv + g) + blockIdx.x) * R;   // partial rows
-      const float inv = whole ? 1.0f / L : 1.0f;
-      const int live = n * G;            // rows that are computed
-      if (half == 0 && copy == 0 && r < live && !whole)
-        *reinterpret_cast<float2 *>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
-      uint16_t *o = p.o + (static_cast<size_t>(i) * p.m * p.Hq + g * G) * HD;
-      if constexpr (RHO == 1) {
-        // each group takes half of the columns of both O
-        const bool has1 = cnt > 1;
-        const float a0 = ex2f(ml[tl].x - M) * inv, a1 = ex2f(ml[128 + tl].x - M) * inv;
+      const int every = p.causal ? w.ctx + 1 : w.ctx + w.n;  // keys that every row sees
+      const int last_key = w.ctx + w.n;
+      const uint32_t o_at = trow + C::O_COL + (seg % C::OB) * C::OCOLS;
 #pragma unroll 1
-        for (int c0 = half * (HD / 2); c0 < (half + 1) * (HD / 2); c0 += 16) {
-          float ov[16], o1[16];
-          tmem_ld16(trow + C::O_COL + c0, ov);
-          tmem_ld16(trow + C::O_COL + HD + c0, o1);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) ov[c] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
-          if (r < live) {
-            if (whole) {
-              uint16_t *dst = o + (static_cast<size_t>(jq) * p.Hq + r % G) * HD + c0;
-#pragma unroll
-              for (int v = 0; v < 2; ++v)
-                reinterpret_cast<uint4 *>(dst)[v] =
-                    make_uint4(pack_bf16x2(ov[8 * v], ov[8 * v + 1]), pack_bf16x2(ov[8 * v + 2], ov[8 * v + 3]),
-                               pack_bf16x2(ov[8 * v + 4], ov[8 * v + 5]), pack_bf16x2(ov[8 * v + 6], ov[8 * v + 7]));
-            } else {
-              float *dst = p.part_o + (row0 + r) * HD + c0;
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                reinterpret_cast<float4 *>(dst)[v] =
-                    make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
-            }
-          }
+      for (int u = 0; u < cnt; u += 2, ++pj) {
+        const int j = j0 + u, base = (w.unit + u) * kUnit;
+        const bool two = u + 1 < cnt;
+        const int jl = j + (two ? 1 : 0);
+        if (chunk < (jl >> 5)) {
+          fail |= !mbar_wait_warp(&sc_full[(chunk + 1) & 1], ((chunk + 1) >> 1) & 1, p.max_spin);
+          ++chunk;
+        }
+        if (freed < (j >> 5)) {          // a chunk is behind this pair
           __syncwarp();
+          mbar_arrive_if(&sc_empty[freed & 1], lane == 0);
+          ++freed;
         }
-      } else {
-        // A chunk of cw columns of every copy goes through shared memory, and the threads add the
-        // copies up. A copy that had no unit of the segment holds what it held before.
-        const float a = ex2f(m_run - M) * inv;
-        const bool has = m_run != kNoMax || l_run != 0.f;
-        float *stage = reinterpret_cast<float *>(smem + C::OFF_STG);
-        int cw = HD;                     // columns per chunk: RHO * live rows of cw fit the buffer
-        while (RHO * live * cw > C::STAGE) cw >>= 1;
-#pragma unroll 1
-        for (int c0 = 0; c0 < HD && ok; c0 += cw) {
-#pragma unroll 1
-          for (int cc = 0; cc < cw; cc += 16) {
-            float ov[16];
-            tmem_ld16(o_mine + c0 + cc, ov);
-            if (r < live) {
-              float *to = stage + (copy * live + r) * cw;
+        const int js = two ? j + slot : j;
+        const float4 sc = sscale[((js >> 5) & 1) * 32 + (js & 31)];  // K scale, log2 V, 1 / V, 1 for zeros
+        fail |= !mbar_wait_warp(&s_full[pj & 1], (pj >> 1) & 1, p.max_spin);
+        tc_fence_after();
+        // y = log2 of P: score in log2 units + log2 V scale - reference + kPBase
+        float y[ROWS];
+        float top = -INFINITY;
+        const uint32_t s_at = trow + C::S_COL + (pj % C::SB) * 2 * RP + r0;
+        const float2 ks2 = make_float2(sc.x, sc.x), c2 = make_float2(sc.y + kPBase, sc.y + kPBase);
 #pragma unroll
-              for (int c = 0; c < 16; ++c)   // columns turned by the row: no bank conflicts
-                to[(cc + c + r) & (cw - 1)] = has ? ov[c] * a : 0.f;
-            }
-            __syncwarp();
+        for (int c = 0; c < ROWS; c += 16) {
+          float h[16], l[16];
+          tmem_ld16(s_at + c, h);
+          tmem_ld16(s_at + RP + c, l);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float4 t = tab[(r0 + c + e) >> 1];
+            const float2 s2 = add2(make_float2(h[e], h[e + 1]), make_float2(l[e], l[e + 1]));
+            const float2 v = fma2(s2, mul2(make_float2(t.x, t.y), ks2), add2(make_float2(t.z, t.w), c2));
+            y[c + e] = v.x;
+            y[c + e + 1] = v.y;
           }
-          ok = half_sync();
-#pragma unroll 1
-          for (int e = tl; e < live * cw / 2 && ok; e += 128) {
-            const int rr = e / (cw / 2), c = (e % (cw / 2)) * 2;
-            float v0 = 0.f, v1 = 0.f;
+        }
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(&s_empty[pj & 1], lane == 0);
+        mbar_arrive_if(&k8_empty[st], tid == 0);  // S complete: the keys have been read
+        const bool there = base + key < last_key && (two || slot == 0);
+        if (base + 2 * kUnit > every || !two) {  // some row does not see the whole pair
 #pragma unroll
-            for (int y = 0; y < RHO; ++y) {
-              const float *from = stage + (y * live + rr) * cw;
-              v0 += from[(c + rr) & (cw - 1)];
-              v1 += from[(c + 1 + rr) & (cw - 1)];
+          for (int c = 0; c < ROWS; ++c) y[c] = there && base + key < slim[r0 + c] ? y[c] : -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < ROWS; c += 2) top = max3(top, y[c], y[c + 1]);
+        // rows of V that hold no value (beyond the last key, or of a scale of zero) may hold anything
+        const bool bad = rg == 0 && (two || slot == 0) && (!there || sc.w != 0.f);
+        if (named_bar_or(1, T, u == 0 || top > kTop || bad || fail)) {
+          // ---- now and then: the segment's first pair, a reference that has to move, values to clear
+          if (named_bar_or(1, T, fail)) {
+            gone = true;
+            break;
+          }
+          if (rg == 0 && __any_sync(0xffffffffu, bad)) {
+            if (pj >= 2) fail |= !mbar_wait_warp(&pv_done[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
+            fail |= !mbar_wait_warp(&v8_full[st], (pj / C::NS) & 1, p.max_spin);
+            if (bad) {
+              uint4 *row = reinterpret_cast<uint4 *>(sV8 + st * C::PAIR8 + key * HD);
+#pragma unroll
+              for (int e = 0; e < HD / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
             }
+          }
+          float mine = 0.f;
+#pragma unroll
+          for (int c = 0; c < ROWS; ++c) {
+            const float m = warp_max(y[c]);
+            mine = lane == (c & 31) ? m : mine;
+            if ((c & 31) == 31 || c == ROWS - 1)
+              if (lane <= (c & 31)) red[quarter * RP + r0 + (c & ~31) + lane] = mine;
+          }
+          named_bar_sync(1, T);
+          float d = 0.f;                 // the row's reference moves by d
+          if (tid < RP) {
+            const float m = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
+            if (tid < w.n * G && (u == 0 ? m > -INFINITY : m > kTop)) d = m - kPBase;
+            srow[tid] = d;
+            nref[4 * (tid >> 1) + 2 + (tid & 1)] -= d;
+          }
+          const bool moved = named_bar_or(1, T, d != 0.f);
+          if (moved) {
+#pragma unroll
+            for (int c = 0; c < ROWS; ++c) {
+              const float dc = srow[r0 + c];
+              y[c] -= dc;
+              lsum[c] *= ex2f(-dc);
+            }
+          }
+          if (u == 0) {
+#pragma unroll
+            for (int c = 0; c < ROWS; ++c) lsum[c] = 0.f;
+          } else if (moved) {
+            // O^T *= 2^-d, once every product before has been added
+            fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
+            tc_fence_after();
+#pragma unroll 1
+            for (int t = 0; t < (C::STACKED ? 3 : 1); ++t) {
+#pragma unroll 1
+              for (int c = 0; c < ROWS; c += 16) {
+                float ov[16];
+                uint32_t x[16];
+                tmem_ld16(o_at + t * RP + r0 + c, ov);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(ov[e] * ex2f(-srow[r0 + c + e]));
+                tmem_st16_raw(o_at + t * RP + r0 + c, x);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // P^T buffer pj % 2: read by the pair before last
+        if (pj >= 2) fail |= !mbar_wait_warp(&pv_done[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
+        uint8_t *prow = sP + (pj & 1) * C::P_BYTES + key * 128;
+        const float2 iv = make_float2(sc.z, sc.z);
+#pragma unroll
+        for (int c = 0; c < ROWS; c += 16) {
+          uint32_t ta[4], tb[4], tc[4];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float2 p0 = make_float2(ex2f(y[c + e]), ex2f(y[c + e + 1]));
+            const float2 p1 = make_float2(ex2f(y[c + e + 2]), ex2f(y[c + e + 3]));
+            const float2 l0 = fma2(p0, iv, make_float2(lsum[c + e], lsum[c + e + 1]));
+            const float2 l1 = fma2(p1, iv, make_float2(lsum[c + e + 2], lsum[c + e + 3]));
+            lsum[c + e] = l0.x;
+            lsum[c + e + 1] = l0.y;
+            lsum[c + e + 2] = l1.x;
+            lsum[c + e + 3] = l1.y;
+            const __half2 a = __floats2half2_rn(p0.x, p0.y), b = __floats2half2_rn(p1.x, p1.y);
+            split4(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b), ta[e / 4],
+                   tb[e / 4], tc[e / 4]);
+          }
+          // column t * RP + row of key's row: 128 columns a block, 16-byte chunks swizzled
+          auto put = [&](int col, const uint32_t (&v)[4]) {
+            *reinterpret_cast<uint4 *>(prow + (col >> 7) * C::PBLOCK + ((((col >> 4) & 7) ^ (key & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          };
+          put(r0 + c, ta);
+          put(RP + r0 + c, tb);
+          put(2 * RP + r0 + c, tc);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(&p_full[pj & 1], lane == 0);
+        st = st + 1 == C::NS ? 0 : st + 1;
+      }
+      if (gone) break;
+      // ---- segment end: sums, then the next segment's queries (its S can start), then the output
+      j0 += cnt;
+      const int live = w.n * G;
+      const size_t row0 = (static_cast<size_t>(w.i * p.Hkv + w.g) + blockIdx.x) * R;  // partial rows
+#pragma unroll
+      for (int c = 0; c < ROWS; c += 32) {
+        constexpr int N = ROWS < 32 ? ROWS : 32;
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = lsum[c + e];
+        const float s = lane_sums<N>(v, lane);
+        if (lane < N) red[quarter * RP + r0 + c + lane] = s;
+      }
+      named_bar_sync(1, T);
+      if (tid < RP) {
+        const float L = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
+        srow[tid] = whole ? 1.0f / L : 1.0f;
+        if (!whole && tid < live)
+          *reinterpret_cast<float2 *>(p.part_ml + (row0 + tid) * 2) =
+              make_float2(L == 0.f ? kNoMax : -nref[4 * (tid >> 1) + 2 + (tid & 1)], L);
+      }
+      named_bar_sync(1, T);
+      uint16_t *o = p.o + (static_cast<size_t>(w.i) * p.m * p.Hq + w.g * G) * HD + key;
+      if (more) {
+        w = wn;
+        put_q(w);
+      }
+      fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
+      tc_fence_after();
+      // lane = column `key` of the head; a row is written by a warp's lanes together
+#pragma unroll 1
+      for (int c = r0; c < r0 + ROWS && c < live; c += 16) {
+        float ov[16];
+        tmem_ld16(o_at + c, ov);
+        if (C::STACKED) {
+#pragma unroll 1
+          for (int t = 1; t < 3; ++t) {
+            float x[16];
+            tmem_ld16(o_at + t * RP + c, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] += x[e];
+          }
+        }
+        int jr = c / G, hr = c % G;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (c + e < live && (HD == 128 || key < HD)) {
+            const float v = ov[e] * srow[c + e];
             if (whole)
-              *reinterpret_cast<uint32_t *>(o + (static_cast<size_t>(rr / G) * p.Hq + rr % G) * HD + c0 + c) =
-                  pack_bf16x2(v0, v1);
+              o[(static_cast<size_t>(jr) * p.Hq + hr) * HD] = static_cast<uint16_t>(pack_bf16x2(v, v));
             else
-              *reinterpret_cast<float2 *>(p.part_o + (row0 + rr) * HD + c0 + c) = make_float2(v0, v1);
+              p.part_o[(row0 + c + e) * HD + key] = v;
           }
-          ok = ok && half_sync();
+          if (++hr == G) {
+            hr = 0;
+            ++jr;
+          }
         }
-        if (!ok) break;
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      mbar_arrive_if(o_free, lane == 0);
-      if (!more) break;
+      mbar_arrive_if(&o_free[seg % C::OB], lane == 0);
+      named_bar_sync(1, T);              // the tables hold the next segment's rows
     }
-    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+    if ((fail || gone) && lane == 0) flag_status(p.status, kStatusTimeout);
   }
 
   tc_fence_before();
@@ -939,7 +931,7 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
 }
 
 // The dynamic shared memory limit is a property of the kernel on one device.
-template <int HD, int RHO>
+template <int HD, int RP>
 static cudaError_t configure_attn8() {
   static std::mutex mutex;
   static bool done[64] = {};
@@ -948,30 +940,33 @@ static cudaError_t configure_attn8() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mutex);
   if (dev < 64 && done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(attn8_kernel<HD, RHO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(A8Cfg<HD, RHO>::SMEM));
+  e = cudaFuncSetAttribute(attn8_kernel<HD, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(A8Cfg<HD, RP>::SMEM));
   if (e == cudaSuccess && dev < 64) done[dev] = true;
   return e;
 }
 
-template <int HD, int RHO>
+template <int HD, int RP>
 static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
   const int R = (p.Hq / p.Hkv) * p.m;
-  cudaError_t e = configure_attn8<HD, RHO>();
+  cudaError_t e = configure_attn8<HD, RP>();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn8_kernel<HD, RHO>, dim3(p.grid), dim3(A8Cfg<HD, RHO>::THREADS), A8Cfg<HD, RHO>::SMEM, s, p);
+  e = launch_pdl(attn8_kernel<HD, RP>, dim3(p.grid), dim3(A8Cfg<HD, RP>::THREADS), A8Cfg<HD, RP>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn8_merge_kernel<HD>, dim3(p.nb * p.Hkv, (R + kMerge8Warps - 1) / kMerge8Warps),
                     dim3(kMerge8Warps * 32), 0, s, p);
 }
 
+template <int HD>
+static cudaError_t launch_attn8_rows(const Attn8Params &p, int R, cudaStream_t s) {
+  return R <= 16 ? launch_attn8<HD, 16>(p, s) : R <= 32 ? launch_attn8<HD, 32>(p, s)
+         : R <= 64 ? launch_attn8<HD, 64>(p, s) : launch_attn8<HD, 128>(p, s);
+}
+
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s) {
   const int R = (p.Hq / p.Hkv) * p.m;
   if (p.Hq % p.Hkv != 0 || R > 128) return cudaErrorInvalidValue;
-  // copies of the query rows that fill the MMA's 128
-  if (p.hd == 128)
-    return R > 64 ? launch_attn8<128, 1>(p, s) : R > 32 ? launch_attn8<128, 2>(p, s) : launch_attn8<128, 4>(p, s);
-  return R > 64 ? launch_attn8<64, 1>(p, s) : R > 32 ? launch_attn8<64, 2>(p, s) : launch_attn8<64, 4>(p, s);
+  return p.hd == 128 ? launch_attn8_rows<128>(p, R, s) : launch_attn8_rows<64>(p, R, s);
 }
 
 }  // namespace df

@@ -301,9 +301,8 @@ cudaError_t launch_kv_append8(const KvRowsParams &p, cudaStream_t s);
 
 // Attention of m query rows per sequence over an 8-bit cache (attention8.cu).
 struct Attn8Params {
-  CUtensorMap tmK;           // the layer's 8-bit key cache as {hd, rows}, box {hd, 64}, swizzled by hd bytes
+  CUtensorMap tmK, tmV;      // the layer's 8-bit caches as {hd, rows}, box {hd, 64}, swizzled by hd bytes
   const uint16_t *q;         // bf16 [nb][m][Hq][hd]
-  const uint8_t *v8;         // e4m3, the layer's value cache
   const float *ks, *vs;      // the layer's scales, one per 64 rows and kv head
   const int *n_rows;         // [nb] or null: m
   const int *ctx_len;        // [nb]

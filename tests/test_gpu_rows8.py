@@ -9,10 +9,13 @@ f32 2^-24):
   8 bits     half a step of e4m3: 2^-4 |y| for normal values, scale * 2^-10 for subnormal ones,
              and the same fp32 steps; scales are exact where amax is not within 2^-15 of a border
              (checked on the oracle's side). Rows that stay are exact.
-  attention  one bf16 rounding 2^-8 |o|; probabilities rounded to 11 bits, 2^-11 sum p|v|; scores:
-             hd products and sums in fp32, hd * 2^-24 * sum|q k| / sqrt(hd), which move p by twice
-             that at most; exponent and log2 steps below 2^-16 of p; probabilities too small for 11
-             bits are off by 2^-32 of the largest p * scale each: rows * 2^-32 * max|v|.
+  attention  one bf16 rounding 2^-8 |o|; probabilities rounded to f16, 2^-11 p, then to a sum of three
+             e5m2 terms: the first keeps 3 bits, so the rest is below 2^-2 of p's power of two, the
+             second rounds that rest to 3 bits (at most 2^-6 off), the third what is then left, at
+             most 2^-6, to 3 bits: at most 2^-10 off. Scores: hd products and sums in fp32,
+             hd * 2^-24 * sum|q k| / sqrt(hd), which move p by twice that at most; exponent and log2
+             steps below 2^-16 of p; e5m2's smallest step is 2^-16, half of it 2^-29 of the largest
+             p * scale (2^12 at the least) for every key: rows * 2^-29 * max|v|.
 """
 import numpy as np
 import pytest
@@ -384,8 +387,8 @@ def check_attention(c, layer, m, q, n, ctx, causal, out, what=""):
         V = c.rows(c.v8, layer, i, ctx[i] + n[i], c.vs) if n[i] else None
         if n[i]:
             o, mag, dot = orc.attention8(f64(q[i, :n[i]]), K, V, ctx[i], causal)
-            tol = (2.0 ** -8 * np.abs(o) + mag * (2.0 ** -11 + 2.0 ** -16 + 2 * c.hd * 2.0 ** -24 * dot[..., None])
-                   + K.shape[1] * 2.0 ** -32 * np.abs(V).max())
+            tol = (2.0 ** -8 * np.abs(o) + mag * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -16 + 2 * c.hd * 2.0 ** -24 * dot[..., None])
+                   + K.shape[1] * 2.0 ** -29 * np.abs(V).max())
             assert_within(f64(out[i, :n[i]]), o, tol, f"{what} sequence {i}")
         assert (out[i, n[i]:] == 7.0).all(), f"{what}: rows behind sequence {i}"
 
