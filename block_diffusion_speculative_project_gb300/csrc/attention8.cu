@@ -119,12 +119,12 @@ __device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
 // so a term costs columns of one pass and not a pass of its own over K or V, nothing is widened,
 // and a softmax thread (a TMEM lane) is one key, whose scale is a number of the thread.
 // Two e4m3 terms (4 bits each) hold bf16's 8 bits; three e5m2 terms keep 9 bits of a probability over
-// f16's range, all that is 2^-24 of the largest or more.
+// f16's range: half a step of the smallest is 2^-27 of the largest or less.
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
 template <int HD, int RP>
 struct A8Cfg {
-  static constexpr int NRG = RP >= 32 ? 2 : 1;       // groups of four softmax warps, ROWS query rows each
+  static constexpr int NRG = RP <= 64 ? RP / 16 : 4; // groups of four softmax warps, ROWS query rows each
   static constexpr int ROWS = RP / NRG;
   static constexpr int NSW = 4 * NRG;
   static constexpr bool STACKED = 3 * RP <= 256;     // P's terms side by side (an MMA has at most 256 columns)
@@ -159,7 +159,7 @@ constexpr int kSeqCache = 128;
 constexpr int kDrainSpin = 1 << 22;
 // P is 2^(x - reference + kPBase) for x in log2 units; the reference moves (and O with it) only when a
 // key exceeds it by more than kRescale: P stays at most 2^15, which e5m2 and f16 hold.
-constexpr float kPBase = 12.f, kRescale = 3.f;
+constexpr float kPBase = 10.f, kRescale = 5.f;
 
 // Warps: producer of values and scales, S issuer, PV issuer, producer of keys, softmax (warp w reads
 // TMEM lanes of quarter w % 4; rows of group (w - 4) / 4).
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         const int j = j0 + u, base = (w.unit + u) * kUnit;
         const bool two = u + 1 < cnt;
         const int jl = j + (two ? 1 : 0);
-        if (chunk < (jl >> 5)) {
+        if (chunk < (jl >> 5)) {         // (a unit that begins a chunk, or the pair after it)
           fail |= !mbar_wait_warp(&sc_full[(chunk + 1) & 1], ((chunk + 1) >> 1) & 1, p.max_spin);
           ++chunk;
         }
@@ -672,8 +672,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
 #pragma unroll
         for (int c = 0; c < ROWS; c += 16) {
           float h[16], l[16];
-          tmem_ld16(s_at + c, h);
-          tmem_ld16(s_at + RP + c, l);
+          tmem_ld16x2(s_at + c, s_at + RP + c, h, l);
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             const float4 t = tab[(r0 + c + e) >> 1];
