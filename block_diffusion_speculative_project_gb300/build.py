@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdflash.so")
-SOURCES = ["gemm_tc.cu", "attention.cu", "attention8.cu", "kv_rows.cu", "small_ops.cu", "sampling.cu", "dflash_api.cu"]
+SOURCES = ["gemm_tc.cu", "attention.cu", "attention8.cu", "attention8_wide.cu", "kv_rows.cu", "small_ops.cu", "sampling.cu", "dflash_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

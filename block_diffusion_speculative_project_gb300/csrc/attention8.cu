@@ -9,138 +9,42 @@
 // of one pair is a segment. A segment that covers its pair writes the output, any other an
 // unnormalised partial (o, running maximum, running sum) to slot pair + cta, which the merge
 // kernel joins in CTA order.
-#include <cfloat>
-#include <cmath>
 #include <mutex>
 
-#include <cuda_fp8.h>
-
-#include "common.cuh"
-#include "kernels.h"
+#include "attention8.cuh"
 
 namespace df {
-
-namespace {
-
-constexpr int kUnit = kPageRows;   // keys per unit: rows that share a scale, rows of a page
-constexpr float kNoMax = -1e30f;   // running maximum (log2 units) before the first key
-
-// Rows of sequence i that the call computes, its context rows (clamped to the caller's bound
-// and the cache) and its units.
-struct Seq8 {
-  int n, ctx, units;
-};
-__device__ __forceinline__ Seq8 seq8(const Attn8Params &p, int i) {
-  Seq8 s;
-  s.n = p.n_rows ? max(0, min(p.n_rows[i], p.m)) : p.m;
-  s.ctx = max(0, min(p.ctx_len[i], min(p.max_ctx, p.Cmax - s.n)));
-  s.units = s.n > 0 ? (s.ctx + s.n + kUnit - 1) / kUnit : 0;
-  return s;
-}
-
-// Unit u of the pair (sequence i, kv head g) as a block index of the cache.
-__device__ __forceinline__ long long block_of(const Attn8Params &p, int i, int g, int u) {
-  if (p.page_table == nullptr) return (static_cast<long long>(i) * p.Hkv + g) * (p.Cmax / kUnit) + u;
-  int pg = p.page_table[static_cast<long long>(i) * p.pages_per_seq + u];
-  if (pg < 0 || pg >= p.num_pages) {
-    flag_status(p.status, kStatusCheck);
-    pg = 0;
-  }
-  return static_cast<long long>(pg) * p.Hkv + g;
-}
-
-// The T units are split over G CTAs: the first T % G take one more than the others (T is below
-// 2^25: a handle's caches hold fewer than 2^31 rows).
-__device__ __forceinline__ int cta_start(int T, int G, int c) { return c * (T / G) + min(c, T % G); }
-__device__ __forceinline__ int cta_of(int T, int G, int u) {
-  const int q = T / G, big = (T % G) * (q + 1);
-  return u < big ? u / (q + 1) : T % G + (u - big) / q;
-}
-
-// Units of the sequences before i (`before`) and of all of them, times Hkv. Warp-collective.
-__device__ __forceinline__ int total_units(const Attn8Params &p, int i, int lane, int *before) {
-  int t = 0, b = 0;
-#pragma unroll 1
-  for (int s = lane; s < p.nb; s += 32) {
-    const int u = seq8(p, s).units;
-    t += u;
-    b += s < i ? u : 0;
-  }
-  *before = __reduce_add_sync(0xffffffffu, b) * p.Hkv;
-  return __reduce_add_sync(0xffffffffu, t) * p.Hkv;
-}
-
-// Where a CTA's range begins (pair i * Hkv + g, unit inside it) and its number of units.
-// Warp-collective.
-__device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
-  int base;
-  const int T = total_units(p, 0, lane, &base);
-  const int Ge = min(T, p.grid);
-  int count = 0, pair = 0, unit = 0;
-  if (cta < Ge) {
-    const int u0 = cta_start(T, Ge, cta);
-    count = cta_start(T, Ge, cta + 1) - u0;
-#pragma unroll 1
-    for (int b = 0; b < p.nb; b += 32) {
-      const int U = b + lane < p.nb ? seq8(p, b + lane).units : 0;
-      int v = p.Hkv * U;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + v > u0);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        const int Ul = __shfl_sync(0xffffffffu, U, l);
-        const int off = u0 - (base + __shfl_sync(0xffffffffu, v, l) - p.Hkv * Ul);
-        pair = (b + l) * p.Hkv + off / Ul;
-        unit = off % Ul;
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  if (lane == 0) {
-    out[0] = pair;
-    out[1] = unit;
-    out[2] = count;
-  }
-}
-
-}  // namespace
 
 // ---------------------------------------------------------------- tensor-core kernel
 
 // Both products read the cache's bytes as they are, with the keys and the head's columns as the 128
 // rows of the MMA and the query rows (RP of them, padded) as its columns:
-//   S^T [128 keys][2 RP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of two e4m3 terms
-//   O^T [hd][3 RP]       += V^T [hd x keys, e4m3] P^T, each probability as the sum of three e5m2 terms
-// so a term costs columns of one pass and not a pass of its own over K or V, nothing is widened,
-// and a softmax thread (a TMEM lane) is one key, whose scale is a number of the thread.
+//   S^T [128 keys][RP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of two e4m3 terms
+//   O^T [hd][3 RP]     += V^T [hd x keys, e4m3] P^T, each probability as the sum of three e5m2 terms
+// so nothing is widened, and a softmax thread (a TMEM lane) is one key, whose scale is a number of the
+// thread. P's terms are columns of one pass over V; Q's are two passes over K, which the tensor cores
+// have the time for and which spare the softmax the second half of the columns.
 // Two e4m3 terms (4 bits each) hold bf16's 8 bits; three e5m2 terms keep 9 bits of a probability over
 // f16's range: half a step of the smallest is 2^-27 of the largest or less.
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
 template <int HD, int RP>
 struct A8Cfg {
-  static constexpr int NRG = RP <= 64 ? RP / 16 : 4; // groups of four softmax warps, ROWS query rows each
-  static constexpr int ROWS = RP / NRG;
+  static constexpr int ROWS = 16;                    // query rows of a softmax thread
+  static constexpr int NRG = RP / ROWS;              // groups of four softmax warps
   static constexpr int NSW = 4 * NRG;
-  static constexpr bool STACKED = 3 * RP <= 256;     // P's terms side by side (an MMA has at most 256 columns)
-  static constexpr int SB = RP <= 64 ? 2 : 1;        // buffers of S, and of O
-  static constexpr int OB = RP <= 32 ? 2 : 1;
+  static constexpr int SB = 2, OB = 2;               // buffers of S, and of O
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values)
   static constexpr int PAIR8 = 2 * UNIT8;
   // rings of pairs, one of keys and one of values, as much as shared memory holds
-  static constexpr int NS = (RP <= 32 ? 5 : RP == 64 ? 4 : 2) * (128 / HD);
-  static constexpr int PBLOCK = 128 * 128;           // P^T: 128 keys of 128 of its columns
-  static constexpr int P_BYTES = (3 * RP + 127) / 128 * PBLOCK;
+  static constexpr int NS = 5 * (128 / HD);
+  static constexpr int P_BYTES = 128 * 128;          // P^T: 128 keys, rows of 128 bytes of which 3 RP hold terms
   static constexpr int OFF_V8 = NS * PAIR8;
   static constexpr int OFF_P = 2 * NS * PAIR8;       // two buffers
   static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;  // 2 RP rows of hd bytes
-  static constexpr int OFF_TAB = OFF_Q + 2 * RP * HD;     // [RP/2] factor and -reference of two rows
-  static constexpr int OFF_LIM = OFF_TAB + RP * 8;        // [RP] keys that a row sees
+  static constexpr int OFF_REF = OFF_Q + 2 * RP * HD;     // [RP] -reference of a row
+  static constexpr int OFF_FAC = OFF_REF + RP * 4;        // [RP] factor of a row, [RP / 16] of a block of rows
+  static constexpr int OFF_LIM = OFF_FAC + RP * 4 + 64;        // [RP] keys that a row sees
   static constexpr int OFF_RED = OFF_LIM + RP * 4;        // [4][RP] a quarter's maxima, sums
   static constexpr int OFF_ROW = OFF_RED + 4 * RP * 4;    // [RP] a number for every row
   static constexpr int OFF_SC = OFF_ROW + RP * 4;         // [2 chunks][32 units] scales
@@ -148,15 +52,16 @@ struct A8Cfg {
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
   static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_REF % 16 == 0 && OFF_LIM % 16 == 0 &&
+                    OFF_RED % 16 == 0 && OFF_SC % 16 == 0 && OFF_BAR % 16 == 0 && OFF_SEQ % 16 == 0,
+                "alignment: 1024 bytes for swizzled tiles, 16 for what is read as vectors");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr int OCOLS = STACKED ? 3 * RP : RP;
-  static constexpr uint32_t S_COL = 0;               // S^T of pair pj in buffer pj % SB: 2 RP columns
-  static constexpr uint32_t O_COL = SB * 2 * RP;     // O^T of segment seg in buffer seg % OB
+  static constexpr int OCOLS = 3 * RP;
+  static constexpr uint32_t S_COL = 0;               // S^T of pair pj in buffer pj % SB: RP columns
+  static constexpr uint32_t O_COL = SB * RP;     // O^T of segment seg in buffer seg % OB
   static_assert(O_COL + OB * OCOLS <= TMEM_COLS, "tensor memory");
   static constexpr int THREADS = (4 + NSW) * 32;
 };
-constexpr int kSeqCache = 128;
-constexpr int kDrainSpin = 1 << 22;
 // P is 2^(x - reference + kPBase) for x in log2 units; the reference moves (and O with it) only when a
 // key exceeds it by more than kRescale: P stays at most 2^15, which e5m2 and f16 hold.
 constexpr float kPBase = 10.f, kRescale = 5.f;
@@ -164,48 +69,6 @@ constexpr float kPBase = 10.f, kRescale = 5.f;
 // Warps: producer of values and scales, S issuer, PV issuer, producer of keys, softmax (warp w reads
 // TMEM lanes of quarter w % 4; rows of group (w - 4) / 4).
 constexpr int kWValues = 0, kWS = 1, kWPV = 2, kWKeys = 3, kWSoft = 4;
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// One of the warp's threads, the same one every time; the branch on it leaves the code around it
-// warp-uniform.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
-}
-
-// A unit inside a CTA's range: sequence i, kv head g, unit of `units`.
-struct Pos8 {
-  int i, g, unit, units, n, ctx;
-};
-__device__ __noinline__ int2 seq_far(const Attn8Params &p, int i) {
-  const Seq8 s = seq8(p, i);
-  return make_int2(s.n, s.ctx);
-}
-__device__ __forceinline__ void pos_seq(Pos8 &w, const Attn8Params &p, const int2 *sseq) {
-#pragma unroll 1
-  for (;; ++w.i) {  // a sequence without rows has no units (one with rows follows)
-    const int2 s = w.i < kSeqCache ? sseq[w.i] : seq_far(p, w.i);
-    w.n = s.x;
-    w.ctx = s.y;
-    w.units = w.n > 0 ? (w.ctx + w.n + kUnit - 1) / kUnit : 0;
-    if (w.units > 0) return;
-  }
-}
-// To the pair (sequence, kv head) after this one.
-__device__ __forceinline__ void pos_next_pair(Pos8 &w, const Attn8Params &p, const int2 *sseq) {
-  w.unit = 0;
-  if (++w.g == p.Hkv) {
-    w.g = 0;
-    ++w.i;
-    pos_seq(w, p, sseq);
-  }
-}
 
 // The blocks of a CTA's units in order, for a producer warp: lane l looks up unit 32 c + l of chunk
 // c, a chunk ahead.
@@ -264,21 +127,20 @@ __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
 }
 
 // Four probabilities (two f16 pairs, non-negative) as three e5m2 terms each, four to a word. e5m2 is
-// f16's upper byte: the first term cuts (the rest is exact), the other two round.
+// f16's upper byte: the first term cuts, the others round (half a step is 0x80, which carries into the
+// byte; the sums and differences are exact), so what is left is at most 2^-10 of the value.
 __device__ __forceinline__ void split4(uint32_t p01, uint32_t p23, uint32_t &a, uint32_t &b, uint32_t &c) {
-  a = __byte_perm(p01, p23, 0x7531);
+  constexpr uint32_t kUpper = 0xFF00FF00u, kHalf = 0x00800080u;
   auto rest = [](uint32_t x, uint32_t y) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
     return *reinterpret_cast<const uint32_t *>(&d);
   };
-  auto round = [](uint32_t x) {
-    return static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw *>(&x),
-                                                            __NV_SATFINITE, __NV_E5M2));
-  };
-  const uint32_t r01 = rest(p01, p01 & 0xFF00FF00u), r23 = rest(p23, p23 & 0xFF00FF00u);
-  const uint32_t b01 = round(r01), b23 = round(r23);
-  b = b01 | (b23 << 16);
-  c = round(rest(r01, __byte_perm(b01, 0, 0x1404))) | (round(rest(r23, __byte_perm(b23, 0, 0x1404))) << 16);
+  a = __byte_perm(p01, p23, 0x7531);
+  const uint32_t r01 = rest(p01, p01 & kUpper), r23 = rest(p23, p23 & kUpper);
+  const uint32_t b01 = r01 + kHalf, b23 = r23 + kHalf;
+  b = __byte_perm(b01, b23, 0x7531);
+  const uint32_t c01 = rest(r01, b01 & kUpper) + kHalf, c23 = rest(r23, b23 & kUpper) + kHalf;
+  c = __byte_perm(c01, c23, 0x7531);
 }
 
 template <int HD, int RP>
@@ -289,7 +151,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *sK8 = smem, *sV8 = smem + C::OFF_V8, *sP = smem + C::OFF_P, *sQ = smem + C::OFF_Q;
-  float4 *tab = reinterpret_cast<float4 *>(smem + C::OFF_TAB);
+  float *nref = reinterpret_cast<float *>(smem + C::OFF_REF);
+  float *sfac = reinterpret_cast<float *>(smem + C::OFF_FAC);
   int *slim = reinterpret_cast<int *>(smem + C::OFF_LIM);
   float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
   float *srow = reinterpret_cast<float *>(smem + C::OFF_ROW);
@@ -451,8 +314,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
 #pragma unroll 1
     for (int x = max(0, pj - C::NS); x < pj; ++x) mbar_wait_warp(&full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
   } else if (warp == kWS) {
-    // ---------------- S issuer: S^T = K Q^T
-    constexpr uint32_t id = idesc_8bit_f32(128, 2 * RP);
+    // ---------------- S issuer: S^T = K Q^T, the queries' two terms one after the other
+    constexpr uint32_t id = idesc_8bit_f32(128, RP);
     const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(sK8)) : sw64_kmajor_desc(smem_u32(sK8));
     const uint64_t qd = HD == 128 ? sw128_kmajor_desc(smem_u32(sQ)) : sw64_kmajor_desc(smem_u32(sQ));
     int st = 0, ph = 0, pj = 0;
@@ -469,10 +332,12 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         if (!ok) break;
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::PAIR8) >> 4);
-        const uint32_t d = tmem + C::S_COL + (pj % C::SB) * 2 * RP;
+        const uint32_t d = tmem + C::S_COL + (pj % C::SB) * RP;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 32; ++kk) tc_mma_8bit(d, kd + kk * 2, qd + kk * 2, id, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 2 * (HD / 32); ++kk)
+            tc_mma_8bit(d, kd + kk % (HD / 32) * 2, qd + kk % (HD / 32) * 2 + kk / (HD / 32) * (RP * HD >> 4), id,
+                        kk > 0 ? 1u : 0u);
           tc_commit(&s_full[pj & 1]);
         }
         __syncwarp();
@@ -496,7 +361,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     // hd = 64: the second half of the MMA's rows reads the next unit's values and is not used
     const uint64_t vd0 = HD == 128 ? sw128_mnmajor_desc(smem_u32(sV8), C::UNIT8)
                                    : sw64_mnmajor_desc(smem_u32(sV8), C::UNIT8);
-    const uint64_t pd0 = sw128_mnmajor_desc(smem_u32(sP), C::PBLOCK);
+    const uint64_t pd0 = sw128_mnmajor_desc(smem_u32(sP), C::P_BYTES);
     int st = 0, ph = 0, pj = 0;
     bool ok = true;
 #pragma unroll 1
@@ -518,11 +383,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk >= 2 && u + 1 >= cnt) break;   // one unit alone
-#pragma unroll
-            for (int t = 0; t < (C::STACKED ? 1 : 3); ++t)
-              tc_mma_8bit(d, vd + static_cast<uint64_t>((kk * 32 * HD) >> 4),
-                          pd + static_cast<uint64_t>((t * C::PBLOCK + kk * 32 * 128) >> 4), id,
-                          (kk > 0 || t > 0) ? 1u : add);
+            tc_mma_8bit(d, vd + static_cast<uint64_t>((kk * 32 * HD) >> 4),
+                        pd + static_cast<uint64_t>((kk * 32 * 128) >> 4), id, kk > 0 ? 1u : add);
           }
           tc_commit(&pv_done[b]);
           tc_commit(&v8_empty[st]);
@@ -550,7 +412,6 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
     constexpr float kTop = kPBase + kRescale;
-    float *nref = reinterpret_cast<float *>(tab);  // -reference of row r at 4 (r / 2) + 2 + r % 2
     bool fail = false, gone = false;
 
     // The query rows of a segment: eight threads a row, hd/8 values each, read a segment ahead.
@@ -566,25 +427,51 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         for (int y = 0; y < HD / 64; ++y) qr[x][y] = j < a.n ? src[y] : make_uint4(0, 0, 0, 0);
       }
     };
-    // A row is scaled by a power of two so that its largest value lies in [2^7, 2^8), and stored as
-    // hi + lo, e4m3: bf16's 8 bits exactly down to 2^-10 of the largest value, below to 2^-18 of it.
+    // The rows are scaled by a power of two so that the largest value of a block of 16 rows lies in
+    // [2^7, 2^8), and stored as hi + lo, e4m3: bf16's 8 bits exactly down to 2^-10 of that value, below
+    // to 2^-18 of it. A block whose rows' largest values differ by more than 2^3 scales every row on its
+    // own (the block's factor is then -1). Two barriers.
     auto put_q = [&](const Pos8 &a) {
+      int *sexp = reinterpret_cast<int *>(red);
+      float am[PASS];
 #pragma unroll
       for (int x = 0; x < PASS; ++x) {
-        const int r = x * (T / 8) + (tid >> 3), part = tid & 7;
-        float am = 0.f;
+        am[x] = 0.f;
 #pragma unroll
         for (int y = 0; y < HD / 64; ++y) {
           const uint32_t v[4] = {qr[x][y].x, qr[x][y].y, qr[x][y].z, qr[x][y].w};
 #pragma unroll
           for (int f = 0; f < 4; ++f)
-            am = fmaxf(am, fmaxf(fabsf(__uint_as_float(v[f] << 16)), fabsf(__uint_as_float(v[f] & 0xFFFF0000u))));
+            am[x] = fmaxf(am[x], fmaxf(fabsf(__uint_as_float(v[f] << 16)), fabsf(__uint_as_float(v[f] & 0xFFFF0000u))));
         }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-        int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;  // -127: zero or subnormal, 128: infinite
-        const bool inf = ex == 128;                                  // the row's outputs are NaN
-        ex = max(min(ex, 127), -100);
+        for (int o = 1; o < 8; o <<= 1) am[x] = fmaxf(am[x], __shfl_xor_sync(0xffffffffu, am[x], o));
+        // -127: zero or subnormal, 128: infinite
+        if ((tid & 7) == 0) sexp[x * (T / 8) + (tid >> 3)] = static_cast<int>(__float_as_uint(am[x]) >> 23) - 127;
+      }
+      named_bar_sync(1, T);
+      int exs[PASS];
+#pragma unroll
+      for (int x = 0; x < PASS; ++x) {
+        const int r = x * (T / 8) + (tid >> 3);
+        int lo = 200, hi = -100;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const int4 v = *reinterpret_cast<const int4 *>(sexp + (r & ~15) + e);
+          hi = max(max(hi, max(v.x, v.y)), max(v.z, v.w));
+          lo = min(min(lo, min(v.x == -127 ? 200 : v.x, v.y == -127 ? 200 : v.y)),
+                   min(v.z == -127 ? 200 : v.z, v.w == -127 ? 200 : v.w));
+        }
+        const bool apart = hi == 128 || hi - lo > 3;
+        exs[x] = apart ? max(sexp[r], -100) : hi;
+        if ((tid & 7) == 0 && (r & 15) == 0)
+          sfac[RP + (r >> 4)] = apart ? -1.f : sl2 * __uint_as_float(static_cast<uint32_t>(hi + 120) << 23);
+      }
+#pragma unroll
+      for (int x = 0; x < PASS; ++x) {
+        const int r = x * (T / 8) + (tid >> 3), part = tid & 7;
+        const bool inf = exs[x] == 128;                              // the row's outputs are NaN
+        const int ex = min(exs[x], 127);
         const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(134 - ex) << 23);
         uint32_t hi[HD / 32], lo[HD / 32];
 #pragma unroll
@@ -618,21 +505,31 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
           // the factor takes S to log2 units, 1/sqrt(hd) included; rows that are not there get P = 0
           const int j = r / G;
           const bool live = j < a.n;
-          nref[4 * (r >> 1) + (r & 1)] = live ? sl2 * __uint_as_float(static_cast<uint32_t>(ex + 120) << 23) : 0.f;
-          nref[4 * (r >> 1) + 2 + (r & 1)] = live ? 0.f : -1e30f;
+          sfac[r] = live ? sl2 * __uint_as_float(static_cast<uint32_t>(ex + 120) << 23) : 0.f;
+          nref[r] = live ? 0.f : -1e30f;
           slim[r] = p.causal ? min(a.ctx + j + 1, a.ctx + a.n) : a.ctx + a.n;
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       mbar_arrive_if(q_full, lane == 0);
+      named_bar_sync(1, T);
     };
 
     fetch_q(w);
     put_q(w);
-    named_bar_sync(1, T);
     int pj = 0, st = 0, chunk = -1, freed = 0;  // chunk: scales that may be read; freed: given back
     float lsum[ROWS];
+    float own[ROWS];       // -references of this thread's rows
+    float fac[ROWS / 16];                // factors of their blocks
+    auto keep_rows = [&]() {
+#pragma unroll
+      for (int c = 0; c < ROWS; c += 4)
+        *reinterpret_cast<float4 *>(own + c) = *reinterpret_cast<const float4 *>(nref + r0 + c);
+#pragma unroll
+      for (int c = 0; c < ROWS / 16; ++c) fac[c] = sfac[RP + r0 / 16 + c];
+    };
+    keep_rows();
 #pragma unroll 1
     for (int j0 = 0, seg = 0; j0 < nunits; ++seg) {
       const int cnt = min(w.units - w.unit, nunits - j0);
@@ -667,17 +564,19 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         // y = log2 of P: score in log2 units + log2 V scale - reference + kPBase
         float y[ROWS];
         float top = -INFINITY;
-        const uint32_t s_at = trow + C::S_COL + (pj % C::SB) * 2 * RP + r0;
-        const float2 ks2 = make_float2(sc.x, sc.x), c2 = make_float2(sc.y + kPBase, sc.y + kPBase);
+        const uint32_t s_at = trow + C::S_COL + (pj % C::SB) * RP + r0;
+        const float2 c2 = make_float2(sc.y + kPBase, sc.y + kPBase);
 #pragma unroll
         for (int c = 0; c < ROWS; c += 16) {
-          float h[16], l[16];
-          tmem_ld16x2(s_at + c, s_at + RP + c, h, l);
+          float h[16];
+          tmem_ld16(s_at + c, h);
+          float2 f2 = make_float2(fac[c / 16] * sc.x, fac[c / 16] * sc.x);
+          const bool apart = fac[c / 16] < 0.f;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float4 t = tab[(r0 + c + e) >> 1];
-            const float2 s2 = add2(make_float2(h[e], h[e + 1]), make_float2(l[e], l[e + 1]));
-            const float2 v = fma2(s2, mul2(make_float2(t.x, t.y), ks2), add2(make_float2(t.z, t.w), c2));
+            const float2 nr = make_float2(own[c + e], own[c + e + 1]);
+            if (apart) f2 = make_float2(sfac[r0 + c + e] * sc.x, sfac[r0 + c + e + 1] * sc.x);
+            const float2 v = fma2(make_float2(h[e], h[e + 1]), f2, add2(nr, c2));
             y[c + e] = v.x;
             y[c + e + 1] = v.y;
           }
@@ -724,10 +623,11 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
             const float m = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
             if (tid < w.n * G && (u == 0 ? m > -INFINITY : m > kTop)) d = m - kPBase;
             srow[tid] = d;
-            nref[4 * (tid >> 1) + 2 + (tid & 1)] -= d;
+            nref[tid] -= d;
           }
           const bool moved = named_bar_or(1, T, d != 0.f);
           if (moved) {
+            keep_rows();
 #pragma unroll
             for (int c = 0; c < ROWS; ++c) {
               const float dc = srow[r0 + c];
@@ -743,7 +643,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
             fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
             tc_fence_after();
 #pragma unroll 1
-            for (int t = 0; t < (C::STACKED ? 3 : 1); ++t) {
+            for (int t = 0; t < 3; ++t) {
 #pragma unroll 1
               for (int c = 0; c < ROWS; c += 16) {
                 float ov[16];
@@ -778,9 +678,9 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
             split4(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b), ta[e / 4],
                    tb[e / 4], tc[e / 4]);
           }
-          // column t * RP + row of key's row: 128 columns a block, 16-byte chunks swizzled
+          // column t * RP + row of the key's row, 16-byte chunks swizzled
           auto put = [&](int col, const uint32_t (&v)[4]) {
-            *reinterpret_cast<uint4 *>(prow + (col >> 7) * C::PBLOCK + ((((col >> 4) & 7) ^ (key & 7)) << 4)) =
+            *reinterpret_cast<uint4 *>(prow + (((col >> 4) ^ (key & 7)) << 4)) =
                 make_uint4(v[0], v[1], v[2], v[3]);
           };
           put(r0 + c, ta);
@@ -813,7 +713,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         srow[tid] = whole ? 1.0f / L : 1.0f;
         if (!whole && tid < live)
           *reinterpret_cast<float2 *>(p.part_ml + (row0 + tid) * 2) =
-              make_float2(L == 0.f ? kNoMax : -nref[4 * (tid >> 1) + 2 + (tid & 1)], L);
+              make_float2(L == 0.f ? kNoMax : -nref[tid], L);
       }
       named_bar_sync(1, T);
       uint16_t *o = p.o + (static_cast<size_t>(w.i) * p.m * p.Hq + w.g * G) * HD + key;
@@ -828,14 +728,12 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       for (int c = r0; c < r0 + ROWS && c < live; c += 16) {
         float ov[16];
         tmem_ld16(o_at + c, ov);
-        if (C::STACKED) {
 #pragma unroll 1
-          for (int t = 1; t < 3; ++t) {
-            float x[16];
-            tmem_ld16(o_at + t * RP + c, x);
+        for (int t = 1; t < 3; ++t) {
+          float x[16];
+          tmem_ld16(o_at + t * RP + c, x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] += x[e];
-          }
+          for (int e = 0; e < 16; ++e) ov[e] += x[e];
         }
         int jr = c / G, hr = c % G;
 #pragma unroll
@@ -857,7 +755,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       tc_fence_before();
       __syncwarp();
       mbar_arrive_if(&o_free[seg % C::OB], lane == 0);
-      named_bar_sync(1, T);              // the tables hold the next segment's rows
+      keep_rows();
     }
     if ((fail || gone) && lane == 0) flag_status(p.status, kStatusTimeout);
   }
@@ -947,25 +845,25 @@ static cudaError_t configure_attn8() {
 
 template <int HD, int RP>
 static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
-  const int R = (p.Hq / p.Hkv) * p.m;
   cudaError_t e = configure_attn8<HD, RP>();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn8_kernel<HD, RP>, dim3(p.grid), dim3(A8Cfg<HD, RP>::THREADS), A8Cfg<HD, RP>::SMEM, s, p);
+  return launch_pdl(attn8_kernel<HD, RP>, dim3(p.grid), dim3(A8Cfg<HD, RP>::THREADS), A8Cfg<HD, RP>::SMEM, s, p);
+}
+
+template <int HD>
+static cudaError_t launch_rows(const Attn8Params &p, cudaStream_t s) {
+  const int R = (p.Hq / p.Hkv) * p.m;
+  cudaError_t e = R <= 16   ? launch_attn8<HD, 16>(p, s)
+                  : R <= 32 ? launch_attn8<HD, 32>(p, s)
+                            : launch_attention8_wide(p, R, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn8_merge_kernel<HD>, dim3(p.nb * p.Hkv, (R + kMerge8Warps - 1) / kMerge8Warps),
                     dim3(kMerge8Warps * 32), 0, s, p);
 }
 
-template <int HD>
-static cudaError_t launch_attn8_rows(const Attn8Params &p, int R, cudaStream_t s) {
-  return R <= 16 ? launch_attn8<HD, 16>(p, s) : R <= 32 ? launch_attn8<HD, 32>(p, s)
-         : R <= 64 ? launch_attn8<HD, 64>(p, s) : launch_attn8<HD, 128>(p, s);
-}
-
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s) {
-  const int R = (p.Hq / p.Hkv) * p.m;
-  if (p.Hq % p.Hkv != 0 || R > 128) return cudaErrorInvalidValue;
-  return p.hd == 128 ? launch_attn8_rows<128>(p, R, s) : launch_attn8_rows<64>(p, R, s);
+  if (p.Hq % p.Hkv != 0 || (p.Hq / p.Hkv) * p.m > 128) return cudaErrorInvalidValue;
+  return p.hd == 128 ? launch_rows<128>(p, s) : launch_rows<64>(p, s);
 }
 
 }  // namespace df

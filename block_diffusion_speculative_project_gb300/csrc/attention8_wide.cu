@@ -1,0 +1,752 @@
+// The 8-bit attention for more than 32 query rows of a kv head (attention8.cu has the formula, the
+// split over CTAs and the form for fewer rows): the query rows are the 128 rows of the MMA,
+//   S [rows][128 keys] = Q K^T     Q two e4m3 terms in tensor memory, K the cache's bytes
+//   O [rows][hd]      += P V       P f16 in tensor memory, V widened to f16 in shared memory
+// so that a softmax thread is a query row. Widening V costs the same for any number of rows; splitting
+// probabilities into 8-bit terms, as the form for few rows does, costs more than that from about 48
+// rows on (one 262,155-row context, 64 rows: 123 us in this form, 194 in the other; 32 rows of 64
+// ragged contexts: 163 and 161).
+#include <mutex>
+
+#include "attention8.cuh"
+
+namespace df {
+
+namespace {
+// RHO copies of the query rows fill the 128 lanes of the MMA (rows padded to 128 / RHO): the lanes
+// of copy c take only the c-th part of a unit's keys, the other parts' probabilities being zero
+// in the P operand, so that every SM quarter's warps share the exponentials of few rows.
+template <int HD, int RHO>
+struct WideCfg {
+  static constexpr int KW = kUnit / RHO;             // keys of a unit per copy
+  static constexpr int ROWS = 128 / RHO;             // padded query rows
+  static constexpr int ATOMS = HD / 64;              // 128-byte swizzle atoms across hd (f16)
+  static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
+  static constexpr int PAIR8 = 2 * UNIT8;
+  // ring of pairs of units in 8 bits, keys then values, as much as shared memory holds
+  static constexpr int NS = 4 * (128 / HD);
+  static constexpr int ATOM16 = kUnit * 128;
+  static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
+  static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
+  static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of a half's exchange of O between copies
+  static constexpr int OFF_8 = 2 * TILE16;
+  static constexpr int OFF_Q = OFF_8 + NS * 2 * PAIR8;
+  static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
+  static constexpr int OFF_ML = OFF_STG + 2 * STAGE * 4;  // [2 halves][128 lanes] (maximum, sum)
+  static constexpr int OFF_SC = OFF_ML + 2 * 128 * 8;     // [2 chunks][32 units] scales
+  static constexpr int OFF_BAR = OFF_SC + 64 * 16;
+  static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
+  static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t S_COL = 0;                // S of a pair of units: 64 columns each
+  static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
+  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // queries, two e4m3 terms: hd / 4 columns each
+  static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of a pair's units: 32 columns each
+  static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
+};
+// P is 2^(x - m_run + kPBase), m_run the maximum at the last rescale: O is rescaled only when the
+// maximum has grown by more than 2^kRescale, so P stays at most 2^15 in f16, and what is 2^-21 of
+// the largest still has all 11 bits (2^-31 one bit).
+constexpr float kPBase = 7.f, kRescale = 8.f;
+
+// A segment's units are taken in pairs: one S product of 128 keys, then softmax, PV and O for each
+// unit of the pair on its own. What bounds the kernel are the steps from one role to the next (with
+// every copy, product and exponential left out it still took 0.8 of its time, a unit at a time), so
+// they are paid for two units at once. Half a pair at the end of a segment of an odd number of units
+// is signalled by every role without work.
+// Warps: producer, S issuer, PV issuer, one that only helps at the start, softmax half h = 0, 1 (a
+// pair's first or second unit) in 4 + 4h .. 7 + 4h (warp w reads TMEM lanes of quarter w % 4), then
+// the converters of V.
+constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWAid = 3, kWSoft = 4, kWConv = 12, kNumConv = 4;
+constexpr int kWideThreads = (kWConv + kNumConv) * 32;
+
+template <int KW>
+__device__ __forceinline__ void load_s(uint32_t taddr, float (&v)[KW]) {
+  if constexpr (KW == 64)
+    tmem_ld64(taddr, v);
+  else
+    tmem_ld32(taddr, v);
+}
+template <int KW>
+__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t *v) {
+  if constexpr (KW == 64)
+    tmem_st32_raw(taddr, v);
+  else
+    tmem_st16_raw(taddr, v);
+}
+
+// 8 e4m3 values to f16 (exact).
+__device__ __forceinline__ uint4 widen8(uint2 u) {
+  uint4 h;
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+      "mov.b32 {a, b}, %4;\n\t"
+      "mov.b32 {c, d}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+      : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
+      : "r"(u.x), "r"(u.y));
+  return h;
+}
+
+template <int HD, int RHO>
+__global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __grid_constant__ Attn8Params p) {
+  using C = WideCfg<HD, RHO>;
+  constexpr int KW = C::KW, ROWS = C::ROWS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *sV16 = smem, *s8 = smem + C::OFF_8, *sQ = smem + C::OFF_Q;
+  float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+  float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
+  uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint64_t *kv8_empty = kv8_full + C::NS;
+  uint64_t *v16_full = kv8_empty + C::NS;   // [2] a pair's first and second unit
+  uint64_t *p_full = v16_full + 2;          // [2]
+  uint64_t *p_empty = p_full + 2;           // [2] PV complete: the P and V16 buffers have been read
+  uint64_t *sc_full = p_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
+  uint64_t *sc_empty = sc_full + 2;         // [2]
+  uint64_t *half_bar = sc_empty + 2;        // [2] the four warps of a half among themselves
+  uint64_t *mma_done = half_bar + 2;        // [2]
+  uint64_t *s_full = mma_done + 2;          // S of a pair complete
+  uint64_t *s_empty = s_full + 1;           // and read by both halves
+  uint64_t *q8_full = s_empty + 1;          // a segment's query rows have landed
+  uint64_t *q8_empty = q8_full + 1;
+  uint64_t *q_full = q8_empty + 1;          // and are in tensor memory
+  uint64_t *q_empty = q_full + 1;
+  uint64_t *seg_bar = q_empty + 1;          // both halves: (maximum, sum) of a segment written
+  uint64_t *o_free = seg_bar + 1;           // both O and ml read
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
+  int *sched = reinterpret_cast<int *>(tmem_slot + 1);
+  static_assert((2 * C::NS + 14 + 8) * 8 + 16 <= 512, "barrier region overflows");
+  int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  const int R = G * p.m;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&kv8_full[s], 1);
+      mbar_init(&kv8_empty[s], kNumConv + 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&v16_full[b], kNumConv);
+      mbar_init(&p_full[b], 4);
+      mbar_init(&p_empty[b], 1);
+      mbar_init(&sc_full[b], 1);
+      mbar_init(&sc_empty[b], 8);
+      mbar_init(&half_bar[b], 4);
+      mbar_init(&mma_done[b], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 8);
+    mbar_init(q8_full, 1);
+    mbar_init(q8_empty, 8);
+    mbar_init(q_full, 4);
+    mbar_init(q_empty, 1);
+    mbar_init(seg_bar, 8);
+    mbar_init(o_free, 8);
+    fence_mbar_init();
+  }
+  if (warp == kWS) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch();
+  if (warp == kWProd) {
+    find_range(p, blockIdx.x, lane, sched);
+  } else if (warp == kWAid) {
+    for (int i = lane; i < p.nb && i < kSeqCache; i += 32) {
+      const Seq8 s = seq8(p, i);
+      sseq[i] = make_int2(s.n, s.ctx);
+    }
+  } else if (warp == kWPV && blockIdx.x == 0) {
+    for (int i = lane; i < p.nb; i += 32) {
+      const int n = p.n_rows ? p.n_rows[i] : p.m, c = p.ctx_len[i];
+      if (n < 0 || n > p.m || c < 0 || c > p.max_ctx || static_cast<long long>(c) + max(n, 0) > p.Cmax)
+        flag_status(p.status, kStatusCheck);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const int nunits = __shfl_sync(0xffffffffu, sched[2], 0);
+  Pos8 w;
+  w.i = sched[0] / p.Hkv;
+  w.g = sched[0] % p.Hkv;
+  w.unit = sched[1];
+  if (nunits > 0) pos_seq(w, p, sseq);
+
+  // Every role goes through the CTA's segments: `cnt` units from unit j0 of the CTA on, in pairs pj
+  // of units u, u + 1 of the segment. A wait that runs out ends the role (ok = false).
+  if (nunits == 0) {
+    // nothing to do
+  } else if (warp == kWProd) {
+    // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each (the keys
+    // arrive swizzled, as the tensor cores read them), a query row hd bf16. Lane l looks up the block of unit 32 c + l of the CTA's range two chunks c
+    // ahead and its scales one chunk ahead, so the copies wait for neither.
+    const uint64_t pol = policy_evict_first();
+    bool ok = !p.stall;
+    int pairs = 0, segs = 0;
+    Pos8 a = w;
+    int x = lane;
+    a.unit += lane;
+    auto look_up = [&]() {
+      if (x >= nunits) return 0;
+      while (a.unit >= a.units) {
+        const int over = a.unit - a.units;
+        pos_next_pair(a, p, sseq);
+        a.unit = over;
+      }
+      const int b = static_cast<int>(block_of(p, a.i, a.g, a.unit));
+      a.unit += 32;
+      return b;
+    };
+    int blk = look_up();
+    x += 32;
+    int blk1 = look_up();
+    float ks = lane < nunits ? p.ks[blk] : 0.f, vs = lane < nunits ? p.vs[blk] : 0.f;
+    int cnt_left = 0, slot = 0, st = 0, ph = 0;
+    bool published = false;
+#pragma unroll 1
+    for (int j = 0; j < nunits && ok; ++j) {
+      const int k = j & 31, c = j >> 5;
+      if (cnt_left == 0) {  // a segment begins: its query rows
+        if (j > 0) pos_next_pair(w, p, sseq);
+        cnt_left = min(w.units - w.unit, nunits - j);
+        ok = segs == 0 || mbar_wait_warp(q8_empty, (segs - 1) & 1, p.max_spin);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
+        __syncwarp();
+#pragma unroll 1
+        for (int r = lane; r < w.n * G; r += 32)
+          bulk_load(sQ + r * C::QPITCH,
+                    p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
+                    pol);
+        ++segs;
+        slot = 0;
+      }
+      --cnt_left;
+      const long long b = __shfl_sync(0xffffffffu, blk, k);
+      if (slot == 0) ok = pairs < C::NS || mbar_wait_warp(&kv8_empty[st], ph ^ 1, p.max_spin);
+      if (!ok) break;
+      if (elect_one()) {
+        uint8_t *dst = s8 + st * 2 * C::PAIR8;
+        if (slot == 0) mbar_arrive_expect_tx(&kv8_full[st], (cnt_left > 0 ? 2 : 1) * C::PAIR8);
+        tma_load_2d(dst + slot * C::UNIT8, &p.tmK, &kv8_full[st], 0, static_cast<int>(b) * kUnit, pol);
+        bulk_load(dst + C::PAIR8 + slot * C::UNIT8, p.v8 + b * C::UNIT8, C::UNIT8, &kv8_full[st], pol);
+      }
+      __syncwarp();
+      if (slot == 0) ++pairs;
+      if (slot == 1 || cnt_left == 0) {  // the pair is complete
+        slot = 0;
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      } else {
+        slot = 1;
+      }
+      // The chunk's scales, after its first copies are under way, and before any wait for a unit
+      // of the chunk: a copy waits for the pair NS > 3 before its own, the next segment's queries
+      // for the units of the segment before last.
+      published = published && k != 0;
+      if (!published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
+        published = true;
+        ok = c < 2 || mbar_wait_warp(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
+        if (!ok) break;
+        const bool zero = vs == 0.f;  // a block of zeros: P must not see the scale
+        sscale[(c & 1) * 32 + lane] = make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 0.f : 1.f);
+        __syncwarp();
+        mbar_arrive_if(&sc_full[c & 1], lane == 0);
+      }
+      if (k == 31) {
+        blk = blk1;
+        x += 32;
+        const bool more = x - 32 < nunits;
+        ks = more ? p.ks[blk] : 0.f;
+        vs = more ? p.vs[blk] : 0.f;
+        blk1 = look_up();
+      }
+    }
+    if (!ok && !p.stall && lane == 0) flag_status(p.status, kStatusTimeout);
+    // every issued copy must land before the CTA may exit (bounded)
+#pragma unroll 1
+    for (int x = max(0, pairs - C::NS); x < pairs; ++x)
+      mbar_wait_warp(&kv8_full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
+    if (segs > 0) mbar_wait_warp(q8_full, (segs - 1) & 1, kDrainSpin);
+  } else if (warp == kWS) {
+    // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two e4m3
+    // terms one after the other from tensor memory
+    constexpr uint32_t id_s = idesc_8bit_f32(128, kUnit);
+    const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(s8)) : sw64_kmajor_desc(smem_u32(s8));
+    constexpr uint32_t id_s2 = idesc_8bit_f32(128, 2 * kUnit);
+    int st = 0, ph = 0, pj = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      ok = mbar_wait_warp(q_full, seg & 1, p.max_spin);
+#pragma unroll 1
+      for (int u = 0; u < cnt && ok; u += 2, ++pj) {
+        ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
+        ok = ok && (pj == 0 || mbar_wait_warp(s_empty, (pj - 1) & 1, p.max_spin));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = kd0 + static_cast<uint64_t>((st * 2 * C::PAIR8) >> 4);
+        const uint32_t id = u + 1 < cnt ? id_s2 : id_s;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 2 * HD / 32; ++kk)
+            tc_mma_e4m3_tmem_a(tmem + C::S_COL, tmem + C::Q_COL + kk * 8,
+                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id, kk > 0 ? 1u : 0u);
+          tc_commit(s_full);
+          if (u + 2 >= cnt) tc_commit(q_empty);
+        }
+        __syncwarp();
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      j0 += cnt;
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
+    }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+    // every issued MMA must complete before TMEM is freed (bounded)
+    if (elect_one()) tc_commit(&mma_done[0]);
+    __syncwarp();
+    mbar_wait_warp(&mma_done[0], 0, kDrainSpin);
+  } else if (warp == kWPV) {
+    // ---------------- PV issuer: O_b += P V for a pair's unit b; a segment's first pair starts the
+    // accumulators, after both O of the previous segment were read
+    constexpr uint32_t id_pv = idesc_f16_f32(128, HD) | kIdescBMajorMN;
+    const uint64_t vd0 = sw128_mnmajor_desc(smem_u32(sV16), C::ATOM16);
+    bool ok = true;
+    int pj = 0;
+#pragma unroll 1
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      if (seg > 0) ok = mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin);
+#pragma unroll 1
+      for (int x = 0; x < ((cnt + 1) & ~1) && ok; ++x) {
+        const int b = x & 1;
+        ok = mbar_wait_warp(&v16_full[b], pj & 1, p.max_spin);
+        ok = ok && mbar_wait_warp(&p_full[b], pj & 1, p.max_spin);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (x < cnt) {
+            const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kUnit / 16; ++kk)
+              tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
+                                 vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, (x > 1 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit(&p_empty[b]);
+        }
+        __syncwarp();
+        pj += b;
+      }
+      j0 += cnt;
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
+    }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+    if (elect_one()) tc_commit(&mma_done[1]);
+    __syncwarp();
+    mbar_wait_warp(&mma_done[1], 0, kDrainSpin);
+  } else if (warp >= kWConv) {
+    // ---------------- converters: V from e4m3 to f16, in the layout of a 128-byte-swizzled copy (rows
+    // of 64 values, 16-byte chunk c of row r at c ^ (r & 7))
+    constexpr int CPR = HD / 8;                        // 8-value chunks of a row: 8 bytes to 16
+    constexpr int RPI = kNumConv * 32 / CPR;           // rows per iteration: 8 or 16
+    constexpr int PER = kUnit / RPI;                   // chunks per thread
+    static_assert(RPI % 8 == 0, "a thread's chunks all lie at the same place of their rows");
+    const int t = (warp - kWConv) * 32 + lane;
+    const int cc = t % CPR, r0 = t / CPR;
+    uint8_t *out = sV16 + (cc >> 3) * C::ATOM16 + r0 * 128 + (((cc & 7) ^ (r0 & 7)) << 4);
+    const uint8_t *src0 = s8 + C::PAIR8 + t * 8;
+    bool ok = true;
+    int st = 0, ph = 0, pj = 0;
+#pragma unroll 1
+    for (int j0 = 0; j0 < nunits && ok;) {
+      const int cnt = min(w.units - w.unit, nunits - j0);
+      int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
+#pragma unroll 1
+      for (int x = 0; x < ((cnt + 1) & ~1); ++x, keys -= kUnit) {
+        const int b = x & 1;
+        if (b == 0) ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
+        ok = ok && (pj == 0 || mbar_wait_warp(&p_empty[b], (pj - 1) & 1, p.max_spin));
+        if (!ok) break;
+        const uint8_t *src = src0 + st * 2 * C::PAIR8 + b * C::UNIT8;
+        uint8_t *dst = out + b * C::TILE16;
+        if (x >= cnt) {
+          // half a pair
+        } else if (keys < kUnit) {
+          // rows beyond the last key may hold anything (even NaN); P is 0 there
+#pragma unroll 2
+          for (int e = 0; e < PER; ++e) {
+            uint4 h = make_uint4(0, 0, 0, 0);
+            if (r0 + e * RPI < keys) h = widen8(*reinterpret_cast<const uint2 *>(src + e * RPI * HD));
+            *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = h;
+          }
+        } else {
+          uint2 u[PER];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) u[e] = *reinterpret_cast<const uint2 *>(src + e * RPI * HD);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = widen8(u[e]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive_if(&v16_full[b], lane == 0);
+        if (b == 1) {
+          mbar_arrive_if(&kv8_empty[st], lane == 0);
+          ++pj;
+          if (++st == C::NS) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      j0 += cnt;
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
+    }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+  } else if (warp >= kWSoft) {
+    // ---------------- softmax: thread = TMEM lane; lane l holds query row l % ROWS, copy l / ROWS
+    const int half = (warp - kWSoft) >> 2, q = warp & 3;
+    const int tl = q * 32 + lane;
+    const int r = tl % ROWS, copy = tl / ROWS;
+    const int k0 = copy * KW;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int jq = r / G;               // row r: query row jq of query head g * G + r % G
+    const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
+    uint32_t half_phase = 0;
+    // Barrier of a half's warps, bounded like every other wait.
+    auto half_sync = [&]() {
+      __syncwarp();
+      mbar_arrive_if(&half_bar[half], lane == 0);
+      const bool done = mbar_wait_warp(&half_bar[half], half_phase, p.max_spin);
+      half_phase ^= 1;
+      return done;
+    };
+    if (RHO > 1) {  // the other copies' parts of the P rows stay zero
+      const uint32_t z[16] = {};
+      tmem_st16_raw(trow + C::P_COL + half * 32, z);
+      tmem_st16_raw(trow + C::P_COL + half * 32 + 16, z);
+      tmem_wait_st();
+    }
+    // The query row of segment `seg` (n rows a sequence), scaled by a power of two so that its
+    // largest value lies in [2^7, 2^8), to tensor memory as the sum of two e4m3 terms: 4 bits each
+    // hold bf16's 8, exactly down to 2^-10 of the largest value, below that to 2^-18 of it.
+    // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
+    auto load_q = [&](int seg, int n) {
+      bool ok = mbar_wait_warp(q8_full, seg & 1, p.max_spin);
+      if (half == 0 && seg > 0) ok = ok && mbar_wait_warp(q_empty, (seg - 1) & 1, p.max_spin);
+      if (!ok) return -1.f;
+      const uint4 *src = reinterpret_cast<const uint4 *>(sQ + r * C::QPITCH);
+      const bool have = r < n * G;
+      float am = 0.f;
+#pragma unroll 4
+      for (int e = 0; e < HD / 8; ++e) {
+        const uint4 u = have ? src[e] : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          am = fmaxf(am, fmaxf(fabsf(__uint_as_float(x[f] << 16)), fabsf(__uint_as_float(x[f] & 0xFFFF0000u))));
+      }
+      int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
+      const bool inf = ex == 128;          // the row's outputs are NaN
+      ex = max(min(ex, 127), -100);
+      if (half == 0) {
+        const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < HD / 32; ++part) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const float2 y = make_float2(__uint_as_float(x[f] << 16) * mul, __uint_as_float(x[f] & 0xFFFF0000u) * mul);
+              const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
+              const float2 af = __half22float2(*reinterpret_cast<const __half2 *>(&ar));
+              const __nv_fp8x2_storage_t b =
+                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E4M3);
+              const int d = 2 * e + f / 2;
+              hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(a) << 16) : a;
+              lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(b) << 16) : b;
+            }
+          }
+          tmem_st8_raw(trow + C::Q_COL + part * 8, hi);
+          tmem_st8_raw(trow + C::Q_COL + HD / 4 + part * 8, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      mbar_arrive_if(q_full, lane == 0 && half == 0);
+      mbar_arrive_if(q8_empty, lane == 0);
+      return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
+    };
+    float qfac = 0.f;
+    bool ok = true;
+    int chunk = -1;                      // chunk of 32 units whose scales this warp may read
+    int pj = 0, st = 0;                  // pair of units, and its stage of the ring
+    // Segment by segment: its units, then the queries of the next one (whose S can start), then the
+    // output of this one. The round before the first segment has the queries alone.
+#pragma unroll 1
+    for (int j0 = 0, seg = -1;; ++seg) {
+      const int cnt = seg < 0 ? 0 : min(w.units - w.unit, nunits - j0);
+      const int lim = p.causal ? min(w.ctx + jq + 1, w.ctx + w.n) : w.ctx + w.n;
+      // keys from the segment's first unit on that every row sees
+      const int all = (p.causal ? w.ctx + 1 : w.ctx + w.n) - w.unit * kUnit;
+      float m_run = kNoMax, l_run = 0.f;
+#pragma unroll 1
+      for (int u = half; u < ((cnt + 1) & ~1) + half; u += 2, ++pj) {
+        const int j = min(j0 + u, j0 + cnt - 1);
+        if (chunk < (j >> 5)) {          // the next chunk: give the one before back
+          __syncwarp();
+          if (chunk >= 0) mbar_arrive_if(&sc_empty[chunk & 1], lane == 0);
+          ++chunk;
+          ok = mbar_wait_warp(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
+        }
+        const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // K scale, log2 V, 1 / V, 0 for zeros
+        ok = ok && mbar_wait_warp(s_full, pj & 1, p.max_spin);
+        if (!ok) break;
+        tc_fence_after();
+        float sv[KW];
+        load_s<KW>(trow + C::S_COL + half * kUnit + k0, sv);
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(s_empty, lane == 0);
+        mbar_arrive_if(&kv8_empty[st], lane == 0 && warp == kWSoft);  // S complete: the keys have been read
+        st = st + 1 == C::NS ? 0 : st + 1;
+        // the P buffer and O_half are free once PV of this half's previous unit has completed
+        bool freed = pj == 0;
+        if (u >= cnt) {                  // half a pair
+          ok = freed || mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          if (!ok) break;
+          mbar_arrive_if(&p_full[half], lane == 0);
+          continue;
+        }
+        if (all - kUnit * u < kUnit) {   // some row does not see the whole unit
+          const int nv = lim - (w.unit + u) * kUnit - k0;  // keys this thread sees of its part
+#pragma unroll
+          for (int c = 0; c < KW; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
+        }
+        const float c1 = fmaxf(qfac * sc.x, 1e-37f);
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int c = 4; c + 8 <= KW; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[c + 2 * e], sv[c + 2 * e + 1]);
+        mx[3] = max3(max3(mx[3], sv[KW - 4], sv[KW - 3]), sv[KW - 2], sv[KW - 1]);
+        const float m_new = fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c1, sc.y);
+        const bool need = m_new - m_run > kRescale;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2f(m_run - m_new);
+          m_run = m_new;
+          l_run *= alpha;
+        }
+        if (u >= 2 && __any_sync(0xffffffffu, need && r < R)) {
+          ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          if (!ok) break;
+          tc_fence_after();
+          freed = true;
+#pragma unroll 1
+          for (int cc = 0; cc < HD / 16; ++cc) {
+            float ov[16];
+            tmem_ld16(trow + C::O_COL + half * HD + cc * 16, ov);
+            uint32_t x[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(ov[c] * alpha);
+            tmem_st16_raw(trow + C::O_COL + half * HD + cc * 16, x);
+          }
+        }
+        const float c2 = sc.y - m_run + kPBase;
+        uint32_t pk[KW / 2];
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < KW; c += 2) {
+          const float2 x = fma2(make_float2(sv[c], sv[c + 1]), make_float2(c1, c1), make_float2(c2, c2));
+          const float2 e = make_float2(ex2f(x.x), ex2f(x.y));
+          ls[(c >> 1) & 1] = add2(ls[(c >> 1) & 1], e);
+          const __half2 y = __floats2half2_rn(e.x, e.y);
+          pk[c / 2] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+        const float2 lt = add2(ls[0], ls[1]);
+        l_run = fmaf(lt.x + lt.y, sc.z, l_run);
+        if (sc.w == 0.f) {
+#pragma unroll
+          for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
+        }
+        if (!freed) {
+          ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        store_p<KW>(trow + C::P_COL + half * 32 + k0 / 2, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_if(&p_full[half], lane == 0);
+      }
+      if (!ok) break;
+      const int i = w.i, g = w.g, n = w.n;
+      const bool whole = w.unit == 0 && cnt == w.units;
+      j0 += cnt;
+      const bool more = j0 < nunits;
+      if (more) {
+        if (seg >= 0) pos_next_pair(w, p, sseq);
+        qfac = load_q(seg + 1, w.n);
+        ok = qfac >= 0.f;
+      }
+      if (seg < 0 && ok) continue;
+      ok = ok && mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
+      // the (maximum, sum) slots are free once the previous segment's were read
+      ok = ok && (seg == 0 || mbar_wait_warp(o_free, (seg - 1) & 1, p.max_spin));
+      if (!ok) break;
+      ml[half * 128 + tl] = make_float2(m_run, l_run);
+      tc_fence_before();
+      __syncwarp();
+      mbar_arrive_if(seg_bar, lane == 0);
+      ok = mbar_wait_warp(seg_bar, seg & 1, p.max_spin);
+      if (!ok) break;
+      tc_fence_after();
+      float M = kNoMax, L = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2 * RHO; ++c) M = fmaxf(M, ml[c * ROWS + r].x);
+#pragma unroll
+      for (int c = 0; c < 2 * RHO; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
+      const size_t row0 = (static_cast<size_t>(i * p.Hkv + g) + blockIdx.x) * R;   // partial rows
+      const float inv = whole ? 1.0f / L : 1.0f;
+      const bool has1 = cnt > 1;
+      const float a0 = ex2f(ml[tl].x - M) * inv, a1 = has1 ? ex2f(ml[128 + tl].x - M) * inv : 0.f;
+      const int live = n * G;            // rows that are computed
+      if (half == 0 && copy == 0 && r < live && !whole)
+        *reinterpret_cast<float2 *>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
+      // Each half takes its half of the columns of O_0 and O_1. With copies, a chunk of cw columns
+      // of every copy goes through shared memory, and the half's threads add the copies up.
+      uint16_t *o = p.o + (static_cast<size_t>(i) * p.m * p.Hq + g * G) * HD;
+      if constexpr (RHO == 1) {
+#pragma unroll 1
+        for (int c0 = half * (HD / 2); c0 < (half + 1) * (HD / 2); c0 += 16) {
+          float ov[16], o1[16];
+          tmem_ld16(trow + C::O_COL + c0, ov);
+          tmem_ld16(trow + C::O_COL + HD + c0, o1);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) ov[c] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
+          if (r < live) {
+            if (whole) {
+              uint16_t *dst = o + (static_cast<size_t>(jq) * p.Hq + r % G) * HD + c0;
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                reinterpret_cast<uint4 *>(dst)[v] =
+                    make_uint4(pack_bf16x2(ov[8 * v], ov[8 * v + 1]), pack_bf16x2(ov[8 * v + 2], ov[8 * v + 3]),
+                               pack_bf16x2(ov[8 * v + 4], ov[8 * v + 5]), pack_bf16x2(ov[8 * v + 6], ov[8 * v + 7]));
+            } else {
+              float *dst = p.part_o + (row0 + r) * HD + c0;
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                reinterpret_cast<float4 *>(dst)[v] =
+                    make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        float *stage = reinterpret_cast<float *>(smem + C::OFF_STG) + half * C::STAGE;
+        int cw = HD / 2;                 // columns per chunk: RHO * live rows of cw fit the buffer
+        while (RHO * live * cw > C::STAGE) cw >>= 1;
+        for (int c0 = 0; c0 < HD / 2 && ok; c0 += cw) {
+#pragma unroll 1
+          for (int cc = 0; cc < cw; cc += 16) {
+            const uint32_t col = half * (HD / 2) + c0 + cc;
+            float ov[16], o1[16];
+            tmem_ld16(trow + C::O_COL + col, ov);
+            tmem_ld16(trow + C::O_COL + HD + col, o1);
+            if (r < live) {
+              float *to = stage + (copy * live + r) * cw;
+#pragma unroll
+              for (int c = 0; c < 16; ++c)   // columns turned by the row: no bank conflicts
+                to[(cc + c + r) & (cw - 1)] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
+            }
+            __syncwarp();
+          }
+          ok = half_sync();
+          for (int e = tl; e < live * cw / 2 && ok; e += 128) {
+            const int rr = e / (cw / 2), c = (e % (cw / 2)) * 2;
+            float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+            for (int y = 0; y < RHO; ++y) {
+              const float *from = stage + (y * live + rr) * cw;
+              v0 += from[(c + rr) & (cw - 1)];
+              v1 += from[(c + 1 + rr) & (cw - 1)];
+            }
+            const int col = half * (HD / 2) + c0 + c;
+            if (whole)
+              *reinterpret_cast<uint32_t *>(o + (static_cast<size_t>(rr / G) * p.Hq + rr % G) * HD + col) =
+                  pack_bf16x2(v0, v1);
+            else
+              *reinterpret_cast<float2 *>(p.part_o + (row0 + rr) * HD + col) = make_float2(v0, v1);
+          }
+          ok = ok && half_sync();
+        }
+        if (!ok) break;
+      }
+      tc_fence_before();
+      __syncwarp();
+      mbar_arrive_if(o_free, lane == 0);
+      if (!more) break;
+    }
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+
+template <int HD, int RHO>
+cudaError_t launch_wide_form(const Attn8Params &p, cudaStream_t s) {
+  static std::mutex mutex;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mutex);
+    if (dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(attn8_wide_kernel<HD, RHO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(WideCfg<HD, RHO>::SMEM));
+      if (e != cudaSuccess) return e;
+      if (dev < 64) done[dev] = true;
+    }
+  }
+  return launch_pdl(attn8_wide_kernel<HD, RHO>, dim3(p.grid), dim3(kWideThreads), WideCfg<HD, RHO>::SMEM, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s) {
+  // copies of the query rows that fill the MMA's 128
+  if (p.hd == 128) return R > 64 ? launch_wide_form<128, 1>(p, s) : launch_wide_form<128, 2>(p, s);
+  return R > 64 ? launch_wide_form<64, 1>(p, s) : launch_wide_form<64, 2>(p, s);
+}
+
+}  // namespace df

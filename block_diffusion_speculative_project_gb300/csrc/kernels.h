@@ -302,6 +302,7 @@ cudaError_t launch_kv_append8(const KvRowsParams &p, cudaStream_t s);
 // Attention of m query rows per sequence over an 8-bit cache (attention8.cu).
 struct Attn8Params {
   CUtensorMap tmK, tmV;      // the layer's 8-bit caches as {hd, rows}, box {hd, 64}, swizzled by hd bytes
+  const uint8_t *v8;         // the layer's value cache
   const uint16_t *q;         // bf16 [nb][m][Hq][hd]
   const float *ks, *vs;      // the layer's scales, one per 64 rows and kv head
   const int *n_rows;         // [nb] or null: m
@@ -320,6 +321,8 @@ struct Attn8Params {
   int stall;                 // test hook: issue no loads so the waits run out
 };
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s);
+// Its kernel for R = G*m > 32 query rows a kv head (attention8_wide.cu), without the merge.
+cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 
 // Slots of partial outputs the attention of nb sequences may write: at most one per
 // (pair, CTA) boundary, i.e. nb * Hkv + grid.
