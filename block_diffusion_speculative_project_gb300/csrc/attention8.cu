@@ -25,7 +25,7 @@ namespace df {
 // thread. P's terms are columns of one pass over V; Q's are two passes over K, which the tensor cores
 // have the time for and which spare the softmax the second half of the columns.
 // Two e4m3 terms (4 bits each) hold bf16's 8 bits; three e5m2 terms keep 9 bits of a probability over
-// f16's range: half a step of the smallest is 2^-27 of the largest or less.
+// f16's range: half a step of the smallest is 2^-24 of the largest or less.
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
 template <int HD, int RP>
@@ -64,7 +64,7 @@ struct A8Cfg {
 };
 // P is 2^(x - reference + kPBase) for x in log2 units; the reference moves (and O with it) only when a
 // key exceeds it by more than kRescale: P stays at most 2^15, which e5m2 and f16 hold.
-constexpr float kPBase = 10.f, kRescale = 5.f;
+constexpr float kPBase = 7.f, kRescale = 8.f;
 
 // Warps: producer of values and scales, S issuer, PV issuer, producer of keys, softmax (warp w reads
 // TMEM lanes of quarter w % 4; rows of group (w - 4) / 4).
@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         int jr = c / G, hr = c % G;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          if (c + e < live && (HD == 128 || key < HD)) {
+          if (c + e >= live) break;
+          if (HD == 128 || key < HD) {
             const float v = ov[e] * srow[c + e];
             if (whole)
               o[(static_cast<size_t>(jr) * p.Hq + hr) * HD] = static_cast<uint16_t>(pack_bf16x2(v, v));

@@ -14,8 +14,8 @@ f32 2^-24):
              second rounds that rest to 3 bits (at most 2^-6 off), the third what is then left, at
              most 2^-6, to 3 bits: at most 2^-10 off. Scores: hd products and sums in fp32,
              hd * 2^-24 * sum|q k| / sqrt(hd), which move p by twice that at most; exponent and log2
-             steps below 2^-16 of p; e5m2's smallest step is 2^-16, half of it 2^-27 of the largest
-             p * scale (2^10 at the least) for every key: rows * 2^-27 * max|v|.
+             steps below 2^-16 of p; e5m2's smallest step is 2^-16, half of it 2^-24 of the largest
+             p * scale (2^7 at the least) for every key: rows * 2^-24 * max|v|.
 """
 import numpy as np
 import pytest
@@ -388,7 +388,7 @@ def check_attention(c, layer, m, q, n, ctx, causal, out, what=""):
         if n[i]:
             o, mag, dot = orc.attention8(f64(q[i, :n[i]]), K, V, ctx[i], causal)
             tol = (2.0 ** -8 * np.abs(o) + mag * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -16 + 2 * c.hd * 2.0 ** -24 * dot[..., None])
-                   + K.shape[1] * 2.0 ** -27 * np.abs(V).max())
+                   + K.shape[1] * 2.0 ** -24 * np.abs(V).max())
             assert_within(f64(out[i, :n[i]]), o, tol, f"{what} sequence {i}")
         assert (out[i, n[i]:] == 7.0).all(), f"{what}: rows behind sequence {i}"
 
