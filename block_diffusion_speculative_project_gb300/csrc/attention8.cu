@@ -5,10 +5,10 @@
 //
 // A block of 64 rows is the unit of work: its scale is one number, so K's goes into the scores'
 // factor and V's into the probabilities. The units of all (sequence, kv head) pairs, in that
-// order, are cut into `grid` contiguous ranges of equal size, one per CTA; a CTA's run of units
-// of one pair is a segment. A segment that covers its pair writes the output, any other an
-// unnormalised partial (o, running maximum, running sum) to slot pair + cta, which the merge
-// kernel joins in CTA order.
+// order, are cut into `grid` contiguous ranges of equal weight, one per CTA (a pair weighs its
+// units and a constant more); a CTA's run of units of one pair is a segment. A segment that covers
+// its pair writes the output, any other an unnormalised partial (o, running maximum, running sum) to
+// slot pair + cta, which the merge kernel joins in a fixed order.
 #include <mutex>
 
 #include "attention8.cuh"
@@ -769,13 +769,19 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
   }
 }
 
-// Joins the partials of every pair whose units several CTAs took, in CTA order. One warp per
-// query row, HD/32 consecutive values per lane.
+// Joins the partials of every pair whose units several CTAs took, in a fixed order. SPLIT warps per
+// query row, HD/32 consecutive values per lane; the maxima and sums come first, a lane per part, so
+// that the partial outputs load without waiting for one another. SPLIT is 8 where a pair has 8 parts
+// or more (128 rows of 19 parts: 12.5 -> 9.0 us with the attention of 32 units a pair before it; 512
+// rows of 19 parts 115 -> 107 us with the attention of 4096) and 1 with fewer, where most of the 8
+// warps had nothing (4096 rows of 3 parts: 34 us with 1, 44 with 8).
 constexpr int kMerge8Warps = 8;
 
-template <int HD>
+template <int HD, int SPLIT>
 __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __grid_constant__ Attn8Params p) {
   constexpr int E = HD / 32;
+  constexpr int ROWS = kMerge8Warps / SPLIT;
+  __shared__ __align__(16) float sum[SPLIT > 1 ? SPLIT - 1 : 1][HD];
   // The schedule reads only the lengths, written before the attention kernel let this one start.
   // This grid's end must imply the attention's: CTA (0, 0) always waits for it; others with
   // nothing to join leave at once.
@@ -784,44 +790,81 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
   const int R = G * p.m;
-  const int r = blockIdx.y * kMerge8Warps + warp;
+  const int r = blockIdx.y * ROWS + warp / SPLIT;
   const Seq8 s = seq8(p, i);
   int before, c0 = 0, c1 = 0;
-  const int T = total_units(p, i, lane, &before);
+  const int T = total_weight(p, i, lane, &before);
   const bool live = r < R && r / G < s.n;
   if (live) {
     const int Ge = min(T, p.grid);
-    const int A = before + g * s.units;
+    const int A = before + g * (s.units + p.pair_cost) + p.pair_cost;
     c0 = cta_of(T, Ge, A);
     c1 = cta_of(T, Ge, A + s.units - 1);
   }
   const bool join = live && c0 != c1;  // else written whole by the attention kernel
   if (join || (blockIdx.x == 0 && blockIdx.y == 0)) griddep_wait();
   griddep_launch();
-  if (!join) return;
-  float M = kNoMax, L = 0.f, acc[E];
+  if (!join) return;  // with SPLIT > 1 a CTA has one row, and leaves as one
+  const size_t row0 = (static_cast<size_t>(pair) + c0) * R + r;  // parts are R rows apart
+  const int parts = c1 - c0 + 1;
+  float M = kNoMax, L = 0.f;
+#pragma unroll 1
+  for (int b = 0; b < parts; b += 32) {
+    const int c = b + lane;
+    float2 ml = make_float2(kNoMax, 0.f);
+    if (c < parts) ml = *reinterpret_cast<const float2 *>(p.part_ml + (row0 + static_cast<size_t>(c) * R) * 2);
+    const float Mn = fmaxf(M, warp_max(ml.x));
+    float l = ml.y * exp2f(ml.x - Mn);
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t row = static_cast<size_t>(pair + c) * R + r;
-    const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + row * 2);
-    float v[E];
-    const float *src = p.part_o + row * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 x = *reinterpret_cast<const float2 *>(src + e);
-      v[e] = x.x;
-      v[e + 1] = x.y;
-    }
-    const float Mn = fmaxf(M, ml.x);
-    const float a_old = exp2f(M - Mn), a_new = exp2f(ml.x - Mn);
-    L = L * a_old + ml.y * a_new;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a_old + v[e] * a_new;
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L = L * exp2f(M - Mn) + l;
     M = Mn;
   }
   const float inv = 1.0f / L;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const float *src = p.part_o + row0 * HD + lane * E;
+#pragma unroll 1
+  for (int b = warp % SPLIT; b < parts; b += 4 * SPLIT) {
+    float v[4][E], w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = b + k * SPLIT;
+      w[k] = kNoMax;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+      if (c < parts) {
+        const size_t at = static_cast<size_t>(c) * R;
+        w[k] = p.part_ml[(row0 + at) * 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = *reinterpret_cast<const float2 *>(src + at * HD + e);
+          v[k][e] = x.x;
+          v[k][e + 1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = exp2f(w[k] - M);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += v[k][e] * f;
+    }
+  }
+  if constexpr (SPLIT > 1) {
+    const int sub = warp % SPLIT;
+    if (sub > 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[sub - 1][lane * E + e] = acc[e];
+    }
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int k = 0; k < SPLIT - 1; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += sum[k][lane * E + e];
+  }
   uint16_t *dst = p.o + ((static_cast<size_t>(i) * p.m + r / G) * p.Hq + g * G + r % G) * HD + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -851,15 +894,29 @@ static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
   return launch_pdl(attn8_kernel<HD, RP>, dim3(p.grid), dim3(A8Cfg<HD, RP>::THREADS), A8Cfg<HD, RP>::SMEM, s, p);
 }
 
+template <int HD, int SPLIT>
+static cudaError_t launch_merge(const Attn8Params &p, int R, cudaStream_t s) {
+  constexpr int ROWS = kMerge8Warps / SPLIT;
+  return launch_pdl(attn8_merge_kernel<HD, SPLIT>, dim3(p.nb * p.Hkv, (R + ROWS - 1) / ROWS), dim3(kMerge8Warps * 32), 0,
+                    s, p);
+}
+
+// What a pair costs besides its units, in units: the pipeline's start and end, the output rows. Even
+// ranges of units alone left the CTAs of many short pairs behind the others (64 sequences of 1024 ..
+// 8191 keys, 8 kv heads: 120 us at 0, 106 at 6, 104 at 8, 105 at 10; with 32 query rows 152, 138, 134
+// and 132).
+constexpr int kPairCost = 8;
+
 template <int HD>
-static cudaError_t launch_rows(const Attn8Params &p, cudaStream_t s) {
+static cudaError_t launch_rows(const Attn8Params &in, cudaStream_t s) {
+  Attn8Params p = in;
+  p.pair_cost = kPairCost;
   const int R = (p.Hq / p.Hkv) * p.m;
   cudaError_t e = R <= 16   ? launch_attn8<HD, 16>(p, s)
                   : R <= 32 ? launch_attn8<HD, 32>(p, s)
                             : launch_attention8_wide(p, R, s);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn8_merge_kernel<HD>, dim3(p.nb * p.Hkv, (R + kMerge8Warps - 1) / kMerge8Warps),
-                    dim3(kMerge8Warps * 32), 0, s, p);
+  return p.nb * p.Hkv * kMerge8Warps <= p.grid ? launch_merge<HD, kMerge8Warps>(p, R, s) : launch_merge<HD, 1>(p, R, s);
 }
 
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s) {

@@ -40,20 +40,24 @@ __device__ __forceinline__ long long block_of(const Attn8Params &p, int i, int g
   return static_cast<long long>(pg) * p.Hkv + g;
 }
 
-// The T units are split over G CTAs: the first T % G take one more than the others (T is below
-// 2^25: a handle's caches hold fewer than 2^31 rows).
+// A weight of T is split over G CTAs: the first T % G take one more than the others (the units are
+// below 2^25, as a handle's caches hold fewer than 2^31 rows, and T is at most 1 + pair_cost times that).
 __device__ __forceinline__ int cta_start(int T, int G, int c) { return c * (T / G) + min(c, T % G); }
 __device__ __forceinline__ int cta_of(int T, int G, int u) {
   const int q = T / G, big = (T % G) * (q + 1);
   return u < big ? u / (q + 1) : T % G + (u - big) / q;
 }
 
-// Units of the sequences before i (`before`) and of all of them, times Hkv. Warp-collective.
-__device__ __forceinline__ int total_units(const Attn8Params &p, int i, int lane, int *before) {
+// What the split counts for a pair: its units and p.pair_cost more before them, the time that a CTA
+// takes to begin a pair and to write its rows, in units.
+__device__ __forceinline__ int weight8(const Attn8Params &p, int units) { return units > 0 ? units + p.pair_cost : 0; }
+
+// Weights of the sequences before i (`before`) and of all of them, times Hkv. Warp-collective.
+__device__ __forceinline__ int total_weight(const Attn8Params &p, int i, int lane, int *before) {
   int t = 0, b = 0;
 #pragma unroll 1
   for (int s = lane; s < p.nb; s += 32) {
-    const int u = seq8(p, s).units;
+    const int u = weight8(p, seq8(p, s).units);
     t += u;
     b += s < i ? u : 0;
   }
@@ -61,41 +65,57 @@ __device__ __forceinline__ int total_units(const Attn8Params &p, int i, int lane
   return __reduce_add_sync(0xffffffffu, t) * p.Hkv;
 }
 
-// Where a CTA's range begins (pair i * Hkv + g, unit inside it) and its number of units.
-// Warp-collective.
+// Where a CTA's range begins (pair i * Hkv + g, unit inside it) and its number of units, which is 0
+// for a range inside one pair's cost. Warp-collective.
 static __device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
   int base;
-  const int T = total_units(p, 0, lane, &base);
+  const int T = total_weight(p, 0, lane, &base);
   const int Ge = min(T, p.grid);
-  int count = 0, pair = 0, unit = 0;
+  int pair = 0, unit = 0, first = 0, last = 0;  // units of all pairs before the range's ends
   if (cta < Ge) {
-    const int u0 = cta_start(T, Ge, cta);
-    count = cta_start(T, Ge, cta + 1) - u0;
+    const int w0 = cta_start(T, Ge, cta), w1 = cta_start(T, Ge, cta + 1);
+    int pairs = 0;  // with units, before this chunk of sequences
+    bool ended = false;
 #pragma unroll 1
-    for (int b = 0; b < p.nb; b += 32) {
+    for (int b = 0; b < p.nb && !ended; b += 32) {
       const int U = b + lane < p.nb ? seq8(p, b + lane).units : 0;
-      int v = p.Hkv * U;
+      const int W = weight8(p, U);
+      int v = p.Hkv * W;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + v > u0);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        const int Ul = __shfl_sync(0xffffffffu, U, l);
-        const int off = u0 - (base + __shfl_sync(0xffffffffu, v, l) - p.Hkv * Ul);
-        pair = (b + l) * p.Hkv + off / Ul;
-        unit = off % Ul;
-        break;
+      const unsigned some = __ballot_sync(0xffffffffu, U > 0);
+      const int start = base + v - p.Hkv * W;  // of the lane's sequence
+      const int units = start - p.pair_cost * (pairs + p.Hkv * __popc(some & ((1u << lane) - 1)));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int w = k == 0 ? w0 : w1;
+        const unsigned hit = __ballot_sync(0xffffffffu, start <= w && w < base + v);
+        if (hit) {
+          const int off = (w - start) / max(W, 1), in = max((w - start) % max(W, 1) - p.pair_cost, 0);
+          const int l = __ffs(hit) - 1;
+          const int at = __shfl_sync(0xffffffffu, units + off * U + in, l);
+          if (k == 0) {
+            pair = (b + l) * p.Hkv + __shfl_sync(0xffffffffu, off, l);
+            unit = __shfl_sync(0xffffffffu, in, l);
+            first = at;
+          } else {
+            last = at;
+            ended = true;
+          }
+        }
       }
       base += __shfl_sync(0xffffffffu, v, 31);
+      pairs += p.Hkv * __popc(some);
     }
+    if (!ended) last = T - p.pair_cost * pairs;  // the last range: w1 = T
   }
   if (lane == 0) {
     out[0] = pair;
     out[1] = unit;
-    out[2] = count;
+    out[2] = last - first;
   }
 }
 

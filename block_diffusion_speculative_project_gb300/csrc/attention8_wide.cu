@@ -28,7 +28,8 @@ struct WideCfg {
   static constexpr int ATOM16 = kUnit * 128;
   static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
   static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
-  static constexpr int STAGE = RHO == 1 ? 0 : 128 * 16;  // floats of a half's exchange of O between copies
+  static constexpr int STAGE = RHO == 1 ? 0 : 128 * HD / 4;  // floats of a half's exchange of O between copies
+  static_assert(RHO <= 2, "copies exchange halves");
   static constexpr int OFF_8 = 2 * TILE16;
   static constexpr int OFF_Q = OFF_8 + NS * 2 * PAIR8;
   static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     mbar_init(s_empty, 8);
     mbar_init(q8_full, 1);
     mbar_init(q8_empty, 8);
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     mbar_init(q_empty, 1);
     mbar_init(seg_bar, 8);
     mbar_init(o_free, 8);
@@ -207,6 +208,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       a.unit += 32;
       return b;
     };
+    // A segment's query rows. The first segment's are asked for before anything else.
+    auto queries = [&]() {
+      ok = segs == 0 || mbar_wait_warp(q8_empty, (segs - 1) & 1, p.max_spin);
+      if (!ok) return;
+      if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
+      __syncwarp();
+#pragma unroll 1
+      for (int r = lane; r < w.n * G; r += 32)
+        bulk_load(sQ + r * C::QPITCH,
+                  p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
+                  pol);
+      ++segs;
+    };
+    if (ok) queries();
     int blk = look_up();
     x += 32;
     int blk1 = look_up();
@@ -219,16 +234,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       if (cnt_left == 0) {  // a segment begins: its query rows
         if (j > 0) pos_next_pair(w, p, sseq);
         cnt_left = min(w.units - w.unit, nunits - j);
-        ok = segs == 0 || mbar_wait_warp(q8_empty, (segs - 1) & 1, p.max_spin);
+        if (j > 0) queries();
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
-        __syncwarp();
-#pragma unroll 1
-        for (int r = lane; r < w.n * G; r += 32)
-          bulk_load(sQ + r * C::QPITCH,
-                    p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
-                    pol);
-        ++segs;
         slot = 0;
       }
       --cnt_left;
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
     auto load_q = [&](int seg, int n) {
       bool ok = mbar_wait_warp(q8_full, seg & 1, p.max_spin);
-      if (half == 0 && seg > 0) ok = ok && mbar_wait_warp(q_empty, (seg - 1) & 1, p.max_spin);
+      if (seg > 0) ok = ok && mbar_wait_warp(q_empty, (seg - 1) & 1, p.max_spin);
       if (!ok) return -1.f;
       const uint4 *src = reinterpret_cast<const uint4 *>(sQ + r * C::QPITCH);
       const bool have = r < n * G;
@@ -464,37 +471,35 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       int ex = static_cast<int>(__float_as_uint(am) >> 23) - 127;   // -127: zero or subnormal, 128: infinite
       const bool inf = ex == 128;          // the row's outputs are NaN
       ex = max(min(ex, 127), -100);
-      if (half == 0) {
-        const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
-        tc_fence_after();
+      const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(7 - ex + 127) << 23);
+      tc_fence_after();
 #pragma unroll 1
-        for (int part = 0; part < HD / 32; ++part) {
-          uint32_t hi[8], lo[8];
+      for (int part = half * (HD / 64); part < (half + 1) * (HD / 64); ++part) {  // a half of the columns
+        uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+        for (int e = 0; e < 4; ++e) {
+          const uint4 u = have ? src[part * 4 + e] : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float2 y = make_float2(__uint_as_float(x[f] << 16) * mul, __uint_as_float(x[f] & 0xFFFF0000u) * mul);
-              const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-              const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
-              const float2 af = __half22float2(*reinterpret_cast<const __half2 *>(&ar));
-              const __nv_fp8x2_storage_t b =
-                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E4M3);
-              const int d = 2 * e + f / 2;
-              hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(a) << 16) : a;
-              lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(b) << 16) : b;
-            }
+          for (int f = 0; f < 4; ++f) {
+            const float2 y = make_float2(__uint_as_float(x[f] << 16) * mul, __uint_as_float(x[f] & 0xFFFF0000u) * mul);
+            const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
+            const float2 af = __half22float2(*reinterpret_cast<const __half2 *>(&ar));
+            const __nv_fp8x2_storage_t b =
+                __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E4M3);
+            const int d = 2 * e + f / 2;
+            hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(a) << 16) : a;
+            lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(b) << 16) : b;
           }
-          tmem_st8_raw(trow + C::Q_COL + part * 8, hi);
-          tmem_st8_raw(trow + C::Q_COL + HD / 4 + part * 8, lo);
         }
-        tmem_wait_st();
-        tc_fence_before();
+        tmem_st8_raw(trow + C::Q_COL + part * 8, hi);
+        tmem_st8_raw(trow + C::Q_COL + HD / 4 + part * 8, lo);
       }
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
-      mbar_arrive_if(q_full, lane == 0 && half == 0);
+      mbar_arrive_if(q_full, lane == 0);
       mbar_arrive_if(q8_empty, lane == 0);
       return sl2 * __uint_as_float(static_cast<uint32_t>(ex - 7 + 127) << 23);
     };
@@ -636,74 +641,62 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       const int live = n * G;            // rows that are computed
       if (half == 0 && copy == 0 && r < live && !whole)
         *reinterpret_cast<float2 *>(p.part_ml + (row0 + r) * 2) = make_float2(M, L);
-      // Each half takes its half of the columns of O_0 and O_1. With copies, a chunk of cw columns
-      // of every copy goes through shared memory, and the half's threads add the copies up.
-      uint16_t *o = p.o + (static_cast<size_t>(i) * p.m * p.Hq + g * G) * HD;
+      // Each half takes its half of the columns of O_0 and O_1. With two copies, a copy's threads
+      // write half of those, and hand their part of the others over through shared memory, which
+      // the next segment writes only after its seg_bar, past every read here.
+      uint16_t *o = p.o + ((static_cast<size_t>(i) * p.m + jq) * p.Hq + g * G + r % G) * HD;
+      float *po = p.part_o + (row0 + r) * HD;
+      auto put = [&](uint32_t col, const float (&v)[16]) {
+        if (r < live && whole) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            reinterpret_cast<uint4 *>(o + col)[e] =
+                make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                           pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+        } else if (r < live) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            reinterpret_cast<float4 *>(po + col)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        __syncwarp();
+      };
       if constexpr (RHO == 1) {
 #pragma unroll 1
-        for (int c0 = half * (HD / 2); c0 < (half + 1) * (HD / 2); c0 += 16) {
-          float ov[16], o1[16];
-          tmem_ld16(trow + C::O_COL + c0, ov);
-          tmem_ld16(trow + C::O_COL + HD + c0, o1);
+        for (uint32_t col = half * (HD / 2); col < (half + 1) * (HD / 2); col += 16) {
+          float v[16], o1[16];
+          tmem_ld16(trow + C::O_COL + col, v);
+          tmem_ld16(trow + C::O_COL + HD + col, o1);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) ov[c] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
-          if (r < live) {
-            if (whole) {
-              uint16_t *dst = o + (static_cast<size_t>(jq) * p.Hq + r % G) * HD + c0;
-#pragma unroll
-              for (int v = 0; v < 2; ++v)
-                reinterpret_cast<uint4 *>(dst)[v] =
-                    make_uint4(pack_bf16x2(ov[8 * v], ov[8 * v + 1]), pack_bf16x2(ov[8 * v + 2], ov[8 * v + 3]),
-                               pack_bf16x2(ov[8 * v + 4], ov[8 * v + 5]), pack_bf16x2(ov[8 * v + 6], ov[8 * v + 7]));
-            } else {
-              float *dst = p.part_o + (row0 + r) * HD + c0;
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                reinterpret_cast<float4 *>(dst)[v] =
-                    make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
-            }
-          }
-          __syncwarp();
+          for (int c = 0; c < 16; ++c) v[c] = v[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
+          put(col, v);
         }
       } else {
         float *stage = reinterpret_cast<float *>(smem + C::OFF_STG) + half * C::STAGE;
-        int cw = HD / 2;                 // columns per chunk: RHO * live rows of cw fit the buffer
-        while (RHO * live * cw > C::STAGE) cw >>= 1;
-        for (int c0 = 0; c0 < HD / 2 && ok; c0 += cw) {
+        auto columns = [&](uint32_t col, float (&v)[16]) {  // of this copy, both units' O
+          float o1[16];
+          tmem_ld16(trow + C::O_COL + col, v);
+          tmem_ld16(trow + C::O_COL + HD + col, o1);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = v[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
+        };
 #pragma unroll 1
-          for (int cc = 0; cc < cw; cc += 16) {
-            const uint32_t col = half * (HD / 2) + c0 + cc;
-            float ov[16], o1[16];
-            tmem_ld16(trow + C::O_COL + col, ov);
-            tmem_ld16(trow + C::O_COL + HD + col, o1);
-            if (r < live) {
-              float *to = stage + (copy * live + r) * cw;
+        for (int cc = 0; cc < HD / 4; cc += 16) {
+          float v[16];
+          columns(half * (HD / 2) + (1 - copy) * (HD / 4) + cc, v);
 #pragma unroll
-              for (int c = 0; c < 16; ++c)   // columns turned by the row: no bank conflicts
-                to[(cc + c + r) & (cw - 1)] = ov[c] * a0 + (has1 ? o1[c] * a1 : 0.f);
-            }
-            __syncwarp();
-          }
-          ok = half_sync();
-          for (int e = tl; e < live * cw / 2 && ok; e += 128) {
-            const int rr = e / (cw / 2), c = (e % (cw / 2)) * 2;
-            float v0 = 0.f, v1 = 0.f;
-#pragma unroll
-            for (int y = 0; y < RHO; ++y) {
-              const float *from = stage + (y * live + rr) * cw;
-              v0 += from[(c + rr) & (cw - 1)];
-              v1 += from[(c + 1 + rr) & (cw - 1)];
-            }
-            const int col = half * (HD / 2) + c0 + c;
-            if (whole)
-              *reinterpret_cast<uint32_t *>(o + (static_cast<size_t>(rr / G) * p.Hq + rr % G) * HD + col) =
-                  pack_bf16x2(v0, v1);
-            else
-              *reinterpret_cast<float2 *>(p.part_o + (row0 + rr) * HD + col) = make_float2(v0, v1);
-          }
-          ok = ok && half_sync();
+          for (int c = 0; c < 16; ++c) stage[((1 - copy) * (HD / 4) + cc + c) * ROWS + r] = v[c];
         }
+        ok = half_sync();
         if (!ok) break;
+#pragma unroll 1
+        for (int cc = 0; cc < HD / 4; cc += 16) {
+          const uint32_t col = half * (HD / 2) + copy * (HD / 4) + cc;
+          float v[16];
+          columns(col, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] += stage[(copy * (HD / 4) + cc + c) * ROWS + r];
+          put(col, v);
+        }
       }
       tc_fence_before();
       __syncwarp();

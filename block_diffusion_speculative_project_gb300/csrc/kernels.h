@@ -311,6 +311,7 @@ struct Attn8Params {
   float *part_o;             // [slots][G*m rows][hd] unnormalised partial outputs
   float *part_ml;            // [slots][G*m rows][2] (running maximum in log2 units, running sum)
   int nb, m, Hq, Hkv, hd, Cmax;
+  int pair_cost;             // what the split counts for a pair besides its units (set by launch_attention8)
   int max_ctx;               // caller's bound on ctx_len (larger values are reported and clamped)
   int causal;
   const int *page_table;
