@@ -10,6 +10,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdflash.so")
 
@@ -127,13 +129,14 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()   # the signatures make it a pointer
 
 
 def _stream(stream=None):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without the Stream object around it: 0.3 us of a call's 10, not 3
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # ----------------------------------------------------------------------------- lifecycle
@@ -175,7 +178,7 @@ def dflash_ctx_project(h, nb, R, hv, n_commit, relay_a, ctx_len, kcache, vcache,
                        stream=None) -> None:
     _check(LIB.dflash_ctx_project(h, nb, R, _ptr(hv), _ptr(n_commit), _ptr(relay_a), _ptr(ctx_len),
                                   _ptr(kcache), _ptr(vcache), _ptr(x0_relay), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)))
+                                  ws.nbytes, _stream(stream)))
 
 
 def dflash_ctx_project_film(h, nb, R, hv, n_commit, relay_a, relay_b, relay_y, ctx_len, kcache,
@@ -183,19 +186,19 @@ def dflash_ctx_project_film(h, nb, R, hv, n_commit, relay_a, relay_b, relay_y, c
     _check(LIB.dflash_ctx_project_film(h, nb, R, _ptr(hv), _ptr(n_commit), _ptr(relay_a),
                                        _ptr(relay_b), _ptr(relay_y), _ptr(ctx_len), _ptr(kcache),
                                        _ptr(vcache), _ptr(x0_relay), _ptr(ws),
-                                       ws.numel() * ws.element_size(), _stream(stream)))
+                                       ws.nbytes, _stream(stream)))
 
 
 def dflash_draft_block(h, nb, block_ids, x0_relay, kcache, vcache, ctx_len, max_ctx_hint,
                        out_hidden, ws, stream=None) -> None:
     _check(LIB.dflash_draft_block(h, nb, _ptr(block_ids), _ptr(x0_relay), _ptr(kcache), _ptr(vcache),
                                   _ptr(ctx_len), int(max_ctx_hint), _ptr(out_hidden), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)))
+                                  ws.nbytes, _stream(stream)))
 
 
 def dflash_lm_head_topk(h, nb, hidden, k, out_ids, out_vals, out_logits, ws, stream=None) -> None:
     _check(LIB.dflash_lm_head_topk(h, nb, _ptr(hidden), k, _ptr(out_ids), _ptr(out_vals),
-                                   _ptr(out_logits), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _ptr(out_logits), _ptr(ws), ws.nbytes,
                                    _stream(stream)))
 
 
@@ -208,7 +211,7 @@ def dflash_lm_head_topk_noalloc(h, nb, hidden, k, out_ids, out_vals, out_status=
 def dflash_attention(h, nb, layer, q, kcache, vcache, ctx_len, max_ctx_hint, out_o, ws,
                      stream=None) -> None:
     _check(LIB.dflash_attention(h, nb, layer, _ptr(q), _ptr(kcache), _ptr(vcache), _ptr(ctx_len),
-                                max_ctx_hint, _ptr(out_o), _ptr(ws), ws.numel() * ws.element_size(),
+                                max_ctx_hint, _ptr(out_o), _ptr(ws), ws.nbytes,
                                 _stream(stream)))
 
 
@@ -221,26 +224,26 @@ def dflash_kv_append(h, nb, layer, R, k, ldk, v, ldv, g_k, rotate, n_rows, ctx_l
                      stream=None) -> None:
     _check(LIB.dflash_kv_append(h, nb, layer, R, _ptr(k), ldk, _ptr(v), ldv, _ptr(g_k), rotate, _ptr(n_rows),
                                 _ptr(ctx_len), _ptr(kcache), _ptr(vcache), _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream)))
+                                ws.nbytes, _stream(stream)))
 
 
 def dflash_kv_append8(h, nb, layer, R, k, ldk, v, ldv, g_k, rotate, n_rows, ctx_len, kcache8, vcache8, kscale,
                       vscale, ws, stream=None) -> None:
     _check(LIB.dflash_kv_append8(h, nb, layer, R, _ptr(k), ldk, _ptr(v), ldv, _ptr(g_k), rotate, _ptr(n_rows),
                                  _ptr(ctx_len), _ptr(kcache8), _ptr(vcache8), _ptr(kscale), _ptr(vscale),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                 _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def dflash_attention8(h, nb, layer, m, q, kcache8, vcache8, kscale, vscale, n_rows, ctx_len, max_ctx_hint,
                       causal, out_o, ws, stream=None) -> None:
     _check(LIB.dflash_attention8(h, nb, layer, m, _ptr(q), _ptr(kcache8), _ptr(vcache8), _ptr(kscale),
                                  _ptr(vscale), _ptr(n_rows), _ptr(ctx_len), max_ctx_hint, causal, _ptr(out_o),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+                                 _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def dflash_topk(h, rows, cols, logits, k, out_ids, out_vals, ws=None, stream=None) -> None:
     _check(LIB.dflash_topk(h, rows, cols, _ptr(logits), k, _ptr(out_ids), _ptr(out_vals), _ptr(ws),
-                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+                           0 if ws is None else ws.nbytes, _stream(stream)))
 
 
 def dflash_accept(h, nb, draft, target, out_tau, out_bonus, stream=None) -> None:
@@ -257,7 +260,7 @@ def dflash_sample(h, rows, logits, temperature, seed, row0, out_ids, out_lse, ou
                   stream=None) -> None:
     _check(LIB.dflash_sample(h, rows, _ptr(logits), float(temperature), int(seed), int(row0),
                              _ptr(out_ids), _ptr(out_lse), _ptr(out_logq), _ptr(ws),
-                             ws.numel() * ws.element_size(), _stream(stream)))
+                             ws.nbytes, _stream(stream)))
 
 
 def dflash_lm_head_sample(h, nb, hidden, temperature, seed, out_cand, out_lse, out_logq, out_logits,
@@ -265,7 +268,7 @@ def dflash_lm_head_sample(h, nb, hidden, temperature, seed, out_cand, out_lse, o
     _check(LIB.dflash_lm_head_sample(h, nb, _ptr(hidden), float(temperature), int(seed),
                                      _ptr(out_cand), _ptr(out_lse), _ptr(out_logq), _ptr(out_logits),
                                      int(k), _ptr(out_ids), _ptr(out_vals), _ptr(ws),
-                                     ws.numel() * ws.element_size(), _stream(stream)))
+                                     ws.nbytes, _stream(stream)))
 
 
 def dflash_draw_gumbel(n, seed, stream_id, row, out_u, out_g, stream=None) -> None:
@@ -278,14 +281,14 @@ def dflash_verify_sample(h, nb, draft_logits, draft_lse, cand, target_logits, te
     _check(LIB.dflash_verify_sample(h, nb, _ptr(draft_logits), _ptr(draft_lse), _ptr(cand),
                                     _ptr(target_logits), float(temperature), int(seed),
                                     _ptr(out_tau), _ptr(out_token), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _stream(stream)))
+                                    ws.nbytes, _stream(stream)))
 
 
 def dflash2_select_sample(h, nb, k, topk_ids, topk_vals, hidden, block_ids, temperature, seed,
                           out_path, out_walk_logq, ws, stream=None) -> None:
     _check(LIB.dflash2_select_sample(h, nb, k, _ptr(topk_ids), _ptr(topk_vals), _ptr(hidden),
                                      _ptr(block_ids), float(temperature), int(seed), _ptr(out_path),
-                                     _ptr(out_walk_logq), _ptr(ws), ws.numel() * ws.element_size(),
+                                     _ptr(out_walk_logq), _ptr(ws), ws.nbytes,
                                      _stream(stream)))
 
 
@@ -294,7 +297,7 @@ def dflash_verify_sample_walk(h, nb, k, cand_ids, walk_logq, path, target_logits
     _check(LIB.dflash_verify_sample_walk(h, nb, k, _ptr(cand_ids), _ptr(walk_logq), _ptr(path),
                                          _ptr(target_logits), float(temperature), int(seed),
                                          _ptr(out_tau), _ptr(out_token), _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream(stream)))
+                                         ws.nbytes, _stream(stream)))
 
 
 def dflash_recall_at_k(h, nb, k, cand_ids, target, hits, eligible, stream=None) -> None:
@@ -303,11 +306,11 @@ def dflash_recall_at_k(h, nb, k, cand_ids, target, hits, eligible, stream=None) 
 
 
 def dflash2_conv(h, layer, which, nb, x, ws, stream=None) -> None:
-    _check(LIB.dflash2_conv(h, layer, which, nb, _ptr(x), _ptr(ws), ws.numel() * ws.element_size(),
+    _check(LIB.dflash2_conv(h, layer, which, nb, _ptr(x), _ptr(ws), ws.nbytes,
                             _stream(stream)))
 
 
 def dflash2_select(h, nb, k, topk_ids, topk_vals, hidden, block_ids, out_path, ws, stream=None) -> None:
     _check(LIB.dflash2_select(h, nb, k, _ptr(topk_ids), _ptr(topk_vals), _ptr(hidden), _ptr(block_ids),
-                              _ptr(out_path), _ptr(ws), ws.numel() * ws.element_size(),
+                              _ptr(out_path), _ptr(ws), ws.nbytes,
                               _stream(stream)))
