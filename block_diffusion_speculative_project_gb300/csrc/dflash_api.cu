@@ -1198,7 +1198,7 @@ int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, const void *k
   p.dst8[1] = static_cast<uint8_t *>(vcache8) + blocks * kPageRows * c.hd;
   p.scale[0] = kscale + blocks;
   p.scale[1] = vscale + blocks;
-  DF_CUDA(launch_kv_append8(p, stream));
+  DF_CUDA(launch_kv_append8(p, h->num_sms, stream));
   return DFLASH_OK;
 }
 

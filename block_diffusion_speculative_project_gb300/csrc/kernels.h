@@ -293,11 +293,11 @@ struct KvRowsParams {
   int pages_per_seq, num_pages;
   float eps;
   int *status;
-  int warps_per_row, iters;     // work split, set by the launch
+  int cta_rows, iters, iters_v; // work split, set by the launch
 };
 cudaError_t launch_qk_norm_rope(KvRowsParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_append(KvRowsParams &p, int num_sms, cudaStream_t s);
-cudaError_t launch_kv_append8(const KvRowsParams &p, cudaStream_t s);
+cudaError_t launch_kv_append8(KvRowsParams &p, int num_sms, cudaStream_t s);
 
 // Attention of m query rows per sequence over an 8-bit cache (attention8.cu).
 struct Attn8Params {

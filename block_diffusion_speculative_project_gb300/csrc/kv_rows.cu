@@ -22,24 +22,58 @@ namespace df {
 
 namespace {
 
+// Sine and cosine of pos * turn 2^-64 turns: the nearest quarter turn comes off in fixed point, exactly, and
+// Taylor's polynomials give the rest of at most pi/4 (left out: x^11/11! < 2^-28 and x^12/12! < 2^-33). The
+// angle is the sum x + xl, and each polynomial adds its first term last, so both results are little
+// more than their last rounding off. In the 8-bit caches a value rounded the other way is off by a whole
+// step: the fast sine's 2^-21 showed there.
 __device__ __forceinline__ void turn_sincos(long long pos, unsigned long long turn, float *sn, float *cs) {
-  // the upper 32 of the fraction's 64 bits, as a signed number of 2^-32 turns in [-1/2, 1/2)
-  const int t = static_cast<int>((static_cast<unsigned long long>(pos) * turn) >> 32);
-  __sincosf(static_cast<float>(t) * 1.4629180792671596e-9f, sn, cs);  // 2 pi / 2^32
+  constexpr double kStep = 1.4629180792671596e-9;  // 2 pi / 2^32
+  constexpr float kHi = static_cast<float>(kStep), kLo = static_cast<float>(kStep - kHi);
+  const uint32_t t = static_cast<uint32_t>((static_cast<unsigned long long>(pos) * turn + 0x80000000u) >> 32);
+  const uint32_t quarter = (t + 0x20000000u) >> 30;
+  const int rest = static_cast<int>(t - (quarter << 30));  // 2^-32 turns
+  const float f = static_cast<float>(rest);
+  const float x = f * kHi;
+  const float xl = fmaf(f, kHi, -x) + fmaf(f, kLo, static_cast<float>(rest - static_cast<int>(f)) * kHi);
+  const float y = x * x;
+  const float ps = fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6);
+  const float pc =
+      fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f);
+  const float s = x + fmaf(xl, fmaf(-0.5f, y, 1.f), x * y * ps);
+  const float c = 1.f + fmaf(-xl, x, y * pc);
+  const bool odd = quarter & 1;
+  const uint32_t us = __float_as_uint(odd ? c : s), uc = __float_as_uint(odd ? s : c);
+  *sn = __uint_as_float(us ^ ((quarter & 2) << 30));
+  *cs = __uint_as_float(uc ^ (((quarter + 1) & 2) << 30));
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Two bf16 values as floats.
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// W consecutive 32-bit words, CW (1, 2 or 4) loaded at once.
+template <int W, int CW>
+__device__ __forceinline__ void load_runs(const void *from, uint32_t (&w)[W]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  for (int q = 0; q < W; q += CW) {
+    const uint32_t *at = static_cast<const uint32_t *>(from) + q;
+    if constexpr (CW == 1) {
+      w[q] = *at;
+    } else if constexpr (CW == 2) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(at);
+      w[q] = u.x, w[q + 1] = u.y;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4 *>(at);
+      w[q] = u.x, w[q + 1] = u.y, w[q + 2] = u.z, w[q + 3] = u.w;
+    }
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+// Two floats to two e4m3 bytes.
+__device__ __forceinline__ uint32_t e4m3x2(float2 v) {
+  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
 // New rows of sequence i (n_rows clipped to [0, R]; every row without n_rows).
@@ -57,279 +91,380 @@ __device__ __forceinline__ void report_lengths(const KvRowsParams &p, int i) {
 
 }  // namespace
 
-// One warp takes one row and `iters` groups of heads (32 / TPH heads each); a head is TPH = hd/16
-// threads, each with 8 values of the lower half and the 8 they rotate with. The angles of
-// a lane are the same for every head of the row: they are computed once. APPEND writes the
-// first tensor's rows (keys) and the second's (values) into the caches.
+// A CTA has four warps: `cta_rows` (1, 2 or 4) rows with 4 / cta_rows warps each, and a warp `iters` groups
+// of heads (32 / TPH heads each). A head is TPH = hd/16 threads, each with 8 values of the lower half and
+// the 8 they rotate with. The CTA computes its rows' angles once; gains and angles meet in four
+// factors per pair of values, the same for every head of a tensor, so that a value costs two
+// products of packed floats and the row's 1 / norm. APPEND writes the first tensor's rows (keys) and the
+// second's (values) into the caches.
+// Memory bounds it: 8191 rows of 40 heads take 29.9 us, 168 MB at 5.6 TB/s, and 2 x 8189 rows appended to
+// 8 + 8 heads 24.1 us, 134 MB at 5.6 TB/s. Groups go in batches of four, all loads before the first
+// store: two at a time took 32.5 us, and each group's loads right after its predecessor's stores 35.8.
+// Registers for five CTAs a SM: six spill (41.7 us). Single tokens are a launch and four dependent
+// loads: 2.7 us.
+constexpr int kRowBatch = 4;  // groups whose loads are in flight together
+
 template <int HD, bool APPEND>
-__global__ void __launch_bounds__(256) kv_rows_kernel(const __grid_constant__ KvRowsParams p) {
+__global__ void __launch_bounds__(128, 5) kv_rows_kernel(const __grid_constant__ KvRowsParams p) {
   constexpr int TPH = HD / 16;
   constexpr int HPW = 32 / TPH;
+  __shared__ __align__(16) float angles[4][2][HD / 2];  // of the CTA's rows: cosines, sines
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const long long row = w / p.warps_per_row;
-  const int part = static_cast<int>(w % p.warps_per_row);
-  if (row >= static_cast<long long>(p.nb) * p.R) return;
-  const int i = static_cast<int>(row / p.R);
-  const int j = static_cast<int>(row % p.R);
-  const long long pos = static_cast<long long>(p.ctx_len[i]) + j;
-  long long crow = 0;  // APPEND: cache row of head 0, and the rows from one head to the next
-  long long chead = 0;
-  if (APPEND) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_row = 4 / p.cta_rows;  // warps
+  const uint32_t rows = static_cast<uint32_t>(p.nb) * p.R;
+  const uint32_t row0 = blockIdx.x * p.cta_rows;
+  const uint32_t row = row0 + warp / per_row;
+  const int part = blockIdx.y * per_row + warp % per_row;
+  const int total = p.heads[0] + p.heads[1];
+  const int d0 = (lane % TPH) * 8;
+  const int h0 = part * p.iters * HPW + lane / TPH;
+  bool live = row < rows && part * p.iters * HPW < total;
+  const int i = live ? row / p.R : 0;
+  const int j = row - i * p.R;
+  long long crow = 0, chead = 0;  // APPEND: cache row of head 0, and the rows from one head to the next
+  if (APPEND && live) {
+    const long long pos = static_cast<long long>(p.ctx_len[i]) + j;
     if (j == 0 && part == 0 && lane == 0) report_lengths(p, i);
-    if (j >= new_rows(p.n_rows, i, p.R) || pos < 0 || pos >= p.Cmax) return;
-    if (p.page_table) {
+    live = j < new_rows(p.n_rows, i, p.R) && pos >= 0 && pos < p.Cmax;
+    if (live && p.page_table) {
       const int pg = p.page_table[static_cast<long long>(i) * p.pages_per_seq + pos / kPageRows];
-      if (pg < 0 || pg >= p.num_pages) {
-        if (lane == 0) flag_status(p.status, kStatusCheck);
-        return;
-      }
       crow = static_cast<long long>(pg) * p.heads[0] * kPageRows + pos % kPageRows;
       chead = kPageRows;
+      if (pg < 0 || pg >= p.num_pages) {
+        if (lane == 0) flag_status(p.status, kStatusCheck);
+        live = false;
+      }
     } else {
       crow = static_cast<long long>(i) * p.heads[0] * p.Cmax + pos;
       chead = p.Cmax;
     }
   }
-  const int d0 = (lane % TPH) * 8;
-  float sn[8], cs[8];
+  uint4 ua[kRowBatch], ub[kRowBatch];
+  auto load = [&](int it0) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    sn[e] = 0.f;
-    cs[e] = 1.f;
-    if (p.rotate) turn_sincos(pos, p.turn[d0 + e], &sn[e], &cs[e]);
-  }
-  const int total = p.heads[0] + p.heads[1];
-  const int h0 = part * p.iters * HPW + lane / TPH;
-#pragma unroll 4
-  for (int it = 0; it < p.iters; ++it) {
-    const int hh = h0 + it * HPW;
-    const bool live = hh < total;
-    const int t = live && hh >= p.heads[0] ? 1 : 0;
-    const int head = t ? hh - p.heads[0] : hh;
-    const uint16_t *src = p.src[t] + row * p.ld[t] + static_cast<long long>(head) * HD + d0;
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (live) {
-      ua = *reinterpret_cast<const uint4 *>(src);
-      ub = *reinterpret_cast<const uint4 *>(src + HD / 2);
+    for (int k = 0; k < kRowBatch; ++k) {
+      const int hh = h0 + (it0 + k) * HPW;
+      ua[k] = ub[k] = make_uint4(0, 0, 0, 0);
+      if (live && it0 + k < p.iters && hh < total) {
+        const int t = hh >= p.heads[0] ? 1 : 0;
+        const uint16_t *src = p.src[t] + row * p.ld[t] + static_cast<long long>(t ? hh - p.heads[0] : hh) * HD + d0;
+        ua[k] = *reinterpret_cast<const uint4 *>(src);
+        ub[k] = *reinterpret_cast<const uint4 *>(src + HD / 2);
+      }
     }
-    const bool plain = APPEND && t == 1;  // values go as they are
-    if (__any_sync(0xffffffffu, !plain)) {
-      float a[8], b[8];
-      unpack8(ua, a);
-      unpack8(ub, b);
-      if (p.g[0] || p.g[1]) {
-        float ss = 0.f;
+  };
+  load(0);
+  for (int e = threadIdx.x; e < p.cta_rows * (HD / 2); e += 128) {
+    const uint32_t r = row0 + e / (HD / 2);
+    const int d = e % (HD / 2);
+    float sn = 0.f, cs = 1.f;
+    if (p.rotate && r < rows) {
+      const uint32_t s = r / p.R;
+      turn_sincos(static_cast<long long>(p.ctx_len[s]) + (r - s * p.R), p.turn[d], &sn, &cs);
+    }
+    angles[e / (HD / 2)][0][d] = cs;
+    angles[e / (HD / 2)][1][d] = sn;
+  }
+  __syncthreads();
+  if (!live) return;
+  int cur = -1;                            // tensor whose factors the lane holds
+  float2 fa[4], fb[4], fc[4], fd[4];       // a' = a fa + b fb,  b' = b fc + a fd
+#pragma unroll 1
+  for (int it0 = 0; it0 < p.iters; it0 += kRowBatch) {
+    if (it0 > 0) load(it0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+    for (int k = 0; k < kRowBatch; ++k) {
+      const int hh = h0 + (it0 + k) * HPW;
+      const bool have = it0 + k < p.iters && hh < total;
+      const int t = have && hh >= p.heads[0] ? 1 : 0;
+      const bool plain = !have || (APPEND && t == 1);  // values go as they are
+      if (__any_sync(0xffffffffu, !plain)) {
+        if (!plain && t != cur) {
+          cur = t;
+          const float *at = angles[warp / per_row][0] + d0;
+          uint32_t ga[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, gb[4];  // ones
+          if (p.g[t]) load_runs<4, 4>(p.g[t] + d0, ga);
 #pragma unroll
-        for (int o = TPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const uint16_t *g = p.g[t];
-        if (g && !plain) {
-          const float inv = rsqrtf(ss * (1.f / HD) + p.eps);
-          float ga[8], gb[8];
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(g + d0)), ga);
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(g + d0 + HD / 2)), gb);
+          for (int e = 0; e < 4; ++e) gb[e] = ga[e];
+          if (p.g[t]) load_runs<4, 4>(p.g[t] + d0 + HD / 2, gb);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] *= inv * ga[e];
-            b[e] *= inv * gb[e];
+          for (int e = 0; e < 4; ++e) {
+            const float2 cs = reinterpret_cast<const float2 *>(at)[e];
+            const float2 sn = reinterpret_cast<const float2 *>(at + HD / 2)[e];
+            const float2 a = unpack2(ga[e]), b = unpack2(gb[e]);
+            fa[e] = mul2(a, cs);
+            fb[e] = mul2(b, make_float2(-sn.x, -sn.y));
+            fc[e] = mul2(b, cs);
+            fd[e] = mul2(a, sn);
           }
         }
-      }
-      if (!plain) {
-        float ra[8], rb[8];
+        const uint32_t wa[4] = {ua[k].x, ua[k].y, ua[k].z, ua[k].w}, wb[4] = {ub[k].x, ub[k].y, ub[k].z, ub[k].w};
+        float2 a[4], b[4], ss = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ra[e] = a[e] * cs[e] - b[e] * sn[e];
-          rb[e] = b[e] * cs[e] + a[e] * sn[e];
+        for (int e = 0; e < 4; ++e) {
+          a[e] = unpack2(wa[e]);
+          b[e] = unpack2(wb[e]);
+          ss = fma2(a[e], a[e], fma2(b[e], b[e], ss));
         }
-        ua = pack8(ra);
-        ub = pack8(rb);
+        float inv = 1.f;
+        if (p.g[0] || p.g[1]) {
+          float sum = ss.x + ss.y;
+#pragma unroll
+          for (int o = TPH / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (p.g[t]) inv = rsqrtf(sum * (1.f / HD) + p.eps);
+        }
+        if (!plain) {
+          const float2 inv2 = make_float2(inv, inv);
+          uint32_t ra[4], rb[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = mul2(a[e], inv2), y = mul2(b[e], inv2);
+            const float2 u = fma2(y, fb[e], mul2(x, fa[e])), v = fma2(x, fd[e], mul2(y, fc[e]));
+            ra[e] = pack_bf16x2(u.x, u.y);
+            rb[e] = pack_bf16x2(v.x, v.y);
+          }
+          ua[k] = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+          ub[k] = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+        }
+      }
+      if (have) {
+        const int head = t ? hh - p.heads[0] : hh;
+        uint16_t *dst = APPEND ? p.dst[t] + (crow + head * chead) * HD + d0
+                               : p.dst[t] + (static_cast<long long>(row) * p.heads[t] + head) * HD + d0;
+        *reinterpret_cast<uint4 *>(dst) = ua[k];
+        *reinterpret_cast<uint4 *>(dst + HD / 2) = ub[k];
       }
     }
-    if (!live) continue;
-    uint16_t *dst;
-    if (APPEND)
-      dst = p.dst[t] + (crow + head * chead) * HD + d0;
-    else
-      dst = p.dst[t] + (row * p.heads[t] + head) * HD + d0;
-    *reinterpret_cast<uint4 *>(dst) = ua;
-    *reinterpret_cast<uint4 *>(dst + HD / 2) = ub;
   }
 }
 
-// Append in 8 bits: one CTA per (64-row block of a sequence, kv head, keys or values), four
-// threads per row, each with HD/8 values of either half. The block's scale is the power of two
-// that takes its largest new value to at most 448 (e4m3's largest), and not less than the
-// scale of the rows that stay; those are rounded again only when the scale grows. A power of
-// two loses nothing against amax / 448: e4m3 is a floating format, and rescaling rows by a
-// power of two is exact but for values that become subnormal.
+// Append in 8 bits: SLOTS * TPR threads per (64-row block of a sequence, keys or values), which go through
+// `iters` kv heads; TPR threads per new row, each with HD / 2 / TPR values of either half, whose angles and
+// gains serve every head. The block's scale is the power of two that takes its largest new value to at
+// most 448 (e4m3's largest), and not less than the scale of the rows that stay; those are rounded
+// again only when the scale grows. A power of two loses nothing against amax / 448: e4m3 is a
+// floating format, and rescaling rows by a power of two is exact but for values that become
+// subnormal. It also joins 1 / norm exactly, so a value costs one product for both.
+// Two prompts of up to 8189 rows (67 MB) take 15.0 us, 4.5 TB/s: a step from head to head is a chain of
+// norm, maximum over the block and scale, which the four warps a scheduler has room for hide in part. With
+// the angles in registers, which leaves room for no more, it was 15.6; with the heads' values
+// asked for two to four steps ahead through shared memory 15 to 16.7.
 constexpr int kScaleExpMin = -100, kScaleExpMax = 119;
 
-template <int HD>
-__global__ void __launch_bounds__(256) kv_append8_kernel(const __grid_constant__ KvRowsParams p) {
-  constexpr int E = HD / 8;  // values of one half per thread
+template <int HD, int SLOTS, int TPR>
+__global__ void __launch_bounds__(SLOTS *TPR < 128 ? 128 : SLOTS * TPR, SLOTS * TPR > 128 ? 2 : 4)
+    kv_append8_kernel(const __grid_constant__ KvRowsParams p) {
+  constexpr int GT = SLOTS * TPR;           // threads that share a block: a warp, or the CTA
+  constexpr int GROUPS = GT < 128 ? 128 / GT : 1;
+  constexpr int E = HD / 2 / TPR, W = E / 2;  // values of one half per thread, and words
+  constexpr int CW = W < 4 ? W : 4;           // words loaded at once
+  static_assert(GT == 32 || GT >= 128, "a warp or a CTA");
   griddep_wait();
   griddep_launch();
-  __shared__ float red[8];
-  const int i = blockIdx.z;
-  const int head = blockIdx.y >> 1, t = blockIdx.y & 1;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_lengths(p, i);
+  __shared__ float red[2][GT / 32];
+  const int i = blockIdx.y;
+  const int tid = threadIdx.x % GT;
+  // keys first: their groups have the most to do
+  const int group = blockIdx.z * GROUPS + threadIdx.x / GT, keys = (p.heads[0] + p.iters - 1) / p.iters;
+  const int t = group >= keys ? 1 : 0, per = t ? p.iters_v : p.iters;
+  const int h0 = (group - t * keys) * per, h1 = min(h0 + per, p.heads[0]);
+  if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) report_lengths(p, i);
   const int n = new_rows(p.n_rows, i, p.R);
   const int c0 = p.ctx_len[i];
-  if (c0 < 0 || n == 0) return;
+  if (c0 < 0 || n == 0 || h0 >= h1) return;
   const int hi = static_cast<int>(min(static_cast<long long>(c0) + n, static_cast<long long>(p.Cmax)));
   const int blk = c0 / kPageRows + blockIdx.x;
-  if (blk * kPageRows >= hi) return;
-  long long block;  // index of this (block, head) in the cache, in blocks of 64 rows
+  const int row0 = blk * kPageRows;
+  if (row0 >= hi) return;
+  long long block, bhead;  // (block, head 0) in the cache, in blocks of 64 rows, and the step to the next head
   if (p.page_table) {
     const int pg = p.page_table[static_cast<long long>(i) * p.pages_per_seq + blk];
     if (pg < 0 || pg >= p.num_pages) {
-      if (threadIdx.x == 0) flag_status(p.status, kStatusCheck);
+      if (tid == 0) flag_status(p.status, kStatusCheck);
       return;
     }
-    block = static_cast<long long>(pg) * p.heads[0] + head;
+    block = static_cast<long long>(pg) * p.heads[0];
+    bhead = 1;
   } else {
-    block = (static_cast<long long>(i) * p.heads[0] + head) * (p.Cmax / kPageRows) + blk;
+    bhead = p.Cmax / kPageRows;
+    block = static_cast<long long>(i) * p.heads[0] * bhead + blk;
   }
-  const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
-  const int pos = blk * kPageRows + r;
-  const bool fresh = pos >= c0 && pos < hi;
-  const bool keeps = blk * kPageRows < c0;  // rows of earlier calls lie in this block
+  const int part = tid % TPR, slot = tid / TPR;
+  const int kept = max(c0 - row0, 0);       // rows of earlier calls in this block
+  const int pos = row0 + kept + slot;
+  const bool fresh = pos < min(hi, row0 + kPageRows);
   const int d0 = part * E;
-  float *scale_at = p.scale[t] + block;
-  const float s_old = keeps ? *scale_at : 0.f;
-  float a[E], b[E];
+  const uint16_t *src = p.src[t] + (static_cast<long long>(i) * p.R + (pos - c0)) * p.ld[t] + d0;
+  const int lane = threadIdx.x & 31;
+  float scales = 0.f;                       // lane l: scale of head h0 + l's kept rows
+  if (kept > 0 && h0 + lane < h1) scales = p.scale[t][block + (h0 + lane) * bhead];
+  uint32_t na[W], nb[W];                    // the next head's values
+  auto load = [&](int head) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) a[e] = b[e] = 0.f;
-  if (fresh) {
-    const long long row = static_cast<long long>(i) * p.R + (pos - c0);
-    const uint16_t *src = p.src[t] + row * p.ld[t] + static_cast<long long>(head) * HD + d0;
+    for (int e = 0; e < W; ++e) na[e] = nb[e] = 0u;
+    if (fresh && head < h1) {
+      load_runs<W, CW>(src + static_cast<long long>(head) * HD, na);
+      load_runs<W, CW>(src + static_cast<long long>(head) * HD + HD / 2, nb);
+    }
+  };
+  load(h0);
+  const bool norm = t == 0 && p.g[0], rotate = t == 0 && p.rotate;
+  constexpr bool TAB = GT > 128;            // a thread's own angles in shared memory, to spare it the registers
+  __shared__ float4 tab[TAB ? W : 1][TAB ? GT : 1];
+  float2 cs[W], sn[W];
+  uint32_t ga[W], gb[W];
+  if (rotate) {
 #pragma unroll
-    for (int q = 0; q < E / 8; ++q) {
-      float x[8];
-      unpack8(*reinterpret_cast<const uint4 *>(src + 8 * q), x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a[8 * q + e] = x[e];
-      unpack8(*reinterpret_cast<const uint4 *>(src + HD / 2 + 8 * q), x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) b[8 * q + e] = x[e];
+    for (int e = 0; e < W; ++e) {
+      turn_sincos(pos, p.turn[d0 + 2 * e], &sn[e].x, &cs[e].x);
+      turn_sincos(pos, p.turn[d0 + 2 * e + 1], &sn[e].y, &cs[e].y);
+      if constexpr (TAB) tab[e][tid] = make_float4(cs[e].x, cs[e].y, sn[e].x, sn[e].y);
     }
   }
-  if (t == 0) {
-    if (p.g[0]) {
-      float ss = 0.f;
+  if (norm) {
+    load_runs<W, CW>(p.g[0] + d0, ga);
+    load_runs<W, CW>(p.g[0] + d0 + HD / 2, gb);
+  }
+#pragma unroll 1
+  for (int head = h0; head < h1; ++head) {
+    float2 a[W], b[W];
 #pragma unroll
-      for (int e = 0; e < E; ++e) ss += a[e] * a[e] + b[e] * b[e];
-      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-      const float inv = rsqrtf(ss * (1.f / HD) + p.eps);
+    for (int e = 0; e < W; ++e) {
+      a[e] = unpack2(na[e]);
+      b[e] = unpack2(nb[e]);
+    }
+    const float s_old = __shfl_sync(0xffffffffu, scales, head - h0);
+    load(head + 1);
+    float inv = 1.f;                        // of the row, joined to its values below
+    if (norm) {
+      float2 sa = make_float2(0.f, 0.f), sb = sa;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        a[e] *= inv * __uint_as_float(static_cast<uint32_t>(p.g[0][d0 + e]) << 16);
-        b[e] *= inv * __uint_as_float(static_cast<uint32_t>(p.g[0][d0 + HD / 2 + e]) << 16);
+      for (int e = 0; e < W; ++e) {
+        sa = fma2(a[e], a[e], sa);
+        sb = fma2(b[e], b[e], sb);
+      }
+      float ss = (sa.x + sa.y) + (sb.x + sb.y);
+#pragma unroll
+      for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      inv = __frsqrt_rn(ss * (1.f / HD) + p.eps);  // rsqrtf may be two steps off: e4m3 roundings would show it
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        a[e] = mul2(a[e], unpack2(ga[e]));
+        b[e] = mul2(b[e], unpack2(gb[e]));
       }
     }
-    if (p.rotate) {
+    if (rotate) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float sn, cs;
-        turn_sincos(pos, p.turn[d0 + e], &sn, &cs);
-        const float x = a[e], y = b[e];
-        a[e] = x * cs - y * sn;
-        b[e] = y * cs + x * sn;
-      }
-    }
-  }
-  // largest finite new value of the block (rows that are not new hold zeros)
-  float m = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float x = fabsf(a[e]), y = fabsf(b[e]);
-    m = fmaxf(m, fmaxf(x <= FLT_MAX ? x : 0.f, y <= FLT_MAX ? y : 0.f));
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-  m = red[0];
-#pragma unroll
-  for (int q = 1; q < 8; ++q) m = fmaxf(m, red[q]);
-  // smallest e with m <= 448 * 2^e = 1.75 * 2^(e + 8)
-  const uint32_t mb = __float_as_uint(m);
-  int ex = static_cast<int>(mb >> 23) - 127 - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  ex = max(kScaleExpMin, min(ex, kScaleExpMax));
-  const float s = fmaxf(__uint_as_float(static_cast<uint32_t>(ex + 127) << 23), s_old);
-  uint8_t *dst = p.dst8[t] + block * (kPageRows * HD) + r * HD + d0;
-  if (fresh) {
-    const float inv = 1.f / s;
-    uint32_t qa[E / 4], qb[E / 4];
-#pragma unroll
-    for (int q = 0; q < E / 4; ++q) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a[4 * q] * inv, a[4 * q + 1] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      const uint32_t up = __nv_cvt_float2_to_fp8x2(make_float2(a[4 * q + 2] * inv, a[4 * q + 3] * inv),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      qa[q] = lo | (up << 16);
-      const uint32_t lo2 = __nv_cvt_float2_to_fp8x2(make_float2(b[4 * q] * inv, b[4 * q + 1] * inv),
-                                                    __NV_SATFINITE, __NV_E4M3);
-      const uint32_t up2 = __nv_cvt_float2_to_fp8x2(make_float2(b[4 * q + 2] * inv, b[4 * q + 3] * inv),
-                                                    __NV_SATFINITE, __NV_E4M3);
-      qb[q] = lo2 | (up2 << 16);
-    }
-    if constexpr (E == 16) {
-      *reinterpret_cast<uint4 *>(dst) = make_uint4(qa[0], qa[1], qa[2], qa[3]);
-      *reinterpret_cast<uint4 *>(dst + HD / 2) = make_uint4(qb[0], qb[1], qb[2], qb[3]);
-    } else {
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(qa[0], qa[1]);
-      *reinterpret_cast<uint2 *>(dst + HD / 2) = make_uint2(qb[0], qb[1]);
-    }
-  } else if (keeps && pos < c0 && s > s_old) {
-    const float ratio = s_old / s;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t *at = reinterpret_cast<uint32_t *>(dst + half * (HD / 2));
-#pragma unroll
-      for (int q = 0; q < E / 4; ++q) {
-        const uint32_t v = at[q];
-        uint32_t out = 0;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-              static_cast<__nv_fp8x2_storage_t>((v >> (16 * x)) & 0xFFFFu), __NV_E4M3);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-          out |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f.x * ratio, f.y * ratio),
-                                                                __NV_SATFINITE, __NV_E4M3))
-                 << (16 * x);
+      for (int e = 0; e < W; ++e) {
+        const float2 x = a[e], y = b[e];
+        if constexpr (TAB) {
+          const float4 f = tab[e][tid];
+          cs[e] = make_float2(f.x, f.y);
+          sn[e] = make_float2(f.z, f.w);
         }
-        at[q] = out;
+        a[e] = fma2(y, make_float2(-sn[e].x, -sn[e].y), mul2(x, cs[e]));
+        b[e] = fma2(x, sn[e], mul2(y, cs[e]));
       }
     }
+    // largest finite new value of the block (slots without a row hold zeros); a NaN is no maximum
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      m = fmaxf(fmaxf(m, fabsf(a[e].x)), fabsf(a[e].y));
+      m = fmaxf(fmaxf(m, fabsf(b[e].x)), fabsf(b[e].y));
+    }
+    if (m > FLT_MAX) {
+      m = 0.f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const float v[4] = {fabsf(a[e].x), fabsf(a[e].y), fabsf(b[e].x), fabsf(b[e].y)};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) m = fmaxf(m, v[x] <= FLT_MAX ? v[x] : 0.f);
+      }
+    }
+    m *= inv;                               // rounding keeps the order: the largest of the products
+    m = m <= FLT_MAX ? m : 0.f;
+    m = warp_max(m);
+    if constexpr (GT > 32) {
+      float *to = red[(head - h0) & 1];     // two, so that one barrier a head is enough
+      if ((tid & 31) == 0) to[tid >> 5] = m;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < GT / 32; ++q) m = fmaxf(m, to[q]);
+    }
+    // smallest e with m <= 448 * 2^e = 1.75 * 2^(e + 8)
+    const uint32_t mb = __float_as_uint(m);
+    int ex = static_cast<int>(mb >> 23) - 127 - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    ex = max(kScaleExpMin, min(ex, kScaleExpMax));
+    const float s = fmaxf(__uint_as_float(static_cast<uint32_t>(ex + 127) << 23), s_old);
+    const long long bi = block + head * bhead;
+    uint8_t *dst = p.dst8[t] + bi * (kPageRows * HD) + d0;
+    if (fresh) {
+      const float f = inv * (1.f / s);
+      const float2 f2 = make_float2(f, f);
+      uint8_t *to = dst + (pos - row0) * HD;
+      if constexpr (W == 1) {
+        *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(e4m3x2(mul2(a[0], f2)));
+        *reinterpret_cast<uint16_t *>(to + HD / 2) = static_cast<uint16_t>(e4m3x2(mul2(b[0], f2)));
+      } else {
+        uint32_t qa[W / 2], qb[W / 2];
+#pragma unroll
+        for (int q = 0; q < W / 2; ++q) {
+          qa[q] = e4m3x2(mul2(a[2 * q], f2)) | (e4m3x2(mul2(a[2 * q + 1], f2)) << 16);
+          qb[q] = e4m3x2(mul2(b[2 * q], f2)) | (e4m3x2(mul2(b[2 * q + 1], f2)) << 16);
+        }
+        if constexpr (W == 2) {
+          *reinterpret_cast<uint32_t *>(to) = qa[0];
+          *reinterpret_cast<uint32_t *>(to + HD / 2) = qb[0];
+        } else if constexpr (W == 4) {
+          *reinterpret_cast<uint2 *>(to) = make_uint2(qa[0], qa[1]);
+          *reinterpret_cast<uint2 *>(to + HD / 2) = make_uint2(qb[0], qb[1]);
+        } else {
+          *reinterpret_cast<uint4 *>(to) = make_uint4(qa[0], qa[1], qa[2], qa[3]);
+          *reinterpret_cast<uint4 *>(to + HD / 2) = make_uint4(qb[0], qb[1], qb[2], qb[3]);
+        }
+      }
+    }
+    if (kept > 0 && s > s_old) {
+      const float ratio = s_old / s;
+#pragma unroll 1
+      for (int r = slot; r < kept; r += SLOTS)
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint16_t *at = reinterpret_cast<uint16_t *>(dst + r * HD + half * (HD / 2));
+#pragma unroll
+          for (int q = 0; q < W; ++q) {
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(at[q]), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+            at[q] = static_cast<uint16_t>(e4m3x2(make_float2(f.x * ratio, f.y * ratio)));
+          }
+        }
+    }
+    if (tid == 0 && !(kept > 0 && s == s_old)) p.scale[t][bi] = s;
   }
-  if (threadIdx.x == 0 && !(keeps && s == s_old)) *scale_at = s;
 }
 
 static cudaError_t launch_rows(KvRowsParams &p, bool append, int num_sms, cudaStream_t s) {
   const int hpw = 32 / (p.hd / 16);
   const int groups = (p.heads[0] + p.heads[1] + hpw - 1) / hpw;  // head groups of a row
   const long long rows = static_cast<long long>(p.nb) * p.R;
-  // few rows: a warp for every head group (latency); many: up to 8 groups per warp, so the
-  // angles are computed once for them and their loads are in flight together
-  const long long target = static_cast<long long>(num_sms) * 32;
-  int iters = static_cast<int>(std::min<long long>(std::min(groups, 8), std::max<long long>(1, rows * groups / target)));
-  p.warps_per_row = (groups + iters - 1) / iters;
-  p.iters = (groups + p.warps_per_row - 1) / p.warps_per_row;
-  const long long ctas = (rows * p.warps_per_row + 7) / 8;
-  if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(ctas));
+  // few rows: a warp for every head group (latency); many: the whole row in one warp, so that the factors
+  // are computed once for it (8191 rows of 40 heads: 29.9 us; with two groups a warp 61)
+  const long long target = static_cast<long long>(num_sms) * 16;
+  const int iters = static_cast<int>(std::min<long long>(groups, std::max<long long>(1, rows * groups / target)));
+  const int parts = (groups + iters - 1) / iters;
+  p.cta_rows = parts == 1 ? 4 : parts == 2 ? 2 : 1;
+  const int per_row = 4 / p.cta_rows;
+  const int y = (parts + per_row - 1) / per_row;
+  p.iters = (groups + y * per_row - 1) / (y * per_row);
+  const dim3 grid(static_cast<unsigned>((rows + p.cta_rows - 1) / p.cta_rows), y);
   if (p.hd == 128)
-    return append ? launch_pdl(kv_rows_kernel<128, true>, grid, dim3(256), 0, s, p)
-                  : launch_pdl(kv_rows_kernel<128, false>, grid, dim3(256), 0, s, p);
-  return append ? launch_pdl(kv_rows_kernel<64, true>, grid, dim3(256), 0, s, p)
-                : launch_pdl(kv_rows_kernel<64, false>, grid, dim3(256), 0, s, p);
+    return append ? launch_pdl(kv_rows_kernel<128, true>, grid, dim3(128), 0, s, p)
+                  : launch_pdl(kv_rows_kernel<128, false>, grid, dim3(128), 0, s, p);
+  return append ? launch_pdl(kv_rows_kernel<64, true>, grid, dim3(128), 0, s, p)
+                : launch_pdl(kv_rows_kernel<64, false>, grid, dim3(128), 0, s, p);
 }
 
 cudaError_t launch_qk_norm_rope(KvRowsParams &p, int num_sms, cudaStream_t s) {
@@ -340,11 +475,36 @@ cudaError_t launch_kv_append(KvRowsParams &p, int num_sms, cudaStream_t s) {
   return launch_rows(p, true, num_sms, s);
 }
 
-cudaError_t launch_kv_append8(const KvRowsParams &p, cudaStream_t s) {
-  // blocks of 64 rows that R rows can touch
-  const dim3 grid((p.R + 62) / kPageRows + 1, 2 * p.heads[0], p.nb);
-  return p.hd == 128 ? launch_pdl(kv_append8_kernel<128>, grid, dim3(256), 0, s, p)
-                     : launch_pdl(kv_append8_kernel<64>, grid, dim3(256), 0, s, p);
+template <int HD, int SLOTS, int TPR>
+static cudaError_t launch_slots(KvRowsParams &p, int num_sms, cudaStream_t s) {
+  constexpr int GT = SLOTS * TPR;
+  constexpr int GROUPS = GT < 128 ? 128 / GT : 1;
+  const int blocks = (p.R + kPageRows - 2) / kPageRows + 1;  // of 64 rows that R rows can touch
+  p.iters = 1;
+  if (GT > 32) {  // heads one after the other while that leaves enough CTAs (64 x 8 rows: 4.7 us at 6 a SM, 5.2 at 3)
+    p.iters = std::min(p.heads[0], 32);
+    auto ctas = [&] { return static_cast<long long>(blocks) * p.nb * 2 * ((p.heads[0] + p.iters - 1) / p.iters); };
+    while (p.iters > 1 && ctas() < (GT > 128 ? 3LL : 6LL) * num_sms) p.iters = (p.iters + 1) / 2;
+  }
+  // values have no angles to share: groups of half as many, which fill in behind the keys (two prompts of
+  // 8189 rows: 14.2 us, with groups as large as the keys' 15.5, of a quarter 14.6)
+  p.iters_v = (p.iters + 1) / 2;
+  const int groups = (p.heads[0] + p.iters - 1) / p.iters + (p.heads[0] + p.iters_v - 1) / p.iters_v;
+  return launch_pdl(kv_append8_kernel<HD, SLOTS, TPR>, dim3(blocks, p.nb, (groups + GROUPS - 1) / GROUPS),
+                    dim3(GT < 128 ? 128 : GT), 0, s, p);
+}
+
+template <int HD>
+static cudaError_t launch_append8(KvRowsParams &p, int num_sms, cudaStream_t s) {
+  // As many row slots as R needs, of 2, 16 or 64: 64 sequences with one row each take 2.9 us with 2 slots, 4.5
+  // with 16 and 8.0 with 64; with 8 rows each 4.7 with 16 slots, 7.7 with 64.
+  return p.R <= 2    ? launch_slots<HD, 2, 16>(p, num_sms, s)
+         : p.R <= 16 ? launch_slots<HD, 16, 8>(p, num_sms, s)
+                     : launch_slots<HD, 64, 4>(p, num_sms, s);
+}
+
+cudaError_t launch_kv_append8(KvRowsParams &p, int num_sms, cudaStream_t s) {
+  return p.hd == 128 ? launch_append8<128>(p, num_sms, s) : launch_append8<64>(p, num_sms, s);
 }
 
 }  // namespace df
