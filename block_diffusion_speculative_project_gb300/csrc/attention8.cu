@@ -30,7 +30,10 @@ namespace df {
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
 template <int HD, int RP>
 struct A8Cfg {
-  static constexpr int ROWS = 16;                    // query rows of a softmax thread
+  // Query rows of a softmax thread. For 16 rows two groups of four warps halve the chain from S to P (64
+  // single tokens 103.5 us with one group, 99.6 with two); for 32 two groups already fill the issue slots
+  // (64 verified blocks 132.9 us, with four groups 146.9).
+  static constexpr int ROWS = RP / 2;
   static constexpr int NRG = RP / ROWS;              // groups of four softmax warps
   static constexpr int NSW = 4 * NRG;
   static constexpr int SB = 2, OB = 2;               // buffers of S, and of O
@@ -105,6 +108,10 @@ struct Blocks8 {
     next = look_up(p, sseq, nunits);
   }
 };
+
+// Columns of tensor memory from `at` on.
+__device__ __forceinline__ void load_cols(uint32_t at, float (&v)[16]) { tmem_ld16(at, v); }
+__device__ __forceinline__ void load_cols(uint32_t at, float (&v)[8]) { tmem_ld8(at, v); }
 
 // Sums v[0 .. N) over the warp's lanes; lane l gets the sum of element l % N (N <= 32), in a fixed order.
 template <int N>
@@ -414,17 +421,24 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     constexpr float kTop = kPBase + kRescale;
     bool fail = false, gone = false;
 
-    // The query rows of a segment: eight threads a row, hd/8 values each, read a segment ahead.
-    constexpr int PASS = RP * 8 / T;
-    uint4 qr[PASS][HD / 64];
+    // The query rows of a segment, read a segment ahead.
+    constexpr int TPQ = T / RP, QW = HD / TPQ / 2;  // threads a row, words of a thread (8 or 4 or 2)
+    const int qrow = tid / TPQ, qpart = tid % TPQ;
+    uint32_t qr[QW];
     auto fetch_q = [&](const Pos8 &a) {
+      const int j = qrow / G;
+      const uint16_t *src =
+          p.q + ((static_cast<size_t>(a.i) * p.m + j) * p.Hq + a.g * G + qrow % G) * HD + qpart * 2 * QW;
+      const bool have = j < a.n;
+      if constexpr (QW == 2) {
+        const uint2 u = have ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
+        qr[0] = u.x, qr[1] = u.y;
+      } else {
 #pragma unroll
-      for (int x = 0; x < PASS; ++x) {
-        const int r = x * (T / 8) + (tid >> 3), j = r / G;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + ((static_cast<size_t>(a.i) * p.m + j) * p.Hq + a.g * G + r % G) * HD + (tid & 7) * (HD / 8));
-#pragma unroll
-        for (int y = 0; y < HD / 64; ++y) qr[x][y] = j < a.n ? src[y] : make_uint4(0, 0, 0, 0);
+        for (int y = 0; y < QW; y += 4) {
+          const uint4 u = have ? reinterpret_cast<const uint4 *>(src)[y / 4] : make_uint4(0, 0, 0, 0);
+          qr[y] = u.x, qr[y + 1] = u.y, qr[y + 2] = u.z, qr[y + 3] = u.w;
+        }
       }
     };
     // The rows are scaled by a power of two so that the largest value of a block of 16 rows lies in
@@ -433,82 +447,63 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     // own (the block's factor is then -1). Two barriers.
     auto put_q = [&](const Pos8 &a) {
       int *sexp = reinterpret_cast<int *>(red);
-      float am[PASS];
+      float am = 0.f;
 #pragma unroll
-      for (int x = 0; x < PASS; ++x) {
-        am[x] = 0.f;
+      for (int y = 0; y < QW; ++y)
+        am = max3(am, fabsf(__uint_as_float(qr[y] << 16)), fabsf(__uint_as_float(qr[y] & 0xFFFF0000u)));
 #pragma unroll
-        for (int y = 0; y < HD / 64; ++y) {
-          const uint32_t v[4] = {qr[x][y].x, qr[x][y].y, qr[x][y].z, qr[x][y].w};
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-            am[x] = fmaxf(am[x], fmaxf(fabsf(__uint_as_float(v[f] << 16)), fabsf(__uint_as_float(v[f] & 0xFFFF0000u))));
-        }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) am[x] = fmaxf(am[x], __shfl_xor_sync(0xffffffffu, am[x], o));
-        // -127: zero or subnormal, 128: infinite
-        if ((tid & 7) == 0) sexp[x * (T / 8) + (tid >> 3)] = static_cast<int>(__float_as_uint(am[x]) >> 23) - 127;
-      }
+      for (int o = 1; o < TPQ; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      // -127: zero or subnormal, 128: infinite
+      if (qpart == 0) sexp[qrow] = static_cast<int>(__float_as_uint(am) >> 23) - 127;
       named_bar_sync(1, T);
-      int exs[PASS];
+      int top = -100, low = 200;
 #pragma unroll
-      for (int x = 0; x < PASS; ++x) {
-        const int r = x * (T / 8) + (tid >> 3);
-        int lo = 200, hi = -100;
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const int4 v = *reinterpret_cast<const int4 *>(sexp + (r & ~15) + e);
-          hi = max(max(hi, max(v.x, v.y)), max(v.z, v.w));
-          lo = min(min(lo, min(v.x == -127 ? 200 : v.x, v.y == -127 ? 200 : v.y)),
-                   min(v.z == -127 ? 200 : v.z, v.w == -127 ? 200 : v.w));
-        }
-        const bool apart = hi == 128 || hi - lo > 3;
-        exs[x] = apart ? max(sexp[r], -100) : hi;
-        if ((tid & 7) == 0 && (r & 15) == 0)
-          sfac[RP + (r >> 4)] = apart ? -1.f : sl2 * __uint_as_float(static_cast<uint32_t>(hi + 120) << 23);
+      for (int e = 0; e < 16; e += 4) {
+        const int4 v = *reinterpret_cast<const int4 *>(sexp + (qrow & ~15) + e);
+        top = max(max(top, max(v.x, v.y)), max(v.z, v.w));
+        low = min(min(low, min(v.x == -127 ? 200 : v.x, v.y == -127 ? 200 : v.y)),
+                  min(v.z == -127 ? 200 : v.z, v.w == -127 ? 200 : v.w));
       }
+      const bool apart = top == 128 || top - low > 3;
+      const int exs = apart ? max(sexp[qrow], -100) : top;
+      if (qpart == 0 && (qrow & 15) == 0)
+        sfac[RP + (qrow >> 4)] = apart ? -1.f : sl2 * __uint_as_float(static_cast<uint32_t>(top + 120) << 23);
+      const bool inf = exs == 128;                              // the row's outputs are NaN
+      const int ex = min(exs, 127);
+      const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(134 - ex) << 23);
+      uint32_t hi[QW / 2], lo[QW / 2];
 #pragma unroll
-      for (int x = 0; x < PASS; ++x) {
-        const int r = x * (T / 8) + (tid >> 3), part = tid & 7;
-        const bool inf = exs[x] == 128;                              // the row's outputs are NaN
-        const int ex = min(exs[x], 127);
-        const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(134 - ex) << 23);
-        uint32_t hi[HD / 32], lo[HD / 32];
-#pragma unroll
-        for (int y = 0; y < HD / 64; ++y) {
-          const uint32_t v[4] = {qr[x][y].x, qr[x][y].y, qr[x][y].z, qr[x][y].w};
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const float2 q = make_float2(__uint_as_float(v[f] << 16) * mul, __uint_as_float(v[f] & 0xFFFF0000u) * mul);
-            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-            const __nv_fp8x2_storage_t l =
-                __nv_cvt_float2_to_fp8x2(make_float2(q.x - hf.x, q.y - hf.y), __NV_SATFINITE, __NV_E4M3);
-            const int d = y * 2 + f / 2;
-            hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(h) << 16) : h;
-            lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(l) << 16) : l;
-          }
-        }
-        // rows r (hi) and RP + r (lo) of the operand, 16-byte chunks swizzled as a copy would
-        uint8_t *dh = sQ + r * HD, *dl = sQ + (RP + r) * HD;
-        if constexpr (HD == 128) {
-          const int at = (part ^ (r & 7)) << 4;
-          *reinterpret_cast<uint4 *>(dh + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(dl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        } else {
-          const int at = (((part >> 1) ^ ((r >> 1) & 3)) << 4) + (part & 1) * 8;
-          *reinterpret_cast<uint2 *>(dh + at) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2 *>(dl + at) = make_uint2(lo[0], lo[1]);
-        }
-        if (part == 0) {
-          // the factor takes S to log2 units, 1/sqrt(hd) included; rows that are not there get P = 0
-          const int j = r / G;
-          const bool live = j < a.n;
-          sfac[r] = live ? sl2 * __uint_as_float(static_cast<uint32_t>(ex + 120) << 23) : 0.f;
-          nref[r] = live ? 0.f : -1e30f;
-          slim[r] = p.causal ? min(a.ctx + j + 1, a.ctx + a.n) : a.ctx + a.n;
-        }
+      for (int y = 0; y < QW; ++y) {
+        const float2 q = make_float2(__uint_as_float(qr[y] << 16) * mul, __uint_as_float(qr[y] & 0xFFFF0000u) * mul);
+        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
+        const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+        const __nv_fp8x2_storage_t l =
+            __nv_cvt_float2_to_fp8x2(make_float2(q.x - hf.x, q.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+        hi[y / 2] = y % 2 ? hi[y / 2] | (static_cast<uint32_t>(h) << 16) : h;
+        lo[y / 2] = y % 2 ? lo[y / 2] | (static_cast<uint32_t>(l) << 16) : l;
+      }
+      // rows r (hi) and RP + r (lo) of the operand, 16-byte chunks swizzled as a copy would
+      constexpr int BYTES = 2 * QW;                             // of a thread
+      const int chunk = qpart * BYTES >> 4, xor8 = HD == 128 ? qrow & 7 : (qrow >> 1) & 3;
+      uint8_t *dh = sQ + qrow * HD + ((chunk ^ xor8) << 4) + (qpart * BYTES & 15), *dl = dh + RP * HD;
+      if constexpr (BYTES == 16) {
+        *reinterpret_cast<uint4 *>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      } else if constexpr (BYTES == 8) {
+        *reinterpret_cast<uint2 *>(dh) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(dl) = make_uint2(lo[0], lo[1]);
+      } else {
+        *reinterpret_cast<uint32_t *>(dh) = hi[0];
+        *reinterpret_cast<uint32_t *>(dl) = lo[0];
+      }
+      if (qpart == 0) {
+        // the factor takes S to log2 units, 1/sqrt(hd) included; rows that are not there get P = 0
+        const int j = qrow / G;
+        const bool live = j < a.n;
+        sfac[qrow] = live ? sl2 * __uint_as_float(static_cast<uint32_t>(ex + 120) << 23) : 0.f;
+        nref[qrow] = live ? 0.f : -1e30f;
+        slim[qrow] = p.causal ? min(a.ctx + j + 1, a.ctx + a.n) : a.ctx + a.n;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -521,13 +516,12 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     int pj = 0, st = 0, chunk = -1, freed = 0;  // chunk: scales that may be read; freed: given back
     float lsum[ROWS];
     float own[ROWS];       // -references of this thread's rows
-    float fac[ROWS / 16];                // factors of their blocks
+    float fac;                           // factor of their block of 16
     auto keep_rows = [&]() {
 #pragma unroll
       for (int c = 0; c < ROWS; c += 4)
         *reinterpret_cast<float4 *>(own + c) = *reinterpret_cast<const float4 *>(nref + r0 + c);
-#pragma unroll
-      for (int c = 0; c < ROWS / 16; ++c) fac[c] = sfac[RP + r0 / 16 + c];
+      fac = sfac[RP + r0 / 16];
     };
     keep_rows();
 #pragma unroll 1
@@ -548,45 +542,45 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         const int j = j0 + u, base = (w.unit + u) * kUnit;
         const bool two = u + 1 < cnt;
         const int jl = j + (two ? 1 : 0);
-        if (chunk < (jl >> 5)) {         // (a unit that begins a chunk, or the pair after it)
+        if (chunk < (jl >> 5)) [[unlikely]] {  // (a unit that begins a chunk, or the pair after it)
           fail |= !mbar_wait_warp(&sc_full[(chunk + 1) & 1], ((chunk + 1) >> 1) & 1, p.max_spin);
           ++chunk;
         }
-        if (freed < (j >> 5)) {          // a chunk is behind this pair
+        if (freed < (j >> 5)) [[unlikely]] {  // a chunk is behind this pair
           __syncwarp();
           mbar_arrive_if(&sc_empty[freed & 1], lane == 0);
           ++freed;
         }
         const int js = two ? j + slot : j;
         const float4 sc = sscale[((js >> 5) & 1) * 32 + (js & 31)];  // K scale, log2 V, 1 / V, 1 for zeros
-        fail |= !mbar_wait_warp(&s_full[pj & 1], (pj >> 1) & 1, p.max_spin);
+        // S^T, and that P^T's buffer was read by the pair before last (before the first two: at once)
+        fail |= !mbar_wait_warp2(&s_full[pj & 1], (pj >> 1) & 1, &pv_done[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
         tc_fence_after();
         // y = log2 of P: score in log2 units + log2 V scale - reference + kPBase
         float y[ROWS];
         float top = -INFINITY;
         const uint32_t s_at = trow + C::S_COL + (pj % C::SB) * RP + r0;
         const float2 c2 = make_float2(sc.y + kPBase, sc.y + kPBase);
+        float h[ROWS];
+        load_cols(s_at, h);
+        if (fac < 0.f) [[unlikely]] {    // the rows' factors are apart
 #pragma unroll
-        for (int c = 0; c < ROWS; c += 16) {
-          float h[16];
-          tmem_ld16(s_at + c, h);
-          float2 f2 = make_float2(fac[c / 16] * sc.x, fac[c / 16] * sc.x);
-          const bool apart = fac[c / 16] < 0.f;
+          for (int e = 0; e < ROWS; ++e) h[e] *= sfac[r0 + e];
+        }
+        const float f = fac < 0.f ? sc.x : fac * sc.x;
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float2 nr = make_float2(own[c + e], own[c + e + 1]);
-            if (apart) f2 = make_float2(sfac[r0 + c + e] * sc.x, sfac[r0 + c + e + 1] * sc.x);
-            const float2 v = fma2(make_float2(h[e], h[e + 1]), f2, add2(nr, c2));
-            y[c + e] = v.x;
-            y[c + e + 1] = v.y;
-          }
+        for (int e = 0; e < ROWS; e += 2) {
+          const float2 v = fma2(make_float2(h[e], h[e + 1]), f2, add2(make_float2(own[e], own[e + 1]), c2));
+          y[e] = v.x;
+          y[e + 1] = v.y;
         }
         tc_fence_before();
         __syncwarp();
         mbar_arrive_if(&s_empty[pj & 1], lane == 0);
         mbar_arrive_if(&k8_empty[st], tid == 0);  // S complete: the keys have been read
         const bool there = base + key < last_key && (two || slot == 0);
-        if (base + 2 * kUnit > every || !two) {  // some row does not see the whole pair
+        if (base + 2 * kUnit > every || !two) [[unlikely]] {  // some row does not see the whole pair
 #pragma unroll
           for (int c = 0; c < ROWS; ++c) y[c] = there && base + key < slim[r0 + c] ? y[c] : -INFINITY;
         }
@@ -594,14 +588,13 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         for (int c = 0; c < ROWS; c += 2) top = max3(top, y[c], y[c + 1]);
         // rows of V that hold no value (beyond the last key, or of a scale of zero) may hold anything
         const bool bad = rg == 0 && (two || slot == 0) && (!there || sc.w != 0.f);
-        if (named_bar_or(1, T, u == 0 || top > kTop || bad || fail)) {
+        if (named_bar_or(1, T, u == 0 || top > kTop || bad || fail)) [[unlikely]] {
           // ---- now and then: the segment's first pair, a reference that has to move, values to clear
           if (named_bar_or(1, T, fail)) {
             gone = true;
             break;
           }
           if (rg == 0 && __any_sync(0xffffffffu, bad)) {
-            if (pj >= 2) fail |= !mbar_wait_warp(&pv_done[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
             fail |= !mbar_wait_warp(&v8_full[st], (pj / C::NS) & 1, p.max_spin);
             if (bad) {
               uint4 *row = reinterpret_cast<uint4 *>(sV8 + st * C::PAIR8 + key * HD);
@@ -613,10 +606,9 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
 #pragma unroll
           for (int c = 0; c < ROWS; ++c) {
             const float m = warp_max(y[c]);
-            mine = lane == (c & 31) ? m : mine;
-            if ((c & 31) == 31 || c == ROWS - 1)
-              if (lane <= (c & 31)) red[quarter * RP + r0 + (c & ~31) + lane] = mine;
+            mine = lane == c ? m : mine;
           }
+          if (lane < ROWS) red[quarter * RP + r0 + lane] = mine;
           named_bar_sync(1, T);
           float d = 0.f;                 // the row's reference moves by d
           if (tid < RP) {
@@ -628,65 +620,69 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
           const bool moved = named_bar_or(1, T, d != 0.f);
           if (moved) {
             keep_rows();
+            float sh[ROWS];              // 2^-d
+            bool any = false;            // of this group's rows
 #pragma unroll
             for (int c = 0; c < ROWS; ++c) {
               const float dc = srow[r0 + c];
+              any |= dc != 0.f;
               y[c] -= dc;
-              lsum[c] *= ex2f(-dc);
+              sh[c] = ex2f(-dc);
+              lsum[c] *= sh[c];
+            }
+            if (u > 0 && any) {
+              // O^T *= 2^-d, once every product before has been added
+              fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
+              tc_fence_after();
+              float ov[3][ROWS];
+#pragma unroll
+              for (int t = 0; t < 3; ++t) load_cols(o_at + t * RP + r0, ov[t]);
+#pragma unroll
+              for (int t = 0; t < 3; ++t) {
+                uint32_t x[ROWS];
+#pragma unroll
+                for (int e = 0; e < ROWS; ++e) x[e] = __float_as_uint(ov[t][e] * sh[e]);
+                if constexpr (ROWS == 16)
+                  tmem_st16_raw(o_at + t * RP + r0, x);
+                else
+                  tmem_st8_raw(o_at + t * RP + r0, x);
+              }
+              tmem_wait_st();
             }
           }
           if (u == 0) {
 #pragma unroll
             for (int c = 0; c < ROWS; ++c) lsum[c] = 0.f;
-          } else if (moved) {
-            // O^T *= 2^-d, once every product before has been added
-            fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
-            tc_fence_after();
-#pragma unroll 1
-            for (int t = 0; t < 3; ++t) {
-#pragma unroll 1
-              for (int c = 0; c < ROWS; c += 16) {
-                float ov[16];
-                uint32_t x[16];
-                tmem_ld16(o_at + t * RP + r0 + c, ov);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(ov[e] * ex2f(-srow[r0 + c + e]));
-                tmem_st16_raw(o_at + t * RP + r0 + c, x);
-              }
-            }
-            tmem_wait_st();
           }
         }
-        // P^T buffer pj % 2: read by the pair before last
-        if (pj >= 2) fail |= !mbar_wait_warp(&pv_done[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
         uint8_t *prow = sP + (pj & 1) * C::P_BYTES + key * 128;
         const float2 iv = make_float2(sc.z, sc.z);
+        uint32_t ta[ROWS / 4], tb[ROWS / 4], tc[ROWS / 4];
 #pragma unroll
-        for (int c = 0; c < ROWS; c += 16) {
-          uint32_t ta[4], tb[4], tc[4];
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float2 p0 = make_float2(ex2f(y[c + e]), ex2f(y[c + e + 1]));
-            const float2 p1 = make_float2(ex2f(y[c + e + 2]), ex2f(y[c + e + 3]));
-            const float2 l0 = fma2(p0, iv, make_float2(lsum[c + e], lsum[c + e + 1]));
-            const float2 l1 = fma2(p1, iv, make_float2(lsum[c + e + 2], lsum[c + e + 3]));
-            lsum[c + e] = l0.x;
-            lsum[c + e + 1] = l0.y;
-            lsum[c + e + 2] = l1.x;
-            lsum[c + e + 3] = l1.y;
-            const __half2 a = __floats2half2_rn(p0.x, p0.y), b = __floats2half2_rn(p1.x, p1.y);
-            split4(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b), ta[e / 4],
-                   tb[e / 4], tc[e / 4]);
-          }
-          // column t * RP + row of the key's row, 16-byte chunks swizzled
-          auto put = [&](int col, const uint32_t (&v)[4]) {
-            *reinterpret_cast<uint4 *>(prow + (((col >> 4) ^ (key & 7)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
-          };
-          put(r0 + c, ta);
-          put(RP + r0 + c, tb);
-          put(2 * RP + r0 + c, tc);
+        for (int e = 0; e < ROWS; e += 4) {
+          const float2 p0 = make_float2(ex2f(y[e]), ex2f(y[e + 1]));
+          const float2 p1 = make_float2(ex2f(y[e + 2]), ex2f(y[e + 3]));
+          const float2 l0 = fma2(p0, iv, make_float2(lsum[e], lsum[e + 1]));
+          const float2 l1 = fma2(p1, iv, make_float2(lsum[e + 2], lsum[e + 3]));
+          lsum[e] = l0.x;
+          lsum[e + 1] = l0.y;
+          lsum[e + 2] = l1.x;
+          lsum[e + 3] = l1.y;
+          const __half2 a = __floats2half2_rn(p0.x, p0.y), b = __floats2half2_rn(p1.x, p1.y);
+          split4(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b), ta[e / 4],
+                 tb[e / 4], tc[e / 4]);
         }
+        // column t * RP + row of the key's row, 16-byte chunks swizzled
+        auto put = [&](int col, const uint32_t (&v)[ROWS / 4]) {
+          uint8_t *to = prow + (((col >> 4) ^ (key & 7)) << 4) + (col & 15);
+          if constexpr (ROWS == 16)
+            *reinterpret_cast<uint4 *>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+          else
+            *reinterpret_cast<uint2 *>(to) = make_uint2(v[0], v[1]);
+        };
+        put(r0, ta);
+        put(RP + r0, tb);
+        put(2 * RP + r0, tc);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -698,15 +694,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       j0 += cnt;
       const int live = w.n * G;
       const size_t row0 = (static_cast<size_t>(w.i * p.Hkv + w.g) + blockIdx.x) * R;  // partial rows
-#pragma unroll
-      for (int c = 0; c < ROWS; c += 32) {
-        constexpr int N = ROWS < 32 ? ROWS : 32;
-        float v[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = lsum[c + e];
-        const float s = lane_sums<N>(v, lane);
-        if (lane < N) red[quarter * RP + r0 + c + lane] = s;
-      }
+      const float sum = lane_sums<ROWS>(lsum, lane);
+      if (lane < ROWS) red[quarter * RP + r0 + lane] = sum;
       named_bar_sync(1, T);
       if (tid < RP) {
         const float L = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
@@ -724,27 +713,26 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
       tc_fence_after();
       // lane = column `key` of the head; a row is written by a warp's lanes together
-#pragma unroll 1
-      for (int c = r0; c < r0 + ROWS && c < live; c += 16) {
-        float ov[16];
-        tmem_ld16(o_at + c, ov);
+      if (r0 < live) {
+        float ov[ROWS];
+        load_cols(o_at + r0, ov);
 #pragma unroll 1
         for (int t = 1; t < 3; ++t) {
-          float x[16];
-          tmem_ld16(o_at + t * RP + c, x);
+          float x[ROWS];
+          load_cols(o_at + t * RP + r0, x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) ov[e] += x[e];
+          for (int e = 0; e < ROWS; ++e) ov[e] += x[e];
         }
-        int jr = c / G, hr = c % G;
+        int jr = r0 / G, hr = r0 % G;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (c + e >= live) break;
+        for (int e = 0; e < ROWS; ++e) {
+          if (r0 + e >= live) break;
           if (HD == 128 || key < HD) {
-            const float v = ov[e] * srow[c + e];
+            const float v = ov[e] * srow[r0 + e];
             if (whole)
               o[(static_cast<size_t>(jr) * p.Hq + hr) * HD] = static_cast<uint16_t>(pack_bf16x2(v, v));
             else
-              p.part_o[(row0 + c + e) * HD + key] = v;
+              p.part_o[(row0 + r0 + e) * HD + key] = v;
           }
           if (++hr == G) {
             hr = 0;

@@ -85,6 +85,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, i
   return false;
 }
 
+// The same for two barriers, with one vote.
+__device__ __forceinline__ bool mbar_wait_warp2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1,
+                                                int max_spin) {
+  const bool t0 = mbar_test_wait(bar0, parity0), t1 = mbar_test_wait(bar1, parity1);
+  if (__all_sync(0xffffffffu, t0 && t1)) return true;
+  return mbar_wait_warp(bar0, parity0, max_spin) && mbar_wait_warp(bar1, parity1, max_spin);
+}
+
 // Arrive if `pred`, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint64_t *bar, bool pred) {
   asm volatile(
@@ -193,6 +201,18 @@ __device__ __forceinline__ void tc_mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_t
 // N consecutive 32-bit columns of this thread's lane (32x32b shape): loads wait inside, the raw
 // stores are waited for by tmem_wait_st.
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
