@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
+  touch8(p);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   if (warp == kWValues) {
@@ -770,6 +771,7 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
   constexpr int E = HD / 32;
   constexpr int ROWS = kMerge8Warps / SPLIT;
   __shared__ __align__(16) float sum[SPLIT > 1 ? SPLIT - 1 : 1][HD];
+  touch8(p);
   // The schedule reads only the lengths, written before the attention kernel let this one start.
   // This grid's end must imply the attention's: CTA (0, 0) always waits for it; others with
   // nothing to join leave at once.
@@ -795,27 +797,9 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
   if (!join) return;  // with SPLIT > 1 a CTA has one row, and leaves as one
   const size_t row0 = (static_cast<size_t>(pair) + c0) * R + r;  // parts are R rows apart
   const int parts = c1 - c0 + 1;
-  float M = kNoMax, L = 0.f;
-#pragma unroll 1
-  for (int b = 0; b < parts; b += 32) {
-    const int c = b + lane;
-    float2 ml = make_float2(kNoMax, 0.f);
-    if (c < parts) ml = *reinterpret_cast<const float2 *>(p.part_ml + (row0 + static_cast<size_t>(c) * R) * 2);
-    const float Mn = fmaxf(M, warp_max(ml.x));
-    float l = ml.y * exp2f(ml.x - Mn);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    L = L * exp2f(M - Mn) + l;
-    M = Mn;
-  }
-  const float inv = 1.0f / L;
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const float *src = p.part_o + row0 * HD + lane * E;
-#pragma unroll 1
-  for (int b = warp % SPLIT; b < parts; b += 4 * SPLIT) {
-    float v[4][E], w[4];
+  float v[4][E], w[4];
+  auto load = [&](int b) {  // parts b, b + SPLIT, .. of this warp
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int c = b + k * SPLIT;
@@ -833,6 +817,28 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
         }
       }
     }
+  };
+  load(warp % SPLIT);
+  float M = kNoMax, L = 0.f;
+#pragma unroll 1
+  for (int b = 0; b < parts; b += 32) {
+    const int c = b + lane;
+    float2 ml = make_float2(kNoMax, 0.f);
+    if (c < parts) ml = *reinterpret_cast<const float2 *>(p.part_ml + (row0 + static_cast<size_t>(c) * R) * 2);
+    const float Mn = fmaxf(M, warp_max(ml.x));
+    float l = ml.y * exp2f(ml.x - Mn);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L = L * exp2f(M - Mn) + l;
+    M = Mn;
+  }
+  const float inv = 1.0f / L;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int b = warp % SPLIT; b < parts; b += 4 * SPLIT) {
+    if (b >= 4 * SPLIT) load(b);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float f = exp2f(w[k] - M);

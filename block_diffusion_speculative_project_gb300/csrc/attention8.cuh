@@ -119,6 +119,12 @@ static __device__ void find_range(const Attn8Params &p, int cta, int lane, int *
   }
 }
 
+// Asks for the parameters that the split reads, so that they come while the launch before this one
+// ends and not one miss after the other behind it.
+__device__ __forceinline__ void touch8(const Attn8Params &p) {
+  asm volatile("" ::"r"(p.nb), "r"(p.m), "r"(p.Hq), "r"(p.Cmax), "r"(p.grid), "l"(p.n_rows), "l"(p.page_table));
+}
+
 constexpr int kSeqCache = 128;     // sequences whose lengths a CTA keeps in shared memory
 constexpr int kDrainSpin = 1 << 22;
 

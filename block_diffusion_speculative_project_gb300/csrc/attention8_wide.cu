@@ -56,10 +56,10 @@ constexpr float kPBase = 7.f, kRescale = 8.f;
 // every copy, product and exponential left out it still took 0.8 of its time, a unit at a time), so
 // they are paid for two units at once. Half a pair at the end of a segment of an odd number of units
 // is signalled by every role without work.
-// Warps: producer, S issuer, PV issuer, one that only helps at the start, softmax half h = 0, 1 (a
+// Warps: producer, S issuer, PV issuer, loader of queries, softmax half h = 0, 1 (a
 // pair's first or second unit) in 4 + 4h .. 7 + 4h (warp w reads TMEM lanes of quarter w % 4), then
 // the converters of V.
-constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWAid = 3, kWSoft = 4, kWConv = 12, kNumConv = 4;
+constexpr int kWProd = 0, kWS = 1, kWPV = 2, kWQ = 3, kWSoft = 4, kWConv = 12, kNumConv = 4;
 constexpr int kWideThreads = (kWConv + kNumConv) * 32;
 
 template <int KW>
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     }
     mbar_init(s_full, 1);
     mbar_init(s_empty, 8);
-    mbar_init(q8_full, 1);
+    mbar_init(q8_full, 32);
     mbar_init(q8_empty, 8);
     mbar_init(q_full, 8);
     mbar_init(q_empty, 1);
@@ -156,11 +156,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
+  touch8(p);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch();
   if (warp == kWProd) {
     find_range(p, blockIdx.x, lane, sched);
-  } else if (warp == kWAid) {
+  } else if (warp == kWQ) {
     for (int i = lane; i < p.nb && i < kSeqCache; i += 32) {
       const Seq8 s = seq8(p, i);
       sseq[i] = make_int2(s.n, s.ctx);
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     // ahead and its scales one chunk ahead, so the copies wait for neither.
     const uint64_t pol = policy_evict_first();
     bool ok = !p.stall;
-    int pairs = 0, segs = 0;
+    int pairs = 0;
     Pos8 a = w;
     int x = lane;
     a.unit += lane;
@@ -208,20 +209,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       a.unit += 32;
       return b;
     };
-    // A segment's query rows. The first segment's are asked for before anything else.
-    auto queries = [&]() {
-      ok = segs == 0 || mbar_wait_warp(q8_empty, (segs - 1) & 1, p.max_spin);
-      if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(q8_full, w.n * G * HD * 2);
-      __syncwarp();
-#pragma unroll 1
-      for (int r = lane; r < w.n * G; r += 32)
-        bulk_load(sQ + r * C::QPITCH,
-                  p.q + ((static_cast<size_t>(w.i) * p.m + r / G) * p.Hq + w.g * G + r % G) * HD, HD * 2, q8_full,
-                  pol);
-      ++segs;
-    };
-    if (ok) queries();
     int blk = look_up();
     x += 32;
     int blk1 = look_up();
@@ -231,11 +218,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
 #pragma unroll 1
     for (int j = 0; j < nunits && ok; ++j) {
       const int k = j & 31, c = j >> 5;
-      if (cnt_left == 0) {  // a segment begins: its query rows
+      if (cnt_left == 0) {  // a segment begins
         if (j > 0) pos_next_pair(w, p, sseq);
         cnt_left = min(w.units - w.unit, nunits - j);
-        if (j > 0) queries();
-        if (!ok) break;
         slot = 0;
       }
       --cnt_left;
@@ -260,8 +245,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         slot = 1;
       }
       // The chunk's scales, after its first copies are under way, and before any wait for a unit
-      // of the chunk: a copy waits for the pair NS > 3 before its own, the next segment's queries
-      // for the units of the segment before last.
+      // of the chunk: a copy waits for the pair NS > 3 before its own.
       published = published && k != 0;
       if (!published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
         published = true;
@@ -286,7 +270,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
 #pragma unroll 1
     for (int x = max(0, pairs - C::NS); x < pairs; ++x)
       mbar_wait_warp(&kv8_full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
-    if (segs > 0) mbar_wait_warp(q8_full, (segs - 1) & 1, kDrainSpin);
+  } else if (warp == kWQ) {
+    // ---------------- query rows of every segment, a segment ahead: 16 bytes a lane (a bulk copy for each
+    // row took 2.4 us for 64, one after the other)
+    bool ok = !p.stall;
+#pragma unroll 1
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
+      ok = seg == 0 || mbar_wait_warp(q8_empty, (seg - 1) & 1, p.max_spin);
+      if (!ok) break;
+      constexpr int CPR = HD / 8;        // 16-byte chunks of a row
+      const uint16_t *src = p.q + (static_cast<size_t>(w.i) * p.m * p.Hq + w.g * G) * HD + lane % CPR * 8;
+      int r = lane / CPR, j = r / G, h = r % G;
+#pragma unroll 1
+      for (; r < w.n * G; r += 32 / CPR) {
+        cp_async16(smem_u32(sQ + r * C::QPITCH + lane % CPR * 16), src + (static_cast<size_t>(j) * p.Hq + h) * HD);
+        for (h += 32 / CPR; h >= G; h -= G) ++j;
+      }
+      cp_async_arrive(q8_full);
+      j0 += min(w.units - w.unit, nunits - j0);
+      if (j0 < nunits) pos_next_pair(w, p, sseq);
+    }
+    if (!ok && !p.stall && lane == 0) flag_status(p.status, kStatusTimeout);
+    cp_async_wait_all();
   } else if (warp == kWS) {
     // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two e4m3
     // terms one after the other from tensor memory
