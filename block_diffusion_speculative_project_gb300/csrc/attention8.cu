@@ -18,9 +18,9 @@ namespace df {
 // ---------------------------------------------------------------- tensor-core kernel
 
 // Both products read the cache's bytes as they are, with the keys and the head's columns as the 128
-// rows of the MMA and the query rows (RP of them, padded) as its columns:
-//   S^T [128 keys][RP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of two e4m3 terms
-//   O^T [hd][3 RP]     += V^T [hd x keys, e4m3] P^T, each probability as the sum of three e5m2 terms
+// rows of the MMA and the query rows (kRP of them, padded) as its columns:
+//   S^T [128 keys][kRP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of two e4m3 terms
+//   O^T [hd][3 kRP]     += V^T [hd x keys, e4m3] P^T, each probability as the sum of three e5m2 terms
 // so nothing is widened, and a softmax thread (a TMEM lane) is one key, whose scale is a number of the
 // thread. P's terms are columns of one pass over V; Q's are two passes over K, which the tensor cores
 // have the time for and which spare the softmax the second half of the columns.
@@ -28,29 +28,30 @@ namespace df {
 // f16's range: half a step of the smallest is 2^-24 of the largest or less.
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
-template <int HD, int RP>
+constexpr int kRP = 16;  // query rows of a kv head, padded
+
+template <int HD>
 struct A8Cfg {
-  // Query rows of a softmax thread. For 16 rows two groups of four warps halve the chain from S to P (64
-  // single tokens 103.5 us with one group, 99.6 with two); for 32 two groups already fill the issue slots
-  // (64 verified blocks 132.9 us, with four groups 146.9).
-  static constexpr int ROWS = RP / 2;
-  static constexpr int NRG = RP / ROWS;              // groups of four softmax warps
+  // Query rows of a softmax thread: two groups of four warps halve the chain from S to P (64 single tokens
+  // 103.5 us with one group, 99.6 with two).
+  static constexpr int ROWS = 8;
+  static constexpr int NRG = kRP / ROWS;              // groups of four softmax warps
   static constexpr int NSW = 4 * NRG;
   static constexpr int SB = 2, OB = 2;               // buffers of S, and of O
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values)
   static constexpr int PAIR8 = 2 * UNIT8;
   // rings of pairs, one of keys and one of values, as much as shared memory holds
   static constexpr int NS = 5 * (128 / HD);
-  static constexpr int P_BYTES = 128 * 128;          // P^T: 128 keys, rows of 128 bytes of which 3 RP hold terms
+  static constexpr int P_BYTES = 128 * 128;          // P^T: 128 keys, rows of 128 bytes of which 3 kRP hold terms
   static constexpr int OFF_V8 = NS * PAIR8;
   static constexpr int OFF_P = 2 * NS * PAIR8;       // two buffers
-  static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;  // 2 RP rows of hd bytes
-  static constexpr int OFF_REF = OFF_Q + 2 * RP * HD;     // [RP] -reference of a row
-  static constexpr int OFF_FAC = OFF_REF + RP * 4;        // [RP] factor of a row, [RP / 16] of a block of rows
-  static constexpr int OFF_LIM = OFF_FAC + RP * 4 + 64;        // [RP] keys that a row sees
-  static constexpr int OFF_RED = OFF_LIM + RP * 4;        // [4][RP] a quarter's maxima, sums
-  static constexpr int OFF_ROW = OFF_RED + 4 * RP * 4;    // [RP] a number for every row
-  static constexpr int OFF_SC = OFF_ROW + RP * 4;         // [2 chunks][32 units] scales
+  static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;  // 2 kRP rows of hd bytes
+  static constexpr int OFF_REF = OFF_Q + 2 * kRP * HD;     // [kRP] -reference of a row
+  static constexpr int OFF_FAC = OFF_REF + kRP * 4;        // [kRP] factor of a row, [kRP / 16] of a block of rows
+  static constexpr int OFF_LIM = OFF_FAC + kRP * 4 + 64;        // [kRP] keys that a row sees
+  static constexpr int OFF_RED = OFF_LIM + kRP * 4;        // [4][kRP] a quarter's maxima, sums
+  static constexpr int OFF_ROW = OFF_RED + 4 * kRP * 4;    // [kRP] a number for every row
+  static constexpr int OFF_SC = OFF_ROW + kRP * 4;         // [2 chunks][32 units] scales
   static constexpr int OFF_BAR = OFF_SC + 64 * 16;
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
   static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
@@ -59,9 +60,9 @@ struct A8Cfg {
                     OFF_RED % 16 == 0 && OFF_SC % 16 == 0 && OFF_BAR % 16 == 0 && OFF_SEQ % 16 == 0,
                 "alignment: 1024 bytes for swizzled tiles, 16 for what is read as vectors");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr int OCOLS = 3 * RP;
-  static constexpr uint32_t S_COL = 0;               // S^T of pair pj in buffer pj % SB: RP columns
-  static constexpr uint32_t O_COL = SB * RP;     // O^T of segment seg in buffer seg % OB
+  static constexpr int OCOLS = 3 * kRP;
+  static constexpr uint32_t S_COL = 0;               // S^T of pair pj in buffer pj % SB: kRP columns
+  static constexpr uint32_t O_COL = SB * kRP;     // O^T of segment seg in buffer seg % OB
   static_assert(O_COL + OB * OCOLS <= TMEM_COLS, "tensor memory");
   static constexpr int THREADS = (4 + NSW) * 32;
 };
@@ -109,10 +110,6 @@ struct Blocks8 {
   }
 };
 
-// Columns of tensor memory from `at` on.
-__device__ __forceinline__ void load_cols(uint32_t at, float (&v)[16]) { tmem_ld16(at, v); }
-__device__ __forceinline__ void load_cols(uint32_t at, float (&v)[8]) { tmem_ld8(at, v); }
-
 // Sums v[0 .. N) over the warp's lanes; lane l gets the sum of element l % N (N <= 32), in a fixed order.
 template <int N>
 __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
@@ -150,9 +147,9 @@ __device__ __forceinline__ void split4(uint32_t p01, uint32_t p23, uint32_t &a, 
   c = __byte_perm(c01, c23, 0x7531);
 }
 
-template <int HD, int RP>
-__global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
-  using C = A8Cfg<HD, RP>;
+template <int HD>
+__global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __grid_constant__ Attn8Params p) {
+  using C = A8Cfg<HD>;
   constexpr int ROWS = C::ROWS, NSW = C::NSW, T = NSW * 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -323,7 +320,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     for (int x = max(0, pj - C::NS); x < pj; ++x) mbar_wait_warp(&full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
   } else if (warp == kWS) {
     // ---------------- S issuer: S^T = K Q^T, the queries' two terms one after the other
-    constexpr uint32_t id = idesc_8bit_f32(128, RP);
+    constexpr uint32_t id = idesc_8bit_f32(128, kRP);
     const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(sK8)) : sw64_kmajor_desc(smem_u32(sK8));
     const uint64_t qd = HD == 128 ? sw128_kmajor_desc(smem_u32(sQ)) : sw64_kmajor_desc(smem_u32(sQ));
     int st = 0, ph = 0, pj = 0;
@@ -340,11 +337,11 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         if (!ok) break;
         tc_fence_after();
         const uint64_t kd = kd0 + static_cast<uint64_t>((st * C::PAIR8) >> 4);
-        const uint32_t d = tmem + C::S_COL + (pj % C::SB) * RP;
+        const uint32_t d = tmem + C::S_COL + (pj % C::SB) * kRP;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 2 * (HD / 32); ++kk)
-            tc_mma_8bit(d, kd + kk % (HD / 32) * 2, qd + kk % (HD / 32) * 2 + kk / (HD / 32) * (RP * HD >> 4), id,
+            tc_mma_8bit(d, kd + kk % (HD / 32) * 2, qd + kk % (HD / 32) * 2 + kk / (HD / 32) * (kRP * HD >> 4), id,
                         kk > 0 ? 1u : 0u);
           tc_commit(&s_full[pj & 1]);
         }
@@ -423,7 +420,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
     bool fail = false, gone = false;
 
     // The query rows of a segment, read a segment ahead.
-    constexpr int TPQ = T / RP, QW = HD / TPQ / 2;  // threads a row, words of a thread (8 or 4 or 2)
+    constexpr int TPQ = T / kRP, QW = HD / TPQ / 2;  // threads a row, words of a thread (4 or 2)
+    static_assert(ROWS == 8 && TPQ == 16, "widths of the accesses below");
     const int qrow = tid / TPQ, qpart = tid % TPQ;
     uint32_t qr[QW];
     auto fetch_q = [&](const Pos8 &a) {
@@ -435,11 +433,8 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         const uint2 u = have ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
         qr[0] = u.x, qr[1] = u.y;
       } else {
-#pragma unroll
-        for (int y = 0; y < QW; y += 4) {
-          const uint4 u = have ? reinterpret_cast<const uint4 *>(src)[y / 4] : make_uint4(0, 0, 0, 0);
-          qr[y] = u.x, qr[y + 1] = u.y, qr[y + 2] = u.z, qr[y + 3] = u.w;
-        }
+        const uint4 u = have ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+        qr[0] = u.x, qr[1] = u.y, qr[2] = u.z, qr[3] = u.w;
       }
     };
     // The rows are scaled by a power of two so that the largest value of a block of 16 rows lies in
@@ -468,7 +463,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       const bool apart = top == 128 || top - low > 3;
       const int exs = apart ? max(sexp[qrow], -100) : top;
       if (qpart == 0 && (qrow & 15) == 0)
-        sfac[RP + (qrow >> 4)] = apart ? -1.f : sl2 * __uint_as_float(static_cast<uint32_t>(top + 120) << 23);
+        sfac[kRP + (qrow >> 4)] = apart ? -1.f : sl2 * __uint_as_float(static_cast<uint32_t>(top + 120) << 23);
       const bool inf = exs == 128;                              // the row's outputs are NaN
       const int ex = min(exs, 127);
       const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(134 - ex) << 23);
@@ -484,14 +479,11 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         hi[y / 2] = y % 2 ? hi[y / 2] | (static_cast<uint32_t>(h) << 16) : h;
         lo[y / 2] = y % 2 ? lo[y / 2] | (static_cast<uint32_t>(l) << 16) : l;
       }
-      // rows r (hi) and RP + r (lo) of the operand, 16-byte chunks swizzled as a copy would
+      // rows r (hi) and kRP + r (lo) of the operand, 16-byte chunks swizzled as a copy would
       constexpr int BYTES = 2 * QW;                             // of a thread
       const int chunk = qpart * BYTES >> 4, xor8 = HD == 128 ? qrow & 7 : (qrow >> 1) & 3;
-      uint8_t *dh = sQ + qrow * HD + ((chunk ^ xor8) << 4) + (qpart * BYTES & 15), *dl = dh + RP * HD;
-      if constexpr (BYTES == 16) {
-        *reinterpret_cast<uint4 *>(dh) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(dl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      } else if constexpr (BYTES == 8) {
+      uint8_t *dh = sQ + qrow * HD + ((chunk ^ xor8) << 4) + (qpart * BYTES & 15), *dl = dh + kRP * HD;
+      if constexpr (BYTES == 8) {
         *reinterpret_cast<uint2 *>(dh) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2 *>(dl) = make_uint2(lo[0], lo[1]);
       } else {
@@ -522,7 +514,7 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
 #pragma unroll
       for (int c = 0; c < ROWS; c += 4)
         *reinterpret_cast<float4 *>(own + c) = *reinterpret_cast<const float4 *>(nref + r0 + c);
-      fac = sfac[RP + r0 / 16];
+      fac = sfac[kRP + r0 / 16];
     };
     keep_rows();
 #pragma unroll 1
@@ -560,10 +552,10 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
         // y = log2 of P: score in log2 units + log2 V scale - reference + kPBase
         float y[ROWS];
         float top = -INFINITY;
-        const uint32_t s_at = trow + C::S_COL + (pj % C::SB) * RP + r0;
+        const uint32_t s_at = trow + C::S_COL + (pj % C::SB) * kRP + r0;
         const float2 c2 = make_float2(sc.y + kPBase, sc.y + kPBase);
         float h[ROWS];
-        load_cols(s_at, h);
+        tmem_ld8(s_at, h);
         if (fac < 0.f) [[unlikely]] {    // the rows' factors are apart
 #pragma unroll
           for (int e = 0; e < ROWS; ++e) h[e] *= sfac[r0 + e];
@@ -609,11 +601,11 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
             const float m = warp_max(y[c]);
             mine = lane == c ? m : mine;
           }
-          if (lane < ROWS) red[quarter * RP + r0 + lane] = mine;
+          if (lane < ROWS) red[quarter * kRP + r0 + lane] = mine;
           named_bar_sync(1, T);
           float d = 0.f;                 // the row's reference moves by d
-          if (tid < RP) {
-            const float m = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
+          if (tid < kRP) {
+            const float m = fmaxf(fmaxf(red[tid], red[kRP + tid]), fmaxf(red[2 * kRP + tid], red[3 * kRP + tid]));
             if (tid < w.n * G && (u == 0 ? m > -INFINITY : m > kTop)) d = m - kPBase;
             srow[tid] = d;
             nref[tid] -= d;
@@ -637,16 +629,13 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
               tc_fence_after();
               float ov[3][ROWS];
 #pragma unroll
-              for (int t = 0; t < 3; ++t) load_cols(o_at + t * RP + r0, ov[t]);
+              for (int t = 0; t < 3; ++t) tmem_ld8(o_at + t * kRP + r0, ov[t]);
 #pragma unroll
               for (int t = 0; t < 3; ++t) {
                 uint32_t x[ROWS];
 #pragma unroll
                 for (int e = 0; e < ROWS; ++e) x[e] = __float_as_uint(ov[t][e] * sh[e]);
-                if constexpr (ROWS == 16)
-                  tmem_st16_raw(o_at + t * RP + r0, x);
-                else
-                  tmem_st8_raw(o_at + t * RP + r0, x);
+                tmem_st8_raw(o_at + t * kRP + r0, x);
               }
               tmem_wait_st();
             }
@@ -673,17 +662,13 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
           split4(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b), ta[e / 4],
                  tb[e / 4], tc[e / 4]);
         }
-        // column t * RP + row of the key's row, 16-byte chunks swizzled
+        // column t * kRP + row of the key's row, 16-byte chunks swizzled
         auto put = [&](int col, const uint32_t (&v)[ROWS / 4]) {
-          uint8_t *to = prow + (((col >> 4) ^ (key & 7)) << 4) + (col & 15);
-          if constexpr (ROWS == 16)
-            *reinterpret_cast<uint4 *>(to) = make_uint4(v[0], v[1], v[2], v[3]);
-          else
-            *reinterpret_cast<uint2 *>(to) = make_uint2(v[0], v[1]);
+          *reinterpret_cast<uint2 *>(prow + (((col >> 4) ^ (key & 7)) << 4) + (col & 15)) = make_uint2(v[0], v[1]);
         };
         put(r0, ta);
-        put(RP + r0, tb);
-        put(2 * RP + r0, tc);
+        put(kRP + r0, tb);
+        put(2 * kRP + r0, tc);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -696,10 +681,10 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       const int live = w.n * G;
       const size_t row0 = (static_cast<size_t>(w.i * p.Hkv + w.g) + blockIdx.x) * R;  // partial rows
       const float sum = lane_sums<ROWS>(lsum, lane);
-      if (lane < ROWS) red[quarter * RP + r0 + lane] = sum;
+      if (lane < ROWS) red[quarter * kRP + r0 + lane] = sum;
       named_bar_sync(1, T);
-      if (tid < RP) {
-        const float L = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
+      if (tid < kRP) {
+        const float L = (red[tid] + red[kRP + tid]) + (red[2 * kRP + tid] + red[3 * kRP + tid]);
         srow[tid] = whole ? 1.0f / L : 1.0f;
         if (!whole && tid < live)
           *reinterpret_cast<float2 *>(p.part_ml + (row0 + tid) * 2) =
@@ -716,11 +701,11 @@ __global__ void __launch_bounds__(A8Cfg<HD, RP>::THREADS, 1) attn8_kernel(const 
       // lane = column `key` of the head; a row is written by a warp's lanes together
       if (r0 < live) {
         float ov[ROWS];
-        load_cols(o_at + r0, ov);
+        tmem_ld8(o_at + r0, ov);
 #pragma unroll 1
         for (int t = 1; t < 3; ++t) {
           float x[ROWS];
-          load_cols(o_at + t * RP + r0, x);
+          tmem_ld8(o_at + t * kRP + r0, x);
 #pragma unroll
           for (int e = 0; e < ROWS; ++e) ov[e] += x[e];
         }
@@ -866,7 +851,7 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
 }
 
 // The dynamic shared memory limit is a property of the kernel on one device.
-template <int HD, int RP>
+template <int HD>
 static cudaError_t configure_attn8() {
   static std::mutex mutex;
   static bool done[64] = {};
@@ -875,17 +860,17 @@ static cudaError_t configure_attn8() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mutex);
   if (dev < 64 && done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(attn8_kernel<HD, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(A8Cfg<HD, RP>::SMEM));
+  e = cudaFuncSetAttribute(attn8_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(A8Cfg<HD>::SMEM));
   if (e == cudaSuccess && dev < 64) done[dev] = true;
   return e;
 }
 
-template <int HD, int RP>
+template <int HD>
 static cudaError_t launch_attn8(const Attn8Params &p, cudaStream_t s) {
-  cudaError_t e = configure_attn8<HD, RP>();
+  cudaError_t e = configure_attn8<HD>();
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn8_kernel<HD, RP>, dim3(p.grid), dim3(A8Cfg<HD, RP>::THREADS), A8Cfg<HD, RP>::SMEM, s, p);
+  return launch_pdl(attn8_kernel<HD>, dim3(p.grid), dim3(A8Cfg<HD>::THREADS), A8Cfg<HD>::SMEM, s, p);
 }
 
 template <int HD, int SPLIT>
@@ -906,9 +891,7 @@ static cudaError_t launch_rows(const Attn8Params &in, cudaStream_t s) {
   Attn8Params p = in;
   p.pair_cost = kPairCost;
   const int R = (p.Hq / p.Hkv) * p.m;
-  cudaError_t e = R <= 16   ? launch_attn8<HD, 16>(p, s)
-                  : R <= 32 ? launch_attn8<HD, 32>(p, s)
-                            : launch_attention8_wide(p, R, s);
+  cudaError_t e = R <= kRP ? launch_attn8<HD>(p, s) : launch_attention8_wide(p, R, s);
   if (e != cudaSuccess) return e;
   return p.nb * p.Hkv * kMerge8Warps <= p.grid ? launch_merge<HD, kMerge8Warps>(p, R, s) : launch_merge<HD, 1>(p, R, s);
 }
