@@ -24,13 +24,13 @@ struct WideCfg {
   static constexpr int UNIT8 = kUnit * HD;           // bytes of a unit's keys (or values) in the cache
   static constexpr int PAIR8 = 2 * UNIT8;
   // ring of pairs of units in 8 bits, keys then values, as much as shared memory holds
-  static constexpr int NS = 4 * (128 / HD);
+  static constexpr int NS = 3 * (128 / HD);
   static constexpr int ATOM16 = kUnit * 128;
   static constexpr int TILE16 = ATOMS * ATOM16;      // a unit's values in f16
   static constexpr int QPITCH = HD * 2 + 16;         // bytes of a query row (bf16): rows apart by 16 bytes mod 128
   static constexpr int STAGE = RHO == 1 ? 0 : 128 * HD / 4;  // floats of a half's exchange of O between copies
   static_assert(RHO <= 2, "copies exchange halves");
-  static constexpr int OFF_8 = 2 * TILE16;
+  static constexpr int OFF_8 = 4 * TILE16;            // values in f16: a pair's two units, two pairs
   static constexpr int OFF_Q = OFF_8 + NS * 2 * PAIR8;
   static constexpr int OFF_STG = OFF_Q + ROWS * QPITCH;
   static constexpr int OFF_ML = OFF_STG + 2 * STAGE * 4;  // [2 halves][128 lanes] (maximum, sum)
@@ -104,9 +104,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
   uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv8_empty = kv8_full + C::NS;
-  uint64_t *v16_full = kv8_empty + C::NS;   // [2] a pair's first and second unit
-  uint64_t *p_full = v16_full + 2;          // [2]
-  uint64_t *p_empty = p_full + 2;           // [2] PV complete: the P and V16 buffers have been read
+  uint64_t *v16_full = kv8_empty + C::NS;   // [4] values in f16: unit b of pair pj in buffer pj % 2 * 2 + b
+  uint64_t *v16_empty = v16_full + 4;       // [4] and read
+  uint64_t *p_full = v16_empty + 4;         // [2] a pair's first and second unit
+  uint64_t *p_empty = p_full + 2;           // [2] PV complete: the P buffer has been read
   uint64_t *sc_full = p_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
   uint64_t *sc_empty = sc_full + 2;         // [2]
   uint64_t *half_bar = sc_empty + 2;        // [2] the four warps of a half among themselves
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   uint64_t *o_free = seg_bar + 1;           // both O and ml read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 14 + 8) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((2 * C::NS + 20 + 8) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -134,7 +135,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       mbar_init(&kv8_empty[s], kNumConv + 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&v16_full[b], kNumConv);
+      for (int x = b; x < 4; x += 2) {
+        mbar_init(&v16_full[x], kNumConv);
+        mbar_init(&v16_empty[x], 1);
+      }
       mbar_init(&p_full[b], 4);
       mbar_init(&p_empty[b], 1);
       mbar_init(&sc_full[b], 1);
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         slot = 1;
       }
       // The chunk's scales, after its first copies are under way, and before any wait for a unit
-      // of the chunk: a copy waits for the pair NS > 3 before its own.
+      // of the chunk: a copy waits for the pair NS >= 3 before its own.
       published = published && k != 0;
       if (!published && (k == 3 || j == nunits - 1 || cnt_left == 0)) {
         published = true;
@@ -348,19 +352,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
 #pragma unroll 1
       for (int x = 0; x < ((cnt + 1) & ~1) && ok; ++x) {
         const int b = x & 1;
-        ok = mbar_wait_warp(&v16_full[b], pj & 1, p.max_spin);
-        ok = ok && mbar_wait_warp(&p_full[b], pj & 1, p.max_spin);
+        const int vb = (pj & 1) * 2 + b;
+        ok = mbar_wait_warp2(&v16_full[vb], (pj >> 1) & 1, &p_full[b], pj & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           if (x < cnt) {
-            const uint64_t vd = vd0 + static_cast<uint64_t>((b * C::TILE16) >> 4);
+            const uint64_t vd = vd0 + static_cast<uint64_t>((vb * C::TILE16) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kUnit / 16; ++kk)
               tc_mma_bf16_tmem_a(tmem + C::O_COL + b * HD, tmem + C::P_COL + b * 32 + kk * 8,
                                  vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, (x > 1 || kk > 0) ? 1u : 0u);
           }
           tc_commit(&p_empty[b]);
+          tc_commit(&v16_empty[vb]);
         }
         __syncwarp();
         pj += b;
@@ -393,10 +398,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       for (int x = 0; x < ((cnt + 1) & ~1); ++x, keys -= kUnit) {
         const int b = x & 1;
         if (b == 0) ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
-        ok = ok && (pj == 0 || mbar_wait_warp(&p_empty[b], (pj - 1) & 1, p.max_spin));
+        const int vb = (pj & 1) * 2 + b;
+        ok = ok && mbar_wait_warp(&v16_empty[vb], ((pj >> 1) - 1) & 1, p.max_spin);  // the first two: at once
         if (!ok) break;
         const uint8_t *src = src0 + st * 2 * C::PAIR8 + b * C::UNIT8;
-        uint8_t *dst = out + b * C::TILE16;
+        uint8_t *dst = out + vb * C::TILE16;
         if (x >= cnt) {
           // half a pair
         } else if (keys < kUnit) {
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         }
         fence_proxy_async_smem();
         __syncwarp();
-        mbar_arrive_if(&v16_full[b], lane == 0);
+        mbar_arrive_if(&v16_full[vb], lane == 0);
         if (b == 1) {
           mbar_arrive_if(&kv8_empty[st], lane == 0);
           ++pj;
