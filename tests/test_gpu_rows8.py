@@ -575,3 +575,97 @@ def test_attention8_wait_limit_is_reported():
     c.attend(0, 4, q, None, [100, 0, 400], False)
     assert c.status() == D.DFLASH_ERR_TIMEOUT
     assert c.status() == D.DFLASH_OK
+
+
+# ------------------------------------------------------------------ splits of the work
+
+@pytest.mark.parametrize("Hkv,hd,nb,R,paged", [(3, 128, 3, 1, True), (33, 64, 2, 2, False), (3, 128, 2, 3, True),
+                                               (5, 64, 2, 16, True), (3, 128, 2, 17, False), (33, 64, 1, 70, True),
+                                               (7, 128, 5, 700, True), (4, 64, 6, 1100, False)])
+def test_append8_row_slots_and_head_groups(Hkv, hd, nb, R, paged):
+    """Every number of row slots, single heads and several in a CTA, also a number that groups do not divide;
+    rows behind a sequence's own hold NaN."""
+    c = Cache(Hkv, Hkv, hd, -(-(R + 140) // PR) * PR, nb, N=1, paged=paged, seed=R)
+    _, k, v, _, gk = fused(nb, R, 1, Hkv, hd, seed=R, big=(0, 200.0))
+    k, v = k.clone(), v.clone()
+    ctx = [(61, 0, 130, 64, 63, 1)[i] for i in range(nb)]
+    n = [max(R - 5 * i, 0) for i in range(nb)]
+    for i in range(nb):
+        k[i * R + n[i]:(i + 1) * R] = float("nan")
+        v[i * R + n[i]:(i + 1) * R] = float("nan")
+    before = snap(c)
+    c.append8(0, R, k, v, n, ctx, gk, 1)
+    assert c.status() == 0
+    check_append8(c, 0, R, torch.nan_to_num(k), torch.nan_to_num(v), n, ctx, gk, 1, before)
+
+
+@pytest.mark.parametrize("Hq,hd,m,L", [(1, 128, 1, 20000), (16, 64, 1, 30001), (4, 128, 7, 20011), (8, 64, 16, 19990)])
+def test_attention8_one_pair_over_all_sms(Hq, hd, m, L):
+    """One sequence and one kv head: more parts to join than a warp has lanes."""
+    c = Cache(Hq, 1, hd, -(-(L + m) // PR) * PR, 1, N=1, B=max(m, 2), seed=m)
+    q = queries(c, m, seed=L)
+    out = c.attend(0, m, q, None, [L], True, hint=L)
+    assert c.status() == 0
+    check_attention(c, 0, m, q, [m], [L], True, out)
+
+
+@pytest.mark.parametrize("hd,Hq,m", [(64, 2, 2), (128, 4, 8)])
+def test_attention8_many_short_sequences(hd, Hq, m):
+    """300 sequences of zero to four blocks, every third without rows, some all the way at the front."""
+    nb = 300
+    c = Cache(Hq, 1, hd, 256, nb, N=1, seed=m)
+    q = queries(c, m, seed=3)
+    rng = np.random.default_rng(m)
+    ctx = [0 if i % 7 == 0 else int(x) for i, x in enumerate(rng.integers(0, 256 - m, nb))]
+    n = [0 if i % 3 == 1 or i < 2 else int(x) for i, x in enumerate(rng.integers(1, m + 1, nb))]
+    out = c.attend(0, m, q, n, ctx, True)
+    assert c.status() == 0
+    check_attention(c, 0, m, q, n, ctx, True, out)
+
+
+def test_calls_on_two_streams_and_two_graphs_of_one_workspace():
+    """Handles with workspaces of their own work side by side, and graphs captured with the same handle and
+    workspace replay in turn, each with its own lengths: all bitwise as one after the other."""
+    D, m = lib(), 4
+    sides = []
+    for s in range(2):
+        c = Cache(8, 2, 128, 4096, 3, N=1, seed=20 + s)
+        qr, k, v, gq, gk = fused(3, m, 8, 2, 128, seed=30 + s)
+        sides.append((c, qr, k, v, gq, gk, torch.empty(3, m, 8, 128, dtype=torch.bfloat16, device="cuda")))
+
+    def step(side, ctx, out):
+        c, qr, k, v, gq, gk, q = side
+        D.dflash_qk_norm_rope(c.h, 3, m, qr, qr.stride(0), None, 0, gq, None, ctx, q, None)
+        c.D.dflash_kv_append8(c.h, 3, 0, m, k, k.stride(0), v, v.stride(0), gk, 1, None, ctx, c.k8, c.v8, c.ks, c.vs,
+                              c.ws)
+        D.dflash_attention8(c.h, 3, 0, m, q, c.k8, c.v8, c.ks, c.vs, None, ctx, 0, 1, out, c.ws)
+
+    lens = [i32([4000, 1, 700]), i32([64, 3000, 2222])]
+    new = lambda: torch.full((3, m, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    want = [[new() for _ in lens] for _ in sides]
+    for s, side in enumerate(sides):
+        for _ in range(2):  # each length's rows lie in what the other reads: from the second round on they are there
+            for a, ctx in enumerate(lens):
+                step(side, ctx, want[s][a])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    got = [[new() for _ in lens] for _ in sides]
+    torch.cuda.synchronize()
+    for a, ctx in enumerate(lens):
+        for s, side in enumerate(sides):
+            with torch.cuda.stream(streams[s]):
+                step(side, ctx, got[s][a])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for a in range(2):
+            assert torch.equal(got[s][a], want[s][a]), (s, a)
+    graphs, outs = [], [new() for _ in lens]
+    for ctx, out in zip(lens, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(sides[0], ctx, out)
+    for a in (0, 1, 0, 1):
+        outs[a].fill_(7.0)
+        graphs[a].replay()
+        assert torch.equal(outs[a], want[0][a])
+    assert all(side[0].status() == 0 for side in sides)
