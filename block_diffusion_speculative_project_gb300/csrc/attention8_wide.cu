@@ -104,9 +104,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   float4 *sscale = reinterpret_cast<float4 *>(smem + C::OFF_SC);
   uint64_t *kv8_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv8_empty = kv8_full + C::NS;
-  uint64_t *v16_full = kv8_empty + C::NS;   // [4] values in f16: unit b of pair pj in buffer pj % 2 * 2 + b
-  uint64_t *v16_empty = v16_full + 4;       // [4] and read
-  uint64_t *p_full = v16_empty + 4;         // [2] a pair's first and second unit
+  uint64_t *v16_full = kv8_empty + C::NS;   // [2] values of pair pj in f16, in buffers pj % 2 * 2 + (0, 1)
+  uint64_t *v16_empty = v16_full + 2;       // [2] and read
+  uint64_t *p_full = v16_empty + 2;         // [2] a pair's first and second unit
   uint64_t *p_empty = p_full + 2;           // [2] PV complete: the P buffer has been read
   uint64_t *sc_full = p_empty + 2;          // [2] scales of 32 units, chunk c in buffer c % 2
   uint64_t *sc_empty = sc_full + 2;         // [2]
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   uint64_t *o_free = seg_bar + 1;           // both O and ml read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 20 + 8) * 8 + 16 <= 512, "barrier region overflows");
+  static_assert((2 * C::NS + 16 + 8) * 8 + 16 <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,10 +135,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       mbar_init(&kv8_empty[s], kNumConv + 1);
     }
     for (int b = 0; b < 2; ++b) {
-      for (int x = b; x < 4; x += 2) {
-        mbar_init(&v16_full[x], kNumConv);
-        mbar_init(&v16_empty[x], 1);
-      }
+      mbar_init(&v16_full[b], kNumConv);
+      mbar_init(&v16_empty[b], 1);
       mbar_init(&p_full[b], 4);
       mbar_init(&p_empty[b], 1);
       mbar_init(&sc_full[b], 1);
@@ -353,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       for (int x = 0; x < ((cnt + 1) & ~1) && ok; ++x) {
         const int b = x & 1;
         const int vb = (pj & 1) * 2 + b;
-        ok = mbar_wait_warp2(&v16_full[vb], (pj >> 1) & 1, &p_full[b], pj & 1, p.max_spin);
+        ok = mbar_wait_warp2(&v16_full[pj & 1], (pj >> 1) & 1, &p_full[b], pj & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -365,7 +363,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
                                  vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv, (x > 1 || kk > 0) ? 1u : 0u);
           }
           tc_commit(&p_empty[b]);
-          tc_commit(&v16_empty[vb]);
+          if (b == 1) tc_commit(&v16_empty[pj & 1]);
         }
         __syncwarp();
         pj += b;
@@ -395,41 +393,43 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       const int cnt = min(w.units - w.unit, nunits - j0);
       int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
 #pragma unroll 1
-      for (int x = 0; x < ((cnt + 1) & ~1); ++x, keys -= kUnit) {
-        const int b = x & 1;
-        if (b == 0) ok = mbar_wait_warp(&kv8_full[st], ph, p.max_spin);
-        const int vb = (pj & 1) * 2 + b;
-        ok = ok && mbar_wait_warp(&v16_empty[vb], ((pj >> 1) - 1) & 1, p.max_spin);  // the first two: at once
+      for (int u = 0; u < cnt; u += 2, ++pj, keys -= 2 * kUnit) {
+        // the pair's bytes, and its f16 buffers read by the pair before last (before the first two: at once)
+        ok = mbar_wait_warp2(&kv8_full[st], ph, &v16_empty[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
         if (!ok) break;
-        const uint8_t *src = src0 + st * 2 * C::PAIR8 + b * C::UNIT8;
-        uint8_t *dst = out + vb * C::TILE16;
-        if (x >= cnt) {
-          // half a pair
-        } else if (keys < kUnit) {
-          // rows beyond the last key may hold anything (even NaN); P is 0 there
+        const uint8_t *src = src0 + st * 2 * C::PAIR8;
+        uint8_t *dst = out + (pj & 1) * 2 * C::TILE16;
+        if (keys < 2 * kUnit || u + 1 >= cnt) [[unlikely]] {
+          // one unit alone, or rows beyond the last key, which may hold anything (even NaN); P is 0 there
+#pragma unroll 1
+          for (int b = 0; b < 2 && u + b < cnt; ++b) {
 #pragma unroll 2
-          for (int e = 0; e < PER; ++e) {
-            uint4 h = make_uint4(0, 0, 0, 0);
-            if (r0 + e * RPI < keys) h = widen8(*reinterpret_cast<const uint2 *>(src + e * RPI * HD));
-            *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = h;
+            for (int e = 0; e < PER; ++e) {
+              uint4 h = make_uint4(0, 0, 0, 0);
+              if (b * kUnit + r0 + e * RPI < keys)
+                h = widen8(*reinterpret_cast<const uint2 *>(src + b * C::UNIT8 + e * RPI * HD));
+              *reinterpret_cast<uint4 *>(dst + b * C::TILE16 + e * RPI * 128) = h;
+            }
           }
         } else {
-          uint2 u[PER];
 #pragma unroll
-          for (int e = 0; e < PER; ++e) u[e] = *reinterpret_cast<const uint2 *>(src + e * RPI * HD);
+          for (int b = 0; b < 2; ++b) {
+            uint2 v[PER];
 #pragma unroll
-          for (int e = 0; e < PER; ++e) *reinterpret_cast<uint4 *>(dst + e * RPI * 128) = widen8(u[e]);
+            for (int e = 0; e < PER; ++e)
+              v[e] = *reinterpret_cast<const uint2 *>(src + b * C::UNIT8 + e * RPI * HD);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+              *reinterpret_cast<uint4 *>(dst + b * C::TILE16 + e * RPI * 128) = widen8(v[e]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        mbar_arrive_if(&v16_full[vb], lane == 0);
-        if (b == 1) {
-          mbar_arrive_if(&kv8_empty[st], lane == 0);
-          ++pj;
-          if (++st == C::NS) {
-            st = 0;
-            ph ^= 1;
-          }
+        mbar_arrive_if(&v16_full[pj & 1], lane == 0);
+        mbar_arrive_if(&kv8_empty[st], lane == 0);
+        if (++st == C::NS) {
+          st = 0;
+          ph ^= 1;
         }
       }
       j0 += cnt;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
 #pragma unroll 1
       for (int u = half; u < ((cnt + 1) & ~1) + half; u += 2, ++pj) {
         const int j = min(j0 + u, j0 + cnt - 1);
-        if (chunk < (j >> 5)) {          // the next chunk: give the one before back
+        if (chunk < (j >> 5)) [[unlikely]] {  // the next chunk: give the one before back
           __syncwarp();
           if (chunk >= 0) mbar_arrive_if(&sc_empty[chunk & 1], lane == 0);
           ++chunk;
@@ -549,13 +549,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         st = st + 1 == C::NS ? 0 : st + 1;
         // the P buffer and O_half are free once PV of this half's previous unit has completed
         bool freed = pj == 0;
-        if (u >= cnt) {                  // half a pair
+        if (u >= cnt) [[unlikely]] {     // half a pair
           ok = freed || mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
           if (!ok) break;
           mbar_arrive_if(&p_full[half], lane == 0);
           continue;
         }
-        if (all - kUnit * u < kUnit) {   // some row does not see the whole unit
+        if (all - kUnit * u < kUnit) [[unlikely]] {  // some row does not see the whole unit
           const int nv = lim - (w.unit + u) * kUnit - k0;  // keys this thread sees of its part
 #pragma unroll
           for (int c = 0; c < KW; ++c) sv[c] = c < nv ? sv[c] : -INFINITY;
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
           m_run = m_new;
           l_run *= alpha;
         }
-        if (u >= 2 && __any_sync(0xffffffffu, need && r < R)) {
+        if (u >= 2 && __any_sync(0xffffffffu, need && r < R)) [[unlikely]] {
           ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
           if (!ok) break;
           tc_fence_after();
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         }
         const float2 lt = add2(ls[0], ls[1]);
         l_run = fmaf(lt.x + lt.y, sc.z, l_run);
-        if (sc.w == 0.f) {
+        if (sc.w == 0.f) [[unlikely]] {
 #pragma unroll
           for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
         }
