@@ -42,7 +42,7 @@ __device__ __forceinline__ long long block_of(const Attn8Params &p, int i, int g
 
 // A weight of T is split over G CTAs: the first T % G take one more than the others (the units are
 // below 2^25, as a handle's caches hold fewer than 2^31 rows, and T is at most 1 + pair_cost times that).
-__device__ __forceinline__ int cta_start(int T, int G, int c) { return c * (T / G) + min(c, T % G); }
+// The CTA that weight u lies in:
 __device__ __forceinline__ int cta_of(int T, int G, int u) {
   const int q = T / G, big = (T % G) * (q + 1);
   return u < big ? u / (q + 1) : T % G + (u - big) / q;
@@ -65,44 +65,62 @@ __device__ __forceinline__ int total_weight(const Attn8Params &p, int i, int lan
   return __reduce_add_sync(0xffffffffu, t) * p.Hkv;
 }
 
-// Where a CTA's range begins (pair i * Hkv + g, unit inside it) and its number of units, which is 0
-// for a range inside one pair's cost. Warp-collective.
-static __device__ void find_range(const Attn8Params &p, int cta, int lane, int *out) {
-  int base;
-  const int T = total_weight(p, 0, lane, &base);
+// x / d for quotients below 2^21: the float estimate is at most one off.
+__device__ __forceinline__ int div_near(int x, int d) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+  const int r = x - q * d;
+  q += r < 0 ? -1 : r >= d ? 1 : 0;
+  return q;
+}
+
+// A CTA's range: sequence, kv head and unit where it begins, its number of units (0 for a range inside one
+// pair's cost), and that sequence's rows, context and units.
+struct Range8 {
+  int i, g, unit, count, n, ctx, units;
+};
+// Warp-collective.
+static __device__ void find_range(const Attn8Params &p, int cta, int lane, Range8 *out) {
+  const Seq8 s0 = lane < p.nb ? seq8(p, lane) : Seq8{0, 0, 0};
+  int t = weight8(p, s0.units);
+#pragma unroll 1
+  for (int s = lane + 32; s < p.nb; s += 32) t += weight8(p, seq8(p, s).units);
+  const int T = __reduce_add_sync(0xffffffffu, t) * p.Hkv;
   const int Ge = min(T, p.grid);
-  int pair = 0, unit = 0, first = 0, last = 0;  // units of all pairs before the range's ends
+  Range8 at = {};
   if (cta < Ge) {
-    const int w0 = cta_start(T, Ge, cta), w1 = cta_start(T, Ge, cta + 1);
-    int pairs = 0;  // with units, before this chunk of sequences
+    const int each = div_near(T, Ge), more = T - each * Ge;
+    const int w0 = cta * each + min(cta, more), w1 = w0 + each + (cta < more ? 1 : 0);
+    int base = 0, pairs = 0;               // weight and pairs with units before this chunk of sequences
+    int first = 0, last = 0;               // units of all pairs before the range's ends
     bool ended = false;
 #pragma unroll 1
     for (int b = 0; b < p.nb && !ended; b += 32) {
-      const int U = b + lane < p.nb ? seq8(p, b + lane).units : 0;
-      const int W = weight8(p, U);
+      const Seq8 s = b == 0 ? s0 : b + lane < p.nb ? seq8(p, b + lane) : Seq8{0, 0, 0};
+      const int W = weight8(p, s.units);
       int v = p.Hkv * W;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
       }
-      const unsigned some = __ballot_sync(0xffffffffu, U > 0);
+      const unsigned some = __ballot_sync(0xffffffffu, s.units > 0);
       const int start = base + v - p.Hkv * W;  // of the lane's sequence
       const int units = start - p.pair_cost * (pairs + p.Hkv * __popc(some & ((1u << lane) - 1)));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int w = k == 0 ? w0 : w1;
-        const unsigned hit = __ballot_sync(0xffffffffu, start <= w && w < base + v);
+        const int x = (k == 0 ? w0 : w1) - start;
+        const unsigned hit = __ballot_sync(0xffffffffu, x >= 0 && x < p.Hkv * W);
         if (hit) {
-          const int off = (w - start) / max(W, 1), in = max((w - start) % max(W, 1) - p.pair_cost, 0);
+          const int g = div_near(x, max(W, 1)), in = max(x - g * W - p.pair_cost, 0);  // the lane that was hit counts
           const int l = __ffs(hit) - 1;
-          const int at = __shfl_sync(0xffffffffu, units + off * U + in, l);
+          const int before = __shfl_sync(0xffffffffu, units + g * s.units + in, l);
           if (k == 0) {
-            pair = (b + l) * p.Hkv + __shfl_sync(0xffffffffu, off, l);
-            unit = __shfl_sync(0xffffffffu, in, l);
-            first = at;
+            at = {b + l, __shfl_sync(0xffffffffu, g, l), __shfl_sync(0xffffffffu, in, l), 0,
+                  __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.ctx, l),
+                  __shfl_sync(0xffffffffu, s.units, l)};
+            first = before;
           } else {
-            last = at;
+            last = before;
             ended = true;
           }
         }
@@ -111,12 +129,9 @@ static __device__ void find_range(const Attn8Params &p, int cta, int lane, int *
       pairs += p.Hkv * __popc(some);
     }
     if (!ended) last = T - p.pair_cost * pairs;  // the last range: w1 = T
+    at.count = last - first;
   }
-  if (lane == 0) {
-    out[0] = pair;
-    out[1] = unit;
-    out[2] = last - first;
-  }
+  if (lane == 0) *out = at;
 }
 
 // Asks for the parameters that the split reads, so that they come while the launch before this one

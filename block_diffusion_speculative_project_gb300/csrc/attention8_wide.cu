@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   uint64_t *seg_bar = q_empty + 1;          // both halves: (maximum, sum) of a segment written
   uint64_t *o_free = seg_bar + 1;           // both O and ml read
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_free + 1);
-  int *sched = reinterpret_cast<int *>(tmem_slot + 1);
-  static_assert((2 * C::NS + 16 + 8) * 8 + 16 <= 512, "barrier region overflows");
+  Range8 *sched = reinterpret_cast<Range8 *>(tmem_slot + 1);
+  static_assert((2 * C::NS + 16 + 8) * 8 + 4 + sizeof(Range8) <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,12 +179,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int nunits = __shfl_sync(0xffffffffu, sched[2], 0);
-  Pos8 w;
-  w.i = sched[0] / p.Hkv;
-  w.g = sched[0] % p.Hkv;
-  w.unit = sched[1];
-  if (nunits > 0) pos_seq(w, p, sseq);
+  const int nunits = __shfl_sync(0xffffffffu, sched->count, 0);
+  Pos8 w = {sched->i, sched->g, sched->unit, sched->units, sched->n, sched->ctx};
 
   // Every role goes through the CTA's segments: `cnt` units from unit j0 of the CTA on, in pairs pj
   // of units u, u + 1 of the segment. A wait that runs out ends the role (ok = false).
