@@ -28,6 +28,12 @@ namespace df {
 // f16's range: half a step of the smallest is 2^-24 of the largest or less.
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
+//
+// What bounds it: HBM for long caches. 64 single tokens over 1024 .. 8191 keys (602 MB) take 95 us, 6.3
+// TB/s; under ncu (16 x 16,385 keys) 6.2 TB/s with the tensor pipe busy for 10% and 37% of the issue slots
+// used. A pair costs about 1150 cycles a CTA where the copies need 1260 for it; a segment costs about 4000
+// besides (queries, the first reference, sums, output). One token over 2047 rows takes 8.9 us, of which
+// reading the lengths and finding the range are 1, the queries 0.8, two units 1.3, the merge 2.5.
 constexpr int kRP = 16;  // query rows of a kv head, padded
 
 template <int HD>
@@ -744,7 +750,7 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
 // that the partial outputs load without waiting for one another. SPLIT is 8 where a pair has 8 parts
 // or more (128 rows of 19 parts: 12.5 -> 9.0 us with the attention of 32 units a pair before it; 512
 // rows of 19 parts 115 -> 107 us with the attention of 4096) and 1 with fewer, where most of the 8
-// warps had nothing (4096 rows of 3 parts: 34 us with 1, 44 with 8).
+// warps had nothing (4096 rows of 3 parts: 34 us with 1, 44 with 8, the attention included).
 constexpr int kMerge8Warps = 8;
 
 template <int HD, int SPLIT>
@@ -878,8 +884,8 @@ static cudaError_t launch_merge(const Attn8Params &p, int R, cudaStream_t s) {
 
 // What a pair costs besides its units, in units: the pipeline's start and end, the output rows. Even
 // ranges of units alone left the CTAs of many short pairs behind the others (64 sequences of 1024 ..
-// 8191 keys, 8 kv heads: 120 us at 0, 106 at 6, 104 at 8, 105 at 10; with 32 query rows 152, 138, 134
-// and 132).
+// 8191 keys, 8 kv heads, single tokens: 120 us at 0, 106 at 6, 104 at 8, 105 at 10; with 32 query rows
+// 122.3 at 8, 123.0 at 12).
 constexpr int kPairCost = 8;
 
 template <int HD>
@@ -887,6 +893,7 @@ static cudaError_t launch_rows(const Attn8Params &in, cudaStream_t s) {
   Attn8Params p = in;
   p.pair_cost = kPairCost;
   const int R = (p.Hq / p.Hkv) * p.m;
+  // both forms' times: attention8_wide.cu
   cudaError_t e = R <= kRP ? launch_attn8<HD>(p, s) : launch_attention8_wide(p, R, s);
   if (e != cudaSuccess) return e;
   return p.nb * p.Hkv * kMerge8Warps <= p.grid ? launch_merge<HD, kMerge8Warps>(p, R, s) : launch_merge<HD, 1>(p, R, s);

@@ -1,11 +1,16 @@
-// The 8-bit attention for more than 32 query rows of a kv head (attention8.cu has the formula, the
+// The 8-bit attention for more than 16 query rows of a kv head (attention8.cu has the formula, the
 // split over CTAs and the form for fewer rows): the query rows are the 128 rows of the MMA,
 //   S [rows][128 keys] = Q K^T     Q two e4m3 terms in tensor memory, K the cache's bytes
 //   O [rows][hd]      += P V       P f16 in tensor memory, V widened to f16 in shared memory
 // so that a softmax thread is a query row. Widening V costs the same for any number of rows; splitting
-// probabilities into 8-bit terms, as the form for few rows does, costs more than that from about 48
-// rows on (one 262,155-row context, 64 rows: 123 us in this form, 194 in the other; 32 rows of 64
-// ragged contexts: 163 and 161).
+// probabilities into 8-bit terms, as the form for few rows does, grows with them: 64 sequences of 1024
+// .. 8191 keys take 97 us there and 121 here with 16 rows, 127 and 122 with 32 (hd 64: 123 and 107);
+// one context of 262,147 keys with 32 rows 97 and 101.
+// What bounds it: the chain from role to role, beside shared memory's bandwidth (72 KB written and read for
+// a unit, 560 cycles of about 720): one context of 262,155 keys and 64 rows (537 MB) takes 101 to 104
+// us, 5.3 TB/s; under ncu (8 x 16,400 keys) DRAM is busy for 56%, the tensor pipe for 46%, and 42% of the
+// issue slots are used. Without the conversion instructions it took as long; with 8 converter warps,
+// which leaves the softmax fewer registers, 114; with the conversion in integer arithmetic 125.
 #include <mutex>
 
 #include "attention8.cuh"
@@ -52,10 +57,9 @@ struct WideCfg {
 constexpr float kPBase = 7.f, kRescale = 8.f;
 
 // A segment's units are taken in pairs: one S product of 128 keys, then softmax, PV and O for each
-// unit of the pair on its own. What bounds the kernel are the steps from one role to the next (with
-// every copy, product and exponential left out it still took 0.8 of its time, a unit at a time), so
-// they are paid for two units at once. Half a pair at the end of a segment of an odd number of units
-// is signalled by every role without work.
+// unit of the pair on its own, so that the steps from one role to the next are paid for two units at
+// once. Half a pair at the end of a segment of an odd number of units is signalled by every role
+// without work.
 // Warps: producer, S issuer, PV issuer, loader of queries, softmax half h = 0, 1 (a
 // pair's first or second unit) in 4 + 4h .. 7 + 4h (warp w reads TMEM lanes of quarter w % 4), then
 // the converters of V.
@@ -188,8 +192,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     // nothing to do
   } else if (warp == kWProd) {
     // ---------------- producer: a unit's keys and values are contiguous 64 * hd bytes each (the keys
-    // arrive swizzled, as the tensor cores read them), a query row hd bf16. Lane l looks up the block of unit 32 c + l of the CTA's range two chunks c
-    // ahead and its scales one chunk ahead, so the copies wait for neither.
+    // arrive swizzled, as the tensor cores read them). Lane l looks up the block of unit 32 c + l of the
+    // CTA's range two chunks c ahead and its scales one chunk ahead, so the copies wait for neither.
     const uint64_t pol = policy_evict_first();
     bool ok = !p.stall;
     int pairs = 0;

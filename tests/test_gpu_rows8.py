@@ -669,3 +669,49 @@ def test_calls_on_two_streams_and_two_graphs_of_one_workspace():
         graphs[a].replay()
         assert torch.equal(outs[a], want[0][a])
     assert all(side[0].status() == 0 for side in sides)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_drafter_with_both_caches(paged):
+    """Drafter(cache8=True): a prompt and a block appended to the bf16 and the 8-bit caches of one layer,
+    then the same rotated queries over either, each against the oracle on the rows that its cache
+    holds. The bf16 attention rounds its probabilities to bf16: 2^-8 of each."""
+    from block_diffusion_speculative_project_gb300 import drafter
+    w = di.TINY
+    nb, Cmax, m, layer = 2, 192, w.B, 1
+    dev = {k: drafter.to_device_bf16(v) for k, v in di.make_weights(w, 0).items()}
+    pps = Cmax // PR
+    dr = drafter.Drafter(w, dev, nb, Cmax, w.B, num_pages=nb * pps + 1 if paged else 0, cache8=True)
+    if paged:
+        table = np.random.default_rng(1).permutation(nb * pps + 1)[:nb * pps].reshape(nb, pps)
+        dr.set_block_table(i32(table))
+    lens, none = [100, 5], i32([0, 0])
+    ctx = i32(lens)
+    for R, n, at, seed in ((100, i32(lens), none, 1), (m, None, ctx, 2)):
+        q, k, v, gq, gk = fused(nb, R, w.Hq, w.Hkv, w.hd, seed=seed)
+        dr.kv_append(nb, layer, R, k, v, at, n_rows=n, g_k=gk)
+        dr.kv_append8(nb, layer, R, k, v, at, n_rows=n, g_k=gk)
+    rot = torch.empty(nb, m, w.Hq, w.hd, dtype=torch.bfloat16, device="cuda")
+    o16, o8 = torch.empty_like(rot), torch.empty_like(rot)
+    dr.qk_norm_rope(nb, m, q, None, ctx, rot, None, g_q=gq)
+    dr.attention(nb, layer, rot, ctx, o16)
+    dr.attention8(nb, layer, m, rot, ctx, o8)
+    assert dr.status() == 0
+
+    def rows(t, i, scale=None):
+        if paged:
+            x = f64(t[layer][table[i].tolist()]).transpose(1, 0, 2, 3)           # [Hkv, pps, 64, hd]
+            s = None if scale is None else f64(scale[layer][table[i].tolist()]).T
+        else:
+            x = f64(t[layer][i]).reshape(w.Hkv, pps, PR, w.hd)
+            s = None if scale is None else f64(scale[layer][i])
+        return (x if s is None else x * s[:, :, None, None]).reshape(w.Hkv, Cmax, w.hd)[:, :lens[i] + m]
+
+    for i in range(nb):
+        for out, K, V, step in ((o16, rows(dr.kcache, i), rows(dr.vcache, i), 2.0 ** -8),
+                                (o8, rows(dr.kcache8, i, dr.kscale), rows(dr.vcache8, i, dr.vscale),
+                                 2.0 ** -11 + 2.0 ** -10)):
+            o, mag, dot = orc.attention8(f64(rot[i]), K, V, lens[i], False)
+            tol = (2.0 ** -8 * np.abs(o) + mag * (step + 2.0 ** -16 + 2 * w.hd * 2.0 ** -24 * dot[..., None])
+                   + K.shape[1] * 2.0 ** -24 * np.abs(V).max())
+            assert_within(f64(out[i]), o, tol, f"sequence {i}")
