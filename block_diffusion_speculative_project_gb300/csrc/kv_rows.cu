@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(SLOTS *TPR < 128 ? 128 : SLOTS * TPR, SLOTS * 
   if (c0 < 0 || n == 0 || h0 >= h1) return;
   const int hi = static_cast<int>(min(static_cast<long long>(c0) + n, static_cast<long long>(p.Cmax)));
   const int blk = c0 / kPageRows + blockIdx.x;
+  if (blk > (hi - 1) / kPageRows) return;  // in blocks: a length near 2^31 times 64 would not fit
   const int row0 = blk * kPageRows;
-  if (row0 >= hi) return;
   long long block, bhead;  // (block, head 0) in the cache, in blocks of 64 rows, and the step to the next head
   if (p.page_table) {
     const int pg = p.page_table[static_cast<long long>(i) * p.pages_per_seq + blk];

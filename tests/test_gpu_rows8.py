@@ -715,3 +715,23 @@ def test_drafter_with_both_caches(paged):
             tol = (2.0 ** -8 * np.abs(o) + mag * (step + 2.0 ** -16 + 2 * w.hd * 2.0 ** -24 * dot[..., None])
                    + K.shape[1] * 2.0 ** -24 * np.abs(V).max())
             assert_within(f64(out[i]), o, tol, f"sequence {i}")
+
+
+@pytest.mark.parametrize("n,ctx", [(130, 2 ** 31 - 1), (130, 2 ** 31 - 64), (2 ** 31 - 1, 0), (-2 ** 31, 0),
+                                   (130, -2 ** 31), (130, 2 ** 31 - 200)])
+def test_lengths_at_the_ends_of_their_type(n, ctx):
+    """Counts and lengths that no cache has: reported, and nothing beyond the rows that exist is touched."""
+    c = Cache(2, 2, 64, 256, 2, N=1)
+    _, k, v, _, _ = fused(2, 130, 1, 2, 64, seed=2)
+    q = queries(c, 4)
+    writes = 0 <= ctx < 256 and n > 0
+    for call, names in ((c.append8, ("k8", "v8", "ks", "vs")), (c.append, ("kc", "vc"))):
+        before = {x: getattr(c, x).clone() for x in names}
+        call(0, 130, k, v, [0, n], [0, ctx])
+        assert c.status() == c.D.DFLASH_ERR_DEVICE_CHECK
+        for x in names:
+            same = torch.equal(getattr(c, x).view(torch.uint8), before[x].view(torch.uint8))
+            assert same != writes, x
+    out = c.attend(0, 4, q, [0, n], [0, ctx], True)
+    assert c.status() == c.D.DFLASH_ERR_DEVICE_CHECK
+    assert torch.isfinite(out.float()).all() and (out[0] == 7.0).all()
