@@ -60,7 +60,8 @@ struct A8Cfg {
   static constexpr int OFF_SC = OFF_ROW + kRP * 4;         // [2 chunks][32 units] scales
   static constexpr int OFF_BAR = OFF_SC + 64 * 16;
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
-  static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
+  static constexpr int OFF_NAN = OFF_SEQ + 128 * 8;       // [hd] first row that sees a NaN in the column
+  static constexpr size_t SMEM = 1024 + OFF_NAN + HD * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_REF % 16 == 0 && OFF_LIM % 16 == 0 &&
                     OFF_RED % 16 == 0 && OFF_SC % 16 == 0 && OFF_BAR % 16 == 0 && OFF_SEQ % 16 == 0,
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
   Range8 *sched = reinterpret_cast<Range8 *>(tmem_slot + 1);
   static_assert((4 * C::NS + 17) * 8 + 4 + sizeof(Range8) <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
+  int *first_nan = reinterpret_cast<int *>(smem + C::OFF_NAN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
@@ -583,18 +585,31 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
         for (int c = 0; c < ROWS; c += 2) top = max3(top, y[c], y[c + 1]);
         // rows of V that hold no value (beyond the last key, or of a scale of zero) may hold anything
         const bool bad = rg == 0 && (two || slot == 0) && (!there || sc.w != 0.f);
-        if (named_bar_or(1, T, u == 0 || top > kTop || bad || fail)) [[unlikely]] {
+        const bool some = rg == 0 && there && base + key >= every;  // seen by some rows: no NaN may stay
+        if (named_bar_or(1, T, u == 0 || top > kTop || bad || some || fail)) [[unlikely]] {
           // ---- now and then: the segment's first pair, a reference that has to move, values to clear
+          if (u == 0 && tid < HD) first_nan[tid] = kNoNan;
           if (named_bar_or(1, T, fail)) {
             gone = true;
             break;
           }
-          if (rg == 0 && __any_sync(0xffffffffu, bad)) {
+          if (rg == 0 && __any_sync(0xffffffffu, bad || some)) {
             fail |= !mbar_wait_warp(&v8_full[st], (pj / C::NS) & 1, p.max_spin);
+            uint4 *row = reinterpret_cast<uint4 *>(sV8 + st * C::PAIR8 + key * HD);
             if (bad) {
-              uint4 *row = reinterpret_cast<uint4 *>(sV8 + st * C::PAIR8 + key * HD);
 #pragma unroll
               for (int e = 0; e < HD / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
+            } else if (some) {
+#pragma unroll 1
+              for (int e = 0; e < HD / 16; ++e) {   // 16-byte chunks as a copy swizzles them
+                const int col = 16 * (e ^ (HD == 128 ? key & 7 : (key >> 1) & 3)), from = base + key - w.ctx;
+                uint4 v = row[e];
+                v.x = take_nan(v.x, first_nan, col, from);
+                v.y = take_nan(v.y, first_nan, col + 4, from);
+                v.z = take_nan(v.z, first_nan, col + 8, from);
+                v.w = take_nan(v.w, first_nan, col + 12, from);
+                row[e] = v;
+              }
             }
           }
           float mine = 0.f;
@@ -716,7 +731,7 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
         for (int e = 0; e < ROWS; ++e) {
           if (r0 + e >= live) break;
           if (HD == 128 || key < HD) {
-            const float v = ov[e] * srow[r0 + e];
+            const float v = jr < first_nan[key] ? ov[e] * srow[r0 + e] : __int_as_float(0x7FC00000);
             if (whole)
               o[(static_cast<size_t>(jr) * p.Hq + hr) * HD] = static_cast<uint16_t>(pack_bf16x2(v, v));
             else

@@ -149,6 +149,20 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// A NaN among values that only some query rows see would reach the others as well, as 0 * NaN in the product
+// of P and V. So it is taken out of the operand, and `first[column]` keeps the first row that sees one; that
+// row and those behind it get the NaN with their output. Returns the word without its NaN bytes, which
+// belong to the columns from col on and are seen from row `row` on.
+constexpr int kNoNan = 1 << 30;
+__device__ __forceinline__ uint32_t take_nan(uint32_t w, int *first, int col, int row) {
+  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  if (nan == 0) [[likely]] return w;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (nan >> (8 * b + 7) & 1) atomicMin(first + col + b, row);
+  return w & ~((nan >> 7) * 0xFFu);
+}
+
 // One of the warp's threads, the same one every time; the branch on it leaves the code around it
 // warp-uniform.
 __device__ __forceinline__ bool elect_one() {

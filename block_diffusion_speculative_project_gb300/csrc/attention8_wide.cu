@@ -42,7 +42,8 @@ struct WideCfg {
   static constexpr int OFF_SC = OFF_ML + 2 * 128 * 8;     // [2 chunks][32 units] scales
   static constexpr int OFF_BAR = OFF_SC + 64 * 16;
   static constexpr int OFF_SEQ = OFF_BAR + 512;           // [kSeqCache] (rows, context)
-  static constexpr size_t SMEM = 1024 + OFF_SEQ + 128 * 8;
+  static constexpr int OFF_NAN = OFF_SEQ + 128 * 8;       // [4 segments][hd] first row that sees a NaN in the column
+  static constexpr size_t SMEM = 1024 + OFF_NAN + 4 * HD * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0;                // S of a pair of units: 64 columns each
@@ -128,6 +129,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
   Range8 *sched = reinterpret_cast<Range8 *>(tmem_slot + 1);
   static_assert((2 * C::NS + 16 + 8) * 8 + 4 + sizeof(Range8) <= 512, "barrier region overflows");
   int2 *sseq = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
+  // Segment seg uses the part seg % 4. The softmax clears it behind seg_bar of seg + 1, past every read, and
+  // before it frees that segment's O; a converter gets to seg + 4 only after a PV of seg + 2, which waits
+  // for that.
+  int *first_nan = reinterpret_cast<int *>(smem + C::OFF_NAN);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv;
@@ -158,6 +163,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     mbar_init(o_free, 8);
     fence_mbar_init();
   }
+  for (int x = threadIdx.x; x < 4 * HD; x += kWideThreads) first_nan[x] = kNoNan;
   if (warp == kWS) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
@@ -389,9 +395,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     bool ok = true;
     int st = 0, ph = 0, pj = 0;
 #pragma unroll 1
-    for (int j0 = 0; j0 < nunits && ok;) {
+    for (int j0 = 0, seg = 0; j0 < nunits && ok; ++seg) {
       const int cnt = min(w.units - w.unit, nunits - j0);
       int keys = w.ctx + w.n - w.unit * kUnit;     // rows of the unit that hold keys
+      const int some = p.causal ? w.n - 1 : 0;     // the last of them are seen by some query rows only
 #pragma unroll 1
       for (int u = 0; u < cnt; u += 2, ++pj, keys -= 2 * kUnit) {
         // the pair's bytes, and its f16 buffers read by the pair before last (before the first two: at once)
@@ -399,15 +406,24 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         if (!ok) break;
         const uint8_t *src = src0 + st * 2 * C::PAIR8;
         uint8_t *dst = out + (pj & 1) * 2 * C::TILE16;
-        if (keys < 2 * kUnit || u + 1 >= cnt) [[unlikely]] {
-          // one unit alone, or rows beyond the last key, which may hold anything (even NaN); P is 0 there
+        if (keys - some < 2 * kUnit || u + 1 >= cnt) [[unlikely]] {
+          // one unit alone; rows that some queries see; rows beyond the last key, which may hold anything
+          // (even NaN): P is 0 there
 #pragma unroll 1
           for (int b = 0; b < 2 && u + b < cnt; ++b) {
 #pragma unroll 2
             for (int e = 0; e < PER; ++e) {
               uint4 h = make_uint4(0, 0, 0, 0);
-              if (b * kUnit + r0 + e * RPI < keys)
-                h = widen8(*reinterpret_cast<const uint2 *>(src + b * C::UNIT8 + e * RPI * HD));
+              const int row = b * kUnit + r0 + e * RPI;
+              if (row < keys) {
+                uint2 v = *reinterpret_cast<const uint2 *>(src + b * C::UNIT8 + e * RPI * HD);
+                if (row >= keys - some) {
+                  int *first = first_nan + (seg & 3) * HD;
+                  v.x = take_nan(v.x, first, cc * 8, row - keys + w.n);
+                  v.y = take_nan(v.y, first, cc * 8 + 4, row - keys + w.n);
+                }
+                h = widen8(v);
+              }
               *reinterpret_cast<uint4 *>(dst + b * C::TILE16 + e * RPI * 128) = h;
             }
           }
@@ -657,7 +673,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       // the next segment writes only after its seg_bar, past every read here.
       uint16_t *o = p.o + ((static_cast<size_t>(i) * p.m + jq) * p.Hq + g * G + r % G) * HD;
       float *po = p.part_o + (row0 + r) * HD;
-      auto put = [&](uint32_t col, const float (&v)[16]) {
+      int *first = first_nan + (seg & 3) * HD;
+      if (seg > 0 && half * 128 + tl < HD) first_nan[((seg - 1) & 3) * HD + half * 128 + tl] = kNoNan;
+      auto put = [&](uint32_t col, float (&v)[16]) {
+        if (p.causal) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) v[c] = jq < first[col + c] ? v[c] : __int_as_float(0x7FC00000);
+        }
         if (r < live && whole) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)

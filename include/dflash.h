@@ -371,9 +371,8 @@ DFLASH_API int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, co
  *               [0, ctx_len[i] + j + 1)
  *   out_o       bf16 [nb, m, Hq, hd]: softmax(q K^T / sqrt(hd)) V, query head h reading kv head
  *               h / (Hq/Hkv)
- * Cache rows beyond those that a sequence's queries attend to may hold anything. With `causal`, a NaN
- * among the values of the call's own rows reaches every query row of its kv head, in its column, also
- * the rows before it. Errors as dflash_attention; a length or
+ * Cache rows that a query row does not attend to may hold anything, NaN too. Errors as
+ * dflash_attention; a length or
  * count out of range is clamped and reported as DFLASH_ERR_DEVICE_CHECK by dflash_status, and a
  * page outside the pool is read as page 0 and reported. Bitwise reproducible as
  * dflash_draft_block is. */

@@ -735,3 +735,70 @@ def test_lengths_at_the_ends_of_their_type(n, ctx):
     out = c.attend(0, 4, q, [0, n], [0, ctx], True)
     assert c.status() == c.D.DFLASH_ERR_DEVICE_CHECK
     assert torch.isfinite(out.float()).all() and (out[0] == 7.0).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,hd,m", [(8, 2, 128, 4), (4, 2, 64, 7), (8, 2, 128, 8), (8, 2, 64, 16), (8, 1, 128, 16)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_attention8_causal_rows_do_not_see_a_later_nan(Hq, Hkv, hd, m, paged):
+    """NaN among the values of the call's own rows: in its column for the rows that attend to it, nowhere else;
+    new rows that end a block, begin one and lie on both sides of a border."""
+    ctx = [62, 640 - m, 64, 0, 505, 127]
+    nb = len(ctx)
+    c = Cache(Hq, Hkv, hd, 640, nb, N=1, paged=paged, seed=hd + m)
+    q = queries(c, m, seed=4)
+    n = [m, m, max(m - 1, 1), m, m, 1]
+    rng = np.random.default_rng(m)
+    nan = np.zeros((nb, Hkv, m, hd), bool)
+    for i in range(nb):
+        for h in range(Hkv):
+            for t in rng.permutation(n[i])[:2] if (i + h) % 3 else []:  # some heads keep all their values
+                nan[i, h, t, rng.permutation(hd)[:5]] = True
+    bytes8 = c.v8.view(torch.uint8)
+
+    def put(values):
+        for i, h, t, d in zip(*np.nonzero(nan)):
+            b, row = divmod(ctx[i] + int(t), PR)
+            bytes8[0][c.at(i, b)][h, row, int(d)] = values
+    put(0)
+    want = []
+    for i in range(nb):
+        K, V = (c.rows(x, 0, i, ctx[i] + n[i], s) for x, s in ((c.k8, c.ks), (c.v8, c.vs)))
+        want.append(orc.attention8(f64(q[i, :n[i]]), K, V, ctx[i], True) + (np.abs(V).max(), K.shape[1]))
+    for byte in (0x7F, 0xFF):
+        put(byte)
+        out = c.attend(0, m, q, n, ctx, True)
+        assert c.status() == 0
+        for i in range(nb):
+            o, mag, dot, vmax, L = want[i]
+            sees = np.repeat(np.cumsum(nan[i, :, :n[i]], axis=1).transpose(1, 0, 2) > 0, Hq // Hkv, axis=1)
+            got = f64(out[i, :n[i]])
+            assert np.array_equal(np.isnan(got), sees), f"sequence {i}"
+            tol = (2.0 ** -8 * np.abs(o) + mag * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -16 + 2 * hd * 2.0 ** -24 * dot[..., None])
+                   + L * 2.0 ** -24 * vmax)
+            assert_within(np.where(sees, o, got), o, tol, f"sequence {i}")
+            assert (out[i, n[i]:] == 7.0).all()
+    every = c.attend(0, m, q, n, ctx, False)  # without the mask every row attends to them
+    for i in range(nb):
+        sees = np.repeat(nan[i, :, :n[i]].any(axis=1), Hq // Hkv, axis=0)
+        assert np.array_equal(np.isnan(f64(every[i, :n[i]])), np.broadcast_to(sees, (n[i], Hq, hd))), f"sequence {i}"
+
+
+@pytest.mark.parametrize("Hq,Hkv,hd,m", [(8, 2, 128, 4), (8, 2, 64, 16), (8, 1, 128, 16)])
+def test_attention8_causal_rows_do_not_see_a_later_nan_key(Hq, Hkv, hd, m):
+    """A key of NaN: the rows that attend to it are NaN, those before it as without it."""
+    ctx, nb, t = [62, 320 - m, 64], 3, 2
+    c = Cache(Hq, Hkv, hd, 320, nb, N=1, seed=m)
+    q = queries(c, m, seed=4)
+    bytes8 = c.k8.view(torch.uint8)
+    for i in range(nb):
+        b, row = divmod(ctx[i] + t, PR)
+        bytes8[0][c.at(i, b)][:, row, 3] = 0x7F
+    out = c.attend(0, m, q, None, ctx, True)
+    assert c.status() == 0
+    assert torch.isnan(out[:, t:]).all()
+    for i in range(nb):
+        K, V = (c.rows(x, 0, i, ctx[i] + t, s) for x, s in ((c.k8, c.ks), (c.v8, c.vs)))
+        o, mag, dot = orc.attention8(f64(q[i, :t]), K, V, ctx[i], True)
+        tol = (2.0 ** -8 * np.abs(o) + mag * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -16 + 2 * hd * 2.0 ** -24 * dot[..., None])
+               + (K.shape[1] + m) * 2.0 ** -24 * np.abs(V).max())
+        assert_within(f64(out[i, :t]), o, tol, f"sequence {i}")
