@@ -322,7 +322,7 @@ struct Attn8Params {
   int stall;                 // test hook: issue no loads so the waits run out
 };
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s);
-// Its kernel for R = G*m > 32 query rows a kv head (attention8_wide.cu), without the merge.
+// Its kernel for R = G*m > 16 query rows a kv head (attention8_wide.cu), without the merge.
 cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 
 // Slots of partial outputs the attention of nb sequences may write: at most one per
