@@ -247,9 +247,9 @@ __global__ void __launch_bounds__(128, 5) kv_rows_kernel(const __grid_constant__
 // again only when the scale grows. A power of two loses nothing against amax / 448: e4m3 is a
 // floating format, and rescaling rows by a power of two is exact but for values that become
 // subnormal. It also joins 1 / norm exactly, so a value costs one product for both.
-// The values before their rounding to e4m3 are fp32's, off by 5e-8 on average, so one key in two million
+// The values before their rounding to e4m3 are fp32's, off by 5e-8 on average, so one key in 1.6 million
 // lies so near the middle of a step that it goes to the other side than in exact arithmetic (with the
-// norm, the gain and the rotation each rounded on its own, one in 1.2 million).
+// norm, the gain and the rotation each rounded on its own, one in 1.1 million).
 // Two prompts of up to 8189 rows (67 MB) take 15.0 us, 4.5 TB/s: a step from head to head is a chain of
 // norm, maximum over the block and scale, which the four warps a scheduler has room for hide in part. With
 // the angles in registers, which leaves room for no more, it was 15.6; with the heads' values
