@@ -4,11 +4,11 @@
 //   O [rows][hd]      += P V       P f16 in tensor memory, V widened to f16 in shared memory
 // so that a softmax thread is a query row. Widening V costs the same for any number of rows; splitting
 // probabilities into 8-bit terms, as the form for few rows does, grows with them: 64 sequences of 1024
-// .. 8191 keys take 97 us there and 121 here with 16 rows, 127 and 122 with 32 (hd 64: 123 and 107);
-// one context of 262,147 keys with 32 rows 97 and 101.
+// .. 8191 keys took 97 us there and 121 here with 16 rows, 127 and 122 with 32 (hd 64: 123 and 107);
+// one context of 262,147 keys with 32 rows 97 and 101. (Here it is 117 with 32 rows since.)
 // What bounds it: the chain from role to role, beside shared memory's bandwidth (72 KB written and read for
-// a unit, 560 cycles of about 720): one context of 262,155 keys and 64 rows (537 MB) takes 101 to 104
-// us, 5.3 TB/s; under ncu (8 x 16,400 keys) DRAM is busy for 56%, the tensor pipe for 46%, and 42% of the
+// a unit, 560 cycles of about 720): one context of 262,155 keys and 64 rows (537 MB) takes 100 us, 5.4
+// TB/s, and 112 for seconds on end, when the power limit holds the clock at 1.70 GHz; under ncu (8 x 16,400 keys) DRAM is busy for 56%, the tensor pipe for 46%, and 42% of the
 // issue slots are used. Without the conversion instructions it took as long; with 8 converter warps,
 // which leaves the softmax fewer registers, 114; with the conversion in integer arithmetic 125.
 #include <mutex>
