@@ -8,9 +8,10 @@
 // one context of 262,147 keys with 32 rows 97 and 101. (Here it is 117 with 32 rows since.)
 // What bounds it: the chain from role to role, beside shared memory's bandwidth (72 KB written and read for
 // a unit, 560 cycles of about 720): one context of 262,155 keys and 64 rows (537 MB) takes 100 us, 5.4
-// TB/s, and 112 for seconds on end, when the power limit holds the clock at 1.70 GHz; under ncu (8 x 16,400 keys) DRAM is busy for 56%, the tensor pipe for 46%, and 42% of the
-// issue slots are used. Without the conversion instructions it took as long; with 8 converter warps,
-// which leaves the softmax fewer registers, 114; with the conversion in integer arithmetic 125.
+// TB/s, and 112 for seconds on end, when the power limit holds the clock at 1.70 GHz; under ncu (8 x
+// 16,400 keys) DRAM is busy for 56%, the tensor pipe for 46%, and 42% of the issue slots are used.
+// Without the conversion instructions it took as long; with 8 converter warps, which leaves the softmax
+// fewer registers, 114; with the conversion in integer arithmetic 125.
 #include <mutex>
 
 #include "attention8.cuh"
