@@ -454,13 +454,15 @@ static cudaError_t launch_rows(KvRowsParams &p, bool append, int num_sms, cudaSt
   const int groups = (p.heads[0] + p.heads[1] + hpw - 1) / hpw;  // head groups of a row
   const long long rows = static_cast<long long>(p.nb) * p.R;
   // few rows: a warp for every head group (latency); many: the whole row in one warp, so that the factors
-  // are computed once for it (8191 rows of 40 heads: 29.9 us; with two groups a warp 61)
-  const long long target = static_cast<long long>(num_sms) * 16;
+  // are computed once for it (8191 rows of 40 heads: 29.9 us; with two groups a warp 61). Between them about
+  // 10 warps a SM and whole CTAs of warps, which all fit at once: 512 rows of 40 heads 4.3 us, at 16 a SM
+  // and with idle warps 5.4; 1024 appended rows 4.7 and 6.4; at 6 a SM 4.7 and 4.7.
+  const long long target = static_cast<long long>(num_sms) * 10;
   const int iters = static_cast<int>(std::min<long long>(groups, std::max<long long>(1, rows * groups / target)));
   const int parts = (groups + iters - 1) / iters;
   p.cta_rows = parts == 1 ? 4 : parts == 2 ? 2 : 1;
   const int per_row = 4 / p.cta_rows;
-  const int y = (parts + per_row - 1) / per_row;
+  const int y = iters == 1 ? (parts + per_row - 1) / per_row : std::max(1, parts / per_row);
   p.iters = (groups + y * per_row - 1) / (y * per_row);
   const dim3 grid(static_cast<unsigned>((rows + p.cta_rows - 1) / p.cta_rows), y);
   if (p.hd == 128)
