@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(128, 5) kv_rows_kernel(const __grid_constant__
 // The values before their rounding to e4m3 are fp32's, off by 5e-8 on average, so one key in 1.6 million
 // lies so near the middle of a step that it goes to the other side than in exact arithmetic (with the
 // norm, the gain and the rotation each rounded on its own, one in 1.1 million).
-// Two prompts of up to 8189 rows (67 MB) take 15.0 us, 4.5 TB/s: a step from head to head is a chain of
+// Two prompts of up to 8189 rows (67 MB) take 14.0 us, 4.8 TB/s: a step from head to head is a chain of
 // norm, maximum over the block and scale, which the four warps a scheduler has room for hide in part. With
 // the angles in registers, which leaves room for no more, it was 15.6; with the heads' values
 // asked for two to four steps ahead through shared memory 15 to 16.7.
@@ -372,12 +372,13 @@ __global__ void __launch_bounds__(SLOTS *TPR < 128 ? 128 : SLOTS * TPR, SLOTS * 
       }
     }
     // largest finite new value of the block (slots without a row hold zeros); a NaN is no maximum
-    float m = 0.f;
+    float m = 0.f, mb = 0.f;
 #pragma unroll
     for (int e = 0; e < W; ++e) {
-      m = fmaxf(fmaxf(m, fabsf(a[e].x)), fabsf(a[e].y));
-      m = fmaxf(fmaxf(m, fabsf(b[e].x)), fabsf(b[e].y));
+      m = max3(m, fabsf(a[e].x), fabsf(a[e].y));
+      mb = max3(mb, fabsf(b[e].x), fabsf(b[e].y));
     }
+    m = fmaxf(m, mb);
     if (m > FLT_MAX) {
       m = 0.f;
 #pragma unroll
@@ -394,18 +395,19 @@ __global__ void __launch_bounds__(SLOTS *TPR < 128 ? 128 : SLOTS * TPR, SLOTS * 
       float *to = red[(head - h0) & 1];     // two, so that one barrier a head is enough
       if ((tid & 31) == 0) to[tid >> 5] = m;
       __syncthreads();
-#pragma unroll
-      for (int q = 0; q < GT / 32; ++q) m = fmaxf(m, to[q]);
+      m = warp_max(to[tid % (GT / 32)]);
     }
     // smallest e with m <= 448 * 2^e = 1.75 * 2^(e + 8)
-    const uint32_t mb = __float_as_uint(m);
-    int ex = static_cast<int>(mb >> 23) - 127 - 8 + ((mb & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    const uint32_t bits = __float_as_uint(m);
+    int ex = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     ex = max(kScaleExpMin, min(ex, kScaleExpMax));
     const float s = fmaxf(__uint_as_float(static_cast<uint32_t>(ex + 127) << 23), s_old);
     const long long bi = block + head * bhead;
     uint8_t *dst = p.dst8[t] + bi * (kPageRows * HD) + d0;
     if (fresh) {
-      const float f = inv * (1.f / s);
+      // a scale that this call has not made need not be a power of two
+      const uint32_t sb = __float_as_uint(s);
+      const float f = inv * ((sb & 0x7FFFFFu) == 0 && sb < 0x7E800000u ? __uint_as_float(0x7F000000u - sb) : 1.f / s);
       const float2 f2 = make_float2(f, f);
       uint8_t *to = dst + (pos - row0) * HD;
       if constexpr (W == 1) {
