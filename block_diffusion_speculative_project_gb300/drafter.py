@@ -159,21 +159,67 @@ class Drafter:
         _d.dflash_attention(self.h, nb, layer, q, self.kcache, self.vcache, ctx_len, max_ctx_hint,
                             out_o, self.ws, stream)
 
+    def _rows(self, name, t, rows, heads):
+        """Row stride of t, which has to be bf16 [rows or more, heads * hd] with dense rows."""
+        self._mine(name, t, torch.bfloat16)
+        width = heads * self.shape.hd
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or t.stride(1) != 1:
+            raise ValueError(f"{name}: rows [{rows}, {width}] with values side by side, "
+                             f"got {tuple(t.shape)} with strides {t.stride()}")
+        return t.stride(0) if t.shape[0] > 1 else width
+
+    def _dense(self, name, t, count, dtype=torch.bfloat16):
+        self._mine(name, t, dtype)
+        if t.numel() < count or not t.is_contiguous():
+            raise ValueError(f"{name}: {count} values without gaps, got {tuple(t.shape)} with strides {t.stride()}")
+
+    def _mine(self, name, t, dtype):
+        if t.dtype != dtype or t.device != self.ws.device:
+            raise ValueError(f"{name}: {dtype} on {self.ws.device}, got {t.dtype} on {t.device}")
+
+    def _append_rows(self, nb, R, k, v, ctx_len, n_rows, g_k):
+        s = self.shape
+        ldk, ldv = self._rows("k", k, nb * R, s.Hkv), self._rows("v", v, nb * R, s.Hkv)
+        self._dense("ctx_len", ctx_len, nb, torch.int32)
+        if n_rows is not None:
+            self._dense("n_rows", n_rows, nb, torch.int32)
+        if g_k is not None:
+            self._dense("g_k", g_k, s.hd)
+        return ldk, ldv
+
     def qk_norm_rope(self, nb, R, q, k, pos0, out_q, out_k, g_q=None, g_k=None, stream=None):
         """q, k: rows [nb * R, heads * hd] of any row stride (k and out_k may be None)."""
-        _d.dflash_qk_norm_rope(self.h, nb, R, q, q.stride(0), k, 0 if k is None else k.stride(0), g_q, g_k, pos0,
-                               out_q, out_k, stream)
+        s = self.shape
+        ldq, ldk = self._rows("q", q, nb * R, s.Hq), 0
+        self._dense("out_q", out_q, nb * R * s.Hq * s.hd)
+        self._dense("pos0", pos0, nb, torch.int32)
+        if k is not None:
+            ldk = self._rows("k", k, nb * R, s.Hkv)
+        if out_k is not None:
+            self._dense("out_k", out_k, nb * R * s.Hkv * s.hd)
+        for name, g in (("g_q", g_q), ("g_k", g_k)):
+            if g is not None:
+                self._dense(name, g, s.hd)
+        _d.dflash_qk_norm_rope(self.h, nb, R, q, ldq, k, ldk, g_q, g_k, pos0, out_q, out_k, stream)
 
     def kv_append(self, nb, layer, R, k, v, ctx_len, n_rows=None, g_k=None, rotate=True, stream=None):
         """k, v: rows [nb * R, Hkv * hd] of any row stride."""
-        _d.dflash_kv_append(self.h, nb, layer, R, k, k.stride(0), v, v.stride(0), g_k, int(rotate), n_rows, ctx_len,
+        ldk, ldv = self._append_rows(nb, R, k, v, ctx_len, n_rows, g_k)
+        _d.dflash_kv_append(self.h, nb, layer, R, k, ldk, v, ldv, g_k, int(rotate), n_rows, ctx_len,
                             self.kcache, self.vcache, self.ws, stream)
 
     def kv_append8(self, nb, layer, R, k, v, ctx_len, n_rows=None, g_k=None, rotate=True, stream=None):
-        _d.dflash_kv_append8(self.h, nb, layer, R, k, k.stride(0), v, v.stride(0), g_k, int(rotate), n_rows, ctx_len,
+        ldk, ldv = self._append_rows(nb, R, k, v, ctx_len, n_rows, g_k)
+        _d.dflash_kv_append8(self.h, nb, layer, R, k, ldk, v, ldv, g_k, int(rotate), n_rows, ctx_len,
                              self.kcache8, self.vcache8, self.kscale, self.vscale, self.ws, stream)
 
     def attention8(self, nb, layer, m, q, ctx_len, out_o, n_rows=None, causal=False, max_ctx_hint=0, stream=None):
+        s = self.shape
+        self._dense("q", q, nb * m * s.Hq * s.hd)
+        self._dense("out_o", out_o, nb * m * s.Hq * s.hd)
+        self._dense("ctx_len", ctx_len, nb, torch.int32)
+        if n_rows is not None:
+            self._dense("n_rows", n_rows, nb, torch.int32)
         _d.dflash_attention8(self.h, nb, layer, m, q, self.kcache8, self.vcache8, self.kscale, self.vscale, n_rows,
                              ctx_len, max_ctx_hint, int(causal), out_o, self.ws, stream)
 

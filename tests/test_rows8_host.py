@@ -67,3 +67,70 @@ def test_null_handles_are_refused():
              lambda: d.LIB.dflash_attention8(N, 1, 0, 1, N, N, N, N, N, N, N, 0, 0, N, N, i, N)]
     for f in calls:
         assert f() == d.DFLASH_ERR_INVALID_ARG
+
+
+def stub_drafter(monkeypatch, calls):
+    """A Drafter without a handle on the CPU whose calls are noted instead of made."""
+    from types import SimpleNamespace
+
+    import torch
+
+    from block_diffusion_speculative_project_gb300 import drafter
+    dr = object.__new__(drafter.Drafter)
+    dr.h, dr.ws, dr.shape = None, torch.zeros(1), SimpleNamespace(Hq=4, Hkv=2, hd=64)
+    dr.kcache = dr.vcache = dr.kcache8 = dr.vcache8 = dr.kscale = dr.vscale = None
+    for name in ("qk_norm_rope", "kv_append", "kv_append8", "attention8"):
+        monkeypatch.setattr(drafter._d, "dflash_" + name, lambda *a, name=name: calls.append((name, a)))
+    return dr
+
+
+def test_drafter_refuses_rows_that_its_calls_would_read_past(monkeypatch):
+    """A row stride is taken from a tensor only if its rows are [nb * R, heads * hd]: the stride of a
+    [nb, R, heads * hd] tensor is R rows, and R times its length would be read."""
+    import torch
+    calls = []
+    dr = stub_drafter(monkeypatch, calls)
+    nb, R, bf16 = 2, 3, torch.bfloat16
+    i32 = torch.zeros(nb, dtype=torch.int32)
+    wide = torch.zeros(nb * R, 8 * 64, dtype=bf16)
+    q, k, v = wide.split([256, 128, 128], dim=1)
+    oq, ok = torch.zeros(nb, R, 4, 64, dtype=bf16), torch.zeros(nb, R, 2, 64, dtype=bf16)
+    g = torch.ones(64, dtype=bf16)
+
+    def norm(q=q, k=k, pos=i32, oq=oq, ok=ok, g=g):
+        dr.qk_norm_rope(nb, R, q, k, pos, oq, ok, g_q=g, g_k=g)
+
+    def both(k=k, v=v, ctx=i32, n=i32, g=g):
+        dr.kv_append(nb, 0, R, k, v, ctx, n_rows=n, g_k=g)
+
+    def app8(k=k, v=v, ctx=i32, n=i32, g=g):
+        dr.kv_append8(nb, 0, R, k, v, ctx, n_rows=n, g_k=g)
+
+    def att(q=oq, ctx=i32, o=oq, n=i32):
+        dr.attention8(nb, 0, R, q, ctx, o, n_rows=n)
+
+    for f in (norm, both, app8, att):
+        f()
+    assert [c[0] for c in calls] == ["qk_norm_rope", "kv_append", "kv_append8", "attention8"]
+    assert calls[0][1][4] == calls[0][1][6] == calls[1][1][5] == calls[2][1][7] == 8 * 64  # the row strides
+    norm(k=None, ok=None)
+    one = torch.zeros(1, 1, 128, dtype=bf16).expand(1, 1, 128)[:, 0]
+    dr.kv_append(1, 0, 1, one, one, i32)  # a single row has any stride
+    assert calls[-1][1][5] == 128
+    del calls[:]
+    three = torch.zeros(nb, R, 128, dtype=bf16)
+    longs = torch.zeros(nb, dtype=torch.int64)
+    rows = [three, three[:, 0], k[:nb * R - 1], k[:, :64], k.float(), torch.zeros(128, nb * R, dtype=bf16).t(),
+            torch.zeros(nb * R, 256, dtype=bf16)[:, ::2], k.to("meta")]
+    for x in rows:
+        for f, kw in ((norm, dict(k=x)), (both, dict(k=x)), (both, dict(v=x)), (app8, dict(k=x)), (app8, dict(v=x))):
+            with pytest.raises(ValueError):
+                f(**kw)
+    for f, kw in ((norm, dict(q=oq.view(nb, R, 256))), (norm, dict(q=k)), (norm, dict(pos=longs)), (norm, dict(pos=i32[:1])),
+                  (norm, dict(oq=oq[:1])), (norm, dict(ok=ok[..., :32])), (norm, dict(g=g[:32])), (norm, dict(g=g.float())),
+                  (both, dict(ctx=longs)), (both, dict(n=i32[:1])), (app8, dict(n=longs)), (app8, dict(g=g[:8])),
+                  (att, dict(q=ok)), (att, dict(o=oq[:, :2])), (att, dict(q=oq.transpose(1, 2))), (att, dict(o=oq.float())),
+                  (att, dict(ctx=longs)), (att, dict(n=i32[:1]))):
+        with pytest.raises(ValueError):
+            f(**kw)
+    assert not calls
