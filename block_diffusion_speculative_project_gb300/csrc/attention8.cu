@@ -25,7 +25,10 @@ namespace df {
 // thread. P's terms are columns of one pass over V; Q's are two passes over K, which the tensor cores
 // have the time for and which spare the softmax the second half of the columns.
 // Two e4m3 terms (4 bits each) hold bf16's 8 bits; three e5m2 terms keep 9 bits of a probability over
-// f16's range: half a step of the smallest is 2^-24 of the largest or less.
+// f16's range. The terms' products lie in columns of their own, so the second and third carry powers of two
+// (2^kSplit2, 2^kSplit3) that put what is left of small probabilities where e5m2 has its bits; the output takes them
+// back. What is lost is at most 2^-24 + 2^-25 (f16) where the largest is 2^kPBase: 2^-31 of it. (All terms alike
+// lost 2^-24 of the largest for every key, which is 40% of a key 2^23 below a sink.)
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
 //
@@ -75,7 +78,9 @@ struct A8Cfg {
 };
 // P is 2^(x - reference + kPBase) for x in log2 units; the reference moves (and O with it) only when a
 // key exceeds it by more than kRescale: P stays at most 2^15, which e5m2 and f16 hold.
-constexpr float kPBase = 7.f, kRescale = 8.f;
+constexpr float kPBase = 8.f, kRescale = 7.f;
+// The second term of p < 2^15 is below 2^12, the third at most 2^8: with these factors both stay at most 2^15.
+constexpr int kSplit2 = 3, kSplit3 = 7;
 
 // Warps: producer of values and scales, S issuer, PV issuer, producer of keys, softmax (warp w reads
 // TMEM lanes of quarter w % 4; rows of group (w - 4) / 4).
@@ -137,20 +142,23 @@ __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
   return s;
 }
 
-// Four probabilities (two f16 pairs, non-negative) as three e5m2 terms each, four to a word. e5m2 is
-// f16's upper byte: the first term cuts, the others round (half a step is 0x80, which carries into the
-// byte; the sums and differences are exact), so what is left is at most 2^-10 of the value.
+// Four probabilities (two f16 pairs, non-negative) as three e5m2 terms each, four to a word, the second times
+// 2^kSplit2 and the third times 2^kSplit3. e5m2 is f16's upper byte: the first term cuts, the others
+// round (half a step is 0x80, which carries into the byte; the sums, differences and products with powers of two
+// are exact), so what is left is at most 2^-10 of the value.
 __device__ __forceinline__ void split4(uint32_t p01, uint32_t p23, uint32_t &a, uint32_t &b, uint32_t &c) {
   constexpr uint32_t kUpper = 0xFF00FF00u, kHalf = 0x00800080u;
-  auto rest = [](uint32_t x, uint32_t y) {
+  auto rest = [](uint32_t x, uint32_t y, float times) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
-    return *reinterpret_cast<const uint32_t *>(&d);
+    const __half2 t = __hmul2(d, __float2half2_rn(times));
+    return *reinterpret_cast<const uint32_t *>(&t);
   };
+  constexpr float k2 = 1 << kSplit2, k3 = 1 << (kSplit3 - kSplit2);
   a = __byte_perm(p01, p23, 0x7531);
-  const uint32_t r01 = rest(p01, p01 & kUpper), r23 = rest(p23, p23 & kUpper);
+  const uint32_t r01 = rest(p01, p01 & kUpper, k2), r23 = rest(p23, p23 & kUpper, k2);
   const uint32_t b01 = r01 + kHalf, b23 = r23 + kHalf;
   b = __byte_perm(b01, b23, 0x7531);
-  const uint32_t c01 = rest(r01, b01 & kUpper) + kHalf, c23 = rest(r23, b23 & kUpper) + kHalf;
+  const uint32_t c01 = rest(r01, b01 & kUpper, k3) + kHalf, c23 = rest(r23, b23 & kUpper, k3) + kHalf;
   c = __byte_perm(c01, c23, 0x7531);
 }
 
@@ -723,8 +731,9 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
         for (int t = 1; t < 3; ++t) {
           float x[ROWS];
           tmem_ld8(o_at + t * kRP + r0, x);
+          const float f = t == 1 ? 1.f / (1 << kSplit2) : 1.f / (1 << kSplit3);
 #pragma unroll
-          for (int e = 0; e < ROWS; ++e) ov[e] += x[e];
+          for (int e = 0; e < ROWS; ++e) ov[e] = fmaf(x[e], f, ov[e]);
         }
         int jr = r0 / G, hr = r0 % G;
 #pragma unroll

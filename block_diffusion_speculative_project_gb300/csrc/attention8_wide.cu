@@ -54,11 +54,10 @@ struct WideCfg {
   static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
 };
 // P is 2^(x - m_run + kPBase), m_run the maximum at the last rescale: O is rescaled only when the
-// maximum has grown by more than 2^kRescale, so P stays at most 2^15 in f16, and what is 2^-16 of
-// the largest still has all 11 bits (2^-26 one bit; half a step of the smallest is 2^-27 of the largest).
-// With 2^8 to grow, which leaves f16's lower end more room, 64 verified blocks took 118.9 us, with 2^12 and
-// 2^14 117.2 and 116.4.
-constexpr float kPBase = 2.f, kRescale = 13.f;
+// maximum has grown by more than 2^kRescale, so P stays at most 2^15 in f16, and half a step of f16's smallest
+// values is 2^-32 of the largest probability. A maximum that may grow by 2^13 costs less (64 verified blocks 117.2 us,
+// 118.9 with 2^8), but with the largest at 2^2 it rounds keys 2^23 below a sink by up to a tenth.
+constexpr float kPBase = 7.f, kRescale = 8.f;
 
 // A segment's units are taken in pairs: one S product of 128 keys, then softmax, PV and O for each
 // unit of the pair on its own, so that the steps from one role to the next are paid for two units at

@@ -1,0 +1,104 @@
+"""The 8-bit attention in the state that long contexts put it in, in both of its forms (up to 16 query
+rows of a kv head, and more: up to 64 and up to 128): tens of pairs of units in one CTA, references that
+move inside a segment, attention sinks, scales far apart, queries with a channel that stands out.
+
+The reference is the formula in 64 bits on the device. Tolerances, besides those that
+test_gpu_rows8.py derives (one bf16 rounding 2^-8 |o|; of each probability 2^-11, 2^-10 and 2^-16;
+scores hd * 2^-24 * sum|q k| / sqrt(hd), which move a probability by twice that at most):
+  small probabilities  P is at least 2^8 (2^7 in the form for many rows) for the key that set the
+             reference. f16's smallest step is 2^-24, half of it 2^-25; in the form for few rows the
+             last e5m2 term has the smallest step 2^-16 after a factor 2^7: half of it 2^-24. Together
+             below 2^-31 of the largest p * V scale for every key: rows * 2^-31 * max p * max|e4m3 V| *
+             max scale
+"""
+import math
+
+import pytest
+import torch
+
+from test_gpu_rows8 import PR, Cache
+
+pytestmark = pytest.mark.gpu
+
+
+def held(c, name, scale, i, rows):
+    """[Hkv, rows, hd] of sequence i's cache in layer 0 in 64 bits, without and with the block scales."""
+    nblk = -(-rows // PR)
+    if c.table is not None:
+        idx = torch.as_tensor(c.table[i, :nblk], device="cuda").long()
+        x, s = getattr(c, name)[0][idx].transpose(0, 1), getattr(c, scale)[0][idx].t()
+    else:
+        x, s = getattr(c, name)[0][i, :, :nblk], getattr(c, scale)[0][i, :, :nblk]
+    raw = x.to(torch.float32).double()
+    full = (raw * s.double()[..., None, None]).reshape(c.Hkv, nblk * PR, c.hd)[:, :rows]
+    return raw.reshape(c.Hkv, nblk * PR, c.hd)[:, :rows], full, s.double()
+
+
+def check(c, q, n, ctx, causal, out, what=""):
+    """Every row of out against 64 bits; rows at n and behind hold 7."""
+    worst = 0.0
+    m, G = q.shape[1], c.Hq // c.Hkv
+    for i in range(len(ctx)):
+        assert (out[i, n[i]:] == 7.0).all(), f"{what}: rows behind sequence {i}"
+        if n[i] == 0:
+            continue
+        L = ctx[i] + n[i]
+        _, K, _ = held(c, "k8", "ks", i, L)
+        V8, V, vs = held(c, "v8", "vs", i, L)
+        pos = torch.arange(L, device="cuda")
+        end = (torch.arange(n[i], device="cuda") + ctx[i] + 1 if causal
+               else torch.full((n[i],), L, device="cuda")).repeat_interleave(G)
+        for h in range(c.Hkv):
+            qh = q[i, :n[i], h * G:(h + 1) * G].double().reshape(-1, c.hd)
+            x = qh @ K[h].t() / math.sqrt(c.hd)
+            x.masked_fill_(pos[None] >= end[:, None], -math.inf)
+            p = torch.softmax(x, dim=-1)
+            del x
+            o, mag = p @ V[h], p @ V[h].abs()
+            dot = (qh.abs() @ K[h].abs().t()).amax(dim=-1, keepdim=True) / math.sqrt(c.hd)
+            floor = L * 2.0 ** -31 * p.amax(dim=-1, keepdim=True) * V8[h].abs().max() * vs[h].max()
+            tol = 2.0 ** -8 * o.abs() + mag * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -16 + 2 * c.hd * 2.0 ** -24 * dot) + floor
+            got = out[i, :n[i], h * G:(h + 1) * G].double().reshape(-1, c.hd)
+            assert torch.isfinite(got).all(), f"{what}: sequence {i} head {h} not finite"
+            r = ((got - o).abs() / tol.clamp(min=1e-300)).max().item()
+            worst = max(worst, r)
+            assert r <= 1, f"{what}: sequence {i} kv head {h}: {r:.2f} of the tolerance"
+    return worst
+
+
+def block(c, name, i, b):
+    return getattr(c, name)[0][c.at(i, b)]
+
+
+def put8(t, value):
+    t.copy_(torch.full(t.shape, value, device="cuda").to(torch.float8_e4m3fn))
+
+
+# (hd, Hq, Hkv, rows m): 1 and 16 rows of a kv head in the form for few, 32 and 63 in the form for up to 64,
+# 96 and 128 in the one for more
+FORMS = [(128, 2, 2, 1), (64, 4, 1, 4), (128, 16, 2, 4), (64, 7, 1, 9), (128, 8, 1, 12), (64, 8, 1, 16)]
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+@pytest.mark.parametrize("below", [20.3, 23.54])
+def test_a_sink_whose_value_is_zero(hd, Hq, Hkv, m, below):
+    """The first key takes 2^below times the weight of each other, and its value is zero: the output is
+    what the others add up to."""
+    nb = 160 // Hkv
+    c = Cache(Hq, Hkv, hd, PR * 96, nb, N=1, B=max(m, 2), seed=3)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c.k8.view(torch.uint8).zero_()
+    c.v8.copy_((67 + 3 * torch.rand(c.v8.shape, generator=g, device="cuda")).to(torch.float8_e4m3fn))
+    c.ks.fill_(1.0)
+    c.vs.fill_(2.0 ** -6)
+    q = torch.zeros(nb, m, Hq, hd, dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = 1.0
+    # score of the sink in powers of two: k / sqrt(hd) / ln 2 * scale
+    for i in range(nb):
+        put8(block(c, "k8", i, 0)[:, 0, 5], 1.0)
+        put8(block(c, "v8", i, 0)[:, 0], 0.0)
+        block(c, "ks", i, 0)[:] = below * math.log(2) * math.sqrt(hd)
+    ctx = [PR * 95 - 3 * i for i in range(nb)]
+    out = c.attend(0, m, q, None, ctx, False)
+    assert c.status() == 0
+    check(c, q, [m] * nb, ctx, False, out)
