@@ -19,13 +19,16 @@ namespace df {
 
 // Both products read the cache's bytes as they are, with the keys and the head's columns as the 128
 // rows of the MMA and the query rows (kRP of them, padded) as its columns:
-//   S^T [128 keys][kRP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of two e4m3 terms
+//   S^T [128 keys][kRP]  = K [keys x hd, e4m3] Q^T, each query row as the sum of an e4m3 and two e5m2 terms
 //   O^T [hd][3 kRP]     += V^T [hd x keys, e4m3] P^T, each probability as the sum of three e5m2 terms
 // so nothing is widened, and a softmax thread (a TMEM lane) is one key, whose scale is a number of the
-// thread. P's terms are columns of one pass over V; Q's are two passes over K, which the tensor cores
-// have the time for and which spare the softmax the second half of the columns.
-// Two e4m3 terms (4 bits each) hold bf16's 8 bits; three e5m2 terms keep 9 bits of a probability over
-// f16's range. The terms' products lie in columns of their own, so the second and third carry powers of two
+// thread. P's terms are columns of one pass over V; Q's are three passes over K, which the tensor cores
+// have the time for and which spare the softmax the columns of the others.
+// Queries: what the first term leaves of bf16's 8 bits is at most 8 of their last steps, which e5m2's 3 bits
+// hold exactly, and its smallest step, 2^-16, lies far enough below: a query's values are exact from 2^-16 of the
+// largest of its block of rows on, and what is smaller is off by at most 2^-24 of that (put_q). Two e4m3 terms were
+// exact from 2^-9 on only, off by 2^-17 below, which shows where a channel of the queries stands out.
+// Probabilities: three e5m2 terms keep 9 bits over f16's range. The terms' products lie in columns of their own, so the second and third carry powers of two
 // (2^kSplit2, 2^kSplit3) that put what is left of small probabilities where e5m2 has its bits; the output takes them
 // back. What is lost is at most 2^-24 + 2^-25 (f16) where the largest is 2^kPBase: 2^-31 of it. (All terms alike
 // lost 2^-24 of the largest for every key, which is 40% of a key 2^23 below a sink.)
@@ -54,8 +57,8 @@ struct A8Cfg {
   static constexpr int P_BYTES = 128 * 128;          // P^T: 128 keys, rows of 128 bytes of which 3 kRP hold terms
   static constexpr int OFF_V8 = NS * PAIR8;
   static constexpr int OFF_P = 2 * NS * PAIR8;       // two buffers
-  static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;  // 2 kRP rows of hd bytes
-  static constexpr int OFF_REF = OFF_Q + 2 * kRP * HD;     // [kRP] -reference of a row
+  static constexpr int OFF_Q = OFF_P + 2 * P_BYTES;  // 3 kRP rows of hd bytes
+  static constexpr int OFF_REF = OFF_Q + 3 * kRP * HD;     // [kRP] -reference of a row
   static constexpr int OFF_FAC = OFF_REF + kRP * 4;        // [kRP] factor of a row, [kRP / 16] of a block of rows
   static constexpr int OFF_LIM = OFF_FAC + kRP * 4 + 64;        // [kRP] keys that a row sees
   static constexpr int OFF_RED = OFF_LIM + kRP * 4;        // [4][kRP] a quarter's maxima, sums
@@ -331,8 +334,9 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
 #pragma unroll 1
     for (int x = max(0, pj - C::NS); x < pj; ++x) mbar_wait_warp(&full[x % C::NS], (x / C::NS) & 1, kDrainSpin);
   } else if (warp == kWS) {
-    // ---------------- S issuer: S^T = K Q^T, the queries' two terms one after the other
+    // ---------------- S issuer: S^T = K Q^T, the queries' three terms one after the other
     constexpr uint32_t id = idesc_8bit_f32(128, kRP);
+    constexpr int STEPS = HD / 32;       // MMAs of a term
     const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(sK8)) : sw64_kmajor_desc(smem_u32(sK8));
     const uint64_t qd = HD == 128 ? sw128_kmajor_desc(smem_u32(sQ)) : sw64_kmajor_desc(smem_u32(sQ));
     int st = 0, ph = 0, pj = 0;
@@ -352,9 +356,9 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
         const uint32_t d = tmem + C::S_COL + (pj % C::SB) * kRP;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 2 * (HD / 32); ++kk)
-            tc_mma_8bit(d, kd + kk % (HD / 32) * 2, qd + kk % (HD / 32) * 2 + kk / (HD / 32) * (kRP * HD >> 4), id,
-                        kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 3 * STEPS; ++kk)
+            tc_mma_8bit(d, kd + kk % STEPS * 2, qd + kk % STEPS * 2 + kk / STEPS * (kRP * HD >> 4),
+                        kk < STEPS ? id : id | kIdescBE5M2, kk > 0 ? 1u : 0u);
           tc_commit(&s_full[pj & 1]);
         }
         __syncwarp();
@@ -450,9 +454,9 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
       }
     };
     // The rows are scaled by a power of two so that the largest value of a block of 16 rows lies in
-    // [2^7, 2^8), and stored as hi + lo, e4m3: bf16's 8 bits exactly down to 2^-10 of that value, below
-    // to 2^-18 of it. A block whose rows' largest values differ by more than 2^3 scales every row on its
-    // own (the block's factor is then -1). Two barriers.
+    // [2^7, 2^8), and stored as an e4m3 term and two e5m2 terms of what is left. A block whose rows'
+    // largest values differ by more than 2^3 scales every row on its own (the block's factor is then -1).
+    // Two barriers.
     auto put_q = [&](const Pos8 &a) {
       int *sexp = reinterpret_cast<int *>(red);
       float am = 0.f;
@@ -479,28 +483,30 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
       const bool inf = exs == 128;                              // the row's outputs are NaN
       const int ex = min(exs, 127);
       const float mul = inf ? __int_as_float(0x7FC00000) : __uint_as_float(static_cast<uint32_t>(134 - ex) << 23);
-      uint32_t hi[QW / 2], lo[QW / 2];
+      uint32_t term[3][QW / 2];
 #pragma unroll
       for (int y = 0; y < QW; ++y) {
-        const float2 q = make_float2(__uint_as_float(qr[y] << 16) * mul, __uint_as_float(qr[y] & 0xFFFF0000u) * mul);
-        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
-        const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-        const __nv_fp8x2_storage_t l =
-            __nv_cvt_float2_to_fp8x2(make_float2(q.x - hf.x, q.y - hf.y), __NV_SATFINITE, __NV_E4M3);
-        hi[y / 2] = y % 2 ? hi[y / 2] | (static_cast<uint32_t>(h) << 16) : h;
-        lo[y / 2] = y % 2 ? lo[y / 2] | (static_cast<uint32_t>(l) << 16) : l;
+        float2 q = make_float2(__uint_as_float(qr[y] << 16) * mul, __uint_as_float(qr[y] & 0xFFFF0000u) * mul);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          const __nv_fp8_interpretation_t kind = t == 0 ? __NV_E4M3 : __NV_E5M2;
+          const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, kind);
+          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, kind);
+          const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+          q = make_float2(q.x - hf.x, q.y - hf.y);  // exact
+          term[t][y / 2] = y % 2 ? term[t][y / 2] | (static_cast<uint32_t>(h) << 16) : h;
+        }
       }
-      // rows r (hi) and kRP + r (lo) of the operand, 16-byte chunks swizzled as a copy would
+      // rows t kRP + r of the operand, 16-byte chunks swizzled as a copy would
       constexpr int BYTES = 2 * QW;                             // of a thread
       const int chunk = qpart * BYTES >> 4, xor8 = HD == 128 ? qrow & 7 : (qrow >> 1) & 3;
-      uint8_t *dh = sQ + qrow * HD + ((chunk ^ xor8) << 4) + (qpart * BYTES & 15), *dl = dh + kRP * HD;
-      if constexpr (BYTES == 8) {
-        *reinterpret_cast<uint2 *>(dh) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2 *>(dl) = make_uint2(lo[0], lo[1]);
-      } else {
-        *reinterpret_cast<uint32_t *>(dh) = hi[0];
-        *reinterpret_cast<uint32_t *>(dl) = lo[0];
+      uint8_t *dst = sQ + qrow * HD + ((chunk ^ xor8) << 4) + (qpart * BYTES & 15);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        if constexpr (BYTES == 8)
+          *reinterpret_cast<uint2 *>(dst + t * (kRP * HD)) = make_uint2(term[t][0], term[t][1]);
+        else
+          *reinterpret_cast<uint32_t *>(dst + t * (kRP * HD)) = term[t][0];
       }
       if (qpart == 0) {
         // the factor takes S to log2 units, 1/sqrt(hd) included; rows that are not there get P = 0

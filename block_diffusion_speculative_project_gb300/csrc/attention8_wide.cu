@@ -1,6 +1,6 @@
 // The 8-bit attention for more than 16 query rows of a kv head (attention8.cu has the formula, the
 // split over CTAs and the form for fewer rows): the query rows are the 128 rows of the MMA,
-//   S [rows][128 keys] = Q K^T     Q two e4m3 terms in tensor memory, K the cache's bytes
+//   S [rows][128 keys] = Q K^T     Q an e4m3 and an e5m2 term in tensor memory, K the cache's bytes
 //   O [rows][hd]      += P V       P f16 in tensor memory, V widened to f16 in shared memory
 // so that a softmax thread is a query row. Widening V costs the same for any number of rows; splitting
 // probabilities into 8-bit terms, as the form for few rows does, grows with them: 64 sequences of 1024
@@ -49,7 +49,7 @@ struct WideCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0;                // S of a pair of units: 64 columns each
   static constexpr uint32_t O_COL = 128;              // O_0, O_1: hd columns each
-  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // queries, two e4m3 terms: hd / 4 columns each
+  static constexpr uint32_t Q_COL = 128 + 2 * HD;     // queries, two terms of 8 bits: hd / 4 columns each
   static constexpr uint32_t P_COL = Q_COL + HD / 2;   // P of a pair's units: 32 columns each
   static_assert(P_COL + 64 <= TMEM_COLS, "tensor memory");
 };
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
     if (!ok && !p.stall && lane == 0) flag_status(p.status, kStatusTimeout);
     cp_async_wait_all();
   } else if (warp == kWS) {
-    // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two e4m3
+    // ---------------- S issuer: S(j) = Q K(j)^T straight from the 8-bit keys, the queries' two
     // terms one after the other from tensor memory
     constexpr uint32_t id_s = idesc_8bit_f32(128, kUnit);
     const uint64_t kd0 = HD == 128 ? sw128_kmajor_desc(smem_u32(s8)) : sw64_kmajor_desc(smem_u32(s8));
@@ -325,8 +325,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 2 * HD / 32; ++kk)
-            tc_mma_e4m3_tmem_a(tmem + C::S_COL, tmem + C::Q_COL + kk * 8,
-                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4), id, kk > 0 ? 1u : 0u);
+            tc_mma_8bit_tmem_a(tmem + C::S_COL, tmem + C::Q_COL + kk * 8,
+                               kd + static_cast<uint64_t>((kk % (HD / 32)) * 32 >> 4),
+                               kk < HD / 32 ? id : id | kIdescAE5M2, kk > 0 ? 1u : 0u);
           tc_commit(s_full);
           if (u + 2 >= cnt) tc_commit(q_empty);
         }
@@ -479,8 +480,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
       tmem_wait_st();
     }
     // The query row of segment `seg` (n rows a sequence), scaled by a power of two so that its
-    // largest value lies in [2^7, 2^8), to tensor memory as the sum of two e4m3 terms: 4 bits each
-    // hold bf16's 8, exactly down to 2^-10 of the largest value, below that to 2^-18 of it.
+    // largest value lies in [2^7, 2^8), to tensor memory as the sum of an e4m3 term and an e5m2 term of what is left
+    // (at most 8 steps of bf16's last bit, which 3 bits hold): exact from 2^-13 of the largest value on, and
+    // off by at most 2^-21 of it below. (Two e4m3 terms: from 2^-9 on, 2^-17 below.)
     // Returns the factor that takes S to log2 units, 1/sqrt(hd) included; < 0 on a wait run out.
     auto load_q = [&](int seg, int n) {
       bool ok = mbar_wait_warp(q8_full, seg & 1, p.max_spin);
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
             const __half2_raw ar = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
             const float2 af = __half22float2(*reinterpret_cast<const __half2 *>(&ar));
             const __nv_fp8x2_storage_t b =
-                __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E4M3);
+                __nv_cvt_float2_to_fp8x2(make_float2(y.x - af.x, y.y - af.y), __NV_SATFINITE, __NV_E5M2);
             const int d = 2 * e + f / 2;
             hi[d] = f % 2 ? hi[d] | (static_cast<uint32_t>(a) << 16) : a;
             lo[d] = f % 2 ? lo[d] | (static_cast<uint32_t>(b) << 16) : b;

@@ -361,9 +361,9 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, e4m3 inputs, fp32 accumulate (kind::f8f6f4): four consecutive
+// D[tmem] (+)= A[tmem] * B[smem]^T, 8-bit inputs, fp32 accumulate (kind::f8f6f4): four consecutive
 // K elements of a row per 32-bit column of its lane, 32 per instruction.
-__device__ __forceinline__ void tc_mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+__device__ __forceinline__ void tc_mma_8bit_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                                    uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -448,11 +448,12 @@ constexpr uint32_t kIdescAMajorMN = 1u << 15;
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Instruction descriptor, kind::f8f6f4: D fp32, A e4m3 (format 0), B e4m3, or e5m2 (format 1) with
-// kIdescBE5M2.
+// Instruction descriptor, kind::f8f6f4: D fp32, A and B e4m3 (format 0), or e5m2 (format 1) with
+// kIdescAE5M2 and kIdescBE5M2.
 __host__ __device__ constexpr uint32_t idesc_8bit_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+constexpr uint32_t kIdescAE5M2 = 1u << 7;
 constexpr uint32_t kIdescBE5M2 = 1u << 10;
 
 // ------------------------------------------------------------------ programmatic launch

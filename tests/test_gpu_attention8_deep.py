@@ -10,6 +10,7 @@ scores hd * 2^-24 * sum|q k| / sqrt(hd), which move a probability by twice that 
              last e5m2 term has the smallest step 2^-16 after a factor 2^7: half of it 2^-24. Together
              below 2^-31 of the largest p * V scale for every key: rows * 2^-31 * max p * max|e4m3 V| *
              max scale
+  queries    bf16 exactly for what is at least 2^-13 of a row's largest value
 """
 import math
 
@@ -102,3 +103,27 @@ def test_a_sink_whose_value_is_zero(hd, Hq, Hkv, m, below):
     out = c.attend(0, m, q, None, ctx, False)
     assert c.status() == 0
     check(c, q, [m] * nb, ctx, False, out)
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+def test_queries_with_a_channel_that_stands_out(hd, Hq, Hkv, m):
+    """One channel of every query row is 2^10 to 2^13 times the others that count, and the keys are zero in
+    it: the scores are those of the small ones, which bf16 holds to 8 bits. Rows of one kv head differ
+    by up to 2^3."""
+    nb = 12
+    c = Cache(Hq, Hkv, hd, 128, nb, N=1, B=max(m, 2), seed=4)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    u = lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    sign = lambda *s: torch.where(u(*s) < 0.5, -1.0, 1.0)  # noqa: E731
+    q = torch.zeros(nb, m, Hq, hd, device="cuda")
+    top = torch.exp2(torch.floor(u(nb, m, Hq) * 4))
+    q[..., 0] = top * 1.5
+    q[..., 1:4] = sign(nb, m, Hq, 3) * (1 + u(nb, m, Hq, 3)) * top[..., None] * torch.exp2(-10 - torch.floor(u(nb, m, Hq, 3) * 3))
+    q = q.to(torch.bfloat16)
+    c.k8.view(torch.uint8).zero_()
+    c.k8[..., 1:4] = (sign(*c.k8.shape[:-1], 3) * (200 + 248 * u(*c.k8.shape[:-1], 3))).to(torch.float8_e4m3fn)
+    c.ks.fill_(16.0)
+    ctx = [1 + i % 5 for i in range(nb)]
+    out = c.attend(0, m, q, None, ctx, True)
+    assert c.status() == 0
+    check(c, q, [m] * nb, ctx, True, out)
