@@ -312,9 +312,7 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
             const int b = chunk & 1;
             ok = chunk < 2 || mbar_wait_warp(&sc_empty[b], ((chunk >> 1) - 1) & 1, p.max_spin);
             if (!ok) break;
-            const bool zero = vs == 0.f;  // a block of zeros: its bytes do not count
-            sscale[b * 32 + lane] =
-                make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 1.f : 0.f);
+            sscale[b * 32 + lane] = scale_terms(ks, vs);
             __syncwarp();
             mbar_arrive_if(&sc_full[b], lane == 0);
             ++chunk;
@@ -563,7 +561,7 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
           ++freed;
         }
         const int js = two ? j + slot : j;
-        const float4 sc = sscale[((js >> 5) & 1) * 32 + (js & 31)];  // K scale, log2 V, 1 / V, 1 for zeros
+        const float4 sc = sscale[((js >> 5) & 1) * 32 + (js & 31)];  // scale_terms
         // S^T, and that P^T's buffer was read by the pair before last (before the first two: at once)
         fail |= !mbar_wait_warp2(&s_full[pj & 1], (pj >> 1) & 1, &pv_done[pj & 1], ((pj >> 1) - 1) & 1, p.max_spin);
         tc_fence_after();
@@ -598,10 +596,10 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
 #pragma unroll
         for (int c = 0; c < ROWS; c += 2) top = max3(top, y[c], y[c + 1]);
         // rows of V that hold no value (beyond the last key, or of a scale of zero) may hold anything
-        const bool bad = rg == 0 && (two || slot == 0) && (!there || sc.w != 0.f);
+        const bool bad = rg == 0 && (two || slot == 0) && (!there || sc.w == kZeroScale);
         const bool some = rg == 0 && there && base + key >= every;  // seen by some rows: no NaN may stay
-        if (named_bar_or(1, T, u == 0 || top > kTop || bad || some || fail)) [[unlikely]] {
-          // ---- now and then: the segment's first pair, a reference that has to move, values to clear
+        if (named_bar_or(1, T, u == 0 || top > kTop || bad || some || sc.w != 0.f || fail)) [[unlikely]] {
+          // ---- now and then: the segment's first pair, a reference that has to move, values to clear, low scales
           if (u == 0 && tid < HD) first_nan[tid] = kNoNan;
           if (named_bar_or(1, T, fail)) {
             gone = true;
@@ -644,17 +642,21 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
           const bool moved = named_bar_or(1, T, d != 0.f);
           if (moved) {
             keep_rows();
-            float sh[ROWS];              // 2^-d
+            float sh[ROWS];              // d, then 2^-d
             bool any = false;            // of this group's rows
 #pragma unroll
             for (int c = 0; c < ROWS; ++c) {
-              const float dc = srow[r0 + c];
-              any |= dc != 0.f;
-              y[c] -= dc;
-              sh[c] = ex2f(-dc);
-              lsum[c] *= sh[c];
+              sh[c] = srow[r0 + c];
+              any |= sh[c] != 0.f;
+              y[c] -= sh[c];
             }
             if (u > 0 && any) {
+#pragma unroll
+              for (int c = 0; c < ROWS; ++c) {
+                const float half = ex2f(-0.5f * sh[c]);  // in two halves: scale_terms
+                lsum[c] = lsum[c] * half * half;
+                sh[c] = half * half;
+              }
               // O^T *= 2^-d, once every product before has been added
               fail |= !mbar_wait_warp(&pv_done[(pj - 1) & 1], ((pj - 1) >> 1) & 1, p.max_spin);
               tc_fence_after();
@@ -674,6 +676,10 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
           if (u == 0) {
 #pragma unroll
             for (int c = 0; c < ROWS; ++c) lsum[c] = 0.f;
+          }
+          if (sc.w != 0.f) {             // the key's share of the sums on its own
+#pragma unroll
+            for (int c = 0; c < ROWS; ++c) lsum[c] += ex2f(y[c] - (sc.y + kSumExp));
           }
         }
         uint8_t *prow = sP + (pj & 1) * C::P_BYTES + key * 128;
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
       named_bar_sync(1, T);
       if (tid < kRP) {
         const float L = (red[tid] + red[kRP + tid]) + (red[2 * kRP + tid] + red[3 * kRP + tid]);
-        srow[tid] = whole ? 1.0f / L : 1.0f;
+        srow[tid] = whole ? kSumScale / L : 1.0f;
         if (!whole && tid < live)
           *reinterpret_cast<float2 *>(p.part_ml + (row0 + tid) * 2) =
               make_float2(L == 0.f ? kNoMax : -nref[tid], L);
@@ -843,13 +849,13 @@ __global__ void __launch_bounds__(kMerge8Warps * 32) attn8_merge_kernel(const __
     float2 ml = make_float2(kNoMax, 0.f);
     if (c < parts) ml = *reinterpret_cast<const float2 *>(p.part_ml + (row0 + static_cast<size_t>(c) * R) * 2);
     const float Mn = fmaxf(M, warp_max(ml.x));
-    float l = ml.y * exp2f(ml.x - Mn);
+    float l = moved_sum(ml.y, ml.x - Mn);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    L = L * exp2f(M - Mn) + l;
+    L = moved_sum(L, M - Mn) + l;
     M = Mn;
   }
-  const float inv = 1.0f / L;
+  const float inv = kSumScale / L;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;

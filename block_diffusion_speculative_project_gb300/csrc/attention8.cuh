@@ -149,6 +149,26 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// A block's scales as the softmax uses them: K's, log2 of V's, the factor that takes P to its share of the sum, and
+// what the block is. P = 2^(x + log2 V - reference + base) weighs a key's values, so the reference follows what
+// counts in the output; the sum takes 2^(x - reference + base - kSumExp), without V's scale. Where that scale is low, P
+// can be zero though the sum counts the key: there (kLowScale, kZeroScale) the sum's terms are exponentials of their
+// own and the factor is zero. Sums move in two halves, since 2^-d may be zero where a sum times 2^-d is not.
+// With V scales of 2^-100 .. 2^80 all of it stays within fp32. Scales below 2^-100 count as that; zero does
+// too, so that it moves no reference, but its values take no part.
+constexpr float kSumExp = 20.f, kSumScale = 1.f / (1 << 20);
+constexpr float kLowScale = 1.f, kZeroScale = 2.f;
+__device__ __forceinline__ float4 scale_terms(float ks, float vs) {
+  const bool low = vs < 1.f / (1 << 20);
+  return make_float4(ks, fmaxf(log2f(vs), -100.f), low ? 0.f : kSumScale / vs,
+                     vs == 0.f ? kZeroScale : low ? kLowScale : 0.f);
+}
+// 2^d times a sum, for d <= 0.
+__device__ __forceinline__ float moved_sum(float sum, float d) {
+  const float h = ex2f(0.5f * d);
+  return sum * h * h;
+}
+
 // A NaN among values that only some query rows see would reach the others as well, as 0 * NaN in the product
 // of P and V. So it is taken out of the operand, and `first[column]` keeps the first row that sees one; that
 // row and those behind it get the NaN with their output. Returns the word without its NaN bytes, which

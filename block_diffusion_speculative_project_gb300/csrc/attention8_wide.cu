@@ -261,8 +261,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         published = true;
         ok = c < 2 || mbar_wait_warp(&sc_empty[c & 1], ((c >> 1) - 1) & 1, p.max_spin);
         if (!ok) break;
-        const bool zero = vs == 0.f;  // a block of zeros: P must not see the scale
-        sscale[(c & 1) * 32 + lane] = make_float4(ks, zero ? 0.f : log2f(vs), zero ? 1.f : 1.f / vs, zero ? 0.f : 1.f);
+        sscale[(c & 1) * 32 + lane] = scale_terms(ks, vs);
         __syncwarp();
         mbar_arrive_if(&sc_full[c & 1], lane == 0);
       }
@@ -556,7 +555,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
           ++chunk;
           ok = mbar_wait_warp(&sc_full[chunk & 1], (chunk >> 1) & 1, p.max_spin);
         }
-        const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // K scale, log2 V, 1 / V, 0 for zeros
+        const float4 sc = sscale[(chunk & 1) * 32 + (j & 31)];  // scale_terms
         ok = ok && mbar_wait_warp(s_full, pj & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
@@ -591,9 +590,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         const bool need = m_new - m_run > kRescale;
         float alpha = 1.f;
         if (need) {
-          alpha = ex2f(m_run - m_new);
+          const float h = ex2f(0.5f * (m_run - m_new));  // in two halves: scale_terms
+          alpha = h * h;
+          l_run = l_run * h * h;
           m_run = m_new;
-          l_run *= alpha;
         }
         if (u >= 2 && __any_sync(0xffffffffu, need && r < R)) [[unlikely]] {
           ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
@@ -610,7 +610,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
             tmem_st16_raw(trow + C::O_COL + half * HD + cc * 16, x);
           }
         }
-        const float c2 = sc.y - m_run + kPBase;
+        float c2 = sc.y - m_run + kPBase;
+        if (sc.w != 0.f) [[unlikely]] {
+          const float cs = c2 - (sc.y + kSumExp);
+          float s = 0.f;
+#pragma unroll
+          for (int c = 0; c < KW; ++c) s += ex2f(fmaf(sv[c], c1, cs));
+          l_run += s;
+          if (sc.w == kZeroScale) c2 = -INFINITY;
+        }
         uint32_t pk[KW / 2];
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -623,10 +631,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
         }
         const float2 lt = add2(ls[0], ls[1]);
         l_run = fmaf(lt.x + lt.y, sc.z, l_run);
-        if (sc.w == 0.f) [[unlikely]] {
-#pragma unroll
-          for (int c = 0; c < KW / 2; ++c) pk[c] = 0u;
-        }
         if (!freed) {
           ok = mbar_wait_warp(&p_empty[half], (pj - 1) & 1, p.max_spin);
           if (!ok) break;
@@ -664,9 +668,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn8_wide_kernel(const __gri
 #pragma unroll
       for (int c = 0; c < 2 * RHO; ++c) M = fmaxf(M, ml[c * ROWS + r].x);
 #pragma unroll
-      for (int c = 0; c < 2 * RHO; ++c) L += ml[c * ROWS + r].y * ex2f(ml[c * ROWS + r].x - M);
+      for (int c = 0; c < 2 * RHO; ++c) L += moved_sum(ml[c * ROWS + r].y, ml[c * ROWS + r].x - M);
       const size_t row0 = (static_cast<size_t>(i * p.Hkv + g) + blockIdx.x) * R;   // partial rows
-      const float inv = whole ? 1.0f / L : 1.0f;
+      const float inv = whole ? kSumScale / L : 1.0f;
       const bool has1 = cnt > 1;
       const float a0 = ex2f(ml[tl].x - M) * inv, a1 = has1 ? ex2f(ml[128 + tl].x - M) * inv : 0.f;
       const int live = n * G;            // rows that are computed

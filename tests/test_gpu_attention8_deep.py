@@ -17,7 +17,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_rows8 import PR, Cache
+from test_gpu_rows8 import PR, Cache, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,26 @@ def test_queries_with_a_channel_that_stands_out(hd, Hq, Hkv, m):
     out = c.attend(0, m, q, None, ctx, True)
     assert c.status() == 0
     check(c, q, [m] * nb, ctx, True, out)
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+@pytest.mark.parametrize("few", [True, False])
+def test_value_scales_far_apart(hd, Hq, Hkv, m, few):
+    """Blocks of equal scores whose values' scales are 2^-100 (what an append of zeros gives), 2^60 and in
+    between weigh the same in the sum of the softmax; a scale of zero takes nothing from the others'
+    small values. In one CTA, or one unit a CTA joined by the merge."""
+    nb = 1 if few else 152 // Hkv + 8
+    for scales in ([2.0 ** -100, 2.0 ** 60, 1.0, 2.0 ** -100, 2.0 ** -40], [2.0 ** -100], [2.0 ** -30, 0.0, 2.0 ** -31],
+                   [0.0], [2.0 ** 80, 2.0 ** -100, 2.0 ** -19]):
+        c = Cache(Hq, Hkv, hd, PR * 24, nb, N=1, B=max(m, 2), seed=6)
+        g = torch.Generator(device="cuda").manual_seed(6)
+        c.k8.copy_(torch.randn(c.k8.shape, generator=g, device="cuda").to(torch.float8_e4m3fn))
+        c.ks.fill_(0.25)
+        for i in range(nb):
+            for b in range(c.pps):
+                c.vs[0][c.at(i, b)] = scales[(b + i) % len(scales)]
+        q = queries(c, m, seed=7)
+        ctx = [PR * 23 - 7 * i % 500 for i in range(nb)]
+        out = c.attend(0, m, q, None, ctx, False)
+        assert c.status() == 0
+        check(c, q, [m] * nb, ctx, False, out, str(scales))
