@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
         }
 #pragma unroll
         for (int c = 0; c < ROWS; c += 2) top = max3(top, y[c], y[c + 1]);
-        // rows of V that hold no value (beyond the last key, or of a scale of zero) may hold anything
-        const bool bad = rg == 0 && (two || slot == 0) && (!there || sc.w == kZeroScale);
+        // rows of V beyond the last key may hold anything
+        const bool bad = rg == 0 && (two || slot == 0) && !there;
         const bool some = rg == 0 && there && base + key >= every;  // seen by some rows: no NaN may stay
         if (named_bar_or(1, T, u == 0 || top > kTop || bad || some || sc.w != 0.f || fail)) [[unlikely]] {
           // ---- now and then: the segment's first pair, a reference that has to move, values to clear, low scales
@@ -679,7 +679,10 @@ __global__ void __launch_bounds__(A8Cfg<HD>::THREADS, 1) attn8_kernel(const __gr
           }
           if (sc.w != 0.f) {             // the key's share of the sums on its own
 #pragma unroll
-            for (int c = 0; c < ROWS; ++c) lsum[c] += ex2f(y[c] - (sc.y + kSumExp));
+            for (int c = 0; c < ROWS; ++c) {
+              lsum[c] += ex2f(y[c] - (sc.y + kSumExp));
+              if (sc.w == kZeroScale) y[c] -= INFINITY;
+            }
           }
         }
         uint8_t *prow = sP + (pj & 1) * C::P_BYTES + key * 128;

@@ -155,7 +155,7 @@ __device__ __forceinline__ float ex2f(float x) {
 // can be zero though the sum counts the key: there (kLowScale, kZeroScale) the sum's terms are exponentials of their
 // own and the factor is zero. Sums move in two halves, since 2^-d may be zero where a sum times 2^-d is not.
 // With V scales of 2^-100 .. 2^80 all of it stays within fp32. Scales below 2^-100 count as that; zero does
-// too, so that it moves no reference, but its values take no part.
+// too, so that it moves no reference, but its P is zero (so a NaN byte gives NaN, as NaN times zero).
 constexpr float kSumExp = 20.f, kSumScale = 1.f / (1 << 20);
 constexpr float kLowScale = 1.f, kZeroScale = 2.f;
 __device__ __forceinline__ float4 scale_terms(float ks, float vs) {

@@ -364,7 +364,8 @@ DFLASH_API int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, co
  *   m           query rows per sequence, 0..B
  *   q           bf16 [nb, m, Hq, hd]: rotated queries
  *   kcache8, vcache8, kscale, vscale  the 8-bit caches; scales finite and >= 0, vscale at most 2^80
- *               (values to 2^88; below 2^-100 it may count as 2^-100)
+ *               (values to 2^88; below 2^-100 it may count as 2^-100). An element of a block of
+ *               scale zero is zero, or NaN if its byte is
  *   n_rows      int32 [nb] device, 0 <= n_rows[i] <= m: query rows of sequence i, or NULL: m. Rows
  *               j >= n_rows[i] of out_o are left as they were.
  *   ctx_len, max_ctx_hint  as for dflash_draft_block; ctx_len[i] + n_rows[i] <= Cmax

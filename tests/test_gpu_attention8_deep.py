@@ -150,3 +150,22 @@ def test_value_scales_far_apart(hd, Hq, Hkv, m, few):
         out = c.attend(0, m, q, None, ctx, False)
         assert c.status() == 0
         check(c, q, [m] * nb, ctx, False, out, str(scales))
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+def test_a_nan_byte_in_a_block_of_scale_zero(hd, Hq, Hkv, m):
+    """An element is its e4m3 value times the scale: NaN times zero is NaN, for any number of query rows."""
+    c = Cache(Hq, Hkv, hd, 256, 2, N=1, B=max(m, 2), seed=8)
+    q = queries(c, m, seed=8)
+    for i in range(2):
+        c.vs[0][c.at(i, 1)] = 0.0
+    ctx = [200, 100]
+    clean = c.attend(0, m, q, None, ctx, False)
+    check(c, q, [m, m], ctx, False, clean)
+    block(c, "v8", 1, 1).view(torch.uint8)[:, 5, 9] = 0x7F
+    out = c.attend(0, m, q, None, ctx, False)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[1, :, :, 9] = True
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], clean[~want])
+    assert c.status() == 0
