@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(128, 5) kv_rows_kernel(const __grid_constant__
       const int hh = h0 + (it0 + k) * HPW;
       const bool have = it0 + k < p.iters && hh < total;
       const int t = have && hh >= p.heads[0] ? 1 : 0;
-      const bool plain = !have || (APPEND && t == 1);  // values go as they are
+      // values go as they are, and so do keys that are rotated and normed already
+      const bool plain = !have || (APPEND && (t == 1 || !(p.rotate || p.g[0])));
       if (__any_sync(0xffffffffu, !plain)) {
         if (!plain && t != cur) {
           cur = t;
@@ -221,7 +222,11 @@ __global__ void __launch_bounds__(128, 5) kv_rows_kernel(const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 x = mul2(a[e], inv2), y = mul2(b[e], inv2);
-            const float2 u = fma2(y, fb[e], mul2(x, fa[e])), v = fma2(x, fd[e], mul2(y, fc[e]));
+            float2 u = mul2(x, fa[e]), v = mul2(y, fc[e]);
+            if (!APPEND || p.rotate) {  // else no product with a sine of zero: infinities would make NaN of it
+              u = fma2(y, fb[e], u);
+              v = fma2(x, fd[e], v);
+            }
             ra[e] = pack_bf16x2(u.x, u.y);
             rb[e] = pack_bf16x2(v.x, v.y);
           }
