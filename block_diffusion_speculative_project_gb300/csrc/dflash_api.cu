@@ -1216,6 +1216,10 @@ int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q
   if (nb == 0 || m == 0) return DFLASH_OK;
   DF_TRY(check_out("q", q));
   DF_TRY(check_out("out_o", out_o));
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out_o);
+  const size_t bytes = (size_t)nb * m * c.Hq * c.hd * 2;
+  if (q0 != o0 && q0 < o0 + bytes && o0 < q0 + bytes)  // a row would be written before it is read
+    return fail(DFLASH_ERR_INVALID_ARG, "out_o must be q or not overlap it");
   DF_TRY(check_cache8(h, kcache8, vcache8, kscale, vscale));
   if (!ctx_len) return fail(DFLASH_ERR_INVALID_ARG, "ctx_len is NULL");
   DF_TRY(check_paging(h));

@@ -372,12 +372,11 @@ DFLASH_API int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, co
  *   causal      0: every row attends to cache rows [0, ctx_len[i] + n_rows[i]); else row j to
  *               [0, ctx_len[i] + j + 1)
  *   out_o       bf16 [nb, m, Hq, hd]: softmax(q K^T / sqrt(hd)) V, query head h reading kv head
- *               h / (Hq/Hkv)
+ *               h / (Hq/Hkv). May be q itself; otherwise it must not overlap q (refused).
  * Cache rows that a query row does not attend to may hold anything, NaN too. Errors as
- * dflash_attention; a length or
- * count out of range is clamped and reported as DFLASH_ERR_DEVICE_CHECK by dflash_status, and a
- * page outside the pool is read as page 0 and reported. Bitwise reproducible as
- * dflash_draft_block is. */
+ * dflash_attention; a length or count out of range is clamped and reported as
+ * DFLASH_ERR_DEVICE_CHECK by dflash_status, and a page outside the pool is read as page 0 and
+ * reported. Bitwise reproducible as dflash_draft_block is. */
 DFLASH_API int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q,
                                  const void *kcache8, const void *vcache8, const float *kscale,
                                  const float *vscale, const int32_t *n_rows, const int32_t *ctx_len,

@@ -169,3 +169,23 @@ def test_a_nan_byte_in_a_block_of_scale_zero(hd, Hq, Hkv, m):
     assert torch.equal(torch.isnan(out), want)
     assert torch.equal(out[~want], clean[~want])
     assert c.status() == 0
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+@pytest.mark.parametrize("L", [40, 20000])
+def test_the_output_may_be_the_queries(hd, Hq, Hkv, m, L):
+    """Written whole by one CTA, or joined from many: a pair's queries are read before its rows are written."""
+    c = Cache(Hq, Hkv, hd, -(-(L + m) // PR) * PR, 3, N=1, B=max(m, 2), seed=2)
+    q = queries(c, m, seed=2)
+    n, ctx = [m, max(m - 1, 0), m], [L, L // 2, L // 3]
+    want = c.attend(0, m, q, n, ctx, True)
+    got = q.clone()
+    c.attend(0, m, got, n, ctx, True, out=got)
+    want[1, n[1]:] = q[1, n[1]:]
+    assert torch.equal(got, want)
+    both = torch.zeros(2 * q.numel(), dtype=torch.bfloat16, device="cuda")
+    for shift in (8, q.numel() - 8):
+        with pytest.raises(c.D.DflashError) as e:  # some rows would be written over before they are read
+            c.attend(0, m, both[:q.numel()].view_as(q), n, ctx, True, out=both[shift:shift + q.numel()].view_as(q))
+        assert e.value.code == c.D.DFLASH_ERR_INVALID_ARG
+    assert c.status() == 0
