@@ -40,7 +40,7 @@ namespace df {
 // used. A pair costs about 1150 cycles a CTA where the copies need 1260 for it; a segment costs about 4000
 // besides (queries, the first reference, sums, output). One token over 2047 rows takes 8.9 us, of which
 // reading the lengths and finding the range are 1, the queries 0.8, two units 1.3, the merge 2.5.
-constexpr int kRP = 16;  // query rows of a kv head, padded
+constexpr int kRP = kAttn8FewRows;  // query rows of a kv head, padded
 
 template <int HD>
 struct A8Cfg {

@@ -1232,8 +1232,7 @@ int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q
   DF_TRY(encode_rows8(&p.tmK, static_cast<const uint8_t *>(kcache8) + blocks * kPageRows * c.hd,
                       cache_layer_rows(c), c.hd));
   p.v8 = static_cast<const uint8_t *>(vcache8) + blocks * kPageRows * c.hd;
-  DF_TRY(encode_rows8(&p.tmV, static_cast<const uint8_t *>(vcache8) + blocks * kPageRows * c.hd,
-                      cache_layer_rows(c), c.hd));
+  if ((c.Hq / c.Hkv) * m <= kAttn8FewRows) DF_TRY(encode_rows8(&p.tmV, p.v8, cache_layer_rows(c), c.hd));
   p.ks = kscale + blocks;
   p.vs = vscale + blocks;
   p.n_rows = n_rows;

@@ -302,7 +302,7 @@ cudaError_t launch_kv_append8(KvRowsParams &p, int num_sms, cudaStream_t s);
 // Attention of m query rows per sequence over an 8-bit cache (attention8.cu).
 struct Attn8Params {
   CUtensorMap tmK, tmV;      // the layer's 8-bit caches as {hd, rows}, box {hd, 64}, swizzled by hd bytes
-  const uint8_t *v8;         // the layer's value cache
+  const uint8_t *v8;         // the layer's value cache, in place of tmV in the form for more rows
   const uint16_t *q;         // bf16 [nb][m][Hq][hd]
   const float *ks, *vs;      // the layer's scales, one per 64 rows and kv head
   const int *n_rows;         // [nb] or null: m
@@ -322,7 +322,8 @@ struct Attn8Params {
   int stall;                 // test hook: issue no loads so the waits run out
 };
 cudaError_t launch_attention8(const Attn8Params &p, cudaStream_t s);
-// Its kernel for R = G*m > 16 query rows a kv head (attention8_wide.cu), without the merge.
+constexpr int kAttn8FewRows = 16;  // query rows R = G*m of a kv head up to which attention8.cu's form is taken
+// The kernel for more of them (attention8_wide.cu), without the merge.
 cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 
 // Slots of partial outputs the attention of nb sequences may write: at most one per
