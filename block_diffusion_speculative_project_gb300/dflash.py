@@ -10,8 +10,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdflash.so")
 
@@ -135,7 +133,9 @@ def _ptr(t):
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
-    # the current stream's handle without the Stream object around it: 0.3 us of a call's 10, not 3
+    import torch  # here, as the constants, types and host checks do without it
+    # the current stream's handle without the Stream object around it: 0.3 us of a call's 10, not 3 (a private name,
+    # which PyTorch 2.9 and 2.11 have)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 

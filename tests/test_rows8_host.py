@@ -134,3 +134,13 @@ def test_drafter_refuses_rows_that_its_calls_would_read_past(monkeypatch):
         with pytest.raises(ValueError):
             f(**kw)
     assert not calls
+
+
+def test_the_binding_needs_torch_only_for_a_stream():
+    import os
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None; from block_diffusion_speculative_project_gb300 import dflash as d; "
+            "assert d.DFLASH_PAGE_ROWS == 64")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
