@@ -14,10 +14,11 @@ scores hd * 2^-24 * sum|q k| / sqrt(hd), which move a probability by twice that 
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_rows8 import PR, Cache, queries
+from test_gpu_rows8 import PR, Cache, lib, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -75,9 +76,67 @@ def put8(t, value):
     t.copy_(torch.full(t.shape, value, device="cuda").to(torch.float8_e4m3fn))
 
 
-# (hd, Hq, Hkv, rows m): 1 and 16 rows of a kv head in the form for few, 32 and 63 in the form for up to 64,
+def poison():
+    """An attention over nothing but NaN, whose bytes stay in the SMs' shared memory."""
+    for Hq, m in ((1, 1), (8, 8)):
+        c = Cache(Hq, 1, 128, 64 * 400, 1, N=1, B=max(m, 2))
+        for name in ("k8", "v8"):
+            getattr(c, name).view(torch.uint8).fill_(0x7F)
+        c.attend(0, m, queries(c, m), None, [64 * 400 - m], False)
+
+
+# (hd, Hq, Hkv, rows m): 1, 16 and 14 rows of a kv head in the form for few, 32 and 63 in the form for up to 64,
 # 96 and 128 in the one for more
-FORMS = [(128, 2, 2, 1), (64, 4, 1, 4), (128, 16, 2, 4), (64, 7, 1, 9), (128, 8, 1, 12), (64, 8, 1, 16)]
+FORMS = [(128, 2, 2, 1), (64, 4, 1, 4), (128, 4, 2, 7), (128, 16, 2, 4), (64, 7, 1, 9), (128, 8, 1, 12), (64, 8, 1, 16)]
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+@pytest.mark.parametrize("paged,causal", [(True, False), (False, True)])
+def test_a_hundred_units_in_one_cta(hd, Hq, Hkv, m, paged, causal):
+    """Two sequences of together 152 * 100 units and more: every CTA has some fifty pairs, the rings wrap several
+    times and the scales come in four chunks. Scores are flat but for one key in every 37 units, which
+    lies 2^14 to 2^15.5 above for half of the query heads: the reference moves inside every CTA's segment,
+    and what was added before it still weighs about a tenth of what the key does."""
+    units = 152 * 104 // Hkv
+    L = [PR * (units * 2 // 3) - 5 - m, PR * (units // 3) + 9]
+    c = Cache(Hq, Hkv, hd, PR * (units * 2 // 3) + PR, 2, N=1, B=max(m, 2), paged=paged, seed=m)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    c.k8.copy_((8 * torch.randn(c.k8.shape, generator=g, device="cuda")).to(torch.float8_e4m3fn))
+    c.v8.copy_((100 + 20 * torch.randn(c.v8.shape, generator=g, device="cuda")).to(torch.float8_e4m3fn))
+    c.k8.view(torch.uint8)[..., 0] = 0
+    q = queries(c, m, seed=1, std=0.25)
+    q[..., 0] = 0
+    q[:, :, ::2, 0] = 8.0
+    c.ks.fill_(2.0 ** -4)
+    step = math.log(2) * math.sqrt(hd) / 8.0            # of channel 0, for one power of two
+    for i in range(2):
+        for x, b in enumerate(range(30, (L[i] + m) // PR, 37)):
+            k = block(c, "k8", i, b)
+            put8(k[:, (x * 11) % PR, 0], (14 + x % 4 * 0.5) * step * 16)
+            put8(block(c, "v8", i, b)[:, (x * 11) % PR], -60.0)
+    n = [m, max(m - 1, 1)]
+    out = c.attend(0, m, q, n, L, causal)
+    assert c.status() == 0
+    check(c, q, n, L, causal, out)
+    poison()
+    again = c.attend(0, m, q, n, L, causal)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+def test_many_segments_of_many_units(hd, Hq, Hkv, m):
+    """40 ragged sequences, so that a CTA's chunks of 32 scales begin anywhere in a segment; some odd, some
+    empty, one of a single row."""
+    nb = 40
+    c = Cache(Hq, Hkv, hd, PR * 1200 // Hkv, nb, N=1, B=max(m, 2), seed=m)
+    rng = np.random.default_rng(m)
+    ctx = [int(x) for x in rng.integers(PR * 150 // Hkv, PR * 1100 // Hkv, nb)]
+    n = [int(x) for x in rng.integers(0, m + 1, nb)]
+    ctx[7], n[7] = 0, 1
+    q = queries(c, m, seed=5)
+    out = c.attend(0, m, q, n, ctx, True)
+    assert c.status() == 0
+    check(c, q, n, ctx, True, out)
 
 
 @pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
@@ -172,6 +231,51 @@ def test_a_nan_byte_in_a_block_of_scale_zero(hd, Hq, Hkv, m):
 
 
 @pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+def test_growing_scores_and_scales_of_keys_and_values(hd, Hq, Hkv, m):
+    """Scores that grow by far more than any reference allows within a CTA's units, for some rows only; scales
+    2^40 apart; blocks of key scale and of value scale zero."""
+    nb = 152 // Hkv + 5
+    c = Cache(Hq, Hkv, hd, PR * 17, nb, N=1, B=max(m, 2), seed=9)
+    q = queries(c, m, seed=9)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for i in range(nb):
+        for b in range(c.pps):
+            x = torch.randn(Hkv, PR, hd, generator=g, device="cuda") + 0.12 * b * q[i, 0, 0].float()
+            block(c, "k8", i, b).copy_((x * 16).clamp(-448, 448).to(torch.float8_e4m3fn))
+            c.ks[0][c.at(i, b)] = 2.0 ** -4 * (1.0 + 0.25 * (b % 3))
+            c.vs[0][c.at(i, b)] = 2.0 ** (-20 + (b % 5) * 10)
+        c.vs[0][c.at(i, 3)] = 0.0
+        c.ks[0][c.at(i, 4)] = 0.0
+    ctx = [PR * 17 - m - i % 70 for i in range(nb)]
+    for causal in (False, True):
+        out = c.attend(0, m, q, None, ctx, causal)
+        check(c, q, [m] * nb, ctx, causal, out)
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS[1:])
+def test_large_small_zero_and_nan_query_rows(hd, Hq, Hkv, m):
+    c = Cache(Hq, Hkv, hd, 256, 3, N=1, B=max(m, 2), seed=3)
+    q = queries(c, m, seed=4)
+    q[0, 0] *= 3e4
+    q[0, 1] *= 1e-6
+    q[0, 2] *= 1e-30
+    q[1, 0, 0] = 0
+    ctx = [200, 100, 60]
+    ref = c.attend(0, m, q, None, ctx, True)
+    check(c, q, [m] * 3, ctx, True, ref)
+    for bad in (float("nan"), float("inf")):
+        q2 = q.clone()
+        q2[2, 1, Hq - 1, 7] = bad
+        out = c.attend(0, m, q2, None, ctx, True)
+        assert torch.isnan(out[2, 1, Hq - 1]).all()
+        out[2, 1, Hq - 1] = ref[2, 1, Hq - 1]
+        check(c, q, [m] * 3, ctx, True, out)  # (an infinite row changes the scaling of those beside it)
+        assert bad == math.inf or torch.equal(out, ref)
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
 @pytest.mark.parametrize("L", [40, 20000])
 def test_the_output_may_be_the_queries(hd, Hq, Hkv, m, L):
     """Written whole by one CTA, or joined from many: a pair's queries are read before its rows are written."""
@@ -189,3 +293,20 @@ def test_the_output_may_be_the_queries(hd, Hq, Hkv, m, L):
             c.attend(0, m, both[:q.numel()].view_as(q), n, ctx, True, out=both[shift:shift + q.numel()].view_as(q))
         assert e.value.code == c.D.DFLASH_ERR_INVALID_ARG
     assert c.status() == 0
+
+
+@pytest.mark.parametrize("hd,Hq,Hkv,m", FORMS)
+def test_wait_limit_in_every_form(hd, Hq, Hkv, m):
+    """No loads are issued, so every wait runs out after 2000 polls: reported, and a handle without the
+    flag works right afterwards."""
+    D = lib()
+    c = Cache(Hq, Hkv, hd, 512, 3, N=1, B=max(m, 2), max_spin=2000, flags=1 << 30)
+    q = queries(c, m)
+    ctx = [100, 0, 400]
+    c.attend(0, m, q, None, ctx, False)
+    assert c.status() == D.DFLASH_ERR_TIMEOUT
+    assert c.status() == D.DFLASH_OK
+    c = Cache(Hq, Hkv, hd, 512, 3, N=1, B=max(m, 2))
+    out = c.attend(0, m, q, None, ctx, False)
+    assert c.status() == 0
+    check(c, q, [m] * 3, ctx, False, out)
