@@ -28,18 +28,20 @@ namespace df {
 // hold exactly, and its smallest step, 2^-16, lies far enough below: a query's values are exact from 2^-16 of the
 // largest of its block of rows on, and what is smaller is off by at most 2^-24 of that (put_q). Two e4m3 terms were
 // exact from 2^-9 on only, off by 2^-17 below, which shows where a channel of the queries stands out.
-// Probabilities: three e5m2 terms keep 9 bits over f16's range. The terms' products lie in columns of their own, so the second and third carry powers of two
-// (2^kSplit2, 2^kSplit3) that put what is left of small probabilities where e5m2 has its bits; the output takes them
-// back. What is lost is at most 2^-24 + 2^-25 (f16) where the largest is 2^kPBase: 2^-31 of it. (All terms alike
-// lost 2^-24 of the largest for every key, which is 40% of a key 2^23 below a sink.)
+// Probabilities: three e5m2 terms keep 9 bits over f16's range. The terms' products lie in columns of their
+// own, so the second and third carry powers of two (2^kSplit2, 2^kSplit3) that put what is left of small
+// probabilities where e5m2 has its bits; the output takes them back. What is lost is at most 2^-24 + 2^-25 (f16)
+// where the largest is 2^kPBase: 2^-31 of it. (All terms alike lost 2^-24 of the largest for every key, which is
+// 40% of a key 2^23 below a sink.)
 //
 // Units are taken in pairs (128 keys); a segment of an odd number of units ends with one alone.
 //
-// What bounds it: HBM for long caches. 64 single tokens over 1024 .. 8191 keys (602 MB) take 95 us, 6.3
-// TB/s; under ncu (16 x 16,385 keys) 6.2 TB/s with the tensor pipe busy for 10% and 37% of the issue slots
-// used. A pair costs about 1150 cycles a CTA where the copies need 1260 for it; a segment costs about 4000
-// besides (queries, the first reference, sums, output). One token over 2047 rows takes 8.9 us, of which
-// reading the lengths and finding the range are 1, the queries 0.8, two units 1.3, the merge 2.5.
+// What bounds it: HBM for long caches. 64 single tokens over 1024 .. 8191 keys (602 MB) take 98 us, 6.1
+// TB/s (with 4 rows each, 16 a kv head, 102); under ncu (16 x 16,385 keys) 6.0 TB/s with the tensor pipe busy for
+// 13% and 39% of the issue slots used. A segment costs about 4000 cycles besides its pairs (queries, the first
+// reference, sums, output). One token over 2047 rows takes 8.7 us, of which reading the lengths and finding
+// the range are 1, the queries 0.8, two units 1.3, the merge 2.5. With hd 64 the same tokens take 94 us: half the
+// bytes, but as many pairs, and a pair's chain takes as long.
 constexpr int kRP = kAttn8FewRows;  // query rows of a kv head, padded
 
 template <int HD>

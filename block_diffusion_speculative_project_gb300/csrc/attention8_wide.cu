@@ -4,14 +4,15 @@
 //   O [rows][hd]      += P V       P f16 in tensor memory, V widened to f16 in shared memory
 // so that a softmax thread is a query row. Widening V costs the same for any number of rows; splitting
 // probabilities into 8-bit terms, as the form for few rows does, grows with them: 64 sequences of 1024
-// .. 8191 keys took 97 us there and 121 here with 16 rows, 127 and 122 with 32 (hd 64: 123 and 107);
-// one context of 262,147 keys with 32 rows 97 and 101. (Here it is 117 with 32 rows since.)
+// .. 8191 keys take 102 us there and 124 here with 16 rows (hd 64: 100 and 104); with 32 rows, when the form for few
+// rows still took them, it was 127 there and 122 here (hd 64: 123 and 107).
 // What bounds it: the chain from role to role, beside shared memory's bandwidth (72 KB written and read for
-// a unit, 560 cycles of about 720): one context of 262,155 keys and 64 rows (537 MB) takes 100 us, 5.4
-// TB/s, and 112 for seconds on end, when the power limit holds the clock at 1.70 GHz; under ncu (8 x
-// 16,400 keys) DRAM is busy for 56%, the tensor pipe for 46%, and 42% of the issue slots are used.
-// Without the conversion instructions it took as long; with 8 converter warps, which leaves the softmax
-// fewer registers, 114; with the conversion in integer arithmetic 125.
+// a unit, 560 cycles of about 720): the same 64 sequences with up to 32 rows (607 MB) take 123 us, 4.9 TB/s, with 64
+// rows 139, with 96 160 and with 128 170 (hd 64: 147); one context of 262,155 keys takes 111 with 64 rows, 4.8 TB/s,
+// and 128 with 128, for seconds on end, when the power limit holds the clock at 1.70 GHz. Under ncu (8 x 16,400 keys)
+// DRAM is busy for 55%, the tensor pipe for 53%, and 42% of the issue slots are used with 64 rows; 47%, 43% and 45%
+// with 128. When it took 107 us, it took as long without the conversion instructions, 114 with 8 converter warps,
+// which leaves the softmax fewer registers, and 125 with the conversion in integer arithmetic.
 #include <mutex>
 
 #include "attention8.cuh"
@@ -55,8 +56,8 @@ struct WideCfg {
 };
 // P is 2^(x - m_run + kPBase), m_run the maximum at the last rescale: O is rescaled only when the
 // maximum has grown by more than 2^kRescale, so P stays at most 2^15 in f16, and half a step of f16's smallest
-// values is 2^-32 of the largest probability. A maximum that may grow by 2^13 costs less (64 verified blocks 117.2 us,
-// 118.9 with 2^8), but with the largest at 2^2 it rounds keys 2^23 below a sink by up to a tenth.
+// values is 2^-32 of the largest probability. A maximum that may grow by 2^13 costs less (64 verified blocks 122.9 us
+// from a graph, 125.3 with 2^8), but with the largest at 2^2 it rounds keys 2^23 below a sink by up to a tenth.
 constexpr float kPBase = 7.f, kRescale = 8.f;
 
 // A segment's units are taken in pairs: one S product of 128 keys, then softmax, PV and O for each

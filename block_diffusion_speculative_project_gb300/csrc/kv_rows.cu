@@ -8,8 +8,8 @@
 //
 // The angle is kept in turns as a 64-bit fixed-point fraction: the host gives
 // base^(-2d/hd) / (2 pi) * 2^64, and the low 64 bits of its product with the position are the
-// angle modulo one turn, so far positions lose nothing (a float product is off by 2^-24 of
-// the whole angle: 0.008 rad at position 131072).
+// angle modulo one turn, so far positions lose little: the host's 64-bit floats are off by 2^-53 of the whole
+// angle, 2^-30 rad at position 2^23 and 2^-22 at 2^31 (a float product by 2^-24: 0.008 rad at position 131072).
 #include <algorithm>
 #include <cfloat>
 
@@ -97,11 +97,12 @@ __device__ __forceinline__ void report_lengths(const KvRowsParams &p, int i) {
 // factors per pair of values, the same for every head of a tensor, so that a value costs two
 // products of packed floats and the row's 1 / norm. APPEND writes the first tensor's rows (keys) and the
 // second's (values) into the caches.
-// Memory bounds it: 8191 rows of 40 heads take 29.9 us, 168 MB at 5.6 TB/s, and 2 x 8189 rows appended to
-// 8 + 8 heads 24.1 us, 134 MB at 5.6 TB/s. Groups go in batches of four, all loads before the first
+// Memory bounds it: 8191 rows of 40 heads take 29.7 us, 168 MB at 5.7 TB/s, and 2 x 8189 rows appended to
+// 8 + 8 heads 24.1 us, 134 MB at 5.6 TB/s, both with the same buffers again and again, of which the L2 keeps
+// a part; with others each time 31.1 and 26.2. Groups go in batches of four, all loads before the first
 // store: two at a time took 32.5 us, and each group's loads right after its predecessor's stores 35.8.
-// Registers for five CTAs a SM: six spill (41.7 us). Single tokens are a launch and four dependent
-// loads: 2.7 us.
+// Registers for five CTAs a SM (the append spills 12 bytes there); six spill more (41.7 us). Single tokens are a
+// launch and four dependent loads: 2.4 us.
 constexpr int kRowBatch = 4;  // groups whose loads are in flight together
 
 template <int HD, bool APPEND>
@@ -255,10 +256,10 @@ __global__ void __launch_bounds__(128, 5) kv_rows_kernel(const __grid_constant__
 // The values before their rounding to e4m3 are fp32's, off by 5e-8 on average, so one key in 1.6 million
 // lies so near the middle of a step that it goes to the other side than in exact arithmetic (with the
 // norm, the gain and the rotation each rounded on its own, one in 1.1 million).
-// Two prompts of up to 8189 rows (67 MB) take 14.0 us, 4.8 TB/s: a step from head to head is a chain of
-// norm, maximum over the block and scale, which the four warps a scheduler has room for hide in part. With
-// the angles in registers, which leaves room for no more, it was 15.6; with the heads' values
-// asked for two to four steps ahead through shared memory 15 to 16.7.
+// Two prompts of up to 8189 rows (67 MB) take 17.4 us, 3.9 TB/s, and 13.8 where they lie in the L2 from the call
+// before: a step from head to head is a chain of norm, maximum over the block and scale, which the four warps
+// a scheduler has room for hide in part. From the L2 it was 15.6 with the angles in registers, which leaves room for
+// no more warps, and 15 to 16.7 with the heads' values asked for two to four steps ahead through shared memory.
 constexpr int kScaleExpMin = -100, kScaleExpMax = 119;
 
 template <int HD, int SLOTS, int TPR>

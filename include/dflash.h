@@ -308,7 +308,8 @@ DFLASH_API int dflash_attention(dflash_handle_t h, int nb, int layer, const void
  * cfg.rope_base) in one pass over a projection's rows ([DFlash] 四、推理流程: the rotated
  * queries and keys of the block; the norms are those of targets and drafters that normalise
  * each head). For each head x of hd values, y = x * g / sqrt(mean(x^2) + eps), then y rotated at
- * the row's position; fp32 arithmetic, angles exact at any position, one rounding to bf16.
+ * the row's position; fp32 arithmetic, one rounding to bf16. Angles are off by 2^-30 rad and by
+ * position * 2^-53 rad (2^-22 at the largest position).
  *   q, k        bf16 rows (nb * R of them, row j of sequence i at i*R + j) of Hq and Hkv heads,
  *               row strides ldq and ldk in elements (multiples of 8; 16-byte aligned: e.g. the
  *               parts of a fused q|k|v projection). k and out_k may be NULL together.
@@ -373,6 +374,11 @@ DFLASH_API int dflash_kv_append8(dflash_handle_t h, int nb, int layer, int R, co
  *               [0, ctx_len[i] + j + 1)
  *   out_o       bf16 [nb, m, Hq, hd]: softmax(q K^T / sqrt(hd)) V, query head h reading kv head
  *               h / (Hq/Hkv). May be q itself; otherwise it must not overlap q (refused).
+ * Arithmetic: scores from the cache's e4m3 keys and the queries as sums of 8-bit terms, exact where a
+ * query's value is at least 2^-13 of its row's largest, off by at most 2^-21 of that below; sums
+ * and the softmax in fp32; each probability rounded to 2^-11 of itself and, with at most 16 query
+ * rows a kv head, to three terms of 8 bits (2^-10 more), and to 2^-31 of the row's largest
+ * probability times value scale; one rounding to bf16.
  * Cache rows that a query row does not attend to may hold anything, NaN too. Errors as
  * dflash_attention; a length or count out of range is clamped and reported as
  * DFLASH_ERR_DEVICE_CHECK by dflash_status, and a page outside the pool is read as page 0 and
