@@ -154,7 +154,8 @@ __device__ __forceinline__ float ex2f(float x) {
 // counts in the output; the sum takes 2^(x - reference + base - kSumExp), without V's scale. Where that scale is low, P
 // can be zero though the sum counts the key: there (kLowScale, kZeroScale) the sum's terms are exponentials of their
 // own and the factor is zero. Sums move in two halves, since 2^-d may be zero where a sum times 2^-d is not.
-// With V scales of 2^-100 .. 2^80 all of it stays within fp32. Scales below 2^-100 count as that; zero does
+// With V scales of 2^-100 .. 2^80 all of it stays within fp32: low is below 2^-20, and beside a scale of 2^80 one of
+// 2^-20 has P zero only for keys 2^34 below the reference's. Scales below 2^-100 count as that; zero does
 // too, so that it moves no reference, but its P is zero (so a NaN byte gives NaN, as NaN times zero).
 constexpr float kSumExp = 20.f, kSumScale = 1.f / (1 << 20);
 constexpr float kLowScale = 1.f, kZeroScale = 2.f;
