@@ -1,7 +1,7 @@
 // C ABI of libdflash (declared in include/dflash.h): argument validation, TMA
 // descriptor encoding, workspace layout and the launch sequence of each step call.
-// All compute runs in the kernels of gemm_tc.cu, attention.cu, attention8.cu, kv_rows.cu,
-// sampling.cu and small_ops.cu.
+// All compute runs in the kernels of gemm_tc.cu, attention.cu, attention8.cu, attention_tree.cu, kv_rows.cu,
+// tree_ops.cu, logits.cu, sampling.cu and small_ops.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -129,7 +129,7 @@ struct WsLayout {
   size_t status = 0;
   size_t pre = 0, h = 0;                       // ctx_project
   size_t x = 0, u = 0, qkv = 0, o = 0, act = 0, xb = 0, corr = 0, ss = 0;  // draft_block
-  size_t apart = 0, aml = 0;                   // attention partials
+  size_t apart = 0, aml = 0;                   // attention partials (dflash_attention_tree's too)
   size_t tk_vals = 0, tk_ids = 0;              // LM head top-k partial lists
   size_t sel_e = 0, sel_ab = 0, sel_g = 0, sel_t = 0;  // selector
   size_t film_cond = 0, film_hid = 0, film_bg = 0;     // FiLM relay
@@ -189,9 +189,13 @@ void plan_workspace(dflash_handle_s *h) {
   L.ss = take((size_t)Mb * ((c.D + 127) / 128) * 4);  // deferred RMSNorm partial sums
   L.corr = take((c.flags & DFLASH_FLAG_CONV) ? (size_t)Mb * 2 * (c.D / c.conv_group) * 4 : 0);
   L.apart_ctas = apart_max;
-  L.apart_bytes = apart_max * rows_attn * c.hd * 4;
+  // a tree's attention writes two slots a CTA of up to two tiles of query rows
+  int npt = 0, groups = 0, tree_rows = 0;
+  attention_tree_plan(kTreeMax, c.Hq / c.Hkv, &npt, &groups, &tree_rows);
+  const size_t part_rows = std::max(apart_max * rows_attn, (size_t)2 * h->num_sms * tree_rows);
+  L.apart_bytes = part_rows * c.hd * 4;
   L.apart = take(L.apart_bytes);
-  L.aml = take(apart_max * rows_attn * 2 * 4);
+  L.aml = take(part_rows * 2 * 4);
   const int ranges = h->num_sms;
   L.tk_vals = take((size_t)ranges * Ml * c.k_top * 4);
   L.tk_ids = take((size_t)ranges * Ml * c.k_top * 4);
@@ -1258,6 +1262,250 @@ int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, const void *q
   if (attention_slots(nb, c.Hkv, p.grid) > h->ws.apart_ctas)
     return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "attention partials exceed the workspace plan");
   DF_CUDA(launch_attention8(p, stream));
+  return DFLASH_OK;
+}
+
+namespace {
+
+// A tree of m nodes a sequence.
+int check_tree(int m, const int32_t *parent, const char *what) {
+  if (m < 0 || m > kTreeMax) return fail(DFLASH_ERR_INVALID_ARG, "m=%d outside [0, %d]", m, kTreeMax);
+  if (reinterpret_cast<uintptr_t>(parent) % 4) return fail(DFLASH_ERR_INVALID_ARG, "%s is not 4-byte aligned", what);
+  return DFLASH_OK;
+}
+
+int check_words(const char *name, const void *p, bool needed) {
+  if ((needed && !p) || reinterpret_cast<uintptr_t>(p) % 4)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s must be a %s4-byte aligned pointer", name, needed ? "non-NULL " : "");
+  return DFLASH_OK;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+int dflash_attention_tree(dflash_handle_t h, int nb, int layer, int m, const void *q, const void *kcache,
+                          const void *vcache, const int32_t *parent, const int32_t *n_rows, const int32_t *ctx_len,
+                          int max_ctx_hint, int window, int sinks, void *out_o, void *ws, size_t ws_bytes,
+                          dflash_stream_t stream) {
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  const auto &c = h->cfg;
+  if (nb < 0 || nb > c.max_batch) return fail(DFLASH_ERR_INVALID_ARG, "nb=%d outside [0, max_batch]", nb);
+  if (layer < 0 || layer >= c.N) return fail(DFLASH_ERR_INVALID_ARG, "layer=%d outside [0, N)", layer);
+  DF_TRY(check_tree(m, parent, "parent"));
+  if (m > c.Cmax) return fail(DFLASH_ERR_INVALID_ARG, "m=%d beyond Cmax=%d", m, c.Cmax);
+  if (max_ctx_hint < 0 || max_ctx_hint > c.Cmax)
+    return fail(DFLASH_ERR_INVALID_ARG, "max_ctx_hint=%d outside [0, Cmax]", max_ctx_hint);
+  if (window < 0 || sinks < 0) return fail(DFLASH_ERR_INVALID_ARG, "window=%d and sinks=%d must be >= 0", window, sinks);
+  if (nb == 0 || m == 0) return DFLASH_OK;
+  DF_TRY(check_out("q", q));
+  DF_TRY(check_out("out_o", out_o));
+  const size_t bytes = (size_t)nb * m * c.Hq * c.hd * 2;
+  if (q != out_o && overlap(q, bytes, out_o, bytes))  // a row would be written before it is read
+    return fail(DFLASH_ERR_INVALID_ARG, "out_o must be q or not overlap it");
+  DF_TRY(check_out("kcache", kcache));
+  DF_TRY(check_out("vcache", vcache));
+  DF_TRY(check_words("n_rows", n_rows, false));
+  DF_TRY(check_words("ctx_len", ctx_len, true));
+  DF_TRY(check_paging(h));
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  Ws w{static_cast<uint8_t *>(ws), h->ws};
+  const int G = c.Hq / c.Hkv;
+  AttnTreeParams p{};
+  attention_tree_plan(m, G, &p.npt, &p.groups, &p.part_rows);
+  const uint64_t rows = (uint64_t)c.N * cache_layer_rows(c);
+  DF_TRY(encode_3d(&p.tmQ, q, c.hd, c.Hq, (uint64_t)nb * m, c.hd, (uint64_t)c.Hq * c.hd, G, p.npt));
+  DF_TRY(encode_3d(&p.tmK, kcache, 64, rows, c.hd / 64, c.hd, 64, kPageRows, c.hd / 64));
+  DF_TRY(encode_3d(&p.tmV, vcache, 64, rows, c.hd / 64, c.hd, 64, kPageRows, c.hd / 64));
+  p.parent = parent;
+  p.n_rows = n_rows;
+  p.ctx_len = ctx_len;
+  p.o = static_cast<uint16_t *>(out_o);
+  p.part_o = w.at<float>(h->ws.apart);
+  p.part_ml = w.at<float>(h->ws.aml);
+  p.nb = nb;
+  p.m = m;
+  p.Hq = c.Hq;
+  p.Hkv = c.Hkv;
+  p.hd = c.hd;
+  p.Cmax = c.Cmax;
+  p.layer_row0 = static_cast<int>(layer * cache_layer_rows(c));
+  p.window = window;
+  p.sinks = sinks;
+  p.max_ctx = max_ctx_hint > 0 ? max_ctx_hint : c.Cmax;
+  p.page_table = c.num_pages > 0 ? h->block_table : nullptr;
+  p.pages_per_seq = c.Cmax / kPageRows;
+  p.num_pages = c.num_pages;
+  p.grid = h->num_sms;
+  p.status = w.status();
+  p.max_spin = c.max_spin;
+  p.stall = (c.flags & DFLASH_FLAG_TEST_STALL) ? 1 : 0;
+  if ((size_t)2 * p.grid * p.part_rows * c.hd * 4 > h->ws.apart_bytes)
+    return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "attention partials exceed the workspace plan");
+  DF_CUDA(launch_attention_tree(p, stream));
+  return DFLASH_OK;
+}
+
+int dflash_accept_tree(dflash_handle_t h, int nb, int m, const int32_t *parent, const int32_t *tokens,
+                       const int32_t *target, const int32_t *n_rows, int32_t *ctx_len, int32_t *out_tau,
+                       int32_t *out_bonus, int32_t *out_path, int32_t *out_tokens, void *ws, size_t ws_bytes,
+                       dflash_stream_t stream) {
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  if (nb < 0) return fail(DFLASH_ERR_INVALID_ARG, "nb < 0");
+  DF_TRY(check_tree(m, parent, "parent"));
+  if (nb == 0) return DFLASH_OK;
+  DF_TRY(check_words("out_tau", out_tau, true));
+  DF_TRY(check_words("out_bonus", out_bonus, true));
+  const bool some = m > 0;
+  DF_TRY(check_words("parent", parent, some));
+  DF_TRY(check_words("tokens", tokens, some));
+  DF_TRY(check_words("target", target, some));
+  DF_TRY(check_words("n_rows", n_rows, false));
+  DF_TRY(check_words("ctx_len", ctx_len, false));
+  DF_TRY(check_words("out_path", out_path, false));
+  DF_TRY(check_words("out_tokens", out_tokens, false));
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  AcceptTreeParams p{};
+  p.parent = parent;
+  p.tokens = tokens;
+  p.target = target;
+  p.n_rows = n_rows;
+  p.ctx_len = ctx_len;
+  p.out_tau = out_tau;
+  p.out_bonus = out_bonus;
+  p.out_path = out_path;
+  p.out_tokens = out_tokens;
+  p.nb = nb;
+  p.m = m;
+  p.status = Ws{static_cast<uint8_t *>(ws), h->ws}.status();
+  DF_CUDA(launch_accept_tree(p, stream));
+  return DFLASH_OK;
+}
+
+int dflash_kv_commit(dflash_handle_t h, int nb, int m, const int32_t *path, const int32_t *tau,
+                     const int32_t *ctx_len, void *kcache, void *vcache, void *ws, size_t ws_bytes,
+                     dflash_stream_t stream) {
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  const auto &c = h->cfg;
+  if (nb < 0 || nb > c.max_batch) return fail(DFLASH_ERR_INVALID_ARG, "nb=%d outside [0, max_batch]", nb);
+  DF_TRY(check_tree(m, path, "path"));
+  if (nb == 0 || m == 0) return DFLASH_OK;
+  DF_TRY(check_words("path", path, true));
+  DF_TRY(check_words("tau", tau, true));
+  DF_TRY(check_words("ctx_len", ctx_len, true));
+  DF_TRY(check_out("kcache", kcache));
+  DF_TRY(check_out("vcache", vcache));
+  DF_TRY(check_paging(h));
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  KvCommitParams p{};
+  p.cache[0] = static_cast<uint16_t *>(kcache);
+  p.cache[1] = static_cast<uint16_t *>(vcache);
+  p.path = path;
+  p.tau = tau;
+  p.ctx_len = ctx_len;
+  p.layer_rows = (long long)cache_layer_rows(c);
+  p.nb = nb;
+  p.m = m;
+  p.layers = c.N;
+  p.Hkv = c.Hkv;
+  p.hd = c.hd;
+  p.Cmax = c.Cmax;
+  p.page_table = c.num_pages > 0 ? h->block_table : nullptr;
+  p.pages_per_seq = c.Cmax / kPageRows;
+  p.num_pages = c.num_pages;
+  p.status = Ws{static_cast<uint8_t *>(ws), h->ws}.status();
+  DF_CUDA(launch_kv_commit(p, stream));
+  return DFLASH_OK;
+}
+
+int dflash_token_counts(dflash_handle_t h, int nb, int n, const int32_t *tokens, int64_t ld, const int32_t *n_tokens,
+                        int prompt, int32_t *counts, void *ws, size_t ws_bytes, dflash_stream_t stream) {
+  if (!h) return fail(DFLASH_ERR_INVALID_ARG, "handle is NULL");
+  if (nb < 0 || n < 0) return fail(DFLASH_ERR_INVALID_ARG, "nb=%d and n=%d must be >= 0", nb, n);
+  if (nb == 0 || n == 0) return DFLASH_OK;
+  if (nb > 65535) return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "nb=%d: at most 65535", nb);
+  if (ld < n) return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld of tokens: at least %d", (long long)ld, n);
+  DF_TRY(check_words("tokens", tokens, true));
+  DF_TRY(check_words("n_tokens", n_tokens, false));
+  DF_TRY(check_words("counts", counts, true));
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  TokenCountsParams p{};
+  p.tokens = tokens;
+  p.ld = ld;
+  p.n_tokens = n_tokens;
+  p.counts = counts;
+  p.nb = nb;
+  p.n = n;
+  p.V = h->cfg.V;
+  p.prompt = prompt ? 1 : 0;
+  p.status = Ws{static_cast<uint8_t *>(ws), h->ws}.status();
+  DF_CUDA(launch_token_counts(p, stream));
+  return DFLASH_OK;
+}
+
+int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const float *logits, int64_t ld,
+                         const dflash_logit_rules *rules, const int32_t *n_rows, float *out, int64_t ld_out,
+                         int32_t *out_ids, void *ws, size_t ws_bytes, dflash_stream_t stream) {
+  if (!h || !rules) return fail(DFLASH_ERR_INVALID_ARG, "handle and rules must be non-NULL");
+  const int V = h->cfg.V;
+  if (nb < 0) return fail(DFLASH_ERR_INVALID_ARG, "nb < 0");
+  if (m < 0 || m > kTreeMax) return fail(DFLASH_ERR_INVALID_ARG, "m=%d outside [0, %d]", m, kTreeMax);
+  if (rules->n_bias < 0) return fail(DFLASH_ERR_INVALID_ARG, "n_bias < 0");
+  if (rules->n_bias > kMaxBias)
+    return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "n_bias=%d: at most %d", rules->n_bias, kMaxBias);
+  if ((rules->parent == nullptr) != (rules->tokens == nullptr))
+    return fail(DFLASH_ERR_INVALID_ARG, "parent and tokens go together");
+  if (!out && !out_ids) return fail(DFLASH_ERR_INVALID_ARG, "out and out_ids must not both be NULL");
+  if (V > logits_max_vocab()) return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "V=%d: at most %d", V, logits_max_vocab());
+  if (nb == 0 || m == 0) return DFLASH_OK;
+  if (nb > (1 << 20)) return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "nb=%d: at most 2^20", nb);
+  if (ld < V || (out && ld_out < V))
+    return fail(DFLASH_ERR_INVALID_ARG, "row strides %lld and %lld: at least V=%d", (long long)ld, (long long)ld_out, V);
+  DF_TRY(check_words("logits", logits, true));
+  DF_TRY(check_words("out", out, false));
+  DF_TRY(check_words("out_ids", out_ids, false));
+  DF_TRY(check_words("n_rows", n_rows, false));
+  DF_TRY(check_words("penalties", rules->penalties, false));
+  DF_TRY(check_words("counts", rules->counts, false));
+  DF_TRY(check_words("bias_ids", rules->bias_ids, rules->n_bias > 0));
+  DF_TRY(check_words("bias", rules->bias, rules->n_bias > 0));
+  DF_TRY(check_words("allowed", rules->allowed, false));
+  DF_TRY(check_words("parent", rules->parent, false));
+  DF_TRY(check_words("tokens", rules->tokens, false));
+  const size_t rows = (size_t)nb * m;
+  if (out && !(out == logits && ld_out == ld) &&
+      overlap(logits, ((rows - 1) * ld + V) * 4, out, ((rows - 1) * ld_out + V) * 4))
+    return fail(DFLASH_ERR_INVALID_ARG, "out must be logits with the same stride or not overlap it");
+  DF_TRY(check_ws(h, ws, ws_bytes));
+  DF_TRY(check_device(h));
+  LogitsParams p{};
+  p.x = logits;
+  p.y = out;
+  p.ids = out_ids;
+  p.ldx = ld;
+  p.ldy = ld_out;
+  p.penalties = rules->penalties;
+  p.counts = rules->counts;
+  p.bias_ids = rules->bias_ids;
+  p.bias = rules->bias;
+  p.n_bias = rules->n_bias;
+  p.allowed = rules->allowed;
+  p.parent = rules->parent;
+  p.tokens = rules->tokens;
+  p.n_rows = n_rows;
+  p.nb = nb;
+  p.m = m;
+  p.V = V;
+  p.words = (V + 31) / 32;
+  p.status = Ws{static_cast<uint8_t *>(ws), h->ws}.status();
+  DF_CUDA(launch_logits_adjust(p, h->num_sms, stream));
   return DFLASH_OK;
 }
 

@@ -326,6 +326,91 @@ constexpr int kAttn8FewRows = 16;  // query rows R = G*m of a kv head up to whic
 // The kernel for more of them (attention8_wide.cu), without the merge.
 cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 
+// ---------------------------------------------------------------- trees of drafted tokens
+
+constexpr int kTreeMax = 64;  // nodes of a tree (a row's ancestors are the bits of 64)
+
+// Attention of a tree's nodes over the bf16 caches (attention_tree.cu).
+struct AttnTreeParams {
+  CUtensorMap tmQ;           // q as {hd, Hq heads, nb*m rows}, box {64, Hq/Hkv, npt}
+  CUtensorMap tmK, tmV;      // caches of every layer as {64, rows, hd/64}, box {64, 64, hd/64}
+  const int *parent;         // [nb][m] or null: a chain
+  const int *n_rows;         // [nb] or null: m
+  const int *ctx_len;        // [nb]
+  uint16_t *o;               // bf16 [nb][m][Hq][hd]
+  float *part_o;             // [2 * grid slots][part_rows][hd] unnormalised partial outputs
+  float *part_ml;            // [2 * grid slots][part_rows][2] (running maximum, running sum)
+  int nb, m, Hq, Hkv, hd, Cmax;
+  int npt, groups, part_rows;  // nodes of a tile, groups of tiles of a kv head, rows of a slot
+  int layer_row0;            // first cache row of the layer
+  int window, sinks;         // window 0: none
+  int max_ctx;               // caller's bound on ctx_len (larger values are reported and clamped)
+  const int *page_table;
+  int pages_per_seq, num_pages;
+  int grid;
+  int *status;
+  int max_spin;
+  int stall;                 // test hook: issue no loads so the waits run out
+};
+void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows);
+cudaError_t launch_attention_tree(const AttnTreeParams &p, cudaStream_t s);
+
+// Walk of the trees along the target's tokens (tree_ops.cu).
+struct AcceptTreeParams {
+  const int *parent, *tokens, *target;  // [nb][m]
+  const int *n_rows;                    // [nb] or null: m
+  int *ctx_len;                         // [nb] or null: advanced by tau
+  int *out_tau, *out_bonus;             // [nb]
+  int *out_path, *out_tokens;           // [nb][m] or null
+  int nb, m;
+  int *status;
+};
+cudaError_t launch_accept_tree(const AcceptTreeParams &p, cudaStream_t s);
+
+// Move of accepted paths' cache rows to the rows behind the context, every layer (tree_ops.cu).
+struct KvCommitParams {
+  uint16_t *cache[2];        // keys, values: every layer
+  const int *path;           // [nb][m]
+  const int *tau, *ctx_len;  // [nb]; ctx_len with tau counted in
+  long long layer_rows;
+  int nb, m, layers, Hkv, hd, Cmax;
+  const int *page_table;
+  int pages_per_seq, num_pages;
+  int *status;
+};
+cudaError_t launch_kv_commit(const KvCommitParams &p, cudaStream_t s);
+
+// Penalties, biases and masks on logits, and the greedy token (logits.cu).
+struct LogitsParams {
+  const float *x;            // [nb * m] rows of stride ldx
+  float *y;                  // rows of stride ldy, or null
+  int *ids;                  // [nb * m] or null
+  long long ldx, ldy;
+  const float *penalties;    // [nb][3] or null
+  const int *counts;         // [nb][V] or null
+  const int *bias_ids;       // [nb][n_bias]
+  const float *bias;
+  const uint32_t *allowed;   // [nb * m][words] or null
+  const int *parent, *tokens;  // [nb][m] or null
+  const int *n_rows;         // [nb] or null: m
+  int nb, m, V, n_bias, words;
+  int *status;
+  int groups, slices, chunk, hash;  // work split, set by the launch
+};
+constexpr int kMaxBias = 1024;
+int logits_max_vocab();
+cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s);
+
+struct TokenCountsParams {
+  const int *tokens;         // [nb] rows of n, stride ld
+  long long ld;
+  const int *n_tokens;       // [nb] or null: n
+  int *counts;               // [nb][V]
+  int nb, n, V, prompt;
+  int *status;
+};
+cudaError_t launch_token_counts(const TokenCountsParams &p, cudaStream_t s);
+
 // Slots of partial outputs the attention of nb sequences may write: at most one per
 // (pair, CTA) boundary, i.e. nb * Hkv + grid.
 inline size_t attention_slots(int nb, int Hkv, int grid) { return (size_t)nb * Hkv + grid; }

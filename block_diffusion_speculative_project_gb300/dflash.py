@@ -44,6 +44,7 @@ class dflash_config(ctypes.Structure):
 
 
 DFLASH_PAGE_ROWS = 64
+DFLASH_TREE_MAX = 64
 
 
 _P = ctypes.c_void_p
@@ -58,6 +59,11 @@ class dflash_layer_weights(ctypes.Structure):
 class dflash_weights(ctypes.Structure):
     _fields_ = [(n, _P) for n in ("W_c", "g_ctx", "E", "W_lm", "g_final", "W_A", "W_B", "W_G")] + [
         ("layers", ctypes.POINTER(dflash_layer_weights)), ("film_W1", _P), ("film_W2", _P)]
+
+
+class dflash_logit_rules(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("penalties", "counts", "bias_ids", "bias")] + [("n_bias", ctypes.c_int)] + [
+        (n, _P) for n in ("allowed", "parent", "tokens")]
 
 
 def _load():
@@ -85,6 +91,12 @@ def _load():
         "dflash_kv_append8": (i, [p, i, i, i, p, ctypes.c_int64, p, ctypes.c_int64, p, i, p, p, p, p, p, p, p,
                                   sz, p]),
         "dflash_attention8": (i, [p, i, i, i, p, p, p, p, p, p, p, i, i, p, p, sz, p]),
+        "dflash_attention_tree": (i, [p, i, i, i, p, p, p, p, p, p, i, i, i, p, p, sz, p]),
+        "dflash_logits_adjust": (i, [p, i, i, p, ctypes.c_int64, ctypes.POINTER(dflash_logit_rules), p, p,
+                                     ctypes.c_int64, p, p, sz, p]),
+        "dflash_token_counts": (i, [p, i, i, p, ctypes.c_int64, p, i, p, p, sz, p]),
+        "dflash_accept_tree": (i, [p, i, i, p, p, p, p, p, p, p, p, p, p, sz, p]),
+        "dflash_kv_commit": (i, [p, i, i, p, p, p, p, p, p, sz, p]),
         "dflash_topk": (i, [p, i, i, p, i, p, p, p, sz, p]),
         "dflash_accept": (i, [p, i, p, p, p, p, p]),
         "dflash_accept_topk": (i, [p, i, p, i, p, p, p, p]),
@@ -118,7 +130,8 @@ EXPORTED = ("dflash_create", "dflash_destroy", "dflash_set_weights", "dflash_set
             "dflash_lm_head_sample", "dflash_draw_gumbel", "dflash2_select_sample",
             "dflash_verify_sample_walk", "dflash_recall_at_k", "dflash2_conv",
             "dflash2_select", "dflash_qk_norm_rope", "dflash_kv_append", "dflash_kv_append8",
-            "dflash_attention8")
+            "dflash_attention8", "dflash_attention_tree", "dflash_logits_adjust", "dflash_token_counts",
+            "dflash_accept_tree", "dflash_kv_commit")
 
 
 def _check(rc: int):
@@ -239,6 +252,44 @@ def dflash_attention8(h, nb, layer, m, q, kcache8, vcache8, kscale, vscale, n_ro
     _check(LIB.dflash_attention8(h, nb, layer, m, _ptr(q), _ptr(kcache8), _ptr(vcache8), _ptr(kscale),
                                  _ptr(vscale), _ptr(n_rows), _ptr(ctx_len), max_ctx_hint, causal, _ptr(out_o),
                                  _ptr(ws), ws.nbytes, _stream(stream)))
+
+
+def dflash_attention_tree(h, nb, layer, m, q, kcache, vcache, parent, n_rows, ctx_len, max_ctx_hint, window, sinks,
+                          out_o, ws, stream=None) -> None:
+    _check(LIB.dflash_attention_tree(h, nb, layer, m, _ptr(q), _ptr(kcache), _ptr(vcache), _ptr(parent),
+                                     _ptr(n_rows), _ptr(ctx_len), max_ctx_hint, window, sinks, _ptr(out_o),
+                                     _ptr(ws), ws.nbytes, _stream(stream)))
+
+
+def logit_rules(penalties=None, counts=None, bias_ids=None, bias=None, allowed=None, parent=None,
+                tokens=None) -> dflash_logit_rules:
+    """The rules of dflash_logits_adjust, which holds the tensors' addresses and keeps them alive."""
+    r = dflash_logit_rules(_ptr(penalties), _ptr(counts), _ptr(bias_ids), _ptr(bias),
+                           0 if bias_ids is None else bias_ids.shape[-1], _ptr(allowed), _ptr(parent), _ptr(tokens))
+    r.tensors = (penalties, counts, bias_ids, bias, allowed, parent, tokens)
+    return r
+
+
+def dflash_logits_adjust(h, nb, m, logits, ld, rules, n_rows, out, ld_out, out_ids, ws, stream=None) -> None:
+    _check(LIB.dflash_logits_adjust(h, nb, m, _ptr(logits), ld, rules, _ptr(n_rows), _ptr(out), ld_out,
+                                    _ptr(out_ids), _ptr(ws), ws.nbytes, _stream(stream)))
+
+
+def dflash_token_counts(h, nb, n, tokens, ld, n_tokens, prompt, counts, ws, stream=None) -> None:
+    _check(LIB.dflash_token_counts(h, nb, n, _ptr(tokens), ld, _ptr(n_tokens), prompt, _ptr(counts), _ptr(ws),
+                                   ws.nbytes, _stream(stream)))
+
+
+def dflash_accept_tree(h, nb, m, parent, tokens, target, n_rows, ctx_len, out_tau, out_bonus, out_path, out_tokens, ws,
+                       stream=None) -> None:
+    _check(LIB.dflash_accept_tree(h, nb, m, _ptr(parent), _ptr(tokens), _ptr(target), _ptr(n_rows), _ptr(ctx_len),
+                                  _ptr(out_tau), _ptr(out_bonus), _ptr(out_path), _ptr(out_tokens), _ptr(ws),
+                                  ws.nbytes, _stream(stream)))
+
+
+def dflash_kv_commit(h, nb, m, path, tau, ctx_len, kcache, vcache, ws, stream=None) -> None:
+    _check(LIB.dflash_kv_commit(h, nb, m, _ptr(path), _ptr(tau), _ptr(ctx_len), _ptr(kcache), _ptr(vcache),
+                                _ptr(ws), ws.nbytes, _stream(stream)))
 
 
 def dflash_topk(h, rows, cols, logits, k, out_ids, out_vals, ws=None, stream=None) -> None:

@@ -223,6 +223,83 @@ class Drafter:
         _d.dflash_attention8(self.h, nb, layer, m, q, self.kcache8, self.vcache8, self.kscale, self.vscale, n_rows,
                              ctx_len, max_ctx_hint, int(causal), out_o, self.ws, stream)
 
+    def attention_tree(self, nb, layer, m, q, ctx_len, out_o, parent=None, n_rows=None, window=0, sinks=0,
+                       max_ctx_hint=0, stream=None):
+        s = self.shape
+        self._dense("q", q, nb * m * s.Hq * s.hd)
+        self._dense("out_o", out_o, nb * m * s.Hq * s.hd)
+        self._dense("ctx_len", ctx_len, nb, torch.int32)
+        self._maybe("parent", parent, nb * m, torch.int32)
+        self._maybe("n_rows", n_rows, nb, torch.int32)
+        _d.dflash_attention_tree(self.h, nb, layer, m, q, self.kcache, self.vcache, parent, n_rows, ctx_len,
+                                 max_ctx_hint, window, sinks, out_o, self.ws, stream)
+
+    def _maybe(self, name, t, count, dtype):
+        if t is not None:
+            self._dense(name, t, count, dtype)
+
+    def _logits(self, name, t, rows):
+        """Row stride of t, which has to be f32 [rows or more, V] with dense rows."""
+        self._mine(name, t, torch.float32)
+        V = self.shape.V
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != V or t.stride(1) != 1 or (rows > 1 and t.stride(0) < V):
+            raise ValueError(f"{name}: rows [{rows}, {V}] with values side by side, "
+                             f"got {tuple(t.shape)} with strides {t.stride()}")
+        return t.stride(0) if t.shape[0] > 1 else V
+
+    def logits_adjust(self, nb, m, logits, out=None, out_ids=None, penalties=None, counts=None, bias_ids=None,
+                      bias=None, allowed=None, parent=None, tokens=None, n_rows=None, stream=None):
+        """logits, out: rows [nb * m, V] of any row stride; out may be logits."""
+        V = self.shape.V
+        ld = self._logits("logits", logits, nb * m)
+        ld_out = V if out is None else self._logits("out", out, nb * m)
+        self._maybe("out_ids", out_ids, nb * m, torch.int32)
+        self._maybe("penalties", penalties, nb * 3, torch.float32)
+        self._maybe("counts", counts, nb * V, torch.int32)
+        if (bias is None) != (bias_ids is None):
+            raise ValueError("bias and bias_ids go together")
+        if bias_ids is not None:
+            if bias_ids.dim() != 2 or bias_ids.shape[0] < nb or bias.shape != bias_ids.shape:
+                raise ValueError(f"bias_ids and bias: [{nb}, n], got {tuple(bias_ids.shape)} and {tuple(bias.shape)}")
+            self._dense("bias_ids", bias_ids, bias_ids.numel(), torch.int32)
+            self._dense("bias", bias, bias.numel(), torch.float32)
+        if allowed is not None:
+            if allowed.dtype not in (torch.int32, torch.uint32):
+                raise ValueError(f"allowed: words of 32 bits, got {allowed.dtype}")
+            self._dense("allowed", allowed, nb * m * (-(-V // 32)), allowed.dtype)
+        self._maybe("parent", parent, nb * m, torch.int32)
+        self._maybe("tokens", tokens, nb * m, torch.int32)
+        self._maybe("n_rows", n_rows, nb, torch.int32)
+        rules = _d.logit_rules(penalties, counts, bias_ids, bias, allowed, parent, tokens)
+        _d.dflash_logits_adjust(self.h, nb, m, logits, ld, rules, n_rows, out, ld_out, out_ids, self.ws, stream)
+
+    def token_counts(self, nb, n, tokens, counts, n_tokens=None, prompt=False, stream=None):
+        """tokens: int32 [nb or more, n or more] of any row stride."""
+        self._mine("tokens", tokens, torch.int32)
+        if tokens.dim() != 2 or tokens.shape[0] < nb or tokens.shape[1] < n or tokens.stride(1) != 1:
+            raise ValueError(f"tokens: rows [{nb}, {n}] with values side by side, "
+                             f"got {tuple(tokens.shape)} with strides {tokens.stride()}")
+        self._dense("counts", counts, nb * self.shape.V, torch.int32)
+        self._maybe("n_tokens", n_tokens, nb, torch.int32)
+        ld = tokens.stride(0) if tokens.shape[0] > 1 else tokens.shape[1]
+        _d.dflash_token_counts(self.h, nb, n, tokens, ld, n_tokens, int(prompt), counts, self.ws, stream)
+
+    def accept_tree(self, nb, m, parent, tokens, target, out_tau, out_bonus, out_path=None, out_tokens=None,
+                    n_rows=None, ctx_len=None, stream=None):
+        for name, t in (("parent", parent), ("tokens", tokens), ("target", target), ("out_path", out_path),
+                        ("out_tokens", out_tokens)):
+            self._maybe(name, t, nb * m, torch.int32)
+        for name, t in (("out_tau", out_tau), ("out_bonus", out_bonus), ("n_rows", n_rows), ("ctx_len", ctx_len)):
+            self._maybe(name, t, nb, torch.int32)
+        _d.dflash_accept_tree(self.h, nb, m, parent, tokens, target, n_rows, ctx_len, out_tau, out_bonus, out_path,
+                              out_tokens, self.ws, stream)
+
+    def kv_commit(self, nb, m, path, tau, ctx_len, stream=None):
+        self._dense("path", path, nb * m, torch.int32)
+        self._dense("tau", tau, nb, torch.int32)
+        self._dense("ctx_len", ctx_len, nb, torch.int32)
+        _d.dflash_kv_commit(self.h, nb, m, path, tau, ctx_len, self.kcache, self.vcache, self.ws, stream)
+
     def topk(self, rows, cols, logits, k, out_ids, out_vals, stream=None):
         _d.dflash_topk(self.h, rows, cols, logits, k, out_ids, out_vals, None, stream)
 

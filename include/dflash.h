@@ -389,6 +389,126 @@ DFLASH_API int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, co
                                  int max_ctx_hint, int causal, void *out_o, void *ws, size_t ws_bytes,
                                  dflash_stream_t stream);
 
+/* ------------------------------------------------------------------ trees of drafted tokens
+ *
+ * The pages draft one path a block; dflash_lm_head_topk's lists hold more, and a verify pass may take
+ * a tree of them (no counterpart on the pages). Sequence i's tree has n <= m <= DFLASH_TREE_MAX nodes
+ * (n = n_rows[i], or m where n_rows is NULL), in the arrays below in rows of m:
+ *   parent      int32 [nb, m] device: parent[0] = -1 for the root, the last committed token (the
+ *               anchor of [DFlash] 符号约定); 0 <= parent[j] < j for every other node. Another value is
+ *               reported as DFLASH_ERR_DEVICE_CHECK by dflash_status, and its node taken for one
+ *               without a parent: no walk accepts it.
+ *   tokens      int32 [nb, m] device: the nodes' token ids
+ * depth(0) = 0, depth(j) = depth(parent[j]) + 1; node j's keys and values lie in cache row
+ * ctx_len[i] + j (dflash_kv_append with rotate = 0), rotated at position ctx_len[i] + depth(j)
+ * (dflash_qk_norm_rope with R = 1 takes a position a row).
+ *
+ * A round: dflash_attention_tree in every layer; dflash_logits_adjust on the target's logits, whose
+ * ids are the greedy tokens (at temperature T, dflash_sample on its output: a token drawn from the
+ * target's own distribution at every node, so the path that follows them is distributed as the
+ * target's own text); dflash_accept_tree; dflash_kv_commit; dflash_token_counts of what was emitted. */
+#define DFLASH_TREE_MAX 64
+
+/* dflash_attention over the bf16 caches for a tree's nodes ([DFlash] 二、块扩散草稿 attention
+ * equations, with a mask): one node is the decode step, a chain (parent = NULL: parent[j] = j - 1) is
+ * causal. Node j sees the context row p < ctx_len[i] if window = 0, if
+ * p > ctx_len[i] + depth(j) - window, or if p < sinks; and the rows of the nodes from j up to the
+ * root by the same rule at their positions. The rows' keys and values have been appended before.
+ *   m           rows of q a sequence, 0..DFLASH_TREE_MAX, at most Cmax; any number of query heads a kv head
+ *   q           bf16 [nb, m, Hq, hd]: rotated queries
+ *   kcache, vcache  the caches, contiguous or paged
+ *   n_rows      int32 [nb] device, 0 <= n_rows[i] <= m, or NULL: m. Rows j >= n_rows[i] of out_o are
+ *               left as they were.
+ *   ctx_len     int32 [nb] device; ctx_len[i] + n_rows[i] <= Cmax
+ *   max_ctx_hint  an upper bound on every ctx_len[i], 0: none
+ *   window      0: no window; else the positions a node sees, its own among them
+ *   sinks       with a window, first cache rows that stay visible
+ *   out_o       bf16 [nb, m, Hq, hd]: softmax(q K^T / sqrt(hd)) V, query head h reading kv head
+ *               h / (Hq/Hkv). May be q itself; otherwise it must not overlap q (refused).
+ * Arithmetic: bf16 products in fp32 sums, the softmax in fp32, probabilities rounded to bf16, one
+ * rounding to bf16. Cache rows that a query row does not see may hold anything, NaN too. A value that is
+ * not finite makes the output of the rows that see it not finite: in its channel, and near a mask's
+ * edge and among the tree's own rows in every channel of the row. Only visible blocks of 64 rows are
+ * read. Lengths and counts out of range are clamped and reported as DFLASH_ERR_DEVICE_CHECK by
+ * dflash_status, a page outside the pool is read as page 0 and reported. Bitwise reproducible as
+ * dflash_draft_block is. */
+DFLASH_API int dflash_attention_tree(dflash_handle_t h, int nb, int layer, int m, const void *q,
+                                     const void *kcache, const void *vcache, const int32_t *parent,
+                                     const int32_t *n_rows, const int32_t *ctx_len, int max_ctx_hint,
+                                     int window, int sinks, void *out_o, void *ws, size_t ws_bytes,
+                                     dflash_stream_t stream);
+
+/* What dflash_logits_adjust does to a row; every pointer is a device pointer, NULL: without it. */
+typedef struct dflash_logit_rules {
+  const float *penalties;   /* f32 [nb, 3]: repetition (> 0, 1: none), frequency and presence (0: none) */
+  const int32_t *counts;    /* int32 [nb, V] of dflash_token_counts: bit 31 the prompt has the token, bits
+                               0..30 how often it was generated */
+  const int32_t *bias_ids;  /* int32 [nb, n_bias]: tokens with a bias; ids outside [0, V) count for nothing */
+  const float *bias;        /* f32 [nb, n_bias]: added; an id given twice gets the sum */
+  int n_bias;               /* 0..1024 */
+  const uint32_t *allowed;  /* [nb * m, (V + 31) / 32]: bit v % 32 of word v / 32: row may emit token v */
+  const int32_t *parent;    /* int32 [nb, m], with tokens: the rows are a tree's nodes */
+  const int32_t *tokens;
+} dflash_logit_rules;
+
+/* Penalties for repeated tokens, biases and masks on the target's (or a draft's) logits, and the greedy
+ * token of each row, in one pass ([DFlash] dflash_cycle takes the argmax of logits as they are). For
+ * token v of row j of sequence i:
+ *   c    = generated count of v, and one more for each node from j up to the root, the root left
+ *          out (its token was counted when it was emitted), whose token is v
+ *   y    = x / repetition (x > 0) or x * repetition where c > 0 or the prompt has v, else x
+ *   y   -= frequency * c + presence * [c > 0];   y += biases of v;   y = -inf where not allowed
+ * in fp32, -inf and NaN as IEEE arithmetic has them.
+ *   logits      f32 rows, row j of sequence i at i*m + j, row stride ld >= V (elements)
+ *   m           rows a sequence, 0..DFLASH_TREE_MAX
+ *   n_rows      int32 [nb] or NULL: m; further rows are neither read nor written
+ *   out         f32 rows of stride ld_out, or NULL. May be logits with the same stride; otherwise
+ *               they must not overlap (refused).
+ *   out_ids     int32 [nb * m] or NULL: argmax of y, the lowest id of equals; -1 where no token is
+ *               above -inf
+ * Rows that are 16-byte aligned with strides and V multiples of 4 are read in 16-byte pieces. Not
+ * limited to max_batch; needs no weights. V up to 1.2 million. */
+DFLASH_API int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const float *logits, int64_t ld,
+                                    const dflash_logit_rules *rules, const int32_t *n_rows, float *out,
+                                    int64_t ld_out, int32_t *out_ids, void *ws, size_t ws_bytes,
+                                    dflash_stream_t stream);
+
+/* Counts of tokens, for the penalties of dflash_logits_adjust.
+ *   tokens      int32 rows of n, row stride ld >= n (elements): e.g. out_tokens of dflash_accept_tree
+ *   n_tokens    int32 [nb] or NULL: n; 0 <= n_tokens[i] <= n tokens of sequence i count (e.g. out_tau)
+ *   prompt      0: counts[i][t] += 1 for each token t; else bit 31 of counts[i][t] is set
+ *   counts      int32 [nb, V]; the caller zeroes a sequence's row when a request begins
+ * A token outside [0, V) is reported as DFLASH_ERR_DEVICE_CHECK by dflash_status and not counted. */
+DFLASH_API int dflash_token_counts(dflash_handle_t h, int nb, int n, const int32_t *tokens, int64_t ld,
+                                   const int32_t *n_tokens, int prompt, int32_t *counts, void *ws,
+                                   size_t ws_bytes, dflash_stream_t stream);
+
+/* dflash_accept for a tree: from the root to the lowest child whose token is target[node], until there
+ * is none ([DFlash] 符号约定: tau counts the bonus token).
+ *   target      int32 [nb, m]: the target's token behind each node; a negative one ends the walk
+ *   ctx_len     int32 [nb] or NULL: advanced by tau (the rows that dflash_kv_commit moves)
+ *   out_tau     int32 [nb]: nodes on the path, the root among them, which is the number of tokens
+ *               emitted; 0 for a sequence without rows
+ *   out_bonus   int32 [nb]: target[last node of the path], the next root's token; -1 without rows
+ *   out_path    int32 [nb, m] or NULL: the path's nodes, then -1
+ *   out_tokens  int32 [nb, m] or NULL: the tau tokens emitted, the bonus token last, then -1 */
+DFLASH_API int dflash_accept_tree(dflash_handle_t h, int nb, int m, const int32_t *parent,
+                                  const int32_t *tokens, const int32_t *target, const int32_t *n_rows,
+                                  int32_t *ctx_len, int32_t *out_tau, int32_t *out_bonus,
+                                  int32_t *out_path, int32_t *out_tokens, void *ws, size_t ws_bytes,
+                                  dflash_stream_t stream);
+
+/* Moves an accepted path's keys and values behind the context, in the bf16 caches of every layer: with
+ * base = ctx_len[i] - tau[i], cache row base + path[i][t] to row base + t for t < tau[i].
+ *   path        int32 [nb, m]: rising, path[i][t] >= t (a row that is not, or lies outside the cache or
+ *               the pool, is not moved and reported as DFLASH_ERR_DEVICE_CHECK by dflash_status)
+ *   tau         int32 [nb], 0..m
+ *   ctx_len     int32 [nb]: the lengths with tau counted in, as dflash_accept_tree leaves them
+ * Sequences of one call share no page that a row moves to. */
+DFLASH_API int dflash_kv_commit(dflash_handle_t h, int nb, int m, const int32_t *path, const int32_t *tau,
+                                const int32_t *ctx_len, void *kcache, void *vcache, void *ws,
+                                size_t ws_bytes, dflash_stream_t stream);
+
 /* Top-k of each row of an fp32 matrix with the same ordering rule as
  * dflash_lm_head_topk (value descending, ties to the lower column; [DFlash2] 洞察一 keeps
  * the top-16 per position). No counterpart call on the pages: it checks the selection rule

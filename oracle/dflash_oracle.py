@@ -749,3 +749,89 @@ def attention8(q: np.ndarray, K: np.ndarray, V: np.ndarray, ctx: int, causal: bo
             mag[j, h] = p @ np.abs(v[:L])
             dot[j, h] = (np.abs(k[:L]) @ np.abs(q[j, h])).max() / np.sqrt(hd)
     return o, mag, dot
+
+
+# --------------------------------------------------------------------------- trees of drafted tokens
+
+def tree_lines(parent):
+    """Each node's line up to the root, itself first."""
+    out = []
+    for j in range(len(parent)):
+        line = [j]
+        while parent[line[-1]] >= 0:
+            line.append(int(parent[line[-1]]))
+        out.append(line)
+    return out
+
+
+def tree_visible(parent, ctx: int, window: int, sinks: int) -> np.ndarray:
+    """[n, ctx + n] truth values: the cache rows that each node of a tree behind ctx rows sees."""
+    n = len(parent)
+    lines = tree_lines(parent)
+    depth = np.array([len(x) - 1 for x in lines])
+    at = np.concatenate([np.arange(ctx), ctx + depth])
+    seen = np.zeros((n, ctx + n), bool)
+    for j in range(n):
+        seen[j, :ctx] = True
+        for a in lines[j]:
+            seen[j, ctx + a] = True
+        if window:
+            seen[j] &= (at > ctx + depth[j] - window) | (at < sinks)
+    return seen
+
+
+def attention_tree(q: np.ndarray, K: np.ndarray, V: np.ndarray, seen: np.ndarray):
+    """q [n, Hq, hd], K and V [Hkv, rows, hd], seen [n, rows]. Returns o [n, Hq, hd] and, for tolerances,
+    sum p |v| [n, Hq, hd] and max_k sum_d |q_d k_d| / sqrt(hd) [n, Hq]. Rows that are not seen do not matter."""
+    n, Hq, hd = q.shape
+    G = Hq // K.shape[0]
+    o, mag, dot = np.zeros(q.shape), np.zeros(q.shape), np.zeros((n, Hq))
+    for j in range(n):
+        rows = np.flatnonzero(seen[j])
+        for h in range(Hq):
+            k, v = K[h // G, rows], V[h // G, rows]
+            x = k @ q[j, h] / np.sqrt(hd)
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            o[j, h] = p @ v
+            mag[j, h] = p @ np.abs(v)
+            dot[j, h] = (np.abs(k) @ np.abs(q[j, h])).max() / np.sqrt(hd)
+    return o, mag, dot
+
+
+def adjust_logits(x, counts=None, penalties=None, drafted=(), bias_ids=(), bias=(), allowed=None) -> np.ndarray:
+    """One row of logits under its rules. counts [V]: bit 31 the prompt's, bits 0..30 generated; drafted:
+    the tokens on the row's path; allowed [V] truth values."""
+    y = np.array(x, np.float64)
+    rep, freq, pres = penalties if penalties is not None else (1.0, 0.0, 0.0)
+    for v in range(len(y)):
+        word = int(counts[v]) & 0xFFFFFFFF if counts is not None else 0
+        c = (word & 0x7FFFFFFF) + sum(int(t) == v for t in drafted)
+        if c or word >> 31:
+            y[v] = y[v] / rep if y[v] > 0 else y[v] * rep
+            y[v] -= freq * c + (pres if c else 0.0)
+    for t, b in zip(bias_ids, bias):
+        if 0 <= t < len(y):
+            y[t] += b
+    if allowed is not None:
+        y[~np.asarray(allowed, bool)] = -np.inf
+    return y
+
+
+def greedy(y) -> int:
+    """The lowest id of the largest value, -1 if none is above -inf (NaN counts for nothing)."""
+    y = np.where(np.isnan(y), -np.inf, y)
+    return int(np.argmax(y)) if y.max() > -np.inf else -1
+
+
+def accept_tree(parent, tokens, target):
+    """(path, emitted) of one tree: from the root to the lowest child with the target's token."""
+    if len(parent) == 0:
+        return [], []
+    path = [0]
+    while True:
+        want = int(target[path[-1]])
+        child = [j for j in range(path[-1] + 1, len(parent)) if parent[j] == path[-1] and tokens[j] == want and want >= 0]
+        if not child:
+            return path, [int(target[a]) for a in path]
+        path.append(child[0])
