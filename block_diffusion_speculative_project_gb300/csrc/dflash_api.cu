@@ -132,6 +132,7 @@ struct WsLayout {
   size_t apart = 0, aml = 0;                   // attention partials (dflash_attention_tree's too)
   size_t tk_vals = 0, tk_ids = 0;              // LM head top-k partial lists
   size_t sel_e = 0, sel_ab = 0, sel_g = 0, sel_t = 0;  // selector
+  size_t lg_part = 0;                          // slices' best of dflash_logits_adjust
   size_t film_cond = 0, film_hid = 0, film_bg = 0;     // FiLM relay
   size_t smp_part = 0, smp_lse = 0, ver_part = 0, ver_nrej = 0;  // sampling
   size_t total = 0;
@@ -210,6 +211,7 @@ void plan_workspace(dflash_handle_s *h) {
   L.smp_lse = take((size_t)Mb * 4);
   L.ver_part = take((size_t)c.max_batch * kSampleMaxSlices * 16);
   L.ver_nrej = take((size_t)c.max_batch * 4);
+  L.lg_part = take((size_t)c.max_batch * kTreeMax * kLogitSlots * sizeof(float2));
   if (c.flags & DFLASH_FLAG_FILM) {
     L.film_cond = take((size_t)Mb * 3 * c.D * 2);
     L.film_hid = take((size_t)Mb * c.film_dim * 2);
@@ -1463,7 +1465,7 @@ int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const float *logits, 
   if ((rules->parent == nullptr) != (rules->tokens == nullptr))
     return fail(DFLASH_ERR_INVALID_ARG, "parent and tokens go together");
   if (!out && !out_ids) return fail(DFLASH_ERR_INVALID_ARG, "out and out_ids must not both be NULL");
-  if (V > logits_max_vocab()) return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "V=%d: at most %d", V, logits_max_vocab());
+  if (V > kMaxVocab) return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "V=%d: at most %d", V, kMaxVocab);
   if (nb == 0 || m == 0) return DFLASH_OK;
   if (nb > (1 << 20)) return fail(DFLASH_ERR_UNSUPPORTED_SHAPE, "nb=%d: at most 2^20", nb);
   if (ld < V || (out && ld_out < V))
@@ -1485,27 +1487,32 @@ int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const float *logits, 
     return fail(DFLASH_ERR_INVALID_ARG, "out must be logits with the same stride or not overlap it");
   DF_TRY(check_ws(h, ws, ws_bytes));
   DF_TRY(check_device(h));
+  Ws w{static_cast<uint8_t *>(ws), h->ws};
   LogitsParams p{};
-  p.x = logits;
-  p.y = out;
-  p.ids = out_ids;
   p.ldx = ld;
   p.ldy = ld_out;
-  p.penalties = rules->penalties;
-  p.counts = rules->counts;
-  p.bias_ids = rules->bias_ids;
-  p.bias = rules->bias;
   p.n_bias = rules->n_bias;
-  p.allowed = rules->allowed;
-  p.parent = rules->parent;
-  p.tokens = rules->tokens;
-  p.n_rows = n_rows;
-  p.nb = nb;
   p.m = m;
   p.V = V;
   p.words = (V + 31) / 32;
-  p.status = Ws{static_cast<uint8_t *>(ws), h->ws}.status();
-  DF_CUDA(launch_logits_adjust(p, h->num_sms, stream));
+  p.part = w.at<float2>(h->ws.lg_part);
+  p.status = w.status();
+  for (int i0 = 0; i0 < nb; i0 += h->cfg.max_batch) {  // the scratch holds max_batch sequences' rows
+    const long long r0 = (long long)i0 * m;
+    p.nb = std::min(nb - i0, h->cfg.max_batch);
+    p.x = logits + r0 * ld;
+    p.y = out ? out + r0 * ld_out : nullptr;
+    p.ids = out_ids ? out_ids + r0 : nullptr;
+    p.penalties = rules->penalties ? rules->penalties + 3LL * i0 : nullptr;
+    p.counts = rules->counts ? rules->counts + (long long)i0 * V : nullptr;
+    p.bias_ids = rules->n_bias ? rules->bias_ids + (long long)i0 * rules->n_bias : nullptr;
+    p.bias = rules->n_bias ? rules->bias + (long long)i0 * rules->n_bias : nullptr;
+    p.allowed = rules->allowed ? rules->allowed + r0 * p.words : nullptr;
+    p.parent = rules->parent ? rules->parent + r0 : nullptr;
+    p.tokens = rules->tokens ? rules->tokens + r0 : nullptr;
+    p.n_rows = n_rows ? n_rows + i0 : nullptr;
+    DF_CUDA(launch_logits_adjust(p, h->num_sms, stream));
+  }
   return DFLASH_OK;
 }
 

@@ -395,10 +395,12 @@ struct LogitsParams {
   const int *n_rows;         // [nb] or null: m
   int nb, m, V, n_bias, words;
   int *status;
-  int groups, slices, chunk, hash;  // work split, set by the launch
+  float2 *part;              // scratch of the ids: kLogitSlots (value, id) pairs a row
+  int slices, chunk, splits, rows, hash;  // work split, set by the launch
 };
 constexpr int kMaxBias = 1024;
-int logits_max_vocab();
+constexpr int kMaxVocab = 1 << 21;
+constexpr int kLogitSlots = 256;  // most slices of a row: kMaxVocab in slices of 8192 tokens
 cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s);
 
 struct TokenCountsParams {

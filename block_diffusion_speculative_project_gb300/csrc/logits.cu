@@ -11,11 +11,17 @@
 //   id   = argmax y, the lowest id of equals, -1 where nothing is above -inf (a NaN never is)
 //
 // One pass over the logits: 8 bytes a value (4 where only ids are asked for), 4 more a sequence for its
-// counts, a bit a value for the mask. A CTA takes a slice of the vocabulary for a few rows of one
-// sequence, so that the counts are loaded once for them; the CTAs of a row are a cluster, whose first
-// one picks the row's id through distributed shared memory, without scratch or a second launch.
-// Biased and drafted tokens are few: a bitmap of the slice in shared memory marks them, and only marked
-// values look their biases up (a hash of the slice's biased ids) and count the drafted nodes.
+// counts, a bit a value for the mask. A warp takes up to 1024 tokens for rows of one sequence, RPC of them
+// at a time: the tokens that are counted, biased or drafted are found once, as a bit each in a word a
+// lane, and every lane's copies of the rows' values run ahead of it through its own places in shared
+// memory, so that a warp waits for nobody.
+// Few tokens are listed so, but next to every row of a warp's values has one, and in line they would cost the
+// warp their division and look-ups for one lane's sake (1159 us for 1024 rows of 151936). So the pass masks
+// and takes the maximum of the others, and behind it the warp works its listed tokens off, a lane a
+// token. Biased and drafted tokens are marked in a bitmap of the CTA; only marked ones look their biases
+// up (a hash has the ids' sums) and the nodes they are drafted by. Where ids are asked for, a second
+// launch picks each row's among its slices'.
+#include <algorithm>
 #include <cfloat>
 
 #include "common.cuh"
@@ -25,8 +31,8 @@ namespace df {
 
 namespace {
 
-constexpr int kMaxSlice = 152 * 1024;    // values of a slice: the bitmap's 19 KB
-constexpr int kSlices = 8;               // CTAs of a row: a portable cluster
+constexpr int kWarps = 8;                // of a CTA
+constexpr int kTiles = 8;                // most of a warp: 128 tokens each, a word of 32 a lane
 
 __device__ __forceinline__ uint32_t id_hash(int id, uint32_t mask) { return (static_cast<uint32_t>(id) * 2654435761u >> 12) & mask; }
 
@@ -35,6 +41,10 @@ __device__ __forceinline__ void take_best(float &v, int &id, float w, int wid) {
   const bool better = w > v || (w == v && wid >= 0 && (id < 0 || wid < id));
   v = better ? w : v;
   id = better ? wid : id;
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 struct RowRules {
@@ -50,57 +60,116 @@ __device__ __forceinline__ float adjust(float x, int count, int drafted, const R
   return x;
 }
 
-template <int T, int RPC, int U, bool VEC>
-__global__ void __launch_bounds__(T) logits_adjust_kernel(const LogitsParams p) {
-  extern __shared__ uint32_t dyn[];
+// RPC rows at a time, S stages of a tile of theirs in flight. VEC: rows of 16-byte pieces, a lane's four
+// values side by side; else they lie 32 apart and are loaded as they are needed. MASK: the rows have masks.
+template <int RPC, int S, bool VEC, bool MASK>
+__global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) logits_adjust_kernel(const LogitsParams p) {
+  constexpr int T = 32 * kWarps;
+  extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ int s_token[kTreeMax];
   __shared__ int s_parent[kTreeMax];
   __shared__ unsigned long long s_line[kTreeMax];  // drafted nodes from a node up
-  __shared__ float s_val[RPC][T / 32];
-  __shared__ int s_id[RPC][T / 32];
-  __shared__ float4 s_best[RPC];
+  __shared__ float s_val[kTreeMax][kWarps];
+  __shared__ int s_id[kTreeMax][kWarps];
+  __shared__ uint32_t marked[kWarps * 32];         // biased or drafted
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float *ring = reinterpret_cast<float *>(dyn) + warp * (S * RPC * 128) + (VEC ? 4 : 1) * lane;
+  int *hkey = reinterpret_cast<int *>(dyn + kWarps * S * RPC * 512);  // [hash]: id, -1 free
+  float *hsum = reinterpret_cast<float *>(hkey + p.hash);
+  int *hcount = reinterpret_cast<int *>(hsum + p.hash);
   const int slice = blockIdx.x % p.slices;
   const int at = blockIdx.x / p.slices;
-  const int i = at / p.groups, grp = at % p.groups;
-  const int v0 = min(p.V, slice * p.chunk), v1 = min(p.V, v0 + p.chunk);
-  const int nwords = (p.chunk + 31) / 32;
-  uint32_t *marked = dyn;                                     // [nwords]
-  int *hkey = reinterpret_cast<int *>(dyn + nwords);          // [hash]: id, -1 free
-  int *hfirst = hkey + p.hash;                                // first place in the list
-  int *hcount = hfirst + p.hash;
-  float *hsum = reinterpret_cast<float *>(hcount + p.hash);
+  const int i = at / p.splits, split = at % p.splits;
+  const int v0 = slice * p.chunk, v1 = min(p.V, v0 + p.chunk);
   const bool special = p.n_bias > 0 || p.parent != nullptr;
   if (special) {
-    for (int e = tid; e < nwords; e += T) marked[e] = 0;
+    marked[tid] = 0;
     for (int e = tid; e < p.hash; e += T) {
       hkey[e] = -1;
-      hfirst[e] = 0x7fffffff;
       hcount[e] = 0;
     }
   }
   griddep_wait();
   griddep_launch();
   int n = p.n_rows ? p.n_rows[i] : p.m;
-  if ((n < 0 || n > p.m) && slice == 0 && grp == 0 && tid == 0) flag_status(p.status, kStatusCheck);
+  if ((n < 0 || n > p.m) && slice == 0 && split == 0 && tid == 0) flag_status(p.status, kStatusCheck);
   n = max(0, min(n, p.m));
-  const int j0 = grp * RPC;
-  const int rows = min(RPC, n - j0);
-  if (rows <= 0) return;  // the same for a whole cluster
+  const int j0 = split * p.rows, j1 = min(n, j0 + p.rows);  // this CTA's rows
+  if (j0 >= j1) return;
+
+  // ---- the pass begins: the first tiles' copies, the counts
+  const int wt = p.chunk / (128 * kWarps);           // tiles of a warp
+  const int base = v0 + warp * wt * 128;             // its first token
+  const int tiles = base < v1 ? min(wt, (v1 - base + 127) / 128) : 0;
+  const int steps = tiles * ((j1 - j0 + RPC - 1) / RPC);
+  const long long seq = (long long)i * p.m;
+  const float *x0 = p.x + seq * p.ldx + base + (VEC ? 4 : 1) * lane;
+  // rows behind the last repeat it: the same values go to the same places
+  int f_row = j0, f_tile = 0;
+  auto fetch = [&](int step) {
+    if (step < steps) {
+#pragma unroll
+      for (int r = 0; r < RPC; ++r) {
+        const float *from = x0 + min(f_row + r, j1 - 1) * p.ldx + 128 * f_tile;
+        const uint32_t to = smem_u32(ring + (step % S * RPC + r) * 128);
+        if (VEC) {
+          if (base + 128 * f_tile + 4 * lane < v1) cp_async16(to, from);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (base + 128 * f_tile + 32 * q + lane < v1) cp_async4(to + 128 * q, from + 32 * q);
+        }
+      }
+      if (++f_tile == tiles) {
+        f_tile = 0;
+        f_row += RPC;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int k = 0; k < S - 1; ++k) fetch(k);
+  const int *counts = p.counts ? p.counts + (long long)i * p.V + base : nullptr;
+  uint32_t listed = 0;  // word `lane` of the warp's tokens
+  if (counts) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      if (t >= tiles) break;
+      if (VEC) {
+        uint32_t w = 0;
+        if (base + 128 * t + 4 * lane < v1) {
+          const int4 c = __ldg(reinterpret_cast<const int4 *>(counts + 128 * t) + lane);
+          w = ((c.x ? 1u : 0u) | (c.y ? 2u : 0u) | (c.z ? 4u : 0u) | (c.w ? 8u : 0u)) << (4 * (lane & 7));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+        w = __shfl_sync(0xffffffffu, w, 8 * (lane & 3));
+        if (lane >> 2 == t) listed = w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 128 * t + 32 * q + lane;
+          const uint32_t w = __ballot_sync(0xffffffffu, base + e < v1 && __ldg(counts + e) != 0);
+          if (lane == 4 * t + q) listed = w;
+        }
+      }
+    }
+  }
   RowRules rules = {1.f, 0.f, 0.f};
   if (p.penalties) {
     rules.rep = p.penalties[3 * i];
     rules.freq = p.penalties[3 * i + 1];
     rules.pres = p.penalties[3 * i + 2];
   }
+
+  // ---- biased and drafted tokens
   const uint32_t hmask = p.hash - 1;
   if (special) {
     if (p.parent)
       for (int j = tid; j < n; j += T) {
-        s_token[j] = p.tokens[(long long)i * p.m + j];
-        const int up = p.parent[(long long)i * p.m + j];
+        s_token[j] = p.tokens[seq + j];
+        const int up = p.parent[seq + j];
         const bool ok = j == 0 ? up == -1 : up >= 0 && up < j;
-        if (!ok && slice == 0 && grp == 0) flag_status(p.status, kStatusCheck);
+        if (!ok && slice == 0 && split == 0) flag_status(p.status, kStatusCheck);
         s_parent[j] = ok ? up : -1;
       }
     __syncthreads();
@@ -117,7 +186,6 @@ __global__ void __launch_bounds__(T) logits_adjust_kernel(const LogitsParams p) 
         h = (h + 1) & hmask;
       }
       atomicAdd(&hcount[h], 1);
-      atomicMin(&hfirst[h], e);
     }
     if (p.parent)
       for (int j = tid; j < n; j += T) {
@@ -128,146 +196,243 @@ __global__ void __launch_bounds__(T) logits_adjust_kernel(const LogitsParams p) 
         if (line >> j & 1 && id >= v0 && id < v1) atomicOr(&marked[(id - v0) >> 5], 1u << ((id - v0) & 31));
       }
     __syncthreads();
-    // an id's first entry adds the others up, in the list's order
-    for (int e = tid; e < p.n_bias; e += T) {
-      const int id = ids[e];
-      if (id < v0 || id >= v1) continue;
-      uint32_t h = id_hash(id, hmask);
-      while (hkey[h] != id) h = (h + 1) & hmask;
-      if (hfirst[h] != e) continue;
-      float sum = bias[e];
-      for (int left = hcount[h] - 1, q = e + 1; left > 0 && q < p.n_bias; ++q)
-        if (ids[q] == id) {
-          sum += bias[q];
-          --left;
+    // An id that comes once has its bias; a warp together adds up what another id has, in the list's order,
+    // whoever of its entries asks.
+    for (int e0 = 32 * warp; e0 < p.n_bias; e0 += T) {
+      const int e = e0 + lane;
+      const int id = e < p.n_bias ? ids[e] : -1;
+      const bool mine = id >= v0 && id < v1;
+      uint32_t h = 0;
+      if (mine) {
+        h = id_hash(id, hmask);
+        while (hkey[h] != id) h = (h + 1) & hmask;
+        if (hcount[h] == 1) hsum[h] = bias[e];
+      }
+      unsigned again = __ballot_sync(0xffffffffu, mine && hcount[h] > 1);
+      while (again) {
+        const int from = __ffs(again) - 1;
+        const int want = __shfl_sync(0xffffffffu, id, from);
+        again &= ~__ballot_sync(0xffffffffu, id == want);
+        float sum = 0.f;
+        for (int q0 = 0; q0 < p.n_bias; q0 += 32) {
+          const int q = q0 + lane;
+          const bool same = q < p.n_bias && ids[q] == want;
+          const float b = same ? bias[q] : 0.f;
+          for (unsigned hit = __ballot_sync(0xffffffffu, same); hit; hit &= hit - 1)
+            sum += __shfl_sync(0xffffffffu, b, __ffs(hit) - 1);
         }
-      hsum[h] = sum;
+        if (lane == from) hsum[h] = sum;  // other warps may write the same
+      }
     }
     __syncthreads();
+    if (lane < 4 * wt) listed |= marked[warp * wt * 4 + lane];
   }
 
-  const long long row0 = (long long)i * p.m + j0;
-  const float *x = p.x + row0 * p.ldx;
-  float *y = p.y ? p.y + row0 * p.ldy : nullptr;
-  const int *counts = p.counts ? p.counts + (long long)i * p.V : nullptr;
-  const uint32_t *allowed = p.allowed ? p.allowed + row0 * p.words : nullptr;
-  float best[RPC];
-  int best_id[RPC];
+  // ---- rows
+  const float *x = p.x + seq * p.ldx + base;
+  float *y = p.y ? p.y + seq * p.ldy + base : nullptr;
+  const uint32_t *allowed = MASK ? p.allowed + seq * p.words + (base >> 5) : nullptr;
+  const int left = (v1 - base + 31) >> 5;  // words of the warp
+  const int ones = __popc(listed);
+  int before = ones;
 #pragma unroll
-  for (int r = 0; r < RPC; ++r) {
-    best[r] = -INFINITY;
-    best_id[r] = -1;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += up;
   }
-  for (int v = v0 + 4 * tid; v < v1; v += 4 * T * U) {
-    float a[U][RPC][4];
-    int c[U][4];
-    uint32_t ok[U][RPC];
+  const int total = __shfl_sync(0xffffffffu, before, 31);
+  before -= ones;
+  int step = 0;
+  for (int j = j0; j < j1; j += RPC) {
+    uint32_t may[RPC];  // word `lane` of a row's mask
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = v + u * 4 * T;
-      if (g >= v1) continue;
+    for (int r = 0; r < RPC; ++r)
+      if (MASK) may[r] = lane < left ? __ldg(allowed + (long long)min(j + r, j1 - 1) * p.words + lane) : 0u;
+    float best[RPC];   // of the values that are not listed, and where: VEC, the first of their four
+    int best_at[RPC];
+#pragma unroll
+    for (int r = 0; r < RPC; ++r) {
+      best[r] = -INFINITY;
+      best_at[r] = -1;
+    }
+    for (int t = 0; t < tiles; ++t, ++step) {
+      const int e = 128 * t + (VEC ? 4 : 1) * lane;
+      const bool in = base + e < v1;
+      uint32_t sp, ok[RPC];  // bits of this lane's four values
       if (VEC) {
-        const int4 w = counts ? __ldg(reinterpret_cast<const int4 *>(counts + g)) : make_int4(0, 0, 0, 0);
-        c[u][0] = w.x, c[u][1] = w.y, c[u][2] = w.z, c[u][3] = w.w;
-      } else {
+        const int from = 4 * t + (lane >> 3), sh = 4 * (lane & 7);
+        sp = __shfl_sync(0xffffffffu, listed, from) >> sh & 15u;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) c[u][q] = counts && g + q < v1 ? __ldg(counts + g + q) : 0;
+        for (int r = 0; r < RPC; ++r)
+          if (MASK) ok[r] = __shfl_sync(0xffffffffu, may[r], from) >> sh;
+      } else {
+        sp = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sp |= (__shfl_sync(0xffffffffu, listed, 4 * t + q) >> lane & 1) << q;
+#pragma unroll
+        for (int r = 0; r < RPC; ++r) {
+          ok[r] = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (MASK) ok[r] |= (__shfl_sync(0xffffffffu, may[r], 4 * t + q) >> lane & 1) << q;
+        }
       }
+      float out[4];  // takes listed values from the maximum, and keeps a NaN one
+#pragma unroll
+      for (int q = 0; q < 4; ++q) out[q] = sp >> q & 1 ? -INFINITY : 0.f;
+      float z[RPC][4];
+      fetch(step + S - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
 #pragma unroll
       for (int r = 0; r < RPC; ++r) {
-        if (r >= rows) continue;
-        ok[u][r] = allowed ? __ldg(allowed + (long long)r * p.words + (g >> 5)) >> (g & 31) : ~0u;
-        const float *from = x + r * p.ldx + g;
+        const float *at_r = ring + (step % S * RPC + r) * 128;
         if (VEC) {
-          const float4 w = *reinterpret_cast<const float4 *>(from);
-          a[u][r][0] = w.x, a[u][r][1] = w.y, a[u][r][2] = w.z, a[u][r][3] = w.w;
+          const float4 w = *reinterpret_cast<const float4 *>(at_r);
+          z[r][0] = w.x, z[r][1] = w.y, z[r][2] = w.z, z[r][3] = w.w;
         } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) a[u][r][q] = g + q < v1 ? from[q] : -INFINITY;
+          for (int q = 0; q < 4; ++q) z[r][q] = base + e + 32 * q < v1 ? at_r[32 * q] : -INFINITY;
         }
       }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = v + u * 4 * T;
-      if (g >= v1) continue;
-      const uint32_t sp = special ? marked[(g - v0) >> 5] >> ((g - v0) & 31) & 15u : 0u;
-      const bool heard = (c[u][0] | c[u][1] | c[u][2] | c[u][3]) != 0;
 #pragma unroll
       for (int r = 0; r < RPC; ++r) {
-        if (r >= rows) continue;
-        float(&z)[4] = a[u][r];
-        if (sp) {
+        if (MASK) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            int drafted = 0;
-            float add = 0.f;
-            if (sp >> q & 1) {
-              if (p.parent)
-                for (unsigned long long line = s_line[j0 + r]; line; line &= line - 1)
-                  drafted += s_token[__ffsll(line) - 1] == g + q;
-              if (p.n_bias) {
-                uint32_t h = id_hash(g + q, hmask);
-                while (hkey[h] != -1 && hkey[h] != g + q) h = (h + 1) & hmask;
-                if (hkey[h] != -1) add = hsum[h];
-              }
-            }
-            z[q] = adjust(z[q], c[u][q], drafted, rules) + add;
-          }
-        } else if (heard) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) z[q] = adjust(z[q], c[u][q], 0, rules);
+          for (int q = 0; q < 4; ++q) z[r][q] = ok[r] >> q & 1 ? z[r][q] : -INFINITY;
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (!(ok[u][r] >> q & 1)) z[q] = -INFINITY;
         if (y) {
-          float *to = y + r * p.ldy + g;
+          float *to = y + min(j + r, j1 - 1) * p.ldy + e;
           if (VEC) {
-            *reinterpret_cast<float4 *>(to) = make_float4(z[0], z[1], z[2], z[3]);
+            if (in) *reinterpret_cast<float4 *>(to) = make_float4(z[r][0], z[r][1], z[r][2], z[r][3]);
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (g + q < v1) to[q] = z[q];
+              if (base + e + 32 * q < v1) to[32 * q] = z[r][q];
           }
         }
-        const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-        if (top > best[r]) {  // a thread's ids rise, so the first of equals stays
-          best[r] = top;
-          best_id[r] = g + (z[0] == top ? 0 : z[1] == top ? 1 : z[2] == top ? 2 : 3);
+        // places rise here, so the first of equals stays
+        if (VEC) {
+          const float m = fmaxf(fmaxf(z[r][0] + out[0], z[r][1] + out[1]), fmaxf(z[r][2] + out[2], z[r][3] + out[3]));
+          const bool more = in && m > best[r];
+          best[r] = more ? m : best[r];
+          best_at[r] = more ? e : best_at[r];
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float m = z[r][q] + out[q];
+            const bool more = m > best[r];
+            best[r] = more ? m : best[r];
+            best_at[r] = more ? e + 32 * q : best_at[r];
+          }
+        }
+      }
+    }
+    __syncwarp();  // the listed values of y are written again by other lanes
+    float top[RPC];
+    int top_at[RPC];
+#pragma unroll
+    for (int r = 0; r < RPC; ++r) {
+      top[r] = -INFINITY;
+      top_at[r] = -1;
+    }
+    for (int k0 = 0; k0 < total; k0 += 32) {
+      // lane k takes the listed token of number k: in the last word with fewer before it
+      const int k = k0 + lane;
+      int from = 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const int b = __shfl_sync(0xffffffffu, before, from + o);
+        if (b <= k) from += o;
+      }
+      uint32_t w = __shfl_sync(0xffffffffu, listed, from);
+      const int skip = k - __shfl_sync(0xffffffffu, before, from);
+      uint32_t mw[RPC];
+#pragma unroll
+      for (int r = 0; r < RPC; ++r)
+        if (MASK) mw[r] = __shfl_sync(0xffffffffu, may[r], from);
+      if (k >= total) continue;
+      for (int s = 0; s < skip; ++s) w &= w - 1;
+      const int bit = __ffs(w) - 1;
+      const int e = 32 * from + bit, id = base + e;
+      float z[RPC];
+#pragma unroll
+      for (int r = 0; r < RPC; ++r) z[r] = x[min(j + r, j1 - 1) * p.ldx + e];
+      const int count = counts ? __ldg(counts + e) : 0;
+      float add = 0.f;
+      unsigned long long nodes = 0;  // with this token
+      if (special && marked[(id - v0) >> 5] >> bit & 1) {
+        if (p.parent)
+          for (int a = 1; a < n; ++a) nodes |= static_cast<unsigned long long>(s_token[a] == id) << a;
+        if (p.n_bias) {
+          uint32_t h = id_hash(id, hmask);
+          while (hkey[h] != -1 && hkey[h] != id) h = (h + 1) & hmask;
+          if (hkey[h] != -1) add = hsum[h];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RPC; ++r) {
+        const int drafted = nodes ? __popcll(s_line[min(j + r, j1 - 1)] & nodes) : 0;
+        const float v = !MASK || mw[r] >> bit & 1 ? adjust(z[r], count, drafted, rules) + add : -INFINITY;
+        if (y) y[min(j + r, j1 - 1) * p.ldy + e] = v;
+        if (v > top[r]) {  // places rise
+          top[r] = v;
+          top_at[r] = e;
+        }
+      }
+    }
+    __syncwarp();
+    if (p.ids) {
+#pragma unroll
+      for (int r = 0; r < RPC; ++r) {
+        const float b = warp_max(best[r]), w = warp_max(top[r]);
+        unsigned at_b = __reduce_min_sync(0xffffffffu, best[r] == b ? static_cast<unsigned>(best_at[r]) : 0xffffffffu);
+        const unsigned at_w = __reduce_min_sync(0xffffffffu, top[r] == w ? static_cast<unsigned>(top_at[r]) : 0xffffffffu);
+        if (VEC && at_b != 0xffffffffu) {  // which of the four: the first that is the maximum, allowed and not listed
+          const uint32_t good = (MASK ? __shfl_sync(0xffffffffu, may[r], at_b >> 5) : ~0u) &
+                                ~__shfl_sync(0xffffffffu, listed, at_b >> 5);
+          const float mine = lane < 4 ? x[min(j + r, j1 - 1) * p.ldx + at_b + lane] : 0.f;
+          const unsigned hit = __ballot_sync(0xffffffffu, lane < 4 && mine == b && (good >> ((at_b & 31) + lane) & 1));
+          at_b += __ffs(hit) - 1;
+        }
+        float v = b;
+        int id = at_b == 0xffffffffu ? -1 : base + static_cast<int>(at_b);
+        take_best(v, id, w, at_w == 0xffffffffu ? -1 : base + static_cast<int>(at_w));
+        if (lane == 0 && j + r < j1) {
+          s_val[j + r][warp] = v;
+          s_id[j + r][warp] = id;
         }
       }
     }
   }
   if (!p.ids) return;
-#pragma unroll
-  for (int r = 0; r < RPC; ++r) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      take_best(best[r], best_id[r], __shfl_xor_sync(0xffffffffu, best[r], o), __shfl_xor_sync(0xffffffffu, best_id[r], o));
-    if (lane == 0) {
-      s_val[r][warp] = best[r];
-      s_id[r][warp] = best_id[r];
-    }
-  }
   __syncthreads();
-  if (tid < rows) {
+  for (int j = j0 + tid; j < j1; j += T) {
     float b = -INFINITY;
     int id = -1;
-    for (int w = 0; w < T / 32; ++w) take_best(b, id, s_val[tid][w], s_id[tid][w]);
-    s_best[tid] = make_float4(b, __int_as_float(id), 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) take_best(b, id, s_val[j][k], s_id[j][k]);
+    p.part[(seq + j) * p.slices + slice] = make_float2(b, __int_as_float(id));
   }
-  cluster_sync_all();
-  if (slice == 0 && tid < rows) {
-    float b = -INFINITY;
-    int id = -1;
-    for (int q = 0; q < p.slices; ++q) {
-      const float4 o = ld_cluster_f4(cluster_map(smem_u32(&s_best[tid]), q));
-      take_best(b, id, o.x, __float_as_int(o.y));
-    }
-    p.ids[row0 + tid] = id;
+}
+
+// The id of each row among its slices' best: one warp a row.
+__global__ void __launch_bounds__(128) logits_ids_kernel(const LogitsParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  griddep_wait();
+  griddep_launch();
+  if (r >= (long long)p.nb * p.m) return;
+  if (p.n_rows && static_cast<int>(r % p.m) >= p.n_rows[r / p.m]) return;
+  float b = -INFINITY;
+  int id = -1;
+  for (int s = lane; s < p.slices; s += 32) {
+    const float2 o = p.part[r * p.slices + s];
+    take_best(b, id, o.x, __float_as_int(o.y));
   }
-  cluster_sync_all();  // the others' shared memory stays until it was read
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    take_best(b, id, __shfl_xor_sync(0xffffffffu, b, o), __shfl_xor_sync(0xffffffffu, id, o));
+  if (lane == 0) p.ids[r] = id;
 }
 
 // counts[i][token] += 1, or its top bit set. Lanes of a warp with the same token send one update of
@@ -295,43 +460,58 @@ __global__ void __launch_bounds__(256) token_counts_kernel(const TokenCountsPara
   }
 }
 
-template <int T, int RPC, int U, bool VEC>
-cudaError_t launch_adjust(LogitsParams &p, cudaStream_t s) {
-  p.groups = (p.m + RPC - 1) / RPC;
-  p.slices = kSlices;
-  // slices of whole mask words, the same length but for the last
-  p.chunk = ((p.V + p.slices - 1) / p.slices + 31) / 32 * 32;
+template <int RPC, int S, bool VEC, bool MASK>
+cudaError_t launch_adjust(LogitsParams &p, int tiles, int rows, cudaStream_t s) {
+  p.chunk = tiles * 128 * kWarps;
+  p.slices = (p.V + p.chunk - 1) / p.chunk;
+  p.rows = rows;
+  p.splits = (p.m + rows - 1) / rows;
   p.hash = 0;
   if (p.n_bias > 0)
     for (p.hash = 32; p.hash < 2 * p.n_bias;) p.hash *= 2;
-  size_t smem = 0;
-  if (p.n_bias > 0 || p.parent) smem = (size_t)(p.chunk / 32 + 4 * p.hash) * 4;
-  if (smem > 40 * 1024) {
-    static const cudaError_t configured = cudaFuncSetAttribute(
-        logits_adjust_kernel<T, RPC, U, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-    if (configured != cudaSuccess) return configured;
-  }
-  const dim3 grid(static_cast<unsigned>((long long)p.nb * p.groups * p.slices));
-  return launch_pdl_cluster(logits_adjust_kernel<T, RPC, U, VEC>, grid, dim3(T), smem, s, p.slices, p);
+  const size_t smem = kWarps * S * RPC * 512 + (size_t)p.hash * 12;
+  static const cudaError_t configured = cudaFuncSetAttribute(logits_adjust_kernel<RPC, S, VEC, MASK>,
+                                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+  if (configured != cudaSuccess) return configured;
+  const dim3 grid(static_cast<unsigned>((long long)p.nb * p.splits * p.slices));
+  const cudaError_t e = launch_pdl(logits_adjust_kernel<RPC, S, VEC, MASK>, grid, dim3(32 * kWarps), smem, s, p);
+  if (e != cudaSuccess || !p.ids) return e;
+  const long long all = (long long)p.nb * p.m;
+  return launch_pdl(logits_ids_kernel, dim3(static_cast<unsigned>((all + 3) / 4)), dim3(128), 0, s, p);
 }
 
-template <int T, int RPC, int U>
-cudaError_t launch_adjust(LogitsParams &p, bool vec, cudaStream_t s) {
-  return vec ? launch_adjust<T, RPC, U, true>(p, s) : launch_adjust<T, RPC, U, false>(p, s);
+template <int RPC, int S>
+cudaError_t launch_adjust(LogitsParams &p, bool vec, int tiles, int rows, cudaStream_t s) {
+  if (vec)
+    return p.allowed ? launch_adjust<RPC, S, true, true>(p, tiles, rows, s)
+                     : launch_adjust<RPC, S, true, false>(p, tiles, rows, s);
+  return p.allowed ? launch_adjust<RPC, S, false, true>(p, tiles, rows, s)
+                   : launch_adjust<RPC, S, false, false>(p, tiles, rows, s);
 }
 
 }  // namespace
-
-int logits_max_vocab() { return kSlices * kMaxSlice; }
 
 cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s) {
   auto aligned = [](const void *q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 4 == 0; };
   const bool vec = aligned(p.x, p.ldx) && (!p.y || aligned(p.y, p.ldy)) && (!p.counts || aligned(p.counts, p.V)) &&
                    p.V % 4 == 0;
-  // rows of one sequence that share the loads of its counts, where enough CTAs remain
-  const long long ctas = (long long)p.nb * p.m * kSlices;
-  if (p.m >= 4 && ctas >= 16LL * num_sms) return launch_adjust<256, 8, 1>(p, vec, s);
-  return launch_adjust<512, 1, 4>(p, vec, s);
+  // A warp of 1024 tokens for all of a sequence's rows where that gives each SM eight CTAs, two rows at a time
+  // (1024 rows of 151936: 236 us; one at a time 240, four 251). Else about eight CTAs a SM, four rows or
+  // more each (64 rows of one sequence 27 us, in warps of 256 tokens for 16 rows 32), and where those are
+  // less than two a SM, fewer tokens a warp (16 rows: 12 us, with 1024 tokens 14; one row 6, with 1024 9).
+  auto slices = [&](int tiles) { return ((long long)p.V + tiles * 128 * kWarps - 1) / (tiles * 128 * kWarps); };
+  if (p.nb * slices(kTiles) >= 8LL * num_sms)
+    return p.m > 1 ? launch_adjust<2, 3>(p, vec, kTiles, p.m, s) : launch_adjust<1, 4>(p, vec, kTiles, 1, s);
+  const int at_once = p.m >= 4 ? 4 : p.m > 1 ? 2 : 1;
+  const int groups = (p.m + at_once - 1) / at_once;
+  const long long per = std::max<long long>(1, p.nb * slices(kTiles) * groups / (8 * num_sms));
+  const int rows = at_once * static_cast<int>(std::min<long long>(per, groups));
+  int tiles = kTiles;
+  while (tiles > 1 && p.nb * slices(tiles) * ((p.m + rows - 1) / rows) < 7LL * num_sms / 4 &&
+         slices(tiles / 2) <= kLogitSlots)
+    tiles /= 2;
+  if (at_once == 4) return launch_adjust<4, 2>(p, vec, tiles, rows, s);
+  return at_once == 2 ? launch_adjust<2, 3>(p, vec, tiles, rows, s) : launch_adjust<1, 4>(p, vec, tiles, rows, s);
 }
 
 cudaError_t launch_token_counts(const TokenCountsParams &p, cudaStream_t s) {

@@ -467,7 +467,7 @@ typedef struct dflash_logit_rules {
  *   out_ids     int32 [nb * m] or NULL: argmax of y, the lowest id of equals; -1 where no token is
  *               above -inf
  * Rows that are 16-byte aligned with strides and V multiples of 4 are read in 16-byte pieces. Not
- * limited to max_batch; needs no weights. V up to 1.2 million. */
+ * limited to max_batch; needs no weights. V up to 2^21. */
 DFLASH_API int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const float *logits, int64_t ld,
                                     const dflash_logit_rules *rules, const int32_t *n_rows, float *out,
                                     int64_t ld_out, int32_t *out_ids, void *ws, size_t ws_bytes,
