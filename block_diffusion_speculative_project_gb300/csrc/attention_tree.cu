@@ -157,12 +157,7 @@ __device__ int find_sequence(const AttnTreeParams &p, long long u0, int lane, lo
 
 constexpr int kSeqCache = 64;  // sequences whose lengths a CTA keeps in shared memory
 
-struct Walk {
-  int pair, unit, seg, seg_unit0, left;
-  int stage;   // units before this one
-  Span s;
-};
-__device__ __forceinline__ Span walk_span(const AttnTreeParams &p, const int2 *seqs, int i) {
+__device__ __forceinline__ Span span_of(const AttnTreeParams &p, const int2 *seqs, int i) {
   int2 v;
   if (i < kSeqCache) {
     v = seqs[i];
@@ -172,28 +167,61 @@ __device__ __forceinline__ Span walk_span(const AttnTreeParams &p, const int2 *s
   }
   return make_span(p, v.x, v.y);
 }
-__device__ __forceinline__ bool walk_first(const Walk &w) { return w.unit == w.seg_unit0; }
-__device__ __forceinline__ bool walk_last(const Walk &w) { return w.left == 1 || w.unit == w.s.U - 1; }
-__device__ __forceinline__ void walk_next(Walk &w, const AttnTreeParams &p, const int2 *seqs) {
-  ++w.stage;
-  --w.left;
-  if (++w.unit == w.s.U) {
-    ++w.pair;
-    w.unit = 0;
-    w.seg_unit0 = 0;
-    ++w.seg;
-    if (w.left > 0) {
-      const int per = p.Hkv * p.groups;
-      int i = w.pair / per;
-      if (w.pair % per == 0) {
-        w.s = walk_span(p, seqs, i);
-        while (w.s.U == 0 && i + 1 < p.nb) {  // sequences without rows have no units
-          w.s = walk_span(p, seqs, ++i);
-          w.pair += per;
-        }
-      }
-    }
+
+// A run of one pair's units [u0, u1) in this CTA's range: sequence i, kv head g, group grp of tiles. All
+// roles go through the same segments; `left` units of the range are not behind it.
+struct Seg {
+  int pair, i, g, grp, u0, u1, index, left;
+  Span s;
+};
+__device__ __forceinline__ void seg_place(Seg &e, const AttnTreeParams &p) {
+  const int per = p.Hkv * p.groups, k = e.pair - e.i * per;
+  e.g = k / p.groups;
+  e.grp = k - e.g * p.groups;
+  e.u1 = min(e.s.U, e.u0 + e.left);
+}
+__device__ __forceinline__ Seg seg_begin(const AttnTreeParams &p, const int2 *seqs, const int *sched) {
+  Seg e;
+  e.pair = sched[0];
+  e.u0 = sched[1];
+  e.left = sched[2];
+  e.index = 0;
+  e.i = 0;
+  if (e.left > 0) {
+    e.i = e.pair / (p.Hkv * p.groups);
+    e.s = span_of(p, seqs, e.i);
+    seg_place(e, p);
   }
+  return e;
+}
+__device__ __forceinline__ void seg_next(Seg &e, const AttnTreeParams &p, const int2 *seqs) {
+  e.left -= e.u1 - e.u0;
+  if (e.left <= 0) return;
+  ++e.index;
+  ++e.pair;
+  e.u0 = 0;
+  const int per = p.Hkv * p.groups;
+  if (e.pair == (e.i + 1) * per) {
+    do {  // sequences without rows have no units
+      e.s = span_of(p, seqs, ++e.i);
+      e.pair = e.i * per;
+    } while (e.s.U == 0 && e.i + 1 < p.nb);
+  }
+  seg_place(e, p);
+}
+
+// A ring's next stage: its place, and the parity of its barriers.
+template <int ST>
+__device__ __forceinline__ void ring_next(int &st, uint32_t &ph) {
+  if (++st == ST) {
+    st = 0;
+    ph ^= 1;
+  }
+}
+// One arrival of a converged warp, behind what all of its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 // Bits [0, k).
@@ -248,7 +276,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   uint8_t *sKV = smem + C::OFF_KV;
   uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *kv_empty = kv_full + ST;    // the last product of the stage, and the cleaner
-  uint64_t *clean = kv_empty + ST;      // masked units: values zeroed, their keys noted
+  uint64_t *clean = kv_empty + ST;      // looked through by the cleaner
   uint64_t *s_full = clean + ST;        // [2]
   uint64_t *s_empty = s_full + 2;       // [2]
   uint64_t *p_full = s_empty + 2;       // [4]: P of step j in buffer j % 4
@@ -279,17 +307,17 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_empty[b], HT);
-      mbar_init(&o_free[b], HT);
+      mbar_init(&s_empty[b], NQ);
+      mbar_init(&o_free[b], NQ);
       mbar_init(&mma_done[b], 1);
     }
     for (int b = 0; b < 4; ++b) {
-      mbar_init(&p_full[b], HT);
+      mbar_init(&p_full[b], NQ);
       mbar_init(&p_empty[b], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(ml_ready, HT);
+    mbar_init(ml_ready, NQ);
     fence_mbar_init();
   }
   if (warp == Ro::PRODUCER && lane == 0) {
@@ -350,62 +378,54 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int nunits = sched[2];
-  const int per = p.Hkv * p.groups;
-  Walk w;
-  w.pair = sched[0];
-  w.unit = w.seg_unit0 = sched[1];
-  w.seg = 0;
-  w.left = nunits;
-  w.stage = 0;
-  if (nunits > 0) w.s = walk_span(p, seqs, w.pair / per);
+  Seg e = seg_begin(p, seqs, sched);
 
   if (warp == Ro::PRODUCER) {
-    if (lane == 0 && nunits > 0 && !p.stall) {
+    if (lane == 0 && e.left > 0 && !p.stall) {
       // K and V of one pair are read by its groups of tiles one after another
       const uint64_t pol_kv = p.groups > 1 ? policy_evict_last() : policy_evict_first();
       const uint64_t pol_q = policy_evict_last();
       bool ok = true;
-      int q_loads = 0, loads = 0;
-      for (; w.left > 0; walk_next(w, p, seqs)) {
-        const int i = w.pair / per, g = w.pair % per / p.groups, grp = w.pair % p.groups;
-        const int base = unit_base(w.s, w.unit);
-        int row;
-        if (p.page_table == nullptr) {
-          row = p.layer_row0 + (i * p.Hkv + g) * p.Cmax + base;
-        } else {
-          int pg = p.page_table[(long long)i * p.pages_per_seq + base / kKeys];
-          if (pg < 0 || pg >= p.num_pages) {
-            flag_status(p.status, kStatusCheck);
-            pg = 0;
-          }
-          row = p.layer_row0 + (pg * p.Hkv + g) * kPageRows;
-        }
-        if (walk_first(w)) {
-          if (w.seg > 0 && !mbar_wait(q_empty, (w.seg - 1) & 1, p.max_spin)) {
-            ok = false;
-            break;
-          }
-          const int node0 = grp * C::TILES * p.npt;
-          const int tiles = TWO && node0 + p.npt < p.m ? 2 : 1;  // a last group may have one tile
-          mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * C::ATOMS * R * 128));
-          for (int h = 0; h < tiles; ++h)
-#pragma unroll
-            for (int a = 0; a < C::ATOMS; ++a)
-              tma_load_3d(sQ + h * C::Q_TILE + a * C::ATOM_Q, &p.tmQ, q_full, a * 64, g * G,
-                          i * p.m + node0 + h * p.npt, pol_q);
-          ++q_loads;
-        }
-        const int st = w.stage % ST;
-        if (w.stage >= ST && !mbar_wait(&kv_empty[st], ((w.stage / ST) & 1) ^ 1, p.max_spin)) {
+      int q_loads = 0, loads = 0, st = 0;
+      uint32_t ph = 0;
+      for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+        if (e.index > 0 && !mbar_wait(q_empty, (e.index - 1) & 1, p.max_spin)) {
           ok = false;
           break;
         }
-        uint8_t *kt = sKV + st * C::STAGE;
-        mbar_arrive_expect_tx(&kv_full[st], C::STAGE);
-        tma_load_3d(kt, &p.tmK, &kv_full[st], 0, row, 0, pol_kv);
-        tma_load_3d(kt + C::KV_TILE, &p.tmV, &kv_full[st], 0, row, 0, pol_kv);
-        loads = w.stage + 1;
+        const int node0 = e.grp * C::TILES * p.npt;
+        const int tiles = TWO && node0 + p.npt < p.m ? 2 : 1;  // a last group may have one tile
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * C::ATOMS * R * 128));
+        for (int h = 0; h < tiles; ++h)
+#pragma unroll
+          for (int a = 0; a < C::ATOMS; ++a)
+            tma_load_3d(sQ + h * C::Q_TILE + a * C::ATOM_Q, &p.tmQ, q_full, a * 64, e.g * G,
+                        e.i * p.m + node0 + h * p.npt, pol_q);
+        ++q_loads;
+        for (int u = e.u0; u < e.u1; ++u) {
+          const int base = unit_base(e.s, u);
+          int row;
+          if (p.page_table == nullptr) {
+            row = p.layer_row0 + (e.i * p.Hkv + e.g) * p.Cmax + base;
+          } else {
+            int pg = p.page_table[(long long)e.i * p.pages_per_seq + base / kKeys];
+            if (pg < 0 || pg >= p.num_pages) {
+              flag_status(p.status, kStatusCheck);
+              pg = 0;
+            }
+            row = p.layer_row0 + (pg * p.Hkv + e.g) * kPageRows;
+          }
+          if (loads >= ST && !mbar_wait(&kv_empty[st], ph ^ 1, p.max_spin)) {
+            ok = false;
+            break;
+          }
+          uint8_t *kt = sKV + st * C::STAGE;
+          mbar_arrive_expect_tx(&kv_full[st], C::STAGE);
+          tma_load_3d(kt, &p.tmK, &kv_full[st], 0, row, 0, pol_kv);
+          tma_load_3d(kt + C::KV_TILE, &p.tmV, &kv_full[st], 0, row, 0, pol_kv);
+          ++loads;
+          ring_next<ST>(st, ph);
+        }
       }
       if (!ok) flag_status(p.status, kStatusTimeout);
       for (int k = max(0, loads - ST); k < loads; ++k)  // every copy lands before the CTA ends
@@ -413,120 +433,129 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, kDrainSpin);
     }
   } else if (warp == Ro::S) {
-    if (lane == 0 && nunits > 0) {
+    if (lane == 0 && e.left > 0) {
       constexpr uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys);
       const uint64_t q_desc0 = sw128_kmajor_desc(smem_u32(sQ));
       const uint64_t k_desc0 = sw128_kmajor_desc(smem_u32(sKV));
       bool ok = true;
-      int step = 0;
-      for (; w.left > 0 && ok; walk_next(w, p, seqs)) {
-        const int st = w.stage % ST;
-        if (walk_first(w) && !mbar_wait(q_full, w.seg & 1, p.max_spin)) ok = false;
-        if (ok && !mbar_wait(&kv_full[st], (w.stage / ST) & 1, p.max_spin)) ok = false;
-#pragma unroll
-        for (int h = 0; h < C::TILES; ++h) {
-          const int sb = step & 1;
-          if (ok && step >= 2 && !mbar_wait(&s_empty[sb], ((step >> 1) - 1) & 1, p.max_spin)) ok = false;
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t qd = q_desc0 + static_cast<uint64_t>((h * C::Q_TILE) >> 4);
+      int step = 0, st = 0;
+      uint32_t ph = 0;
+      for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+        ok = mbar_wait(q_full, e.index & 1, p.max_spin);
+        for (int u = e.u0; u < e.u1 && ok; ++u) {
+          ok = mbar_wait(&kv_full[st], ph, p.max_spin);
           const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-          const uint32_t d_s = tmem_base + C::S_COL + sb * kKeys;
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            tc_mma_bf16(d_s, qd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_Q + (kk & 3) * 32) >> 4),
-                        kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
-                        kk > 0 ? 1u : 0u);
-          tc_commit(&s_full[sb]);
-          ++step;
+          for (int h = 0; h < C::TILES; ++h) {
+            const int sb = step & 1;
+            if (ok && step >= 2) ok = mbar_wait(&s_empty[sb], ((step >> 1) - 1) & 1, p.max_spin);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>((h * C::Q_TILE) >> 4);
+            const uint32_t d_s = tmem_base + C::S_COL + sb * kKeys;
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk)
+              tc_mma_bf16(d_s, qd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_Q + (kk & 3) * 32) >> 4),
+                          kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
+                          kk > 0 ? 1u : 0u);
+            tc_commit(&s_full[sb]);
+            ++step;
+          }
+          ring_next<ST>(st, ph);
         }
-        if (ok && walk_last(w)) tc_commit(q_empty);
+        if (ok) tc_commit(q_empty);
       }
       if (!ok) flag_status(p.status, kStatusTimeout);
       tc_commit(&mma_done[0]);  // every product completes before tensor memory is freed
       mbar_wait(&mma_done[0], 0, kDrainSpin);
     }
   } else if (warp == Ro::PV) {
-    if (lane == 0 && nunits > 0) {
+    if (lane == 0 && e.left > 0) {
       constexpr uint32_t id_pv = idesc_bf16_f32(kTileRows, HD) | kIdescBMajorMN;
       const uint64_t v_desc0 = sw128_mnmajor_desc(smem_u32(sKV + C::KV_TILE), C::ATOM_KV);
       bool ok = true;
-      int step = 0, first = 0;
-      for (; w.left > 0 && ok; walk_next(w, p, seqs)) {
-        const int st = w.stage % ST;
-        if (walk_first(w)) first = step;
-#pragma unroll
-        for (int h = 0; h < C::TILES; ++h) {
-          const int half = step & 1, pb = step & 3;
-          const bool start = step < first + 2;  // the half's first unit of the segment
-          if (!mbar_wait(&p_full[pb], (step >> 2) & 1, p.max_spin)) ok = false;
-          if (ok && start && w.seg > 0 && !mbar_wait(&o_free[TWO ? half : 0], (w.seg - 1) & 1, p.max_spin)) ok = false;
-          if (!ok) break;
-          tc_fence_after();
+      int step = 0, st = 0;
+      uint32_t ph = 0;
+      for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+        const int first = step;
+        for (int u = e.u0; u < e.u1 && ok; ++u) {
           const uint64_t vd = v_desc0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-          const uint32_t d_o = tmem_base + C::O_COL + half * HD;
-          const uint32_t a_p = tmem_base + C::P_COL + pb * 32;
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc_mma_bf16_tmem_a(d_o, a_p + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
-                               (!start || kk > 0) ? 1u : 0u);
-          tc_commit(&p_empty[pb]);
-          ++step;
+          for (int h = 0; h < C::TILES; ++h) {
+            const int half = step & 1, pb = step & 3;
+            const bool start = step < first + 2;  // the half's first unit of the segment
+            ok = mbar_wait(&p_full[pb], (step >> 2) & 1, p.max_spin);
+            if (ok && start && e.index > 0) ok = mbar_wait(&o_free[TWO ? half : 0], (e.index - 1) & 1, p.max_spin);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d_o = tmem_base + C::O_COL + half * HD;
+            const uint32_t a_p = tmem_base + C::P_COL + pb * 32;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc_mma_bf16_tmem_a(d_o, a_p + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
+                                 (!start || kk > 0) ? 1u : 0u);
+            tc_commit(&p_empty[pb]);
+            ++step;
+          }
+          if (ok) tc_commit(&kv_empty[st]);
+          ring_next<ST>(st, ph);
         }
-        if (ok) tc_commit(&kv_empty[st]);
       }
       if (!ok) flag_status(p.status, kStatusTimeout);
       tc_commit(&mma_done[1]);
       mbar_wait(&mma_done[1], 0, kDrainSpin);
     }
   } else if (warp == Ro::CLEAN) {
-    // follows every stage, in order, so that it never takes one phase of a barrier for another
     bool ok = true;
-    for (; w.left > 0; walk_next(w, p, seqs)) {
-      const int st = w.stage % ST;
-      ok = mbar_wait_warp(&kv_full[st], (w.stage / ST) & 1, p.max_spin);
-      if (!ok) break;
-      const int base = unit_base(w.s, w.unit);
-      if (!unit_plain(p, w.s, base)) {
-        const int nv = w.s.ctx + w.s.n - base;  // keys of the unit that exist
-        uint8_t *vt = sKV + st * C::STAGE + C::KV_TILE;
-        unsigned long long found = 0;
-#pragma unroll 4
-        for (int e = lane; e < C::KV_TILE / 16; e += 32) {
-          const int key = (e >> 3) % kKeys;  // 16-byte pieces, eight of a row and atom
-          uint4 *at = reinterpret_cast<uint4 *>(vt + e * 16);
-          if (key >= nv) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 x = *at;
-          uint32_t *word = &x.x;
-          bool odd = false;
+    int st = 0;
+    uint32_t ph = 0;
+    for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+      for (int u = e.u0; u < e.u1; ++u) {
+        ok = mbar_wait_warp(&kv_full[st], ph, p.max_spin);
+        if (!ok) break;
+        const int base = unit_base(e.s, u);
+        if (!unit_plain(p, e.s, base)) {
+          const int nv = e.s.ctx + e.s.n - base;  // keys of the unit that exist
+          uint8_t *vt = sKV + st * C::STAGE + C::KV_TILE;
+          uint32_t found0 = 0, found1 = 0;
+          // 16-byte pieces, eight of a row and atom: a lane's are those of key lane / 8 and every fourth from it
+#pragma unroll 8
+          for (int k = 0; k < C::KV_TILE / 512; ++k) {
+            const int key = (4 * k + (lane >> 3)) % kKeys;
+            uint4 *at = reinterpret_cast<uint4 *>(vt + (k * 32 + lane) * 16);
+            const uint4 x = *at;
+            uint32_t word[4] = {x.x, x.y, x.z, x.w};
+            uint32_t odd = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const bool lo = (word[q] & 0x7F80u) == 0x7F80u, hi = (word[q] & 0x7F800000u) == 0x7F800000u;
-            word[q] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
-            odd |= lo | hi;
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t lo = (word[q] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
+              const uint32_t hi = (word[q] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+              word[q] &= ~(lo | hi);
+              odd |= lo | hi;
+            }
+            if (key >= nv) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else if (odd) {
+              *at = make_uint4(word[0], word[1], word[2], word[3]);
+              (key < 32 ? found0 : found1) |= 1u << (key & 31);
+            }
           }
-          if (odd) {
-            *at = x;
-            found |= 1ull << key;
-          }
-        }
-        fence_proxy_async_smem();
-        const uint32_t f0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(found));
-        const uint32_t f1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(found >> 32));
-        if (lane == 0) {
-          poison[st] = static_cast<unsigned long long>(f1) << 32 | f0;
-          mbar_arrive(&clean[st]);
+          fence_proxy_async_smem();
+          const uint32_t f0 = __reduce_or_sync(0xffffffffu, found0), f1 = __reduce_or_sync(0xffffffffu, found1);
+          if (lane == 0) poison[st] = static_cast<unsigned long long>(f1) << 32 | f0;
         }
         __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&clean[st]);
+          mbar_arrive(&kv_empty[st]);
+        }
+        ring_next<ST>(st, ph);
       }
-      if (lane == 0) mbar_arrive(&kv_empty[st]);
     }
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   } else if ((warp & 3) < NQ) {
     // ---------------- softmax
+    constexpr int STRIDE = TWO ? 1 : 2;  // units between two of this half's
     const int half = warp >> 2;
     const int q = warp & 3;
     const int r = q * 32 + lane;
@@ -534,57 +563,53 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t o_mine = trow + C::O_COL + half * HD;
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-    float m_run = -FLT_MAX, l_run = 0.f;
-    unsigned long long line = 0;  // nodes this row sees
-    int lo = 0;                   // its first context row behind the sinks
-    bool have_line = false, real = false, warp_real = false;
-    uint32_t clean_phase = 0;
     bool ok = true;
-    int step = 0, first = 0, node = 0;
-    for (; w.left > 0 && ok; walk_next(w, p, seqs), step += C::TILES) {
-      const int st = w.stage % ST;
-      if (walk_first(w)) {
-        first = step;
-        m_run = -FLT_MAX;
-        l_run = 0.f;
-        have_line = false;
-        const int grp = w.pair % p.groups;
-        const int node0 = (grp * C::TILES + (TWO ? half : 0)) * p.npt;
-        node = node0 + jr;
-        real = r < R && node < w.s.n;
-        warp_real = __any_sync(0xffffffffu, real);
-      }
-      const int base = unit_base(w.s, w.unit);
-      const bool masked = !unit_plain(p, w.s, base);
-      const uint32_t cph = clean_phase >> st & 1;
-      if (masked) clean_phase ^= 1u << st;
-      const int mine = TWO ? step + half : step;  // this half's step of the unit
-      if (TWO || (step & 1) == half) {
-        const bool start = mine < first + 2;
-        const int pb = mine & 3;
-        ok = mbar_wait_warp(&s_full[half], (mine >> 1) & 1, p.max_spin);
+    int units = 0;  // of the segments before
+    for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+      const int node = (e.grp * C::TILES + (TWO ? half : 0)) * p.npt + jr;
+      const bool real = r < R && node < e.s.n;
+      const bool warp_real = __any_sync(0xffffffffu, real);
+      float m_run = -FLT_MAX, l_run = 0.f;
+      unsigned long long line = 0;  // nodes this row sees
+      int lo = 0;                   // its first context row behind the sinks
+      bool have_line = false;
+      const int u_first = TWO ? e.u0 : e.u0 + ((units ^ half) & 1);
+      int step = 0;
+#pragma unroll 1
+      for (int u = u_first; u < e.u1; u += STRIDE) {
+        const int stage = units + u - e.u0;
+        step = TWO ? 2 * stage + half : stage;
+        const bool start = u == u_first;
+        const int pb = step & 3;
+        const int base = unit_base(e.s, u);
+        ok = mbar_wait_warp(&s_full[half], (step >> 1) & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
         float sv[kKeys];
         if (warp_real) tmem_ld64(trow + C::S_COL + half * kKeys, sv);
         tc_fence_before();
-        mbar_arrive(&s_empty[half]);
+        warp_arrive(&s_empty[half], lane);
 
         unsigned long long bad = 0;
-        if (masked) {
+        if (!unit_plain(p, e.s, base)) {
           if (!have_line) {
             int depth = 0;
-            line = real ? line_of(p, w.s, w.pair / per, node, &depth) : 0;
-            lo = p.window > 0 ? w.s.ctx + depth - p.window + 1 : 0;
+            line = real ? line_of(p, e.s, e.i, node, &depth) : 0;
+            lo = p.window > 0 ? e.s.ctx + depth - p.window + 1 : 0;
             have_line = true;
           }
-          unsigned long long keep = low_bits(w.s.ctx - base);
+          unsigned long long keep = low_bits(e.s.ctx - base);
           if (p.window > 0) keep &= ~low_bits(lo - base) | low_bits(p.sinks - base);
-          const int sh = base - w.s.ctx;  // key k of the unit is node k + sh
+          const int sh = base - e.s.ctx;  // key k of the unit is node k + sh
           keep |= sh >= 64 || sh <= -64 ? 0ull : sh >= 0 ? line >> sh : line << -sh;
+          const uint32_t k0 = static_cast<uint32_t>(keep), k1 = static_cast<uint32_t>(keep >> 32);
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) sv[c] = keep >> c & 1 ? sv[c] : -INFINITY;
-          ok = mbar_wait_warp(&clean[st], cph, p.max_spin);
+          for (int c = 0; c < 32; ++c) {
+            sv[c] = k0 >> c & 1 ? sv[c] : -INFINITY;
+            sv[c + 32] = k1 >> c & 1 ? sv[c + 32] : -INFINITY;
+          }
+          const int st = stage % ST;
+          ok = mbar_wait_warp(&clean[st], (stage / ST) & 1, p.max_spin);
           if (!ok) break;
           bad = poison[st] & keep;
         }
@@ -601,7 +626,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
 #pragma unroll
           for (int a = 0; a < 8; ++a) m8[a] = fmaxf(m8[a], sv[a + 56]);
           const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-          need = real && (mx - m_run) * sl2 > kGrowLog2;
+          need = (mx - m_run) * sl2 > kGrowLog2;
           if (need) {
             alpha = ex2((m_run - mx) * sl2);
             m_run = mx;
@@ -614,7 +639,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         }
         if (!start && __any_sync(0xffffffffu, need)) {
           // O *= alpha once the half's product before is done
-          ok = mbar_wait_warp(&p_empty[(mine - 2) & 3], ((mine - 2) >> 2) & 1, p.max_spin);
+          ok = mbar_wait_warp(&p_empty[(step - 2) & 3], ((step - 2) >> 2) & 1, p.max_spin);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -626,105 +651,100 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
             tmem_st32(o_mine + cc * 32, ov);
           }
         }
-        ok = mine < 4 || mbar_wait_warp(&p_empty[pb], ((mine >> 2) - 1) & 1, p.max_spin);
+        ok = step < 4 || mbar_wait_warp(&p_empty[pb], ((step >> 2) - 1) & 1, p.max_spin);
         if (!ok) break;
         if (warp_real) {
-          uint32_t pk[kKeys / 2];
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          const float mb = m_run * sl2;
+          const float2 sc = make_float2(sl2, sl2), nm = make_float2(-m_run * sl2, -m_run * sl2);
+          float2 sum[2] = {make_float2(l_run, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 2) {
-            const float p0 = ex2(fmaf(sv[c], sl2, -mb));
-            const float p1 = ex2(fmaf(sv[c + 1], sl2, -mb));
-            ls[(c >> 1) & 3] += p0 + p1;
-            pk[c >> 1] = real ? pack_bf16x2(p0, p1) : 0u;
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float2 x = fma2(make_float2(sv[32 * cc + 2 * c], sv[32 * cc + 2 * c + 1]), sc, nm);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum[c & 1] = add2(sum[c & 1], x);
+              pk[c] = pack_bf16x2(x.x, x.y);
+            }
+            tmem_st16_raw(trow + C::P_COL + pb * 32 + cc * 16, pk);
           }
-          l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          tmem_st32_raw(trow + C::P_COL + pb * 32, pk);
+          l_run = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[pb]);
+        warp_arrive(&p_full[pb], lane);
       }
-      if (!walk_last(w)) continue;
+      if (!ok) break;
 
-      // ---------------- a segment's end
-      const int seg = w.seg;
-      const bool whole = w.seg_unit0 == 0 && w.unit == w.s.U - 1;
-      const int i = w.pair / per, g = w.pair % per / p.groups;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0);
-      float M, L, a0 = 1.f, a1 = 0.f;
-      bool has0 = true, has1 = false;
-      if (TWO) {
-        ok = mbar_wait_warp(&p_empty[mine & 3], (mine >> 2) & 1, p.max_spin);
-        if (!ok) break;
-        tc_fence_after();
-        M = m_run;
-        L = l_run;
-      } else {
-        // the halves' last steps of the segment, -1: none
-        const int e0 = (step & 1) == 0 ? step : step - 1, e1 = (step & 1) ? step : step - 1;
-        const int last0 = e0 >= first ? e0 : -1, last1 = e1 >= first ? e1 : -1;
-        if (half == 1) {
-          ok = seg == 0 || mbar_wait_warp(&o_free[0], (seg - 1) & 1, p.max_spin);  // half 0 read the one before
-          if (ok && last1 >= 0) ok = mbar_wait_warp(&p_empty[last1 & 3], (last1 >> 2) & 1, p.max_spin);
-          if (!ok) break;
-          ml1[r] = last1 >= 0 ? make_float2(m_run, l_run) : make_float2(-FLT_MAX, 0.f);
-          tc_fence_before();
-          mbar_arrive(ml_ready);
-          continue;
-        }
-        ok = last0 < 0 || mbar_wait_warp(&p_empty[last0 & 3], (last0 >> 2) & 1, p.max_spin);
-        if (ok) ok = mbar_wait_warp(ml_ready, seg & 1, p.max_spin);
-        if (!ok) break;
-        tc_fence_after();
-        const float2 o1 = ml1[r];
-        has0 = last0 >= 0;
-        has1 = last1 >= 0;
-        const float m0 = has0 ? m_run : -FLT_MAX;
-        M = fmaxf(m0, o1.x);
-        a0 = has0 ? ex2((m0 - M) * sl2) : 0.f;
-        a1 = has1 ? ex2((o1.x - M) * sl2) : 0.f;
-        L = (has0 ? l_run * a0 : 0.f) + (has1 ? o1.y * a1 : 0.f);
+      // ---------------- the segment's end
+      const bool whole = e.u0 == 0 && e.u1 == e.s.U;
+      const bool mine = u_first < e.u1;  // this half had units of it, the last one at `step`
+      units += e.u1 - e.u0;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (e.index > 0);
+      float M = m_run, L = l_run, a0 = 1.f, a1 = 0.f;
+      bool has1 = false;
+      if (!TWO && half == 1) ok = e.index == 0 || mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);
+      if (ok && mine) ok = mbar_wait_warp(&p_empty[step & 3], (step >> 2) & 1, p.max_spin);
+      if (!ok) break;
+      if (!TWO && half == 1) {  // half 0 joins the two; it has read the segment before
+        ml1[r] = mine ? make_float2(m_run, l_run) : make_float2(-FLT_MAX, -1.f);
+        tc_fence_before();
+        warp_arrive(ml_ready, lane);
+        continue;
       }
+      if (!TWO) {
+        ok = mbar_wait_warp(ml_ready, e.index & 1, p.max_spin);
+        if (!ok) break;
+        const float2 o1 = ml1[r];
+        has1 = o1.y >= 0.f || o1.y != o1.y;
+        M = fmaxf(m_run, o1.x);
+        a0 = mine ? ex2((m_run - M) * sl2) : 0.f;
+        a1 = has1 ? ex2((o1.x - M) * sl2) : 0.f;
+        L = (mine ? l_run * a0 : 0.f) + (has1 ? o1.y * a1 : 0.f);
+      }
+      tc_fence_after();
       if (warp_real) {
+        const bool any1 = __any_sync(0xffffffffu, has1);
         const float inv = 1.0f / L;
         const int prow = slot * p.part_rows + (TWO ? half * kTileRows : 0) + r;
 #pragma unroll 1
-        for (int cc = 0; cc < HD / 32; ++cc) {
-          float ov[32];
+        for (int cc = 0; cc < HD / 16; ++cc) {
+          float ov[16];
           if (TWO) {
-            tmem_ld32(o_mine + cc * 32, ov);
+            tmem_ld16(o_mine + cc * 16, ov);
           } else {
-            float o1v[32];
-            if (has0) tmem_ld32(trow + C::O_COL + cc * 32, ov);
-            if (has1) tmem_ld32(trow + C::O_COL + HD + cc * 32, o1v);
+            float o1v[16];
+            if (any1)
+              tmem_ld16_two(trow + C::O_COL + cc * 16, ov, trow + C::O_COL + HD + cc * 16, o1v);
+            else
+              tmem_ld16(trow + C::O_COL + cc * 16, ov);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1v[c] * a1 : 0.f);
+            for (int c = 0; c < 16; ++c) ov[c] = (mine ? ov[c] * a0 : 0.f) + (has1 ? o1v[c] * a1 : 0.f);
           }
           if (!real) continue;
           if (whole) {
-            uint16_t *dst = p.o + (((long long)i * p.m + node) * p.Hq + g * G + hq) * HD + cc * 32;
+            uint16_t *dst = p.o + (((long long)e.i * p.m + node) * p.Hq + e.g * G + hq) * HD + cc * 16;
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
+            for (int v = 0; v < 2; ++v)
               reinterpret_cast<uint4 *>(dst)[v] =
                   make_uint4(pack_bf16x2(ov[8 * v] * inv, ov[8 * v + 1] * inv),
                              pack_bf16x2(ov[8 * v + 2] * inv, ov[8 * v + 3] * inv),
                              pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
                              pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
           } else {
-            float *dst = p.part_o + (long long)prow * HD + cc * 32;
+            float *dst = p.part_o + (long long)prow * HD + cc * 16;
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
+            for (int v = 0; v < 4; ++v)
               reinterpret_cast<float4 *>(dst)[v] = make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
           }
         }
         if (real && !whole) *reinterpret_cast<float2 *>(p.part_ml + (long long)prow * 2) = make_float2(M, L);
       }
       tc_fence_before();
-      mbar_arrive(&o_free[TWO ? half : 0]);
+      warp_arrive(&o_free[TWO ? half : 0], lane);
     }
-    if (!ok) flag_status(p.status, kStatusTimeout);
+    if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   }
 
   tc_fence_before();
