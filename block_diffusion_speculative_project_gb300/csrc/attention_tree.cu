@@ -26,8 +26,8 @@
 // such a key get a NaN probability for it.
 //
 // One CTA: TMA producer (Q tiles of the segment; K and V of a unit per stage), S issuer (S = Q K^T into
-// buffer step % 2), PV issuer (O_half += P V, P from tensor memory, buffer step % 4), the cleaner, and
-// the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32,
+// buffer step % 2, the first tile's Q from tensor memory), PV issuer (O_half += P V, P from tensor memory),
+// the cleaner, and the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32,
 // rounds P to bf16 (2^-9 of each probability, as the values have) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
 #include <cfloat>
@@ -53,7 +53,6 @@ struct Roles {
   static constexpr int PV = NQ == 4 ? 10 : NQ == 2 ? 6 : 3;
   static constexpr int CLEAN = NQ == 4 ? 11 : NQ == 2 ? 7 : 5;
   static constexpr int THREADS = NQ == 4 ? 384 : NQ == 2 ? 256 : 192;
-  static constexpr int HALF = NQ * 32;
 };
 
 template <int HD, bool TWO>
@@ -73,7 +72,9 @@ struct Cfg {
   static constexpr size_t SMEM = 1024 + OFF_ML + kTileRows * 8;
   static constexpr uint32_t S_COL = 0;             // two S buffers of 64 columns
   static constexpr uint32_t O_COL = 128;           // O of the two halves
-  static constexpr uint32_t P_COL = 128 + 2 * HD;  // four P buffers of 32 columns
+  static constexpr uint32_t P_COL = 128 + 2 * HD;  // P of the two halves, 32 columns each
+  static constexpr uint32_t Q_COL = P_COL + 64;    // the (first) Q tile: hd / 2 columns
+  static_assert(Q_COL + HD / 2 <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -268,7 +269,6 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   using C = Cfg<HD, TWO>;
   using Ro = Roles<NQ>;
   constexpr int ST = C::STAGES;
-  constexpr int HT = Ro::HALF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -279,11 +279,12 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   uint64_t *clean = kv_empty + ST;      // looked through by the cleaner
   uint64_t *s_full = clean + ST;        // [2]
   uint64_t *s_empty = s_full + 2;       // [2]
-  uint64_t *p_full = s_empty + 2;       // [4]: P of step j in buffer j % 4
-  uint64_t *p_empty = p_full + 4;       // [4]: its product done
-  uint64_t *q_full = p_empty + 4;
-  uint64_t *q_empty = q_full + 1;
-  uint64_t *o_free = q_empty + 1;       // [2]: O read at a segment's end (one tile: both by half 0)
+  uint64_t *p_full = s_empty + 2;       // [2]
+  uint64_t *p_empty = p_full + 2;       // [2]: the product done
+  uint64_t *q_full = p_empty + 2;       // Q landed in shared memory
+  uint64_t *q_ready = q_full + 1;       // the first tile copied to tensor memory
+  uint64_t *q_free = q_ready + 1;       // every S of the segment done
+  uint64_t *o_free = q_free + 1;        // [2]: O read at a segment's end (one tile: both by half 0)
   uint64_t *ml_ready = o_free + 2;      // one tile: half 1's maximum and sum written
   uint64_t *mma_done = ml_ready + 1;    // [2]
   uint64_t *poison = mma_done + 2;      // [ST] keys of the stage whose values were not finite
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // pair, unit, count
   int2 *seqs = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
   float2 *ml1 = reinterpret_cast<float2 *>(smem + C::OFF_ML);
-  static_assert((4 * ST + 2 + 2 + 4 + 4 + 2 + 2 + 1 + 2) * 8 + 16 <= 512, "barrier region");
+  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 1 + 2) * 8 + 16 <= 512, "barrier region");
   static_assert(kSeqCache * 8 <= 512, "lengths");
 
   const int warp = threadIdx.x >> 5;
@@ -310,13 +311,12 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       mbar_init(&s_empty[b], NQ);
       mbar_init(&o_free[b], NQ);
       mbar_init(&mma_done[b], 1);
-    }
-    for (int b = 0; b < 4; ++b) {
       mbar_init(&p_full[b], NQ);
       mbar_init(&p_empty[b], 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_ready, NQ);
+    mbar_init(q_free, 1);
     mbar_init(ml_ready, NQ);
     fence_mbar_init();
   }
@@ -328,13 +328,6 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   if (warp == Ro::S) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
-  }
-  if (warp < NQ) {
-    // rows that no copy fills stay zero
-    for (int a = 0; a < C::TILES * C::ATOMS; ++a)
-      for (int e = R * 8 + static_cast<int>(threadIdx.x); e < kTileRows * 8; e += HT)
-        *reinterpret_cast<uint4 *>(sQ + a * C::ATOM_Q + e * 16) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
   }
   griddep_wait();  // the lengths may come from the launch before
   if (threadIdx.x == 0) griddep_launch();
@@ -389,7 +382,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       int q_loads = 0, loads = 0, st = 0;
       uint32_t ph = 0;
       for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
-        if (e.index > 0 && !mbar_wait(q_empty, (e.index - 1) & 1, p.max_spin)) {
+        // the place is free when the one tile is in tensor memory; the second is read where it lies
+        if (e.index > 0 && !mbar_wait(TWO ? q_free : q_ready, (e.index - 1) & 1, p.max_spin)) {
           ok = false;
           break;
         }
@@ -441,7 +435,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       int step = 0, st = 0;
       uint32_t ph = 0;
       for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
-        ok = mbar_wait(q_full, e.index & 1, p.max_spin);
+        ok = mbar_wait(q_ready, e.index & 1, p.max_spin);
+        if (TWO && ok) ok = mbar_wait(q_full, e.index & 1, p.max_spin);
         for (int u = e.u0; u < e.u1 && ok; ++u) {
           ok = mbar_wait(&kv_full[st], ph, p.max_spin);
           const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
@@ -451,19 +446,27 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
             if (ok && step >= 2) ok = mbar_wait(&s_empty[sb], ((step >> 1) - 1) & 1, p.max_spin);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t qd = q_desc0 + static_cast<uint64_t>((h * C::Q_TILE) >> 4);
             const uint32_t d_s = tmem_base + C::S_COL + sb * kKeys;
+            if (h == 0) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-              tc_mma_bf16(d_s, qd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_Q + (kk & 3) * 32) >> 4),
-                          kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
-                          kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < HD / 16; ++kk)
+                tc_mma_bf16_tmem_a(d_s, tmem_base + C::Q_COL + kk * 8,
+                                   kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
+                                   kk > 0 ? 1u : 0u);
+            } else {
+              const uint64_t qd = q_desc0 + static_cast<uint64_t>(C::Q_TILE >> 4);
+#pragma unroll
+              for (int kk = 0; kk < HD / 16; ++kk)
+                tc_mma_bf16(d_s, qd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_Q + (kk & 3) * 32) >> 4),
+                            kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
+                            kk > 0 ? 1u : 0u);
+            }
             tc_commit(&s_full[sb]);
             ++step;
           }
           ring_next<ST>(st, ph);
         }
-        if (ok) tc_commit(q_empty);
+        if (ok) tc_commit(q_free);
       }
       if (!ok) flag_status(p.status, kStatusTimeout);
       tc_commit(&mma_done[0]);  // every product completes before tensor memory is freed
@@ -482,19 +485,19 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
           const uint64_t vd = v_desc0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
 #pragma unroll
           for (int h = 0; h < C::TILES; ++h) {
-            const int half = step & 1, pb = step & 3;
+            const int half = step & 1;
             const bool start = step < first + 2;  // the half's first unit of the segment
-            ok = mbar_wait(&p_full[pb], (step >> 2) & 1, p.max_spin);
+            ok = mbar_wait(&p_full[half], (step >> 1) & 1, p.max_spin);
             if (ok && start && e.index > 0) ok = mbar_wait(&o_free[TWO ? half : 0], (e.index - 1) & 1, p.max_spin);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d_o = tmem_base + C::O_COL + half * HD;
-            const uint32_t a_p = tmem_base + C::P_COL + pb * 32;
+            const uint32_t a_p = tmem_base + C::P_COL + half * 32;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
               tc_mma_bf16_tmem_a(d_o, a_p + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
                                  (!start || kk > 0) ? 1u : 0u);
-            tc_commit(&p_empty[pb]);
+            tc_commit(&p_empty[half]);
             ++step;
           }
           if (ok) tc_commit(&kv_empty[st]);
@@ -563,9 +566,35 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t o_mine = trow + C::O_COL + half * HD;
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
+    // The first Q tile of a segment to tensor memory, where the products read it at full rate (from shared
+    // memory an S of 64 keys takes twice as long): by half 1, or with two tiles by half 0, whose rows they are.
+    const bool copies = half == (TWO ? 0 : 1);
+    auto copy_q = [&](int index) {
+      bool good = index == 0 || mbar_wait_warp(q_free, (index - 1) & 1, p.max_spin);
+      if (good) good = mbar_wait_warp(q_full, index & 1, p.max_spin);
+      if (!good) return false;
+      tc_fence_after();
+#pragma unroll 1
+      for (int a = 0; a < HD / 32; ++a) {
+        uint32_t v[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(sQ + (a >> 1) * C::ATOM_Q + r * 128 +
+                                                           ((((a & 1) * 4 + c) ^ (r & 7)) << 4));
+          v[4 * c] = x.x, v[4 * c + 1] = x.y, v[4 * c + 2] = x.z, v[4 * c + 3] = x.w;
+        }
+        tmem_st16_raw(trow + C::Q_COL + a * 16, v);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(q_ready, lane);
+      return true;
+    };
     bool ok = true;
+    if (copies && e.left > 0) ok = copy_q(0);
     int units = 0;  // of the segments before
     for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+      const bool more = e.left > e.u1 - e.u0;  // a segment follows
       const int node = (e.grp * C::TILES + (TWO ? half : 0)) * p.npt + jr;
       const bool real = r < R && node < e.s.n;
       const bool warp_real = __any_sync(0xffffffffu, real);
@@ -580,7 +609,6 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         const int stage = units + u - e.u0;
         step = TWO ? 2 * stage + half : stage;
         const bool start = u == u_first;
-        const int pb = step & 3;
         const int base = unit_base(e.s, u);
         ok = mbar_wait_warp(&s_full[half], (step >> 1) & 1, p.max_spin);
         if (!ok) break;
@@ -637,10 +665,10 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
             for (int c = 0; c < kKeys; ++c) sv[c] = bad >> c & 1 ? __int_as_float(0x7fffffff) : sv[c];
           }
         }
+        // P's place is free, and O at rest, once the half's product before is done
+        ok = step < 2 || mbar_wait_warp(&p_empty[half], ((step >> 1) - 1) & 1, p.max_spin);
+        if (!ok) break;
         if (!start && __any_sync(0xffffffffu, need)) {
-          // O *= alpha once the half's product before is done
-          ok = mbar_wait_warp(&p_empty[(step - 2) & 3], ((step - 2) >> 2) & 1, p.max_spin);
-          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
@@ -651,8 +679,6 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
             tmem_st32(o_mine + cc * 32, ov);
           }
         }
-        ok = step < 4 || mbar_wait_warp(&p_empty[pb], ((step >> 2) - 1) & 1, p.max_spin);
-        if (!ok) break;
         if (warp_real) {
           const float2 sc = make_float2(sl2, sl2), nm = make_float2(-m_run * sl2, -m_run * sl2);
           float2 sum[2] = {make_float2(l_run, 0.f), make_float2(0.f, 0.f)};
@@ -667,13 +693,13 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
               sum[c & 1] = add2(sum[c & 1], x);
               pk[c] = pack_bf16x2(x.x, x.y);
             }
-            tmem_st16_raw(trow + C::P_COL + pb * 32 + cc * 16, pk);
+            tmem_st16_raw(trow + C::P_COL + half * 32 + cc * 16, pk);
           }
           l_run = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
         }
         tc_fence_before();
-        warp_arrive(&p_full[pb], lane);
+        warp_arrive(&p_full[half], lane);
       }
       if (!ok) break;
 
@@ -684,8 +710,9 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       const int slot = 2 * static_cast<int>(blockIdx.x) + (e.index > 0);
       float M = m_run, L = l_run, a0 = 1.f, a1 = 0.f;
       bool has1 = false;
-      if (!TWO && half == 1) ok = e.index == 0 || mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);
-      if (ok && mine) ok = mbar_wait_warp(&p_empty[step & 3], (step >> 2) & 1, p.max_spin);
+      if (!TWO && half == 1 && more) ok = copy_q(e.index + 1);
+      if (ok && !TWO && half == 1) ok = e.index == 0 || mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);
+      if (ok && mine) ok = mbar_wait_warp(&p_empty[half], (step >> 1) & 1, p.max_spin);
       if (!ok) break;
       if (!TWO && half == 1) {  // half 0 joins the two; it has read the segment before
         ml1[r] = mine ? make_float2(m_run, l_run) : make_float2(-FLT_MAX, -1.f);
@@ -743,6 +770,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       }
       tc_fence_before();
       warp_arrive(&o_free[TWO ? half : 0], lane);
+      if (TWO && copies && more) ok = copy_q(e.index + 1);
     }
     if (!ok && lane == 0) flag_status(p.status, kStatusTimeout);
   }
