@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
   static constexpr int OFF_SEQ = OFF_BAR + 512;
   static constexpr int OFF_ML = OFF_SEQ + 512;
-  static constexpr size_t SMEM = 1024 + OFF_ML + kTileRows * 8;
+  static constexpr size_t SMEM = OFF_ML + 2 * kTileRows * 8;
   static constexpr uint32_t S_COL = 0;             // two S buffers of 64 columns
   static constexpr uint32_t O_COL = 128;           // O of the two halves
   static constexpr uint32_t P_COL = 128 + 2 * HD;  // P of the two halves, 32 columns each
@@ -106,54 +106,11 @@ __device__ __forceinline__ Span make_span(const AttnTreeParams &p, int ctx, int 
   s.U = n > 0 ? s.A + (L + kKeys - 1) / kKeys - s.W0 : 0;
   return s;
 }
-__device__ __forceinline__ int units_of(const AttnTreeParams &p, int i) {
-  const int n = clamp_nodes(p, i);
-  return make_span(p, clamp_ctx(p, i, n), n).U;
-}
 __device__ __forceinline__ int unit_base(const Span &s, int u) { return (u < s.A ? u : u - s.A + s.W0) * kKeys; }
 // Whether every row sees all of the unit's keys.
 __device__ __forceinline__ bool unit_plain(const AttnTreeParams &p, const Span &s, int base) {
   return base + kKeys <= s.ctx &&
          (p.window <= 0 || base >= s.ctx + s.n - p.window || base + kKeys <= p.sinks);
-}
-
-// First unit of CTA c's range, T units over G CTAs; and the CTA that has unit u.
-__device__ __forceinline__ long long range_start(long long T, int G, int c) { return (long long)c * T / G; }
-__device__ __forceinline__ int range_of(long long T, int G, long long u) {
-  return static_cast<int>(((u + 1) * G + T - 1) / T - 1);
-}
-
-// Warp-collective: units of all pairs.
-__device__ long long all_units(const AttnTreeParams &p, int lane) {
-  long long s = 0;
-  for (int i = lane; i < p.nb; i += 32) s += units_of(p, i);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s * (p.Hkv * p.groups);
-}
-
-// Warp-collective: the sequence that has unit u0 of all, and the units before it; -1: none.
-__device__ int find_sequence(const AttnTreeParams &p, long long u0, int lane, long long *before) {
-  const int per = p.Hkv * p.groups;
-  long long base = 0;
-  for (int b = 0; b < p.nb; b += 32) {
-    const int i = b + lane;
-    const long long own = i < p.nb ? (long long)per * units_of(p, i) : 0;
-    long long v = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, i < p.nb && base + v > u0);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      *before = base + __shfl_sync(0xffffffffu, v - own, l);
-      return b + l;
-    }
-    base += __shfl_sync(0xffffffffu, v, 31);
-  }
-  return -1;
 }
 
 constexpr int kSeqCache = 64;  // sequences whose lengths a CTA keeps in shared memory
@@ -169,29 +126,92 @@ __device__ __forceinline__ Span span_of(const AttnTreeParams &p, const int2 *seq
   return make_span(p, v.x, v.y);
 }
 
+// All units of a call over its CTAs: CTA c has q or (the first r CTAs) q + 1 of them in a row. Their number
+// stays below 2^31: pairs of fewer than 2^31 cache rows, in up to 16 groups.
+struct Split {
+  int T, ctas, q, r;
+};
+__device__ __forceinline__ int range_start(const Split &s, int c) { return c * s.q + min(c, s.r); }
+__device__ __forceinline__ int range_of(const Split &s, int u) {  // the CTA that has unit u
+  const int first = s.r * (s.q + 1);
+  return u < first ? u / (s.q + 1) : s.r + (u - first) / s.q;
+}
+
+// Where a unit of all units is: sequence i (-1: nowhere), kv head g, group grp, `unit` of a pair of U.
+struct Place {
+  int i, g, grp, unit, U;
+};
+
+// Warp-collective: the lengths of the first sequences to `seqs` (if not null), and the split.
+__device__ __forceinline__ Split make_split(const AttnTreeParams &p, int2 *seqs, int lane) {
+  int sum = 0;
+  for (int i = lane; i < p.nb; i += 32) {
+    const int n = clamp_nodes(p, i), ctx = clamp_ctx(p, i, n);
+    if (seqs && i < kSeqCache) seqs[i] = make_int2(ctx, n);
+    sum += make_span(p, ctx, n).U;
+  }
+  Split s;
+  s.T = __reduce_add_sync(0xffffffffu, sum) * (p.Hkv * p.groups);
+  s.ctas = max(1, min(s.T, p.grid));
+  s.q = s.T / s.ctas;
+  s.r = s.T - s.q * s.ctas;
+  return s;
+}
+
+// Warp-collective: the place of unit u, 0 <= u < T.
+__device__ __forceinline__ Place find_unit(const AttnTreeParams &p, int u, int lane) {
+  const int per = p.Hkv * p.groups;
+  Place f = {-1, 0, 0, 0, 1};
+  int base = 0;
+  for (int b = 0; b < p.nb; b += 32) {
+    const int i = b + lane;
+    int U = 0;
+    if (i < p.nb) {
+      const int n = clamp_nodes(p, i);
+      U = make_span(p, clamp_ctx(p, i, n), n).U;
+    }
+    int v = U * per;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, i < p.nb && base + v > u);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      f.i = b + l;
+      f.U = __shfl_sync(0xffffffffu, U, l);
+      const int off = u - base - (__shfl_sync(0xffffffffu, v, l) - f.U * per);
+      const int k = off / f.U;
+      f.unit = off - k * f.U;
+      f.g = k / p.groups;
+      f.grp = k - f.g * p.groups;
+      return f;
+    }
+    base += __shfl_sync(0xffffffffu, v, 31);
+  }
+  return f;
+}
+
 // A run of one pair's units [u0, u1) in this CTA's range: sequence i, kv head g, group grp of tiles. All
 // roles go through the same segments; `left` units of the range are not behind it.
 struct Seg {
-  int pair, i, g, grp, u0, u1, index, left;
+  int i, g, grp, u0, u1, index, left;
   Span s;
 };
-__device__ __forceinline__ void seg_place(Seg &e, const AttnTreeParams &p) {
-  const int per = p.Hkv * p.groups, k = e.pair - e.i * per;
-  e.g = k / p.groups;
-  e.grp = k - e.g * p.groups;
-  e.u1 = min(e.s.U, e.u0 + e.left);
-}
+// sched: sequence, kv head, group, unit, units of the range
 __device__ __forceinline__ Seg seg_begin(const AttnTreeParams &p, const int2 *seqs, const int *sched) {
   Seg e;
-  e.pair = sched[0];
-  e.u0 = sched[1];
-  e.left = sched[2];
+  e.i = sched[0];
+  e.g = sched[1];
+  e.grp = sched[2];
+  e.u0 = sched[3];
+  e.left = sched[4];
   e.index = 0;
-  e.i = 0;
+  e.u1 = e.u0;
   if (e.left > 0) {
-    e.i = e.pair / (p.Hkv * p.groups);
     e.s = span_of(p, seqs, e.i);
-    seg_place(e, p);
+    e.u1 = min(e.s.U, e.u0 + e.left);
   }
   return e;
 }
@@ -199,16 +219,17 @@ __device__ __forceinline__ void seg_next(Seg &e, const AttnTreeParams &p, const 
   e.left -= e.u1 - e.u0;
   if (e.left <= 0) return;
   ++e.index;
-  ++e.pair;
   e.u0 = 0;
-  const int per = p.Hkv * p.groups;
-  if (e.pair == (e.i + 1) * per) {
-    do {  // sequences without rows have no units
-      e.s = span_of(p, seqs, ++e.i);
-      e.pair = e.i * per;
-    } while (e.s.U == 0 && e.i + 1 < p.nb);
+  if (++e.grp == p.groups) {
+    e.grp = 0;
+    if (++e.g == p.Hkv) {
+      e.g = 0;
+      do {  // sequences without rows have no units
+        e.s = span_of(p, seqs, ++e.i);
+      } while (e.s.U == 0 && e.i + 1 < p.nb);
+    }
   }
-  seg_place(e, p);
+  e.u1 = min(e.s.U, e.left);
 }
 
 // A ring's next stage: its place, and the parity of its barriers.
@@ -230,38 +251,99 @@ __device__ __forceinline__ unsigned long long low_bits(int k) {
   return k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
 }
 
-// The nodes that node j sees, itself among them, and its depth.
-__device__ __forceinline__ unsigned long long line_of(const AttnTreeParams &p, const Span &s, int i, int j, int *depth) {
-  unsigned long long seen = 0;
+// Warp-collective: the nodes that this lane's node j sees, itself among them, and its depth (j < 0: none). up0 and
+// up1 of lane k are the parents of nodes k and k + 32.
+__device__ __forceinline__ unsigned long long line_of(const AttnTreeParams &p, const Span &s, int j, int up0, int up1,
+                                                      int *depth) {
   if (p.parent == nullptr) {
-    *depth = j;
-    seen = low_bits(j + 1);
+    *depth = max(j, 0);
+    unsigned long long seen = low_bits(j + 1);
     if (p.window > 0) seen &= ~low_bits(j + 1 - p.window) | low_bits(p.sinks - s.ctx);
     return seen;
   }
-  const int *parent = p.parent + (long long)i * p.m;
-  int d = 0;
-  bool bad = false;
-  for (int a = j;; ++d) {  // parents lie below their nodes
-    if (p.window <= 0 || d < p.window) seen |= 1ull << a;
-    const int up = parent[a];
-    if (a == 0 || up < 0 || up >= a) {
-      bad = a == 0 ? up != -1 : true;
-      break;
+  unsigned long long seen = 0;
+  int a = max(j, 0), d = 0;
+  bool on = j >= 0, bad = false;
+  while (__any_sync(0xffffffffu, on)) {  // parents lie below their nodes
+    if (on && (p.window <= 0 || d < p.window)) seen |= 1ull << a;
+    const int x = __shfl_sync(0xffffffffu, up0, a & 31), y = __shfl_sync(0xffffffffu, up1, a & 31);
+    const int up = a < 32 ? x : y;
+    const bool top = a == 0 || up < 0 || up >= a;
+    bad |= on && top && (a != 0 || up != -1);
+    on &= !top;
+    if (on) {
+      a = up;
+      ++d;
     }
-    a = up;
   }
   *depth = d;
   if (p.window > 0 && p.sinks > s.ctx) {  // nodes among the first rows
-    int a = j;
-    for (int e = d;; --e) {
-      if (s.ctx + e < p.sinks) seen |= 1ull << a;
-      if (e == 0) break;
-      a = parent[a];
+    a = max(j, 0);
+    int e = d;
+    on = j >= 0;
+    while (__any_sync(0xffffffffu, on)) {
+      if (on && s.ctx + e < p.sinks) seen |= 1ull << a;
+      const int x = __shfl_sync(0xffffffffu, up0, a & 31), y = __shfl_sync(0xffffffffu, up1, a & 31);
+      on &= e-- > 0;
+      if (on) a = a < 32 ? x : y;
     }
   }
   if (bad) flag_status(p.status, kStatusCheck);
   return seen;
+}
+
+// The larger magnitude of each of two bf16 values, NaN if one is.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Warp-collective: zeroes a unit's values (ATOMS pieces of 64 rows of 128 bytes side by side) that are not finite, and its
+// rows from nv on; returns the keys that had such values. One look at the magnitudes first: they hardly ever have.
+template <int ATOMS>
+__device__ __forceinline__ unsigned long long clean_values(uint8_t *v, int nv, int lane) {
+  constexpr int PIECE = kKeys * 128;
+  if (nv < kKeys) {
+#pragma unroll
+    for (int a = 0; a < ATOMS; ++a)
+      for (int k = max(nv, 0) * 8 + lane; k < kKeys * 8; k += 32)
+        *reinterpret_cast<uint4 *>(v + a * PIECE + k * 16) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  uint32_t m = 0;
+#pragma unroll 8
+  for (int k = 0; k < 16 * ATOMS; ++k) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(v + (k * 32 + lane) * 16);
+    m = max_abs2(max_abs2(m, x.x), max_abs2(max_abs2(x.y, x.z), x.w));
+  }
+  unsigned long long found = 0;
+  if (__any_sync(0xffffffffu, (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u)) {
+    uint32_t found0 = 0, found1 = 0;
+    // 16-byte pieces, eight of a row: a lane's are those of row lane / 8 and every fourth from it
+    for (int k = 0; k < 16 * ATOMS; ++k) {
+      const int key = (4 * k + (lane >> 3)) % kKeys;
+      uint4 *at = reinterpret_cast<uint4 *>(v + (k * 32 + lane) * 16);
+      const uint4 x = *at;
+      uint32_t word[4] = {x.x, x.y, x.z, x.w};
+      uint32_t odd = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = (word[q] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
+        const uint32_t hi = (word[q] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+        word[q] &= ~(lo | hi);
+        odd |= lo | hi;
+      }
+      if (odd) {
+        *at = make_uint4(word[0], word[1], word[2], word[3]);
+        (key < 32 ? found0 : found1) |= 1u << (key & 31);
+      }
+    }
+    found = static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, found1)) << 32 |
+            __reduce_or_sync(0xffffffffu, found0);
+  }
+  fence_proxy_async_smem();
+  return found;
 }
 
 template <int HD, int NQ, bool TWO>
@@ -269,9 +351,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   using C = Cfg<HD, TWO>;
   using Ro = Roles<NQ>;
   constexpr int ST = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem;
   uint8_t *sKV = smem + C::OFF_KV;
   uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -284,15 +364,15 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   uint64_t *q_full = p_empty + 2;       // Q landed in shared memory
   uint64_t *q_ready = q_full + 1;       // the first tile copied to tensor memory
   uint64_t *q_free = q_ready + 1;       // every S of the segment done
-  uint64_t *o_free = q_free + 1;        // [2]: O read at a segment's end (one tile: both by half 0)
-  uint64_t *ml_ready = o_free + 2;      // one tile: half 1's maximum and sum written
-  uint64_t *mma_done = ml_ready + 1;    // [2]
+  uint64_t *o_free = q_free + 1;        // [2]: O read at a segment's end (one tile: both, as [0])
+  uint64_t *ml_ready = o_free + 2;      // [2], one tile: the half's maximum and sum written, its O done
+  uint64_t *mma_done = ml_ready + 2;    // [2]
   uint64_t *poison = mma_done + 2;      // [ST] keys of the stage whose values were not finite
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + ST);
-  int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // pair, unit, count
+  int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // [5]
   int2 *seqs = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
-  float2 *ml1 = reinterpret_cast<float2 *>(smem + C::OFF_ML);
-  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 1 + 2) * 8 + 16 <= 512, "barrier region");
+  float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);  // [2][128] a half's maximum and sum
+  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 2 + 2) * 8 + 24 <= 512, "barrier region");
   static_assert(kSeqCache * 8 <= 512, "lengths");
 
   const int warp = threadIdx.x >> 5;
@@ -309,7 +389,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
       mbar_init(&s_empty[b], NQ);
-      mbar_init(&o_free[b], NQ);
+      mbar_init(&o_free[b], TWO ? NQ : 2 * NQ);
+      mbar_init(&ml_ready[b], NQ);
       mbar_init(&mma_done[b], 1);
       mbar_init(&p_full[b], NQ);
       mbar_init(&p_empty[b], 1);
@@ -317,8 +398,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     mbar_init(q_full, 1);
     mbar_init(q_ready, NQ);
     mbar_init(q_free, 1);
-    mbar_init(ml_ready, NQ);
     fence_mbar_init();
+    if (smem_u32(smem) & 1023) flag_status(p.status, kStatusTimeout);  // never: the swizzled tiles' alignment
   }
   if (warp == Ro::PRODUCER && lane == 0) {
     tma_prefetch_desc(&p.tmQ);
@@ -332,31 +413,20 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   griddep_wait();  // the lengths may come from the launch before
   if (threadIdx.x == 0) griddep_launch();
   if (warp == Ro::PRODUCER) {
-    for (int i = lane; i < p.nb && i < kSeqCache; i += 32) {
-      const int n = clamp_nodes(p, i);
-      seqs[i] = make_int2(clamp_ctx(p, i, n), n);
-    }
-    const long long T = all_units(p, lane);
-    const int Ge = T < p.grid ? static_cast<int>(T) : p.grid;
-    int count = 0, pair0 = 0, unit0 = 0;
-    if (static_cast<int>(blockIdx.x) < Ge) {
-      const long long u0 = range_start(T, Ge, blockIdx.x);
-      count = static_cast<int>(range_start(T, Ge, blockIdx.x + 1) - u0);
-      long long before = 0;
-      const int i = find_sequence(p, u0, lane, &before);
-      if (i < 0) {
-        count = 0;
-      } else {
-        const int U = units_of(p, i);
-        const int off = static_cast<int>(u0 - before);
-        pair0 = i * p.Hkv * p.groups + off / U;
-        unit0 = off % U;
-      }
+    const Split sp = make_split(p, seqs, lane);
+    Place at = {0, 0, 0, 0, 1};
+    int count = 0;
+    if (static_cast<int>(blockIdx.x) < sp.ctas && sp.T > 0) {
+      const int u0 = range_start(sp, blockIdx.x);
+      at = find_unit(p, u0, lane);
+      count = at.i < 0 ? 0 : range_start(sp, blockIdx.x + 1) - u0;
     }
     if (lane == 0) {
-      sched[0] = pair0;
-      sched[1] = unit0;
-      sched[2] = count;
+      sched[0] = at.i;
+      sched[1] = at.g;
+      sched[2] = at.grp;
+      sched[3] = at.unit;
+      sched[4] = count;
     }
   }
   if (warp == Ro::CLEAN && blockIdx.x == 0) {
@@ -373,29 +443,34 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   const uint32_t tmem_base = *tmem_slot;
   Seg e = seg_begin(p, seqs, sched);
 
+  auto load_q = [&](const Seg &s) {
+    const uint64_t pol_q = policy_evict_last();
+    const int node0 = s.grp * C::TILES * p.npt;
+    const int tiles = TWO && node0 + p.npt < p.m ? 2 : 1;  // a last group may have one tile
+    mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * C::ATOMS * R * 128));
+    for (int h = 0; h < tiles; ++h)
+#pragma unroll
+      for (int a = 0; a < C::ATOMS; ++a)
+        tma_load_3d(sQ + h * C::Q_TILE + a * C::ATOM_Q, &p.tmQ, q_full, a * 64, s.g * G, s.i * p.m + node0 + h * p.npt,
+                    pol_q);
+  };
   if (warp == Ro::PRODUCER) {
     if (lane == 0 && e.left > 0 && !p.stall) {
       // K and V of one pair are read by its groups of tiles one after another
       const uint64_t pol_kv = p.groups > 1 ? policy_evict_last() : policy_evict_first();
-      const uint64_t pol_q = policy_evict_last();
       bool ok = true;
-      int q_loads = 0, loads = 0, st = 0;
+      int q_loads = 1, loads = 0, st = 0;
       uint32_t ph = 0;
       for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
-        // the place is free when the one tile is in tensor memory; the second is read where it lies
-        if (e.index > 0 && !mbar_wait(TWO ? q_free : q_ready, (e.index - 1) & 1, p.max_spin)) {
-          ok = false;
-          break;
+        if (e.index > 0) {  // the first segment's is loaded by the PV issuer, which has the time
+          // the place is free when the one tile is in tensor memory; the second is read where it lies
+          if (!mbar_wait(TWO ? q_free : q_ready, (e.index - 1) & 1, p.max_spin)) {
+            ok = false;
+            break;
+          }
+          load_q(e);
+          ++q_loads;
         }
-        const int node0 = e.grp * C::TILES * p.npt;
-        const int tiles = TWO && node0 + p.npt < p.m ? 2 : 1;  // a last group may have one tile
-        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(tiles * C::ATOMS * R * 128));
-        for (int h = 0; h < tiles; ++h)
-#pragma unroll
-          for (int a = 0; a < C::ATOMS; ++a)
-            tma_load_3d(sQ + h * C::Q_TILE + a * C::ATOM_Q, &p.tmQ, q_full, a * 64, e.g * G,
-                        e.i * p.m + node0 + h * p.npt, pol_q);
-        ++q_loads;
         for (int u = e.u0; u < e.u1; ++u) {
           const int base = unit_base(e.s, u);
           int row;
@@ -424,7 +499,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       if (!ok) flag_status(p.status, kStatusTimeout);
       for (int k = max(0, loads - ST); k < loads; ++k)  // every copy lands before the CTA ends
         mbar_wait(&kv_full[k % ST], (k / ST) & 1, kDrainSpin);
-      if (q_loads > 0) mbar_wait(q_full, (q_loads - 1) & 1, kDrainSpin);
+      mbar_wait(q_full, (q_loads - 1) & 1, kDrainSpin);
     }
   } else if (warp == Ro::S) {
     if (lane == 0 && e.left > 0) {
@@ -474,6 +549,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     }
   } else if (warp == Ro::PV) {
     if (lane == 0 && e.left > 0) {
+      if (!p.stall) load_q(e);
       constexpr uint32_t id_pv = idesc_bf16_f32(kTileRows, HD) | kIdescBMajorMN;
       const uint64_t v_desc0 = sw128_mnmajor_desc(smem_u32(sKV + C::KV_TILE), C::ATOM_KV);
       bool ok = true;
@@ -518,34 +594,9 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         if (!ok) break;
         const int base = unit_base(e.s, u);
         if (!unit_plain(p, e.s, base)) {
-          const int nv = e.s.ctx + e.s.n - base;  // keys of the unit that exist
-          uint8_t *vt = sKV + st * C::STAGE + C::KV_TILE;
-          uint32_t found0 = 0, found1 = 0;
-          // 16-byte pieces, eight of a row and atom: a lane's are those of key lane / 8 and every fourth from it
-#pragma unroll 8
-          for (int k = 0; k < C::KV_TILE / 512; ++k) {
-            const int key = (4 * k + (lane >> 3)) % kKeys;
-            uint4 *at = reinterpret_cast<uint4 *>(vt + (k * 32 + lane) * 16);
-            const uint4 x = *at;
-            uint32_t word[4] = {x.x, x.y, x.z, x.w};
-            uint32_t odd = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t lo = (word[q] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
-              const uint32_t hi = (word[q] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-              word[q] &= ~(lo | hi);
-              odd |= lo | hi;
-            }
-            if (key >= nv) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if (odd) {
-              *at = make_uint4(word[0], word[1], word[2], word[3]);
-              (key < 32 ? found0 : found1) |= 1u << (key & 31);
-            }
-          }
-          fence_proxy_async_smem();
-          const uint32_t f0 = __reduce_or_sync(0xffffffffu, found0), f1 = __reduce_or_sync(0xffffffffu, found1);
-          if (lane == 0) poison[st] = static_cast<unsigned long long>(f1) << 32 | f0;
+          const unsigned long long found =
+              clean_values<C::ATOMS>(sKV + st * C::STAGE + C::KV_TILE, e.s.ctx + e.s.n - base, lane);
+          if (lane == 0) poison[st] = found;
         }
         __syncwarp();
         if (lane == 0) {
@@ -602,6 +653,12 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       unsigned long long line = 0;  // nodes this row sees
       int lo = 0;                   // its first context row behind the sinks
       bool have_line = false;
+      int up0 = -1, up1 = -1;       // parents of nodes `lane` and lane + 32, for the masks to come
+      if (p.parent) {
+        const int *up = p.parent + (long long)e.i * p.m;
+        if (lane < p.m) up0 = up[lane];
+        if (lane + 32 < p.m) up1 = up[lane + 32];
+      }
       const int u_first = TWO ? e.u0 : e.u0 + ((units ^ half) & 1);
       int step = 0;
 #pragma unroll 1
@@ -622,7 +679,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         if (!unit_plain(p, e.s, base)) {
           if (!have_line) {
             int depth = 0;
-            line = real ? line_of(p, e.s, e.i, node, &depth) : 0;
+            line = line_of(p, e.s, real ? node : -1, up0, up1, &depth);
             lo = p.window > 0 ? e.s.ctx + depth - p.window + 1 : 0;
             have_line = true;
           }
@@ -709,49 +766,45 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       units += e.u1 - e.u0;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (e.index > 0);
       float M = m_run, L = l_run, a0 = 1.f, a1 = 0.f;
-      bool has1 = false;
       if (!TWO && half == 1 && more) ok = copy_q(e.index + 1);
-      if (ok && !TWO && half == 1) ok = e.index == 0 || mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);
+      if (ok && !TWO && e.index > 0) ok = mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);  // ml was read
       if (ok && mine) ok = mbar_wait_warp(&p_empty[half], (step >> 1) & 1, p.max_spin);
       if (!ok) break;
-      if (!TWO && half == 1) {  // half 0 joins the two; it has read the segment before
-        ml1[r] = mine ? make_float2(m_run, l_run) : make_float2(-FLT_MAX, -1.f);
+      if (!TWO) {  // each half ends half of the channels, of both O
+        ml[half * kTileRows + r] = mine ? make_float2(M, L) : make_float2(-FLT_MAX, -1.f);
         tc_fence_before();
-        warp_arrive(ml_ready, lane);
-        continue;
-      }
-      if (!TWO) {
-        ok = mbar_wait_warp(ml_ready, e.index & 1, p.max_spin);
+        warp_arrive(&ml_ready[half], lane);
+        ok = mbar_wait_warp(&ml_ready[half ^ 1], e.index & 1, p.max_spin);
         if (!ok) break;
-        const float2 o1 = ml1[r];
-        has1 = o1.y >= 0.f || o1.y != o1.y;
-        M = fmaxf(m_run, o1.x);
-        a0 = mine ? ex2((m_run - M) * sl2) : 0.f;
-        a1 = has1 ? ex2((o1.x - M) * sl2) : 0.f;
-        L = (mine ? l_run * a0 : 0.f) + (has1 ? o1.y * a1 : 0.f);
+        const float2 h0 = ml[r], h1 = ml[kTileRows + r];
+        M = fmaxf(h0.x, h1.x);
+        a0 = h0.y < 0.f ? 0.f : ex2((h0.x - M) * sl2);
+        a1 = h1.y < 0.f ? 0.f : ex2((h1.x - M) * sl2);
+        L = (h0.y < 0.f ? 0.f : h0.y * a0) + (h1.y < 0.f ? 0.f : h1.y * a1);
       }
       tc_fence_after();
       if (warp_real) {
-        const bool any1 = __any_sync(0xffffffffu, has1);
         const float inv = 1.0f / L;
         const int prow = slot * p.part_rows + (TWO ? half * kTileRows : 0) + r;
+        // with one unit only, one of the two O was not begun
+        const int first0 = TWO || e.u1 - e.u0 > 1 ? -1 : (units - (e.u1 - e.u0)) & 1;
+        const int c0 = TWO ? 0 : half * (HD / 2), cn = TWO ? HD : HD / 2;
 #pragma unroll 1
-        for (int cc = 0; cc < HD / 16; ++cc) {
+        for (int cc = c0; cc < c0 + cn; cc += 16) {
           float ov[16];
           if (TWO) {
-            tmem_ld16(o_mine + cc * 16, ov);
-          } else {
-            float o1v[16];
-            if (any1)
-              tmem_ld16_two(trow + C::O_COL + cc * 16, ov, trow + C::O_COL + HD + cc * 16, o1v);
-            else
-              tmem_ld16(trow + C::O_COL + cc * 16, ov);
+            tmem_ld16(o_mine + cc, ov);
+          } else if (first0 < 0) {
+            float o1[16];
+            tmem_ld16_two(trow + C::O_COL + cc, ov, trow + C::O_COL + HD + cc, o1);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) ov[c] = (mine ? ov[c] * a0 : 0.f) + (has1 ? o1v[c] * a1 : 0.f);
+            for (int c = 0; c < 16; ++c) ov[c] = ov[c] * a0 + o1[c] * a1;
+          } else {
+            tmem_ld16(trow + C::O_COL + first0 * HD + cc, ov);
           }
           if (!real) continue;
           if (whole) {
-            uint16_t *dst = p.o + (((long long)e.i * p.m + node) * p.Hq + e.g * G + hq) * HD + cc * 16;
+            uint16_t *dst = p.o + (((long long)e.i * p.m + node) * p.Hq + e.g * G + hq) * HD + cc;
 #pragma unroll
             for (int v = 0; v < 2; ++v)
               reinterpret_cast<uint4 *>(dst)[v] =
@@ -760,13 +813,14 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
                              pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
                              pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
           } else {
-            float *dst = p.part_o + (long long)prow * HD + cc * 16;
+            float *dst = p.part_o + (long long)prow * HD + cc;
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               reinterpret_cast<float4 *>(dst)[v] = make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
           }
         }
-        if (real && !whole) *reinterpret_cast<float2 *>(p.part_ml + (long long)prow * 2) = make_float2(M, L);
+        if (real && !whole && (TWO || half == 0))
+          *reinterpret_cast<float2 *>(p.part_ml + (long long)prow * 2) = make_float2(M, L);
       }
       tc_fence_before();
       warp_arrive(&o_free[TWO ? half : 0], lane);
@@ -792,45 +846,39 @@ template <int HD>
 __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const __grid_constant__ AttnTreeParams p) {
   constexpr int E = HD / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.Hq / p.Hkv, R = p.npt * G, per = p.Hkv * p.groups;
+  const int G = p.Hq / p.Hkv, R = p.npt * G;
   const int r = blockIdx.y * kMergeWarps + warp;  // row of the slot
   // This grid's end has to imply the attention's: CTA (0, 0) always waits for it. The lengths are older than
   // the attention, which lets this launch begin only once it waited itself.
   const bool anchor = blockIdx.x == 0 && blockIdx.y == 0;
-  const long long T = all_units(p, lane);
-  const int Ge = T < p.grid ? static_cast<int>(T) : p.grid;
+  griddep_launch();  // the next launch may begin too: it waits for this grid's end
+  const Split sp = make_split(p, nullptr, lane);
   const int c0 = blockIdx.x;
-  int i = -1, c1 = 0, pair = 0, first_slot = 0;
-  if (c0 + 1 < Ge) {
-    const long long u = range_start(T, Ge, c0 + 1);
-    long long before = 0;
-    i = find_sequence(p, u, lane, &before);
-    if (i >= 0) {
-      const int U = units_of(p, i);
-      const int k = static_cast<int>((u - before) / U);
-      const long long start = before + (long long)k * U;
-      pair = i * per + k;
-      // cut here, and not in an earlier range
-      if (start == u || range_of(T, Ge, start) != c0) i = -1;
-      c1 = range_of(T, Ge, start + U - 1);
-      first_slot = 2 * c0 + (range_start(T, Ge, c0) != start);
-    }
+  Place at = {-1, 0, 0, 0, 1};
+  int c1 = 0, first_slot = 0, node = 0, hq = 0;
+  if (c0 + 1 < sp.ctas) {
+    const int u = range_start(sp, c0 + 1);
+    at = find_unit(p, u, lane);
+    const int start = u - at.unit;
+    // cut here, and not in an earlier range
+    if (at.unit == 0 || range_of(sp, start) != c0) at.i = -1;
+    c1 = range_of(sp, start + at.U - 1);
+    first_slot = 2 * c0 + (range_start(sp, c0) != start);
   }
-  int node = 0, hq = 0;
-  if (i >= 0) {
+  const int i = [&] {
+    if (at.i < 0) return -1;
     const int tile = r / kTileRows, rt = r % kTileRows;
     const int tiles = p.part_rows > kTileRows ? 2 : 1;
     const int jr = rt / G;
     hq = rt - jr * G;
-    node = (pair % p.groups * tiles + tile) * p.npt + jr;
-    if (rt >= R || node >= clamp_nodes(p, i)) i = -1;
-  }
+    node = (at.grp * tiles + tile) * p.npt + jr;
+    return rt < R && node < clamp_nodes(p, at.i) ? at.i : -1;
+  }();
   if (i < 0) {
     if (anchor) griddep_wait();
     return;
   }
   griddep_wait();
-  griddep_launch();
   const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
   float M = -FLT_MAX, L = 0.f, acc[E];
 #pragma unroll
@@ -856,8 +904,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
     M = Mn;
   }
   const float inv = 1.0f / L;
-  const int g = pair % per / p.groups;
-  uint16_t *dst = p.o + (((long long)i * p.m + node) * p.Hq + g * G + hq) * HD + lane * E;
+  uint16_t *dst = p.o + (((long long)i * p.m + node) * p.Hq + at.g * G + hq) * HD + lane * E;
   if constexpr (E == 4)
     *reinterpret_cast<uint2 *>(dst) =
         make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));

@@ -20,9 +20,9 @@ constexpr int kAcceptWarps = 4;
 
 // One warp per sequence, two nodes per lane: every load first, then a step of the walk is two ballots
 // (the lowest child whose token is the target's). Latency: a launch, one round of loads, depth * ~30 cycles.
+// It lets the next launch begin only at its end: a call's kernels may read lengths before they wait.
 __global__ void __launch_bounds__(kAcceptWarps * 32) accept_tree_kernel(const AcceptTreeParams p) {
   griddep_wait();
-  griddep_launch();
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5);
   if (i >= p.nb) return;
