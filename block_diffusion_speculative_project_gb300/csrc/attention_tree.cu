@@ -55,15 +55,16 @@ struct Roles {
   static constexpr int THREADS = NQ == 4 ? 384 : NQ == 2 ? 256 : 192;
 };
 
-template <int HD, bool TWO>
+template <int HD, int NQ, bool TWO>
 struct Cfg {
   static constexpr int ATOMS = HD / 64;            // 128-byte swizzle atoms across hd
-  static constexpr int ATOM_Q = kTileRows * 128;
+  static constexpr int ATOM_Q = (TWO ? kTileRows : NQ * 32) * 128;
   static constexpr int TILES = TWO ? 2 : 1;
   static constexpr int Q_TILE = ATOMS * ATOM_Q;
   static constexpr int ATOM_KV = kKeys * 128;
   static constexpr int KV_TILE = ATOMS * ATOM_KV;
   static constexpr int STAGE = 2 * KV_TILE;        // K, then V
+  // 160 to 192 KB of K and V on the way (64 single tokens: 178 us, with 160 KB 184)
   static constexpr int STAGES = HD == 64 ? 8 : TWO ? 5 : 6;
   static constexpr int OFF_KV = TILES * Q_TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
@@ -113,6 +114,7 @@ __device__ __forceinline__ bool unit_plain(const AttnTreeParams &p, const Span &
          (p.window <= 0 || base >= s.ctx + s.n - p.window || base + kKeys <= p.sinks);
 }
 
+constexpr int kCostFrom = 16;  // units of a CTA from which a pair's cost counts
 constexpr int kSeqCache = 64;  // sequences whose lengths a CTA keeps in shared memory
 
 __device__ __forceinline__ Span span_of(const AttnTreeParams &p, const int2 *seqs, int i) {
@@ -126,10 +128,11 @@ __device__ __forceinline__ Span span_of(const AttnTreeParams &p, const int2 *seq
   return make_span(p, v.x, v.y);
 }
 
-// All units of a call over its CTAs: CTA c has q or (the first r CTAs) q + 1 of them in a row. Their number
-// stays below 2^31: pairs of fewer than 2^31 cache rows, in up to 16 groups.
+// All units of a call over its CTAs: CTA c has q or (the first r CTAs) q + 1 of them in a row. Where a CTA has
+// some, a pair counts as `cost` units more, which come first: what a segment takes besides its units. Their
+// number stays below 2^31: pairs of fewer than 2^31 cache rows, in up to 16 groups.
 struct Split {
-  int T, ctas, q, r;
+  int T, ctas, q, r, cost;
 };
 __device__ __forceinline__ int range_start(const Split &s, int c) { return c * s.q + min(c, s.r); }
 __device__ __forceinline__ int range_of(const Split &s, int u) {  // the CTA that has unit u
@@ -137,29 +140,33 @@ __device__ __forceinline__ int range_of(const Split &s, int u) {  // the CTA tha
   return u < first ? u / (s.q + 1) : s.r + (u - first) / s.q;
 }
 
-// Where a unit of all units is: sequence i (-1: nowhere), kv head g, group grp, `unit` of a pair of U.
+// Where one of these is: sequence i (-1: nowhere), kv head g, group grp, place `at` in a pair of U units.
 struct Place {
-  int i, g, grp, unit, U;
+  int i, g, grp, at, U;
 };
 
 // Warp-collective: the lengths of the first sequences to `seqs` (if not null), and the split.
 __device__ __forceinline__ Split make_split(const AttnTreeParams &p, int2 *seqs, int lane) {
-  int sum = 0;
+  int sum = 0, some = 0;
   for (int i = lane; i < p.nb; i += 32) {
     const int n = clamp_nodes(p, i), ctx = clamp_ctx(p, i, n);
     if (seqs && i < kSeqCache) seqs[i] = make_int2(ctx, n);
     sum += make_span(p, ctx, n).U;
+    some += n > 0;
   }
+  const int per = p.Hkv * p.groups;
   Split s;
-  s.T = __reduce_add_sync(0xffffffffu, sum) * (p.Hkv * p.groups);
+  s.T = __reduce_add_sync(0xffffffffu, sum) * per;
+  s.cost = s.T >= kCostFrom * p.grid ? p.pair_cost : 0;
+  s.T += __reduce_add_sync(0xffffffffu, some) * per * s.cost;
   s.ctas = max(1, min(s.T, p.grid));
   s.q = s.T / s.ctas;
   s.r = s.T - s.q * s.ctas;
   return s;
 }
 
-// Warp-collective: the place of unit u, 0 <= u < T.
-__device__ __forceinline__ Place find_unit(const AttnTreeParams &p, int u, int lane) {
+// Warp-collective: the place of u, 0 <= u < T.
+__device__ __forceinline__ Place find_unit(const AttnTreeParams &p, const Split &s, int u, int lane) {
   const int per = p.Hkv * p.groups;
   Place f = {-1, 0, 0, 0, 1};
   int base = 0;
@@ -170,7 +177,8 @@ __device__ __forceinline__ Place find_unit(const AttnTreeParams &p, int u, int l
       const int n = clamp_nodes(p, i);
       U = make_span(p, clamp_ctx(p, i, n), n).U;
     }
-    int v = U * per;
+    const int all = U > 0 ? U + s.cost : 0;
+    int v = all * per;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, v, o);
@@ -181,9 +189,10 @@ __device__ __forceinline__ Place find_unit(const AttnTreeParams &p, int u, int l
       const int l = __ffs(hit) - 1;
       f.i = b + l;
       f.U = __shfl_sync(0xffffffffu, U, l);
-      const int off = u - base - (__shfl_sync(0xffffffffu, v, l) - f.U * per);
-      const int k = off / f.U;
-      f.unit = off - k * f.U;
+      const int V = f.U + s.cost;
+      const int off = u - base - (__shfl_sync(0xffffffffu, v, l) - V * per);
+      const int k = off / V;
+      f.at = off - k * V;
       f.g = k / p.groups;
       f.grp = k - f.g * p.groups;
       return f;
@@ -194,32 +203,40 @@ __device__ __forceinline__ Place find_unit(const AttnTreeParams &p, int u, int l
 }
 
 // A run of one pair's units [u0, u1) in this CTA's range: sequence i, kv head g, group grp of tiles. All
-// roles go through the same segments; `left` units of the range are not behind it.
+// roles go through the same segments; `left` of the range are not before its pair's, 0 behind the last one.
 struct Seg {
-  int i, g, grp, u0, u1, index, left;
+  int i, g, grp, u0, u1, index, left, cost;
   Span s;
 };
-// sched: sequence, kv head, group, unit, units of the range
+__device__ __forceinline__ void seg_units(Seg &e, int at) {
+  e.u0 = max(0, at - e.cost);
+  e.u1 = min(e.s.U, at + e.left - e.cost);
+  if (e.u1 <= e.u0) e.left = 0;  // the range ends before the pair's first unit
+}
+__device__ __forceinline__ bool seg_more(const Seg &e) {  // a segment follows
+  return e.left - (e.s.U - e.u0 + e.cost) > e.cost;
+}
+// sched: sequence, kv head, group, place in the pair, length of the range, cost
 __device__ __forceinline__ Seg seg_begin(const AttnTreeParams &p, const int2 *seqs, const int *sched) {
   Seg e;
   e.i = sched[0];
   e.g = sched[1];
   e.grp = sched[2];
-  e.u0 = sched[3];
   e.left = sched[4];
+  e.cost = sched[5];
   e.index = 0;
-  e.u1 = e.u0;
   if (e.left > 0) {
     e.s = span_of(p, seqs, e.i);
-    e.u1 = min(e.s.U, e.u0 + e.left);
+    const int at = sched[3];
+    seg_units(e, at);
+    if (e.left > 0) e.left += min(at, e.cost);  // as if the range had begun with the pair's cost
   }
   return e;
 }
 __device__ __forceinline__ void seg_next(Seg &e, const AttnTreeParams &p, const int2 *seqs) {
-  e.left -= e.u1 - e.u0;
+  e.left -= e.s.U - e.u0 + e.cost;
   if (e.left <= 0) return;
   ++e.index;
-  e.u0 = 0;
   if (++e.grp == p.groups) {
     e.grp = 0;
     if (++e.g == p.Hkv) {
@@ -229,7 +246,7 @@ __device__ __forceinline__ void seg_next(Seg &e, const AttnTreeParams &p, const 
       } while (e.s.U == 0 && e.i + 1 < p.nb);
     }
   }
-  e.u1 = min(e.s.U, e.left);
+  seg_units(e, 0);
 }
 
 // A ring's next stage: its place, and the parity of its barriers.
@@ -348,7 +365,7 @@ __device__ __forceinline__ unsigned long long clean_values(uint8_t *v, int nv, i
 
 template <int HD, int NQ, bool TWO>
 __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const __grid_constant__ AttnTreeParams p) {
-  using C = Cfg<HD, TWO>;
+  using C = Cfg<HD, NQ, TWO>;
   using Ro = Roles<NQ>;
   constexpr int ST = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -369,10 +386,10 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   uint64_t *mma_done = ml_ready + 2;    // [2]
   uint64_t *poison = mma_done + 2;      // [ST] keys of the stage whose values were not finite
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + ST);
-  int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // [5]
+  int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // [6]
   int2 *seqs = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
   float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);  // [2][128] a half's maximum and sum
-  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 2 + 2) * 8 + 24 <= 512, "barrier region");
+  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 2 + 2) * 8 + 28 <= 512, "barrier region");
   static_assert(kSeqCache * 8 <= 512, "lengths");
 
   const int warp = threadIdx.x >> 5;
@@ -414,19 +431,20 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   if (threadIdx.x == 0) griddep_launch();
   if (warp == Ro::PRODUCER) {
     const Split sp = make_split(p, seqs, lane);
-    Place at = {0, 0, 0, 0, 1};
+    Place at = {-1, 0, 0, 0, 1};
     int count = 0;
     if (static_cast<int>(blockIdx.x) < sp.ctas && sp.T > 0) {
       const int u0 = range_start(sp, blockIdx.x);
-      at = find_unit(p, u0, lane);
+      at = find_unit(p, sp, u0, lane);
       count = at.i < 0 ? 0 : range_start(sp, blockIdx.x + 1) - u0;
     }
     if (lane == 0) {
       sched[0] = at.i;
       sched[1] = at.g;
       sched[2] = at.grp;
-      sched[3] = at.unit;
+      sched[3] = at.at;
       sched[4] = count;
+      sched[5] = sp.cost;
     }
   }
   if (warp == Ro::CLEAN && blockIdx.x == 0) {
@@ -645,7 +663,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     if (copies && e.left > 0) ok = copy_q(0);
     int units = 0;  // of the segments before
     for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
-      const bool more = e.left > e.u1 - e.u0;  // a segment follows
+      const bool more = seg_more(e);
       const int node = (e.grp * C::TILES + (TWO ? half : 0)) * p.npt + jr;
       const bool real = r < R && node < e.s.n;
       const bool warp_real = __any_sync(0xffffffffu, real);
@@ -837,17 +855,20 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   }
 }
 
-// Joins the partials of a pair that several CTAs share, in CTA order. CTA x of this grid stands for the
-// boundary at the start of range x + 1, and joins the pair that is cut there for the first time; one warp
-// a row, hd/32 values a lane.
+// Joins the partials of a pair that several CTAs share. CTA x of this grid stands for the boundary at the
+// start of range x + 1, and joins the pair that is cut there for the first time; WPR warps a row, each every
+// WPR-th part, hd/32 values a lane: with few rows the parts' loads are what it takes.
 constexpr int kMergeWarps = 8;
+constexpr int kMaxParts = kTreeCtas;
 
-template <int HD>
+template <int HD, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const __grid_constant__ AttnTreeParams p) {
   constexpr int E = HD / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, R = p.npt * G;
-  const int r = blockIdx.y * kMergeWarps + warp;  // row of the slot
+  const int r = blockIdx.y * (kMergeWarps / WPR) + warp / WPR;  // row of the slot
+  const int sub = warp % WPR;
+  __shared__ float part[WPR > 1 ? kMergeWarps : 1][HD];
   // This grid's end has to imply the attention's: CTA (0, 0) always waits for it. The lengths are older than
   // the attention, which lets this launch begin only once it waited itself.
   const bool anchor = blockIdx.x == 0 && blockIdx.y == 0;
@@ -858,12 +879,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
   int c1 = 0, first_slot = 0, node = 0, hq = 0;
   if (c0 + 1 < sp.ctas) {
     const int u = range_start(sp, c0 + 1);
-    at = find_unit(p, u, lane);
-    const int start = u - at.unit;
-    // cut here, and not in an earlier range
-    if (at.unit == 0 || range_of(sp, start) != c0) at.i = -1;
-    c1 = range_of(sp, start + at.U - 1);
-    first_slot = 2 * c0 + (range_start(sp, c0) != start);
+    at = find_unit(p, sp, u, lane);
+    const int start = u - at.at;
+    // units on both sides, and not cut in an earlier range
+    if (at.at <= sp.cost || range_of(sp, start + sp.cost) != c0) at.i = -1;
+    c1 = range_of(sp, start + sp.cost + at.U - 1);
+    first_slot = 2 * c0 + (range_start(sp, c0) < start);
   }
   const int i = [&] {
     if (at.i < 0) return -1;
@@ -880,28 +901,56 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
   }
   griddep_wait();
   const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-  float M = -FLT_MAX, L = 0.f, acc[E];
+  // maxima and sums of the parts, one a lane, so that the parts' loads wait for nothing
+  const int n = c1 - c0 + 1;
+  auto row_of = [&](int k) { return (long long)(k == 0 ? first_slot : 2 * (c0 + k)) * p.part_rows + r; };
+  float w[kMaxParts / 32], M = -FLT_MAX, L = 0.f;
+  {
+    float2 ml[kMaxParts / 32];
+#pragma unroll
+    for (int b = 0; b < kMaxParts / 32; ++b) {
+      const int k = 32 * b + lane;
+      ml[b] = k < n ? *reinterpret_cast<const float2 *>(p.part_ml + row_of(k) * 2) : make_float2(-FLT_MAX, 0.f);
+      M = fmaxf(M, ml[b].x);
+    }
+    M = warp_max(M);
+#pragma unroll
+    for (int b = 0; b < kMaxParts / 32; ++b) {
+      w[b] = 32 * b + lane < n ? exp2f((ml[b].x - M) * sl2) : 0.f;
+      L += 32 * b + lane < n ? ml[b].y * w[b] : 0.f;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const long long row = (long long)(c == c0 ? first_slot : 2 * c) * p.part_rows + r;
-    const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + row * 2);
-    float v[E];
-    const float *src = p.part_o + row * HD + lane * E;
-    if constexpr (E == 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(src);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2 *>(src);
-      v[0] = x.x, v[1] = x.y;
-    }
-    const float Mn = fmaxf(M, ml.x);
-    const float a_old = exp2f((M - Mn) * sl2), a_new = exp2f((ml.x - Mn) * sl2);
-    L = L * a_old + ml.y * a_new;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a_old + v[e] * a_new;
-    M = Mn;
+  for (int b = 0; b < kMaxParts / 32; ++b) {
+    const int to = min(32, n - 32 * b);
+#pragma unroll 8
+    for (int k = sub; k < to; k += WPR) {
+      const float *src = p.part_o + row_of(32 * b + k) * HD + lane * E;
+      const float a = __shfl_sync(0xffffffffu, w[b], k);
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(src);
+        acc[0] = fmaf(a, x.x, acc[0]), acc[1] = fmaf(a, x.y, acc[1]);
+        acc[2] = fmaf(a, x.z, acc[2]), acc[3] = fmaf(a, x.w, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2 *>(src);
+        acc[0] = fmaf(a, x.x, acc[0]), acc[1] = fmaf(a, x.y, acc[1]);
+      }
+    }
+  }
+  if (WPR > 1) {  // all of a block's warps have the same row
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += part[k][lane * E + e];
   }
   const float inv = 1.0f / L;
   uint16_t *dst = p.o + (((long long)i * p.m + node) * p.Hq + at.g * G + hq) * HD + lane * E;
@@ -912,17 +961,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
     *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
+template <int HD, int WPR>
+cudaError_t launch_merge(const AttnTreeParams &p, int rows, cudaStream_t s) {
+  // the attention's split of the SM's memory, so that this grid's CTAs may stand by next to it
+  static const cudaError_t configured = cudaFuncSetAttribute(
+      attn_tree_merge_kernel<HD, WPR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (configured != cudaSuccess) return configured;
+  constexpr int per = kMergeWarps / WPR;
+  return launch_pdl(attn_tree_merge_kernel<HD, WPR>, dim3(p.grid, (rows + per - 1) / per), dim3(kMergeWarps * 32), 0, s,
+                    p);
+}
+
 template <int HD, int NQ, bool TWO>
 cudaError_t launch(const AttnTreeParams &p, cudaStream_t s) {
-  using C = Cfg<HD, TWO>;
+  using C = Cfg<HD, NQ, TWO>;
   static const cudaError_t configured = cudaFuncSetAttribute(
       attn_tree_kernel<HD, NQ, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (configured != cudaSuccess) return configured;
   cudaError_t e = launch_pdl(attn_tree_kernel<HD, NQ, TWO>, dim3(p.grid), dim3(Roles<NQ>::THREADS), C::SMEM, s, p);
   if (e != cudaSuccess) return e;
   const int rows = TWO ? 2 * kTileRows : p.npt * (p.Hq / p.Hkv);
-  return launch_pdl(attn_tree_merge_kernel<HD>, dim3(p.grid, (rows + kMergeWarps - 1) / kMergeWarps),
-                    dim3(kMergeWarps * 32), 0, s, p);
+  return rows <= 16 ? launch_merge<HD, kMergeWarps>(p, rows, s) : launch_merge<HD, 1>(p, rows, s);
 }
 
 template <int HD>
@@ -950,7 +1009,10 @@ void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows) {
   *part_rows = 2 * kTileRows;
 }
 
-cudaError_t launch_attention_tree(const AttnTreeParams &p, cudaStream_t s) {
+cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s) {
+  // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 198.7 us
+  // without, 195.2 with 4, 64 x 64 rows 321, 293 with 7; a unit of 64 channels takes half the time.
+  p.pair_cost = (p.npt * (p.Hq / p.Hkv) > 64 ? 7 : 4) * (128 / p.hd);
   switch (p.hd) {
     case 64: return launch_form<64>(p, s);
     case 128: return launch_form<128>(p, s);

@@ -1342,7 +1342,7 @@ int dflash_attention_tree(dflash_handle_t h, int nb, int layer, int m, const voi
   p.page_table = c.num_pages > 0 ? h->block_table : nullptr;
   p.pages_per_seq = c.Cmax / kPageRows;
   p.num_pages = c.num_pages;
-  p.grid = h->num_sms;
+  p.grid = std::min(h->num_sms, kTreeCtas);
   p.status = w.status();
   p.max_spin = c.max_spin;
   p.stall = (c.flags & DFLASH_FLAG_TEST_STALL) ? 1 : 0;

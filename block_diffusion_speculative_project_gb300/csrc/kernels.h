@@ -328,7 +328,8 @@ cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 
 // ---------------------------------------------------------------- trees of drafted tokens
 
-constexpr int kTreeMax = 64;  // nodes of a tree (a row's ancestors are the bits of 64)
+constexpr int kTreeMax = 64;   // nodes of a tree (a row's ancestors are the bits of 64)
+constexpr int kTreeCtas = 160;  // most CTAs of a tree's attention, and so parts of a pair
 
 // Attention of a tree's nodes over the bf16 caches (attention_tree.cu).
 struct AttnTreeParams {
@@ -342,6 +343,7 @@ struct AttnTreeParams {
   float *part_ml;            // [2 * grid slots][part_rows][2] (running maximum, running sum)
   int nb, m, Hq, Hkv, hd, Cmax;
   int npt, groups, part_rows;  // nodes of a tile, groups of tiles of a kv head, rows of a slot
+  int pair_cost;             // what the split counts for a pair besides its units (set by the launch)
   int layer_row0;            // first cache row of the layer
   int window, sinks;         // window 0: none
   int max_ctx;               // caller's bound on ctx_len (larger values are reported and clamped)
@@ -353,7 +355,7 @@ struct AttnTreeParams {
   int stall;                 // test hook: issue no loads so the waits run out
 };
 void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows);
-cudaError_t launch_attention_tree(const AttnTreeParams &p, cudaStream_t s);
+cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s);
 
 // Walk of the trees along the target's tokens (tree_ops.cu).
 struct AcceptTreeParams {
