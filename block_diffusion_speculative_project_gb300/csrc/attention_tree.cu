@@ -30,6 +30,7 @@
 // the cleaner, and the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32,
 // rounds P to bf16 (2^-9 of each probability, as the values have) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
+#include <algorithm>
 #include <cfloat>
 
 #include "common.cuh"
@@ -65,10 +66,11 @@ struct Cfg {
   static constexpr int KV_TILE = ATOMS * ATOM_KV;
   static constexpr int STAGE = 2 * KV_TILE;        // K, then V
   // 160 to 192 KB of K and V on the way (64 single tokens: 178 us, with 160 KB 184)
-  static constexpr int STAGES = HD == 64 ? 8 : TWO ? 5 : 6;
+  static constexpr int STAGES = HD == 64 ? (TWO ? 10 : 12) : TWO ? 5 : 6;
+  static constexpr int BARS = HD == 64 ? 1024 : 512;  // bytes for the barriers
   static constexpr int OFF_KV = TILES * Q_TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * STAGE;
-  static constexpr int OFF_SEQ = OFF_BAR + 512;
+  static constexpr int OFF_SEQ = OFF_BAR + BARS;
   static constexpr int OFF_ML = OFF_SEQ + 512;
   static constexpr size_t SMEM = OFF_ML + 2 * kTileRows * 8;
   static constexpr uint32_t S_COL = 0;             // two S buffers of 64 columns
@@ -145,15 +147,16 @@ struct Place {
   int i, g, grp, at, U;
 };
 
-// Warp-collective: the lengths of the first sequences to `seqs` (if not null), and the split.
+// Warp-collective: the lengths of the first sequences to `seqs`, and the split.
 __device__ __forceinline__ Split make_split(const AttnTreeParams &p, int2 *seqs, int lane) {
   int sum = 0, some = 0;
   for (int i = lane; i < p.nb; i += 32) {
     const int n = clamp_nodes(p, i), ctx = clamp_ctx(p, i, n);
-    if (seqs && i < kSeqCache) seqs[i] = make_int2(ctx, n);
+    if (i < kSeqCache) seqs[i] = make_int2(ctx, n);
     sum += make_span(p, ctx, n).U;
     some += n > 0;
   }
+  __syncwarp();
   const int per = p.Hkv * p.groups;
   Split s;
   s.T = __reduce_add_sync(0xffffffffu, sum) * per;
@@ -166,17 +169,14 @@ __device__ __forceinline__ Split make_split(const AttnTreeParams &p, int2 *seqs,
 }
 
 // Warp-collective: the place of u, 0 <= u < T.
-__device__ __forceinline__ Place find_unit(const AttnTreeParams &p, const Split &s, int u, int lane) {
+__device__ __forceinline__ Place find_unit(const AttnTreeParams &p, const int2 *seqs, const Split &s, int u,
+                                           int lane) {
   const int per = p.Hkv * p.groups;
   Place f = {-1, 0, 0, 0, 1};
   int base = 0;
   for (int b = 0; b < p.nb; b += 32) {
     const int i = b + lane;
-    int U = 0;
-    if (i < p.nb) {
-      const int n = clamp_nodes(p, i);
-      U = make_span(p, clamp_ctx(p, i, n), n).U;
-    }
+    const int U = i < p.nb ? span_of(p, seqs, i).U : 0;
     const int all = U > 0 ? U + s.cost : 0;
     int v = all * per;
 #pragma unroll
@@ -203,9 +203,10 @@ __device__ __forceinline__ Place find_unit(const AttnTreeParams &p, const Split 
 }
 
 // A run of one pair's units [u0, u1) in this CTA's range: sequence i, kv head g, group grp of tiles. All
-// roles go through the same segments; `left` of the range are not before its pair's, 0 behind the last one.
+// roles go through the same segments; `left` of the range are not before its pair's, 0 behind the last one; the
+// pair begins at `pos` of all units.
 struct Seg {
-  int i, g, grp, u0, u1, index, left, cost;
+  int i, g, grp, u0, u1, index, left, cost, pos;
   Span s;
 };
 __device__ __forceinline__ void seg_units(Seg &e, int at) {
@@ -216,15 +217,16 @@ __device__ __forceinline__ void seg_units(Seg &e, int at) {
 __device__ __forceinline__ bool seg_more(const Seg &e) {  // a segment follows
   return e.left - (e.s.U - e.u0 + e.cost) > e.cost;
 }
-// sched: sequence, kv head, group, place in the pair, length of the range, cost
+// sched: sequence, kv head, group, place in the pair, length of the range; first unit, and the split's q, r and cost
 __device__ __forceinline__ Seg seg_begin(const AttnTreeParams &p, const int2 *seqs, const int *sched) {
   Seg e;
   e.i = sched[0];
   e.g = sched[1];
   e.grp = sched[2];
   e.left = sched[4];
-  e.cost = sched[5];
+  e.cost = sched[8];
   e.index = 0;
+  e.pos = sched[5] - sched[3];
   if (e.left > 0) {
     e.s = span_of(p, seqs, e.i);
     const int at = sched[3];
@@ -237,6 +239,7 @@ __device__ __forceinline__ void seg_next(Seg &e, const AttnTreeParams &p, const 
   e.left -= e.s.U - e.u0 + e.cost;
   if (e.left <= 0) return;
   ++e.index;
+  e.pos += e.s.U + e.cost;
   if (++e.grp == p.groups) {
     e.grp = 0;
     if (++e.g == p.Hkv) {
@@ -271,12 +274,44 @@ __device__ __forceinline__ unsigned long long low_bits(int k) {
 // Warp-collective: the nodes that this lane's node j sees, itself among them, and its depth (j < 0: none). up0 and
 // up1 of lane k are the parents of nodes k and k + 32.
 __device__ __forceinline__ unsigned long long line_of(const AttnTreeParams &p, const Span &s, int j, int up0, int up1,
-                                                      int *depth) {
+                                                      int lane, int *depth) {
   if (p.parent == nullptr) {
     *depth = max(j, 0);
     unsigned long long seen = low_bits(j + 1);
     if (p.window > 0) seen &= ~low_bits(j + 1 - p.window) | low_bits(p.sinks - s.ctx);
     return seen;
+  }
+  if (p.window <= 0 || p.window >= kTreeMax) {  // all of them: a line grows by its end's line, in log2 of the depth
+    const int k1 = lane + 32;
+    const bool top0 = up0 < 0 || up0 >= lane, top1 = up1 < 0 || up1 >= k1;
+    const bool bad = (lane < s.n && top0 && (lane != 0 || up0 != -1)) || (k1 < s.n && top1);
+    if (bad) flag_status(p.status, kStatusCheck);
+    int end0 = top0 ? lane : up0, end1 = top1 ? k1 : up1;
+    uint32_t line0 = 1u << lane, low1 = 0, high1 = 1u << lane;  // nodes below 32 have their line there
+    bool grew;
+    do {
+      const uint32_t to0 = __shfl_sync(0xffffffffu, line0, end0), next0 = __shfl_sync(0xffffffffu, end0, end0);
+      grew = next0 != static_cast<uint32_t>(end0);
+      if (p.m > 32) {
+        const int at = end1 & 31;
+        const uint32_t a = __shfl_sync(0xffffffffu, line0, at), b = __shfl_sync(0xffffffffu, low1, at);
+        const uint32_t c = __shfl_sync(0xffffffffu, high1, at);
+        const int x = __shfl_sync(0xffffffffu, end0, at), y = __shfl_sync(0xffffffffu, end1, at);
+        const int next1 = end1 < 32 ? x : y;
+        low1 |= end1 < 32 ? a : b;
+        high1 |= end1 < 32 ? 0u : c;
+        grew |= next1 != end1;
+        end1 = next1;
+      }
+      line0 |= to0;
+      end0 = next0;
+    } while (__any_sync(0xffffffffu, grew));
+    const int at = max(j, 0) & 31;
+    const uint32_t a = __shfl_sync(0xffffffffu, line0, at), b = __shfl_sync(0xffffffffu, low1, at);
+    const uint32_t c = __shfl_sync(0xffffffffu, high1, at);
+    const unsigned long long seen = j < 32 ? a : static_cast<unsigned long long>(c) << 32 | b;
+    *depth = __popcll(seen) - 1;
+    return j < 0 ? 0ull : seen;
   }
   unsigned long long seen = 0;
   int a = max(j, 0), d = 0;
@@ -329,7 +364,7 @@ __device__ __forceinline__ unsigned long long clean_values(uint8_t *v, int nv, i
     __syncwarp();
   }
   uint32_t m = 0;
-#pragma unroll 8
+#pragma unroll 16
   for (int k = 0; k < 16 * ATOMS; ++k) {
     const uint4 x = *reinterpret_cast<const uint4 *>(v + (k * 32 + lane) * 16);
     m = max_abs2(max_abs2(m, x.x), max_abs2(max_abs2(x.y, x.z), x.w));
@@ -386,10 +421,10 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   uint64_t *mma_done = ml_ready + 2;    // [2]
   uint64_t *poison = mma_done + 2;      // [ST] keys of the stage whose values were not finite
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + ST);
-  int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // [6]
+  int *sched = reinterpret_cast<int *>(tmem_slot + 1);  // [9]
   int2 *seqs = reinterpret_cast<int2 *>(smem + C::OFF_SEQ);
   float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);  // [2][128] a half's maximum and sum
-  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 2 + 2) * 8 + 28 <= 512, "barrier region");
+  static_assert((4 * ST + 2 + 2 + 2 + 2 + 3 + 2 + 2 + 2) * 8 + 40 <= C::BARS, "barrier region");
   static_assert(kSeqCache * 8 <= 512, "lengths");
 
   const int warp = threadIdx.x >> 5;
@@ -433,9 +468,9 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     const Split sp = make_split(p, seqs, lane);
     Place at = {-1, 0, 0, 0, 1};
     int count = 0;
+    const int u0 = range_start(sp, blockIdx.x);
     if (static_cast<int>(blockIdx.x) < sp.ctas && sp.T > 0) {
-      const int u0 = range_start(sp, blockIdx.x);
-      at = find_unit(p, sp, u0, lane);
+      at = find_unit(p, seqs, sp, u0, lane);
       count = at.i < 0 ? 0 : range_start(sp, blockIdx.x + 1) - u0;
     }
     if (lane == 0) {
@@ -444,9 +479,13 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       sched[2] = at.grp;
       sched[3] = at.at;
       sched[4] = count;
-      sched[5] = sp.cost;
+      sched[5] = u0;
+      sched[6] = sp.q;
+      sched[7] = sp.r;
+      sched[8] = sp.cost;
     }
   }
+  if (threadIdx.x == 0) p.joins[blockIdx.x].parts = 0;
   if (warp == Ro::CLEAN && blockIdx.x == 0) {
     bool bad = false;  // lengths out of range, reported once a launch
     for (int i = lane; i < p.nb; i += 32) {
@@ -473,51 +512,58 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
                     pol_q);
   };
   if (warp == Ro::PRODUCER) {
-    if (lane == 0 && e.left > 0 && !p.stall) {
+    if (e.left > 0 && !p.stall) {
       // K and V of one pair are read by its groups of tiles one after another
       const uint64_t pol_kv = p.groups > 1 ? policy_evict_last() : policy_evict_first();
       bool ok = true;
       int q_loads = 1, loads = 0, st = 0;
       uint32_t ph = 0;
       for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+        // a lane finds the cache row of a unit, so that 32 pages are looked up in the time of one
+        auto row_of = [&](int u) {
+          if (u >= e.u1) return 0;
+          const int base = unit_base(e.s, u);
+          if (p.page_table == nullptr) return p.layer_row0 + (e.i * p.Hkv + e.g) * p.Cmax + base;
+          int pg = p.page_table[(long long)e.i * p.pages_per_seq + base / kKeys];
+          if (pg < 0 || pg >= p.num_pages) {
+            flag_status(p.status, kStatusCheck);
+            pg = 0;
+          }
+          return p.layer_row0 + (pg * p.Hkv + e.g) * kPageRows;
+        };
+        int row = row_of(e.u0 + lane);
         if (e.index > 0) {  // the first segment's is loaded by the PV issuer, which has the time
           // the place is free when the one tile is in tensor memory; the second is read where it lies
-          if (!mbar_wait(TWO ? q_free : q_ready, (e.index - 1) & 1, p.max_spin)) {
-            ok = false;
-            break;
-          }
-          load_q(e);
+          ok = mbar_wait_warp(TWO ? q_free : q_ready, (e.index - 1) & 1, p.max_spin);
+          if (!ok) break;
+          if (lane == 0) load_q(e);
           ++q_loads;
         }
-        for (int u = e.u0; u < e.u1; ++u) {
-          const int base = unit_base(e.s, u);
-          int row;
-          if (p.page_table == nullptr) {
-            row = p.layer_row0 + (e.i * p.Hkv + e.g) * p.Cmax + base;
-          } else {
-            int pg = p.page_table[(long long)e.i * p.pages_per_seq + base / kKeys];
-            if (pg < 0 || pg >= p.num_pages) {
-              flag_status(p.status, kStatusCheck);
-              pg = 0;
-            }
-            row = p.layer_row0 + (pg * p.Hkv + e.g) * kPageRows;
+        for (int u = e.u0, k = 0; u < e.u1; ++u, ++k) {
+          if (k == 32) {
+            k = 0;
+            row = row_of(u + lane);
           }
-          if (loads >= ST && !mbar_wait(&kv_empty[st], ph ^ 1, p.max_spin)) {
-            ok = false;
-            break;
+          const int at = __shfl_sync(0xffffffffu, row, k);
+          ok = loads < ST || mbar_wait_warp(&kv_empty[st], ph ^ 1, p.max_spin);
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t *kt = sKV + st * C::STAGE;
+            mbar_arrive_expect_tx(&kv_full[st], C::STAGE);
+            tma_load_3d(kt, &p.tmK, &kv_full[st], 0, at, 0, pol_kv);
+            tma_load_3d(kt + C::KV_TILE, &p.tmV, &kv_full[st], 0, at, 0, pol_kv);
           }
-          uint8_t *kt = sKV + st * C::STAGE;
-          mbar_arrive_expect_tx(&kv_full[st], C::STAGE);
-          tma_load_3d(kt, &p.tmK, &kv_full[st], 0, row, 0, pol_kv);
-          tma_load_3d(kt + C::KV_TILE, &p.tmV, &kv_full[st], 0, row, 0, pol_kv);
+          __syncwarp();
           ++loads;
           ring_next<ST>(st, ph);
         }
       }
-      if (!ok) flag_status(p.status, kStatusTimeout);
-      for (int k = max(0, loads - ST); k < loads; ++k)  // every copy lands before the CTA ends
-        mbar_wait(&kv_full[k % ST], (k / ST) & 1, kDrainSpin);
-      mbar_wait(q_full, (q_loads - 1) & 1, kDrainSpin);
+      if (lane == 0) {
+        if (!ok) flag_status(p.status, kStatusTimeout);
+        for (int k = max(0, loads - ST); k < loads; ++k)  // every copy lands before the CTA ends
+          mbar_wait(&kv_full[k % ST], (k / ST) & 1, kDrainSpin);
+        mbar_wait(q_full, (q_loads - 1) & 1, kDrainSpin);
+      }
     }
   } else if (warp == Ro::S) {
     if (lane == 0 && e.left > 0) {
@@ -697,7 +743,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         if (!unit_plain(p, e.s, base)) {
           if (!have_line) {
             int depth = 0;
-            line = line_of(p, e.s, real ? node : -1, up0, up1, &depth);
+            line = line_of(p, e.s, real ? node : -1, up0, up1, lane, &depth);
             lo = p.window > 0 ? e.s.ctx + depth - p.window + 1 : 0;
             have_line = true;
           }
@@ -801,13 +847,18 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         L = (h0.y < 0.f ? 0.f : h0.y * a0) + (h1.y < 0.f ? 0.f : h1.y * a1);
       }
       tc_fence_after();
+      if (threadIdx.x == 0 && e.u0 == 0 && !whole) {  // the pair's first part: what the merge has to know
+        const Split sp = {0, 0, sched[6], sched[7], e.cost};
+        p.joins[blockIdx.x] = {e.i, e.g, e.grp, slot, range_of(sp, e.pos + e.cost + e.s.U - 1) - static_cast<int>(blockIdx.x) + 1,
+                               e.s.n};
+      }
       if (warp_real) {
         const float inv = 1.0f / L;
-        const int prow = slot * p.part_rows + (TWO ? half * kTileRows : 0) + r;
+        const int prow = (TWO ? half * R : 0) + r;
         // with one unit only, one of the two O was not begun
         const int first0 = TWO || e.u1 - e.u0 > 1 ? -1 : (units - (e.u1 - e.u0)) & 1;
         const int c0 = TWO ? 0 : half * (HD / 2), cn = TWO ? HD : HD / 2;
-#pragma unroll 1
+#pragma unroll 2
         for (int cc = c0; cc < c0 + cn; cc += 16) {
           float ov[16];
           if (TWO) {
@@ -818,7 +869,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
 #pragma unroll
             for (int c = 0; c < 16; ++c) ov[c] = ov[c] * a0 + o1[c] * a1;
           } else {
-            tmem_ld16(trow + C::O_COL + first0 * HD + cc, ov);
+            tmem_ld16(trow + C::O_COL + (first0 == 1 ? HD : 0) + cc, ov);
           }
           if (!real) continue;
           if (whole) {
@@ -831,14 +882,15 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
                              pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
                              pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
           } else {
-            float *dst = p.part_o + (long long)prow * HD + cc;
+            // rows side by side, four channels each: a warp's store is a piece of 512 bytes
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o) + ((long long)slot * (HD / 4) + cc / 4) * p.part_rows + prow;
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              reinterpret_cast<float4 *>(dst)[v] = make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+              dst[v * p.part_rows] = make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
           }
         }
         if (real && !whole && (TWO || half == 0))
-          *reinterpret_cast<float2 *>(p.part_ml + (long long)prow * 2) = make_float2(M, L);
+          reinterpret_cast<float2 *>(p.part_ml)[(long long)slot * p.part_rows + prow] = make_float2(M, L);
       }
       tc_fence_before();
       warp_arrive(&o_free[TWO ? half : 0], lane);
@@ -855,121 +907,131 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
   }
 }
 
-// Joins the partials of a pair that several CTAs share. CTA x of this grid stands for the boundary at the
-// start of range x + 1, and joins the pair that is cut there for the first time; WPR warps a row, each every
-// WPR-th part, hd/32 values a lane: with few rows the parts' loads are what it takes.
+// Warp-collective: the place of the first of pair x's units (or cost), 0 <= x < pairs; *start is where it lies.
+__device__ __forceinline__ Place find_pair(const AttnTreeParams &p, const int2 *seqs, const Split &s, int x, int lane,
+                                           int *start) {
+  const int per = p.Hkv * p.groups;
+  Place f = {x / per, 0, 0, 0, 0};
+  const int k = x - f.i * per;
+  f.g = k / p.groups;
+  f.grp = k - f.g * p.groups;
+  int before = 0;
+  for (int i = lane; i <= f.i; i += 32) {
+    const int U = span_of(p, seqs, i).U;
+    if (i == f.i)
+      f.U = U;
+    else
+      before += U > 0 ? U + s.cost : 0;
+  }
+  f.U = __shfl_sync(0xffffffffu, f.U, f.i & 31);
+  *start = __reduce_add_sync(0xffffffffu, before) * per + k * (f.U + s.cost);
+  return f;
+}
+
+// Joins the partials of a pair that several CTAs share. Where there are no more pairs than CTAs block x stands for pair
+// x, and finds its parts by itself while it waits for the attention; else it has the pair whose first part is CTA x's,
+// from that CTA's word. A lane has four channels of a row, as the partials lie; WPR warps share 32 lanes' parts where
+// they are what it waits for.
 constexpr int kMergeWarps = 8;
-constexpr int kMaxParts = kTreeCtas;
 
 template <int HD, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const __grid_constant__ AttnTreeParams p) {
-  constexpr int E = HD / 32;
+  const bool by_pair = p.nb * p.Hkv * p.groups <= p.grid;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.Hq / p.Hkv, R = p.npt * G;
-  const int r = blockIdx.y * (kMergeWarps / WPR) + warp / WPR;  // row of the slot
+  const int G = p.Hq / p.Hkv, R = p.npt * G, rows = p.part_rows;
+  const int f = (blockIdx.y * (kMergeWarps / WPR) + warp / WPR) * 32 + lane;  // four channels of a slot
   const int sub = warp % WPR;
-  __shared__ float part[WPR > 1 ? kMergeWarps : 1][HD];
-  // This grid's end has to imply the attention's: CTA (0, 0) always waits for it. The lengths are older than
-  // the attention, which lets this launch begin only once it waited itself.
-  const bool anchor = blockIdx.x == 0 && blockIdx.y == 0;
-  griddep_launch();  // the next launch may begin too: it waits for this grid's end
-  const Split sp = make_split(p, nullptr, lane);
-  const int c0 = blockIdx.x;
-  Place at = {-1, 0, 0, 0, 1};
-  int c1 = 0, first_slot = 0, node = 0, hq = 0;
-  if (c0 + 1 < sp.ctas) {
-    const int u = range_start(sp, c0 + 1);
-    at = find_unit(p, sp, u, lane);
-    const int start = u - at.at;
-    // units on both sides, and not cut in an earlier range
-    if (at.at <= sp.cost || range_of(sp, start + sp.cost) != c0) at.i = -1;
-    c1 = range_of(sp, start + sp.cost + at.U - 1);
-    first_slot = 2 * c0 + (range_start(sp, c0) < start);
+  const int chunk = f / rows, r = f - chunk * rows;
+  const int tile = r / R, rt = r - tile * R, jr = rt / G;
+  griddep_launch();  // the next launch may begin: it waits for this grid's end
+  TreeJoin at = {0, 0, 0, 0, 0, 0};
+  int c0 = blockIdx.x;
+  if (by_pair) {  // the lengths are older than the attention, which lets this launch begin once it waited itself
+    __shared__ int2 seqs[kSeqCache];  // every warp writes the same
+    const Split sp = make_split(p, seqs, lane);
+    int start = 0;
+    const Place f = find_pair(p, seqs, sp, blockIdx.x, lane, &start);
+    if (f.U > 0) {
+      c0 = range_of(sp, start + sp.cost);
+      at = {f.i, f.g, f.grp, 2 * c0 + (range_start(sp, c0) < start), range_of(sp, start + sp.cost + f.U - 1) - c0 + 1,
+            clamp_nodes(p, f.i)};
+    }
+    griddep_wait();  // every block: this grid's end has to imply the attention's
+  } else {
+    griddep_wait();
+    at = p.joins[blockIdx.x];
   }
-  const int i = [&] {
-    if (at.i < 0) return -1;
-    const int tile = r / kTileRows, rt = r % kTileRows;
-    const int tiles = p.part_rows > kTileRows ? 2 : 1;
-    const int jr = rt / G;
-    hq = rt - jr * G;
-    node = (at.grp * tiles + tile) * p.npt + jr;
-    return rt < R && node < clamp_nodes(p, at.i) ? at.i : -1;
-  }();
-  if (i < 0) {
-    if (anchor) griddep_wait();
-    return;
-  }
-  griddep_wait();
+  const int n = at.parts;
+  if (n < 2) return;
+  const int node = (at.grp * (rows / R) + tile) * p.npt + jr;
+  const bool real = chunk < HD / 4 && node < at.nodes;
   const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-  // maxima and sums of the parts, one a lane, so that the parts' loads wait for nothing
-  const int n = c1 - c0 + 1;
-  auto row_of = [&](int k) { return (long long)(k == 0 ? first_slot : 2 * (c0 + k)) * p.part_rows + r; };
-  float w[kMaxParts / 32], M = -FLT_MAX, L = 0.f;
-  {
-    float2 ml[kMaxParts / 32];
+  float M = -FLT_MAX, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, float l, const float4 &x) {
+    L = fmaf(w, l, L);
+    acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
+  };
+  auto grow = [&](float m) {
+    const float a = ex2((M - m) * sl2);
+    M = m;
+    L *= a;
+    acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+  };
+  if (real) {
+    constexpr int AT = 4;  // parts at a time
+    for (int k0 = sub; k0 < n; k0 += AT * WPR) {
+      float2 ml[AT];
+      float4 x[AT];
 #pragma unroll
-    for (int b = 0; b < kMaxParts / 32; ++b) {
-      const int k = 32 * b + lane;
-      ml[b] = k < n ? *reinterpret_cast<const float2 *>(p.part_ml + row_of(k) * 2) : make_float2(-FLT_MAX, 0.f);
-      M = fmaxf(M, ml[b].x);
-    }
-    M = warp_max(M);
-#pragma unroll
-    for (int b = 0; b < kMaxParts / 32; ++b) {
-      w[b] = 32 * b + lane < n ? exp2f((ml[b].x - M) * sl2) : 0.f;
-      L += 32 * b + lane < n ? ml[b].y * w[b] : 0.f;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int b = 0; b < kMaxParts / 32; ++b) {
-    const int to = min(32, n - 32 * b);
-#pragma unroll 8
-    for (int k = sub; k < to; k += WPR) {
-      const float *src = p.part_o + row_of(32 * b + k) * HD + lane * E;
-      const float a = __shfl_sync(0xffffffffu, w[b], k);
-      if constexpr (E == 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(src);
-        acc[0] = fmaf(a, x.x, acc[0]), acc[1] = fmaf(a, x.y, acc[1]);
-        acc[2] = fmaf(a, x.z, acc[2]), acc[3] = fmaf(a, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2 *>(src);
-        acc[0] = fmaf(a, x.x, acc[0]), acc[1] = fmaf(a, x.y, acc[1]);
+      for (int j = 0; j < AT; ++j) {
+        const int k = k0 + j * WPR;
+        const long long slot = k == 0 ? at.slot : 2 * (c0 + min(k, n - 1));
+        ml[j] = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
+        x[j] = reinterpret_cast<const float4 *>(p.part_o)[(slot * (HD / 4) + chunk) * rows + r];
       }
+      float m = M;
+#pragma unroll
+      for (int j = 0; j < AT; ++j) m = fmaxf(m, ml[j].x);
+      grow(m);
+#pragma unroll
+      for (int j = 0; j < AT; ++j)
+        if (k0 + j * WPR < n) add(ex2((ml[j].x - M) * sl2), ml[j].y, x[j]);
     }
   }
-  if (WPR > 1) {  // all of a block's warps have the same row
-#pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+  if constexpr (WPR > 1) {
+    __shared__ float4 part[kMergeWarps][32];
+    __shared__ float2 part_ml[kMergeWarps][32];
+    part[warp][lane] = acc;
+    part_ml[warp][lane] = make_float2(M, L);
     __syncthreads();
     if (sub > 0) return;
+    float m = M;
 #pragma unroll
-    for (int k = 1; k < WPR; ++k)
+    for (int k = 1; k < WPR; ++k) m = fmaxf(m, part_ml[warp + k][lane].x);
+    grow(m);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += part[k][lane * E + e];
+    for (int k = 1; k < WPR; ++k) {
+      const float2 ml = part_ml[warp + k][lane];
+      add(ex2((ml.x - M) * sl2), ml.y, part[warp + k][lane]);
+    }
   }
+  if (!real) return;
   const float inv = 1.0f / L;
-  uint16_t *dst = p.o + (((long long)i * p.m + node) * p.Hq + at.g * G + hq) * HD + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  uint16_t *dst = p.o + (((long long)at.i * p.m + node) * p.Hq + at.g * G + rt - jr * G) * HD + chunk * 4;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 template <int HD, int WPR>
-cudaError_t launch_merge(const AttnTreeParams &p, int rows, cudaStream_t s) {
+cudaError_t launch_merge(const AttnTreeParams &p, cudaStream_t s) {
   // the attention's split of the SM's memory, so that this grid's CTAs may stand by next to it
   static const cudaError_t configured = cudaFuncSetAttribute(
       attn_tree_merge_kernel<HD, WPR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (configured != cudaSuccess) return configured;
-  constexpr int per = kMergeWarps / WPR;
-  return launch_pdl(attn_tree_merge_kernel<HD, WPR>, dim3(p.grid, (rows + per - 1) / per), dim3(kMergeWarps * 32), 0, s,
-                    p);
+  constexpr int per = kMergeWarps / WPR * 32;
+  const dim3 grid(std::min(p.grid, p.nb * p.Hkv * p.groups), (p.part_rows * (HD / 4) + per - 1) / per);
+  return launch_pdl(attn_tree_merge_kernel<HD, WPR>, grid, dim3(kMergeWarps * 32), 0, s, p);
 }
 
 template <int HD, int NQ, bool TWO>
@@ -980,14 +1042,13 @@ cudaError_t launch(const AttnTreeParams &p, cudaStream_t s) {
   if (configured != cudaSuccess) return configured;
   cudaError_t e = launch_pdl(attn_tree_kernel<HD, NQ, TWO>, dim3(p.grid), dim3(Roles<NQ>::THREADS), C::SMEM, s, p);
   if (e != cudaSuccess) return e;
-  const int rows = TWO ? 2 * kTileRows : p.npt * (p.Hq / p.Hkv);
-  return rows <= 16 ? launch_merge<HD, kMergeWarps>(p, rows, s) : launch_merge<HD, 1>(p, rows, s);
+  return p.part_rows <= 16 ? launch_merge<HD, kMergeWarps>(p, s) : launch_merge<HD, 1>(p, s);
 }
 
 template <int HD>
 cudaError_t launch_form(const AttnTreeParams &p, cudaStream_t s) {
   const int R = p.npt * (p.Hq / p.Hkv);
-  if (p.part_rows > kTileRows) return launch<HD, 4, true>(p, s);
+  if (p.part_rows > R) return launch<HD, 4, true>(p, s);
   if (R > 64) return launch<HD, 4, false>(p, s);
   return R > 32 ? launch<HD, 2, false>(p, s) : launch<HD, 1, false>(p, s);
 }
@@ -1001,12 +1062,12 @@ void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows) {
   if (m <= most) {
     *npt = m;
     *groups = 1;
-    *part_rows = kTileRows;
+    *part_rows = m * G;
     return;
   }
   *groups = (m + 2 * most - 1) / (2 * most);
   *npt = (m + 2 * *groups - 1) / (2 * *groups);
-  *part_rows = 2 * kTileRows;
+  *part_rows = 2 * *npt * G;
 }
 
 cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s) {

@@ -130,6 +130,7 @@ struct WsLayout {
   size_t pre = 0, h = 0;                       // ctx_project
   size_t x = 0, u = 0, qkv = 0, o = 0, act = 0, xb = 0, corr = 0, ss = 0;  // draft_block
   size_t apart = 0, aml = 0;                   // attention partials (dflash_attention_tree's too)
+  size_t joins = 0;                            // and the pairs that it has partials of
   size_t tk_vals = 0, tk_ids = 0;              // LM head top-k partial lists
   size_t sel_e = 0, sel_ab = 0, sel_g = 0, sel_t = 0;  // selector
   size_t lg_part = 0;                          // slices' best of dflash_logits_adjust
@@ -191,12 +192,11 @@ void plan_workspace(dflash_handle_s *h) {
   L.corr = take((c.flags & DFLASH_FLAG_CONV) ? (size_t)Mb * 2 * (c.D / c.conv_group) * 4 : 0);
   L.apart_ctas = apart_max;
   // a tree's attention writes two slots a CTA of up to two tiles of query rows
-  int npt = 0, groups = 0, tree_rows = 0;
-  attention_tree_plan(kTreeMax, c.Hq / c.Hkv, &npt, &groups, &tree_rows);
-  const size_t part_rows = std::max(apart_max * rows_attn, (size_t)2 * h->num_sms * tree_rows);
+  const size_t part_rows = std::max(apart_max * rows_attn, (size_t)2 * h->num_sms * kTreePartRows);
   L.apart_bytes = part_rows * c.hd * 4;
   L.apart = take(L.apart_bytes);
   L.aml = take(part_rows * 2 * 4);
+  L.joins = take((size_t)kTreeCtas * sizeof(TreeJoin));
   const int ranges = h->num_sms;
   L.tk_vals = take((size_t)ranges * Ml * c.k_top * 4);
   L.tk_ids = take((size_t)ranges * Ml * c.k_top * 4);
@@ -1329,6 +1329,7 @@ int dflash_attention_tree(dflash_handle_t h, int nb, int layer, int m, const voi
   p.o = static_cast<uint16_t *>(out_o);
   p.part_o = w.at<float>(h->ws.apart);
   p.part_ml = w.at<float>(h->ws.aml);
+  p.joins = w.at<TreeJoin>(h->ws.joins);
   p.nb = nb;
   p.m = m;
   p.Hq = c.Hq;

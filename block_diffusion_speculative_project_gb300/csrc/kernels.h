@@ -329,7 +329,14 @@ cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 // ---------------------------------------------------------------- trees of drafted tokens
 
 constexpr int kTreeMax = 64;   // nodes of a tree (a row's ancestors are the bits of 64)
-constexpr int kTreeCtas = 160;  // most CTAs of a tree's attention, and so parts of a pair
+constexpr int kTreeCtas = 160;      // most CTAs of a tree's attention
+constexpr int kTreePartRows = 256;  // most rows of a slot of its partials
+
+// A pair that several CTAs of a tree's attention share: where it belongs, the slot of its first part, parts (below 2:
+// none), rows of its tree.
+struct TreeJoin {
+  int i, g, grp, slot, parts, nodes;
+};
 
 // Attention of a tree's nodes over the bf16 caches (attention_tree.cu).
 struct AttnTreeParams {
@@ -339,8 +346,9 @@ struct AttnTreeParams {
   const int *n_rows;         // [nb] or null: m
   const int *ctx_len;        // [nb]
   uint16_t *o;               // bf16 [nb][m][Hq][hd]
-  float *part_o;             // [2 * grid slots][part_rows][hd] unnormalised partial outputs
+  float *part_o;             // [2 * grid slots][hd / 4][part_rows][4] unnormalised partial outputs
   float *part_ml;            // [2 * grid slots][part_rows][2] (running maximum, running sum)
+  TreeJoin *joins;           // [grid] by the CTA that has the first part
   int nb, m, Hq, Hkv, hd, Cmax;
   int npt, groups, part_rows;  // nodes of a tile, groups of tiles of a kv head, rows of a slot
   int pair_cost;             // what the split counts for a pair besides its units (set by the launch)
