@@ -7,17 +7,22 @@
 // (KV injection and the attention equations of "DFlash 投机解码：块扩散草稿与 KV 注入", 二; the pages verify
 // one path, a tree holds several). A chain of nodes is causal attention, one node the decode step.
 //
-// Bound: the visible K and V rows, read once; at 256 query rows a kv head as much tensor time. So
-// query rows R = (Hq/Hkv) * m of a kv head are the rows of M = 128 MMAs, in one of two forms:
+// Bound: the visible K and V rows, read once. Query rows R = (Hq/Hkv) * m of a kv head are the rows of M = 128 MMAs,
+// in one of two forms:
 //   one tile (R <= 128)   two halves of softmax warps take units of 64 keys in turn, each with its own
-//                         running maximum, sum and O, joined at the end of a segment
+//                         running maximum, sum and O, joined at the end of a segment. 64 sequences of 1024 to 8191
+//                         rows, 32 heads over 8: one token 178 us and 6.8 TB/s, trees of 16 nodes 193 us and 6.3 TB/s.
 //   two tiles (R > 128)   both halves work on every unit, each for its own tile of up to 128 rows: K and
-//                         V are read once for 256 rows. More rows take further groups of two tiles.
+//                         V are read once for 256 rows. More rows take further groups of two tiles. Bound by the
+//                         tensor core: an MMA of 128 rows takes some 76 cycles at 64 keys (S) as at 128 channels
+//                         (O), 24 a unit, 1824 cycles where the loads take 1400. 262147 rows under 64 nodes: 220 us,
+//                         1.25 PFLOP/s; with each tile's rows in a CTA of its own, K and V read twice, 314 us.
 // A (sequence, kv head, group) is a pair; the visible units of all pairs are cut into equal ranges, one
-// per CTA (one CTA per SM). The run of one pair inside a range is a segment: it writes the output, or if
-// the pair goes on in another CTA an unnormalised partial (only a range's first and last segment can
-// be one: two slots a CTA), which attn_tree_merge_kernel joins in CTA order. With a window a pair's units
-// are those of the sinks, then those from the root's first visible row on.
+// per CTA (one CTA per SM; two one-tile CTAs an SM, each with half the stages: 206 us for the trees above).
+// The run of one pair inside a range is a segment: it writes the output, or if the pair goes on in another
+// CTA an unnormalised partial (only a range's first and last segment can be one: two slots a CTA), which
+// attn_tree_merge_kernel joins in CTA order. With a window a pair's units are those of the sinks, then those
+// from the root's first visible row on.
 //
 // Masks: a unit that every row sees whole takes none. The others (the window's edge, the end of the
 // sinks, the tree's own rows) get a 64-bit mask a row from its node's line of ancestors. Values in
@@ -25,10 +30,10 @@
 // cleaner) zeroes such values before the product sees them and notes their keys, and the rows that see
 // such a key get a NaN probability for it.
 //
-// One CTA: TMA producer (Q tiles of the segment; K and V of a unit per stage), S issuer (S = Q K^T into
-// buffer step % 2, the first tile's Q from tensor memory), PV issuer (O_half += P V, P from tensor memory),
-// the cleaner, and the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32,
-// rounds P to bf16 (2^-9 of each probability, as the values have) and rescales O only when the row's
+// One CTA: TMA producer (K and V of a unit per stage, Q tiles of the segments), S issuer (S = Q K^T into buffer
+// step % 2, the first tile's Q from tensor memory), PV issuer (O_half += P V, P from tensor memory), the cleaner, and
+// the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32, rounds P to bf16
+// (by up to 2^-9 of each probability, the type of the values that it multiplies) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
 #include <algorithm>
 #include <cfloat>
@@ -65,7 +70,8 @@ struct Cfg {
   static constexpr int ATOM_KV = kKeys * 128;
   static constexpr int KV_TILE = ATOMS * ATOM_KV;
   static constexpr int STAGE = 2 * KV_TILE;        // K, then V
-  // 160 to 192 KB of K and V on the way (64 single tokens: 178 us, with 160 KB 184)
+  // K and V on the way, 160 to 192 KB. 64 single tokens of 128 channels: 178 us, with 160 KB 184, with K and V in
+  // places of their own (K's free sooner) 182; of 64 channels 100.5 us with 12 stages, with 8 102.6.
   static constexpr int STAGES = HD == 64 ? (TWO ? 10 : 12) : TWO ? 5 : 6;
   static constexpr int BARS = HD == 64 ? 1024 : 512;  // bytes for the barriers
   static constexpr int OFF_KV = TILES * Q_TILE;
@@ -519,7 +525,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       int q_loads = 1, loads = 0, st = 0;
       uint32_t ph = 0;
       for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
-        // a lane finds the cache row of a unit, so that 32 pages are looked up in the time of one
+        // a lane finds the cache row of a unit: 32 pages are looked up in the time of one (trees of 16 nodes
+        // 192.8 us, by one thread four at a time 193.4)
         auto row_of = [&](int u) {
           if (u >= e.u1) return 0;
           const int base = unit_base(e.s, u);
@@ -681,8 +688,9 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t o_mine = trow + C::O_COL + half * HD;
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-    // The first Q tile of a segment to tensor memory, where the products read it at full rate (from shared
-    // memory an S of 64 keys takes twice as long): by half 1, or with two tiles by half 0, whose rows they are.
+    // The first Q tile of a segment to tensor memory, by half 1, or with two tiles by half 0, whose rows they are. Its
+    // place in shared memory is free for the next segment's then, and the products read it faster (262147 rows under
+    // 64 nodes: 233 us, from shared memory 240).
     const bool copies = half == (TWO ? 0 : 1);
     auto copy_q = [&](int index) {
       bool good = index == 0 || mbar_wait_warp(q_free, (index - 1) & 1, p.max_spin);
@@ -849,8 +857,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       tc_fence_after();
       if (threadIdx.x == 0 && e.u0 == 0 && !whole) {  // the pair's first part: what the merge has to know
         const Split sp = {0, 0, sched[6], sched[7], e.cost};
-        p.joins[blockIdx.x] = {e.i, e.g, e.grp, slot, range_of(sp, e.pos + e.cost + e.s.U - 1) - static_cast<int>(blockIdx.x) + 1,
-                               e.s.n};
+        const int last = range_of(sp, e.pos + e.cost + e.s.U - 1);
+        p.joins[blockIdx.x] = {e.i, e.g, e.grp, slot, last - static_cast<int>(blockIdx.x) + 1, e.s.n};
       }
       if (warp_real) {
         const float inv = 1.0f / L;
@@ -882,8 +890,10 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
                              pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
                              pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
           } else {
-            // rows side by side, four channels each: a warp's store is a piece of 512 bytes
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o) + ((long long)slot * (HD / 4) + cc / 4) * p.part_rows + prow;
+            // rows side by side, four channels each: a warp's store is four lines, with a row's channels side by side
+            // it was 32 (64 x 64 rows 293 us, so 286)
+            float4 *dst =
+                reinterpret_cast<float4 *>(p.part_o) + ((long long)slot * (HD / 4) + cc / 4) * p.part_rows + prow;
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               dst[v * p.part_rows] = make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
@@ -928,10 +938,12 @@ __device__ __forceinline__ Place find_pair(const AttnTreeParams &p, const int2 *
   return f;
 }
 
-// Joins the partials of a pair that several CTAs share. Where there are no more pairs than CTAs block x stands for pair
-// x, and finds its parts by itself while it waits for the attention; else it has the pair whose first part is CTA x's,
-// from that CTA's word. A lane has four channels of a row, as the partials lie; WPR warps share 32 lanes' parts where
-// they are what it waits for.
+// Joins the partials of a pair that several CTAs share. Where there are no more pairs than CTAs block x stands
+// for pair x, and finds its parts by itself while it waits for the attention (one token: 9.4 us, from the CTAs'
+// words 9.9; 262147 rows under 64 nodes, few pairs of many parts: 220, and 259). Else it has the pair whose first
+// part is CTA x's, from that CTA's word, which spares some 2000 blocks the search (64 x 64 rows 277 us, with it
+// 287). A lane has four channels of a row, as the partials lie. Bound by the latency of the parts' loads: with up
+// to 16 rows eight warps share a lane's parts (WPR).
 constexpr int kMergeWarps = 8;
 
 template <int HD, int WPR>
@@ -1020,7 +1032,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
   if (!real) return;
   const float inv = 1.0f / L;
   uint16_t *dst = p.o + (((long long)at.i * p.m + node) * p.Hq + at.g * G + rt - jr * G) * HD + chunk * 4;
-  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2 *>(dst) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 template <int HD, int WPR>
@@ -1071,9 +1084,10 @@ void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows) {
 }
 
 cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s) {
-  // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 198.7 us
-  // without, 195.2 with 4, 64 x 64 rows 321, 293 with 7; a unit of 64 channels takes half the time.
-  p.pair_cost = (p.npt * (p.Hq / p.Hkv) > 64 ? 7 : 4) * (128 / p.hd);
+  // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 194.7 us
+  // without, 191.3 with 4, 193.0 with 12; 64 x 64 rows (two tiles) 299.7, with 4 278.9, with 6 273.1, with 12 279.2.
+  // A unit of 64 channels takes half the time.
+  p.pair_cost = (p.part_rows > p.npt * (p.Hq / p.Hkv) ? 6 : 4) * (128 / p.hd);
   switch (p.hd) {
     case 64: return launch_form<64>(p, s);
     case 128: return launch_form<128>(p, s);

@@ -189,6 +189,66 @@ def test_a_long_context_over_every_sm():
         check_attention(t, m, queries(1, m, 8, 128, 3), trees(1, m, 3), None, [20480 - m], window, 3)
 
 
+# Hq, Hkv, hd, sequences, nodes, window: many units a CTA, so that ranges begin and end anywhere in a pair and before its
+# first unit; more pairs than CTAs, and fewer; one tile, two, two groups of two
+@pytest.mark.parametrize("Hq,Hkv,hd,nb,m,window", [
+    (16, 8, 64, 24, 20, 0), (32, 8, 128, 20, 64, 0), (32, 8, 64, 12, 64, 0), (64, 8, 64, 10, 64, 0), (8, 8, 128, 22, 9, 1500),
+    (24, 8, 128, 20, 43, 2000), (16, 8, 128, 9, 64, 0)])
+def test_ranges_of_many_units(Hq, Hkv, hd, nb, m, window):
+    t = Target(Hq, Hkv, hd, Cmax=4096, nb=nb, paged=True, seed=m + nb)
+    t.ws[256:].fill_(0xFF)   # behind the status word a workspace may hold anything
+    rng = np.random.default_rng(nb)
+    ctx, n = rng.integers(1200, 4096 - m, nb), rng.integers(1, m + 1, nb)
+    ctx[[1, nb - 2]], n[[0, nb // 2, nb - 1]] = (0, 64), 0
+    check_attention(t, m, queries(nb, m, Hq, hd, 4), trees(nb, m, 4), n.tolist(), ctx.tolist(), window, 70)
+
+
+@pytest.mark.parametrize("Hq,m,paged", [(8, 1, True), (32, 16, True), (32, 25, False), (32, 33, True)])
+def test_segments_of_many_units(Hq, m, paged):
+    """Some 60 units of one pair in a row: every ring goes round many times, pages are looked up more than once."""
+    nb = 8
+    t = Target(Hq, 8, 128, Cmax=9216, nb=nb, paged=paged, seed=m)
+    ctx, n = [8960 - 64 * i for i in range(nb)], [m - i % m for i in range(nb)]
+    check_attention(t, m, queries(nb, m, Hq, 128, 4), trees(nb, m, 4), n, ctx, seqs=[0, 3, 7])
+
+
+def test_graphs_of_one_workspace_and_handles_at_once():
+    """Two captured calls that share a workspace, replayed in turn; two handles, each on a stream of its own, at once."""
+    nb = 6
+    ts = [Target(32, 8, 128, Cmax=2048, nb=nb, paged=True, seed=s) for s in (1, 2)]
+    calls = []   # shape, inputs, the output alone
+    for m, window in ((64, 0), (7, 300)):
+        args = (m, queries(nb, m, 32, 128, m), i32(trees(nb, m, m)), i32([m - k for k in range(nb)]),
+                i32([1900 - 300 * k for k in range(nb)]), window, 4)
+        calls.append((args, [t.attend(*args) for t in ts]))
+    torch.cuda.synchronize()
+    graphs = []
+    for args, want in calls:
+        out, g = torch.empty_like(want[0]), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ts[0].attend(*args, out=out)
+        graphs.append((g, out, want[0]))
+    for k in range(6):
+        for g, out, want in graphs[::1 if k % 2 else -1]:
+            out.fill_(7)
+            g.replay()
+    for _, out, want in graphs:
+        assert torch.equal(out, want)
+    streams = [torch.cuda.Stream() for _ in ts]
+    outs = [[torch.full_like(w[k], 7.0) for _, w in calls] for k in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                for (args, _), out in zip(calls, outs[k]):
+                    ts[k].attend(*args, out=out)
+    torch.cuda.synchronize()
+    for k, t in enumerate(ts):
+        assert t.status() == 0
+        for (_, want), out in zip(calls, outs[k]):
+            assert torch.equal(out, want[k])
+
+
 def test_rows_that_nobody_sees_may_hold_anything():
     """NaN and infinities in keys and values outside the window, behind the tree and in the nodes of other branches."""
     nb, m, window, sinks = 3, 16, 100, 4
