@@ -35,7 +35,6 @@
 // the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32, rounds P to bf16
 // (by up to 2^-9 of each probability, the type of the values that it multiplies) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
-#include <algorithm>
 #include <cfloat>
 
 #include "common.cuh"
@@ -491,10 +490,13 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       sched[8] = sp.cost;
     }
   }
-  if (threadIdx.x == 0) p.joins[blockIdx.x].parts = 0;
+  // The merge's words: of each pair, by the CTA that has its first unit, or of a pair that this CTA has the first part of
+  if (threadIdx.x == 0 && !p.by_pair) p.joins[blockIdx.x].parts = 0;
   if (warp == Ro::CLEAN && blockIdx.x == 0) {
     bool bad = false;  // lengths out of range, reported once a launch
     for (int i = lane; i < p.nb; i += 32) {
+      if (p.by_pair && clamp_nodes(p, i) == 0)  // pairs without units
+        for (int k = 0; k < p.Hkv * p.groups; ++k) p.joins[i * p.Hkv * p.groups + k].parts = 0;
       const int n = p.n_rows ? p.n_rows[i] : p.m, c = p.ctx_len[i];
       bad |= n < 0 || n > p.m || c < 0 || c > p.max_ctx || c > p.Cmax - clamp_nodes(p, i);
     }
@@ -855,10 +857,10 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         L = (h0.y < 0.f ? 0.f : h0.y * a0) + (h1.y < 0.f ? 0.f : h1.y * a1);
       }
       tc_fence_after();
-      if (threadIdx.x == 0 && e.u0 == 0 && !whole) {  // the pair's first part: what the merge has to know
+      if (threadIdx.x == 0 && e.u0 == 0 && (p.by_pair || !whole)) {  // what the merge has to know
         const Split sp = {0, 0, sched[6], sched[7], e.cost};
-        const int last = range_of(sp, e.pos + e.cost + e.s.U - 1);
-        p.joins[blockIdx.x] = {e.i, e.g, e.grp, slot, last - static_cast<int>(blockIdx.x) + 1, e.s.n};
+        const int c0 = blockIdx.x, last = range_of(sp, e.pos + e.cost + e.s.U - 1);
+        p.joins[p.by_pair ? (e.i * p.Hkv + e.g) * p.groups + e.grp : c0] = {e.i, e.g, e.grp, c0, slot, last - c0 + 1, e.s.n};
       }
       if (warp_real) {
         const float inv = 1.0f / L;
@@ -938,17 +940,16 @@ __device__ __forceinline__ Place find_pair(const AttnTreeParams &p, const int2 *
   return f;
 }
 
-// Joins the partials of a pair that several CTAs share. Where there are no more pairs than CTAs block x stands
-// for pair x, and finds its parts by itself while it waits for the attention (one token: 9.4 us, from the CTAs'
-// words 9.9; 262147 rows under 64 nodes, few pairs of many parts: 220, and 259). Else it has the pair whose first
-// part is CTA x's, from that CTA's word, which spares some 2000 blocks the search (64 x 64 rows 277 us, with it
-// 287). A lane has four channels of a row, as the partials lie. Bound by the latency of the parts' loads: with up
-// to 16 rows eight warps share a lane's parts (WPR).
+// Joins the partials of a pair that several CTAs share: block x those of pair x, or where there are more pairs than
+// CTAs of the pair whose first part CTA x has, from the attention's word about it, which spares some 2000 blocks the
+// search for it (64 x 64 rows 277 us, with it 287). A lane has four channels of a row, as the partials lie. Bound by the
+// latency of the parts' loads: with up to 16 rows eight warps share a lane's parts (WPR), and the blocks, which are few
+// then and may stand by next to the attention, find their pair's parts while they wait (one token 9.4 us, by its word
+// 9.9).
 constexpr int kMergeWarps = 8;
 
 template <int HD, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const __grid_constant__ AttnTreeParams p) {
-  const bool by_pair = p.nb * p.Hkv * p.groups <= p.grid;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, R = p.npt * G, rows = p.part_rows;
   const int f = (blockIdx.y * (kMergeWarps / WPR) + warp / WPR) * 32 + lane;  // four channels of a slot
@@ -956,24 +957,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
   const int chunk = f / rows, r = f - chunk * rows;
   const int tile = r / R, rt = r - tile * R, jr = rt / G;
   griddep_launch();  // the next launch may begin: it waits for this grid's end
-  TreeJoin at = {0, 0, 0, 0, 0, 0};
-  int c0 = blockIdx.x;
-  if (by_pair) {  // the lengths are older than the attention, which lets this launch begin once it waited itself
+  TreeJoin at = {0, 0, 0, 0, 0, 0, 0};
+  if (WPR > 1 && p.by_pair) {
+    // the lengths are older than the attention, which lets this launch begin once it waited itself
     __shared__ int2 seqs[kSeqCache];  // every warp writes the same
     const Split sp = make_split(p, seqs, lane);
     int start = 0;
     const Place f = find_pair(p, seqs, sp, blockIdx.x, lane, &start);
     if (f.U > 0) {
-      c0 = range_of(sp, start + sp.cost);
-      at = {f.i, f.g, f.grp, 2 * c0 + (range_start(sp, c0) < start), range_of(sp, start + sp.cost + f.U - 1) - c0 + 1,
-            clamp_nodes(p, f.i)};
+      const int c0 = range_of(sp, start + sp.cost), last = range_of(sp, start + sp.cost + f.U - 1);
+      at = {f.i, f.g, f.grp, c0, 2 * c0 + (range_start(sp, c0) < start), last - c0 + 1, clamp_nodes(p, f.i)};
     }
     griddep_wait();  // every block: this grid's end has to imply the attention's
   } else {
     griddep_wait();
     at = p.joins[blockIdx.x];
+    // an attention whose waits ran out leaves words of before
+    if (p.by_pair && (at.c0 < 0 || at.parts > p.grid - at.c0 || (at.slot & ~1) != 2 * at.c0 || at.i < 0 || at.i >= p.nb || at.g < 0 ||
+        at.g >= p.Hkv || at.grp < 0 || at.grp >= p.groups || at.nodes > p.m))
+      return;
   }
-  const int n = at.parts;
+  const int n = at.parts, c0 = at.c0;
   if (n < 2) return;
   const int node = (at.grp * (rows / R) + tile) * p.npt + jr;
   const bool real = chunk < HD / 4 && node < at.nodes;
@@ -1043,7 +1047,7 @@ cudaError_t launch_merge(const AttnTreeParams &p, cudaStream_t s) {
       attn_tree_merge_kernel<HD, WPR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (configured != cudaSuccess) return configured;
   constexpr int per = kMergeWarps / WPR * 32;
-  const dim3 grid(std::min(p.grid, p.nb * p.Hkv * p.groups), (p.part_rows * (HD / 4) + per - 1) / per);
+  const dim3 grid(p.by_pair ? p.nb * p.Hkv * p.groups : p.grid, (p.part_rows * (HD / 4) + per - 1) / per);
   return launch_pdl(attn_tree_merge_kernel<HD, WPR>, grid, dim3(kMergeWarps * 32), 0, s, p);
 }
 
@@ -1087,6 +1091,7 @@ cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s) {
   // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 194.7 us
   // without, 191.3 with 4, 193.0 with 12; 64 x 64 rows (two tiles) 299.7, with 4 278.9, with 6 273.1, with 12 279.2.
   // A unit of 64 channels takes half the time.
+  p.by_pair = p.nb * p.Hkv * p.groups <= p.grid;
   p.pair_cost = (p.part_rows > p.npt * (p.Hq / p.Hkv) ? 6 : 4) * (128 / p.hd);
   switch (p.hd) {
     case 64: return launch_form<64>(p, s);

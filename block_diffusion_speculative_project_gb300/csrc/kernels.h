@@ -332,10 +332,10 @@ constexpr int kTreeMax = 64;   // nodes of a tree (a row's ancestors are the bit
 constexpr int kTreeCtas = 160;      // most CTAs of a tree's attention
 constexpr int kTreePartRows = 256;  // most rows of a slot of its partials
 
-// A pair that several CTAs of a tree's attention share: where it belongs, the slot of its first part, parts (below 2:
-// none), rows of its tree.
+// A pair that several CTAs of a tree's attention share: where it belongs, the CTA and slot of its first part, parts (below
+// 2: none), rows of its tree.
 struct TreeJoin {
-  int i, g, grp, slot, parts, nodes;
+  int i, g, grp, c0, slot, parts, nodes;
 };
 
 // Attention of a tree's nodes over the bf16 caches (attention_tree.cu).
@@ -348,9 +348,10 @@ struct AttnTreeParams {
   uint16_t *o;               // bf16 [nb][m][Hq][hd]
   float *part_o;             // [2 * grid slots][hd / 4][part_rows][4] unnormalised partial outputs
   float *part_ml;            // [2 * grid slots][part_rows][2] (running maximum, running sum)
-  TreeJoin *joins;           // [grid] by the CTA that has the first part
+  TreeJoin *joins;           // [grid] by the pair, or of more pairs by the CTA that has the first part
   int nb, m, Hq, Hkv, hd, Cmax;
   int npt, groups, part_rows;  // nodes of a tile, groups of tiles of a kv head, rows of a slot
+  int by_pair;               // no more pairs than CTAs (set by the launch)
   int pair_cost;             // what the split counts for a pair besides its units (set by the launch)
   int layer_row0;            // first cache row of the layer
   int window, sinks;         // window 0: none
