@@ -63,7 +63,7 @@ __device__ __forceinline__ float adjust(float x, int count, int drafted, const R
 // RPC rows at a time, S stages of a tile of theirs in flight. VEC: rows of 16-byte pieces, a lane's four
 // values side by side; else they lie 32 apart and are loaded as they are needed. MASK: the rows have masks.
 template <int RPC, int S, bool VEC, bool MASK>
-__global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) logits_adjust_kernel(const LogitsParams p) {
+__global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : 3) logits_adjust_kernel(const LogitsParams p) {
   constexpr int T = 32 * kWarps;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ int s_token[kTreeMax];
@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) 
   __shared__ unsigned long long s_line[kTreeMax];  // drafted nodes from a node up
   __shared__ float s_val[kTreeMax][kWarps];
   __shared__ int s_id[kTreeMax][kWarps];
-  __shared__ uint32_t marked[kWarps * 32];         // biased or drafted
+  __shared__ uint32_t marked[kWarps * 32];         // biased tokens
+  __shared__ uint32_t drafted[kWarps * 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *ring = reinterpret_cast<float *>(dyn) + warp * (S * RPC * 128) + (VEC ? 4 : 1) * lane;
   int *hkey = reinterpret_cast<int *>(dyn + kWarps * S * RPC * 512);  // [hash]: id, -1 free
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) 
   const int v0 = slice * p.chunk, v1 = min(p.V, v0 + p.chunk);
   const bool special = p.n_bias > 0 || p.parent != nullptr;
   if (special) {
-    marked[tid] = 0;
+    marked[tid] = drafted[tid] = 0;
     for (int e = tid; e < p.hash; e += T) {
       hkey[e] = -1;
       hcount[e] = 0;
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) 
         for (int a = j; s_parent[a] >= 0; a = s_parent[a]) line |= 1ull << a;
         s_line[j] = line;
         const int id = s_token[j];
-        if (line >> j & 1 && id >= v0 && id < v1) atomicOr(&marked[(id - v0) >> 5], 1u << ((id - v0) & 31));
+        if (line >> j & 1 && id >= v0 && id < v1) atomicOr(&drafted[(id - v0) >> 5], 1u << ((id - v0) & 31));
       }
     __syncthreads();
     // An id that comes once has its bias; a warp together adds up what another id has, in the list's order,
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) 
       }
     }
     __syncthreads();
-    if (lane < 4 * wt) listed |= marked[warp * wt * 4 + lane];
+    if (lane < 4 * wt) listed |= marked[warp * wt * 4 + lane] | drafted[warp * wt * 4 + lane];
   }
 
   // ---- rows
@@ -360,19 +361,17 @@ __global__ void __launch_bounds__(32 * kWarps, RPC == 1 ? 4 : RPC == 2 ? 3 : 2) 
       const int count = counts ? __ldg(counts + e) : 0;
       float add = 0.f;
       unsigned long long nodes = 0;  // with this token
-      if (special && marked[(id - v0) >> 5] >> bit & 1) {
-        if (p.parent)
-          for (int a = 1; a < n; ++a) nodes |= static_cast<unsigned long long>(s_token[a] == id) << a;
-        if (p.n_bias) {
-          uint32_t h = id_hash(id, hmask);
-          while (hkey[h] != -1 && hkey[h] != id) h = (h + 1) & hmask;
-          if (hkey[h] != -1) add = hsum[h];
-        }
+      if (p.parent && drafted[(id - v0) >> 5] >> bit & 1)
+        for (int a = 1; a < n; ++a) nodes |= static_cast<unsigned long long>(s_token[a] == id) << a;
+      if (p.n_bias && marked[(id - v0) >> 5] >> bit & 1) {
+        uint32_t h = id_hash(id, hmask);
+        while (hkey[h] != id) h = (h + 1) & hmask;
+        add = hsum[h];
       }
 #pragma unroll
       for (int r = 0; r < RPC; ++r) {
-        const int drafted = nodes ? __popcll(s_line[min(j + r, j1 - 1)] & nodes) : 0;
-        const float v = !MASK || mw[r] >> bit & 1 ? adjust(z[r], count, drafted, rules) + add : -INFINITY;
+        const int again = nodes ? __popcll(s_line[min(j + r, j1 - 1)] & nodes) : 0;
+        const float v = !MASK || mw[r] >> bit & 1 ? adjust(z[r], count, again, rules) + add : -INFINITY;
         if (y) y[min(j + r, j1 - 1) * p.ldy + e] = v;
         if (v > top[r]) {  // places rise
           top[r] = v;
@@ -495,22 +494,24 @@ cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s) {
   auto aligned = [](const void *q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 4 == 0; };
   const bool vec = aligned(p.x, p.ldx) && (!p.y || aligned(p.y, p.ldy)) && (!p.counts || aligned(p.counts, p.V)) &&
                    p.V % 4 == 0;
-  // A warp of 1024 tokens for all of a sequence's rows where that gives each SM eight CTAs, two rows at a time
-  // (1024 rows of 151936: 236 us; one at a time 240, four 251). Else about eight CTAs a SM, four rows or
-  // more each (64 rows of one sequence 27 us, in warps of 256 tokens for 16 rows 32), and where those are
-  // less than two a SM, fewer tokens a warp (16 rows: 12 us, with 1024 tokens 14; one row 6, with 1024 9).
-  auto slices = [&](int tiles) { return ((long long)p.V + tiles * 128 * kWarps - 1) / (tiles * 128 * kWarps); };
-  if (p.nb * slices(kTiles) >= 8LL * num_sms)
-    return p.m > 1 ? launch_adjust<2, 3>(p, vec, kTiles, p.m, s) : launch_adjust<1, 4>(p, vec, kTiles, 1, s);
-  const int at_once = p.m >= 4 ? 4 : p.m > 1 ? 2 : 1;
-  const int groups = (p.m + at_once - 1) / at_once;
-  const long long per = std::max<long long>(1, p.nb * slices(kTiles) * groups / (8 * num_sms));
-  const int rows = at_once * static_cast<int>(std::min<long long>(per, groups));
+  // Two rows at a time, a warp of 1024 tokens for as many rows of a sequence as leave two CTAs a SM (1024 rows of
+  // 151936: 236 us, one at a time 240, four 251; 8 x 16 rows 40.6, in 1216 CTAs 48), six where values come one by one
+  // (1024 rows of 32003: 62 us, with two 81). Fewer tokens a warp where there are fewer CTAs, or tokens (16 rows:
+  // 11.7 us, with 1024 tokens 12.4; one row 6, with 1024 9).
+  const int at_once = p.m > 1 ? 2 : 1;
   int tiles = kTiles;
-  while (tiles > 1 && p.nb * slices(tiles) * ((p.m + rows - 1) / rows) < 7LL * num_sms / 4 &&
-         slices(tiles / 2) <= kLogitSlots)
+  auto slices = [&] { return ((long long)p.V + tiles * 128 * kWarps - 1) / (tiles * 128 * kWarps); };
+  while (tiles > 1 && slices() == 1 && tiles / 2 * 128 * kWarps >= p.V) tiles /= 2;
+  const long long want = (vec ? 2LL : 6LL) * num_sms, have = p.nb * slices();
+  const int parts = static_cast<int>(std::min<long long>(p.m, (want + have - 1) / have));
+  const int rows = ((p.m + parts - 1) / parts + at_once - 1) / at_once * at_once;
+  while (tiles > 1 && p.nb * slices() * ((p.m + rows - 1) / rows) < 7LL * num_sms / 4) {
     tiles /= 2;
-  if (at_once == 4) return launch_adjust<4, 2>(p, vec, tiles, rows, s);
+    if (slices() > kLogitSlots) {
+      tiles *= 2;
+      break;
+    }
+  }
   return at_once == 2 ? launch_adjust<2, 3>(p, vec, tiles, rows, s) : launch_adjust<1, 4>(p, vec, tiles, rows, s);
 }
 
