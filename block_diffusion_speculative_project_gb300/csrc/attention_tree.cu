@@ -356,8 +356,8 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Warp-collective: zeroes a unit's values (ATOMS pieces of 64 rows of 128 bytes side by side) that are not finite, and its
-// rows from nv on; returns the keys that had such values. One look at the magnitudes first: they hardly ever have.
+// Warp-collective: zeroes a unit's values (ATOMS pieces of 64 rows of 128 bytes side by side) that are not finite, and
+// its rows from nv on; returns the keys that had such values. One look at the magnitudes first: they hardly ever have.
 template <int ATOMS>
 __device__ __forceinline__ unsigned long long clean_values(uint8_t *v, int nv, int lane) {
   constexpr int PIECE = kKeys * 128;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       sched[8] = sp.cost;
     }
   }
-  // The merge's words: of each pair, by the CTA that has its first unit, or of a pair that this CTA has the first part of
+  // The merge's words: of each pair, by the CTA that has its first unit, or of the pair whose first part this CTA has
   if (threadIdx.x == 0 && !p.by_pair) p.joins[blockIdx.x].parts = 0;
   if (warp == Ro::CLEAN && blockIdx.x == 0) {
     bool bad = false;  // lengths out of range, reported once a launch
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
           if (!have_line) {
             int depth = 0;
             line = line_of(p, e.s, real ? node : -1, up0, up1, lane, &depth);
-            lo = p.window > 0 ? e.s.ctx + depth - p.window + 1 : 0;
+            lo = p.window > 0 ? max(0, e.s.ctx + depth + 1 - p.window) : 0;
             have_line = true;
           }
           unsigned long long keep = low_bits(e.s.ctx - base);
@@ -860,7 +860,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       if (threadIdx.x == 0 && e.u0 == 0 && (p.by_pair || !whole)) {  // what the merge has to know
         const Split sp = {0, 0, sched[6], sched[7], e.cost};
         const int c0 = blockIdx.x, last = range_of(sp, e.pos + e.cost + e.s.U - 1);
-        p.joins[p.by_pair ? (e.i * p.Hkv + e.g) * p.groups + e.grp : c0] = {e.i, e.g, e.grp, c0, slot, last - c0 + 1, e.s.n};
+        const int word = p.by_pair ? (e.i * p.Hkv + e.g) * p.groups + e.grp : c0;
+        p.joins[word] = {e.i, e.g, e.grp, c0, slot, last - c0 + 1, e.s.n};
       }
       if (warp_real) {
         const float inv = 1.0f / L;
@@ -973,8 +974,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
     griddep_wait();
     at = p.joins[blockIdx.x];
     // an attention whose waits ran out leaves words of before
-    if (p.by_pair && (at.c0 < 0 || at.parts > p.grid - at.c0 || (at.slot & ~1) != 2 * at.c0 || at.i < 0 || at.i >= p.nb || at.g < 0 ||
-        at.g >= p.Hkv || at.grp < 0 || at.grp >= p.groups || at.nodes > p.m))
+    if (p.by_pair && (at.c0 < 0 || at.parts > p.grid - at.c0 || (at.slot & ~1) != 2 * at.c0 || at.i < 0 ||
+                      at.i >= p.nb || at.g < 0 || at.g >= p.Hkv || at.grp < 0 || at.grp >= p.groups || at.nodes > p.m))
       return;
   }
   const int n = at.parts, c0 = at.c0;

@@ -249,6 +249,16 @@ def test_graphs_of_one_workspace_and_handles_at_once():
             assert torch.equal(out, want[k])
 
 
+@pytest.mark.parametrize("Hq,m,kind", [(4, 64, "wide"), (8, 64, "tree"), (4, 1, "chain"), (4, 40, "chain")])
+def test_the_widest_window_is_none(Hq, m, kind):
+    nb = 4
+    t = Target(Hq, 2, 64, Cmax=448, nb=nb, paged=True, seed=m)
+    q, par, ctx = queries(nb, m, Hq, 64, m), trees(nb, m, m, kind), [0, 70, 129, 448 - m]
+    want = check_attention(t, m, q, par, None, ctx)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (448, 5), (1, 2 ** 31 - 1)):
+        assert torch.equal(t.attend(m, q, par, None, ctx, window, sinks), want) and t.status() == 0
+
+
 def test_rows_that_nobody_sees_may_hold_anything():
     """NaN and infinities in keys and values outside the window, behind the tree and in the nodes of other branches."""
     nb, m, window, sinks = 3, 16, 100, 4
