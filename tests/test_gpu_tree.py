@@ -259,6 +259,13 @@ def test_the_widest_window_is_none(Hq, m, kind):
         assert torch.equal(t.attend(m, q, par, None, ctx, window, sinks), want) and t.status() == 0
 
 
+@pytest.mark.parametrize("Hq,m", [(2, 1), (2, 17), (4, 40)])
+def test_a_quarter_million_rows(Hq, m):
+    t = Target(Hq, 1, 64, Cmax=262144, nb=1, paged=False, seed=m)
+    check_attention(t, m, queries(1, m, Hq, 64, 3), trees(1, m, 3), None, [262144 - m])
+    check_attention(t, m, queries(1, m, Hq, 64, 5), trees(1, m, 5), None, [262144 - m], 200000, 130)
+
+
 def test_rows_that_nobody_sees_may_hold_anything():
     """NaN and infinities in keys and values outside the window, behind the tree and in the nodes of other branches."""
     nb, m, window, sinks = 3, 16, 100, 4
