@@ -1044,9 +1044,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
 template <int HD, int WPR>
 cudaError_t launch_merge(const AttnTreeParams &p, cudaStream_t s) {
   // the attention's split of the SM's memory, so that this grid's CTAs may stand by next to it
-  static const cudaError_t configured = cudaFuncSetAttribute(
-      attn_tree_merge_kernel<HD, WPR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (configured != cudaSuccess) return configured;
+  static OncePerDevice once;
+  const cudaError_t e = once([] {
+    return cudaFuncSetAttribute(attn_tree_merge_kernel<HD, WPR>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
+  });
+  if (e != cudaSuccess) return e;
   constexpr int per = kMergeWarps / WPR * 32;
   const dim3 grid(p.by_pair ? p.nb * p.Hkv * p.groups : p.grid, (p.part_rows * (HD / 4) + per - 1) / per);
   return launch_pdl(attn_tree_merge_kernel<HD, WPR>, grid, dim3(kMergeWarps * 32), 0, s, p);
@@ -1055,10 +1058,12 @@ cudaError_t launch_merge(const AttnTreeParams &p, cudaStream_t s) {
 template <int HD, int NQ, bool TWO>
 cudaError_t launch(const AttnTreeParams &p, cudaStream_t s) {
   using C = Cfg<HD, NQ, TWO>;
-  static const cudaError_t configured = cudaFuncSetAttribute(
-      attn_tree_kernel<HD, NQ, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-  if (configured != cudaSuccess) return configured;
-  cudaError_t e = launch_pdl(attn_tree_kernel<HD, NQ, TWO>, dim3(p.grid), dim3(Roles<NQ>::THREADS), C::SMEM, s, p);
+  static OncePerDevice once;
+  cudaError_t e = once([] {
+    return cudaFuncSetAttribute(attn_tree_kernel<HD, NQ, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_tree_kernel<HD, NQ, TWO>, dim3(p.grid), dim3(Roles<NQ>::THREADS), C::SMEM, s, p);
   if (e != cudaSuccess) return e;
   return p.part_rows <= 16 ? launch_merge<HD, kMergeWarps>(p, s) : launch_merge<HD, 1>(p, s);
 }

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace df {
 
 // Launch with programmatic stream serialization: the kernel may start while the
@@ -46,6 +48,23 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+// A kernel's attributes are those of one device: `set` is called once on each, from any thread.
+struct OncePerDevice {
+  std::mutex mutex;
+  bool done[64] = {};
+  template <typename F>
+  cudaError_t operator()(F set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (dev < 64 && done[dev]) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+  }
+};
 
 // Bits of the device status word (first word of the workspace).
 constexpr int kStatusTimeout = 1;  // a bounded wait ran out

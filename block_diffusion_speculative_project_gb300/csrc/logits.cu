@@ -476,11 +476,14 @@ cudaError_t launch_adjust(LogitsParams &p, int tiles, int rows, cudaStream_t s) 
   if (p.n_bias > 0)
     for (p.hash = 32; p.hash < 2 * p.n_bias;) p.hash *= 2;
   const size_t smem = kWarps * S * RPC * 512 + (size_t)p.hash * 12;
-  static const cudaError_t configured = cudaFuncSetAttribute(logits_adjust_kernel<RPC, S, VEC, MASK>,
-                                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
-  if (configured != cudaSuccess) return configured;
+  static OncePerDevice once;
+  cudaError_t e = once([] {
+    return cudaFuncSetAttribute(logits_adjust_kernel<RPC, S, VEC, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                100 * 1024);
+  });
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>((long long)p.nb * p.splits * p.slices));
-  const cudaError_t e = launch_pdl(logits_adjust_kernel<RPC, S, VEC, MASK>, grid, dim3(32 * kWarps), smem, s, p);
+  e = launch_pdl(logits_adjust_kernel<RPC, S, VEC, MASK>, grid, dim3(32 * kWarps), smem, s, p);
   if (e != cudaSuccess || !p.ids) return e;
   const long long all = (long long)p.nb * p.m;
   return launch_pdl(logits_ids_kernel, dim3(static_cast<unsigned>((all + 3) / 4)), dim3(128), 0, s, p);

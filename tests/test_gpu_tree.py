@@ -388,6 +388,37 @@ def test_lengths_trees_and_pages_out_of_range_are_reported():
     assert t.status() == 0
 
 
+@pytest.mark.parametrize("n,ctx", [(8, 2 ** 31 - 1), (8, -2 ** 31), (2 ** 31 - 1, 5), (-2 ** 31, 5), (-2 ** 31, 2 ** 31 - 1),
+                                   (2 ** 31 - 1, -2 ** 31)])
+def test_lengths_at_the_ends_of_their_type(n, ctx):
+    """Counts and lengths that no cache has: reported, and the other sequence's rows as without them."""
+    D = lib()
+    t = Target(4, 2, 64, Cmax=256, nb=2, paged=True, seed=14)
+    for m in (8, 64):
+        q, par = queries(2, m, 4, 64, 1), trees(2, m, 1)
+        for window in (0, 60):
+            want = check_attention(t, m, q, par, [8, 0], [100, 0], window, 2)
+            got = t.attend(m, q, par, [8, n], [100, ctx], window, 2)
+            assert t.status() == D.DFLASH_ERR_DEVICE_CHECK
+            assert torch.equal(got[0], want[0])
+        before = t.kc.clone(), t.vc.clone()
+        path = i32([[0, 2, 3] + [-1] * (m - 3)] * 2)
+        D.dflash_kv_commit(t.h, 2, m, path, i32([0, n]), i32([0, ctx]), t.kc, t.vc, t.ws)
+        assert t.status() == D.DFLASH_ERR_DEVICE_CHECK
+        assert torch.equal(t.kc, before[0]) and torch.equal(t.vc, before[1])
+        for d_ctx in (i32([0, ctx]), None):
+            tau, bonus = i32([7, 7]), i32([7, 7])
+            D.dflash_accept_tree(t.h, 2, m, i32(par), i32(np.zeros((2, m))), i32(np.full((2, m), -1)), i32([1, n]), d_ctx,
+                                 tau, bonus, None, None, t.ws)
+            assert (t.status() == 0) == (n == 8)
+            assert tau.tolist() == [1, int(n > 0)]
+    V = 64
+    counts = i32(np.zeros((2, V)))
+    D.dflash_token_counts(t.h, 2, 3, i32([[1, 2, 3]] * 2), 3, i32([1, n]), 0, counts, t.ws)
+    assert t.status() == D.DFLASH_ERR_DEVICE_CHECK
+    assert counts.sum(1).tolist() == [1, 3 if n > 0 else 0]
+
+
 def test_a_wait_that_runs_out_is_reported():
     D = lib()
     t = Target(4, 2, 64, Cmax=256, nb=2, max_spin=50, flags=D.FLAG_TEST_STALL)
@@ -969,3 +1000,73 @@ def test_tree_rounds_emit_what_single_tokens_emit(paged, window):
             for i in range(nb):
                 x, y = (f64(c.rows(s, layer, i, C0 - 1 + n)) for c, s in ((force.t, a), (many.t, b)))
                 assert (np.abs(x - y) <= 3 * 2.0 ** -4 + 2.0 ** -7 * np.abs(x)).all(), (layer, i)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_drafters_round(paged):
+    """The calls of a round through Drafter, every layer: attention, ids, walk and the moved rows against the oracle."""
+    import dflash_inputs as di
+    from block_diffusion_speculative_project_gb300 import drafter
+    w = di.TINY
+    nb, Cmax, m = 2, 192, 12
+    Hq, Hkv, hd, V = w.Hq, w.Hkv, w.hd, w.V
+    dev = {k: drafter.to_device_bf16(v) for k, v in di.make_weights(w, 0).items()}
+    pps = Cmax // PR
+    dr = drafter.Drafter(w, dev, nb, Cmax, w.B, num_pages=nb * pps + 1 if paged else 0)
+    table = np.random.default_rng(1).permutation(nb * pps + 1)[:nb * pps].reshape(nb, pps)
+    if paged:
+        dr.set_block_table(i32(table))
+    lens = [100, 3]
+    ctx, par = i32(lens), trees(nb, m, 1)
+    depth = i32([[len(line) - 1 for line in orc.tree_lines(par[i])] for i in range(nb)])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+
+    def rows(t, layer, i, n):
+        if paged:
+            return t[layer][i32(table[i]).long()].transpose(0, 1).reshape(Hkv, -1, hd)[:, :n].clone()
+        return t[layer, i, :, :n].clone()
+
+    pos = (ctx[:, None] + depth).view(-1)
+    for layer in range(w.N):
+        k, v = rnd(nb * 100, Hkv * hd), rnd(nb * 100, Hkv * hd)
+        dr.kv_append(nb, layer, 100, k, v, i32([0, 0]), n_rows=ctx)
+        q, k, v = rnd(nb * m, (Hq + 2 * Hkv) * hd).split([Hq * hd, Hkv * hd, Hkv * hd], dim=1)
+        q_rot, k_rot = rnd(nb, m, Hq, hd), rnd(nb * m, Hkv * hd)
+        dr.qk_norm_rope(nb * m, 1, q, k, pos, q_rot, k_rot)
+        dr.kv_append(nb, layer, m, k_rot, v, ctx, rotate=False)
+        out = torch.empty_like(q_rot)
+        dr.attention_tree(nb, layer, m, q_rot, ctx, out, parent=i32(par), window=50, sinks=4)
+        for i in range(nb):
+            K, V_ = (f64(rows(c, layer, i, lens[i] + m)) for c in (dr.kcache, dr.vcache))
+            o, mag, dot = orc.attention_tree(f64(q_rot[i]), K, V_, orc.tree_visible(par[i], lens[i], 50, 4))
+            tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -14 + 2 * hd * 2.0 ** -24 * dot[..., None]) * mag
+            assert (np.abs(f64(out[i]) - o) <= tol).all()
+    r = Row(nb, m, V, 3, n_bias=5, mask=True, tree=True)
+    r.parent = par
+    want = [[orc.greedy(r.want(i, j)[0]) for j in range(m)] for i in range(nb)]
+    for i in range(nb):   # some nodes hold what will be asked for; a drafted token changes only rows below it
+        for j in range(1, m, 2):
+            r.tokens[i, j] = orc.greedy(r.want(i, int(par[i, j]))[0])
+        want[i] = [orc.greedy(r.want(i, j)[0]) for j in range(m)]
+    rules = r.rules().tensors
+    x = torch.from_numpy(r.x).cuda()
+    ids, tau, bonus = i32(np.zeros((nb, m))), i32(np.zeros(nb)), i32(np.zeros(nb))
+    path, emitted = i32(np.zeros((nb, m))), i32(np.zeros((nb, m)))
+    old = [[[rows(c, layer, i, lens[i] + m) for c in (dr.kcache, dr.vcache)] for i in range(nb)] for layer in range(w.N)]
+    dr.logits_adjust(nb, m, x, None, ids, *rules)
+    dr.accept_tree(nb, m, rules[5], rules[6], ids, tau, bonus, out_path=path, out_tokens=emitted, ctx_len=ctx)
+    dr.kv_commit(nb, m, path, tau, ctx)
+    dr.token_counts(nb, m, emitted, rules[1], n_tokens=tau)
+    assert dr.status() == 0 and ids.tolist() == want
+    counts = r.counts.copy()
+    for i in range(nb):
+        walk, said = orc.accept_tree(par[i], r.tokens[i], want[i])
+        assert path[i].tolist()[:len(walk)] == walk and emitted[i].tolist()[:len(said)] == said
+        assert int(ctx[i]) == lens[i] + len(walk) and int(bonus[i]) == said[-1]
+        np.add.at(counts[i], said, 1)
+        keep = list(range(lens[i])) + [lens[i] + a for a in walk]
+        for layer in range(w.N):
+            for c, was in zip((dr.kcache, dr.vcache), old[layer][i]):
+                assert torch.equal(rows(c, layer, i, len(keep)), was[:, keep])
+    assert np.array_equal(rules[1].cpu().numpy(), counts.view(np.int32))
