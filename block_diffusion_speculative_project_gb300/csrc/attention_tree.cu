@@ -14,9 +14,9 @@
 //                         rows, 32 heads over 8: one token 178 us and 6.8 TB/s, trees of 16 nodes 193 us and 6.3 TB/s.
 //   two tiles (R > 128)   both halves work on every unit, each for its own tile of up to 128 rows: K and
 //                         V are read once for 256 rows. More rows take further groups of two tiles. Bound by the
-//                         tensor core: an MMA of 128 rows takes some 76 cycles at 64 keys (S) as at 128 channels
-//                         (O), 24 a unit, 1824 cycles where the loads take 1400. 262147 rows under 64 nodes: 220 us,
-//                         1.25 PFLOP/s; with each tile's rows in a CTA of its own, K and V read twice, 314 us.
+//                         chain of a unit, S, softmax, product, and what the products of both tiles take from
+//                         shared memory: 262147 rows under 64 nodes 191 us, 1.44 PFLOP/s and 5.6 TB/s; with each
+//                         tile's rows in a CTA of its own, K and V read twice, 314 us.
 // A (sequence, kv head, group) is a pair; the visible units of all pairs are cut into equal ranges, one
 // per CTA (one CTA per SM; two one-tile CTAs an SM, each with half the stages: 206 us for the trees above).
 // The run of one pair inside a range is a segment: it writes the output, or if the pair goes on in another
@@ -31,7 +31,7 @@
 // such a key get a NaN probability for it.
 //
 // One CTA: TMA producer (K and V of a unit per stage, Q tiles of the segments), S issuer (S = Q K^T into buffer
-// step % 2, the first tile's Q from tensor memory), PV issuer (O_half += P V, P from tensor memory), the cleaner, and
+// step % 2, Q from tensor memory as far as it fits), PV issuer (O_half += P V, P from tensor memory), the cleaner, and
 // the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32, rounds P to bf16
 // (by up to 2^-9 of each probability, the type of the values that it multiplies) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
@@ -81,8 +81,9 @@ struct Cfg {
   static constexpr uint32_t S_COL = 0;             // two S buffers of 64 columns
   static constexpr uint32_t O_COL = 128;           // O of the two halves
   static constexpr uint32_t P_COL = 128 + 2 * HD;  // P of the two halves, 32 columns each
-  static constexpr uint32_t Q_COL = P_COL + 64;    // the (first) Q tile: hd / 2 columns
-  static_assert(Q_COL + HD / 2 <= 512, "tensor memory");
+  static constexpr uint32_t Q_COL = P_COL + 64;    // the first QT tiles of Q: hd / 2 columns each
+  static constexpr int QT = TWO && HD == 64 ? 2 : 1;
+  static_assert(Q_COL + QT * HD / 2 <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -271,6 +272,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+// One lane of a converged warp, always the same. The operands of the products that it issues stay in uniform registers:
+// two tiles' 24 products of a unit go out in 1150 cycles, from a thread of its own in 1410 (the S issuer so: 262147
+// rows under 64 nodes 217 us, so 191; the PV issuer, too, 64 single tokens of 64 channels 102.6 us, so 108).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t mine;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(mine));
+  return mine != 0;
+}
+
 // Bits [0, k).
 __device__ __forceinline__ unsigned long long low_bits(int k) {
   return k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       mbar_init(&p_empty[b], 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_ready, NQ);
+    mbar_init(q_ready, NQ * C::QT);
     mbar_init(q_free, 1);
     fence_mbar_init();
     if (smem_u32(smem) & 1023) flag_status(p.status, kStatusTimeout);  // never: the swizzled tiles' alignment
@@ -543,7 +555,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         int row = row_of(e.u0 + lane);
         if (e.index > 0) {  // the first segment's is loaded by the PV issuer, which has the time
           // the place is free when the one tile is in tensor memory; the second is read where it lies
-          ok = mbar_wait_warp(TWO ? q_free : q_ready, (e.index - 1) & 1, p.max_spin);
+          ok = mbar_wait_warp(C::TILES > C::QT ? q_free : q_ready, (e.index - 1) & 1, p.max_spin);
           if (!ok) break;
           if (lane == 0) load_q(e);
           ++q_loads;
@@ -575,50 +587,54 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       }
     }
   } else if (warp == Ro::S) {
-    if (lane == 0 && e.left > 0) {
+    if (__any_sync(0xffffffffu, e.left > 0)) {
       constexpr uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys);
       const uint64_t q_desc0 = sw128_kmajor_desc(smem_u32(sQ));
       const uint64_t k_desc0 = sw128_kmajor_desc(smem_u32(sKV));
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
       bool ok = true;
       int step = 0, st = 0;
       uint32_t ph = 0;
-      for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
-        ok = mbar_wait(q_ready, e.index & 1, p.max_spin);
-        if (TWO && ok) ok = mbar_wait(q_full, e.index & 1, p.max_spin);
-        for (int u = e.u0; u < e.u1 && ok; ++u) {
-          ok = mbar_wait(&kv_full[st], ph, p.max_spin);
+      for (; ok && __any_sync(0xffffffffu, e.left > 0); seg_next(e, p, seqs)) {
+        ok = mbar_wait_warp(q_ready, e.index & 1, p.max_spin);
+        if (C::TILES > C::QT && ok) ok = mbar_wait_warp(q_full, e.index & 1, p.max_spin);
+        const int n = __reduce_max_sync(0xffffffffu, e.u1 - e.u0);
+        for (int k = 0; k < n && ok; ++k) {
+          ok = mbar_wait_warp(&kv_full[st], ph, p.max_spin);
           const uint64_t kd = k_desc0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
 #pragma unroll
           for (int h = 0; h < C::TILES; ++h) {
             const int sb = step & 1;
-            if (ok && step >= 2) ok = mbar_wait(&s_empty[sb], ((step >> 1) - 1) & 1, p.max_spin);
+            if (ok && step >= 2) ok = mbar_wait_warp(&s_empty[sb], ((step >> 1) - 1) & 1, p.max_spin);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d_s = tmem_base + C::S_COL + sb * kKeys;
-            if (h == 0) {
+            const uint32_t d_s = tm + C::S_COL + sb * kKeys;
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>((h * C::Q_TILE) >> 4);
+            if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk)
-                tc_mma_bf16_tmem_a(d_s, tmem_base + C::Q_COL + kk * 8,
-                                   kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
-                                   kk > 0 ? 1u : 0u);
-            } else {
-              const uint64_t qd = q_desc0 + static_cast<uint64_t>(C::Q_TILE >> 4);
-#pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk)
-                tc_mma_bf16(d_s, qd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_Q + (kk & 3) * 32) >> 4),
-                            kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4), id_s,
-                            kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint64_t kkd = kd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_KV + (kk & 3) * 32) >> 4);
+                if (h < C::QT)
+                  tc_mma_bf16_tmem_a(d_s, tm + C::Q_COL + h * (HD / 2) + kk * 8, kkd, id_s, kk > 0 ? 1u : 0u);
+                else
+                  tc_mma_bf16(d_s, qd + static_cast<uint64_t>(((kk >> 2) * C::ATOM_Q + (kk & 3) * 32) >> 4), kkd, id_s,
+                              kk > 0 ? 1u : 0u);
+              }
+              tc_commit(&s_full[sb]);
             }
-            tc_commit(&s_full[sb]);
+            __syncwarp();
             ++step;
           }
           ring_next<ST>(st, ph);
         }
-        if (ok) tc_commit(q_free);
+        if (ok && elect_one()) tc_commit(q_free);
+        __syncwarp();
       }
-      if (!ok) flag_status(p.status, kStatusTimeout);
-      tc_commit(&mma_done[0]);  // every product completes before tensor memory is freed
-      mbar_wait(&mma_done[0], 0, kDrainSpin);
+      if (elect_one()) {
+        if (!ok) flag_status(p.status, kStatusTimeout);
+        tc_commit(&mma_done[0]);  // every product completes before tensor memory is freed
+        mbar_wait(&mma_done[0], 0, kDrainSpin);
+      }
     }
   } else if (warp == Ro::PV) {
     if (lane == 0 && e.left > 0) {
@@ -690,10 +706,12 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t o_mine = trow + C::O_COL + half * HD;
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
-    // The first Q tile of a segment to tensor memory, by half 1, or with two tiles by half 0, whose rows they are. Its
-    // place in shared memory is free for the next segment's then, and the products read it faster (262147 rows under
-    // 64 nodes: 233 us, from shared memory 240).
-    const bool copies = half == (TWO ? 0 : 1);
+    // The first QT tiles of a segment's Q to tensor memory, by half 1, or with two tiles by the halves whose rows they
+    // are. One tile's place in shared memory is free for the next segment's then, and the products do not read it from
+    // there beside the keys (262147 rows under 64 nodes: 203 us, both tiles from shared memory 219; of 64 channels,
+    // where tensor memory has the columns, 173 with both in it, 179 with one).
+    const bool copies = TWO ? half < C::QT : half == 1;
+    const int tile = TWO ? half : 0;
     auto copy_q = [&](int index) {
       bool good = index == 0 || mbar_wait_warp(q_free, (index - 1) & 1, p.max_spin);
       if (good) good = mbar_wait_warp(q_full, index & 1, p.max_spin);
@@ -704,11 +722,11 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         uint32_t v[16];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(sQ + (a >> 1) * C::ATOM_Q + r * 128 +
+          const uint4 x = *reinterpret_cast<const uint4 *>(sQ + tile * C::Q_TILE + (a >> 1) * C::ATOM_Q + r * 128 +
                                                            ((((a & 1) * 4 + c) ^ (r & 7)) << 4));
           v[4 * c] = x.x, v[4 * c + 1] = x.y, v[4 * c + 2] = x.z, v[4 * c + 3] = x.w;
         }
-        tmem_st16_raw(trow + C::Q_COL + a * 16, v);
+        tmem_st16_raw(trow + C::Q_COL + tile * (HD / 2) + a * 16, v);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -1060,7 +1078,8 @@ cudaError_t launch(const AttnTreeParams &p, cudaStream_t s) {
   using C = Cfg<HD, NQ, TWO>;
   static OncePerDevice once;
   cudaError_t e = once([] {
-    return cudaFuncSetAttribute(attn_tree_kernel<HD, NQ, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    return cudaFuncSetAttribute(attn_tree_kernel<HD, NQ, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::SMEM);
   });
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_tree_kernel<HD, NQ, TWO>, dim3(p.grid), dim3(Roles<NQ>::THREADS), C::SMEM, s, p);
@@ -1094,11 +1113,11 @@ void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows) {
 }
 
 cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s) {
-  // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 194.7 us
-  // without, 191.3 with 4, 193.0 with 12; 64 x 64 rows (two tiles) 299.7, with 4 278.9, with 6 273.1, with 12 279.2.
-  // A unit of 64 channels takes half the time.
   p.by_pair = p.nb * p.Hkv * p.groups <= p.grid;
-  p.pair_cost = (p.part_rows > p.npt * (p.Hq / p.Hkv) ? 6 : 4) * (128 / p.hd);
+  // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 194.7 us
+  // without, 191.3 with 4, 193.0 with 12; 32 x 25 rows under a window 38.5 with 4, 37.7 with 6; 64 x 64 rows (two tiles)
+  // 255 with 4, 246 with 6, 250 with 8. A unit of 64 channels takes half the time.
+  p.pair_cost = (p.npt * (p.Hq / p.Hkv) > 64 ? 6 : 4) * (128 / p.hd);
   switch (p.hd) {
     case 64: return launch_form<64>(p, s);
     case 128: return launch_form<128>(p, s);
