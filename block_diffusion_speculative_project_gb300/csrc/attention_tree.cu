@@ -116,11 +116,20 @@ __device__ __forceinline__ Span make_span(const AttnTreeParams &p, int ctx, int 
   return s;
 }
 __device__ __forceinline__ int unit_base(const Span &s, int u) { return (u < s.A ? u : u - s.A + s.W0) * kKeys; }
-// Whether every row sees all of the unit's keys.
-__device__ __forceinline__ bool unit_plain(const AttnTreeParams &p, const Span &s, int base) {
-  return base + kKeys <= s.ctx &&
-         (p.window <= 0 || base >= s.ctx + s.n - p.window || base + kKeys <= p.sinks);
+// The units all of whose keys every row sees, as far as their places tell: whole ones of the sinks, and from the last
+// window's edge to the tree's own rows.
+struct Plain {
+  int sinks, from, to;
+};
+__device__ __forceinline__ Plain plain_units(const AttnTreeParams &p, const Span &s) {
+  Plain u = {0, 0, s.A + s.ctx / kKeys - s.W0};
+  if (p.window > 0) {
+    u.sinks = min(s.A, min(p.sinks, s.ctx) / kKeys);
+    u.from = s.A + max(0, (max(0, s.ctx + s.n - p.window) + kKeys - 1) / kKeys - s.W0);
+  }
+  return u;
 }
+__device__ __forceinline__ bool unit_plain(const Plain &s, int u) { return u < s.sinks || (u >= s.from && u < s.to); }
 
 constexpr int kCostFrom = 16;  // units of a CTA from which a pair's cost counts
 constexpr int kSeqCache = 64;  // sequences whose lengths a CTA keeps in shared memory
@@ -273,8 +282,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 }
 
 // One lane of a converged warp, always the same. The operands of the products that it issues stay in uniform registers:
-// two tiles' 24 products of a unit go out in 1150 cycles, from a thread of its own in 1410 (the S issuer so: 262147
-// rows under 64 nodes 217 us, so 191; the PV issuer, too, 64 single tokens of 64 channels 102.6 us, so 108).
+// two tiles' 24 products of a unit go out in 1150 cycles, from a thread of its own in 1410 (262147 rows under 64 nodes
+// 217 us, so 191).
 __device__ __forceinline__ bool elect_one() {
   uint32_t mine;
   asm volatile(
@@ -637,54 +646,68 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       }
     }
   } else if (warp == Ro::PV) {
-    if (lane == 0 && e.left > 0) {
-      if (!p.stall) load_q(e);
+    // a warp with an elected lane, or a thread: of 64 channels, whose units come sooner than a warp's votes, 64 single
+    // tokens take 102 us with a thread, 108 with a warp; of 128, 64 x 64 rows 250 with a warp, 252 with a thread
+    constexpr bool WARP = HD == 128;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return WARP ? mbar_wait_warp(bar, parity, p.max_spin) : mbar_wait(bar, parity, p.max_spin);
+    };
+    if (WARP ? __any_sync(0xffffffffu, e.left > 0) != 0 : lane == 0 && e.left > 0) {
+      if (lane == 0 && !p.stall) load_q(e);
+      if (WARP) __syncwarp();
       constexpr uint32_t id_pv = idesc_bf16_f32(kTileRows, HD) | kIdescBMajorMN;
       const uint64_t v_desc0 = sw128_mnmajor_desc(smem_u32(sKV + C::KV_TILE), C::ATOM_KV);
+      const uint32_t tm = WARP ? __reduce_max_sync(0xffffffffu, tmem_base) : tmem_base;
       bool ok = true;
       int step = 0, st = 0;
       uint32_t ph = 0;
-      for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+      for (; ok && (WARP ? __any_sync(0xffffffffu, e.left > 0) != 0 : e.left > 0); seg_next(e, p, seqs)) {
         const int first = step;
-        for (int u = e.u0; u < e.u1 && ok; ++u) {
+        const int n = WARP ? __reduce_max_sync(0xffffffffu, e.u1 - e.u0) : e.u1 - e.u0;
+        for (int k = 0; k < n && ok; ++k) {
           const uint64_t vd = v_desc0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
 #pragma unroll
           for (int h = 0; h < C::TILES; ++h) {
             const int half = step & 1;
             const bool start = step < first + 2;  // the half's first unit of the segment
-            ok = mbar_wait(&p_full[half], (step >> 1) & 1, p.max_spin);
-            if (ok && start && e.index > 0) ok = mbar_wait(&o_free[TWO ? half : 0], (e.index - 1) & 1, p.max_spin);
+            ok = wait(&p_full[half], (step >> 1) & 1);
+            if (ok && start && e.index > 0) ok = wait(&o_free[TWO ? half : 0], (e.index - 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d_o = tmem_base + C::O_COL + half * HD;
-            const uint32_t a_p = tmem_base + C::P_COL + half * 32;
+            const uint32_t d_o = tm + C::O_COL + half * HD;
+            const uint32_t a_p = tm + C::P_COL + half * 32;
+            if (!WARP || elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc_mma_bf16_tmem_a(d_o, a_p + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
-                                 (!start || kk > 0) ? 1u : 0u);
-            tc_commit(&p_empty[half]);
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc_mma_bf16_tmem_a(d_o, a_p + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id_pv,
+                                   (!start || kk > 0) ? 1u : 0u);
+              tc_commit(&p_empty[half]);
+              if (h == C::TILES - 1) tc_commit(&kv_empty[st]);
+            }
+            if (WARP) __syncwarp();
             ++step;
           }
-          if (ok) tc_commit(&kv_empty[st]);
           ring_next<ST>(st, ph);
         }
       }
-      if (!ok) flag_status(p.status, kStatusTimeout);
-      tc_commit(&mma_done[1]);
-      mbar_wait(&mma_done[1], 0, kDrainSpin);
+      if (!WARP || elect_one()) {
+        if (!ok) flag_status(p.status, kStatusTimeout);
+        tc_commit(&mma_done[1]);
+        mbar_wait(&mma_done[1], 0, kDrainSpin);
+      }
     }
   } else if (warp == Ro::CLEAN) {
     bool ok = true;
     int st = 0;
     uint32_t ph = 0;
     for (; e.left > 0 && ok; seg_next(e, p, seqs)) {
+      const Plain plain = plain_units(p, e.s);
       for (int u = e.u0; u < e.u1; ++u) {
         ok = mbar_wait_warp(&kv_full[st], ph, p.max_spin);
         if (!ok) break;
-        const int base = unit_base(e.s, u);
-        if (!unit_plain(p, e.s, base)) {
-          const unsigned long long found =
-              clean_values<C::ATOMS>(sKV + st * C::STAGE + C::KV_TILE, e.s.ctx + e.s.n - base, lane);
+        if (!unit_plain(plain, u)) {
+          const unsigned long long found = clean_values<C::ATOMS>(
+              sKV + st * C::STAGE + C::KV_TILE, e.s.ctx + e.s.n - unit_base(e.s, u), lane);
           if (lane == 0) poison[st] = found;
         }
         __syncwarp();
@@ -752,13 +775,13 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         if (lane + 32 < p.m) up1 = up[lane + 32];
       }
       const int u_first = TWO ? e.u0 : e.u0 + ((units ^ half) & 1);
+      const Plain plain = plain_units(p, e.s);
       int step = 0;
 #pragma unroll 1
       for (int u = u_first; u < e.u1; u += STRIDE) {
         const int stage = units + u - e.u0;
         step = TWO ? 2 * stage + half : stage;
         const bool start = u == u_first;
-        const int base = unit_base(e.s, u);
         ok = mbar_wait_warp(&s_full[half], (step >> 1) & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();
@@ -768,7 +791,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         warp_arrive(&s_empty[half], lane);
 
         unsigned long long bad = 0;
-        if (!unit_plain(p, e.s, base)) {
+        if (!unit_plain(plain, u)) {
+          const int base = unit_base(e.s, u);
           if (!have_line) {
             int depth = 0;
             line = line_of(p, e.s, real ? node : -1, up0, up1, lane, &depth);
