@@ -389,12 +389,15 @@ __device__ __forceinline__ unsigned long long clean_values(uint8_t *v, int nv, i
         *reinterpret_cast<uint4 *>(v + a * PIECE + k * 16) = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
-  uint32_t m = 0;
+  uint4 top = make_uint4(0, 0, 0, 0);
 #pragma unroll 16
   for (int k = 0; k < 16 * ATOMS; ++k) {
     const uint4 x = *reinterpret_cast<const uint4 *>(v + (k * 32 + lane) * 16);
-    m = max_abs2(max_abs2(m, x.x), max_abs2(max_abs2(x.y, x.z), x.w));
+    top.x = max_abs2(top.x, x.x), top.y = max_abs2(top.y, x.y);
+    top.z = max_abs2(top.z, x.z), top.w = max_abs2(top.w, x.w);
   }
+  const uint32_t m = max_abs2(max_abs2(top.x, top.y), max_abs2(top.z, top.w));
+  bool wrote = nv < kKeys;
   unsigned long long found = 0;
   if (__any_sync(0xffffffffu, (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u)) {
     uint32_t found0 = 0, found1 = 0;
@@ -419,8 +422,9 @@ __device__ __forceinline__ unsigned long long clean_values(uint8_t *v, int nv, i
     }
     found = static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, found1)) << 32 |
             __reduce_or_sync(0xffffffffu, found0);
+    wrote = true;
   }
-  fence_proxy_async_smem();
+  if (wrote) fence_proxy_async_smem();  // for the products
   return found;
 }
 
@@ -884,15 +888,15 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
       units += e.u1 - e.u0;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (e.index > 0);
       float M = m_run, L = l_run, a0 = 1.f, a1 = 0.f;
-      if (!TWO && half == 1 && more) ok = copy_q(e.index + 1);
-      if (ok && !TWO && e.index > 0) ok = mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);  // ml was read
+      if (!TWO && e.index > 0) ok = mbar_wait_warp(&o_free[0], (e.index - 1) & 1, p.max_spin);  // ml was read
       if (ok && mine) ok = mbar_wait_warp(&p_empty[half], (step >> 1) & 1, p.max_spin);
       if (!ok) break;
       if (!TWO) {  // each half ends half of the channels, of both O
         ml[half * kTileRows + r] = mine ? make_float2(M, L) : make_float2(-FLT_MAX, -1.f);
         tc_fence_before();
         warp_arrive(&ml_ready[half], lane);
-        ok = mbar_wait_warp(&ml_ready[half ^ 1], e.index & 1, p.max_spin);
+        if (half == 1 && more) ok = copy_q(e.index + 1);
+        if (ok) ok = mbar_wait_warp(&ml_ready[half ^ 1], e.index & 1, p.max_spin);
         if (!ok) break;
         const float2 h0 = ml[r], h1 = ml[kTileRows + r];
         M = fmaxf(h0.x, h1.x);
