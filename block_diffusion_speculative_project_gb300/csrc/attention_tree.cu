@@ -11,7 +11,7 @@
 // in one of two forms:
 //   one tile (R <= 128)   two halves of softmax warps take units of 64 keys in turn, each with its own
 //                         running maximum, sum and O, joined at the end of a segment. 64 sequences of 1024 to 8191
-//                         rows, 32 heads over 8: one token 178 us and 6.8 TB/s, trees of 16 nodes 193 us and 6.3 TB/s.
+//                         rows, 32 heads over 8: one token 178 us and 6.8 TB/s, trees of 16 nodes 192 us and 6.4 TB/s.
 //   two tiles (R > 128)   both halves work on every unit, each for its own tile of up to 128 rows: K and
 //                         V are read once for 256 rows. More rows take further groups of two tiles. Bound by the
 //                         chain of a unit, S, softmax, product, and what the products of both tiles take from
@@ -33,7 +33,7 @@
 // One CTA: TMA producer (K and V of a unit per stage, Q tiles of the segments), S issuer (S = Q K^T into buffer
 // step % 2, Q from tensor memory as far as it fits), PV issuer (O_half += P V, P from tensor memory), the cleaner, and
 // the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32, rounds P to bf16
-// (by up to 2^-9 of each probability, the type of the values that it multiplies) and rescales O only when the row's
+// (by up to 2^-8 of each probability, the type of the values that it multiplies) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
 #include <cfloat>
 
