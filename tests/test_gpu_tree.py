@@ -266,6 +266,29 @@ def test_a_quarter_million_rows(Hq, m):
     check_attention(t, m, queries(1, m, Hq, 64, 5), trees(1, m, 5), None, [262144 - m], 200000, 130)
 
 
+@pytest.mark.parametrize("Hq,Hkv,hd,m", [(4, 2, 64, 1), (8, 2, 128, 33), (16, 2, 64, 50), (3, 3, 128, 64)])
+def test_contiguous_caches_of_odd_length(Hq, Hkv, hd, m):
+    """Pages of the last rows reach into the next head's, sequence's and layer's, and past the cache's end."""
+    nb, Cmax = 3, 397
+    t = Target(Hq, Hkv, hd, Cmax=Cmax, nb=nb, N=2, paged=False, seed=m)
+    ctx, n, par = [Cmax - m, 320, 0], [m, max(1, m - 3), m], trees(nb, m, m)
+    q = queries(nb, m, Hq, hd, m)
+    for layer in (0, 1):
+        for window in (0, 90):
+            check_attention(t, m, q, par, n, ctx, window, 5, layer=layer)
+    want = [[t.rows(c, layer, i, Cmax) for c in (t.kc, t.vc)] for layer in (0, 1) for i in range(nb)]
+    path = [list(range(0, k, 2)) for k in n]
+    tau = [len(w) for w in path]
+    t.D.dflash_kv_commit(t.h, nb, m, i32([w + [-1] * (m - len(w)) for w in path]), i32(tau),
+                         i32([c + k for c, k in zip(ctx, tau)]), t.kc, t.vc, t.ws)
+    assert t.status() == 0
+    for layer in (0, 1):
+        for i in range(nb):
+            for c, was in zip((t.kc, t.vc), want[layer * nb + i]):
+                was[:, ctx[i]:ctx[i] + tau[i]] = was[:, [ctx[i] + a for a in path[i]]]
+                assert torch.equal(t.rows(c, layer, i, Cmax), was)
+
+
 def test_rows_that_nobody_sees_may_hold_anything():
     """NaN and infinities in keys and values outside the window, behind the tree and in the nodes of other branches."""
     nb, m, window, sinks = 3, 16, 100, 4
@@ -427,6 +450,24 @@ def test_a_wait_that_runs_out_is_reported():
         assert t.status() == D.DFLASH_ERR_TIMEOUT
     t = Target(4, 2, 64, Cmax=256, nb=2)
     check_attention(t, 20, queries(2, 20, 4, 64, 1), trees(2, 20, 1), None, [100, 50])
+
+
+def test_a_wait_that_runs_out_leaves_the_workspace_usable():
+    """What calls before left in the workspace, or anything, is no harm to a call whose waits run out, nor that to the next."""
+    D = lib()
+    good = Target(8, 2, 64, Cmax=1024, nb=3, seed=3)
+    stall = Target(8, 2, 64, Cmax=1024, nb=3, seed=3, max_spin=50, flags=D.FLAG_TEST_STALL)
+    assert good.ws.numel() == stall.ws.numel()
+    stall.ws = good.ws
+    for fill in (None, 0xFF, 0x01):
+        for m, then in ((64, 20), (20, 64), (9, 9), (1, 3)):
+            q, par = queries(3, m, 8, 64, m), trees(3, m, m)
+            check_attention(good, m, q, par, None, [900, 300, 5])
+            if fill is not None:
+                good.ws[256:].fill_(fill)
+            out = stall.attend(then, queries(3, then, 8, 64, 1), trees(3, then, 1), None, [700, 50, 0])
+            assert stall.status() == D.DFLASH_ERR_TIMEOUT and out.shape[1] == then
+            check_attention(good, m, q, par, None, [900, 300, 5])
 
 
 def refused(code, f):
