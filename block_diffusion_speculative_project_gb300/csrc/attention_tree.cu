@@ -847,8 +847,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         // nodes 196 us, behind them 216).
         ok = step < 2 || mbar_wait_warp(&p_empty[half], ((step >> 1) - 1) & 1, p.max_spin);
         if (!ok) break;
+        tc_fence_after();  // behind that product come what is written of O, and P
         if (!start && __any_sync(0xffffffffu, need)) {
-          tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < HD / 32; ++cc) {
             float ov[32];

@@ -289,6 +289,25 @@ def test_contiguous_caches_of_odd_length(Hq, Hkv, hd, m):
                 assert torch.equal(t.rows(c, layer, i, Cmax), was)
 
 
+@pytest.mark.parametrize("Hq,Hkv,hd,m", [(4, 2, 64, 1), (32, 8, 128, 16), (32, 8, 128, 64), (64, 8, 64, 64)])
+def test_probabilities_that_change_from_unit_to_unit(Hq, Hkv, hd, m):
+    """No row's maximum grows by 2^8, so O is never rescaled, while the probabilities of a unit are about 1 or about 2^-6,
+    in turns of no one length: a unit's in the place of another's would show."""
+    t = Target(Hq, Hkv, hd, Cmax=4096, nb=2, paged=True, seed=m)
+    unit = torch.arange(t.kc.shape[1] * PR, device="cuda").view(-1, 1, PR, 1) // PR
+    high = (unit % 2 == 0) | (unit % 5 < 2)
+    d = torch.where(torch.rand(hd, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") < 0.5, -1.0, 1.0)
+    t.kc.copy_((torch.where(high, 1.0, 0.25) * d).to(torch.bfloat16).expand_as(t.kc[0]))
+    for i in range(2):
+        t.put(t.kc, 0, i, 0, d.to(torch.bfloat16))
+    q = (0.25 * queries(2, m, Hq, hd, m).float() + 6 / hd ** 0.5 * d).to(torch.bfloat16)
+    ctx, n, par = [4096 - m, 2500], [m, max(1, m - 5)], trees(2, m, m)
+    want = check_attention(t, m, q, par, n, ctx)
+    for _ in range(20):
+        assert torch.equal(t.attend(m, q, par, n, ctx), want)
+    assert t.status() == 0
+
+
 def test_rows_that_nobody_sees_may_hold_anything():
     """NaN and infinities in keys and values outside the window, behind the tree and in the nodes of other branches."""
     nb, m, window, sinks = 3, 16, 100, 4
