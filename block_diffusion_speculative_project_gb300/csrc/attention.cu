@@ -533,6 +533,7 @@ __global__ void __launch_bounds__(AttnRoles<NQ>::THREADS, 1)
           ok = false;
           break;
         }
+        tc_fence_after();
         if (warp_real) {
           // P (bf16 pairs) into this half's P columns of the row's TMEM lane
           float pk[kKeys / 2];

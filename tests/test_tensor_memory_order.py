@@ -11,7 +11,7 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "block_diffusion_speculative_project_gb300", "csrc")
-FILES = ("attention8.cu", "attention8_wide.cu", "attention_tree.cu", "gemm_tc.cu")
+FILES = sorted(f for f in os.listdir(CSRC) if f.endswith(".cu") and "tc_commit(" in open(os.path.join(CSRC, f)).read())
 
 TOKEN = re.compile(r"[{}]|\b(?:mbar_wait|mbar_wait_warp|wait)\(\s*&?(\w+)|\btc_fence_after\(|\btmem_(?:ld|st)\d\w*\(|\btc_mma_\w+\(")
 
