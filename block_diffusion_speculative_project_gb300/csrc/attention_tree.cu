@@ -930,8 +930,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
           } else {
             tmem_ld16(trow + C::O_COL + (first0 == 1 ? HD : 0) + cc, ov);
           }
-          if (!real) continue;
-          if (whole) {
+          if (real && whole) {
             uint16_t *dst = p.o + (((long long)e.i * p.m + node) * p.Hq + e.g * G + hq) * HD + cc;
 #pragma unroll
             for (int v = 0; v < 2; ++v)
@@ -940,7 +939,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
                              pack_bf16x2(ov[8 * v + 2] * inv, ov[8 * v + 3] * inv),
                              pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
                              pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
-          } else {
+          } else if (real) {
             // rows side by side, four channels each: a warp's store is four lines, with a row's channels side by side
             // it was 32 (64 x 64 rows 293 us, so 286)
             float4 *dst =
@@ -949,6 +948,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
             for (int v = 0; v < 4; ++v)
               dst[v * p.part_rows] = make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
           }
+          __syncwarp();  // the next load is the whole warp's
         }
         if (real && !whole && (TWO || half == 0))
           reinterpret_cast<float2 *>(p.part_ml)[(long long)slot * p.part_rows + prow] = make_float2(M, L);

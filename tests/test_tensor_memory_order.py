@@ -3,6 +3,9 @@
 A wait on a barrier that tensor products arrive on (tc_commit) orders what follows behind those products only
 together with tc_fence_after: the sources are read block by block, and a load or store of tensor memory, or a
 product, has to find a fence on every way from the last such wait to it.
+
+Loads and stores of tensor memory are a whole warp's. A `continue` of some lanes in the loop that they stand in would
+leave it to the compiler whether the others wait for them.
 """
 import os
 import re
@@ -62,3 +65,42 @@ def test_the_reading_finds_what_it_looks_for():
 @pytest.mark.parametrize("name", FILES)
 def test_tensor_memory_is_touched_behind_a_fence(name):
     assert unfenced(open(os.path.join(CSRC, name)).read()) == []
+
+
+def skipped(text):
+    """Lines with a `continue` in a loop that accesses tensor memory itself, not by a loop inside it."""
+    text = plain(text)
+    found, blocks = [], []   # a block: is it a loop's or a lambda's, has it accesses, lines of its `continue`
+    for m in re.finditer(r"[{}]|\bcontinue\b|\btmem_(?:ld|st)\d\w*\(|\bfetch\(", text):
+        t, inner = m.group(), next((b for b in reversed(blocks) if b[0]), None)
+        if t == "{":
+            head = text[:m.start()].rstrip()
+            at, depth = len(head), 0
+            while head.endswith(")") and at > 0:
+                at -= 1
+                depth += (head[at] == ")") - (head[at] == "(")
+                if depth == 0:
+                    break
+            blocks.append([bool(re.search(r"(\b(for|while)|\])\s*$", head[:at])), False, []])
+        elif t == "}":
+            _, touches, lines = blocks.pop()
+            found += lines if touches else []
+        elif inner is not None:
+            if t == "continue":
+                inner[2].append(text.count("\n", 0, m.start()) + 1)
+            else:
+                inner[1] = True
+    return found
+
+
+def test_the_reading_finds_lanes_that_skip():
+    for text, lines in (("void f() { for (int i = 0; i < 4; ++i) { tmem_ld16(a, v);\nif (!real) continue;\nx = v; } }", [2]),
+                        ("void f() { for (int i = 0; i < 4; ++i) { if (x) {\ncontinue; }\ntmem_st16_raw(a, v); } }", [2]),
+                        ("void f() { while (g(1)) { for (;;) { tmem_ld16(a, v); }\nif (x) continue; } }", []),
+                        ("void f() { for (;;) { if (x) continue; } tmem_ld16(a, v); }", [])):
+        assert skipped(text) == lines, text
+
+
+@pytest.mark.parametrize("name", [f for f in FILES if f not in ("attention.cu", "gemm_tc.cu")])
+def test_no_lane_skips_a_warps_access(name):
+    assert skipped(open(os.path.join(CSRC, name)).read()) == []
