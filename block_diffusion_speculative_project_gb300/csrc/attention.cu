@@ -613,8 +613,7 @@ __global__ void __launch_bounds__(AttnRoles<NQ>::THREADS, 1)
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 ov[c] = (has0 ? ov[c] * a0 : 0.f) + (has1 ? o1v[c] * a1 : 0.f);
-              if (!real) continue;
-              if (whole) {
+              if (real && whole) {
                 uint16_t *dst = p.o + ((size_t)i * p.B + jq) * ((size_t)p.Hq * HD) +
                                 (size_t)(g * G + hq) * HD + cc * 32;
 #pragma unroll
@@ -624,13 +623,14 @@ __global__ void __launch_bounds__(AttnRoles<NQ>::THREADS, 1)
                                  pack_bf16x2(ov[8 * v + 2] * inv, ov[8 * v + 3] * inv),
                                  pack_bf16x2(ov[8 * v + 4] * inv, ov[8 * v + 5] * inv),
                                  pack_bf16x2(ov[8 * v + 6] * inv, ov[8 * v + 7] * inv));
-              } else {
+              } else if (real) {
                 float *dst = p.part_o + ((size_t)slot * R + r) * HD + cc * 32;
 #pragma unroll
                 for (int v = 0; v < 8; ++v)
                   reinterpret_cast<float4 *>(dst)[v] =
                       make_float4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
               }
+              __syncwarp();  // the next load is the whole warp's
             }
           }
           if (real && !whole)

@@ -520,12 +520,12 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams &p, const Item &t
           const long long cr = cache_row(p, seq, head, pos);
           if (cr < 0) {
             flag_status(p.status, kStatusCheck);
-            continue;
+          } else {
+            if (isk) rope_pair(p, pos, cc, a, b);
+            uint16_t *o = cache + (layer * p.layer_rows + cr) * p.hd;
+            store_bf16_32(o + cc, a, 32);
+            store_bf16_32(o + half + cc, b, 32);
           }
-          if (isk) rope_pair(p, pos, cc, a, b);
-          uint16_t *o = cache + (layer * p.layer_rows + cr) * p.hd;
-          store_bf16_32(o + cc, a, 32);
-          store_bf16_32(o + half + cc, b, 32);
         }
       }
     }

@@ -101,6 +101,6 @@ def test_the_reading_finds_lanes_that_skip():
         assert skipped(text) == lines, text
 
 
-@pytest.mark.parametrize("name", [f for f in FILES if f not in ("attention.cu", "gemm_tc.cu")])
+@pytest.mark.parametrize("name", FILES)
 def test_no_lane_skips_a_warps_access(name):
     assert skipped(open(os.path.join(CSRC, name)).read()) == []
