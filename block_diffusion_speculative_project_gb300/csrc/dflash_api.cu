@@ -211,7 +211,8 @@ void plan_workspace(dflash_handle_s *h) {
   L.smp_lse = take((size_t)Mb * 4);
   L.ver_part = take((size_t)c.max_batch * kSampleMaxSlices * 16);
   L.ver_nrej = take((size_t)c.max_batch * 4);
-  L.lg_part = take((size_t)c.max_batch * kTreeMax * kLogitSlots * sizeof(float2));
+  // dflash_logits_adjust refuses larger vocabularies
+  L.lg_part = take(c.V > kMaxVocab ? 0 : (size_t)c.max_batch * kTreeMax * logit_slots(c.V) * sizeof(float2));
   if (c.flags & DFLASH_FLAG_FILM) {
     L.film_cond = take((size_t)Mb * 3 * c.D * 2);
     L.film_hid = take((size_t)Mb * c.film_dim * 2);

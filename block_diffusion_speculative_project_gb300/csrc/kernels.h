@@ -425,12 +425,15 @@ struct LogitsParams {
   const int *n_rows;         // [nb] or null: m
   int nb, m, V, n_bias, words;
   int *status;
-  float2 *part;              // scratch of the ids: kLogitSlots (value, id) pairs a row
+  float2 *part;              // scratch of the ids: logit_slots(V) (value, id) pairs a row
   int slices, chunk, splits, rows, hash;  // work split, set by the launch
 };
 constexpr int kMaxBias = 1024;
 constexpr int kMaxVocab = 1 << 21;
-constexpr int kLogitSlots = 256;  // most slices of a row: kMaxVocab in slices of 8192 tokens
+constexpr int kLogitSlots = 256;    // most slices of a row: kMaxVocab in slices of 8192 tokens
+constexpr int kLogitSlice = 1024;   // tokens of the smallest slice
+// Most slices of a row of V tokens: what the launch keeps to and the workspace holds.
+inline int logit_slots(int V) { return (V - 1) / kLogitSlice + 1 < kLogitSlots ? (V - 1) / kLogitSlice + 1 : kLogitSlots; }
 cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s);
 
 struct TokenCountsParams {

@@ -37,6 +37,8 @@ namespace {
 
 constexpr int kWarps = 8;                // of a CTA
 constexpr int kTiles = 8;                // most of a warp: 128 tokens each, four of them a lane's
+static_assert(kLogitSlice == 128 * kWarps, "one tile a warp");
+static_assert((kMaxVocab - 1) / (kTiles * kLogitSlice) < kLogitSlots, "the largest vocabulary in the largest slices");
 
 // Pieces of 128 values of a warp's stage: the rows', and for one row its counts.
 __host__ __device__ constexpr int ring_slots(int rpc) { return rpc == 1 ? 2 : rpc; }
@@ -561,7 +563,7 @@ cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s) {
   const int rows = ((p.m + parts - 1) / parts + at_once - 1) / at_once * at_once;
   while (tiles > 1 && p.nb * slices() * ((p.m + rows - 1) / rows) < 7LL * num_sms / 4) {
     tiles /= 2;
-    if (slices() > kLogitSlots) {
+    if (slices() > logit_slots(p.V)) {
       tiles *= 2;
       break;
     }

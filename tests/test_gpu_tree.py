@@ -868,6 +868,26 @@ def test_biases_of_one_slice_and_of_one_token():
     r.check(*run_row(r, t))
 
 
+@pytest.mark.parametrize("nb,m,V", [(1, 1, 64), (256, 64, 64), (200, 64, 1024), (90, 64, 1025), (5, 3, 151936),
+                                    (1, 1, 2 ** 21), (2, 64, 2 ** 21)])
+def test_scratch_of_the_ids(nb, m, V):
+    """A sequence's scratch follows the vocabulary: at most a pair of words for each row and 1024 tokens. Nothing is
+    written behind the workspace's end, where that scratch lies."""
+    D = lib()
+    t, one = Target(nb=nb, V=V, Cmax=64, paged=False), Target(nb=1, V=V, Cmax=64, paged=False)
+    per = (t.ws.numel() - one.ws.numel()) / max(nb - 1, 1)
+    assert per <= 8 * 64 * min(256, -(-V // 1024)) + 16384   # the rest of these small handles: below 16 KB a sequence
+    size = t.ws.numel()
+    ws = torch.full((size + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    ws[:size] = 0
+    x = torch.randint(-1000, 1000, (nb * m, V), generator=torch.Generator(device="cuda").manual_seed(V), device="cuda").float()
+    ids = i32(np.full(nb * m, 7))
+    D.dflash_logits_adjust(t.h, nb, m, x, V, D.logit_rules(), None, None, V, ids, ws)
+    assert D.dflash_status(t.h, ws) == 0 and (ws[size:] == 0x5A).all()
+    first = torch.arange(V, dtype=torch.int32, device="cuda").where(x == x.max(1, keepdim=True).values, V).min(1).values
+    assert torch.equal(ids, first)
+
+
 @pytest.mark.parametrize("nb,m", [(3, 2), (40, 8)])
 def test_special_values_and_ties(nb, m):
     V = 520
