@@ -1142,6 +1142,16 @@ void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows) {
   *part_rows = 2 * *npt * G;
 }
 
+int attention_tree_part_rows(int m, int G) {
+  int most = 0;
+  for (int k = 1; k <= m; ++k) {
+    int npt, groups, rows;
+    attention_tree_plan(k, G, &npt, &groups, &rows);
+    most = rows > most ? rows : most;
+  }
+  return most;
+}
+
 cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s) {
   p.by_pair = p.nb * p.Hkv * p.groups <= p.grid;
   // Set-up, masks and output of a segment in units of the loads' time, by measurement: 64 x 16 rows of 4 heads 194.7 us

@@ -192,7 +192,9 @@ void plan_workspace(dflash_handle_s *h) {
   L.corr = take((c.flags & DFLASH_FLAG_CONV) ? (size_t)Mb * 2 * (c.D / c.conv_group) * 4 : 0);
   L.apart_ctas = apart_max;
   // a tree's attention writes two slots a CTA of up to two tiles of query rows
-  const size_t part_rows = std::max(apart_max * rows_attn, (size_t)2 * h->num_sms * kTreePartRows);
+  const size_t tree_slots = (size_t)2 * std::min(h->num_sms, kTreeCtas);
+  const size_t part_rows =
+      std::max(apart_max * rows_attn, tree_slots * attention_tree_part_rows(std::min(kTreeMax, c.Cmax), c.Hq / c.Hkv));
   L.apart_bytes = part_rows * c.hd * 4;
   L.apart = take(L.apart_bytes);
   L.aml = take(part_rows * 2 * 4);

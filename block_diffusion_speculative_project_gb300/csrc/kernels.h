@@ -347,9 +347,8 @@ cudaError_t launch_attention8_wide(const Attn8Params &p, int R, cudaStream_t s);
 
 // ---------------------------------------------------------------- trees of drafted tokens
 
-constexpr int kTreeMax = 64;   // nodes of a tree (a row's ancestors are the bits of 64)
-constexpr int kTreeCtas = 160;      // most CTAs of a tree's attention
-constexpr int kTreePartRows = 256;  // most rows of a slot of its partials
+constexpr int kTreeMax = 64;    // nodes of a tree (a row's ancestors are the bits of 64)
+constexpr int kTreeCtas = 160;  // most CTAs of a tree's attention
 
 // A pair that several CTAs of a tree's attention share: where it belongs, the CTA and slot of its first part, parts (below
 // 2: none), rows of its tree.
@@ -383,6 +382,8 @@ struct AttnTreeParams {
   int stall;                 // test hook: issue no loads so the waits run out
 };
 void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows);
+// The most rows of a slot for trees of up to m nodes: what the workspace holds.
+int attention_tree_part_rows(int m, int G);
 cudaError_t launch_attention_tree(AttnTreeParams &p, cudaStream_t s);
 
 // Walk of the trees along the target's tokens (tree_ops.cu).

@@ -249,6 +249,19 @@ def test_graphs_of_one_workspace_and_handles_at_once():
             assert torch.equal(out, want[k])
 
 
+@pytest.mark.parametrize("Hq,Hkv,Cmax", [(1, 1, 8192), (2, 1, 8192), (3, 1, 8192), (4, 2, 40), (5, 1, 8192), (32, 1, 8192)])
+def test_scratch_of_the_partials(Hq, Hkv, Cmax):
+    """Partials of two slots a SM hold the rows that a tree of the handle's can have, no more; the longest trees fit."""
+    D = lib()
+    t = Target(Hq, Hkv, 128, Cmax=Cmax, nb=1, paged=False, V=64)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = min(256, Hq // Hkv * min(64, Cmax))
+    assert t.ws.numel() <= 2 * sms * rows * (128 * 4 + 8) + (1 << 20)   # the rest of so small a handle: below 1 MB
+    for m in (min(64, Cmax), 33, 1):
+        check_attention(t, m, queries(1, m, Hq, 128, m), trees(1, m, m), None, [Cmax - m])
+    assert D.dflash_status(t.h, t.ws) == 0
+
+
 @pytest.mark.parametrize("Hq,m,kind", [(4, 64, "wide"), (8, 64, "tree"), (4, 1, "chain"), (4, 40, "chain")])
 def test_the_widest_window_is_none(Hq, m, kind):
     nb = 4
