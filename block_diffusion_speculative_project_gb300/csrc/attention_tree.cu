@@ -339,11 +339,11 @@ __device__ __forceinline__ unsigned long long line_of(const AttnTreeParams &p, c
     *depth = __popcll(seen) - 1;
     return j < 0 ? 0ull : seen;
   }
-  unsigned long long seen = 0;
+  unsigned long long seen = 0;  // a window of fewer positions than a tree may have
   int a = max(j, 0), d = 0;
   bool on = j >= 0, bad = false;
   while (__any_sync(0xffffffffu, on)) {  // parents lie below their nodes
-    if (on && (p.window <= 0 || d < p.window)) seen |= 1ull << a;
+    if (on && d < p.window) seen |= 1ull << a;
     const int x = __shfl_sync(0xffffffffu, up0, a & 31), y = __shfl_sync(0xffffffffu, up1, a & 31);
     const int up = a < 32 ? x : y;
     const bool top = a == 0 || up < 0 || up >= a;
@@ -355,7 +355,7 @@ __device__ __forceinline__ unsigned long long line_of(const AttnTreeParams &p, c
     }
   }
   *depth = d;
-  if (p.window > 0 && p.sinks > s.ctx) {  // nodes among the first rows
+  if (p.sinks > s.ctx) {  // nodes among the first rows
     a = max(j, 0);
     int e = d;
     on = j >= 0;
@@ -1127,8 +1127,8 @@ cudaError_t launch_form(const AttnTreeParams &p, cudaStream_t s) {
 
 }  // namespace
 
-// Nodes per tile and groups of tiles for m nodes of G query heads: one tile where all rows fit, else
-// pairs of tiles of about the same size.
+// Nodes per tile and groups of tiles for m nodes of G <= 64 query heads (dflash_create takes no more): one tile where
+// all rows fit, else pairs of tiles of about the same size.
 void attention_tree_plan(int m, int G, int *npt, int *groups, int *part_rows) {
   const int most = kTileRows / G;  // nodes of a tile
   if (m <= most) {
