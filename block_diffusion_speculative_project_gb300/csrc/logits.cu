@@ -493,12 +493,12 @@ __global__ void __launch_bounds__(256) token_counts_kernel(const TokenCountsPara
   griddep_wait();
   griddep_launch();
   const int i = blockIdx.y;
-  const int t = blockIdx.x * 256 + threadIdx.x;
+  const unsigned t = blockIdx.x * 256u + threadIdx.x;  // up to 2^31 + 254
   int n = p.n_tokens ? p.n_tokens[i] : p.n;
   bool bad = n < 0 || n > p.n;
   n = max(0, min(n, p.n));
-  const bool live = t < n;
-  const int id = t < p.n ? p.tokens[(long long)i * p.ld + t] : -1;
+  const bool live = t < static_cast<unsigned>(n);
+  const int id = t < static_cast<unsigned>(p.n) ? p.tokens[(long long)i * p.ld + t] : -1;
   const bool fits = live && id >= 0 && id < p.V;
   bad |= live && !fits;
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) flag_status(p.status, kStatusCheck);
@@ -574,7 +574,7 @@ cudaError_t launch_logits_adjust(LogitsParams &p, int num_sms, cudaStream_t s) {
 }
 
 cudaError_t launch_token_counts(const TokenCountsParams &p, cudaStream_t s) {
-  return launch_pdl(token_counts_kernel, dim3((p.n + 255) / 256, p.nb), dim3(256), 0, s, p);
+  return launch_pdl(token_counts_kernel, dim3((p.n - 1) / 256 + 1, p.nb), dim3(256), 0, s, p);
 }
 
 }  // namespace df

@@ -722,6 +722,20 @@ def test_counts_of_tokens(nb, n, ld, V):
     assert t.status() == D.DFLASH_ERR_DEVICE_CHECK
 
 
+def test_counts_of_the_longest_row():
+    """A row of 2^31 - 1 tokens: 8.6 GB."""
+    D = lib()
+    n, V = 2 ** 31 - 1, 64
+    t = Target(nb=1, V=V)
+    tokens = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    tokens[0], tokens[2 ** 31 - 257], tokens[n - 1] = 1, 2, 3
+    for num, want in ((None, {1: 1, 2: 1, 3: 1, 5: n - 3}), (n, {1: 1, 2: 1, 3: 1, 5: n - 3}), (n - 1, {1: 1, 2: 1, 5: n - 3}),
+                      (9, {1: 1, 5: 8})):
+        counts = i32(np.zeros((1, V)))
+        D.dflash_token_counts(t.h, 1, n, tokens, n, None if num is None else i32([num]), 0, counts, t.ws)
+        assert t.status() == 0 and {v: c for v, c in enumerate(counts[0].tolist()) if c} == want
+
+
 def pack(allowed):
     rows, V = allowed.shape
     pad = np.zeros((rows, -(-V // 32) * 32), bool)
