@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kCommitWarps * 32) kv_commit_kernel(const KvCo
 }  // namespace
 
 cudaError_t launch_accept_tree(const AcceptTreeParams &p, cudaStream_t s) {
-  return launch_pdl(accept_tree_kernel, dim3((p.nb + kAcceptWarps - 1) / kAcceptWarps), dim3(kAcceptWarps * 32), 0, s,
+  return launch_pdl(accept_tree_kernel, dim3((p.nb - 1) / kAcceptWarps + 1), dim3(kAcceptWarps * 32), 0, s,
                     p);
 }
 

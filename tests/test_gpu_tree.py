@@ -618,6 +618,16 @@ def test_accepted_paths(nb, m):
         assert torch.equal(t2, tau) and torch.equal(b2, bonus)
 
 
+def test_paths_of_the_most_sequences():
+    """2^31 - 1 sequences without nodes: 8.6 GB for each output."""
+    D = lib()
+    t, nb = Target(nb=1), 2 ** 31 - 1
+    tau, bonus = (torch.full((nb,), 7, dtype=torch.int32, device="cuda") for _ in range(2))
+    D.dflash_accept_tree(t.h, nb, 0, None, None, None, None, None, tau, bonus, None, None, t.ws)
+    assert t.status() == 0
+    assert int(tau.min()) == int(tau.max()) == 0 and int(bonus.min()) == int(bonus.max()) == -1
+
+
 def test_trees_that_are_none_are_reported_and_end_the_walk():
     D = lib()
     t = Target(nb=1)
