@@ -905,6 +905,42 @@ def test_biases_of_one_slice_and_of_one_token():
     r.check(*run_row(r, t))
 
 
+# Sequences, rows and vocabularies of serving batches: several groups of rows a CTA, eight tiles a warp with one row and
+# with two at a time, values one by one; and more sequences than the handle's scratch holds
+@pytest.mark.parametrize("nb,m,V,most", [(64, 16, 151936, 64), (64, 15, 151936, 64), (64, 1, 151936, 64), (16, 64, 32003, 16),
+                                         (64, 16, 151935, 64), (64, 1, 151935, 64), (8, 16, 151936, 8), (1, 64, 151936, 1),
+                                         (64, 16, 32003, 37), (64, 1, 151936, 37), (300, 3, 4096, 300), (16, 64, 4096, 16)])
+def test_adjusted_logits_of_serving_batches(nb, m, V, most):
+    """All rules, ragged, in place and not: three sequences against the oracle, and every sequence of the batch, which has
+    the rules and logits of one of them, as the handle of one sequence gives it, whose work is split otherwise."""
+    D = lib()
+    k = min(3, nb)
+    r = Row(k, m, V, nb + m, n_bias=50, mask=True, tree=True)
+    y, g = run_row(r, Target(nb=1, V=V))
+    r.check(y, g)
+    want, want_g = y.view(torch.int32).view(k, m, V), g.view(k, m)
+    tile = lambda a: a.repeat(-(-nb // k), *[1] * (a.dim() - 1))  # noqa: E731
+    rules = D.logit_rules(*[tile(a)[:nb * a.shape[0] // k].contiguous() for a in r.rules().tensors])
+    n = [m - (i * 5) % (m + 1) for i in range(nb)]
+    t = Target(nb=most, V=V, Cmax=64, paged=False)
+    x = tile(torch.from_numpy(r.x).cuda())[:nb * m].contiguous()
+    same = x.clone()
+    out, ids, only = torch.full_like(x, 7.0), i32(np.full(nb * m, 7)), i32(np.full(nb * m, 7))
+    D.dflash_logits_adjust(t.h, nb, m, x, V, rules, i32(n), out, V, ids, t.ws)
+    D.dflash_logits_adjust(t.h, nb, m, x, V, rules, i32(n), None, V, only, t.ws)
+    assert torch.equal(x, same) and torch.equal(ids, only)
+    D.dflash_logits_adjust(t.h, nb, m, same, V, rules, i32(n), same, V, None, t.ws)
+    assert t.status() == 0
+    left = torch.tensor(7.0).view(torch.int32).item()
+    for i in range(nb):
+        rows, behind = slice(i * m, i * m + n[i]), slice(i * m + n[i], (i + 1) * m)
+        assert torch.equal(out[rows].view(torch.int32), want[i % k, :n[i]]), i
+        assert torch.equal(same[rows].view(torch.int32), want[i % k, :n[i]]), i
+        assert torch.equal(ids[rows], want_g[i % k, :n[i]]), i
+        assert (out[behind].view(torch.int32) == left).all() and (ids[behind] == 7).all(), i
+        assert torch.equal(same[behind], x[behind]), i
+
+
 @pytest.mark.parametrize("nb,m,V", [(1, 1, 64), (256, 64, 64), (200, 64, 1024), (90, 64, 1025), (5, 3, 151936),
                                     (1, 1, 2 ** 21), (2, 64, 2 ** 21)])
 def test_scratch_of_the_ids(nb, m, V):
