@@ -15,8 +15,9 @@
 //   two tiles (R > 128)   both halves work on every unit, each for its own tile of up to 128 rows: K and
 //                         V are read once for 256 rows. More rows take further groups of two tiles. Bound by the
 //                         chain of a unit, S, softmax, product, and what the products of both tiles take from
-//                         shared memory: 262147 rows under 64 nodes 191 us, 1.44 PFLOP/s and 5.6 TB/s; with each
-//                         tile's rows in a CTA of its own, K and V read twice, 314 us.
+//                         shared memory: 262147 rows under 64 nodes 194 us in short graph runs, 1.42 PFLOP/s and
+//                         5.5 TB/s; called for seconds on end, at the power limit, 226 us, 1.21 PFLOP/s and 4.7 TB/s;
+//                         with each tile's rows in a CTA of its own, K and V read twice, 314 us.
 // A (sequence, kv head, group) is a pair; the visible units of all pairs are cut into equal ranges, one
 // per CTA (one CTA per SM; two one-tile CTAs an SM, each with half the stages: 206 us for the trees above).
 // The run of one pair inside a range is a segment: it writes the output, or if the pair goes on in another
@@ -35,6 +36,9 @@
 // the softmax warps: a thread owns a query row (its TMEM lane), keeps its maximum and sum in fp32, rounds P to bf16
 // (by up to 2^-8 of each probability, the type of the values that it multiplies) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
+//
+// Figures above are of the kernel as it is, from graphs of some thirty calls; pairs of figures beside the code
+// compare a step with what stood before it, as things were then.
 #include <cfloat>
 
 #include "common.cuh"
@@ -282,8 +286,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 }
 
 // One lane of a converged warp, always the same. The operands of the products that it issues stay in uniform registers:
-// two tiles' 24 products of a unit go out in 1150 cycles, from a thread of its own in 1410 (262147 rows under 64 nodes
-// 217 us, so 191).
+// two tiles' 24 products of a unit go out in 1150 cycles, from a thread of its own in 1410 (262147 rows under 64 nodes,
+// short graph runs: 217 us, so 191).
 __device__ __forceinline__ bool elect_one() {
   uint32_t mine;
   asm volatile(
@@ -735,8 +739,8 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;
     // The first QT tiles of a segment's Q to tensor memory, by half 1, or with two tiles by the halves whose rows they
     // are. One tile's place in shared memory is free for the next segment's then, and the products do not read it from
-    // there beside the keys (262147 rows under 64 nodes: 203 us, both tiles from shared memory 219; of 64 channels,
-    // where tensor memory has the columns, 173 with both in it, 179 with one).
+    // there beside the keys (262147 rows under 64 nodes: 203 us then, both tiles from shared memory 219; of 64
+    // channels, where tensor memory has the columns, 173 with both in it, 179 with one).
     const bool copies = TWO ? half < C::QT : half == 1;
     const int tile = TWO ? half : 0;
     auto copy_q = [&](int index) {
@@ -844,7 +848,7 @@ __global__ void __launch_bounds__(Roles<NQ>::THREADS, 1) attn_tree_kernel(const 
         }
         // P's place is free, and O at rest, once the half's product before is done. Asked for here and not behind the
         // exponentials, where it would be there already, it keeps the halves' exponentials apart (262147 rows under 64
-        // nodes 196 us, behind them 216).
+        // nodes 196 us then, behind them 216).
         ok = step < 2 || mbar_wait_warp(&p_empty[half], ((step >> 1) - 1) & 1, p.max_spin);
         if (!ok) break;
         tc_fence_after();  // behind that product come what is written of O, and P

@@ -17,8 +17,8 @@
 // lane, and every lane's copies of the rows' values run ahead of it through its own places in shared
 // memory, so that a warp waits for nobody. The counts of a sequence with one row run through the same places (64
 // rows 24.6 us, read before the row 28.8). Bound by HBM for many rows; one row a sequence
-// by what a CTA begins with, lists and first copies, in two waves; a single row (6.3 us) by that and two
-// launches. Rows of odd strides or vocabularies go value by value, bound by their instructions (266 us).
+// by what a CTA begins with, lists and first copies, in two waves; a single row (5.8 us) by that and two
+// launches. Rows of odd strides or vocabularies go value by value, bound by their instructions (265 us).
 // Few tokens are listed so, but next to every row of a warp's values has one, and in line they would cost the
 // warp their division and look-ups for one lane's sake (1159 us for 1024 rows of 151936). So the pass masks
 // and takes the maximum of the others, and behind it the warp works its listed tokens off, a lane a

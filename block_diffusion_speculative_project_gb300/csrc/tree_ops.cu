@@ -87,7 +87,8 @@ constexpr int kCommitLoads = 8;  // 16-byte loads of a lane in flight
 // One warp per (sequence, layer, kv head, K or V): rows base + path[t] move to base + t. Rows go in
 // batches of kCommitLoads loads a lane, a batch read whole before it is written: a later batch reads
 // rows path[t] >= t, behind everything that an earlier one wrote. The tree's rows lie in two pages at
-// most, so the table's entries come with two loads. Latency: lengths and path, table, rows (one sequence's path of 5 layers 2.0 us, of 64 sequences 4.7, 17 MB).
+// most, so the table's entries come with two loads. Latency: lengths and path, table, rows (one sequence's path of
+// 5 layers 2.0 us, of 64 sequences 4.7, 17 MB).
 template <int HD>
 __global__ void __launch_bounds__(kCommitWarps * 32) kv_commit_kernel(const KvCommitParams p) {
   constexpr int LPR = HD / 8;      // lanes of a row

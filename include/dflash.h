@@ -415,6 +415,7 @@ DFLASH_API int dflash_attention8(dflash_handle_t h, int nb, int layer, int m, co
  * p > ctx_len[i] + depth(j) - window, or if p < sinks; and the rows of the nodes from j up to the
  * root by the same rule at their positions. The rows' keys and values have been appended before.
  *   m           rows of q a sequence, 0..DFLASH_TREE_MAX, at most Cmax; any number of query heads a kv head
+ *               that dflash_create takes (up to 64)
  *   q           bf16 [nb, m, Hq, hd]: rotated queries
  *   kcache, vcache  the caches, contiguous or paged
  *   n_rows      int32 [nb] device, 0 <= n_rows[i] <= m, or NULL: m. Rows j >= n_rows[i] of out_o are
@@ -467,7 +468,7 @@ typedef struct dflash_logit_rules {
  *   out_ids     int32 [nb * m] or NULL: argmax of y, the lowest id of equals; -1 where no token is
  *               above -inf
  * Rows that are 16-byte aligned with strides and V multiples of 4 are read in 16-byte pieces. Not
- * limited to max_batch; needs no weights. V up to 2^21. */
+ * limited to max_batch (nb up to 2^20); needs no weights. V up to 2^21. */
 DFLASH_API int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const float *logits, int64_t ld,
                                     const dflash_logit_rules *rules, const int32_t *n_rows, float *out,
                                     int64_t ld_out, int32_t *out_ids, void *ws, size_t ws_bytes,
@@ -478,7 +479,8 @@ DFLASH_API int dflash_logits_adjust(dflash_handle_t h, int nb, int m, const floa
  *   n_tokens    int32 [nb] or NULL: n; 0 <= n_tokens[i] <= n tokens of sequence i count (e.g. out_tau)
  *   prompt      0: counts[i][t] += 1 for each token t; else bit 31 of counts[i][t] is set
  *   counts      int32 [nb, V]; the caller zeroes a sequence's row when a request begins
- * A token outside [0, V) is reported as DFLASH_ERR_DEVICE_CHECK by dflash_status and not counted. */
+ * nb up to 65535. A token outside [0, V) is reported as DFLASH_ERR_DEVICE_CHECK by dflash_status and not
+ * counted. */
 DFLASH_API int dflash_token_counts(dflash_handle_t h, int nb, int n, const int32_t *tokens, int64_t ld,
                                    const int32_t *n_tokens, int prompt, int32_t *counts, void *ws,
                                    size_t ws_bytes, dflash_stream_t stream);
@@ -491,7 +493,9 @@ DFLASH_API int dflash_token_counts(dflash_handle_t h, int nb, int n, const int32
  *               emitted; 0 for a sequence without rows
  *   out_bonus   int32 [nb]: target[last node of the path], the next root's token; -1 without rows
  *   out_path    int32 [nb, m] or NULL: the path's nodes, then -1
- *   out_tokens  int32 [nb, m] or NULL: the tau tokens emitted, the bonus token last, then -1 */
+ *   out_tokens  int32 [nb, m] or NULL: the tau tokens emitted, the bonus token last, then -1
+ * Where the target has no token behind the last node (an id of -1 from dflash_logits_adjust, whose rules
+ * left nothing), that is the bonus token: the sequence cannot go on, and dflash_token_counts reports it. */
 DFLASH_API int dflash_accept_tree(dflash_handle_t h, int nb, int m, const int32_t *parent,
                                   const int32_t *tokens, const int32_t *target, const int32_t *n_rows,
                                   int32_t *ctx_len, int32_t *out_tau, int32_t *out_bonus,
