@@ -37,8 +37,8 @@
 // (by up to 2^-8 of each probability, the type of the values that it multiplies) and rescales O only when the row's
 // maximum grew by more than 2^8, so most units need no round trip of O.
 //
-// Figures above are of the kernel as it is, from graphs of some thirty calls; pairs of figures beside the code
-// compare a step with what stood before it, as things were then.
+// Figures above are of the kernel as it is, from graphs of some thirty calls where nothing else is said; pairs of
+// figures beside the code compare a step with what stood before it, as things were then.
 #include <cfloat>
 
 #include "common.cuh"

@@ -493,12 +493,12 @@ __global__ void __launch_bounds__(256) token_counts_kernel(const TokenCountsPara
   griddep_wait();
   griddep_launch();
   const int i = blockIdx.y;
-  const unsigned t = blockIdx.x * 256u + threadIdx.x;  // up to 2^31 + 254
+  const int t = blockIdx.x * 256 + threadIdx.x;
   int n = p.n_tokens ? p.n_tokens[i] : p.n;
   bool bad = n < 0 || n > p.n;
   n = max(0, min(n, p.n));
-  const bool live = t < static_cast<unsigned>(n);
-  const int id = t < static_cast<unsigned>(p.n) ? p.tokens[(long long)i * p.ld + t] : -1;
+  const bool live = t < n;
+  const int id = t < p.n ? p.tokens[(long long)i * p.ld + t] : -1;
   const bool fits = live && id >= 0 && id < p.V;
   bad |= live && !fits;
   if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) flag_status(p.status, kStatusCheck);
